@@ -216,6 +216,7 @@ def _plain_logp(s, k):
         lse[rows] = torch.where(keep, (m * it + log_total)[:, 0], 0.0)
         logp[rows] = torch.where(keep, log_p.gather(1, i)[:, 0], 0.0)
         ent[rows] = torch.where(keep, h[:, 0], 0.0)
+        x = x.clone() if k else x  # the search below strikes out what it has found; the logits stay
         for j in range(k):
             best = x.amax(-1, keepdim=True)
             at = torch.where(x == best, column, V).amin(-1, keepdim=True)
