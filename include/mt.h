@@ -493,8 +493,98 @@ int mt_op_moe_ffn_bwd(const void* m, const void* Wr, const void* Wgu, const void
                       float* dWr, float* dWgu, float* dWd, int32_t* route, void* workspace, int T, int h, int E,
                       int top_k, int Fe, void* stream);
 
-/* Device error word of the kernels (barrier timeouts etc.): returns and
- * clears it (0 = none). Synchronizes the device. */
+/* Activation checkpoints in 8 bits. A row's columns are cut into blocks of
+ * 32 (the last may be shorter); a block keeps one scale byte b, its scale
+ * being 2^(b-127), and one code byte per value. b is the least byte with
+ * max|x| <= limit * 2^(b-127); a code is x / scale rounded to nearest even:
+ *  MT_CKPT_I8   : limit 127, codes are two's complement whole numbers
+ *  MT_CKPT_E4M3 : limit 448, codes are FP8 E4M3
+ * (i8 has the finer steps near a block's maximum, e4m3 keeps 2^-4 relative
+ * error for values far below it). A block with an infinity or a NaN gets
+ * b = 255 and code 0 and stands for NaN throughout. */
+typedef enum { MT_CKPT_F32 = 0, MT_CKPT_I8 = 1, MT_CKPT_E4M3 = 2 } mt_ckpt_format;
+
+/* Pack x [T, n] (x_dtype MT_F32 or MT_BF16, row stride ldx elements) into
+ * codes [T, ldc] bytes and scales [T, ceil(n/32)] bytes; unpack restores
+ * x = code * scale (rounded once for MT_BF16). Any n >= 1, T in [1, 2^30],
+ * ldx, ldc >= n and <= 2^29; columns past n are left as they are. */
+int mt_op_ckpt8_pack(const void* x, int x_dtype, int fmt, void* codes, void* scales, int T, int n, int ldx, int ldc,
+                     void* stream);
+int mt_op_ckpt8_unpack(const void* codes, const void* scales, int fmt, void* x, int x_dtype, int T, int n, int ldc,
+                       int ldx, void* stream);
+
+/* mt_op_rmsnorm_fwd that also packs its input x [T, h] (same results and
+ * sizes; h a multiple of 4, at most 8192): codes [T, h], scales
+ * [T, ceil(h/32)]. x, w 16-byte, y 8-byte, codes 4-byte aligned. */
+int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd, void* codes, void* scales, int fmt,
+                            int T, int h, float eps, void* stream);
+
+/* mt_op_rmsnorm_bwd that reads x from its 8-bit form (the formulas with x =
+ * code * scale and the given rstd). resid may be null or equal dx, dx_bf16
+ * may be null. workspace: mt_op_rmsnorm_bwd_ckpt8_workspace floats, 16-byte
+ * aligned like w, dy, resid and dx (codes 4, dx_bf16 8). Deterministic. */
+size_t mt_op_rmsnorm_bwd_ckpt8_workspace(int T, int h);
+int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, const float* w, const float* rstd,
+                            const float* dy, const float* resid, float* dx, void* dx_bf16, float* dw,
+                            float* workspace, int T, int h, void* stream);
+
+/* mt_op_swiglu_fwd that also packs g|u: codes [T, 2*ld] in gu's layout,
+ * scales [T, 2*ceil(F/32)] (g's blocks, then u's; g and u are cut into
+ * blocks separately). Padding columns F..ld-1 get codes and act 0. act comes
+ * from the exact g and u. Backward: dgu [T, 2*ld] = (dact*u*silu'(g),
+ * dact*silu(g)) with g, u = code * scale; padding columns 0. dact's padding
+ * is not read. Any F >= 1, ld in [F, 2^29]. */
+int mt_op_swiglu_fwd_ckpt8(const void* gu, void* act, void* codes, void* scales, int fmt, int T, int F, int ld,
+                           void* stream);
+int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const void* dact, void* dgu, int T, int F,
+                           int ld, void* stream);
+
+/* Log probability of one given token per row of logits [T, V] (dtype MT_F32
+ * or MT_BF16, row stride ld): with z = inv_temp * logits[t],
+ *   lse[t] = log sum_j e^{z_j}, logp[t] = z_{ids[t]} - lse[t],
+ *   entropy[t] = -sum_j p_j log p_j (null: not wanted), and the k most
+ *   likely tokens, top_ids / top_logp [T, k] in descending order, equal
+ *   logits by ascending index (k in [0, min(32, V)]; null with k = 0).
+ * Logits at or below -1e30 (-inf, a type's lowest value) are masked out:
+ * probability 0, log probability -inf, never listed (places that remain hold
+ * -1 and -inf). A row with nothing left has lse = logp = -inf, entropy 0. A
+ * row with a NaN or +inf has NaN for all four and -1. ids[t] < 0: the row is
+ * not scored; its logits are not read, its outputs are 0 and its top_ids -1.
+ * ids[t] >= V: outputs NaN and -1, and a bit in mt_op_device_error. ids are
+ * device int32, everything else fp32; inv_temp in [1e-30, 1e30]. */
+int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, float inv_temp, int k, float* lse,
+                         float* logp, float* entropy, int32_t* top_ids, float* top_logp, int T, int V, int ld,
+                         void* stream);
+
+/* Its gradient: dlogits [T, V] (d_dtype, row stride ldd) =
+ *   inv_temp * (g_logp ([j = id] - p_j) - g_entropy p_j (log p_j + entropy)),
+ * p = e^{z - lse}, for given g_logp and g_entropy [T] (either may be null:
+ * zero); lse and entropy as the forward wrote them (entropy is read only with
+ * g_entropy). Rows not scored and rows with nothing left get 0. dlogits may
+ * be logits itself when type and stride are the same. */
+int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, float inv_temp, const float* lse,
+                             const float* entropy, const float* g_logp, const float* g_entropy, void* dlogits,
+                             int d_dtype, int T, int V, int ld, int ldd, void* stream);
+
+/* Embedding lookup: out[t] = scale * table[ids[t]] for table [V, h] and out
+ * [T, h] (MT_F32 or MT_BF16 each, one rounding); 0 where ids[t] < 0 (padding).
+ * ids[t] >= V: 0, and a bit in mt_op_device_error. */
+int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, float scale, void* out, int out_dtype,
+                    int T, int V, int h, void* stream);
+
+/* The table's gradient: dtable[v] = scale * sum of dout[t] over the t with
+ * ids[t] = v, every row written (0 for unused ids); accumulate != 0: dtable
+ * += that, rows of unused ids left as they are. Sums in fp32, in a fixed
+ * order (ascending positions): deterministic. workspace:
+ * mt_op_embed_bwd_workspace(T, V, h) bytes of device memory, 256-byte
+ * aligned (0 for sizes the call refuses). Ids outside [0, V) as above. */
+size_t mt_op_embed_bwd_workspace(int T, int V, int h);
+int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float scale, void* dtable, int dtable_dtype,
+                    int accumulate, void* workspace, int T, int V, int h, void* stream);
+
+/* Device error word of the kernels (barrier timeouts, token ids outside the
+ * vocabulary etc.): returns and clears it (0 = none). Synchronizes the
+ * device. */
 int mt_op_device_error(void);
 
 #ifdef __cplusplus

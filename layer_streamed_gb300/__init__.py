@@ -30,6 +30,7 @@ MT_ERR_CUDA, MT_ERR_TIMEOUT, MT_ERR_STATE, MT_ERR_UNSUPPORTED, MT_ERR_DEVICE = -
 MT_F32, MT_BF16, MT_FP8 = 0, 1, 2
 MT_GEMM_NT, MT_GEMM_NN, MT_GEMM_TN = 0, 1, 2
 MT_EPI_BF16, MT_EPI_F32, MT_EPI_F32_ADD = 0, 1, 2
+MT_CKPT_F32, MT_CKPT_I8, MT_CKPT_E4M3 = 0, 1, 2
 
 STATUS_NAMES = {0: "MT_OK", -1: "MT_ERR_ARG", -2: "MT_ERR_BUDGET", -3: "MT_ERR_NOT_PINNED", -4: "MT_ERR_ALIGN",
                 -5: "MT_ERR_CUDA", -6: "MT_ERR_TIMEOUT", -7: "MT_ERR_STATE", -8: "MT_ERR_UNSUPPORTED",
@@ -46,7 +47,10 @@ EXPORTS = ("mt_packed_bytes", "mt_tensor_offset", "mt_required_budget", "mt_crea
            "mt_op_swiglu_bwd", "mt_op_lmhead_ce_workspace", "mt_op_lmhead_ce", "mt_op_device_error",
            "mt_adamw_update", "mt_bind_optimizer", "mt_train_step", "mt_train_step_async", "mt_optimizer_flush",
            "mt_get_routing", "mt_replay_weight_stream", "mt_quantize_params_fp8", "mt_op_moe_workspace", "mt_op_moe_ffn_fwd", "mt_op_moe_bwd_workspace",
-           "mt_op_moe_ffn_bwd")
+           "mt_op_moe_ffn_bwd", "mt_op_ckpt8_pack", "mt_op_ckpt8_unpack", "mt_op_rmsnorm_fwd_ckpt8",
+           "mt_op_rmsnorm_bwd_ckpt8_workspace", "mt_op_rmsnorm_bwd_ckpt8", "mt_op_swiglu_fwd_ckpt8",
+           "mt_op_swiglu_bwd_ckpt8", "mt_op_token_logprobs", "mt_op_token_logprobs_bwd", "mt_op_embed_fwd",
+           "mt_op_embed_bwd_workspace", "mt_op_embed_bwd")
 
 
 class MtError(RuntimeError):
@@ -164,6 +168,18 @@ def lib() -> ctypes.CDLL:
         "mt_op_moe_ffn_fwd": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
         "mt_op_moe_bwd_workspace": (sz, [i32, i32, i32, i32, i32]),
         "mt_op_moe_ffn_bwd": (i32, [vp] * 11 + [i32, i32, i32, i32, i32, vp]),
+        "mt_op_ckpt8_pack": (i32, [vp, i32, i32, vp, vp, i32, i32, i32, i32, vp]),
+        "mt_op_ckpt8_unpack": (i32, [vp, vp, i32, vp, i32, i32, i32, i32, i32, vp]),
+        "mt_op_rmsnorm_fwd_ckpt8": (i32, [vp] * 6 + [i32, i32, i32, f32, vp]),
+        "mt_op_rmsnorm_bwd_ckpt8_workspace": (sz, [i32, i32]),
+        "mt_op_rmsnorm_bwd_ckpt8": (i32, [vp, vp, i32] + [vp] * 8 + [i32, i32, vp]),
+        "mt_op_swiglu_fwd_ckpt8": (i32, [vp] * 4 + [i32, i32, i32, i32, vp]),
+        "mt_op_swiglu_bwd_ckpt8": (i32, [vp, vp, i32, vp, vp, i32, i32, i32, vp]),
+        "mt_op_token_logprobs": (i32, [vp, i32, vp, f32, i32] + [vp] * 5 + [i32, i32, i32, vp]),
+        "mt_op_token_logprobs_bwd": (i32, [vp, i32, vp, f32] + [vp] * 5 + [i32, i32, i32, i32, i32, vp]),
+        "mt_op_embed_fwd": (i32, [vp, i32, vp, f32, vp, i32, i32, i32, i32, vp]),
+        "mt_op_embed_bwd_workspace": (sz, [i32, i32, i32]),
+        "mt_op_embed_bwd": (i32, [vp, vp, i32, f32, vp, i32, i32, vp, i32, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -602,6 +618,77 @@ def mt_op_lmhead_ce_workspace(T, V, h) -> int:
 def mt_op_lmhead_ce(X, W, labels, scale, dX, dW, loss, workspace, T, V, h, stream=None):
     _check(lib().mt_op_lmhead_ce(_ptr(X), _ptr(W), _ptr(labels), scale, _ptr(dX), _ptr(dW), _ptr(loss),
                                  _ptr(workspace), T, V, h, _stream(stream)))
+
+
+def mt_op_ckpt8_pack(x, x_dtype, fmt, codes, scales, T, n, ldx, ldc, stream=None):
+    """Pack x [T, n] into 8-bit codes and one scale byte per 32 columns (fmt
+    MT_CKPT_I8 or MT_CKPT_E4M3; see include/mt.h)."""
+    _check(lib().mt_op_ckpt8_pack(_ptr(x), x_dtype, fmt, _ptr(codes), _ptr(scales), T, n, ldx, ldc, _stream(stream)))
+
+
+def mt_op_ckpt8_unpack(codes, scales, fmt, x, x_dtype, T, n, ldc, ldx, stream=None):
+    _check(lib().mt_op_ckpt8_unpack(_ptr(codes), _ptr(scales), fmt, _ptr(x), x_dtype, T, n, ldc, ldx,
+                                    _stream(stream)))
+
+
+def mt_op_rmsnorm_fwd_ckpt8(x, w, y, rstd, codes, scales, fmt, T, h, eps, stream=None):
+    """RMSNorm forward that also packs its input."""
+    _check(lib().mt_op_rmsnorm_fwd_ckpt8(_ptr(x), _ptr(w), _ptr(y), _ptr(rstd), _ptr(codes), _ptr(scales), fmt, T, h,
+                                         eps, _stream(stream)))
+
+
+def mt_op_rmsnorm_bwd_ckpt8_workspace(T, h) -> int:
+    return lib().mt_op_rmsnorm_bwd_ckpt8_workspace(T, h)
+
+
+def mt_op_rmsnorm_bwd_ckpt8(codes, scales, fmt, w, rstd, dy, resid, dx, dx_bf16, dw, workspace, T, h, stream=None):
+    """RMSNorm backward that reads its input from the packed form."""
+    _check(lib().mt_op_rmsnorm_bwd_ckpt8(_ptr(codes), _ptr(scales), fmt, _ptr(w), _ptr(rstd), _ptr(dy), _ptr(resid),
+                                         _ptr(dx), _ptr(dx_bf16), _ptr(dw), _ptr(workspace), T, h, _stream(stream)))
+
+
+def mt_op_swiglu_fwd_ckpt8(gu, act, codes, scales, fmt, T, F, ld, stream=None):
+    """SwiGLU forward that also packs g|u."""
+    _check(lib().mt_op_swiglu_fwd_ckpt8(_ptr(gu), _ptr(act), _ptr(codes), _ptr(scales), fmt, T, F, ld,
+                                        _stream(stream)))
+
+
+def mt_op_swiglu_bwd_ckpt8(codes, scales, fmt, dact, dgu, T, F, ld, stream=None):
+    """SwiGLU backward that reads g|u from the packed form."""
+    _check(lib().mt_op_swiglu_bwd_ckpt8(_ptr(codes), _ptr(scales), fmt, _ptr(dact), _ptr(dgu), T, F, ld,
+                                        _stream(stream)))
+
+
+def mt_op_token_logprobs(logits, dtype, ids, inv_temp, k, lse, logp, entropy, top_ids, top_logp, T, V, ld,
+                         stream=None):
+    """Per row of logits: log-sum-exp, log probability of one given token,
+    entropy (optional) and the k most likely tokens (see include/mt.h)."""
+    _check(lib().mt_op_token_logprobs(_ptr(logits), dtype, _ptr(ids), inv_temp, k, _ptr(lse), _ptr(logp),
+                                      _ptr(entropy), _ptr(top_ids), _ptr(top_logp), T, V, ld, _stream(stream)))
+
+
+def mt_op_token_logprobs_bwd(logits, dtype, ids, inv_temp, lse, entropy, g_logp, g_entropy, dlogits, d_dtype, T, V,
+                             ld, ldd, stream=None):
+    """Gradient of the logits for given gradients of logp and entropy."""
+    _check(lib().mt_op_token_logprobs_bwd(_ptr(logits), dtype, _ptr(ids), inv_temp, _ptr(lse), _ptr(entropy),
+                                          _ptr(g_logp), _ptr(g_entropy), _ptr(dlogits), d_dtype, T, V, ld, ldd,
+                                          _stream(stream)))
+
+
+def mt_op_embed_fwd(table, table_dtype, ids, scale, out, out_dtype, T, V, h, stream=None):
+    """out[t] = scale * table[ids[t]], 0 for negative ids."""
+    _check(lib().mt_op_embed_fwd(_ptr(table), table_dtype, _ptr(ids), scale, _ptr(out), out_dtype, T, V, h,
+                                 _stream(stream)))
+
+
+def mt_op_embed_bwd_workspace(T, V, h) -> int:
+    return lib().mt_op_embed_bwd_workspace(T, V, h)
+
+
+def mt_op_embed_bwd(ids, dout, dout_dtype, scale, dtable, dtable_dtype, accumulate, workspace, T, V, h, stream=None):
+    """The table's gradient, summed per token in a fixed order."""
+    _check(lib().mt_op_embed_bwd(_ptr(ids), _ptr(dout), dout_dtype, scale, _ptr(dtable), dtable_dtype,
+                                 int(accumulate), _ptr(workspace), T, V, h, _stream(stream)))
 
 
 def mt_op_device_error() -> int:

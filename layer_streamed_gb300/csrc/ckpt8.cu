@@ -1,0 +1,669 @@
+// Activation checkpoints in 8 bits and their use in the backward pass.
+//
+// Block form: the columns of a row are cut into blocks of 32 (the last one
+// may be shorter); a block keeps one scale 2^(b-127), its byte b, and one
+// 8-bit code per value. b is the least byte with max|x| <= limit * 2^(b-127),
+// limit = 127 for int8 codes (x / scale rounded to the nearest whole number)
+// and 448 for e4m3 codes (x / scale rounded to e4m3), ties to even. Because
+// the scale is a power of two, x / scale and code * scale are exact: the one
+// rounding is the code's, and nothing ever saturates. A block that holds an
+// infinity or a NaN has b = 255 and codes 0, and stands for NaN throughout
+// (the same convention as the OCP microscaling formats' E8M0 scale).
+//
+// int8 steps evenly (error <= max|x| / 127 of the block's maximum when the
+// scale is tight, twice that at worst); e4m3 keeps 2^-4 relative error down
+// to 2^-14 of the block's maximum, so a block with one outlier keeps its
+// other values.
+//
+// All kernels here are bound by HBM traffic: every operand is read once and
+// every result written once, loads are 16 bytes a thread, and a block's
+// maximum is a shuffle reduction over the 4 (16-bit sources) or 8 (fp32)
+// lanes that hold it.
+#include <algorithm>
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mt {
+namespace {
+
+enum { FMT_I8 = 1, FMT_E4M3 = 2 };
+
+// Scale byte of a block from the bit pattern of max|x| (as an unsigned
+// integer it orders like the value, infinities and NaN above all numbers).
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  constexpr int off = FMT == FMT_I8 ? 6 : 8;                           // 127 = 1.984375 * 2^6, 448 = 1.75 * 2^8
+  constexpr uint32_t top = FMT == FMT_I8 ? 0x7e0000u : 0x600000u;      // fraction bits of 1.984375, 1.75
+  const uint32_t e = amax_bits >> 23;
+  if (e == 255u) return 255u;
+  const int b = (int)e - off + ((amax_bits & 0x7fffffu) > top ? 1 : 0);
+  return (uint32_t)max(b, 0);
+}
+__device__ __forceinline__ float scale_up(uint32_t b) {  // 2^(b-127); 2^-127 is subnormal
+  return __uint_as_float(b == 255u ? 0x7fffffffu : b ? b << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float scale_down(uint32_t b) {  // 2^(127-b), b <= 249
+  return __uint_as_float((254u - b) << 23);
+}
+
+// Four values to four code bytes.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  if (FMT == FMT_I8) {
+    // adding 1.5 * 2^23 leaves the nearest whole number (ties to even) in the low bits
+    constexpr float magic = 12582912.f;
+    const uint32_t ua = __float_as_uint(fmaf(a, inv, magic)), ub = __float_as_uint(fmaf(b, inv, magic));
+    const uint32_t uc = __float_as_uint(fmaf(c, inv, magic)), ud = __float_as_uint(fmaf(d, inv, magic));
+    return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
+  }
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// Four code bytes to the values they stand for.
+template <int FMT>
+__device__ __forceinline__ float4 decode4(uint32_t w, float s) {
+  if (FMT == FMT_I8) {
+    // byte + 128 in the low bits of 2^23; the subtraction is exact
+    w ^= 0x80808080u;
+    constexpr float bias = 8388736.f;  // 2^23 + 128
+    return make_float4((__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - bias) * s,
+                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - bias) * s,
+                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)) - bias) * s,
+                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - bias) * s);
+  }
+  uint32_t lo, hi;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+  const float2 l = __half22float2(*(const __half2*)&lo), h = __half22float2(*(const __half2*)&hi);
+  return make_float4(l.x * s, l.y * s, h.x * s, h.y * s);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Maximum over aligned groups of G lanes.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// E consecutive values (4 fp32 or 8 bf16) of a row from column c; columns at
+// or past n read as 0. VEC: one 16-byte load (c + E <= n and aligned).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load_unit(const void* row, int c, int n, float (&v)[BF16 ? 8 : 4]) {
+  constexpr int E = BF16 ? 8 : 4;
+  if (VEC && c + E <= n) {
+    if (BF16) {
+      const uint4 u = __ldcs((const uint4*)((const uint16_t*)row + c));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        v[2 * i] = __uint_as_float(w[i & 3] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i & 3] & 0xffff0000u);
+      }
+    } else {
+      const float4 f = __ldcs((const float4*)((const float*)row + c));
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    v[i] = c + i < n ? (BF16 ? bf2f(((const uint16_t*)row)[c + i]) : ((const float*)row)[c + i]) : 0.f;
+}
+// E code bytes (E / 4 words) to columns c.. of a row of codes.
+template <int E, bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, const uint32_t (&w)[E / 4]) {
+  if (VEC && c + E <= n) {
+    if (E == 8) *(uint2*)(row + c) = make_uint2(w[0], w[E / 4 - 1]);
+    else *(uint32_t*)(row + c) = w[0];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (c + i < n) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+}
+template <int E, bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int c, int n, uint32_t (&w)[E / 4]) {
+  if (VEC && c + E <= n) {
+    if (E == 8) {
+      const uint2 u = __ldcs((const uint2*)(row + c));
+      w[0] = u.x;
+      w[E / 4 - 1] = u.y;
+    } else {
+      w[0] = __ldcs((const uint32_t*)(row + c));
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < E / 4; ++k) w[k] = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (c + i < n) w[i >> 2] |= (uint32_t)row[c + i] << (8 * (i & 3));
+}
+
+// Codes and scale byte of one thread's unit; the G lanes of the block agree
+// on the scale. Every lane of the warp calls this.
+template <int FMT, int E>
+__device__ __forceinline__ uint32_t encode_unit(const float (&v)[E], uint32_t (&w)[E / 4]) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) am = max(am, abs_bits(v[i]));
+  const uint32_t b = scale_byte<FMT>(group_max<32 / E>(am));
+  if (b == 255u) {
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) w[k] = 0;
+  } else {
+    const float inv = scale_down(b);
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k)
+      w[k] = encode4<FMT>(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+  }
+  return b;
+}
+
+// ---------------------------------------------------------------------------
+// Pack and unpack. A thread owns one unit of 16 source bytes in each of kRows
+// rows (their loads are in flight together); a 2D block covers blockDim.x
+// units of blockDim.y rows at a time, so narrow matrices still fill a block.
+// ---------------------------------------------------------------------------
+constexpr int kRows = 4;
+
+template <int FMT, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes,
+                                                         uint8_t* __restrict__ scales, int T, int n, int ldx, int ldc,
+                                                         int nb) {
+  constexpr int E = BF16 ? 8 : 4, G = 32 / E, esz = BF16 ? 2 : 4;
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
+  const int step = gridDim.y * blockDim.y;
+  // the whole block leaves the loop together: shuffles need every lane
+  for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kRows) {
+    float v[kRows][E];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int t = t0 + r * step + threadIdx.y;
+      load_unit<BF16, VEC>((const uint8_t*)x + (size_t)t * ldx * esz, c, t < T ? n : 0, v[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int t = t0 + r * step + threadIdx.y;
+      uint32_t w[E / 4];
+      const uint32_t b = encode_unit<FMT, E>(v[r], w);
+      if (t < T) {
+        store_codes<E, VEC>(codes + (size_t)t * ldc, c, n, w);
+        if ((threadIdx.x & (G - 1)) == 0 && c < n) scales[(size_t)t * nb + c / 32] = (uint8_t)b;
+      }
+    }
+  }
+}
+
+template <int FMT, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __restrict__ codes,
+                                                           const uint8_t* __restrict__ scales, void* __restrict__ x,
+                                                           int T, int n, int ldc, int ldx, int nb) {
+  constexpr int E = BF16 ? 8 : 4;
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
+  if (c >= n) return;
+  const int step = gridDim.y * blockDim.y;
+  for (int t0 = blockIdx.y * blockDim.y + threadIdx.y; t0 < T; t0 += step * kRows) {
+    uint32_t w[kRows][E / 4];
+    uint32_t b[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int t = t0 + r * step;
+      if (t < T) {
+        load_codes<E, VEC>(codes + (size_t)t * ldc, c, n, w[r]);
+        b[r] = scales[(size_t)t * nb + c / 32];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int t = t0 + r * step;
+      if (t >= T) break;
+      const float s = scale_up(b[r]);
+      float v[E];
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) {
+        const float4 f = decode4<FMT>(w[r][k], s);
+        v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
+      }
+      if (BF16) {
+        uint16_t* dst = (uint16_t*)x + (size_t)t * ldx + c;
+        if (VEC && c + E <= n) {
+          *(uint4*)dst = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[E - 4], v[E - 3]),
+                                    pack_bf2(v[E - 2], v[E - 1]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (c + i < n) dst[i] = f2bf(v[i]);
+        }
+      } else {
+        float* dst = (float*)x + (size_t)t * ldx + c;
+        if (VEC && c + E <= n) {
+          *(float4*)dst = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (c + i < n) dst[i] = v[i];
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// RMSNorm forward that keeps its input: one pass over x writes y, rstd and
+// the 8-bit block form (7 bytes a value instead of the 6 of the plain
+// forward). A 128-thread block per row; a thread holds V float4 of the row in
+// registers, eight neighbouring lanes hold a block of 32 columns.
+// ---------------------------------------------------------------------------
+constexpr int kFwdThreads = 128;
+
+template <int FMT, int V>
+__global__ void __launch_bounds__(kFwdThreads)
+    rmsnorm_fwd_ckpt8_kernel(const float* __restrict__ x, const float* __restrict__ w, uint16_t* __restrict__ y,
+                             float* __restrict__ rstd, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                             int h, int nb, float eps) {
+  __shared__ float red[kFwdThreads / 32];
+  const size_t t = blockIdx.x;
+  const float4* xr = (const float4*)(x + t * h);
+  const float4* w4 = (const float4*)w;
+  const int n4 = h >> 2, tid = threadIdx.x;
+  float4 v[V];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int i = tid + k * kFwdThreads;
+    v[k] = i < n4 ? __ldcs(xr + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) ss += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+  ss = warp_sum(ss);
+  if ((tid & 31) == 0) red[tid >> 5] = ss;
+  // the checkpoint does not need the norm: its stores go out during the reduction
+  uint32_t* crow = (uint32_t*)(codes + t * h);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int i = tid + k * kFwdThreads;
+    const float u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t q[1];
+    const uint32_t b = encode_unit<FMT, 4>(u, q);
+    if (i < n4) {
+      crow[i] = q[0];
+      if ((tid & 7) == 0) scales[t * nb + i / 8] = (uint8_t)b;
+    }
+  }
+  __syncthreads();
+  ss = (red[0] + red[1]) + (red[2] + red[3]);
+  const float r = rsqrtf(ss / (float)h + eps);
+  if (tid == 0) rstd[t] = r;
+  uint2* yr = (uint2*)(y + t * h);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int i = tid + k * kFwdThreads;
+    if (i < n4) {
+      const float4 g = w4[i];
+      yr[i] = make_uint2(pack_bf2(v[k].x * r * g.x, v[k].y * r * g.y), pack_bf2(v[k].z * r * g.z, v[k].w * r * g.w));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// RMSNorm backward that reads its input from the 8-bit form:
+//   xh = x' rstd, dx = resid + rstd (dy w - xh mean(dy w xh)), dw = sum_t dy xh,
+// x' the checkpoint's values. Blocks take rows in turn (row t belongs to part
+// t mod parts, so a part's sum has a fixed order) and hold their share of dw
+// in registers; a second kernel adds the parts in order.
+// ---------------------------------------------------------------------------
+constexpr int kBwdThreads = 256;
+constexpr int kBwdParts = 456;  // three blocks on each of 152 SMs
+
+template <int FMT, int V>
+__global__ void __launch_bounds__(kBwdThreads)
+    rmsnorm_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                             const float* __restrict__ w, const float* __restrict__ rstd,
+                             const float* __restrict__ dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
+                             float* __restrict__ part, int T, int h, int nb) {
+  __shared__ float red[2][kBwdThreads / 32];
+  const int n4 = h >> 2, tid = threadIdx.x;
+  const float inv_h = 1.f / (float)h;
+  const float4* w4 = (const float4*)w;
+  float4 acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int flip = 0;
+#pragma unroll 1
+  for (int t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
+    float4 xv[V], gv[V], rv[V];
+    uint32_t q[V], b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = tid + j * kBwdThreads;
+      if (i < n4) {
+        q[j] = __ldcs((const uint32_t*)(codes + (size_t)t * h) + i);
+        b[j] = scales[(size_t)t * nb + i / 8];
+        gv[j] = __ldcs((const float4*)(dy + (size_t)t * h) + i);
+        if (resid) rv[j] = ((const float4*)(resid + (size_t)t * h))[i];
+      }
+    }
+    const float r = rstd[t];
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = tid + j * kBwdThreads;
+      if (i < n4) {
+        const float4 wv = w4[i];
+        xv[j] = decode4<FMT>(q[j], scale_up(b[j]));
+        dot += gv[j].x * wv.x * xv[j].x + gv[j].y * wv.y * xv[j].y + gv[j].z * wv.z * xv[j].z +
+               gv[j].w * wv.w * xv[j].w;
+      }
+    }
+    dot = warp_sum(dot);
+    if ((tid & 31) == 0) red[flip][tid >> 5] = dot;
+    __syncthreads();  // two buffers in turn: one barrier a row is enough
+    dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBwdThreads / 32; ++i) dot += red[flip][i];
+    const float mean = dot * r * inv_h;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = tid + j * kBwdThreads;
+      if (i < n4) {
+        const float4 wv = w4[i];
+        const float4 xh = make_float4(xv[j].x * r, xv[j].y * r, xv[j].z * r, xv[j].w * r);
+        float4 o = make_float4(r * (gv[j].x * wv.x - xh.x * mean), r * (gv[j].y * wv.y - xh.y * mean),
+                               r * (gv[j].z * wv.z - xh.z * mean), r * (gv[j].w * wv.w - xh.w * mean));
+        if (resid) {
+          o.x += rv[j].x;
+          o.y += rv[j].y;
+          o.z += rv[j].z;
+          o.w += rv[j].w;
+        }
+        ((float4*)(dx + (size_t)t * h))[i] = o;
+        if (dxb) ((uint2*)(dxb + (size_t)t * h))[i] = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
+        acc[j].x += gv[j].x * xh.x;
+        acc[j].y += gv[j].y * xh.y;
+        acc[j].z += gv[j].z * xh.z;
+        acc[j].w += gv[j].w * xh.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = tid + j * kBwdThreads;
+    if (i < n4) ((float4*)(part + (size_t)blockIdx.x * h))[i] = acc[j];
+  }
+}
+
+// out[c] = sum over the parts, in a fixed order: 16 warps take the parts in
+// turn for 32 columns, then their sums are added in warp order.
+__global__ void __launch_bounds__(512) sum_parts_kernel(const float* __restrict__ part, int nparts, int n,
+                                                        float* __restrict__ out) {
+  __shared__ float red[16][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < n) {
+#pragma unroll 8
+    for (int p = w; p < nparts; p += 16) s += part[(size_t)p * n + c];
+  }
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < n) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[i][lane];
+    out[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// SwiGLU forward and backward around an 8-bit g|u. Columns of g and of u are
+// cut into blocks of 32 separately. A thread owns 8 columns of g and the
+// same 8 of u, four lanes a block.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid_(float g) { return 1.f / (1.f + __expf(-g)); }
+constexpr int kSwRows = 2;
+
+template <int FMT, bool VEC>
+__global__ void __launch_bounds__(256) swiglu_fwd_ckpt8_kernel(const uint16_t* __restrict__ gu,
+                                                               uint16_t* __restrict__ act,
+                                                               uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales, int T, int F, int ld,
+                                                               int nb) {
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const int step = gridDim.y * blockDim.y;
+  for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kSwRows) {
+    float g[kSwRows][8], u[kSwRows][8];
+#pragma unroll
+    for (int r = 0; r < kSwRows; ++r) {
+      const int t = t0 + r * step + threadIdx.y;
+      const uint16_t* row = gu + (size_t)t * 2 * ld;
+      load_unit<true, VEC>(row, c, t < T ? F : 0, g[r]);
+      load_unit<true, VEC>(row + ld, c, t < T ? F : 0, u[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kSwRows; ++r) {
+      const int t = t0 + r * step + threadIdx.y;
+      uint32_t wg[2], wu[2];
+      const uint32_t bg = encode_unit<FMT, 8>(g[r], wg), bu = encode_unit<FMT, 8>(u[r], wu);
+      if (t < T) {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = g[r][i] * sigmoid_(g[r][i]) * u[r][i];
+        uint8_t* crow = codes + (size_t)t * 2 * ld;
+        uint16_t* arow = act + (size_t)t * ld;
+        // columns F..ld-1 are padding: codes and act are 0 there (the loads gave 0)
+        store_codes<8, VEC>(crow, c, ld, wg);
+        store_codes<8, VEC>(crow + ld, c, ld, wu);
+        if (VEC && c + 8 <= ld) {
+          *(uint4*)(arow + c) = make_uint4(pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3]), pack_bf2(a[4], a[5]),
+                                           pack_bf2(a[6], a[7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < ld) arow[c + i] = f2bf(a[i]);
+        }
+        if ((threadIdx.x & 3) == 0 && c < F) {
+          scales[(size_t)t * 2 * nb + c / 32] = (uint8_t)bg;
+          scales[(size_t)t * 2 * nb + nb + c / 32] = (uint8_t)bu;
+        }
+      }
+    }
+  }
+}
+
+// dg = dact u silu'(g), du = dact silu(g), with g and u from the 8-bit form.
+template <int FMT, bool VEC>
+__global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes,
+                                                               const uint8_t* __restrict__ scales,
+                                                               const uint16_t* __restrict__ dact,
+                                                               uint16_t* __restrict__ dgu, int T, int F, int ld,
+                                                               int nb) {
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  if (c >= ld) return;
+  const int step = gridDim.y * blockDim.y;
+  for (int t0 = blockIdx.y * blockDim.y + threadIdx.y; t0 < T; t0 += step * kSwRows) {
+    uint32_t wg[kSwRows][2], wu[kSwRows][2], bg[kSwRows], bu[kSwRows];
+    float d[kSwRows][8];
+#pragma unroll
+    for (int r = 0; r < kSwRows; ++r) {
+      const int t = t0 + r * step;
+      if (t < T) {
+        const uint8_t* crow = codes + (size_t)t * 2 * ld;
+        load_codes<8, VEC>(crow, c, F, wg[r]);
+        load_codes<8, VEC>(crow + ld, c, F, wu[r]);
+        // a unit that lies in the padding has no block of its own
+        bg[r] = c < F ? scales[(size_t)t * 2 * nb + c / 32] : 0u;
+        bu[r] = c < F ? scales[(size_t)t * 2 * nb + nb + c / 32] : 0u;
+        load_unit<true, VEC>(dact + (size_t)t * ld, c, F, d[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kSwRows; ++r) {
+      const int t = t0 + r * step;
+      if (t >= T) break;
+      const float sg = scale_up(bg[r]), su = scale_up(bu[r]);
+      float og[8], ou[8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 g4 = decode4<FMT>(wg[r][k], sg), u4 = decode4<FMT>(wu[r][k], su);
+        const float gg[4] = {g4.x, g4.y, g4.z, g4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s = sigmoid_(gg[i]), dd = d[r][4 * k + i];
+          og[4 * k + i] = dd * uu[i] * s * (1.f + gg[i] * (1.f - s));
+          ou[4 * k + i] = dd * gg[i] * s;
+        }
+      }
+      uint16_t* row = dgu + (size_t)t * 2 * ld;
+      if (VEC && c + 8 <= F) {
+        *(uint4*)(row + c) = make_uint4(pack_bf2(og[0], og[1]), pack_bf2(og[2], og[3]), pack_bf2(og[4], og[5]),
+                                        pack_bf2(og[6], og[7]));
+        *(uint4*)(row + ld + c) = make_uint4(pack_bf2(ou[0], ou[1]), pack_bf2(ou[2], ou[3]), pack_bf2(ou[4], ou[5]),
+                                             pack_bf2(ou[6], ou[7]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < ld) {  // padding columns carry no gradient
+            row[c + i] = c + i < F ? f2bf(og[i]) : (uint16_t)0;
+            row[ld + c + i] = c + i < F ? f2bf(ou[i]) : (uint16_t)0;
+          }
+      }
+    }
+  }
+}
+
+// Block and grid of the 2D kernels: units of E columns along x, rows along y.
+struct Shape2 {
+  dim3 grid, block;
+};
+Shape2 shape2(int T, int units, int rows) {
+  int bx = 8;
+  while (bx < units && bx < 256) bx *= 2;
+  const int by = 256 / bx;
+  const int gy = (T + by * rows - 1) / (by * rows);
+  return {dim3((unsigned)((units + bx - 1) / bx), (unsigned)std::min(gy, 65535)), dim3((unsigned)bx, (unsigned)by)};
+}
+
+inline int blocks32(int n) { return (n + 31) / 32; }
+inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline int done(int launches) {
+  count_launches(launches);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+// Sizes: row and column counters stay within 31 bits with room for a grid's step.
+inline bool dims_ok(int T, int n, int ld) { return T > 0 && n > 0 && ld >= n && T <= (1 << 30) && ld <= (1 << 29); }
+inline bool fmt_ok(int fmt) { return fmt == FMT_I8 || fmt == FMT_E4M3; }
+
+}  // namespace
+
+int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scales, int T, int n, int ldx, int ldc,
+               cudaStream_t st) {
+  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
+  const int E = bf16 ? 8 : 4, nb = blocks32(n);
+  const Shape2 s = shape2(T, (n + E - 1) / E, kRows);
+  // whole 16-byte loads and E-byte stores where every row starts on such a boundary
+  const bool vec = al(x, 16) && ldx % E == 0 && al(codes, E) && ldc % E == 0;
+  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(x, codes, scales, T, n, ldx, ldc, nb); };
+  if (fmt == FMT_I8) {
+    if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
+    else vec ? go(ckpt8_pack_kernel<FMT_I8, false, true>) : go(ckpt8_pack_kernel<FMT_I8, false, false>);
+  } else {
+    if (bf16) vec ? go(ckpt8_pack_kernel<FMT_E4M3, true, true>) : go(ckpt8_pack_kernel<FMT_E4M3, true, false>);
+    else vec ? go(ckpt8_pack_kernel<FMT_E4M3, false, true>) : go(ckpt8_pack_kernel<FMT_E4M3, false, false>);
+  }
+  return done(1);
+}
+
+int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, bool bf16, int T, int n, int ldc,
+                 int ldx, cudaStream_t st) {
+  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
+  const int E = bf16 ? 8 : 4, nb = blocks32(n);
+  const Shape2 s = shape2(T, (n + E - 1) / E, kRows);
+  const bool vec = al(x, 16) && ldx % E == 0 && al(codes, E) && ldc % E == 0;
+  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, x, T, n, ldc, ldx, nb); };
+  if (fmt == FMT_I8) {
+    if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
+    else vec ? go(ckpt8_unpack_kernel<FMT_I8, false, true>) : go(ckpt8_unpack_kernel<FMT_I8, false, false>);
+  } else {
+    if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_E4M3, true, true>) : go(ckpt8_unpack_kernel<FMT_E4M3, true, false>);
+    else vec ? go(ckpt8_unpack_kernel<FMT_E4M3, false, true>) : go(ckpt8_unpack_kernel<FMT_E4M3, false, false>);
+  }
+  return done(1);
+}
+
+int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, uint8_t* codes, uint8_t* scales,
+                      int fmt, int T, int h, float eps, cudaStream_t st) {
+  if (T <= 0 || h <= 0 || (h & 3) || h > 16 * 4 * kFwdThreads || !fmt_ok(fmt) || !al(x, 16) || !al(w, 16) ||
+      !al(y, 8) || !al(codes, 4))
+    return -1;
+  const int n4 = h / 4, nb = blocks32(h);
+  auto go = [&](auto k) { k<<<T, kFwdThreads, 0, st>>>(x, w, y, rstd, codes, scales, h, nb, eps); };
+  auto pick = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (n4 <= kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 1>);
+    else if (n4 <= 2 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 2>);
+    else if (n4 <= 4 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 4>);
+    else if (n4 <= 8 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 8>);
+    else go(rmsnorm_fwd_ckpt8_kernel<F, 16>);
+  };
+  if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
+  else pick(std::integral_constant<int, FMT_E4M3>());
+  return done(1);
+}
+
+size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)std::min(T, kBwdParts) * h; }
+
+int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
+                      const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,
+                      int T, int h, cudaStream_t st) {
+  if (T <= 0 || h <= 0 || (h & 3) || h > 8 * 4 * kBwdThreads || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) ||
+      !al(dy, 16) || !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
+    return -1;
+  const int n4 = h / 4, nb = blocks32(h), parts = std::min(T, kBwdParts);
+  auto go = [&](auto k) {
+    k<<<parts, kBwdThreads, 0, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb);
+  };
+  auto pick = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (n4 <= kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 1>);
+    else if (n4 <= 2 * kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 2>);
+    else if (n4 <= 4 * kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 4>);
+    else go(rmsnorm_bwd_ckpt8_kernel<F, 8>);
+  };
+  if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
+  else pick(std::integral_constant<int, FMT_E4M3>());
+  sum_parts_kernel<<<(h + 31) / 32, 512, 0, st>>>(work, parts, h, dw);
+  return done(2);
+}
+
+int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t* scales, int fmt, int T, int F,
+                     int ld, cudaStream_t st) {
+  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return -1;
+  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows);
+  const bool vec = ld % 8 == 0 && al(gu, 16) && al(act, 16) && al(codes, 8);
+  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(gu, act, codes, scales, T, F, ld, blocks32(F)); };
+  if (fmt == FMT_I8) vec ? go(swiglu_fwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_I8, false>);
+  else vec ? go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, false>);
+  return done(1);
+}
+
+int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const uint16_t* dact, uint16_t* dgu,
+                     int T, int F, int ld, cudaStream_t st) {
+  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return -1;
+  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows);
+  const bool vec = ld % 8 == 0 && al(dact, 16) && al(dgu, 16) && al(codes, 8);
+  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
+  if (fmt == FMT_I8) vec ? go(swiglu_bwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_I8, false>);
+  else vec ? go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, false>);
+  return done(1);
+}
+
+}  // namespace mt

@@ -138,6 +138,43 @@ int ce_finalize(const float2* part, int nslices, const float* zlab, float* lse, 
 int ce_slice_grad(const float* logits, int T, int R, int ld, int row0, const int32_t* labels, const float* lse,
                   float scale, uint16_t* dz, cudaStream_t st);
 
+// Activation checkpoints in 8 bits (ckpt8.cu): blocks of 32 columns with one
+// power-of-two scale byte each, fmt MT_CKPT_I8 or MT_CKPT_E4M3; a row has
+// ceil(n / 32) scale bytes (SwiGLU: ceil(F / 32) for g, then as many for u).
+int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scales, int T, int n, int ldx, int ldc,
+               cudaStream_t st);
+int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, bool bf16, int T, int n, int ldc,
+                 int ldx, cudaStream_t st);
+int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, uint8_t* codes, uint8_t* scales,
+                      int fmt, int T, int h, float eps, cudaStream_t st);
+size_t rmsnorm_bwd_ckpt8_partials(int T, int h);  // floats of workspace
+int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
+                      const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,
+                      int T, int h, cudaStream_t st);
+int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t* scales, int fmt, int T, int F,
+                     int ld, cudaStream_t st);
+int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const uint16_t* dact, uint16_t* dgu,
+                     int T, int F, int ld, cudaStream_t st);
+
+// Log probabilities of given tokens, entropy and top-k of rows of logits
+// times c, and the logits' gradient (token_logprobs.cu). ent may be null; no
+// top outputs with k = 0; g_logp or g_ent may be null.
+int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k, float* lse, float* logp, float* ent,
+                   int32_t* top_ids, float* top_logp, int T, int V, int ld, cudaStream_t st);
+int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, const float* lse, const float* ent,
+                       const float* g_logp, const float* g_ent, void* dz, bool dz_bf16, int T, int V, int ld, int ldd,
+                       cudaStream_t st);
+
+// Embedding lookup with a scale and the table's gradient by sorted tokens
+// (embedding.cu). work: embed_bwd_workspace bytes, 256-byte aligned.
+int embed_fwd(const void* table, bool table_bf16, const int32_t* ids, float scale, void* out, bool out_bf16, int T,
+              int V, int h, cudaStream_t st);
+size_t embed_bwd_workspace(int T, int V, int h);
+int embed_bwd(const int32_t* ids, const void* dout, bool dout_bf16, float scale, void* dtable, bool dtable_bf16,
+              bool add, void* work, int T, int V, int h, cudaStream_t st);
+uint32_t token_logprobs_take_device_error();
+uint32_t embedding_take_device_error();
+
 // Read and clear the device error words of the kernels that wait on
 // barriers (0 = no error). Synchronous with respect to the device.
 uint32_t gemm_take_device_error();
