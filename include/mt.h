@@ -545,21 +545,22 @@ int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const
  *   entropy[t] = -sum_j p_j log p_j (null: not wanted), and the k most
  *   likely tokens, top_ids / top_logp [T, k] in descending order, equal
  *   logits by ascending index (k in [0, min(32, V)]; null with k = 0).
- * Logits at or below -1e30 (-inf, a type's lowest value) are masked out:
+ * Logits at or below -2^100 (-inf, a type's lowest value) are masked out:
  * probability 0, log probability -inf, never listed (places that remain hold
  * -1 and -inf). A row with nothing left has lse = logp = -inf, entropy 0. A
- * row with a NaN or +inf has NaN for all four and -1. ids[t] < 0: the row is
- * not scored; its logits are not read, its outputs are 0 and its top_ids -1.
- * ids[t] >= V: outputs NaN and -1, and a bit in mt_op_device_error. ids are
- * device int32, everything else fp32; inv_temp in [1e-30, 1e30]. */
+ * row with a NaN or a logit of 2^100 or more has NaN for all four and -1.
+ * ids[t] < 0: the row is not scored; its logits are not used, its outputs are
+ * 0 and its top_ids -1. ids[t] >= V: outputs NaN and -1, and a bit in
+ * mt_op_device_error. ids are device int32, everything else fp32; inv_temp in
+ * [1e-6, 1e6]. */
 int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, float inv_temp, int k, float* lse,
                          float* logp, float* entropy, int32_t* top_ids, float* top_logp, int T, int V, int ld,
                          void* stream);
 
 /* Its gradient: dlogits [T, V] (d_dtype, row stride ldd) =
  *   inv_temp * (g_logp ([j = id] - p_j) - g_entropy p_j (log p_j + entropy)),
- * p = e^{z - lse}, for given g_logp and g_entropy [T] (either may be null:
- * zero); lse and entropy as the forward wrote them (entropy is read only with
+ * p = e^{z - lse} (good to about 2^-24 |lse|: lse is fp32), for given g_logp
+ * and g_entropy [T] (either may be null: zero); lse and entropy as the forward wrote them (entropy is read only with
  * g_entropy). Rows not scored and rows with nothing left get 0. dlogits may
  * be logits itself when type and stride are the same. */
 int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, float inv_temp, const float* lse,

@@ -512,9 +512,9 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
+    if stream is None:  # the current stream's handle, without building a Stream object for every launch
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream)
 
 

@@ -5,12 +5,13 @@
 //   S = sum_j e^{d_j},  A = sum_j e^{d_j} d_j
 //   lse = c m + ln S,  log p_j = d_j - ln S,  H = ln S - A / S
 // Forward: one pass over the logits with a running (m, S, A) per thread, in
-// 32 bits; differences from the maximum are formed before the scaling, so
-// neither large logits nor masks of the type's lowest value overflow, and
-// log p near 0 keeps its absolute accuracy. The k largest logits come from
-// the same pass (see TopList). Backward: with p_j = e^{c z_j - lse},
+// 32 bits and log2 units (e^d = 2^{c2 (z - m)}, c2 = c log2 e; the difference
+// is formed first, so large logits cost no accuracy). The k largest logits
+// come from the maxima of that pass (see below). Backward: with p_j = e^{c z_j - lse},
 //   dz_j = c (g_logp ([j = t] - p_j) - g_H p_j (log p_j + H)).
-// Both directions are bound by reading the logits (and writing the gradient).
+// Both directions are bound by reading the logits (and writing the gradient)
+// where there are many; 16-bit logits come close to the issue rate too, so
+// maxima and clamps are taken on packed pairs and sums on pairs of fp32.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -26,36 +27,69 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kFar = -1000.f;  // 2^kFar is 0, and 0 * kFar too: stands for -inf in sums of e d
 constexpr int kMaxTop = 32;
+// Logits at or below -kBig (-inf, a mask of the type's lowest value) are
+// masked out; a row with one at or above kBig (or a NaN) has no distribution.
+// 2^100 is a bf16 value too, and kBig * c stays finite for every allowed c.
+constexpr float kBig = 1.2676506002282294e30f;
+constexpr uint32_t kBigPair = 0xf180f180u;  // two bf16 -2^100
+constexpr float kMinScale = 1e-6f, kMaxScale = 1e6f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+// NaN if any argument is.
+__device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Pairs of fp32 in one register pair.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-// Running statistics of a set of logits: largest, sum of 2^d, sum of 2^d d,
-// d = c2 (z - m) in log2 units. The empty set has m = -FLT_MAX, s = 0.
+// Statistics of a set of logits: the largest, and the sums of 2^d and 2^d d
+// with d = c2 (z - m).
 struct Stat {
   float m, s, a;
 };
-__device__ __forceinline__ void rescale(Stat& x, float m, float c2) {
-  const float d = fmaxf((x.m - m) * c2, kFar), r = ex2(d);
-  x.a = (x.a + d * x.s) * r;
-  x.s *= r;
-  x.m = m;
-}
-__device__ __forceinline__ Stat merge(Stat x, Stat y, float c2) {
-  const float m = fmaxf(x.m, y.m);
-  rescale(x, m, c2);
-  rescale(y, m, c2);
-  return {m, x.s + y.s, x.a + y.a};
+__device__ __forceinline__ Stat merge(const Stat& x, const Stat& y, float c2) {
+  const float m = fmaxf(x.m, y.m), dx = (x.m - m) * c2, dy = (y.m - m) * c2;
+  const float ex = ex2(dx), ey = ex2(dy);
+  return {m, x.s * ex + y.s * ey, (x.a + dx * x.s) * ex + (y.a + dy * y.s) * ey};
 }
 
 // Order-preserving whole number of a float (no NaN); both zeros get one.
@@ -66,46 +100,79 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-// Logits at or below kMasked count as masked out, like -inf (a mask of the
-// type's lowest value): probability 0, never listed.
-constexpr float kMasked = -1e30f;
-constexpr uint32_t kKeyNone = 0xeb60d35u;  // key of kMasked: an empty place of a list
+constexpr uint32_t kKeyNone = ~0xf1800000u;  // key of -kBig: masked out, or nothing there
 
-// The k best (value, then lower index) that a warp has seen, place j in lane j.
-struct TopList {
-  uint32_t key, idx;
-  __device__ __forceinline__ void insert(uint32_t k, uint32_t i, uint32_t lane) {
-    const bool stays = key > k || (key == k && idx < i);
-    const int at = __popc(__ballot_sync(0xffffffffu, stays));
-    const uint32_t pk = __shfl_up_sync(0xffffffffu, key, 1), pi = __shfl_up_sync(0xffffffffu, idx, 1);
-    if ((int)lane == at) {
-      key = k;
-      idx = i;
-    } else if ((int)lane > at) {
-      key = pk;
-      idx = pi;
-    }
+// The lanes' sets joined: one maximum, each lane's sums brought to it, then
+// plain sums in a fixed order.
+__device__ __forceinline__ Stat warp_join(Stat x, float c2) {
+  const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(x.m))), d = (x.m - m) * c2, e = ex2(d);
+  x.a = (x.a + d * x.s) * e;
+  x.s *= e;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x.s += __shfl_xor_sync(0xffffffffu, x.s, o);
+    x.a += __shfl_xor_sync(0xffffffffu, x.a, o);
   }
-};
+  x.m = m;
+  return x;
+}
 
-// The k-th largest of the warp's 32 keys.
-__device__ __forceinline__ uint32_t warp_kth(uint32_t key, int k, uint32_t lane) {
+// The warp's 32 keys in descending order.
+__device__ __forceinline__ uint32_t warp_sort(uint32_t key, uint32_t lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size *= 2)
 #pragma unroll
     for (int o = size / 2; o > 0; o /= 2) {
       const uint32_t other = __shfl_xor_sync(0xffffffffu, key, o);
-      const bool down = (lane & size) == 0;            // descending runs
-      const bool low = (lane & o) == 0;
-      key = (low == down) ? max(key, other) : min(key, other);
+      key = ((lane & o) == 0) == ((lane & size) == 0) ? max(key, other) : min(key, other);
     }
-  return __shfl_sync(0xffffffffu, key, k - 1);
+  return key;
+}
+// The 32 largest of two descending lists, descending.
+__device__ __forceinline__ uint32_t warp_merge(uint32_t a, uint32_t b, uint32_t lane) {
+  uint32_t key = max(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, key, o);
+    key = (lane & o) == 0 ? max(key, other) : min(key, other);
+  }
+  return key;
 }
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 16;  // logits a thread holds at a time
+constexpr int kMaxThreads = 512;
+constexpr int kVecs = 4;  // 16-byte vectors a thread holds at a time
 constexpr int kMaxCluster = 8;
+constexpr int kSegs = 32;
+
+// A block's shared memory. cap: logits that may reach the bound before the
+// slow search takes over.
+struct Smem {
+  uint2 *cand, *list;  // [cap]; [C * k], k of each block, best first (the first block's is used)
+  Stat* stat;          // [C * warps] (the first block's)
+  uint32_t* key;       // [warps][32]
+  float* seg;          // [segments][threads]
+  uint16_t* hot;       // [cap] segment * threads + thread
+};
+__host__ __device__ inline size_t smem_layout(uint8_t* base, int NT, int C, int k, int cap, int segs, Smem* o) {
+  size_t x = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base + x;
+    x += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  const int nw = NT / 32;
+  Smem m;
+  m.stat = (Stat*)take((size_t)C * nw * sizeof(Stat));
+  if (k > 0) {
+    m.cand = (uint2*)take((size_t)cap * 8);
+    m.list = (uint2*)take((size_t)C * k * 8);
+    m.key = (uint32_t*)take((size_t)nw * 128);
+    m.seg = (float*)take((size_t)segs * NT * 4);
+    m.hot = (uint16_t*)take((size_t)cap * 2);
+  }
+  *o = m;
+  return x;
+}
 
 struct FwdArgs {
   const void* z;
@@ -114,6 +181,7 @@ struct FwdArgs {
   int32_t* top_ids;
   int T, V, ld, k;
   float c;
+  int C, G, cap, segs;  // blocks a row, chunks a segment, see Smem
 };
 
 // Vectors (16 bytes) of a row between its unaligned ends.
@@ -133,6 +201,11 @@ struct RowView {
     return BF16 ? bf2f(((const uint16_t*)p)[i]) : ((const float*)p)[i];
   }
   __device__ __forceinline__ const uint4* vec(int v) const { return (const uint4*)(p + (size_t)head * esz) + v; }
+  // End logit e (0..7 the head's, 8..15 the tail's) of a block that owns those ends, or -1.
+  __device__ __forceinline__ int end_index(int e, bool lo, bool hi, int V) const {
+    if (e < 8) return lo && e < head ? e : -1;
+    return hi && e < 16 && tail0 + e - 8 < V ? tail0 + e - 8 : -1;
+  }
 };
 template <bool BF16>
 __device__ __forceinline__ void spread(const uint4& u, float* out) {
@@ -148,238 +221,317 @@ __device__ __forceinline__ void spread(const uint4& u, float* out) {
   }
 }
 
-// A cluster of C blocks per row (C = 1 for many rows; more where the rows
-// alone would leave SMs idle), each over its part of the row's vectors; the
-// blocks' statistics and lists are joined in the first one's shared memory.
+// A thread's running statistics, sums kept as pairs.
+struct Run {
+  float m;
+  uint64_t s, a;
+  bool bad;
+};
+// One chunk of kVecs vectors. Masked logits are raised to -kBig, where 2^d is
+// 0 and 2^d d too.
+template <bool BF16>
+__device__ __forceinline__ float take(Run& r, uint4 (&u)[kVecs], float c2) {
+  float cm;
+  if (BF16) {
+    uint32_t top = kBigPair;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      u[j].x = max_nan_bf2(u[j].x, kBigPair);
+      u[j].y = max_nan_bf2(u[j].y, kBigPair);
+      u[j].z = max_nan_bf2(u[j].z, kBigPair);
+      u[j].w = max_nan_bf2(u[j].w, kBigPair);
+      top = max_nan_bf2(top, max_nan_bf2(max_nan_bf2(u[j].x, u[j].y), max_nan_bf2(u[j].z, u[j].w)));
+    }
+    cm = max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+  } else {
+    cm = -kBig;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float* f = (float*)&u[j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = max_nan(f[i], -kBig);
+      cm = max3_nan(cm, f[0], f[1]);
+      cm = max3_nan(cm, f[2], f[3]);
+    }
+  }
+  r.bad |= !(cm < kBig);
+  const float m = fmaxf(r.m, cm), d0 = (r.m - m) * c2, e0 = ex2(d0);
+  const uint64_t e02 = pair(e0, e0);
+  r.a = mul2(fma2(pair(d0, d0), r.s, r.a), e02);
+  r.s = mul2(r.s, e02);
+  r.m = m;
+  const uint64_t cc = pair(c2, c2), mm = pair(-m, -m);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    float z[BF16 ? 8 : 4];
+    spread<BF16>(u[j], z);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 8 : 4); i += 2) {
+      const uint64_t d = mul2(add2(pair(z[i], z[i + 1]), mm), cc);
+      float d0_, d1_;
+      unpair(d, d0_, d1_);
+      const uint64_t e = pair(ex2(d0_), ex2(d1_));
+      r.s = add2(r.s, e);
+      r.a = fma2(e, d, r.a);
+    }
+  }
+  return cm;
+}
+
+// Forward. A cluster of C blocks a row (C = 1 for many rows; more where the
+// rows alone would leave SMs idle), each over its part of the row's vectors;
+// the blocks' results are joined in the first one's shared memory.
+//
+// The k largest: with the threads' maxima, the k-th largest of them is a
+// value that at least k logits reach (kth below). Each thread also leaves the
+// maxima of up to kSegs segments of its logits (G chunks each) in shared
+// memory; the few segments that reach kth are read a second time, and their
+// logits that reach it are collected and ranked by (value, index). Where more
+// than cap do (rows of one value), the k are searched one by one.
+// Sorted lists kept while streaming took 230 us more for k = 8 on 8192 x
+// 128256 fp32 rows (828 against 598 us without a list), and reading all of
+// the k best threads' logits again 137 us more, since DRAM moves 64 bytes for
+// every 16 of them.
 template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(FwdArgs a, int C) {
+__global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) {
   using R = RowView<BF16>;
-  constexpr int U = kChunk / R::E;  // vectors a thread holds at a time
-  __shared__ Stat sh_stat[kMaxCluster * kWarps];
-  __shared__ uint32_t sh_key[TOP ? kMaxCluster * kWarps : 1][kMaxTop], sh_idx[TOP ? kMaxCluster * kWarps : 1][kMaxTop];
-  __shared__ int sh_bad;
-  __shared__ uint32_t sh_thr;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ uint32_t sh_kth;
+  __shared__ int sh_bad, sh_nhot, sh_n;
+  const int C = a.C, G = a.G, cap = a.cap;
   const int t = blockIdx.x / C, rank = blockIdx.x % C;
   const uint32_t lane = lane_id(), warp = warp_id();
+  const int tid = (int)threadIdx.x, NT = (int)blockDim.x, nw = NT >> 5;
+  Smem sm;
+  smem_layout(smem_raw, NT, C, a.k, cap, a.segs, &sm);
+  const R row(a.z, t, a.ld, a.V);
+  const float c2 = a.c * kLog2e;
+  const int v_lo = (int)((int64_t)row.nv * rank / C), v_hi = (int)((int64_t)row.nv * (rank + 1) / C);
+  const bool lo_end = rank == 0, hi_end = rank == C - 1;
+  const uint32_t none = BF16 ? kBigPair : 0xf1800000u;
+  auto fetch = [&](int v, uint4 (&u)[kVecs]) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      u[j] = v + j * NT < v_hi ? __ldcs(row.vec(v + j * NT)) : make_uint4(none, none, none, none);
+  };
+  // the first chunk is requested before the row's token is known: their
+  // latencies overlap
+  uint4 next[kVecs];
+  fetch(v_lo + tid, next);
   const int id = a.ids[t];
   if (id < 0 || id >= a.V) {  // the same for every block of the cluster
     if (rank == 0) {
       const float fill = id < 0 ? 0.f : __int_as_float(0x7fffffff);
-      if (threadIdx.x == 0) {
+      if (tid == 0) {
         a.lse[t] = fill;
         a.logp[t] = fill;
         if (a.ent) a.ent[t] = fill;
         if (id >= a.V) report_error(kErrBadArg);
       }
-      if (TOP && (int)threadIdx.x < a.k) {
-        a.top_ids[(size_t)t * a.k + threadIdx.x] = -1;
-        a.top_logp[(size_t)t * a.k + threadIdx.x] = fill;
+      if (TOP && tid < a.k) {
+        a.top_ids[(size_t)t * a.k + tid] = -1;
+        a.top_logp[(size_t)t * a.k + tid] = fill;
       }
     }
     return;
   }
-  if (threadIdx.x == 0) {
-    sh_bad = 0;
-    sh_thr = kKeyNone + 1;
-  }
-  __syncthreads();
+  if (tid == 0) sh_bad = 0, sh_nhot = 0, sh_n = 0;
   if (C > 1) cluster_sync();  // every block's shared memory is set up before another one writes to it
-  const R row(a.z, t, a.ld, a.V);
-  const float c2 = a.c * kLog2e;
-  const int v_lo = (int)((int64_t)row.nv * rank / C), v_hi = (int)((int64_t)row.nv * (rank + 1) / C);
-  Stat st{-FLT_MAX, 0.f, 0.f};
-  bool bad = false;
-  TopList top{kKeyNone, 0xffffffffu};
-  uint32_t tkey = kKeyNone + 1;  // values below cannot enter
-  float thr = of_key(kKeyNone + 1);
-  bool first = true;
-
-  // One chunk: z[i] is the logit of index index_of(i), -inf where there is none.
-  auto take = [&](const float (&z)[kChunk], auto index_of) {
-    float cm = z[0];
+  float given = 0.f;  // the given token's logit
+  if (rank == 0 && tid == 0) given = row.at(id);
+  Run run{-kBig, 0ull, 0ull, false};
+  {
+    float seg = -kBig;  // largest of this segment
+    int left = G, entry = tid;
+    for (int v = v_lo + tid; v < v_hi; v += NT * kVecs) {  // the next chunk's loads run under this one's sums
+      uint4 u[kVecs];
 #pragma unroll
-    for (int i = 1; i < kChunk; ++i) cm = max_nan(cm, z[i]);
-    bad |= !(cm <= FLT_MAX);
-    const float m = fmaxf(st.m, cm);
-    rescale(st, m, c2);
-    float s = 0.f, q = 0.f;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      const float d = fmaxf((z[i] - m) * c2, kFar);
-      const float e = ex2(d);
-      s += e;
-      q = fmaf(e, d, q);
-    }
-    st.s += s;
-    st.a += q;
-    if (TOP) {
-      if (first) {  // at least k logits of this chunk reach the k-th largest of the lanes' maxima
-        first = false;
-        tkey = max(tkey, warp_kth(key_of(cm), a.k, lane));
-        thr = of_key(tkey);
-      } else {
-        const uint32_t shared = *(volatile uint32_t*)&sh_thr;
-        if (shared > tkey) {
-          tkey = shared;
-          thr = of_key(tkey);
-        }
-      }
-      if (__any_sync(0xffffffffu, cm >= thr)) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) bits |= z[i] >= thr ? 1u << i : 0u;
-        while (true) {
-          const uint32_t who = __ballot_sync(0xffffffffu, bits != 0);
-          if (!who) break;
-          const int src = __ffs(who) - 1;
-          const int i = __ffs(bits) - 1;
-          float v = z[0];
-#pragma unroll
-          for (int j = 1; j < kChunk; ++j) v = i == j ? z[j] : v;
-          const uint32_t k = __shfl_sync(0xffffffffu, key_of(v), src);
-          const uint32_t x = __shfl_sync(0xffffffffu, (uint32_t)index_of(i), src);
-          if ((int)lane == src) bits &= bits - 1;
-          top.insert(k, x, lane);
-        }
-        // later logits of this warp have higher indexes: they must exceed its
-        // k-th best; another warp's must reach it
-        const uint32_t kth = __shfl_sync(0xffffffffu, top.key, a.k - 1);
-        if (kth > kKeyNone) {
-          if (lane == 0) atomicMax(&sh_thr, kth);
-          if (kth + 1 > tkey) {
-            tkey = kth + 1;
-            thr = of_key(tkey);
-          }
+      for (int j = 0; j < kVecs; ++j) u[j] = next[j];
+      fetch(v + NT * kVecs, next);
+      const float cm = take<BF16>(run, u, c2);
+      if (TOP) {
+        seg = fmaxf(seg, cm);
+        if (--left == 0) {
+          sm.seg[entry] = seg;
+          seg = -kBig;
+          left = G;
+          entry += NT;
         }
       }
     }
-  };
-
-  for (int v = v_lo + (int)warp * 32; v < v_hi; v += kThreads * U) {  // whole warps
-    float z[kChunk];
-    uint4 u[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int w = v + j * kThreads + (int)lane;
-      if (w < v_hi) u[j] = __ldcs(row.vec(w));
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (v + j * kThreads + (int)lane < v_hi) {
-        spread<BF16>(u[j], z + j * R::E);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R::E; ++i) z[j * R::E + i] = -INFINITY;
-      }
-    }
-    take(z, [&](int i) { return row.head + (v + (i / R::E) * kThreads + (int)lane) * R::E + i % R::E; });
+    if (TOP && left != G) sm.seg[entry] = seg;
   }
-  if (warp == 0) {  // the unaligned ends of the row: fewer than one vector each
-    const bool lo = rank == 0, hi = rank == C - 1;
-    int i0 = -1;
-    if (lane < 8) i0 = lo && (int)lane < row.head ? (int)lane : -1;
-    else if (lane < 16) i0 = hi && row.tail0 + (int)lane - 8 < a.V ? row.tail0 + (int)lane - 8 : -1;
-    if (__any_sync(0xffffffffu, i0 >= 0)) {
-      float z[kChunk];
+  const float tmax = run.m;  // of the whole vectors
+  {  // the unaligned ends of the row: fewer than one vector each
+    const int i = row.end_index(tid, lo_end, hi_end, a.V);
+    if (i >= 0) {
+      uint4 u[kVecs];
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) z[i] = -INFINITY;
-      if (i0 >= 0) z[0] = row.at(i0);
-      // indexes below those already listed may tie with the k-th best
-      if (TOP && !first) {
-        const uint32_t kth = __shfl_sync(0xffffffffu, top.key, a.k - 1);
-        if (tkey == kth + 1 && kth > kKeyNone) {
-          tkey = kth;
-          thr = of_key(tkey);
-        }
-      }
-      take(z, [&](int) { return i0; });
+      for (int j = 0; j < kVecs; ++j) u[j] = make_uint4(none, none, none, none);
+      u[0].x = BF16 ? (none & 0xffff0000u) | ((const uint16_t*)row.p)[i] : ((const uint32_t*)row.p)[i];
+      take<BF16>(run, u, c2);
     }
   }
 
   // join: lanes, then warps (and blocks) in order
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat y{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-           __shfl_xor_sync(0xffffffffu, st.a, o)};
-    st = merge(st, y, c2);
+  float s0, s1, a0, a1;
+  unpair(run.s, s0, s1);
+  unpair(run.a, a0, a1);
+  Stat st{run.m, s0 + s1, a0 + a1};
+  st = warp_join(st, c2);
+  const bool bad = __any_sync(0xffffffffu, run.bad);
+  auto put = [rank](void* p, uint32_t v) {  // to the first block's shared memory
+    if (rank == 0) *(volatile uint32_t*)p = v;
+    else asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(p, 0)), "r"(v) : "memory");
+  };
+  __syncthreads();  // sh_bad, sh_nhot and sh_n are set up
+  if (lane == 0) {
+    Stat* slot = &sm.stat[rank * nw + (int)warp];
+    put(&slot->m, __float_as_uint(st.m));
+    put(&slot->s, __float_as_uint(st.s));
+    put(&slot->a, __float_as_uint(st.a));
+    if (bad) put(&sh_bad, 1u);
   }
-  bad = __any_sync(0xffffffffu, bad);
-  {
-    // the first block's shared memory, as a cluster address where there is one
-    const int slot = rank * kWarps + (int)warp;
-    if (C == 1 || rank == 0) {
-      if (lane == 0) {
-        sh_stat[slot] = st;
-        if (bad) sh_bad = 1;
+
+  if (TOP) {
+    const uint32_t mine = max(key_of(tmax), kKeyNone);
+    uint32_t key = warp_sort(mine, lane);
+    for (int o = 1; o < nw; o *= 2) {  // the warps' lists joined pairwise
+      if ((warp & (2 * o - 1)) == (uint32_t)o) sm.key[warp * 32 + lane] = key;
+      __syncthreads();
+      if ((warp & (2 * o - 1)) == 0) key = warp_merge(key, sm.key[(warp + o) * 32 + lane], lane);
+    }
+    if (warp == 0 && (int)lane == a.k - 1) sh_kth = max(key, kKeyNone + 1);
+    __syncthreads();
+    const uint32_t kth = sh_kth;
+    const int chunks = v_lo + tid < v_hi ? (v_hi - v_lo - tid + NT * kVecs - 1) / (NT * kVecs) : 0;
+    if (mine >= kth) {
+      const float bound = of_key(kth);
+      for (int e = tid, c = 0; c < chunks; e += NT, c += G)
+        if (sm.seg[e] >= bound) {
+          const int at = atomicAdd(&sh_nhot, 1);
+          if (at < cap) sm.hot[at] = (uint16_t)e;
+        }
+    }
+    __syncthreads();
+    const int nhot = sh_nhot;
+    auto offer = [&](float z, int i) {
+      const uint32_t q = key_of(z);
+      if (q >= kth) {
+        const int at = atomicAdd(&sh_n, 1);
+        if (at < cap) sm.cand[at] = make_uint2(q, (uint32_t)i);
       }
-      if (TOP && (int)lane < a.k) {
-        sh_key[slot][lane] = top.key;
-        sh_idx[slot][lane] = top.idx;
+    };
+    // warps take the vectors of a segment in turn, a lane each
+    const int per = G * kVecs;
+    for (int q = (int)warp; q < min(nhot, cap); q += nw) {
+      const int e = sm.hot[q], x = e & (NT - 1), c = e / NT * per;
+      for (int j = (int)lane; j < per; j += 32) {
+        const int v = v_lo + x + (c + j) * NT;
+        if (v >= v_hi) break;
+        float z[R::E];
+        spread<BF16>(*row.vec(v), z);
+#pragma unroll
+        for (int i = 0; i < R::E; ++i) offer(z[i], row.head + v * R::E + i);
       }
+    }
+    const int end = row.end_index(tid, lo_end, hi_end, a.V);
+    if (end >= 0) offer(row.at(end), end);
+    __syncthreads();
+    const int n = max(sh_n, nhot);  // too many segments count as too many logits
+    auto list = [&](int place, uint2 e) {
+      put(&sm.list[rank * a.k + place].x, e.x);
+      put(&sm.list[rank * a.k + place].y, e.y);
+    };
+    if (n <= cap) {
+      for (int i = tid; i < sh_n; i += NT) {
+        const uint2 e = sm.cand[i];
+        int better = 0;
+        for (int j = 0; j < sh_n; ++j) {
+          const uint2 f = sm.cand[j];
+          better += f.x > e.x || (f.x == e.x && f.y < e.y) ? 1 : 0;
+        }
+        if (better < a.k) list(better, e);
+      }
+      if (tid >= sh_n && tid < a.k) list(tid, make_uint2(kKeyNone, 0xffffffffu));
     } else {
-      auto put = [](const void* p, uint32_t v) {
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(p, 0)), "r"(v) : "memory");
-      };
-      if (lane == 0) {
-        put(&sh_stat[slot].m, __float_as_uint(st.m));
-        put(&sh_stat[slot].s, __float_as_uint(st.s));
-        put(&sh_stat[slot].a, __float_as_uint(st.a));
-        if (bad) put(&sh_bad, 1u);
-      }
-      if (TOP && (int)lane < a.k) {
-        put(&sh_key[slot][lane], top.key);
-        put(&sh_idx[slot][lane], top.idx);
+      uint2 last = make_uint2(0xffffffffu, 0u);
+      for (int r = 0; r < a.k; ++r) {
+        uint2 best = make_uint2(kKeyNone, 0xffffffffu);
+        auto look = [&](float z, int i) {
+          const uint32_t q = key_of(z);
+          const bool open = q < last.x || (q == last.x && (uint32_t)i > last.y);
+          if (open && (q > best.x || (q == best.x && (uint32_t)i < best.y)) && q > kKeyNone)
+            best = make_uint2(q, (uint32_t)i);
+        };
+        for (int v = v_lo + tid; v < v_hi; v += NT) {
+          float z[R::E];
+          spread<BF16>(*row.vec(v), z);
+#pragma unroll
+          for (int i = 0; i < R::E; ++i) look(z[i], row.head + v * R::E + i);
+        }
+        if (end >= 0) look(row.at(end), end);
+        const uint32_t wk = __reduce_max_sync(0xffffffffu, best.x);
+        const uint32_t wi = __reduce_min_sync(0xffffffffu, best.x == wk ? best.y : 0xffffffffu);
+        __syncthreads();  // the last round's entries have been read
+        if (lane == 0) sm.cand[warp] = make_uint2(wk, wi);
+        __syncthreads();
+        last = make_uint2(kKeyNone, 0xffffffffu);
+        for (int w = 0; w < nw; ++w) {
+          const uint2 e = sm.cand[w];
+          if (e.x > last.x || (e.x == last.x && e.y < last.y)) last = e;
+        }
+        if (tid == 0) list(r, last);
       }
     }
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
-  if (rank != 0 || warp != 0) return;
+  if (rank != 0) return;
 
-  const int n = C * kWarps;
-  Stat f{-FLT_MAX, 0.f, 0.f};
-  for (int i = (int)lane; i < n; i += 32) f = merge(f, sh_stat[i], c2);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat y{__shfl_xor_sync(0xffffffffu, f.m, o), __shfl_xor_sync(0xffffffffu, f.s, o),
-           __shfl_xor_sync(0xffffffffu, f.a, o)};
-    f = merge(f, y, c2);
-  }
   const float nan = __int_as_float(0x7fffffff);
-  const bool none = f.m <= kMasked;  // every logit is masked out
-  const float ln_s = none ? 0.f : logf(f.s);
-  auto logp_of = [&](float z) { return sh_bad ? nan : z <= kMasked ? -INFINITY : (z - f.m) * a.c - ln_s; };
-  if (lane == 0) {
-    a.lse[t] = sh_bad ? nan : none ? -INFINITY : fmaf(f.m, a.c, ln_s);
-    a.logp[t] = logp_of(row.at(id));
-    if (a.ent) a.ent[t] = sh_bad ? nan : none ? 0.f : fmaxf(ln_s - kLn2 * f.a / f.s, 0.f);
+  const bool broken = sh_bad != 0;
+  Stat f{-kBig, 0.f, 0.f};
+  for (int i = (int)lane; i < C * nw; i += 32) f = merge(f, sm.stat[i], c2);
+  f = warp_join(f, c2);
+  const bool empty = f.m <= -kBig;  // every logit is masked out
+  const float ln_s = logf(f.s);
+  auto logp_of = [&](float z) { return broken ? nan : z <= -kBig ? -INFINITY : (z - f.m) * a.c - ln_s; };
+  if (tid == 0) {
+    a.lse[t] = broken ? nan : empty ? -INFINITY : fmaf(f.m, a.c, ln_s);
+    a.logp[t] = logp_of(given);
+    if (a.ent) a.ent[t] = broken ? nan : empty ? 0.f : fmaxf(ln_s - kLn2 * (f.a / f.s), 0.f);
   }
   if (TOP) {
-    // k rounds: the best head of the sorted lists (two a lane at most)
-    int p0 = 0, p1 = 0;
-    for (int r = 0; r < a.k; ++r) {
-      uint32_t k0 = kKeyNone, x0 = 0xffffffffu, k1 = kKeyNone, x1 = 0xffffffffu;
-      if ((int)lane < n && p0 < a.k) k0 = sh_key[lane][p0], x0 = sh_idx[lane][p0];
-      if ((int)lane + 32 < n && p1 < a.k) k1 = sh_key[lane + 32][p1], x1 = sh_idx[lane + 32][p1];
-      const bool second = k1 > k0 || (k1 == k0 && x1 < x0);
-      const uint32_t kb = second ? k1 : k0, xb = second ? x1 : x0;
-      const uint32_t best = __reduce_max_sync(0xffffffffu, kb);
-      const uint32_t at = __reduce_min_sync(0xffffffffu, kb == best ? xb : 0xffffffffu);
-      if (kb == best && xb == at) {
-        if (second) ++p1;
-        else ++p0;
-      }
-      if (lane == 0) {
-        const bool there = best > kKeyNone && !sh_bad;
-        a.top_ids[(size_t)t * a.k + r] = there ? (int32_t)at : -1;
-        a.top_logp[(size_t)t * a.k + r] = there ? logp_of(of_key(best)) : sh_bad ? nan : -INFINITY;
+    const int n = C * a.k;
+    auto write = [&](int place, uint2 e) {
+      const bool there = e.x > kKeyNone && !broken;
+      a.top_ids[(size_t)t * a.k + place] = there ? (int32_t)e.y : -1;
+      a.top_logp[(size_t)t * a.k + place] = there ? logp_of(of_key(e.x)) : broken ? nan : -INFINITY;
+    };
+    if (C == 1) {
+      if (tid < a.k) write(tid, sm.list[tid]);
+    } else {
+      // rank every block's entries (empty ones follow the others in their
+      // order), four lanes an entry
+      for (int i0 = 0; i0 < n; i0 += NT / 4) {
+        const int i = i0 + tid / 4;
+        const uint2 e = i < n ? sm.list[i] : make_uint2(0u, 0u);
+        int better = 0;
+        for (int j = tid & 3; j < n; j += 4) {
+          const uint2 g = sm.list[j];
+          better += g.x > e.x || (g.x == e.x && (g.y < e.y || (g.y == e.y && j < i))) ? 1 : 0;
+        }
+        better += __shfl_xor_sync(0xffffffffu, better, 1);
+        better += __shfl_xor_sync(0xffffffffu, better, 2);
+        if (i < n && (tid & 3) == 0 && better < a.k) write(better, e);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward: a block takes kThreads * kChunk logits of one row.
+// Backward: a thread holds kBwdVecs vectors of neighbouring logits of one row.
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const void* z;
@@ -389,63 +541,96 @@ struct BwdArgs {
   int T, V, ld, ldd;
   float c;
 };
+constexpr int kBwdThreads = 256;
+constexpr int kBwdVecs = 2;
 
+// Blocks of blockDim.x threads along a row by blockDim.y rows (short rows
+// share a block). A thread's logits are requested before the row's scalars,
+// whose loads they do not depend on.
 template <bool BF16, bool OBF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
-  constexpr int W = 8;  // logits a thread holds at a time: 8 neighbours
-  for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
-    const int id = a.ids[t];
-    const bool off = id < 0 || id >= a.V;
-    const float l = off ? 0.f : a.lse[t];
-    // a row without any finite logit has no gradient; a NaN row's is NaN
-    const bool zero = off || l == -INFINITY;
-    const float gl = zero || !a.g_logp ? 0.f : a.g_logp[t];
-    const float ge = zero || !a.g_ent ? 0.f : a.g_ent[t];
-    const float h = zero || !a.ent ? 0.f : a.ent[t];
-    // dz = c (gl [j = t] - p (gl + ge (log p + H)))
-    const float k0 = -a.c * (gl + ge * h), k1 = -a.c * ge;
+  constexpr int W = kBwdVecs * (BF16 ? 8 : 4);  // logits a thread holds at a time
+  const uint64_t cc = pair(a.c, a.c), ll = pair(kLog2e, kLog2e);
+  const int j = (int)(blockIdx.x * blockDim.x + threadIdx.x) * W;
+  if (j >= a.V) return;
+  const bool whole = VEC && j + W <= a.V;
+  for (int t = blockIdx.y * blockDim.y + threadIdx.y; t < a.T; t += gridDim.y * blockDim.y) {
     const uint8_t* zr = (const uint8_t*)a.z + (size_t)t * a.ld * esz;
     uint8_t* dr = (uint8_t*)a.dz + (size_t)t * a.ldd * (OBF16 ? 2 : 4);
-    for (int j = (blockIdx.x * kThreads + (int)threadIdx.x) * W; j < a.V; j += gridDim.x * kThreads * W) {
-      float z[W], g[W];
-      const bool whole = VEC && j + W <= a.V;
-      if (zero) {
+    uint4 u[kBwdVecs];
+    if (whole) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) g[i] = 0.f;
-      } else {
-        if (whole) {
-          const uint4* p = (const uint4*)(zr + (size_t)j * esz);
-          spread<BF16>(__ldcs(p), z);
-          if (!BF16) spread<BF16>(__ldcs(p + 1), z + 4);
-        } else {
+      for (int i = 0; i < kBwdVecs; ++i) u[i] = __ldcs((const uint4*)(zr + (size_t)j * esz) + i);
+    }
+    const int id = a.ids[t];
+    const bool off = id < 0 || id >= a.V;
+    const float l = a.lse[t];
+    // a row without any logit left has no gradient; a NaN row's is NaN
+    const bool zero = off || l == -INFINITY;
+    const float gl = a.g_logp ? a.g_logp[t] : 0.f, ge = a.g_ent ? a.g_ent[t] : 0.f;
+    const float h = a.g_ent ? a.ent[t] : 0.f;
+    // dz = c (gl [j = t] - p (gl + ge (log p + H)))
+    const float k0 = -a.c * (gl + ge * h), k1 = -a.c * ge;
+    const uint64_t kk0 = pair(k0, k0), kk1 = pair(k1, k1), nl = pair(-l, -l);
+    float g[W];
+    if (zero) {
 #pragma unroll
-          for (int i = 0; i < W; ++i)
-            z[i] = j + i < a.V ? (BF16 ? bf2f(((const uint16_t*)zr)[j + i]) : ((const float*)zr)[j + i]) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float d = fmaf(z[i], a.c, -l), p = ex2(d * kLog2e);  // log p, p
-          g[i] = p * fmaf(k1, fmaxf(d, kFar), k0);
-          if (j + i == id) g[i] += a.c * gl;
-        }
-      }
+      for (int i = 0; i < W; ++i) g[i] = 0.f;
+    } else {
+      float z[W];
       if (whole) {
-        if (OBF16) {
-          __stcs((uint4*)(dr + (size_t)j * 2), make_uint4(pack_bf2(g[0], g[1]), pack_bf2(g[2], g[3]),
-                                                          pack_bf2(g[4], g[5]), pack_bf2(g[6], g[7])));
-        } else {
-          __stcs((float4*)(dr + (size_t)j * 4), make_float4(g[0], g[1], g[2], g[3]));
-          __stcs((float4*)(dr + (size_t)j * 4) + 1, make_float4(g[4], g[5], g[6], g[7]));
+#pragma unroll
+        for (int i = 0; i < kBwdVecs; ++i) {
+          if (BF16) {
+            u[i].x = max_nan_bf2(u[i].x, kBigPair);
+            u[i].y = max_nan_bf2(u[i].y, kBigPair);
+            u[i].z = max_nan_bf2(u[i].z, kBigPair);
+            u[i].w = max_nan_bf2(u[i].w, kBigPair);
+          }
+          spread<BF16>(u[i], z + i * (W / kBwdVecs));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-          if (j + i < a.V) {
-            if (OBF16) ((uint16_t*)dr)[j + i] = f2bf(g[i]);
-            else ((float*)dr)[j + i] = g[i];
-          }
+          z[i] = j + i < a.V ? (BF16 ? bf2f(((const uint16_t*)zr)[j + i]) : ((const float*)zr)[j + i]) : 0.f;
       }
+      if (!BF16 || !whole) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) z[i] = max_nan(z[i], -kBig);  // keeps log p finite where p is 0
+      }
+#pragma unroll
+      for (int i = 0; i < W; i += 2) {
+        const uint64_t lp = fma2(pair(z[i], z[i + 1]), cc, nl), x = mul2(lp, ll);  // log p, log2 p
+        float x0, x1;
+        unpair(x, x0, x1);
+        unpair(mul2(pair(ex2(x0), ex2(x1)), fma2(kk1, lp, kk0)), g[i], g[i + 1]);
+      }
+      if ((unsigned)(id - j) < (unsigned)W) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (j + i == id) g[i] += a.c * gl;
+      }
+    }
+    if (whole) {
+      if (OBF16) {
+#pragma unroll
+        for (int i = 0; i < W; i += 8)
+          __stcs((uint4*)(dr + (size_t)(j + i) * 2),
+                 make_uint4(pack_bf2(g[i], g[i + 1]), pack_bf2(g[i + 2], g[i + 3]), pack_bf2(g[i + 4], g[i + 5]),
+                            pack_bf2(g[i + 6], g[i + 7])));
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+          __stcs((float4*)(dr + (size_t)(j + i) * 4), make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (j + i < a.V) {
+          if (OBF16) ((uint16_t*)dr)[j + i] = f2bf(g[i]);
+          else ((float*)dr)[j + i] = g[i];
+        }
     }
   }
 }
@@ -456,17 +641,29 @@ inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k, float* lse, float* logp, float* ent,
                    int32_t* top_ids, float* top_logp, int T, int V, int ld, cudaStream_t st) {
-  if (T <= 0 || V <= 0 || ld < V || k < 0 || k > kMaxTop || k > V || !(c >= 1e-30f) || !(c <= 1e30f) ||
+  if (T <= 0 || V <= 0 || ld < V || k < 0 || k > kMaxTop || k > V || !(c >= kMinScale) || !(c <= kMaxScale) ||
       ((uintptr_t)z & (bf16 ? 1 : 3)) || T > (1 << 28))
     return -1;
-  // Blocks a row: enough that the rows fill the GPU twice over, while a block
-  // keeps at least four chunks a thread.
-  int C = 1;
-  while (C < kMaxCluster && (int64_t)T * C < 2 * mt_host::num_sms() && V >= 2 * C * kThreads * kChunk) C *= 2;
-  FwdArgs a{z, ids, lse, logp, ent, top_logp, top_ids, T, V, ld, k, c};
+  // Threads a block: for many rows four chunks each (short rows then need no
+  // more than a warp or two), else one; blocks a row: where the rows alone do
+  // not fill the GPU twice over, as many as leave every thread a chunk, and
+  // larger blocks where even that does not.
+  const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
+  const int each = T >= 8 * sms ? 4 * chunk : chunk;
+  int NT = 32, C = 1;
+  while (NT < 256 && NT * each < V) NT *= 2;
+  while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
+  if (C == kMaxCluster && T * C <= sms && V > C * NT * chunk) NT = kMaxThreads;
+  // a block's vectors, at most, in chunks a thread; segments of G chunks
+  const int vecs = V / (bf16 ? 8 : 4) / C + 1, chunks = (vecs + NT * kVecs - 1) / (NT * kVecs);
+  const int G = (chunks + kSegs - 1) / kSegs;
+  const int segs = (chunks + G - 1) / G, cap = std::max(256, 4 * NT);
+  FwdArgs a{z, ids, lse, logp, ent, top_logp, top_ids, T, V, ld, k, c, C, G, cap, segs};
+  Smem unused;
+  const size_t smem = smem_layout(nullptr, NT, C, k, cap, segs, &unused);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(T * C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)NT);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -475,13 +672,18 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  cudaError_t e;
+  cfg.dynamicSmemBytes = smem;
+  cudaError_t e = cudaSuccess;
+  if (smem > 47 * 1024)  // with the static part past the default limit
+    e = cudaFuncSetAttribute(bf16 ? token_logprobs_kernel<true, true> : token_logprobs_kernel<false, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  if (e != cudaSuccess) return -1;
   if (k > 0)
-    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, true>, a, C)
-             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, true>, a, C);
+    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, true>, a)
+             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, true>, a);
   else
-    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, false>, a, C)
-             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, false>, a, C);
+    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, false>, a)
+             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, false>, a);
   count_launches(1);
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
@@ -489,13 +691,18 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
 int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, const float* lse, const float* ent,
                        const float* g_logp, const float* g_ent, void* dz, bool dz_bf16, int T, int V, int ld, int ldd,
                        cudaStream_t st) {
-  if (T <= 0 || V <= 0 || ld < V || ldd < V || V > (1 << 30) || !(c >= 1e-30f) || !(c <= 1e30f) || (g_ent && !ent) ||
+  if (T <= 0 || V <= 0 || ld < V || ldd < V || V > (1 << 30) || !(c >= kMinScale) || !(c <= kMaxScale) || (g_ent && !ent) ||
       ((uintptr_t)z & (bf16 ? 1 : 3)) || ((uintptr_t)dz & (dz_bf16 ? 1 : 3)))
     return -1;
   BwdArgs a{z, ids, lse, ent, g_logp, g_ent, dz, T, V, ld, ldd, c};
   const bool vec = al16(z) && al16(dz) && ld % (bf16 ? 8 : 4) == 0 && ldd % (dz_bf16 ? 8 : 4) == 0;
-  const dim3 grid((unsigned)std::min((V + kThreads * 16 - 1) / (kThreads * 16), 65535), (unsigned)std::min(T, 65535));
-  auto go = [&](auto k) { k<<<grid, kThreads, 0, st>>>(a); };
+  const int W = kBwdVecs * (bf16 ? 8 : 4), units = (V + W - 1) / W;
+  int bx = 8;
+  while (bx < units && bx < kBwdThreads) bx *= 2;
+  const int by = kBwdThreads / bx;
+  const dim3 block((unsigned)bx, (unsigned)by);
+  const dim3 grid((unsigned)((units + bx - 1) / bx), (unsigned)std::min((T + by - 1) / by, 65535));
+  auto go = [&](auto k) { k<<<grid, block, 0, st>>>(a); };
   auto pick = [&](auto v) {
     constexpr bool X = decltype(v)::value;
     if (bf16) dz_bf16 ? go(token_logprobs_bwd_kernel<true, true, X>) : go(token_logprobs_bwd_kernel<true, false, X>);

