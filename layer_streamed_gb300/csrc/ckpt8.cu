@@ -16,9 +16,9 @@
 // other values.
 //
 // All kernels here are bound by HBM traffic: every operand is read once and
-// every result written once, loads are 16 bytes a thread, and a block's
-// maximum is a shuffle reduction over the 4 (16-bit sources) or 8 (fp32)
-// lanes that hold it.
+// every result written once, loads are 16 or 32 bytes a thread, and a
+// block's maximum is a shuffle reduction over the four or eight lanes that
+// hold it.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,6 +28,9 @@
 #include "kernels.h"
 
 namespace mt {
+
+MT_DEVICE_ERROR_READER(ckpt8_take_device_error)
+
 namespace {
 
 enum { FMT_I8 = 1, FMT_E4M3 = 2 };
@@ -93,28 +96,38 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
-// E consecutive values (4 fp32 or 8 bf16) of a row from column c; columns at
-// or past n read as 0. VEC: one 16-byte load (c + E <= n and aligned).
+// 32-byte accesses (one instruction for eight fp32).
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store8f(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// Eight consecutive values of a row from column c; columns at or past n read
+// as 0. VEC: one 16-byte (bf16) or 32-byte (fp32) load.
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_unit(const void* row, int c, int n, float (&v)[BF16 ? 8 : 4]) {
-  constexpr int E = BF16 ? 8 : 4;
-  if (VEC && c + E <= n) {
+__device__ __forceinline__ void load_unit(const void* row, int c, int n, float (&v)[8]) {
+  if (VEC && c + 8 <= n) {
     if (BF16) {
       const uint4 u = __ldcs((const uint4*)((const uint16_t*)row + c));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        v[2 * i] = __uint_as_float(w[i & 3] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i & 3] & 0xffff0000u);
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
       }
     } else {
-      const float4 f = __ldcs((const float4*)((const float*)row + c));
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      load8f((const float*)row + c, v);
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i)
+  for (int i = 0; i < 8; ++i)
     v[i] = c + i < n ? (BF16 ? bf2f(((const uint16_t*)row)[c + i]) : ((const float*)row)[c + i]) : 0.f;
 }
 // E code bytes (E / 4 words) to columns c.. of a row of codes.
@@ -148,6 +161,26 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int c, int n, uin
     if (c + i < n) w[i >> 2] |= (uint32_t)row[c + i] << (8 * (i & 3));
 }
 
+// The same from a maximum known already (bits of the largest |v|).
+template <int FMT, int E>
+__device__ __forceinline__ uint32_t encode_with(uint32_t amax_bits, const float (&v)[E], uint32_t (&w)[E / 4]) {
+  const uint32_t b = scale_byte<FMT>(group_max<32 / E>(amax_bits));
+  const float inv = scale_down(min(b, 249u));
+#pragma unroll
+  for (int k = 0; k < E / 4; ++k) {
+    w[k] = encode4<FMT>(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+    if (b == 255u) w[k] = 0;
+  }
+  return b;
+}
+// Largest |value| of eight bf16 (as fp32 bits): bf16 magnitudes order like
+// whole numbers, two at a time.
+__device__ __forceinline__ uint32_t amax_bf16x8(const uint4& u) {
+  constexpr uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+  return max(a << 16, a & 0xffff0000u);
+}
+
 // Codes and scale byte of one thread's unit; the G lanes of the block agree
 // on the scale. Every lane of the warp calls this.
 template <int FMT, int E>
@@ -155,21 +188,11 @@ __device__ __forceinline__ uint32_t encode_unit(const float (&v)[E], uint32_t (&
   uint32_t am = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) am = max(am, abs_bits(v[i]));
-  const uint32_t b = scale_byte<FMT>(group_max<32 / E>(am));
-  if (b == 255u) {
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k) w[k] = 0;
-  } else {
-    const float inv = scale_down(b);
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k)
-      w[k] = encode4<FMT>(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
-  }
-  return b;
+  return encode_with<FMT, E>(am, v, w);
 }
 
 // ---------------------------------------------------------------------------
-// Pack and unpack. A thread owns one unit of 16 source bytes in each of kRows
+// Pack and unpack. A thread owns one unit of eight values in each of kRows
 // rows (their loads are in flight together); a 2D block covers blockDim.x
 // units of blockDim.y rows at a time, so narrow matrices still fill a block.
 // ---------------------------------------------------------------------------
@@ -179,7 +202,7 @@ template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales, int T, int n, int ldx, int ldc,
                                                          int nb) {
-  constexpr int E = BF16 ? 8 : 4, G = 32 / E, esz = BF16 ? 2 : 4;
+  constexpr int E = 8, G = 32 / E, esz = BF16 ? 2 : 4;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
   const int step = gridDim.y * blockDim.y;
   // the whole block leaves the loop together: shuffles need every lane
@@ -207,7 +230,7 @@ template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, void* __restrict__ x,
                                                            int T, int n, int ldc, int ldx, int nb) {
-  constexpr int E = BF16 ? 8 : 4;
+  constexpr int E = 8;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
   if (c >= n) return;
   const int step = gridDim.y * blockDim.y;
@@ -246,7 +269,7 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __rest
       } else {
         float* dst = (float*)x + (size_t)t * ldx + c;
         if (VEC && c + E <= n) {
-          *(float4*)dst = make_float4(v[0], v[1], v[2], v[3]);
+          store8f(dst, v);
         } else {
 #pragma unroll
           for (int i = 0; i < E; ++i)
@@ -321,106 +344,197 @@ __global__ void __launch_bounds__(kFwdThreads)
 // t mod parts, so a part's sum has a fixed order) and hold their share of dw
 // in registers; a second kernel adds the parts in order.
 // ---------------------------------------------------------------------------
-constexpr int kBwdThreads = 256;
-constexpr int kBwdParts = 456;  // three blocks on each of 152 SMs
+// A block holds a row: V float4 a thread (two where h > 1024), w and the
+// sums of dw in registers. One thread requests whole rows of codes, dy and
+// resid kBwdStages - 1 rows ahead as bulk copies into shared memory, so loads
+// stay in flight across a row's reduction and hold no registers; rows that
+// are not whole 16-byte pieces (BULK false) are loaded by the threads.
+// Measured at 8192 x 4096 (floor 74 us): per-thread loads 103 us, per-thread
+// cp.async staging 128 us (its 4-byte copies and second reads cost more than
+// the loads it hides).
+// ---------------------------------------------------------------------------
+constexpr int kBwdMaxThreads = 1024;
+constexpr int kBwdStages = 3;
+constexpr int kBwdMaxParts = 1216;  // blocks, and rows of partial sums
 
-template <int FMT, int V>
-__global__ void __launch_bounds__(kBwdThreads)
+// Threads and vectors of a block, and blocks: what 152 SMs hold at once by
+// the stages' shared memory (9 h bytes each with a residual), up to eight an SM.
+struct BwdShape {
+  int threads, vecs, parts;
+};
+BwdShape bwd_shape(int T, int h) {
+  BwdShape s;
+  const int n4 = h / 4;
+  s.vecs = h > 1024 ? 2 : 1;
+  s.threads = std::max(32, (n4 + s.vecs * 32 - 1) / (s.vecs * 32) * 32);
+  const int an_sm = std::min({8, 2048 / s.threads, 220 * 1024 / (kBwdStages * 9 * h)});
+  s.parts = std::min(T, std::min(kBwdMaxParts, 152 * std::max(1, an_sm)));
+  return s;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <int FMT, int V, bool BULK>
+__global__ void __launch_bounds__(kBwdMaxThreads)
     rmsnorm_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                              const float* __restrict__ w, const float* __restrict__ rstd,
                              const float* __restrict__ dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
                              float* __restrict__ part, int T, int h, int nb) {
-  __shared__ float red[2][kBwdThreads / 32];
-  const int n4 = h >> 2, tid = threadIdx.x;
+  extern __shared__ __align__(128) uint8_t stage[];  // [kBwdStages]: dy, resid, codes of a row
+  __shared__ float red[2][kBwdMaxThreads / 32];
+  __shared__ uint64_t full[kBwdStages];
+  __shared__ int abort_flag;
+  const int n4 = h >> 2, tid = threadIdx.x, NT = blockDim.x, nw = NT >> 5;
   const float inv_h = 1.f / (float)h;
-  const float4* w4 = (const float4*)w;
-  float4 acc[V];
+  const uint32_t row_bytes = (uint32_t)h * (resid ? 9u : 5u);
+  auto request = [&](int t, int s) {  // one thread
+    if (t >= T) return;
+    uint8_t* p = stage + (size_t)s * row_bytes;
+    mbar_arrive_expect_tx(&full[s], row_bytes);
+    bulk_load(p, dy + (size_t)t * h, 4u * h, &full[s]);
+    if (resid) bulk_load(p + 4 * h, resid + (size_t)t * h, 4u * h, &full[s]);
+    bulk_load(p + row_bytes - h, codes + (size_t)t * h, (uint32_t)h, &full[s]);
+  };
+  if (BULK) {
+    if (tid == 0) {
+      abort_flag = 0;
+      for (int s = 0; s < kBwdStages; ++s) mbar_init(&full[s], 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
+    if (tid == 0)
+      for (int s = 0; s < kBwdStages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
+  }
+  float4 acc[V], wv[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  int flip = 0;
-#pragma unroll 1
-  for (int t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
-    float4 xv[V], gv[V], rv[V];
-    uint32_t q[V], b[V];
+  for (int j = 0; j < V; ++j) {
+    const int i = tid + j * NT;
+    acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    wv[j] = i < n4 ? ((const float4*)w)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // a row's scales and rstd, requested one row ahead
+  uint32_t b_next[V];
+  float r_next = 0.f;
+  auto small = [&](int t) {
+    if (t < T) {
+      r_next = rstd[t];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = tid + j * kBwdThreads;
-      if (i < n4) {
-        q[j] = __ldcs((const uint32_t*)(codes + (size_t)t * h) + i);
-        b[j] = scales[(size_t)t * nb + i / 8];
-        gv[j] = __ldcs((const float4*)(dy + (size_t)t * h) + i);
-        if (resid) rv[j] = ((const float4*)(resid + (size_t)t * h))[i];
+      for (int j = 0; j < V; ++j) {
+        const int i = tid + j * NT;
+        if (i < n4) b_next[j] = scales[(size_t)t * nb + i / 8];
       }
     }
-    const float r = rstd[t];
+  };
+  small(blockIdx.x);
+  int flip = 0, st = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
+    const float r = r_next;
+    float4 g[V], e[V], x[V];
+    uint32_t q[V];
+    if (BULK) {
+      if (!mbar_wait(&full[st], phase, &abort_flag, kErrTimeoutTma)) break;
+    }
+    const uint8_t* p = stage + (size_t)st * row_bytes;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = tid + j * NT;
+      if (i < n4) {
+        if (BULK) {
+          g[j] = ((const float4*)p)[i];
+          q[j] = ((const uint32_t*)(p + row_bytes - h))[i];
+        } else {
+          g[j] = __ldcs((const float4*)(dy + (size_t)t * h) + i);
+          q[j] = __ldcs((const uint32_t*)(codes + (size_t)t * h) + i);
+          if (resid) e[j] = ((const float4*)(resid + (size_t)t * h))[i];
+        }
+      }
+    }
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int i = tid + j * kBwdThreads;
+      const int i = tid + j * NT;
       if (i < n4) {
-        const float4 wv = w4[i];
-        xv[j] = decode4<FMT>(q[j], scale_up(b[j]));
-        dot += gv[j].x * wv.x * xv[j].x + gv[j].y * wv.y * xv[j].y + gv[j].z * wv.z * xv[j].z +
-               gv[j].w * wv.w * xv[j].w;
+        x[j] = decode4<FMT>(q[j], scale_up(b_next[j]));
+        dot += g[j].x * wv[j].x * x[j].x + g[j].y * wv[j].y * x[j].y + g[j].z * wv[j].z * x[j].z +
+               g[j].w * wv[j].w * x[j].w;
       }
     }
+    small(t + gridDim.x);
     dot = warp_sum(dot);
     if ((tid & 31) == 0) red[flip][tid >> 5] = dot;
-    __syncthreads();  // two buffers in turn: one barrier a row is enough
-    dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < kBwdThreads / 32; ++i) dot += red[flip][i];
-    const float mean = dot * r * inv_h;
+    // two buffers in turn: one barrier a row is enough; it also says that the
+    // last row's stage has been read
+    __syncthreads();
+    if (BULK && tid == 0) request(t + (kBwdStages - 1) * gridDim.x, st == 0 ? kBwdStages - 1 : st - 1);
+    dot = (tid & 31) < nw ? red[flip][tid & 31] : 0.f;
+    const float mean = warp_sum(dot) * r * inv_h;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int i = tid + j * kBwdThreads;
+      const int i = tid + j * NT;
       if (i < n4) {
-        const float4 wv = w4[i];
-        const float4 xh = make_float4(xv[j].x * r, xv[j].y * r, xv[j].z * r, xv[j].w * r);
-        float4 o = make_float4(r * (gv[j].x * wv.x - xh.x * mean), r * (gv[j].y * wv.y - xh.y * mean),
-                               r * (gv[j].z * wv.z - xh.z * mean), r * (gv[j].w * wv.w - xh.w * mean));
+        const float4 xh = make_float4(x[j].x * r, x[j].y * r, x[j].z * r, x[j].w * r);
+        float4 o = make_float4(r * (g[j].x * wv[j].x - xh.x * mean), r * (g[j].y * wv[j].y - xh.y * mean),
+                               r * (g[j].z * wv[j].z - xh.z * mean), r * (g[j].w * wv[j].w - xh.w * mean));
         if (resid) {
-          o.x += rv[j].x;
-          o.y += rv[j].y;
-          o.z += rv[j].z;
-          o.w += rv[j].w;
+          if (BULK) e[j] = ((const float4*)(p + 4 * h))[i];
+          o.x += e[j].x;
+          o.y += e[j].y;
+          o.z += e[j].z;
+          o.w += e[j].w;
         }
         ((float4*)(dx + (size_t)t * h))[i] = o;
         if (dxb) ((uint2*)(dxb + (size_t)t * h))[i] = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
-        acc[j].x += gv[j].x * xh.x;
-        acc[j].y += gv[j].y * xh.y;
-        acc[j].z += gv[j].z * xh.z;
-        acc[j].w += gv[j].w * xh.w;
+        acc[j].x += g[j].x * xh.x;
+        acc[j].y += g[j].y * xh.y;
+        acc[j].z += g[j].z * xh.z;
+        acc[j].w += g[j].w * xh.w;
+      }
+    }
+    if (++st == kBwdStages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+  if (BULK && *(volatile int*)&abort_flag) {  // a wait ran out: give the copies in flight time to land
+    for (int k = 0; k < kBwdStages - 1; ++k) {
+      for (int spin = 0; spin < (1 << 20) && !mbar_try_wait(smem_u32(&full[st]), phase); ++spin) {
+      }
+      if (++st == kBwdStages) {
+        st = 0;
+        phase ^= 1;
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = tid + j * kBwdThreads;
+    const int i = tid + j * NT;
     if (i < n4) ((float4*)(part + (size_t)blockIdx.x * h))[i] = acc[j];
   }
 }
 
-// out[c] = sum over the parts, in a fixed order: 16 warps take the parts in
-// turn for 32 columns, then their sums are added in warp order.
-__global__ void __launch_bounds__(512) sum_parts_kernel(const float* __restrict__ part, int nparts, int n,
-                                                        float* __restrict__ out) {
-  __shared__ float red[16][33];
+// out[c] = sum over the parts, in a fixed order: 32 warps take the parts in
+// turn for 32 columns, then their sums are added by a shuffle tree.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int nparts, int n,
+                                                         float* __restrict__ out) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < n) {
 #pragma unroll 8
-    for (int p = w; p < nparts; p += 16) s += part[(size_t)p * n + c];
+    for (int p = w; p < nparts; p += 32) s += part[(size_t)p * n + c];
   }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < n) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[i][lane];
-    out[c] = s;
-  }
+  s = warp_sum(red[lane][w]);  // warp w: column w of the 32
+  if (lane == 0 && blockIdx.x * 32 + w < n) out[blockIdx.x * 32 + w] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -428,7 +542,32 @@ __global__ void __launch_bounds__(512) sum_parts_kernel(const float* __restrict_
 // cut into blocks of 32 separately. A thread owns 8 columns of g and the
 // same 8 of u, four lanes a block.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float sigmoid_(float g) { return 1.f / (1.f + __expf(-g)); }
+// 1 / (1 + e^-g), with the hardware reciprocal (one unit in the last place,
+// subnormal results kept): the exact division costs more instructions than
+// the rest of the formula.
+__device__ __forceinline__ float sigmoid_(float g) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  return r;
+}
+__device__ __forceinline__ void spread8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+// Eight bf16 from column c; columns at or past n read as 0.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int n) {
+  if (VEC && c + 8 <= n) return __ldcs((const uint4*)(row + c));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 constexpr int kSwRows = 2;
 
 template <int FMT, bool VEC>
@@ -439,24 +578,29 @@ __global__ void __launch_bounds__(256) swiglu_fwd_ckpt8_kernel(const uint16_t* _
                                                                int nb) {
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   const int step = gridDim.y * blockDim.y;
+  // the whole block leaves the loop together: shuffles need every lane
   for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kSwRows) {
-    float g[kSwRows][8], u[kSwRows][8];
+    uint4 gq[kSwRows], uq[kSwRows];
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
       const uint16_t* row = gu + (size_t)t * 2 * ld;
-      load_unit<true, VEC>(row, c, t < T ? F : 0, g[r]);
-      load_unit<true, VEC>(row + ld, c, t < T ? F : 0, u[r]);
+      gq[r] = load8<VEC>(row, c, t < T ? F : 0);
+      uq[r] = load8<VEC>(row + ld, c, t < T ? F : 0);
     }
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
+      float g[8], u[8];
+      spread8(gq[r], g);
+      spread8(uq[r], u);
       uint32_t wg[2], wu[2];
-      const uint32_t bg = encode_unit<FMT, 8>(g[r], wg), bu = encode_unit<FMT, 8>(u[r], wu);
+      const uint32_t bg = encode_with<FMT, 8>(amax_bf16x8(gq[r]), g, wg);
+      const uint32_t bu = encode_with<FMT, 8>(amax_bf16x8(uq[r]), u, wu);
       if (t < T) {
         float a[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = g[r][i] * sigmoid_(g[r][i]) * u[r][i];
+        for (int i = 0; i < 8; ++i) a[i] = g[i] * sigmoid_(g[i]) * u[i];
         uint8_t* crow = codes + (size_t)t * 2 * ld;
         uint16_t* arow = act + (size_t)t * ld;
         // columns F..ld-1 are padding: codes and act are 0 there (the loads gave 0)
@@ -491,7 +635,7 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
   const int step = gridDim.y * blockDim.y;
   for (int t0 = blockIdx.y * blockDim.y + threadIdx.y; t0 < T; t0 += step * kSwRows) {
     uint32_t wg[kSwRows][2], wu[kSwRows][2], bg[kSwRows], bu[kSwRows];
-    float d[kSwRows][8];
+    uint4 dq[kSwRows];
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step;
@@ -499,10 +643,10 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
         const uint8_t* crow = codes + (size_t)t * 2 * ld;
         load_codes<8, VEC>(crow, c, F, wg[r]);
         load_codes<8, VEC>(crow + ld, c, F, wu[r]);
+        dq[r] = load8<VEC>(dact + (size_t)t * ld, c, F);
         // a unit that lies in the padding has no block of its own
         bg[r] = c < F ? scales[(size_t)t * 2 * nb + c / 32] : 0u;
         bu[r] = c < F ? scales[(size_t)t * 2 * nb + nb + c / 32] : 0u;
-        load_unit<true, VEC>(dact + (size_t)t * ld, c, F, d[r]);
       }
     }
 #pragma unroll
@@ -510,16 +654,17 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
       const int t = t0 + r * step;
       if (t >= T) break;
       const float sg = scale_up(bg[r]), su = scale_up(bu[r]);
-      float og[8], ou[8];
+      float d[8], og[8], ou[8];
+      spread8(dq[r], d);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float4 g4 = decode4<FMT>(wg[r][k], sg), u4 = decode4<FMT>(wu[r][k], su);
         const float gg[4] = {g4.x, g4.y, g4.z, g4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float s = sigmoid_(gg[i]), dd = d[r][4 * k + i];
-          og[4 * k + i] = dd * uu[i] * s * (1.f + gg[i] * (1.f - s));
-          ou[4 * k + i] = dd * gg[i] * s;
+          const float s = sigmoid_(gg[i]), ds = d[4 * k + i] * s, du = ds * gg[i];
+          og[4 * k + i] = uu[i] * fmaf(du, 1.f - s, ds);  // dact u s (1 + g (1 - s))
+          ou[4 * k + i] = du;
         }
       }
       uint16_t* row = dgu + (size_t)t * 2 * ld;
@@ -567,10 +712,10 @@ inline bool fmt_ok(int fmt) { return fmt == FMT_I8 || fmt == FMT_E4M3; }
 int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scales, int T, int n, int ldx, int ldc,
                cudaStream_t st) {
   if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
-  const int E = bf16 ? 8 : 4, nb = blocks32(n);
-  const Shape2 s = shape2(T, (n + E - 1) / E, kRows);
-  // whole 16-byte loads and E-byte stores where every row starts on such a boundary
-  const bool vec = al(x, 16) && ldx % E == 0 && al(codes, E) && ldc % E == 0;
+  const int nb = blocks32(n);
+  const Shape2 s = shape2(T, (n + 7) / 8, kRows);
+  // whole loads and stores of eight values where every row starts on their boundary
+  const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(x, codes, scales, T, n, ldx, ldc, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
@@ -585,9 +730,9 @@ int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scale
 int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, bool bf16, int T, int n, int ldc,
                  int ldx, cudaStream_t st) {
   if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
-  const int E = bf16 ? 8 : 4, nb = blocks32(n);
-  const Shape2 s = shape2(T, (n + E - 1) / E, kRows);
-  const bool vec = al(x, 16) && ldx % E == 0 && al(codes, E) && ldc % E == 0;
+  const int nb = blocks32(n);
+  const Shape2 s = shape2(T, (n + 7) / 8, kRows);
+  const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, x, T, n, ldc, ldx, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
@@ -619,28 +764,34 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
   return done(1);
 }
 
-size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)std::min(T, kBwdParts) * h; }
+size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)bwd_shape(T, h).parts * h; }
 
 int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
                       const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,
                       int T, int h, cudaStream_t st) {
-  if (T <= 0 || h <= 0 || (h & 3) || h > 8 * 4 * kBwdThreads || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) ||
+  if (T <= 0 || h <= 0 || (h & 3) || h > 8192 || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) ||
       !al(dy, 16) || !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
     return -1;
-  const int n4 = h / 4, nb = blocks32(h), parts = std::min(T, kBwdParts);
-  auto go = [&](auto k) {
-    k<<<parts, kBwdThreads, 0, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb);
+  const int nb = blocks32(h);
+  const BwdShape shape = bwd_shape(T, h);
+  const bool bulk = h % 16 == 0 && al(codes, 16);  // every row of codes starts and ends on 16 bytes
+  bool ok = true;
+  auto go = [&](auto k, bool staged) {
+    const int smem = staged ? kBwdStages * h * (resid ? 9 : 5) : 0;
+    if (smem > 48 * 1024)
+      ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdStages * 9 * 8192) == cudaSuccess;
+    if (ok)
+      k<<<shape.parts, shape.threads, smem, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb);
   };
   auto pick = [&](auto f) {
     constexpr int F = decltype(f)::value;
-    if (n4 <= kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 1>);
-    else if (n4 <= 2 * kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 2>);
-    else if (n4 <= 4 * kBwdThreads) go(rmsnorm_bwd_ckpt8_kernel<F, 4>);
-    else go(rmsnorm_bwd_ckpt8_kernel<F, 8>);
+    if (shape.vecs == 1) bulk ? go(rmsnorm_bwd_ckpt8_kernel<F, 1, true>, true) : go(rmsnorm_bwd_ckpt8_kernel<F, 1, false>, false);
+    else bulk ? go(rmsnorm_bwd_ckpt8_kernel<F, 2, true>, true) : go(rmsnorm_bwd_ckpt8_kernel<F, 2, false>, false);
   };
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
-  sum_parts_kernel<<<(h + 31) / 32, 512, 0, st>>>(work, parts, h, dw);
+  if (!ok) return -1;
+  sum_parts_kernel<<<(h + 31) / 32, 1024, 0, st>>>(work, shape.parts, h, dw);
   return done(2);
 }
 

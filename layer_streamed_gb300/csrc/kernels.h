@@ -172,6 +172,7 @@ int embed_fwd(const void* table, bool table_bf16, const int32_t* ids, float scal
 size_t embed_bwd_workspace(int T, int V, int h);
 int embed_bwd(const int32_t* ids, const void* dout, bool dout_bf16, float scale, void* dtable, bool dtable_bf16,
               bool add, void* work, int T, int V, int h, cudaStream_t st);
+uint32_t ckpt8_take_device_error();
 uint32_t token_logprobs_take_device_error();
 uint32_t embedding_take_device_error();
 

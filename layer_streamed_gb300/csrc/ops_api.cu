@@ -427,8 +427,8 @@ int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float 
 
 int mt_op_device_error(void) {
   cudaDeviceSynchronize();
-  return (int)(gemm_take_device_error() | attention_tc_take_device_error() | token_logprobs_take_device_error() |
-               embedding_take_device_error());
+  return (int)(gemm_take_device_error() | attention_tc_take_device_error() | ckpt8_take_device_error() |
+               token_logprobs_take_device_error() | embedding_take_device_error());
 }
 
 }  // extern "C"
