@@ -37,57 +37,77 @@ enum { FMT_I8 = 1, FMT_E4M3 = 2 };
 
 // Scale byte of a block from the bit pattern of max|x| (as an unsigned
 // integer it orders like the value, infinities and NaN above all numbers).
-template <int FMT>
+// SHIFT: fraction bits of the pattern (23, or 7 for a bf16). The exponent
+// goes up by one where the fraction is past the limit's (127 = 1.984375 * 2^6,
+// 448 = 1.75 * 2^8): a carry out of the fraction.
+template <int FMT, int SHIFT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  constexpr int off = FMT == FMT_I8 ? 6 : 8;                           // 127 = 1.984375 * 2^6, 448 = 1.75 * 2^8
-  constexpr uint32_t top = FMT == FMT_I8 ? 0x7e0000u : 0x600000u;      // fraction bits of 1.984375, 1.75
-  const uint32_t e = amax_bits >> 23;
-  if (e == 255u) return 255u;
-  const int b = (int)e - off + ((amax_bits & 0x7fffffu) > top ? 1 : 0);
-  return (uint32_t)max(b, 0);
+  constexpr int off = FMT == FMT_I8 ? 6 : 8;
+  constexpr uint32_t ones = (1u << SHIFT) - 1;
+  constexpr uint32_t top = FMT == FMT_I8 ? 126u << (SHIFT - 7) : 96u << (SHIFT - 7);
+  const int b = max((int)((amax_bits + (ones - top)) >> SHIFT) - off, 0);
+  return amax_bits >= (255u << SHIFT) ? 255u : (uint32_t)b;
 }
 __device__ __forceinline__ float scale_up(uint32_t b) {  // 2^(b-127); 2^-127 is subnormal
   return __uint_as_float(b == 255u ? 0x7fffffffu : b ? b << 23 : 0x00400000u);
 }
-__device__ __forceinline__ float scale_down(uint32_t b) {  // 2^(127-b), b <= 249
-  return __uint_as_float((254u - b) << 23);
+// 2^(127-b), b <= 249; 0 for a block that stands for NaN, whose codes come out 0
+__device__ __forceinline__ float scale_down(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0u : (254u - b) << 23);
 }
 
-// Four values to four code bytes.
+// Four values to four code bytes. inv = 0 gives 0 even for infinities and NaN
+// in int8; e4m3 clears them.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+__device__ __forceinline__ uint32_t encode4(uint64_t ab, uint64_t cd, float inv) {
+  const uint64_t ii = pair(inv, inv);
   if (FMT == FMT_I8) {
     // adding 1.5 * 2^23 leaves the nearest whole number (ties to even) in the low bits
     constexpr float magic = 12582912.f;
-    const uint32_t ua = __float_as_uint(fmaf(a, inv, magic)), ub = __float_as_uint(fmaf(b, inv, magic));
-    const uint32_t uc = __float_as_uint(fmaf(c, inv, magic)), ud = __float_as_uint(fmaf(d, inv, magic));
-    return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
+    const uint64_t mm = pair(magic, magic), x = fma2(ab, ii, mm), y = fma2(cd, ii, mm);
+    return __byte_perm(__byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x0040),
+                       __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x0040), 0x5410);
   }
+  float a, b, c, d;
+  unpair(mul2(ab, ii), a, b);
+  unpair(mul2(cd, ii), c, d);
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// Four code bytes to the values they stand for.
+// Four code bytes to the two pairs of values they stand for.
 template <int FMT>
-__device__ __forceinline__ float4 decode4(uint32_t w, float s) {
+__device__ __forceinline__ void decode4(uint32_t w, float s, uint64_t& ab, uint64_t& cd) {
+  const uint64_t ss = pair(s, s);
   if (FMT == FMT_I8) {
     // byte + 128 in the low bits of 2^23; the subtraction is exact
     w ^= 0x80808080u;
-    constexpr float bias = 8388736.f;  // 2^23 + 128
-    return make_float4((__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - bias) * s,
-                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - bias) * s,
-                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)) - bias) * s,
-                       (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - bias) * s);
+    constexpr float bias = -8388736.f;  // -(2^23 + 128)
+    const uint64_t bb = pair(bias, bias);
+    ab = mul2(add2(pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
+                        __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))), bb), ss);
+    cd = mul2(add2(pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)),
+                        __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443))), bb), ss);
+    return;
   }
   uint32_t lo, hi;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
   const float2 l = __half22float2(*(const __half2*)&lo), h = __half22float2(*(const __half2*)&hi);
-  return make_float4(l.x * s, l.y * s, h.x * s, h.y * s);
+  ab = mul2(pair(l.x, l.y), ss);
+  cd = mul2(pair(h.x, h.y), ss);
+}
+template <int FMT>
+__device__ __forceinline__ float4 decode4(uint32_t w, float s) {
+  uint64_t ab, cd;
+  decode4<FMT>(w, s, ab, cd);
+  float4 v;
+  unpair(ab, v.x, v.y);
+  unpair(cd, v.z, v.w);
+  return v;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 // Maximum over aligned groups of G lanes.
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
@@ -161,34 +181,29 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int c, int n, uin
     if (c + i < n) w[i >> 2] |= (uint32_t)row[c + i] << (8 * (i & 3));
 }
 
-// The same from a maximum known already (bits of the largest |v|).
+// Codes of one thread's E values under a block's scale byte.
 template <int FMT, int E>
-__device__ __forceinline__ uint32_t encode_with(uint32_t amax_bits, const float (&v)[E], uint32_t (&w)[E / 4]) {
-  const uint32_t b = scale_byte<FMT>(group_max<32 / E>(amax_bits));
-  const float inv = scale_down(min(b, 249u));
+__device__ __forceinline__ void encode_unit(uint32_t b, const float (&v)[E], uint32_t (&w)[E / 4]) {
+  const float inv = scale_down(b);
 #pragma unroll
   for (int k = 0; k < E / 4; ++k) {
-    w[k] = encode4<FMT>(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+    w[k] = encode4<FMT>(pair(v[4 * k], v[4 * k + 1]), pair(v[4 * k + 2], v[4 * k + 3]), inv);
     if (b == 255u) w[k] = 0;
   }
-  return b;
 }
-// Largest |value| of eight bf16 (as fp32 bits): bf16 magnitudes order like
-// whole numbers, two at a time.
+// Scale byte of the block that G lanes hold, from each lane's E values.
+template <int FMT, int E>
+__device__ __forceinline__ uint32_t block_byte(const float (&v)[E]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) m = max3_nan(m, fabsf(v[i]), fabsf(v[i + 1]));
+  return scale_byte<FMT, 23>(group_max<32 / E>(__float_as_uint(m)));
+}
+// Larger of each half's magnitudes over eight bf16 (magnitudes order like
+// whole numbers, two at a time).
 __device__ __forceinline__ uint32_t amax_bf16x8(const uint4& u) {
   constexpr uint32_t m = 0x7fff7fffu;
-  const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
-  return max(a << 16, a & 0xffff0000u);
-}
-
-// Codes and scale byte of one thread's unit; the G lanes of the block agree
-// on the scale. Every lane of the warp calls this.
-template <int FMT, int E>
-__device__ __forceinline__ uint32_t encode_unit(const float (&v)[E], uint32_t (&w)[E / 4]) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) am = max(am, abs_bits(v[i]));
-  return encode_with<FMT, E>(am, v, w);
+  return __vmaxu2(__vimax3_u16x2(u.x & m, u.y & m, u.z & m), u.w & m);
 }
 
 // ---------------------------------------------------------------------------
@@ -217,7 +232,8 @@ __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict_
     for (int r = 0; r < kRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
       uint32_t w[E / 4];
-      const uint32_t b = encode_unit<FMT, E>(v[r], w);
+      const uint32_t b = block_byte<FMT, E>(v[r]);
+      encode_unit<FMT, E>(b, v[r], w);
       if (t < T) {
         store_codes<E, VEC>(codes + (size_t)t * ldc, c, n, w);
         if ((threadIdx.x & (G - 1)) == 0 && c < n) scales[(size_t)t * nb + c / 32] = (uint8_t)b;
@@ -283,56 +299,70 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __rest
 // ---------------------------------------------------------------------------
 // RMSNorm forward that keeps its input: one pass over x writes y, rstd and
 // the 8-bit block form (7 bytes a value instead of the 6 of the plain
-// forward). A 128-thread block per row; a thread holds V float4 of the row in
-// registers, eight neighbouring lanes hold a block of 32 columns.
+// forward). A block per row; a thread holds V units of eight columns of the
+// row in registers, four neighbouring lanes hold a block of 32 columns.
 // ---------------------------------------------------------------------------
-constexpr int kFwdThreads = 128;
-
-template <int FMT, int V>
-__global__ void __launch_bounds__(kFwdThreads)
+// Measured at 8192 x 4096 (floor 34.5 us): 256 threads 37.8 us, 128 threads
+// 38.9, four columns a unit 41.2.
+template <int FMT, int NT, int V, bool VEC>
+__global__ void __launch_bounds__(NT)
     rmsnorm_fwd_ckpt8_kernel(const float* __restrict__ x, const float* __restrict__ w, uint16_t* __restrict__ y,
                              float* __restrict__ rstd, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                              int h, int nb, float eps) {
-  __shared__ float red[kFwdThreads / 32];
+  __shared__ float red[NT / 32];
   const size_t t = blockIdx.x;
-  const float4* xr = (const float4*)(x + t * h);
-  const float4* w4 = (const float4*)w;
-  const int n4 = h >> 2, tid = threadIdx.x;
-  float4 v[V];
+  const float* xr = x + t * h;
+  const int tid = threadIdx.x;
+  float v[V][8];
   float ss = 0.f;
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int i = tid + k * kFwdThreads;
-    v[k] = i < n4 ? __ldcs(xr + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int k = 0; k < V; ++k) load_unit<false, VEC>(xr, (tid + k * NT) * 8, h, v[k]);
 #pragma unroll
-  for (int k = 0; k < V; ++k) ss += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      ss += v[k][i] * v[k][i] + v[k][i + 1] * v[k][i + 1] + v[k][i + 2] * v[k][i + 2] + v[k][i + 3] * v[k][i + 3];
   ss = warp_sum(ss);
   if ((tid & 31) == 0) red[tid >> 5] = ss;
   // the checkpoint does not need the norm: its stores go out during the reduction
-  uint32_t* crow = (uint32_t*)(codes + t * h);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int i = tid + k * kFwdThreads;
-    const float u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-    uint32_t q[1];
-    const uint32_t b = encode_unit<FMT, 4>(u, q);
-    if (i < n4) {
-      crow[i] = q[0];
-      if ((tid & 7) == 0) scales[t * nb + i / 8] = (uint8_t)b;
+    const int c = (tid + k * NT) * 8;
+    uint32_t q[2];
+    const uint32_t b = block_byte<FMT, 8>(v[k]);
+    encode_unit<FMT, 8>(b, v[k], q);
+    if (c < h) {
+      store_codes<8, VEC>(codes + t * h, c, h, q);
+      if ((tid & 3) == 0) scales[t * nb + c / 32] = (uint8_t)b;
     }
   }
   __syncthreads();
-  ss = (red[0] + red[1]) + (red[2] + red[3]);
+  ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) ss += red[i];
   const float r = rsqrtf(ss / (float)h + eps);
   if (tid == 0) rstd[t] = r;
-  uint2* yr = (uint2*)(y + t * h);
+  uint16_t* yr = y + t * h;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int i = tid + k * kFwdThreads;
-    if (i < n4) {
-      const float4 g = w4[i];
-      yr[i] = make_uint2(pack_bf2(v[k].x * r * g.x, v[k].y * r * g.y), pack_bf2(v[k].z * r * g.z, v[k].w * r * g.w));
+    const int c = (tid + k * NT) * 8;
+    float g[8];
+    uint32_t o[4];
+    if (VEC && c + 8 <= h) {
+      const float4 g0 = *(const float4*)(w + c), g1 = *(const float4*)(w + c + 4);
+      g[0] = g0.x, g[1] = g0.y, g[2] = g0.z, g[3] = g0.w, g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = c + i < h ? w[c + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf2(v[k][2 * i] * r * g[2 * i], v[k][2 * i + 1] * r * g[2 * i + 1]);
+    if (VEC && c + 8 <= h) {
+      *(uint4*)(yr + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < h) yr[c + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
     }
   }
 }
@@ -344,31 +374,32 @@ __global__ void __launch_bounds__(kFwdThreads)
 // t mod parts, so a part's sum has a fixed order) and hold their share of dw
 // in registers; a second kernel adds the parts in order.
 // ---------------------------------------------------------------------------
-// A block holds a row: V float4 a thread (two where h > 1024), w and the
+// A block holds a row: V float4 a thread (two where h > 4096), w and the
 // sums of dw in registers. One thread requests whole rows of codes, dy and
-// resid kBwdStages - 1 rows ahead as bulk copies into shared memory, so loads
+// resid stages - 1 rows ahead as bulk copies into shared memory, so loads
 // stay in flight across a row's reduction and hold no registers; rows that
 // are not whole 16-byte pieces (BULK false) are loaded by the threads.
-// Measured at 8192 x 4096 (floor 74 us): per-thread loads 103 us, per-thread
-// cp.async staging 128 us (its 4-byte copies and second reads cost more than
-// the loads it hides).
+// Measured at 8192 x 4096 (504 MB, floor 74 us) with the sum of the parts:
+// per-thread loads 103 us, per-thread cp.async staging 128 us (its 4-byte
+// copies and second reads cost more than the loads it hides), bulk copies
+// with two blocks an SM and three stages 87 us, one block and five 82 us.
 // ---------------------------------------------------------------------------
 constexpr int kBwdMaxThreads = 1024;
-constexpr int kBwdStages = 3;
-constexpr int kBwdMaxParts = 1216;  // blocks, and rows of partial sums
+constexpr int kBwdMaxStages = 8;
 
-// Threads and vectors of a block, and blocks: what 152 SMs hold at once by
-// the stages' shared memory (9 h bytes each with a residual), up to eight an SM.
 struct BwdShape {
-  int threads, vecs, parts;
+  int threads, vecs, stages, parts;
 };
+// 1024 threads an SM where the rows allow, the shared memory shared out among
+// their blocks as stages of 9 h bytes (5 h without a residual).
 BwdShape bwd_shape(int T, int h) {
   BwdShape s;
   const int n4 = h / 4;
-  s.vecs = h > 1024 ? 2 : 1;
+  s.vecs = h > 4096 ? 2 : 1;
   s.threads = std::max(32, (n4 + s.vecs * 32 - 1) / (s.vecs * 32) * 32);
-  const int an_sm = std::min({8, 2048 / s.threads, 220 * 1024 / (kBwdStages * 9 * h)});
-  s.parts = std::min(T, std::min(kBwdMaxParts, 152 * std::max(1, an_sm)));
+  const int an_sm = std::min(8, 1024 / s.threads);
+  s.stages = std::min(kBwdMaxStages, 222 * 1024 / an_sm / (9 * h));
+  s.parts = std::min(T, 152 * an_sm);
   return s;
 }
 
@@ -384,10 +415,10 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     rmsnorm_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                              const float* __restrict__ w, const float* __restrict__ rstd,
                              const float* __restrict__ dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
-                             float* __restrict__ part, int T, int h, int nb) {
-  extern __shared__ __align__(128) uint8_t stage[];  // [kBwdStages]: dy, resid, codes of a row
+                             float* __restrict__ part, int T, int h, int nb, int stages) {
+  extern __shared__ __align__(128) uint8_t stage[];  // [stages]: dy, resid, codes of a row
   __shared__ float red[2][kBwdMaxThreads / 32];
-  __shared__ uint64_t full[kBwdStages];
+  __shared__ uint64_t full[kBwdMaxStages];
   __shared__ int abort_flag;
   const int n4 = h >> 2, tid = threadIdx.x, NT = blockDim.x, nw = NT >> 5;
   const float inv_h = 1.f / (float)h;
@@ -403,12 +434,12 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
   if (BULK) {
     if (tid == 0) {
       abort_flag = 0;
-      for (int s = 0; s < kBwdStages; ++s) mbar_init(&full[s], 1);
+      for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
       fence_barrier_init();
     }
     __syncthreads();
     if (tid == 0)
-      for (int s = 0; s < kBwdStages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
+      for (int s = 0; s < stages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
   }
   float4 acc[V], wv[V];
 #pragma unroll
@@ -472,7 +503,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     // two buffers in turn: one barrier a row is enough; it also says that the
     // last row's stage has been read
     __syncthreads();
-    if (BULK && tid == 0) request(t + (kBwdStages - 1) * gridDim.x, st == 0 ? kBwdStages - 1 : st - 1);
+    if (BULK && tid == 0) request(t + (stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
     dot = (tid & 31) < nw ? red[flip][tid & 31] : 0.f;
     const float mean = warp_sum(dot) * r * inv_h;
 #pragma unroll
@@ -497,16 +528,17 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
         acc[j].w += g[j].w * xh.w;
       }
     }
-    if (++st == kBwdStages) {
+    if (++st == stages) {
       st = 0;
       phase ^= 1;
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (BULK && *(volatile int*)&abort_flag) {  // a wait ran out: give the copies in flight time to land
-    for (int k = 0; k < kBwdStages - 1; ++k) {
+    for (int k = 0; k < stages - 1; ++k) {
       for (int spin = 0; spin < (1 << 20) && !mbar_try_wait(smem_u32(&full[st]), phase); ++spin) {
       }
-      if (++st == kBwdStages) {
+      if (++st == stages) {
         st = 0;
         phase ^= 1;
       }
@@ -521,9 +553,12 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
 
 // out[c] = sum over the parts, in a fixed order: 32 warps take the parts in
 // turn for 32 columns, then their sums are added by a shuffle tree.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int nparts, int n,
+// Launched while the kernel that writes the parts still runs (it waits for
+// that kernel's end here), so its own launch costs nothing.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int nparts, int n,
                                                          float* __restrict__ out) {
   __shared__ float red[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
@@ -542,13 +577,24 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 // cut into blocks of 32 separately. A thread owns 8 columns of g and the
 // same 8 of u, four lanes a block.
 // ---------------------------------------------------------------------------
-// 1 / (1 + e^-g), with the hardware reciprocal (one unit in the last place,
-// subnormal results kept): the exact division costs more instructions than
-// the rest of the formula.
-__device__ __forceinline__ float sigmoid_(float g) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
-  return r;
+// 1 / (1 + e^-g) of two values with the hardware's exponential and
+// reciprocal (the exact division and the subnormal range of both cost more
+// instructions than the rest of the formula): results below 2^-126 are 0.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  constexpr float k = -1.4426950408889634f;
+  float a, b;
+  unpair(mul2(g, pair(k, k)), a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  unpair(add2(pair(a, b), pair(1.f, 1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pair(a, b);
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  unpair(v, a, b);
+  return pack_bf2(a, b);
 }
 __device__ __forceinline__ void spread8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -591,28 +637,36 @@ __global__ void __launch_bounds__(256) swiglu_fwd_ckpt8_kernel(const uint16_t* _
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
+      // the maxima of g and u, a half of a word each, go through the shuffles together
+      const uint32_t mg = amax_bf16x8(gq[r]), mu = amax_bf16x8(uq[r]);
+      uint32_t m = __vmaxu2(__byte_perm(mg, mu, 0x5410), __byte_perm(mg, mu, 0x7632));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
       float g[8], u[8];
       spread8(gq[r], g);
       spread8(uq[r], u);
       uint32_t wg[2], wu[2];
-      const uint32_t bg = encode_with<FMT, 8>(amax_bf16x8(gq[r]), g, wg);
-      const uint32_t bu = encode_with<FMT, 8>(amax_bf16x8(uq[r]), u, wu);
+      const uint32_t bg = scale_byte<FMT, 7>(m & 0xffffu), bu = scale_byte<FMT, 7>(m >> 16);
+      encode_unit<FMT, 8>(bg, g, wg);
+      encode_unit<FMT, 8>(bu, u, wu);
       if (t < T) {
-        float a[8];
+        uint32_t a[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = g[i] * sigmoid_(g[i]) * u[i];
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t g2 = pair(g[2 * i], g[2 * i + 1]), u2 = pair(u[2 * i], u[2 * i + 1]);
+          a[i] = pack_pair(mul2(mul2(g2, sigmoid2(g2)), u2));
+        }
         uint8_t* crow = codes + (size_t)t * 2 * ld;
         uint16_t* arow = act + (size_t)t * ld;
         // columns F..ld-1 are padding: codes and act are 0 there (the loads gave 0)
         store_codes<8, VEC>(crow, c, ld, wg);
         store_codes<8, VEC>(crow + ld, c, ld, wu);
         if (VEC && c + 8 <= ld) {
-          *(uint4*)(arow + c) = make_uint4(pack_bf2(a[0], a[1]), pack_bf2(a[2], a[3]), pack_bf2(a[4], a[5]),
-                                           pack_bf2(a[6], a[7]));
+          *(uint4*)(arow + c) = make_uint4(a[0], a[1], a[2], a[3]);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (c + i < ld) arow[c + i] = f2bf(a[i]);
+            if (c + i < ld) arow[c + i] = (uint16_t)(a[i >> 1] >> (16 * (i & 1)));
         }
         if ((threadIdx.x & 3) == 0 && c < F) {
           scales[(size_t)t * 2 * nb + c / 32] = (uint8_t)bg;
@@ -654,31 +708,34 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
       const int t = t0 + r * step;
       if (t >= T) break;
       const float sg = scale_up(bg[r]), su = scale_up(bu[r]);
-      float d[8], og[8], ou[8];
+      float d[8];
       spread8(dq[r], d);
+      uint32_t og[4], ou[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 g4 = decode4<FMT>(wg[r][k], sg), u4 = decode4<FMT>(wu[r][k], su);
-        const float gg[4] = {g4.x, g4.y, g4.z, g4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
+        uint64_t g2[2], u2[2];
+        decode4<FMT>(wg[r][k], sg, g2[0], g2[1]);
+        decode4<FMT>(wu[r][k], su, u2[0], u2[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = sigmoid_(gg[i]), ds = d[4 * k + i] * s, du = ds * gg[i];
-          og[4 * k + i] = uu[i] * fmaf(du, 1.f - s, ds);  // dact u s (1 + g (1 - s))
-          ou[4 * k + i] = du;
+        for (int i = 0; i < 2; ++i) {
+          const int e = 4 * k + 2 * i;
+          const uint64_t s = sigmoid2(g2[i]), ds = mul2(pair(d[e], d[e + 1]), s), du = mul2(ds, g2[i]);
+          // dact u s (1 + g (1 - s)); dact g s
+          const uint64_t rest = fma2(s, pair(-1.f, -1.f), pair(1.f, 1.f));
+          og[2 * k + i] = pack_pair(mul2(u2[i], fma2(du, rest, ds)));
+          ou[2 * k + i] = pack_pair(du);
         }
       }
       uint16_t* row = dgu + (size_t)t * 2 * ld;
       if (VEC && c + 8 <= F) {
-        *(uint4*)(row + c) = make_uint4(pack_bf2(og[0], og[1]), pack_bf2(og[2], og[3]), pack_bf2(og[4], og[5]),
-                                        pack_bf2(og[6], og[7]));
-        *(uint4*)(row + ld + c) = make_uint4(pack_bf2(ou[0], ou[1]), pack_bf2(ou[2], ou[3]), pack_bf2(ou[4], ou[5]),
-                                             pack_bf2(ou[6], ou[7]));
+        *(uint4*)(row + c) = make_uint4(og[0], og[1], og[2], og[3]);
+        *(uint4*)(row + ld + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (c + i < ld) {  // padding columns carry no gradient
-            row[c + i] = c + i < F ? f2bf(og[i]) : (uint16_t)0;
-            row[ld + c + i] = c + i < F ? f2bf(ou[i]) : (uint16_t)0;
+            row[c + i] = c + i < F ? (uint16_t)(og[i >> 1] >> (16 * (i & 1))) : (uint16_t)0;
+            row[ld + c + i] = c + i < F ? (uint16_t)(ou[i >> 1] >> (16 * (i & 1))) : (uint16_t)0;
           }
       }
     }
@@ -746,21 +803,24 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
 
 int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, uint8_t* codes, uint8_t* scales,
                       int fmt, int T, int h, float eps, cudaStream_t st) {
-  if (T <= 0 || h <= 0 || (h & 3) || h > 16 * 4 * kFwdThreads || !fmt_ok(fmt) || !al(x, 16) || !al(w, 16) ||
+  if (T <= 0 || h <= 0 || (h & 3) || h > 8192 || !fmt_ok(fmt) || !al(x, 16) || !al(w, 16) ||
       !al(y, 8) || !al(codes, 4))
     return -1;
-  const int n4 = h / 4, nb = blocks32(h);
-  auto go = [&](auto k) { k<<<T, kFwdThreads, 0, st>>>(x, w, y, rstd, codes, scales, h, nb, eps); };
-  auto pick = [&](auto f) {
+  const int units = (h + 7) / 8, nb = blocks32(h);
+  // whole units where every row starts on a 32-byte boundary
+  const bool vec = h % 8 == 0 && al(x, 32) && al(y, 16) && al(codes, 8);
+  auto go = [&](auto k, int threads) { k<<<T, threads, 0, st>>>(x, w, y, rstd, codes, scales, h, nb, eps); };
+  auto pick = [&](auto f, auto v) {
     constexpr int F = decltype(f)::value;
-    if (n4 <= kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 1>);
-    else if (n4 <= 2 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 2>);
-    else if (n4 <= 4 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 4>);
-    else if (n4 <= 8 * kFwdThreads) go(rmsnorm_fwd_ckpt8_kernel<F, 8>);
-    else go(rmsnorm_fwd_ckpt8_kernel<F, 16>);
+    constexpr bool X = decltype(v)::value;
+    if (units <= 128) go(rmsnorm_fwd_ckpt8_kernel<F, 128, 1, X>, 128);
+    else if (units <= 256) go(rmsnorm_fwd_ckpt8_kernel<F, 256, 1, X>, 256);
+    else if (units <= 512) go(rmsnorm_fwd_ckpt8_kernel<F, 256, 2, X>, 256);
+    else go(rmsnorm_fwd_ckpt8_kernel<F, 256, 4, X>, 256);
   };
-  if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
-  else pick(std::integral_constant<int, FMT_E4M3>());
+  auto pick_f = [&](auto f) { vec ? pick(f, std::true_type()) : pick(f, std::false_type()); };
+  if (fmt == FMT_I8) pick_f(std::integral_constant<int, FMT_I8>());
+  else pick_f(std::integral_constant<int, FMT_E4M3>());
   return done(1);
 }
 
@@ -777,11 +837,12 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   const bool bulk = h % 16 == 0 && al(codes, 16);  // every row of codes starts and ends on 16 bytes
   bool ok = true;
   auto go = [&](auto k, bool staged) {
-    const int smem = staged ? kBwdStages * h * (resid ? 9 : 5) : 0;
+    const int smem = staged ? shape.stages * h * (resid ? 9 : 5) : 0;
     if (smem > 48 * 1024)
-      ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdStages * 9 * 8192) == cudaSuccess;
+      ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) == cudaSuccess;
     if (ok)
-      k<<<shape.parts, shape.threads, smem, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb);
+      k<<<shape.parts, shape.threads, smem, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb,
+                                                  shape.stages);
   };
   auto pick = [&](auto f) {
     constexpr int F = decltype(f)::value;
@@ -791,7 +852,16 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
   if (!ok) return -1;
-  sum_parts_kernel<<<(h + 31) / 32, 1024, 0, st>>>(work, shape.parts, h, dw);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((h + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, sum_parts_kernel, (const float*)work, shape.parts, h, dw) != cudaSuccess) return -1;
   return done(2);
 }
 
