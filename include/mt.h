@@ -576,7 +576,7 @@ int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, floa
 /* The table's gradient: dtable[v] = scale * sum of dout[t] over the t with
  * ids[t] = v, every row written (0 for unused ids); accumulate != 0: dtable
  * += that, rows of unused ids left as they are. Sums in fp32, in a fixed
- * order (ascending positions): deterministic. workspace:
+ * order (ascending positions, long runs in pieces): deterministic. workspace:
  * mt_op_embed_bwd_workspace(T, V, h) bytes of device memory, 256-byte
  * aligned (0 for sizes the call refuses). Ids outside [0, V) as above. */
 size_t mt_op_embed_bwd_workspace(int T, int V, int h);

@@ -4,15 +4,16 @@
 // Backward: dtable[v] = scale * sum of dout[t] over the positions t with
 // id_t = v, in 32 bits and in a fixed order, so it is bitwise reproducible:
 //  1. one cluster of eight blocks sorts the positions by id (stable radix
-//     sort, so equal ids keep ascending positions) and writes, for every
-//     vocabulary row, its range of sorted positions; ranges longer than 64
-//     are cut into pieces;
-//  2. the pieces are summed, each in position order;
-//  3. every row of the table gets its sum (short ranges straight from dout,
-//     long ones from their pieces in order) or zeros.
+//     sort, so equal ids keep ascending positions) and lists the runs of
+//     equal ids, those longer than 8 in pieces; meanwhile the other blocks of
+//     the same launch clear the table's gradient;
+//  2. blocks take the pieces in turn, then warps the short runs, and add
+//     their rows in position order; the block that finishes a run's last
+//     piece adds the pieces in order.
 // The pieces keep a frequent id (or a constant batch) from leaving one block
 // with all the work. HBM traffic bounds the whole: dout read once, the table's
-// gradient written once.
+// gradient written once (used rows twice). The sort (12 us for small batches)
+// hides behind the clearing of all but small tables.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,6 +63,11 @@ __device__ __forceinline__ void storen(void* p, size_t i, const float4& v) {
   if (N == 4) store4<BF16>(p, i, v);
   else store1<BF16>(p, i, v.x);
 }
+// N partial sums that another block wrote during this launch.
+template <int N>
+__device__ __forceinline__ float4 load_part(const float* p, size_t i) {
+  return N == 4 ? __ldcg((const float4*)(p + i)) : make_float4(__ldcg(p + i), 0.f, 0.f, 0.f);
+}
 __device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
@@ -105,44 +111,101 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
 // contiguous part of the positions; a pass counts its digits per warp (equal
 // digits of 32 neighbouring keys are found with match.any), turns the counts
 // into offsets (digit, then block, then warp: a stable order) with one scan
-// over the cluster, and walks its part again to place its keys.
+// over the cluster, and walks its part again to place its keys. The last step
+// counts and lists the heads of runs the same way.
 // ---------------------------------------------------------------------------
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 10;  // bits: 32 warps x 1024 counters in shared memory
-constexpr int kShort = 64;     // longest range summed in one go
+constexpr int kShort = 8;      // longest run summed by one warp
+constexpr int kPiece = 32;     // least length of a longer run's pieces
+constexpr int kClearBytes = 128 * 1024;  // cleared by one block
 
 struct SortArgs {
   const int32_t* ids;
-  int2 *a, *b;      // (key, position), ping-pong
-  int2* range;      // [V]: sorted positions [x, y) of an id
-  int32_t* piece0;  // [V]: first piece of a long range
-  int4* pieces;     // (first, last) sorted position of a piece
-  int32_t* n_pieces;
-  int T, V, passes, digit;
+  int2 *a, *b;       // (key, position), ping-pong
+  int32_t* head;     // first sorted position of each run, then the end
+  int4* runs;        // of each run: sorted positions [x, y), id z, w: first position (short) or first partial sum
+  int4* pieces;      // sorted positions [x, y), run z, partial sum w (-1: the piece is the run)
+  int32_t* left;     // per run and column chunk: pieces not yet summed
+  int32_t* n;        // [0] pieces, [1] partial sums, [2] runs
+  void* clear;       // table gradient to clear (null: none)
+  size_t clear_bytes;
+  int T, V, passes, digit, chunks;
 };
 
-// Positions a piece of a range of n covers: about the square root of n, so
-// that summing a piece and adding up the pieces take equally long.
+// Positions a piece of a run of n covers: about the square root of n, so that
+// summing a piece and adding up the pieces take equally long.
 __host__ __device__ inline int piece_len(int n) {
-  int l = kShort;
+  int l = kPiece;
   while ((long long)l * l < n) l *= 2;
   return l;
 }
 
+// One block's share of clearing: 16-byte stores, 2-byte ones at the ends.
+__device__ __forceinline__ void clear_share(void* base, size_t bytes, int block) {
+  uint8_t* p = (uint8_t*)base;
+  const size_t head = min((size_t)((16 - ((uintptr_t)p & 15)) & 15), bytes);
+  const size_t vecs = (bytes - head) / 16;
+  constexpr size_t per = kClearBytes / 16;
+  const size_t lo = (size_t)block * per, hi = min(lo + per, vecs);
+  uint4* v = (uint4*)(p + head);
+  const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
+  for (size_t i = lo + threadIdx.x; i < hi; i += kSortThreads) v[i] = z;
+  if (block == 0) {
+    uint16_t* e = (uint16_t*)p;
+    const size_t tail = head + vecs * 16;
+    if (threadIdx.x < head / 2) e[threadIdx.x] = 0;
+    if (threadIdx.x < (bytes - tail) / 2) e[tail / 2 + threadIdx.x] = 0;
+  }
+}
+
+// Exclusive sum of x over the block's threads.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* scratch) {
+  const uint32_t lane = lane_id(), warp = warp_id();
+  uint32_t s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if ((int)lane >= o) s += y;
+  }
+  if (lane == 31) scratch[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t v = scratch[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if ((int)lane >= o) v += y;
+    }
+    scratch[lane] = v;
+  }
+  __syncthreads();
+  return s - x + (warp ? scratch[warp - 1] : 0u);
+}
+__device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(mapa_shared(p, rank)) : "memory");
+  return x;
+}
+
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the block's totals [bins]
-  __shared__ uint32_t scan[kSortWarps];
+  __shared__ uint32_t scratch[kSortWarps];
+  __shared__ uint32_t heads[kSortWarps + 1];  // run heads of each warp's part, of the block
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums wait for this launch's end themselves
+  if (blockIdx.x >= kSortCtas) {
+    clear_share(a.clear, a.clear_bytes, (int)blockIdx.x - kSortCtas);
+    return;
+  }
   const int bins = 1 << a.digit;
   uint32_t* tot = cnt + kSortWarps * bins;
-  const uint32_t rank = cluster_rank(), warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank(), warp = warp_id(), lane = lane_id(), below_mask = (1u << lane) - 1;
   const int tid = threadIdx.x;
   uint32_t* mine = cnt + warp * bins;
-
-  // empty ranges, while the first pass runs
-  for (int v = (int)rank * kSortThreads + tid; v < a.V; v += kSortCtas * kSortThreads) a.range[v] = make_int2(0, 0);
-  if (rank == 0 && tid == 0) *a.n_pieces = 0;
+  if (rank == 0 && tid == 0) a.n[0] = a.n[1] = 0;
 
   // the warp's part: whole groups of 32 positions
   const int groups = (a.T + 31) / 32, all = kSortCtas * kSortWarps;
@@ -155,57 +218,45 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     int2* dst = (p & 1) ? a.b : a.a;
     const int shift = p * a.digit;
     auto key_at = [&](int i) {
+      if (i >= hi) return make_int2(0, 0);
       if (src) return __ldcg(src + i);
       const int id = a.ids[i];
       if (id >= a.V) report_error(kErrBadArg);
       return make_int2(id < 0 || id >= a.V ? a.V : id, i);  // ids outside the table sort last
     };
+    int2 next = key_at(lo + (int)lane);
     for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
       const bool on = i + (int)lane < hi;
-      const uint32_t d = on ? ((uint32_t)key_at(i + (int)lane).x >> shift) & (bins - 1) : 0xffffffffu;
+      const uint32_t d = on ? ((uint32_t)next.x >> shift) & (bins - 1) : 0xffffffffu;
+      next = key_at(i + 32 + (int)lane);
       const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      if (on && (peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+      if (on && (peers & below_mask) == 0) mine[d] += __popc(peers);
       __syncwarp();
     }
+    next = key_at(lo + (int)lane);
     __syncthreads();
     uint32_t own = 0;
     if (tid < bins) {
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) own += cnt[w * bins + tid];
       tot[tid] = own;
     }
     cluster_sync();
     uint32_t before = 0, total = 0;
     if (tid < bins) {
+#pragma unroll
       for (uint32_t r = 0; r < kSortCtas; ++r) {
-        uint32_t x;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(mapa_shared(tot + tid, r)) : "memory");
+        const uint32_t x = peer_word(tot + tid, r);
         if (r < rank) before += x;
         total += x;
       }
     }
-    // exclusive sum of the digits' totals over the block
-    uint32_t s = total;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
-      if ((int)lane >= o) s += x;
-    }
-    if (lane == 31) scan[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t x = scan[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((int)lane >= o) x += y;
-      }
-      scan[lane] = x;
-    }
-    __syncthreads();
+    const uint32_t base = block_scan(total, scratch);
     if (tid < bins) {
-      uint32_t at = s - total + (warp ? scan[warp - 1] : 0u) + before;
+      uint32_t at = base + before;
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t x = cnt[w * bins + tid];
         cnt[w * bins + tid] = at;
@@ -215,10 +266,11 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
       const bool on = i + (int)lane < hi;
-      const int2 kv = on ? key_at(i + (int)lane) : make_int2(0, 0);
+      const int2 kv = next;
       const uint32_t d = on ? ((uint32_t)kv.x >> shift) & (bins - 1) : 0xffffffffu;
+      next = key_at(i + 32 + (int)lane);
       const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      const uint32_t below = __popc(peers & ((1u << lane) - 1));
+      const uint32_t below = __popc(peers & below_mask);
       uint32_t at = 0;
       if (on) at = mine[d] + below;
       __syncwarp();
@@ -228,98 +280,174 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       }
       __syncwarp();
     }
-    cluster_sync();  // the sorted keys (and, after the first pass, the empty ranges) are visible to the cluster
+    cluster_sync();  // the sorted keys are visible to the cluster
   }
 
-  // ranges of equal ids
+  // heads of runs of equal ids: counted, then listed in order
   const int2* s = (a.passes & 1) ? a.a : a.b;
-  for (int i = (int)rank * kSortThreads + tid; i < a.T; i += kSortCtas * kSortThreads) {
-    const int k = __ldcg(s + i).x;
-    if (k >= a.V) continue;
-    if (i == 0 || __ldcg(s + i - 1).x != k) __stcg(&a.range[k].x, i);
-    if (i == a.T - 1 || __ldcg(s + i + 1).x != k) __stcg(&a.range[k].y, i + 1);
+  auto is_head = [&](int i) { return i < hi && (i == 0 || __ldcg(s + i).x != __ldcg(s + i - 1).x); };
+  uint32_t h = 0;
+  for (int i = lo; i < hi; i += 32) h += __popc(__ballot_sync(0xffffffffu, is_head(i + (int)lane)));
+  if (lane == 0) heads[warp] = h;
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t x = heads[w];
+      heads[w] = sum;
+      sum += x;
+    }
+    heads[kSortWarps] = sum;
   }
   cluster_sync();
-  // pieces of the long ones
-  for (int i = (int)rank * kSortThreads + tid; i < a.T; i += kSortCtas * kSortThreads) {
-    const int k = __ldcg(s + i).x;
-    if (k >= a.V || (i > 0 && __ldcg(s + i - 1).x == k)) continue;
-    const int end = __ldcg(&a.range[k].y), n = end - i;
-    if (n <= kShort) continue;
-    const int l = piece_len(n), np = (n + l - 1) / l;
-    const int p0 = atomicAdd(a.n_pieces, np);  // where a range's pieces lie does not enter their sums
-    a.piece0[k] = p0;
-    for (int q = 0; q < np; ++q) a.pieces[p0 + q] = make_int4(i + q * l, min(end, i + (q + 1) * l), 0, 0);
+  uint32_t at = heads[warp], runs = 0;
+  for (uint32_t r = 0; r < kSortCtas; ++r) {
+    const uint32_t x = peer_word(&heads[kSortWarps], r);
+    if (r < rank) at += x;
+    runs += x;
+  }
+  for (int i = lo; i < hi; i += 32) {
+    const bool here = is_head(i + (int)lane);
+    const uint32_t m = __ballot_sync(0xffffffffu, here);
+    if (here) __stcg(a.head + at + __popc(m & below_mask), i + (int)lane);
+    at += __popc(m);
+  }
+  if (rank == 0 && tid == 0) {
+    __stcg(a.head + runs, a.T);
+    a.n[2] = (int)runs;
+  }
+  cluster_sync();
+  for (int r = (int)rank * kSortThreads + tid; r < (int)runs; r += kSortCtas * kSortThreads) {
+    const int x = __ldcg(a.head + r), id = __ldcg(s + x).x;
+    const int y = id < a.V ? __ldcg(a.head + r + 1) : x, n = y - x;  // ids outside the table: an empty run
+    int w = 0;
+    if (n > kShort) {
+      const int l = piece_len(n), np = (n + l - 1) / l, p0 = atomicAdd(a.n, np);
+      // where a run's pieces and partial sums lie does not enter their values
+      w = np > 1 ? atomicAdd(a.n + 1, np) : -1;
+      for (int q = 0; q < np; ++q)
+        a.pieces[p0 + q] = make_int4(x + q * l, min(y, x + (q + 1) * l), r, np > 1 ? w + q : -1);
+      if (np > 1)
+        for (int c = 0; c < a.chunks; ++c) a.left[(size_t)r * a.chunks + c] = np;
+    } else if (n > 0) {
+      w = __ldcg(s + x).y;
+    }
+    a.runs[r] = make_int4(x, y, id, w);
   }
 }
 
-// Sum of dout over the sorted positions [i0, i1), N columns from c: eight
-// rows' loads in flight, added in position order.
+// ---------------------------------------------------------------------------
+// Sums, 256 N columns at a time. A block adds a piece with a column group of
+// N a thread and eight rows in flight. A warp adds a short run with eight
+// column groups a thread, the next row requested under the sum of the last:
+// most runs have one or two rows, and only many bytes in flight a warp hide
+// the way from the run's entry to its rows and the table (one block a run,
+// one group a thread: 166 against 106 us for 8192 tokens of 128256 x 4096,
+// added to the table).
+// ---------------------------------------------------------------------------
 template <bool DB, int N>
 __device__ __forceinline__ float4 sum_rows(const int2* s, int i0, int i1, const void* dout, int h, int c) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int i = i0;
-  for (; i + 8 <= i1; i += 8) {
+  for (int i = i0; i < i1; i += 8) {
     float4 v[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = loadn<DB, N>(dout, (size_t)s[i + q].y * h + c);
+    for (int q = 0; q < 8; ++q)
+      if (i + q < i1) v[q] = loadn<DB, N>(dout, (size_t)s[i + q].y * h + c);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc = add4(acc, v[q]);
+    for (int q = 0; q < 8; ++q)
+      if (i + q < i1) acc = add4(acc, v[q]);
   }
-  for (; i < i1; ++i) acc = add4(acc, loadn<DB, N>(dout, (size_t)s[i].y * h + c));
   return acc;
 }
 
-template <bool DB, int N>
-__global__ void __launch_bounds__(256) embed_pieces_kernel(const int2* __restrict__ s, const int4* __restrict__ pieces,
-                                                           const int32_t* __restrict__ n_pieces,
-                                                           const void* __restrict__ dout, float* __restrict__ part,
-                                                           int h) {
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
-  if (c >= h) return;
-  const int n = *n_pieces;
-  for (int p = blockIdx.x; p < n; p += gridDim.x) {
-    const int4 d = pieces[p];
-    storen<false, N>(part, (size_t)p * h + c, sum_rows<DB, N>(s, d.x, d.y, dout, h, c));
-  }
-}
-
-constexpr int kTableRows = 8;  // vocabulary rows of a block
-
 template <bool DB, bool EB, int N>
-__global__ void __launch_bounds__(256) embed_table_kernel(const int2* __restrict__ s, const int2* __restrict__ range,
-                                                          const int32_t* __restrict__ piece0,
-                                                          const float* __restrict__ part,
-                                                          const void* __restrict__ dout, float scale, void* dtable,
-                                                          int V, int h, int add) {
-  __shared__ int2 sr[kTableRows];
-  const int v0 = blockIdx.x * kTableRows, rows = min(kTableRows, V - v0);
-  if ((int)threadIdx.x < rows) sr[threadIdx.x] = range[v0 + threadIdx.x];
-  __syncthreads();
-  for (int r = 0; r < rows; ++r) {
-    const int2 d = sr[r];
-    const int n = d.y - d.x;
-    if (n == 0 && add) continue;
-    const size_t at = (size_t)(v0 + r) * h;
-    const int l = piece_len(n), np = (n + l - 1) / l;
-    const int p0 = n > kShort ? piece0[v0 + r] : 0;
-    for (int c = threadIdx.x * N; c < h; c += blockDim.x * N) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (n > kShort) {
-#pragma unroll 8
-        for (int p = 0; p < np; ++p) acc = add4(acc, loadn<false, N>(part, (size_t)(p0 + p) * h + c));
-      } else if (n > 0) {
-        acc = sum_rows<DB, N>(s, d.x, d.y, dout, h, c);
+__global__ void __launch_bounds__(256, 2) embed_sum_kernel(const int2* s, const int4* runs, const int4* pieces,
+                                                           int32_t* left, const int32_t* n, float* part,
+                                                           const void* __restrict__ dout, float scale, void* dtable,
+                                                           int h, int add) {
+  __shared__ int last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int chunk = blockIdx.y, n_pieces = n[0], n_runs = n[2];
+  const int c = (chunk * 256 + (int)threadIdx.x) * N;
+  auto finish = [&](int id, float4 acc) {
+    acc = scaled(acc, scale);
+    const size_t at = (size_t)id * h + c;
+    if (add) acc = add4(loadn<EB, N>(dtable, at), acc);
+    storen<EB, N>(dtable, at, acc);
+  };
+  for (int i = blockIdx.x; i < n_pieces; i += gridDim.x) {
+    const int4 d = pieces[i];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < h) acc = sum_rows<DB, N>(s, d.x, d.y, dout, h, c);
+    if (d.w < 0) {
+      if (c < h) finish(runs[d.z].z, acc);
+      continue;
+    }
+    if (c < h) storen<false, N>(part, (size_t)d.w * h + c, acc);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicSub(&left[(size_t)d.z * gridDim.y + chunk], 1) == 1;
+    __syncthreads();
+    if (last && c < h) {  // every piece of the run is there: add them in order
+      __threadfence();
+      const int4 r = runs[d.z];
+      const int l = piece_len(r.y - r.x), k = (r.y - r.x + l - 1) / l;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < k; q += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q + j < k) v[j] = load_part<N>(part, (size_t)(r.w + q + j) * h + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q + j < k) acc = add4(acc, v[j]);
       }
-      acc = scaled(acc, scale);
-      if (add) acc = add4(loadn<EB, N>(dtable, at + c), acc);
-      storen<EB, N>(dtable, at + c, acc);
+      finish(r.z, acc);
+    }
+    __syncthreads();  // `last` is read before the next piece sets it
+  }
+
+  // short runs
+  const int lane = (int)lane_id(), step = gridDim.x * 8;
+  const int c0 = chunk * 256 * N + lane * N;  // column groups c0 + 32 N k
+  auto row = [&](int pos, float4 (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + 32 * N * k < h) v[k] = loadn<DB, N>(dout, (size_t)pos * h + c0 + 32 * N * k);
+  };
+  auto entry = [&](int i) { return i < n_runs ? runs[i] : make_int4(0, 0, 0, 0); };
+  int i = blockIdx.x * 8 + (int)warp_id();
+  int4 next = entry(i);
+  for (; i < n_runs; i += step) {
+    const int4 d = next;
+    next = entry(i + step);
+    const int rows = d.y - d.x;
+    if (rows == 0 || rows > kShort) continue;
+    float4 acc[8], v[8];
+    row(d.w, acc);
+    const int pos = lane < rows ? s[d.x + lane].y : 0;
+    if (rows > 1) row(__shfl_sync(0xffffffffu, pos, 1), v);
+    for (int q = 1; q < rows; ++q) {
+      const int p = __shfl_sync(0xffffffffu, pos, q + 1 < rows ? q + 1 : 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = add4(acc[k], v[k]);
+      if (q + 1 < rows) row(p, v);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int cc = c0 + 32 * N * k;
+      if (cc < h) {
+        const size_t at = (size_t)d.z * h + cc;
+        acc[k] = scaled(acc[k], scale);
+        if (add) acc[k] = add4(loadn<EB, N>(dtable, at), acc[k]);
+        storen<EB, N>(dtable, at, acc[k]);
+      }
     }
   }
 }
 
 struct EmbedWs {
-  size_t a, b, range, piece0, pieces, n_pieces, part, total;
+  size_t a, b, head, runs, pieces, left, n, part, total;
 };
 EmbedWs embed_ws(int T, int V, int h) {
   EmbedWs o;
@@ -329,20 +457,23 @@ EmbedWs embed_ws(int T, int V, int h) {
     x += (bytes + 255) / 256 * 256;
     return r;
   };
-  const size_t max_pieces = (size_t)T / 32 + 1;  // ranges over 64, pieces of 64 or more
+  const size_t max_pieces = (size_t)T / 8 + 1;  // runs over 8: one piece, or pieces of 32 or more
+  const size_t max_parts = (size_t)T / 16 + 1;  // runs over 32
+  const size_t max_runs = std::min((size_t)T, (size_t)V + 1);
   o.a = take((size_t)T * 8);
   o.b = take((size_t)T * 8);
-  o.range = take((size_t)V * 8);
-  o.piece0 = take((size_t)V * 4);
+  o.head = take((max_runs + 1) * 4);
+  o.runs = take(max_runs * 16);
   o.pieces = take(max_pieces * 16);
-  o.n_pieces = take(4);
-  o.part = take(max_pieces * (size_t)h * 4);
+  o.left = take(max_runs * (size_t)((h + 255) / 256) * 4);
+  o.n = take(12);
+  o.part = take(max_parts * (size_t)h * 4);
   o.total = x;
   return o;
 }
 
 bool embed_dims_ok(int T, int V, int h) {
-  return T > 0 && V > 0 && h > 0 && T <= (1 << 28) && V < (1 << 30) && h <= (1 << 24);
+  return T > 0 && V > 0 && h > 0 && T <= (1 << 28) && V < (1 << 30) && h <= (1 << 22);
 }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -377,16 +508,22 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (!embed_dims_ok(T, V, h) || !al(work, 256) || !al(dout, db ? 2 : 4) || !al(dtable, eb ? 2 : 4)) return -1;
   const EmbedWs o = embed_ws(T, V, h);
   uint8_t* w = (uint8_t*)work;
+  const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
+  const int units = vec ? h / 4 : h;
   SortArgs a;
   a.ids = ids;
   a.a = (int2*)(w + o.a);
   a.b = (int2*)(w + o.b);
-  a.range = (int2*)(w + o.range);
-  a.piece0 = (int32_t*)(w + o.piece0);
+  a.head = (int32_t*)(w + o.head);
+  a.runs = (int4*)(w + o.runs);
   a.pieces = (int4*)(w + o.pieces);
-  a.n_pieces = (int32_t*)(w + o.n_pieces);
+  a.left = (int32_t*)(w + o.left);
+  a.n = (int32_t*)(w + o.n);
+  a.clear = add ? nullptr : dtable;
+  a.clear_bytes = add ? 0 : (size_t)V * h * (eb ? 2 : 4);
   a.T = T;
   a.V = V;
+  a.chunks = (units + 255) / 256;
   int bits = 1;
   while ((V >> bits) != 0) ++bits;  // keys 0..V
   a.passes = (bits + kMaxDigit - 1) / kMaxDigit;
@@ -395,31 +532,37 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ((kSortWarps + 1) << kMaxDigit) * 4) != cudaSuccess)
     return -1;
-  embed_sort_kernel<<<kSortCtas, kSortThreads, smem, st>>>(a);
-  const int2* s = (a.passes & 1) ? a.a : a.b;
-  float* part = (float*)(w + o.part);
-  const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
-  const int units = vec ? h / 4 : h;
-  const int cols = (units + 255) / 256;
-  const bool long_ranges = T > kShort;
-  auto pieces = [&](auto k) {
-    k<<<dim3((unsigned)std::min(T / 32 + 1, 2048), (unsigned)cols), 256, 0, st>>>(s, a.pieces, a.n_pieces, dout, part,
-                                                                                 h);
-  };
-  auto table = [&](auto k) {
-    k<<<(V + kTableRows - 1) / kTableRows, 256, 0, st>>>(s, a.range, a.piece0, part, dout, scale, dtable, V, h,
-                                                        add ? 1 : 0);
+  size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
+  clearers = (clearers + kSortCtas - 1) / kSortCtas * kSortCtas;
+  if (clearers > (1u << 30)) return -1;
+  embed_sort_kernel<<<(unsigned)(kSortCtas + clearers), kSortThreads, smem, st>>>(a);
+
+  // as many blocks as run at once, launched while the last ones of the sort end
+  const int most = std::max(T / 8 + 1, (std::min(T, V) + 7) / 8), fit = std::max(1, 152 * 2 / a.chunks);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min(most, fit), (unsigned)a.chunks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) {
+    e = cudaLaunchKernelEx(&cfg, k, (const int2*)((a.passes & 1) ? a.a : a.b), (const int4*)a.runs,
+                           (const int4*)a.pieces, a.left, (const int32_t*)a.n, (float*)(w + o.part), dout, scale,
+                           dtable, h, add ? 1 : 0);
   };
   auto pick = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    if (long_ranges) db ? pieces(embed_pieces_kernel<true, N>) : pieces(embed_pieces_kernel<false, N>);
-    if (db) eb ? table(embed_table_kernel<true, true, N>) : table(embed_table_kernel<true, false, N>);
-    else eb ? table(embed_table_kernel<false, true, N>) : table(embed_table_kernel<false, false, N>);
+    if (db) eb ? go(embed_sum_kernel<true, true, N>) : go(embed_sum_kernel<true, false, N>);
+    else eb ? go(embed_sum_kernel<false, true, N>) : go(embed_sum_kernel<false, false, N>);
   };
   if (vec) pick(std::integral_constant<int, 4>());
   else pick(std::integral_constant<int, 1>());
-  count_launches(long_ranges ? 3 : 2);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  count_launches(2);
+  return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace mt

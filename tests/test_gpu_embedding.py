@@ -112,16 +112,17 @@ def test_sort_over_the_vocabulary(V):
 
 
 def test_sum_order_is_by_position():
-    """fp32 sums of a short range are those of adding its rows in ascending position."""
+    """fp32 sums are those of adding the rows in ascending position, runs
+    longer than 32 in pieces of 32 whose sums are then added in order."""
     torch, mt = need_gpu()
     T, V, h = 40, 2, 4
     dout = (torch.randn((T, h), device="cuda") * torch.exp(4 * torch.randn((T, 1), device="cuda")))
     ids = torch.zeros(T, dtype=torch.int32, device="cuda")
-    got = from_dev(_grad(torch, mt, ids, dout, False, False, 1.0, V))[0]
-    want = np.zeros(h, np.float32)
-    for row in from_dev(dout):
-        want = want + row
-    assert np.array_equal(got, want)
+    x = from_dev(dout)
+    pieces = [sum(x[i:i + 32], np.zeros(h, np.float32)) for i in (0, 32)]
+    assert np.array_equal(from_dev(_grad(torch, mt, ids, dout, False, False, 1.0, V))[0], pieces[0] + pieces[1])
+    got = _grad(torch, mt, ids[:32], dout[:32], False, False, 1.0, V)
+    assert np.array_equal(from_dev(got)[0], pieces[0])
 
 
 def test_ids_past_the_vocabulary_are_reported():
