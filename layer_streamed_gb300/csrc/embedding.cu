@@ -4,16 +4,17 @@
 // Backward: dtable[v] = scale * sum of dout[t] over the positions t with
 // id_t = v, in 32 bits and in a fixed order, so it is bitwise reproducible:
 //  1. one cluster of eight blocks sorts the positions by id (stable radix
-//     sort, so equal ids keep ascending positions) and lists the runs of
-//     equal ids, those longer than 8 in pieces; meanwhile the other blocks of
-//     the same launch clear the table's gradient;
-//  2. blocks take the pieces in turn, then warps the short runs, and add
-//     their rows in position order; the block that finishes a run's last
-//     piece adds the pieces in order.
-// The pieces keep a frequent id (or a constant batch) from leaving one block
-// with all the work. HBM traffic bounds the whole: dout read once, the table's
-// gradient written once (used rows twice). The sort (12 us for small batches)
-// hides behind the clearing of all but small tables.
+//     sort, so equal ids keep ascending positions) and marks the used rows;
+//     meanwhile other blocks of the launch clear the first rows of the table;
+//  2. warps stream over ranges of the sorted positions with the next rows
+//     always in flight, add runs of equal ids and write their rows; a run
+//     longer than 32 leaves a partial sum per range. Other warps clear the
+//     unused rows that are left;
+//  3. the partial sums of the long runs are added in order.
+// Cutting long runs at fixed positions keeps a frequent id (or a constant
+// batch) from leaving one warp with all the work. HBM traffic bounds the
+// whole: dout read once, the table's gradient written once; the sort (some 10
+// us for small batches) hides behind the first clearing.
 #include <algorithm>
 #include <type_traits>
 
@@ -63,16 +64,28 @@ __device__ __forceinline__ void storen(void* p, size_t i, const float4& v) {
   if (N == 4) store4<BF16>(p, i, v);
   else store1<BF16>(p, i, v.x);
 }
-// N partial sums that another block wrote during this launch.
-template <int N>
-__device__ __forceinline__ float4 load_part(const float* p, size_t i) {
-  return N == 4 ? __ldcg((const float4*)(p + i)) : make_float4(__ldcg(p + i), 0.f, 0.f, 0.f);
-}
 __device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 __device__ __forceinline__ float4 scaled(const float4& a, float s) {
   return make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
+}
+
+// p[i..] += v, one writer a value. fp32: a reduction in memory, which the
+// thread does not wait for (reading the old row first stalled the stream of
+// rows: 179 against 92 us for 8192 tokens of 128256 x 4096). bf16: added in
+// fp32 and rounded once.
+template <bool BF16, int N>
+__device__ __forceinline__ void accumulate(void* p, size_t i, const float4& v) {
+  if (BF16) {
+    storen<true, N>(p, i, add4(loadn<true, N>(p, i), v));
+  } else if (N == 4) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"((float*)p + i), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+  } else {
+    atomicAdd((float*)p + i, v.x);
+  }
 }
 
 // A thread takes N columns of four rows; blockDim.y rows side by side.
@@ -108,40 +121,28 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
 
 // ---------------------------------------------------------------------------
 // Sort: one cluster of kSortCtas blocks of 32 warps. Every warp owns a
-// contiguous part of the positions; a pass counts its digits per warp (equal
-// digits of 32 neighbouring keys are found with match.any), turns the counts
-// into offsets (digit, then block, then warp: a stable order) with one scan
-// over the cluster, and walks its part again to place its keys. The last step
-// counts and lists the heads of runs the same way.
+// contiguous part of the positions; a pass counts its digits per warp, turns
+// the counts into offsets (digit, then block, then warp: a stable order) with
+// one scan over the cluster, and walks its part again to place its keys (equal
+// digits of 32 neighbouring keys are found with a ballot a bit: match.any took
+// 78 us for 131072 positions, counting with it included).
 // ---------------------------------------------------------------------------
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 10;  // bits: 32 warps x 1024 counters in shared memory
-constexpr int kShort = 8;      // longest run summed by one warp
-constexpr int kPiece = 32;     // least length of a longer run's pieces
-constexpr int kClearBytes = 128 * 1024;  // cleared by one block
+constexpr int kClearBytes = 128 * 1024;     // cleared by one block of the sort's launch
+constexpr size_t kClearFirst = 64u << 20;   // and by all of them: what takes as long as the sort
 
 struct SortArgs {
   const int32_t* ids;
   int2 *a, *b;       // (key, position), ping-pong
-  int32_t* head;     // first sorted position of each run, then the end
-  int4* runs;        // of each run: sorted positions [x, y), id z, w: first position (short) or first partial sum
-  int4* pieces;      // sorted positions [x, y), run z, partial sum w (-1: the piece is the run)
-  int32_t* left;     // per run and column chunk: pieces not yet summed
-  int32_t* n;        // [0] pieces, [1] partial sums, [2] runs
-  void* clear;       // table gradient to clear (null: none)
+  uint8_t* used;     // [V] rows with a position (null: not wanted)
+  int32_t* ctl;      // counters of the later steps, zeroed here: [0] long runs, [1] clearing
+  void* clear;       // the part of the table's gradient to clear here
   size_t clear_bytes;
-  int T, V, passes, digit, chunks;
+  int T, V, passes, digit;
 };
-
-// Positions a piece of a run of n covers: about the square root of n, so that
-// summing a piece and adding up the pieces take equally long.
-__host__ __device__ inline int piece_len(int n) {
-  int l = kPiece;
-  while ((long long)l * l < n) l *= 2;
-  return l;
-}
 
 // One block's share of clearing: 16-byte stores, 2-byte ones at the ends.
 __device__ __forceinline__ void clear_share(void* base, size_t bytes, int block) {
@@ -194,7 +195,6 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the block's totals [bins]
   __shared__ uint32_t scratch[kSortWarps];
-  __shared__ uint32_t heads[kSortWarps + 1];  // run heads of each warp's part, of the block
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums wait for this launch's end themselves
   if (blockIdx.x >= kSortCtas) {
     clear_share(a.clear, a.clear_bytes, (int)blockIdx.x - kSortCtas);
@@ -205,7 +205,13 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   const uint32_t rank = cluster_rank(), warp = warp_id(), lane = lane_id(), below_mask = (1u << lane) - 1;
   const int tid = threadIdx.x;
   uint32_t* mine = cnt + warp * bins;
-  if (rank == 0 && tid == 0) a.n[0] = a.n[1] = 0;
+  if (rank == 0 && tid < 2) a.ctl[tid] = 0;
+  if (a.used) {  // [V] rounded up to whole 16-byte words
+    uint4* u = (uint4*)a.used;
+    for (int i = (int)rank * kSortThreads + tid; i < (a.V + 15) / 16; i += kSortCtas * kSortThreads)
+      u[i] = make_uint4(0, 0, 0, 0);
+    cluster_sync();
+  }
 
   // the warp's part: whole groups of 32 positions
   const int groups = (a.T + 31) / 32, all = kSortCtas * kSortWarps;
@@ -222,18 +228,17 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       if (src) return __ldcg(src + i);
       const int id = a.ids[i];
       if (id >= a.V) report_error(kErrBadArg);
-      return make_int2(id < 0 || id >= a.V ? a.V : id, i);  // ids outside the table sort last
+      const bool off = id < 0 || id >= a.V;  // ids outside the table sort last
+      if (!off && a.used) a.used[id] = 1;
+      return make_int2(off ? a.V : id, i);
     };
     int2 next = key_at(lo + (int)lane);
     for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
       const bool on = i + (int)lane < hi;
-      const uint32_t d = on ? ((uint32_t)next.x >> shift) & (bins - 1) : 0xffffffffu;
+      if (on) atomicAdd(&mine[((uint32_t)next.x >> shift) & (bins - 1)], 1u);
       next = key_at(i + 32 + (int)lane);
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      if (on && (peers & below_mask) == 0) mine[d] += __popc(peers);
-      __syncwarp();
     }
     next = key_at(lo + (int)lane);
     __syncthreads();
@@ -267,9 +272,16 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     for (int i = lo; i < hi; i += 32) {
       const bool on = i + (int)lane < hi;
       const int2 kv = next;
-      const uint32_t d = on ? ((uint32_t)kv.x >> shift) & (bins - 1) : 0xffffffffu;
+      const uint32_t d = ((uint32_t)kv.x >> shift) & (bins - 1);
       next = key_at(i + 32 + (int)lane);
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      uint32_t peers = __ballot_sync(0xffffffffu, on);  // lanes with the same digit
+#pragma unroll
+      for (int b = 0; b < kMaxDigit; ++b)
+        if (b < a.digit) {
+          const bool set = (d >> b) & 1;
+          const uint32_t m = __ballot_sync(0xffffffffu, set);
+          peers &= set ? m : ~m;
+        }
       const uint32_t below = __popc(peers & below_mask);
       uint32_t at = 0;
       if (on) at = mine[d] + below;
@@ -283,171 +295,216 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     cluster_sync();  // the sorted keys are visible to the cluster
   }
 
-  // heads of runs of equal ids: counted, then listed in order
-  const int2* s = (a.passes & 1) ? a.a : a.b;
-  auto is_head = [&](int i) { return i < hi && (i == 0 || __ldcg(s + i).x != __ldcg(s + i - 1).x); };
-  uint32_t h = 0;
-  for (int i = lo; i < hi; i += 32) h += __popc(__ballot_sync(0xffffffffu, is_head(i + (int)lane)));
-  if (lane == 0) heads[warp] = h;
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t x = heads[w];
-      heads[w] = sum;
-      sum += x;
-    }
-    heads[kSortWarps] = sum;
-  }
-  cluster_sync();
-  uint32_t at = heads[warp], runs = 0;
-  for (uint32_t r = 0; r < kSortCtas; ++r) {
-    const uint32_t x = peer_word(&heads[kSortWarps], r);
-    if (r < rank) at += x;
-    runs += x;
-  }
-  for (int i = lo; i < hi; i += 32) {
-    const bool here = is_head(i + (int)lane);
-    const uint32_t m = __ballot_sync(0xffffffffu, here);
-    if (here) __stcg(a.head + at + __popc(m & below_mask), i + (int)lane);
-    at += __popc(m);
-  }
-  if (rank == 0 && tid == 0) {
-    __stcg(a.head + runs, a.T);
-    a.n[2] = (int)runs;
-  }
-  cluster_sync();
-  for (int r = (int)rank * kSortThreads + tid; r < (int)runs; r += kSortCtas * kSortThreads) {
-    const int x = __ldcg(a.head + r), id = __ldcg(s + x).x;
-    const int y = id < a.V ? __ldcg(a.head + r + 1) : x, n = y - x;  // ids outside the table: an empty run
-    int w = 0;
-    if (n > kShort) {
-      const int l = piece_len(n), np = (n + l - 1) / l, p0 = atomicAdd(a.n, np);
-      // where a run's pieces and partial sums lie does not enter their values
-      w = np > 1 ? atomicAdd(a.n + 1, np) : -1;
-      for (int q = 0; q < np; ++q)
-        a.pieces[p0 + q] = make_int4(x + q * l, min(y, x + (q + 1) * l), r, np > 1 ? w + q : -1);
-      if (np > 1)
-        for (int c = 0; c < a.chunks; ++c) a.left[(size_t)r * a.chunks + c] = np;
-    } else if (n > 0) {
-      w = __ldcg(s + x).y;
-    }
-    a.runs[r] = make_int4(x, y, id, w);
-  }
 }
 
 // ---------------------------------------------------------------------------
-// Sums, 256 N columns at a time. A block adds a piece with a column group of
-// N a thread and eight rows in flight. A warp adds a short run with eight
-// column groups a thread, the next row requested under the sum of the last:
-// most runs have one or two rows, and only many bytes in flight a warp hide
-// the way from the run's entry to its rows and the table (one block a run,
-// one group a thread: 166 against 106 us for 8192 tokens of 128256 x 4096,
-// added to the table).
+// Sums. A warp takes a range of L sorted positions and 256 N columns (eight
+// groups of N a lane), two rows ahead of the sums. Runs of at most kShort
+// belong whole to the range of their first position; a longer one is cut at
+// the ranges' borders, each piece going to a partial sum: slot 2 j + 1 in the
+// range j where the run begins, slot 2 j in the later ones.
+// Measured for 8192 tokens of 128256 x 4096, added to the table: a block a
+// run 136 us, blocks for pieces and warps for short runs 92 us.
 // ---------------------------------------------------------------------------
-template <bool DB, int N>
-__device__ __forceinline__ float4 sum_rows(const int2* s, int i0, int i1, const void* dout, int h, int c) {
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = i0; i < i1; i += 8) {
-    float4 v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (i + q < i1) v[q] = loadn<DB, N>(dout, (size_t)s[i + q].y * h + c);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (i + q < i1) acc = add4(acc, v[q]);
-  }
-  return acc;
-}
+constexpr int kShort = 32;
+constexpr int kGroups = 8;
+
+struct SumArgs {
+  const int2* s;
+  const void* dout;
+  void* dtable;
+  float* part;
+  int2* longs;         // (range of the run's first position, id)
+  const uint8_t* used;
+  int32_t* ctl;
+  float scale;
+  int T, V, h, L, chunks, add;
+  int clear_row0, clear_rows;  // rows from clear_row0 on are cleared, clear_rows at a time (0: none)
+};
 
 template <bool DB, bool EB, int N>
-__global__ void __launch_bounds__(256, 2) embed_sum_kernel(const int2* s, const int4* runs, const int4* pieces,
-                                                           int32_t* left, const int32_t* n, float* part,
-                                                           const void* __restrict__ dout, float scale, void* dtable,
-                                                           int h, int add) {
-  __shared__ int last;
+__global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = (int)lane_id(), h = a.h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int chunk = blockIdx.y, n_pieces = n[0], n_runs = n[2];
-  const int c = (chunk * 256 + (int)threadIdx.x) * N;
-  auto finish = [&](int id, float4 acc) {
-    acc = scaled(acc, scale);
-    const size_t at = (size_t)id * h + c;
-    if (add) acc = add4(loadn<EB, N>(dtable, at), acc);
-    storen<EB, N>(dtable, at, acc);
-  };
-  for (int i = blockIdx.x; i < n_pieces; i += gridDim.x) {
-    const int4 d = pieces[i];
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < h) acc = sum_rows<DB, N>(s, d.x, d.y, dout, h, c);
-    if (d.w < 0) {
-      if (c < h) finish(runs[d.z].z, acc);
-      continue;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ranges = (a.T + a.L - 1) / a.L, jobs = ranges * a.chunks;
+  for (int job = blockIdx.x * 8 + (int)warp_id(); job < jobs; job += gridDim.x * 8) {
+    const int j = job / a.chunks, chunk = job - j * a.chunks, lo = j * a.L;
+    const int c0 = chunk * 32 * kGroups * N + lane * N;  // column groups c0 + 32 N k
+    // keys (and positions) from 32 before the range to 64 past its start; -1 outside the table's
+    auto at = [&](int i) {
+      int2 kv = i >= 0 && i < a.T ? a.s[i] : make_int2(-1, 0);
+      if (kv.x >= a.V) kv.x = -1;
+      return kv;
+    };
+    const int kp = at(lo - 32 + lane).x;
+    const int2 cur = at(lo + lane), fol = at(lo + 32 + lane);
+    const int e = min(a.L, __popc(__ballot_sync(kAll, cur.x >= 0)));
+    if (e == 0) continue;
+    // bit i: position i starts a run
+    int prev = __shfl_up_sync(kAll, cur.x, 1);
+    const int before = __shfl_sync(kAll, kp, 31);
+    if (lane == 0) prev = before;
+    uint32_t m = __ballot_sync(kAll, cur.x != prev);
+    uint64_t heads = m;
+    prev = __shfl_up_sync(kAll, fol.x, 1);
+    const int border = __shfl_sync(kAll, cur.x, 31);
+    if (lane == 0) prev = border;
+    m = __ballot_sync(kAll, fol.x != prev);
+    heads |= (uint64_t)m << 32;
+    auto next_head = [&](int i) {  // first head past i, 64 if none is in sight
+      const uint64_t r = i < 63 ? heads >> (i + 1) : 0ull;
+      return r ? i + __ffsll((long long)r) : 64;
+    };
+    int p0 = 0, pend;
+    bool head_piece = false, tail_piece = false;
+    if (!(heads & 1)) {  // a run that began earlier
+      const int first = __shfl_sync(kAll, cur.x, 0), fwd = next_head(0) < 64 ? next_head(0) : 64;
+      const int back = __clz(~__ballot_sync(kAll, kp == first));  // 32 where all of them are (clz of 0)
+      if (back + fwd > kShort) head_piece = true;
+      else p0 = fwd;
+      pend = head_piece ? min(fwd, e) : fwd;
+      if (fwd >= e && !head_piece) continue;
+    } else {
+      pend = 0;
     }
-    if (c < h) storen<false, N>(part, (size_t)d.w * h + c, acc);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicSub(&left[(size_t)d.z * gridDim.y + chunk], 1) == 1;
-    __syncthreads();
-    if (last && c < h) {  // every piece of the run is there: add them in order
-      __threadfence();
-      const int4 r = runs[d.z];
-      const int l = piece_len(r.y - r.x), k = (r.y - r.x + l - 1) / l;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < k; q += 8) {
-        float4 v[8];
+    const uint64_t mine = heads & ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((pend < 64 ? 1ull << pend : 0ull) - 1ull);
+    if (mine) {  // runs that begin here; the last one decides where the range's work ends
+      const int last = 63 - __clzll((long long)mine), n = next_head(last);
+      tail_piece = n - last > kShort;
+      pend = tail_piece ? e : n;
+    }
+    const int tail_from = tail_piece ? 63 - __clzll((long long)mine) : 64;
+    float4 acc[kGroups], v0[kGroups], v1[kGroups];
+    auto load = [&](int p, float4 (&v)[kGroups]) {
+      const int pos = __shfl_sync(kAll, p < 32 ? cur.y : fol.y, p & 31);
+      const size_t base = (size_t)pos * h + c0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (q + j < k) v[j] = load_part<N>(part, (size_t)(r.w + q + j) * h + c);
+      for (int k = 0; k < kGroups; ++k)
+        if (c0 + 32 * N * k < h) v[k] = loadn<DB, N>(a.dout, base + 32 * N * k);
+    };
+    bool fresh = true, in_head = head_piece;
+    auto step = [&](int p, const float4 (&v)[kGroups]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (q + j < k) acc = add4(acc, v[j]);
+      for (int k = 0; k < kGroups; ++k) acc[k] = fresh ? v[k] : add4(acc[k], v[k]);
+      fresh = p + 1 == pend || ((heads >> (p + 1)) & 1);
+      if (!fresh) return;
+      const bool tail = p >= tail_from;
+      if (in_head || tail) {
+        float* dst = a.part + (size_t)(2 * j + (in_head ? 0 : 1)) * h + c0;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k)
+          if (c0 + 32 * N * k < h) storen<false, N>(dst, 32 * N * k, acc[k]);
+      } else {
+        const int id = __shfl_sync(kAll, p < 32 ? cur.x : fol.x, p & 31);
+        const size_t to = (size_t)id * h + c0;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k)
+          if (c0 + 32 * N * k < h) {
+            const float4 o = scaled(acc[k], a.scale);
+            if (a.add) accumulate<EB, N>(a.dtable, to + 32 * N * k, o);
+            else storen<EB, N>(a.dtable, to + 32 * N * k, o);
+          }
       }
-      finish(r.z, acc);
+      in_head = false;
+    };
+    if (tail_piece && chunk == 0) {
+      const int id = __shfl_sync(kAll, cur.x, tail_from);
+      if (lane == 0) a.longs[atomicAdd(a.ctl, 1)] = make_int2(j, id);  // their order does not enter the sums
     }
-    __syncthreads();  // `last` is read before the next piece sets it
+    if (p0 < pend) load(p0, v0);
+    if (p0 + 1 < pend) load(p0 + 1, v1);
+    for (int p = p0; p < pend; p += 2) {
+      step(p, v0);
+      if (p + 2 < pend) load(p + 2, v0);
+      if (p + 1 < pend) {
+        step(p + 1, v1);
+        if (p + 3 < pend) load(p + 3, v1);
+      }
+    }
   }
 
-  // short runs
-  const int lane = (int)lane_id(), step = gridDim.x * 8;
-  const int c0 = chunk * 256 * N + lane * N;  // column groups c0 + 32 N k
-  auto row = [&](int pos, float4 (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c0 + 32 * N * k < h) v[k] = loadn<DB, N>(dout, (size_t)pos * h + c0 + 32 * N * k);
-  };
-  auto entry = [&](int i) { return i < n_runs ? runs[i] : make_int4(0, 0, 0, 0); };
-  int i = blockIdx.x * 8 + (int)warp_id();
-  int4 next = entry(i);
-  for (; i < n_runs; i += step) {
-    const int4 d = next;
-    next = entry(i + step);
-    const int rows = d.y - d.x;
-    if (rows == 0 || rows > kShort) continue;
-    float4 acc[8], v[8];
-    row(d.w, acc);
-    const int pos = lane < rows ? s[d.x + lane].y : 0;
-    if (rows > 1) row(__shfl_sync(0xffffffffu, pos, 1), v);
-    for (int q = 1; q < rows; ++q) {
-      const int p = __shfl_sync(0xffffffffu, pos, q + 1 < rows ? q + 1 : 0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = add4(acc[k], v[k]);
-      if (q + 1 < rows) row(p, v);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int cc = c0 + 32 * N * k;
-      if (cc < h) {
-        const size_t at = (size_t)d.z * h + cc;
-        acc[k] = scaled(acc[k], scale);
-        if (add) acc[k] = add4(loadn<EB, N>(dtable, at), acc[k]);
-        storen<EB, N>(dtable, at, acc[k]);
+  // what is left to clear, a few rows at a time
+  if (a.clear_rows == 0) return;
+  constexpr int esz = EB ? 2 : 4;
+  auto ticket = [&] { return lane == 0 ? atomicAdd(a.ctl + 1, 1) : 0; };
+  const int end = (a.V - a.clear_row0 + a.clear_rows - 1) / a.clear_rows;
+  int next = ticket();
+  while (true) {
+    const int k = __shfl_sync(kAll, next, 0);
+    if (k >= end) break;
+    next = ticket();  // on its way during the stores
+    const int v_lo = a.clear_row0 + k * a.clear_rows, v_hi = min(a.V, v_lo + a.clear_rows);
+    for (int v = v_lo; v < v_hi; ++v) {
+      if (a.used[v]) continue;
+      uint8_t* row = (uint8_t*)a.dtable + (size_t)v * h * esz;
+      if (N == 4) {
+        for (int c = lane; c < h / 4; c += 32) {
+          if (EB) ((uint2*)row)[c] = make_uint2(0, 0);
+          else ((uint4*)row)[c] = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        for (int c = lane; c < h; c += 32) store1<EB>(row, c, 0.f);
       }
     }
   }
+}
+
+// Long runs: their partial sums added in order, four groups of 256 threads
+// each a quarter of them, then the quarters in order.
+template <bool EB, int N>
+__global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a) {
+  __shared__ float4 quarter[4][256];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = (int)threadIdx.x >> 8, x = (int)threadIdx.x & 255, c = ((int)blockIdx.y * 256 + x) * N, h = a.h;
+  const int n = a.ctl[0];
+  for (int r = blockIdx.x; r < n; r += gridDim.x) {
+    const int j0 = a.longs[r].x, id = a.longs[r].y;
+    int k = 0;  // later ranges that the run reaches into
+    while (true) {
+      const int64_t i = (int64_t)(j0 + 1 + k + (int)threadIdx.x) * a.L;
+      const int more = __syncthreads_count(i < a.T && a.s[i].x == id);
+      k += more;
+      if (more < 1024) break;
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < h) {
+      const int lo = (int)((int64_t)k * g / 4), hi = (int)((int64_t)k * (g + 1) / 4);
+      if (g == 0) acc = loadn<false, N>(a.part, (size_t)(2 * j0 + 1) * h + c);
+      for (int q = lo; q < hi; q += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (q + i < hi) v[i] = loadn<false, N>(a.part, (size_t)(2 * (j0 + 1 + q + i)) * h + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (q + i < hi) acc = add4(acc, v[i]);
+      }
+    }
+    quarter[g][x] = acc;
+    __syncthreads();
+    if (g == 0 && c < h) {
+      acc = scaled(add4(add4(acc, quarter[1][x]), add4(quarter[2][x], quarter[3][x])), a.scale);
+      const size_t to = (size_t)id * h + c;
+      if (a.add) accumulate<EB, N>(a.dtable, to, acc);
+      else storen<EB, N>(a.dtable, to, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// Positions a range covers: 32 for many, fewer where that would leave warps
+// without work.
+int range_len(int T, int h) {
+  const int chunks = (h + 1023) / 1024;
+  int L = 32;
+  while (L > 4 && (int64_t)(T / L) * chunks < 2048) L /= 2;
+  return L;
 }
 
 struct EmbedWs {
-  size_t a, b, head, runs, pieces, left, n, part, total;
+  size_t a, b, used, ctl, longs, part, total;
 };
 EmbedWs embed_ws(int T, int V, int h) {
   EmbedWs o;
@@ -457,17 +514,13 @@ EmbedWs embed_ws(int T, int V, int h) {
     x += (bytes + 255) / 256 * 256;
     return r;
   };
-  const size_t max_pieces = (size_t)T / 8 + 1;  // runs over 8: one piece, or pieces of 32 or more
-  const size_t max_parts = (size_t)T / 16 + 1;  // runs over 32
-  const size_t max_runs = std::min((size_t)T, (size_t)V + 1);
+  const int L = range_len(T, h);
   o.a = take((size_t)T * 8);
   o.b = take((size_t)T * 8);
-  o.head = take((max_runs + 1) * 4);
-  o.runs = take(max_runs * 16);
-  o.pieces = take(max_pieces * 16);
-  o.left = take(max_runs * (size_t)((h + 255) / 256) * 4);
-  o.n = take(12);
-  o.part = take(max_parts * (size_t)h * 4);
+  o.used = take((size_t)V);
+  o.ctl = take(8);
+  o.longs = take(((size_t)T / kShort + 1) * 8);
+  o.part = take((size_t)2 * ((T + L - 1) / L) * h * 4);
   o.total = x;
   return o;
 }
@@ -509,21 +562,19 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   const EmbedWs o = embed_ws(T, V, h);
   uint8_t* w = (uint8_t*)work;
   const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
-  const int units = vec ? h / 4 : h;
+  const int units = vec ? h / 4 : h, esz = eb ? 2 : 4;
+  const size_t row = (size_t)h * esz;
   SortArgs a;
   a.ids = ids;
   a.a = (int2*)(w + o.a);
   a.b = (int2*)(w + o.b);
-  a.head = (int32_t*)(w + o.head);
-  a.runs = (int4*)(w + o.runs);
-  a.pieces = (int4*)(w + o.pieces);
-  a.left = (int32_t*)(w + o.left);
-  a.n = (int32_t*)(w + o.n);
-  a.clear = add ? nullptr : dtable;
-  a.clear_bytes = add ? 0 : (size_t)V * h * (eb ? 2 : 4);
+  a.ctl = (int32_t*)(w + o.ctl);
+  const int first = add ? 0 : (int)std::min<size_t>((size_t)V, kClearFirst / row + 1);  // rows cleared beside the sort
+  a.used = !add && first < V ? w + o.used : nullptr;
+  a.clear = dtable;
+  a.clear_bytes = first * row;
   a.T = T;
   a.V = V;
-  a.chunks = (units + 255) / 256;
   int bits = 1;
   while ((V >> bits) != 0) ++bits;  // keys 0..V
   a.passes = (bits + kMaxDigit - 1) / kMaxDigit;
@@ -532,36 +583,59 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ((kSortWarps + 1) << kMaxDigit) * 4) != cudaSuccess)
     return -1;
-  size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
-  clearers = (clearers + kSortCtas - 1) / kSortCtas * kSortCtas;
-  if (clearers > (1u << 30)) return -1;
-  embed_sort_kernel<<<(unsigned)(kSortCtas + clearers), kSortThreads, smem, st>>>(a);
+  const size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
+  const unsigned blocks = (unsigned)(kSortCtas + (clearers + kSortCtas - 1) / kSortCtas * kSortCtas);
+  embed_sort_kernel<<<blocks, kSortThreads, smem, st>>>(a);
 
-  // as many blocks as run at once, launched while the last ones of the sort end
-  const int most = std::max(T / 8 + 1, (std::min(T, V) + 7) / 8), fit = std::max(1, 152 * 2 / a.chunks);
+  SumArgs b;
+  b.s = (a.passes & 1) ? a.a : a.b;
+  b.dout = dout;
+  b.dtable = dtable;
+  b.part = (float*)(w + o.part);
+  b.longs = (int2*)(w + o.longs);
+  b.used = a.used;
+  b.ctl = a.ctl;
+  b.scale = scale;
+  b.T = T;
+  b.V = V;
+  b.h = h;
+  b.L = range_len(T, h);
+  b.chunks = (units + 32 * kGroups - 1) / (32 * kGroups);
+  b.add = add ? 1 : 0;
+  b.clear_row0 = first;
+  b.clear_rows = a.used ? (int)std::max<size_t>(1, 32768 / row) : 0;
+  // launched while the step before ends; they wait for it themselves
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(most, fit), (unsigned)a.chunks);
-  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute early[1];
   early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = early;
   cfg.numAttrs = 1;
+  const int64_t jobs = (int64_t)((T + b.L - 1) / b.L) * b.chunks;
+  if (jobs > (1 << 30)) return -1;
+  cfg.gridDim = dim3((unsigned)(a.used ? 304 : std::min<int64_t>(304, (jobs + 7) / 8)));
+  cfg.blockDim = dim3(256);
   cudaError_t e = cudaSuccess;
-  auto go = [&](auto k) {
-    e = cudaLaunchKernelEx(&cfg, k, (const int2*)((a.passes & 1) ? a.a : a.b), (const int4*)a.runs,
-                           (const int4*)a.pieces, a.left, (const int32_t*)a.n, (float*)(w + o.part), dout, scale,
-                           dtable, h, add ? 1 : 0);
-  };
-  auto pick = [&](auto n) {
+  auto go = [&](auto k) { e = cudaLaunchKernelEx(&cfg, k, b); };
+  auto sums = [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (db) eb ? go(embed_sum_kernel<true, true, N>) : go(embed_sum_kernel<true, false, N>);
     else eb ? go(embed_sum_kernel<false, true, N>) : go(embed_sum_kernel<false, false, N>);
   };
-  if (vec) pick(std::integral_constant<int, 4>());
-  else pick(std::integral_constant<int, 1>());
-  count_launches(2);
+  if (vec) sums(std::integral_constant<int, 4>());
+  else sums(std::integral_constant<int, 1>());
+  if (T > kShort && e == cudaSuccess) {
+    cfg.gridDim = dim3((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + 255) / 256));
+    cfg.blockDim = dim3(1024);
+    auto longs = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      eb ? go(embed_long_kernel<true, N>) : go(embed_long_kernel<false, N>);
+    };
+    if (vec) longs(std::integral_constant<int, 4>());
+    else longs(std::integral_constant<int, 1>());
+  }
+  count_launches(T > kShort ? 3 : 2);
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 

@@ -112,17 +112,21 @@ def test_sort_over_the_vocabulary(V):
 
 
 def test_sum_order_is_by_position():
-    """fp32 sums are those of adding the rows in ascending position, runs
-    longer than 32 in pieces of 32 whose sums are then added in order."""
+    """fp32 sums of up to 32 rows are those of adding them in ascending
+    position, wherever the rows lie among others."""
     torch, mt = need_gpu()
-    T, V, h = 40, 2, 4
+    T, V, h = 40, 4, 4
     dout = (torch.randn((T, h), device="cuda") * torch.exp(4 * torch.randn((T, 1), device="cuda")))
-    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
     x = from_dev(dout)
-    pieces = [sum(x[i:i + 32], np.zeros(h, np.float32)) for i in (0, 32)]
-    assert np.array_equal(from_dev(_grad(torch, mt, ids, dout, False, False, 1.0, V))[0], pieces[0] + pieces[1])
-    got = _grad(torch, mt, ids[:32], dout[:32], False, False, 1.0, V)
-    assert np.array_equal(from_dev(got)[0], pieces[0])
+    for first, n in ((0, 32), (5, 32), (3, 2), (30, 10)):
+        ids = np.full(T, 3, np.int32)
+        ids[:first] = 0
+        ids[first:first + n] = 2
+        got = from_dev(_grad(torch, mt, torch.from_numpy(ids).cuda(), dout, False, False, 1.0, V))
+        want = np.zeros(h, np.float32)
+        for row in x[first:first + n]:
+            want = want + row
+        assert np.array_equal(got[2], want)
 
 
 def test_ids_past_the_vocabulary_are_reported():
