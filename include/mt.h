@@ -52,6 +52,10 @@ typedef enum {
 
 typedef enum { MT_F32 = 0, MT_BF16 = 1, MT_FP8 = 2 } mt_dtype;
 
+/* Form of an activation checkpoint; the 8-bit ones are described at
+ * mt_op_ckpt8_pack. */
+typedef enum { MT_CKPT_F32 = 0, MT_CKPT_I8 = 1, MT_CKPT_E4M3 = 2 } mt_ckpt_format;
+
 /* Model and capacity description.
  * Shapes: hidden h, n_heads query heads and n_kv_heads key/value heads of
  * head_dim d (n_heads % n_kv_heads == 0; query head j reads KV head
@@ -83,6 +87,13 @@ typedef struct {
    * even on the device before they stream back: half the D2H bytes; the host
    * optimizer entry points take MT_F32 gradients only). */
   int32_t grad_dtype;
+  /* mt_ckpt_format of the residual checkpoints on the device: MT_CKPT_F32 (0,
+   * the default), or MT_CKPT_I8 / MT_CKPT_E4M3 (8 bits and a scale per 32
+   * channels, a quarter of the bytes). The loss, the head's gradients and
+   * those of the layers in the top block are the same bits as with fp32
+   * checkpoints; lower blocks are recomputed from the rounded residual, so
+   * their gradients carry its rounding and depend on K. */
+  int32_t ckpt_format;
 } mt_layer_cfg;
 
 typedef struct mt_ctx mt_ctx;
@@ -166,7 +177,7 @@ int mt_bind_host_params(mt_ctx* ctx, const void* host_params, mt_dtype dtype);
  *  loss_out       : host; Loss = mean over the B*S positions of
  *                   logsumexp(z_t) - z_t[label_t]
  * Synchronous: on return every gradient has landed. Results are bitwise
- * independent of K. */
+ * independent of K (with fp32 checkpoints; see ckpt_format). */
 int mt_forward_backward(mt_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B, int S, int K,
                         float* host_grad_out, float* loss_out);
 
@@ -502,7 +513,6 @@ int mt_op_moe_ffn_bwd(const void* m, const void* Wr, const void* Wgu, const void
  * (i8 has the finer steps near a block's maximum, e4m3 keeps 2^-4 relative
  * error for values far below it). A block with an infinity or a NaN gets
  * b = 255 and code 0 and stands for NaN throughout. */
-typedef enum { MT_CKPT_F32 = 0, MT_CKPT_I8 = 1, MT_CKPT_E4M3 = 2 } mt_ckpt_format;
 
 /* Pack x [T, n] (x_dtype MT_F32 or MT_BF16, row stride ldx elements) into
  * codes [T, ldc] bytes and scales [T, ceil(n/32)] bytes; unpack restores

@@ -65,7 +65,7 @@ class mt_layer_cfg(ctypes.Structure):
                 ("vocab", ctypes.c_int32), ("rope_theta", ctypes.c_float), ("norm_eps", ctypes.c_float),
                 ("max_batch", ctypes.c_int32), ("max_seq", ctypes.c_int32), ("max_K", ctypes.c_int32),
                 ("param_dtype", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
-                ("expert_ffn", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+                ("expert_ffn", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("ckpt_format", ctypes.c_int32)]
 
 
 class mt_stats(ctypes.Structure):
@@ -203,9 +203,10 @@ def _check(rc: int, ctx=None):
 # ---------------------------------------------------------------------------
 def make_cfg(n_layers, hidden, n_heads, n_kv_heads, head_dim, ffn_dim, vocab, rope_theta=1e4, norm_eps=1e-5,
              max_batch=1, max_seq=1, max_K=1, param_dtype=MT_F32, n_experts=0, top_k=0,
-             expert_ffn=0, grad_dtype=MT_F32) -> mt_layer_cfg:
+             expert_ffn=0, grad_dtype=MT_F32, ckpt_format=MT_CKPT_F32) -> mt_layer_cfg:
     return mt_layer_cfg(n_layers, hidden, n_heads, n_kv_heads, head_dim, ffn_dim, vocab, rope_theta, norm_eps,
-                        max_batch, max_seq, max_K, param_dtype, n_experts, top_k, expert_ffn, grad_dtype)
+                        max_batch, max_seq, max_K, param_dtype, n_experts, top_k, expert_ffn, grad_dtype,
+                        ckpt_format)
 
 
 def mt_packed_bytes(cfg: mt_layer_cfg, dtype: int) -> int:
@@ -394,10 +395,11 @@ class Session:
 
     def __init__(self, shape: ModelShape, max_batch: int, max_seq: int, max_K: int, param_dtype: int = MT_F32,
                  device_budget: int | None = None, device_arena: int | None = None, streams=None,
-                 grad_dtype: int = MT_F32):
+                 grad_dtype: int = MT_F32, ckpt_format: int = MT_CKPT_F32):
         self.cfg = make_cfg(shape.n_layers, shape.hidden, shape.n_heads, shape.n_kv_heads, shape.head_dim,
                             shape.ffn_dim, shape.vocab, shape.rope_theta, shape.norm_eps, max_batch, max_seq,
-                            max_K, param_dtype, shape.n_experts, shape.top_k, shape.expert_ffn, grad_dtype)
+                            max_K, param_dtype, shape.n_experts, shape.top_k, shape.expert_ffn, grad_dtype,
+                            ckpt_format)
         self.grad_dtype = grad_dtype
         self._gnp = np.float32 if grad_dtype == MT_F32 else np.uint16  # bf16 gradients as bit patterns
         self.shape = shape

@@ -314,6 +314,8 @@ bool cfg_valid(const mt_layer_cfg& c, std::string* why) {
     return fail("param_dtype must be MT_F32, MT_BF16 or MT_FP8");
   if (c.param_dtype == MT_FP8 && c.ffn_dim % 16) return fail("FP8 params need ffn_dim % 16 == 0");
   if (c.grad_dtype != MT_F32 && c.grad_dtype != MT_BF16) return fail("grad_dtype must be MT_F32 or MT_BF16");
+  if (c.ckpt_format != MT_CKPT_F32 && c.ckpt_format != MT_CKPT_I8 && c.ckpt_format != MT_CKPT_E4M3)
+    return fail("ckpt_format must be MT_CKPT_F32, MT_CKPT_I8 or MT_CKPT_E4M3");
   if (c.param_dtype == MT_BF16 && c.ffn_dim % 8) return fail("bf16 params need ffn_dim % 8 == 0");
   if (c.max_batch < 1 || c.max_seq < 1 || c.max_K < 1) return fail("max_batch, max_seq, max_K must be >= 1");
   if (!(c.rope_theta > 0.f) || !(c.norm_eps > 0.f)) return fail("rope_theta and norm_eps must be positive");
@@ -338,6 +340,8 @@ struct Plan {
   int head_rows, n_head_slices;
   // sizes
   size_t wbuf, wcast, gbuf, ckpt_one, act_layer, fixed_ws, dyn_max, total;
+  size_t ckpt_scales;  // 8-bit checkpoints: offset of the scales behind the codes
+  size_t norm_ws;      // floats of partial sums of the RMSNorm backward
   // activation layout inside one block-arena slot (byte offsets)
   size_t o_x, o_a, o_rstd1, o_qkv, o_o, o_lse, o_hmid, o_m, o_rstd2, o_gu, o_act;
   // mixture-of-experts slot: router logits, selection, weights, slot <-> row
@@ -409,7 +413,10 @@ bool make_plan(const mt_layer_cfg& c, Plan* P) {
   p.wcast = p.esz != 2 ? rup(std::max(layer_cast_bytes(p), (size_t)p.head_rows * p.h * 2), 4096) : 0;
   p.gbuf = rup(std::max({layer_grad_bytes, (size_t)p.head_rows * p.h * p.gesz, (size_t)p.h * p.gesz}), 4096);
   const size_t T = p.Tmax, h = p.h;
-  p.ckpt_one = rup(T * h * 4, 256);
+  p.ckpt_scales = rup(T * h, 256);
+  p.ckpt_one = c.ckpt_format == MT_CKPT_F32 ? rup(T * h * 4, 256) : p.ckpt_scales + rup(T * (h / 32), 256);
+  p.norm_ws = rmsnorm_bwd_partials((int)T, p.h);
+  if (c.ckpt_format != MT_CKPT_F32) p.norm_ws = std::max(p.norm_ws, rmsnorm_bwd_ckpt8_partials((int)T, p.h));
   size_t a = 0;
   auto take = [&](size_t bytes) {
     size_t r = a;
@@ -452,7 +459,7 @@ bool make_plan(const mt_layer_cfg& c, Plan* P) {
   ws(T * p.qd * 2);                                // do
   ws(T * p.qkv * 2);                               // dqkv
   ws(attention_bwd_workspace(c.max_batch, c.max_seq, p.nq) * 4);
-  ws(rmsnorm_bwd_partials((int)T, p.h) * 4);
+  ws(p.norm_ws * 4);
   ws(T * h * 2);                                   // xf bf16
   ws(T * 4);                                       // rstd_f
   ws(T * (size_t)p.head_rows * 4);                 // logits slice fp32
@@ -724,7 +731,7 @@ int carve(mt_ctx* ctx) {
   ctx->do_b = (uint16_t*)take(T * p.qd * 2);
   ctx->dqkv = (uint16_t*)take(T * p.qkv * 2);
   ctx->attn_ws = (float*)take(attention_bwd_workspace(ctx->cfg.max_batch, ctx->cfg.max_seq, p.nq) * 4);
-  ctx->norm_ws = (float*)take(rmsnorm_bwd_partials((int)T, p.h) * 4);
+  ctx->norm_ws = (float*)take(p.norm_ws * 4);
   ctx->xf_b = (uint16_t*)take(T * h * 2);
   ctx->rstd_f = (float*)take(T * 4);
   ctx->logits = (float*)take(T * (size_t)p.head_rows * 4);
@@ -845,6 +852,9 @@ ActSlot act_slot(mt_ctx* ctx, int K, int nb, int j) {
 }
 
 float* ckpt(mt_ctx* ctx, int b) { return (float*)(ctx->dyn + (size_t)b * ctx->P.ckpt_one); }
+// The same in 8 bits: codes [T, h], scales [T, h / 32].
+uint8_t* ckpt8_codes(mt_ctx* ctx, int b) { return ctx->dyn + (size_t)b * ctx->P.ckpt_one; }
+uint8_t* ckpt8_scales(mt_ctx* ctx, int b) { return ckpt8_codes(ctx, b) + ctx->P.ckpt_scales; }
 
 // Brackets one kernel launch with events when per-kernel tracing is on.
 struct OpTimer {
@@ -1183,10 +1193,15 @@ const uint16_t* bind_head(Step& st, int s, int slot, bool fresh, int* rows) {
   return ctx->wcast[slot];
 }
 
-// x_in / x_out of layer l (1-based) for checkpoint interval K.
+// x_in / x_out of layer l (1-based) for checkpoint interval K. With 8-bit
+// checkpoints a block's input lives in its first activation slot while the
+// block runs: the checkpoint is packed from it as the block's first layer
+// reads it, and unpacked into it before a recompute. The recompute's last
+// layer writes over it again (the next block's input); the backward of the
+// first layer reads the checkpoint itself.
 float* layer_input(Step& st, int l) {
   const int i = l - 1;  // index of the input residual h_{l-1}
-  if (i % st.K == 0) return ckpt(st.ctx, i / st.K);
+  if (i % st.K == 0 && st.ctx->cfg.ckpt_format == MT_CKPT_F32) return ckpt(st.ctx, i / st.K);
   return act_slot(st.ctx, st.K, st.nb, i % st.K).x;
 }
 float* layer_output(Step& st, int l) {
@@ -1242,7 +1257,16 @@ int moe_ffn_forward(Step& st, int l, const LayerView& w, const ActSlot& a, float
   return MT_OK;
 }
 
-int layer_forward(Step& st, int l, const LayerView& w) {
+// 8-bit checkpoint that layer l's input is kept in: its index, or -1 (fp32
+// checkpoints, a layer inside a block, or the top block, whose activations
+// stay until its backward).
+int ckpt8_of(const Step& st, int l) {
+  if (st.ctx->cfg.ckpt_format == MT_CKPT_F32 || (l - 1) % st.K) return -1;
+  const int b = (l - 1) / st.K;
+  return b == st.nb - 1 && st.ctx->fuse_top ? -1 : b;
+}
+
+int layer_forward(Step& st, int l, const LayerView& w, bool recompute) {
   mt_ctx* ctx = st.ctx;
   const Plan& p = ctx->P;
   const int T = st.T, h = p.h;
@@ -1250,6 +1274,14 @@ int layer_forward(Step& st, int l, const LayerView& w) {
   float* x = layer_input(st, l);
   float* y = layer_output(st, l);
   cudaStream_t s = ctx->s_comp;
+  const int b8 = ckpt8_of(st, l), fmt = ctx->cfg.ckpt_format;
+  // (packed beside the norm, not by its fused form, whose sums run in another
+  // order: the forward stays bitwise that of fp32 checkpoints for 27 us a
+  // block at T = 8192, h = 4096)
+  if (b8 >= 0 && recompute)
+    CKL(ckpt8_unpack(ckpt8_codes(ctx, b8), ckpt8_scales(ctx, b8), fmt, x, false, T, h, h, h, s));
+  else if (b8 >= 0)
+    CKL(ckpt8_pack(x, false, fmt, ckpt8_codes(ctx, b8), ckpt8_scales(ctx, b8), T, h, h, h, s));
   CKL(rmsnorm_fwd(x, w.w1, a.a, a.rstd1, T, h, ctx->cfg.norm_eps, s));
   // q|k|v projection with RoPE applied to the q and k heads in the epilogue
   CKR(gemm(ctx, GEMM_NT, EPI_BF16, a.a, w.wqkv, a.qkv, nullptr, T, p.qkv, h, h, h, p.qkv, st.S, p.qd + p.kd));
@@ -1444,7 +1476,12 @@ int layer_backward(Step& st, int l, const LayerView& w) {
   CKR(gemm(ctx, GEMM_TN, p.gepi, ctx->dqkv, a.a, GT(1), nullptr, p.qkv, h, T, p.qkv, h, h));
   CKR(gemm(ctx, GEMM_NN, EPI_F32, ctx->dqkv, w.wqkv, ctx->dm, nullptr, T, h, p.qkv, p.qkv, h, h));
   // RMSNorm 1 (+ residual): new dh
-  CKL(rmsnorm_bwd(x, w.w1, a.rstd1, ctx->dm, a.hmid, ctx->dh, ctx->dh_b, GGAIN(0), ctx->norm_ws, T, h, s));
+  const int b8 = ckpt8_of(st, l);
+  if (b8 >= 0)
+    CKL(rmsnorm_bwd_ckpt8(ckpt8_codes(ctx, b8), ckpt8_scales(ctx, b8), ctx->cfg.ckpt_format, w.w1, a.rstd1, ctx->dm,
+                          a.hmid, ctx->dh, ctx->dh_b, GGAIN(0), ctx->norm_ws, T, h, s));
+  else
+    CKL(rmsnorm_bwd(x, w.w1, a.rstd1, ctx->dm, a.hmid, ctx->dh, ctx->dh_b, GGAIN(0), ctx->norm_ws, T, h, s));
   CKR(gain_grad_out(0));
   CKR(grad_piece(st, g, l, 0, 3));
   if (st.train || st.async) {
@@ -1679,7 +1716,7 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
     // On the weight stream, queued right behind the first layer's copy (the
     // copy engine serves one H2D stream at a time, so issuing it from the
     // compute stream would put it behind the second layer's copy too).
-    void* land = p.esz == 4 ? (void*)ckpt(ctx, 0) : (void*)ctx->xf_b;
+    void* land = p.esz == 4 ? (void*)layer_input(st, 1) : (void*)ctx->xf_b;
     cudaEvent_t rows_in = next_event(ctx);
     {
       SegScope sg(ctx, 1, ctx->s_h2d, (double)T * row_bytes, -1);
@@ -1689,7 +1726,7 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
     CK(cudaStreamWaitEvent(s, rows_in, 0));
     if (p.esz != 4) {
       SegScope sg(ctx, 0, s, 0, -1);
-      CKL(cast_bf16_f32(ctx->xf_b, ckpt(ctx, 0), (size_t)T * h, s));
+      CKL(cast_bf16_f32(ctx->xf_b, layer_input(st, 1), (size_t)T * h, s));
     }
   }
   ctx->stats.h2d_bytes += (double)T * h * (p.esz == 4 ? 4 : 2);
@@ -1719,7 +1756,7 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
         LayerView w;
         CKR(bind_layer(st, l, slot, fresh, &w));
         if (it.index > 0) {
-          CKR(layer_forward(st, l, w));
+          CKR(layer_forward(st, l, w, (int)i >= L));
         } else {
           CKR(layer_backward(st, l, w));
         }

@@ -85,3 +85,16 @@ def test_embedding_refusals():
     _refused(lambda: mt.mt_op_embed_bwd(buf, buf, F, 1.0, buf, F, 0, al[off:], 2, 3, 4, 0))
     assert mt.mt_op_embed_bwd_workspace(0, 3, 4) == 0
     assert mt.mt_op_embed_bwd_workspace(2, 3, 4) > 0
+
+
+def test_checkpoint_format_in_the_configuration():
+    def budget(fmt):
+        return mt.mt_required_budget(mt.make_cfg(4, 64, 4, 4, 16, 172, 256, max_batch=2, max_seq=512, max_K=1,
+                                                 ckpt_format=fmt))
+    T, h, L = 1024, 64, 4
+    saved = budget(mt.MT_CKPT_F32) - budget(mt.MT_CKPT_I8)
+    assert budget(mt.MT_CKPT_I8) == budget(mt.MT_CKPT_E4M3)
+    # four checkpoints shrink from 4 bytes to 1 + 1/32 a value, against more partial sums of the norm backward
+    parts = mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, h) - mt.mt_op_rmsnorm_bwd_workspace(T, h)
+    assert saved == L * (4 * T * h - T * h - T * h // 32) - max(parts, 0) * 4
+    assert budget(3) == 0 and budget(-1) == 0
