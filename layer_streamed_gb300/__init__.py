@@ -513,11 +513,20 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_torch_c = None
+
+
 def _stream(stream) -> int | None:
-    if stream is None:  # the current stream's handle, without building a Stream object for every launch
+    """The given cudaStream_t, or torch's current stream (its handle, without
+    building a Stream object for every launch)."""
+    global _torch_c
+    if stream is not None:
+        return int(stream)
+    if _torch_c is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return int(stream)
+        torch.cuda.init()
+        _torch_c = torch._C
+    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
 
 
 def mt_op_gemm(mode, epi, A, B, C, addend, M, N, K, lda, ldb, ldc, stream=None):

@@ -742,13 +742,15 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
   }
 }
 
-// Block and grid of the 2D kernels: units of E columns along x, rows along y.
+// Block and grid of the 2D kernels: units of 8 columns along x, rows along y.
 struct Shape2 {
   dim3 grid, block;
 };
 Shape2 shape2(int T, int units, int rows) {
   int bx = 8;
   while (bx < units && bx < 256) bx *= 2;
+  // narrower blocks where the last one along a row would idle by a quarter or more
+  while (bx > 32 && (units + bx - 1) / bx * bx - units >= units / 4) bx /= 2;
   const int by = 256 / bx;
   const int gy = (T + by * rows - 1) / (by * rows);
   return {dim3((unsigned)((units + bx - 1) / bx), (unsigned)std::min(gy, 65535)), dim3((unsigned)bx, (unsigned)by)};
