@@ -300,7 +300,12 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     return;
   }
   if (tid == 0) sh_bad = 0, sh_nhot = 0, sh_n = 0;
-  if (C > 1) cluster_sync();  // every block's shared memory is set up before another one writes to it
+  // every block's shared memory is set up before another one writes to it
+  // (waited for just before the first such write)
+  if (C > 1) {
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
   float given = 0.f;  // the given token's logit
   if (rank == 0 && tid == 0) given = row.at(id);
   Run run{-kBig, 0ull, 0ull, false};
@@ -348,6 +353,7 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     if (rank == 0) *(volatile uint32_t*)p = v;
     else asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(p, 0)), "r"(v) : "memory");
   };
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();  // sh_bad, sh_nhot and sh_n are set up
   if (lane == 0) {
     Stat* slot = &sm.stat[rank * nw + (int)warp];
@@ -386,15 +392,13 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
         if (at < cap) sm.cand[at] = make_uint2(q, (uint32_t)i);
       }
     };
-    // warps take the vectors of a segment in turn, a lane each
-    const int per = G * kVecs;
-    for (int q = (int)warp; q < min(nhot, cap); q += nw) {
-      const int e = sm.hot[q], x = e & (NT - 1), c = e / NT * per;
-      for (int j = (int)lane; j < per; j += 32) {
-        const int v = v_lo + x + (c + j) * NT;
-        if (v >= v_hi) break;
+    const int per = G * kVecs, all = min(nhot, cap) * per;  // vectors of the listed segments
+    for (int q = tid; q < all; q += NT) {
+      const int e = sm.hot[q / per], v = v_lo + (e & (NT - 1)) + (e / NT * per + q % per) * NT;
+      if (v < v_hi) {
+        const uint4 u = *row.vec(v);
         float z[R::E];
-        spread<BF16>(*row.vec(v), z);
+        spread<BF16>(u, z);
 #pragma unroll
         for (int i = 0; i < R::E; ++i) offer(z[i], row.head + v * R::E + i);
       }
@@ -402,22 +406,23 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     const int end = row.end_index(tid, lo_end, hi_end, a.V);
     if (end >= 0) offer(row.at(end), end);
     __syncthreads();
-    const int n = max(sh_n, nhot);  // too many segments count as too many logits
+    const int found = sh_n, n = max(found, nhot);  // too many segments count as too many logits
     auto list = [&](int place, uint2 e) {
       put(&sm.list[rank * a.k + place].x, e.x);
       put(&sm.list[rank * a.k + place].y, e.y);
     };
     if (n <= cap) {
-      for (int i = tid; i < sh_n; i += NT) {
+      for (int i = tid; i < found; i += NT) {
         const uint2 e = sm.cand[i];
         int better = 0;
-        for (int j = 0; j < sh_n; ++j) {
+#pragma unroll 8
+        for (int j = 0; j < found; ++j) {
           const uint2 f = sm.cand[j];
           better += f.x > e.x || (f.x == e.x && f.y < e.y) ? 1 : 0;
         }
         if (better < a.k) list(better, e);
       }
-      if (tid >= sh_n && tid < a.k) list(tid, make_uint2(kKeyNone, 0xffffffffu));
+      if (tid >= found && tid < a.k) list(tid, make_uint2(kKeyNone, 0xffffffffu));
     } else {
       uint2 last = make_uint2(0xffffffffu, 0u);
       for (int r = 0; r < a.k; ++r) {
@@ -476,20 +481,28 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     if (C == 1) {
       if (tid < a.k) write(tid, sm.list[tid]);
     } else {
-      // rank every block's entries (empty ones follow the others in their
-      // order), four lanes an entry
-      for (int i0 = 0; i0 < n; i0 += NT / 4) {
-        const int i = i0 + tid / 4;
-        const uint2 e = i < n ? sm.list[i] : make_uint2(0u, 0u);
-        int better = 0;
-        for (int j = tid & 3; j < n; j += 4) {
+      // an entry's place: for every block's list, the number of its entries
+      // that come before (found by halving: the lists are sorted; empty
+      // entries follow the others, by block and place)
+      int* place = (int*)sm.cand;
+      for (int i = tid; i < n; i += NT) place[i] = 0;
+      __syncthreads();
+      for (int q = tid; q < n * C; q += NT) {
+        const int i = q / C, b = q % C;
+        const uint2 e = sm.list[i];
+        int lo = 0, hi = a.k;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2, j = b * a.k + mid;
           const uint2 g = sm.list[j];
-          better += g.x > e.x || (g.x == e.x && (g.y < e.y || (g.y == e.y && j < i))) ? 1 : 0;
+          const bool first = g.x > e.x || (g.x == e.x && (g.y < e.y || (g.y == e.y && j < i)));
+          if (first) lo = mid + 1;
+          else hi = mid;
         }
-        better += __shfl_xor_sync(0xffffffffu, better, 1);
-        better += __shfl_xor_sync(0xffffffffu, better, 2);
-        if (i < n && (tid & 3) == 0 && better < a.k) write(better, e);
+        if (lo) atomicAdd(&place[i], lo);
       }
+      __syncthreads();
+      for (int i = tid; i < n; i += NT)
+        if (place[i] < a.k) write(place[i], sm.list[i]);
     }
   }
 }
