@@ -617,7 +617,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int n) {
 constexpr int kSwRows = 2;
 
 template <int FMT, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_fwd_ckpt8_kernel(const uint16_t* __restrict__ gu,
+__global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t* __restrict__ gu,
                                                                uint16_t* __restrict__ act,
                                                                uint8_t* __restrict__ codes,
                                                                uint8_t* __restrict__ scales, int T, int F, int ld,

@@ -525,7 +525,7 @@ constexpr int kBwdVecs = 2;
 // share a block). A thread's logits are requested before the row's scalars,
 // whose loads they do not depend on.
 template <bool BF16, bool OBF16, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
   constexpr int W = kBwdVecs * (BF16 ? 8 : 4);  // logits a thread holds at a time
   const uint64_t cc = pair(a.c, a.c), ll = pair(kLog2e, kLog2e);
@@ -628,7 +628,7 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
   const int each = T >= 8 * sms ? 4 * chunk : chunk;
   int NT = 32, C = 1;
-  while (NT < 256 && NT * each < V) NT *= 2;
+  while (NT < 128 && NT * each < V) NT *= 2;
   while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
   if (C == kMaxCluster && T * C <= sms && V > C * NT * chunk) NT = kMaxThreads;
   // a block's vectors, at most, in chunks a thread; segments of G chunks
