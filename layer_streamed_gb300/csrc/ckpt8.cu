@@ -116,69 +116,178 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
-// 32-byte accesses (one instruction for eight fp32).
-__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+// ---------------------------------------------------------------------------
+// A unit is eight neighbouring columns, as WORDS 32-bit words: codes (2),
+// bf16 (4) or fp32 (8). VEC: every row's units start on their own boundary
+// and move in one access. Otherwise rows start anywhere: a unit is read as
+// the aligned blocks that cover it (BLK bytes each, within the tensor) and
+// shifted into place, and written as the aligned blocks that start in it,
+// completed by the next lane's words; only a row's first and last bytes go
+// one element at a time. The next lane has to hold the next unit, so a warp
+// then takes 28 units of its own and the first four (one scale block) of the
+// next warp's. (8192 x 14335 SwiGLU forward element by element: 680 us.)
+// ---------------------------------------------------------------------------
+template <int WORDS>
+constexpr int block_bytes() { return WORDS == 2 ? 8 : 16; }
+template <int WORDS>
+constexpr int elem_bytes() { return WORDS / 2; }
+constexpr int kOwnUnits = 28;
+
+__device__ __forceinline__ void load_block(const uint8_t* p, uint32_t (&w)[2]) {
+  const uint2 u = __ldcs((const uint2*)p);
+  w[0] = u.x, w[1] = u.y;
+}
+__device__ __forceinline__ void load_block(const uint8_t* p, uint32_t (&w)[4]) {
+  const uint4 u = __ldcs((const uint4*)p);
+  w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+}
+__device__ __forceinline__ void load_block(const uint8_t* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p));
 }
-__device__ __forceinline__ void store8f(float* p, const float (&v)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+__device__ __forceinline__ void store_block(uint8_t* p, const uint32_t (&w)[2]) { *(uint2*)p = make_uint2(w[0], w[1]); }
+__device__ __forceinline__ void store_block(uint8_t* p, const uint32_t (&w)[4]) {
+  *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_block(uint8_t* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-
-// Eight consecutive values of a row from column c; columns at or past n read
-// as 0. VEC: one 16-byte (bf16) or 32-byte (fp32) load.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_unit(const void* row, int c, int n, float (&v)[8]) {
-  if (VEC && c + 8 <= n) {
-    if (BF16) {
-      const uint4 u = __ldcs((const uint4*)((const uint16_t*)row + c));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// WORDS words from byte offset o (less than a block) of NX words.
+template <int WORDS, int NX>
+__device__ __forceinline__ void shift_words(const uint32_t (&x)[NX], uint32_t o, uint32_t (&w)[WORDS]) {
+  constexpr int BW = block_bytes<WORDS>() / 4;
+  uint32_t a[WORDS + 1 + (BW == 4 ? 2 : 0)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      load8f((const float*)row + c, v);
-    }
+  for (int i = 0; i < (int)(sizeof(a) / 4); ++i) a[i] = i + 1 < NX && (o & 4) ? x[i + 1] : i < NX ? x[i] : 0u;
+  if constexpr (BW == 4) {
+#pragma unroll
+    for (int i = 0; i <= WORDS; ++i) a[i] = (o & 8) ? a[i + 2] : a[i];
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) w[i] = __funnelshift_r(a[i], a[i + 1], (o & 3) * 8);
+}
+template <int WORDS>
+__device__ __forceinline__ void load_elem(const uint8_t* p, int i, uint32_t (&w)[WORDS]) {
+  if (WORDS == 2) w[(i >> 2) % WORDS] |= (uint32_t)p[i] << (8 * (i & 3));
+  else if (WORDS == 4) w[(i >> 1) % WORDS] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
+  else w[i % WORDS] = ((const uint32_t*)p)[i];
+}
+template <int WORDS>
+__device__ __forceinline__ void store_elem(uint8_t* p, int i, const uint32_t (&w)[WORDS]) {
+  if (WORDS == 2) p[i] = (uint8_t)(w[(i >> 2) % WORDS] >> (8 * (i & 3)));
+  else if (WORDS == 4) ((uint16_t*)p)[i] = (uint16_t)(w[(i >> 1) % WORDS] >> (16 * (i & 1)));
+  else ((uint32_t*)p)[i] = w[i % WORDS];
+}
+// Element i (ES bytes) of a block's words.
+template <int ES, int BW>
+__device__ __forceinline__ void store_elem_of(uint8_t* p, int i, const uint32_t (&y)[BW]) {
+  if (ES == 1) p[i] = (uint8_t)(y[(i >> 2) % BW] >> (8 * (i & 3)));
+  else if (ES == 2) ((uint16_t*)p)[i] = (uint16_t)(y[(i >> 1) % BW] >> (16 * (i & 1)));
+  else ((uint32_t*)p)[i] = y[i % BW];
+}
+// Unit u of a row of n columns, 0 past them. lo, hi: the tensor's bytes.
+template <int WORDS, bool VEC>
+__device__ __forceinline__ void load_cols(const void* row, int u, int n, const void* lo, const void* hi,
+                                          uint32_t (&w)[WORDS]) {
+  constexpr int BLK = block_bytes<WORDS>(), BW = BLK / 4, NB = WORDS / BW + 1;
+  const uint8_t* p = (const uint8_t*)row + (size_t)u * (WORDS * 4);
+  if (VEC && u * 8 + 8 <= n) {
+    load_block(p, w);
     return;
   }
+  if (!VEC && u * 8 + 8 <= n) {
+    const uint32_t o = (uint32_t)(uintptr_t)p & (BLK - 1);
+    const uint8_t* q = p - o;
+    if (q >= (const uint8_t*)lo && q + NB * BLK <= (const uint8_t*)hi) {
+      uint32_t x[NB * BW];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        uint32_t y[BW];
+        load_block(q + k * BLK, y);
+#pragma unroll
+        for (int i = 0; i < BW; ++i) x[k * BW + i] = y[i];
+      }
+      shift_words<WORDS>(x, o, w);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) w[i] = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    v[i] = c + i < n ? (BF16 ? bf2f(((const uint16_t*)row)[c + i]) : ((const float*)row)[c + i]) : 0.f;
+    if (u * 8 + i < n) load_elem(p, i, w);
 }
-// E code bytes (E / 4 words) to columns c.. of a row of codes.
-template <int E, bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, const uint32_t (&w)[E / 4]) {
-  if (VEC && c + E <= n) {
-    if (E == 8) *(uint2*)(row + c) = make_uint2(w[0], w[E / 4 - 1]);
-    else *(uint32_t*)(row + c) = w[0];
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (c + i < n) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-}
-template <int E, bool VEC>
-__device__ __forceinline__ void load_codes(const uint8_t* row, int c, int n, uint32_t (&w)[E / 4]) {
-  if (VEC && c + E <= n) {
-    if (E == 8) {
-      const uint2 u = __ldcs((const uint2*)(row + c));
-      w[0] = u.x;
-      w[E / 4 - 1] = u.y;
+// Unit u of a row of n columns. Without VEC the whole warp calls it; `own`:
+// this lane's unit is the warp's to write (and there is a row to write to).
+template <int WORDS, bool VEC>
+__device__ __forceinline__ void store_cols(void* row, int u, int n, const uint32_t (&w)[WORDS], bool own) {
+  constexpr int BLK = block_bytes<WORDS>(), BW = BLK / 4, ES = elem_bytes<WORDS>();
+  uint8_t* p = (uint8_t*)row + (size_t)u * (WORDS * 4);
+  if (VEC) {
+    if (!own) return;
+    if (u * 8 + 8 <= n) {
+      store_block(p, w);
     } else {
-      w[0] = __ldcs((const uint32_t*)(row + c));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (u * 8 + i < n) store_elem(p, i, w);
     }
     return;
   }
+  uint32_t x[WORDS + BW], v[WORDS];
 #pragma unroll
-  for (int k = 0; k < E / 4; ++k) w[k] = 0;
+  for (int i = 0; i < WORDS; ++i) x[i] = w[i];
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (c + i < n) w[i >> 2] |= (uint32_t)row[c + i] << (8 * (i & 3));
+  for (int i = 0; i < BW; ++i) x[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  const uint32_t o = (0u - (uint32_t)(uintptr_t)p) & (BLK - 1);  // bytes before the first boundary
+  shift_words<WORDS>(x, o, v);
+  if (!own) return;
+  const int first = u * 8 + (int)o / ES;  // column of the boundary
+#pragma unroll
+  for (int k = 0; k < WORDS / BW; ++k) {
+    const int c = first + k * (BLK / ES);
+    uint32_t y[BW];
+#pragma unroll
+    for (int i = 0; i < BW; ++i) y[i] = v[k * BW + i];
+    if (c + BLK / ES <= n) {
+      store_block(p + o + k * BLK, y);
+    } else if (c < n) {
+#pragma unroll
+      for (int i = 0; i < BLK / ES; ++i)
+        if (c + i < n) store_elem_of<ES>(p + o + k * BLK, i, y);
+    }
+  }
+  if (u == 0 && o) {
+#pragma unroll
+    for (int i = 0; i < BLK / ES; ++i)
+      if (i < (int)o / ES && i < n) store_elem(p, i, w);
+  }
+}
+// The unit of a thread that is the x-th along its row, and whether it is its own.
+template <bool VEC>
+__device__ __forceinline__ int unit_of(int x, bool& own) {
+  if (VEC) {
+    own = true;
+    return x;
+  }
+  own = (x & 31) < kOwnUnits;
+  return (x >> 5) * kOwnUnits + (x & 31);
+}
+template <int WORDS>
+__device__ __forceinline__ void to_floats(const uint32_t (&w)[WORDS], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (WORDS == 4) {
+      v[2 * i] = __uint_as_float(w[i % WORDS] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i % WORDS] & 0xffff0000u);
+    } else {
+      v[2 * i] = __uint_as_float(w[(2 * i) % WORDS]);
+      v[2 * i + 1] = __uint_as_float(w[(2 * i + 1) % WORDS]);
+    }
+  }
 }
 
 // Codes of one thread's E values under a block's scale byte.
@@ -201,9 +310,9 @@ __device__ __forceinline__ uint32_t block_byte(const float (&v)[E]) {
 }
 // Larger of each half's magnitudes over eight bf16 (magnitudes order like
 // whole numbers, two at a time).
-__device__ __forceinline__ uint32_t amax_bf16x8(const uint4& u) {
+__device__ __forceinline__ uint32_t amax_bf16x8(const uint32_t (&w)[4]) {
   constexpr uint32_t m = 0x7fff7fffu;
-  return __vmaxu2(__vimax3_u16x2(u.x & m, u.y & m, u.z & m), u.w & m);
+  return __vmaxu2(__vimax3_u16x2(w[0] & m, w[1] & m, w[2] & m), w[3] & m);
 }
 
 // ---------------------------------------------------------------------------
@@ -217,27 +326,29 @@ template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales, int T, int n, int ldx, int ldc,
                                                          int nb) {
-  constexpr int E = 8, G = 32 / E, esz = BF16 ? 2 : 4;
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
+  constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
+  bool own;
+  const int u = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
+  const void* hi = (const uint8_t*)x + ((size_t)(T - 1) * ldx + n) * esz;
   // the whole block leaves the loop together: shuffles need every lane
   for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kRows) {
-    float v[kRows][E];
+    uint32_t xw[kRows][W];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
-      load_unit<BF16, VEC>((const uint8_t*)x + (size_t)t * ldx * esz, c, t < T ? n : 0, v[r]);
+      load_cols<W, VEC>((const uint8_t*)x + (size_t)t * ldx * esz, u, t < T ? n : 0, x, hi, xw[r]);
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
-      uint32_t w[E / 4];
-      const uint32_t b = block_byte<FMT, E>(v[r]);
-      encode_unit<FMT, E>(b, v[r], w);
-      if (t < T) {
-        store_codes<E, VEC>(codes + (size_t)t * ldc, c, n, w);
-        if ((threadIdx.x & (G - 1)) == 0 && c < n) scales[(size_t)t * nb + c / 32] = (uint8_t)b;
-      }
+      float v[8];
+      to_floats(xw[r], v);
+      uint32_t w[2];
+      const uint32_t b = block_byte<FMT, 8>(v);
+      encode_unit<FMT, 8>(b, v, w);
+      store_cols<2, VEC>(codes + (size_t)t * ldc, u, n, w, own && t < T);
+      if (t < T && (u & 3) == 0 && u * 8 < n) scales[(size_t)t * nb + u / 4] = (uint8_t)b;
     }
   }
 }
@@ -246,52 +357,34 @@ template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ scales, void* __restrict__ x,
                                                            int T, int n, int ldc, int ldx, int nb) {
-  constexpr int E = 8;
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * E;
-  if (c >= n) return;
+  constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
+  bool own;
+  const int u = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
-  for (int t0 = blockIdx.y * blockDim.y + threadIdx.y; t0 < T; t0 += step * kRows) {
-    uint32_t w[kRows][E / 4];
+  const void* hi = codes + (size_t)(T - 1) * ldc + n;
+  for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kRows) {
+    uint32_t w[kRows][2];
     uint32_t b[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int t = t0 + r * step;
-      if (t < T) {
-        load_codes<E, VEC>(codes + (size_t)t * ldc, c, n, w[r]);
-        b[r] = scales[(size_t)t * nb + c / 32];
-      }
+      const int t = t0 + r * step + threadIdx.y;
+      load_cols<2, VEC>(codes + (size_t)t * ldc, u, t < T ? n : 0, codes, hi, w[r]);
+      b[r] = t < T && u * 8 < n ? scales[(size_t)t * nb + u / 4] : 0u;
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int t = t0 + r * step;
-      if (t >= T) break;
+      const int t = t0 + r * step + threadIdx.y;
       const float s = scale_up(b[r]);
-      float v[E];
-#pragma unroll
-      for (int k = 0; k < E / 4; ++k) {
-        const float4 f = decode4<FMT>(w[r][k], s);
-        v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
-      }
+      const float4 f = decode4<FMT>(w[r][0], s), g = decode4<FMT>(w[r][1], s);
+      uint32_t o[W];
       if (BF16) {
-        uint16_t* dst = (uint16_t*)x + (size_t)t * ldx + c;
-        if (VEC && c + E <= n) {
-          *(uint4*)dst = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[E - 4], v[E - 3]),
-                                    pack_bf2(v[E - 2], v[E - 1]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (c + i < n) dst[i] = f2bf(v[i]);
-        }
+        o[0] = pack_bf2(f.x, f.y), o[1] = pack_bf2(f.z, f.w), o[2] = pack_bf2(g.x, g.y), o[3] = pack_bf2(g.z, g.w);
       } else {
-        float* dst = (float*)x + (size_t)t * ldx + c;
-        if (VEC && c + E <= n) {
-          store8f(dst, v);
-        } else {
+        const float v[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
 #pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (c + i < n) dst[i] = v[i];
-        }
+        for (int i = 0; i < W; ++i) o[i] = __float_as_uint(v[i]);
       }
+      store_cols<W, VEC>((uint8_t*)x + (size_t)t * ldx * esz, u, n, o, own && t < T);
     }
   }
 }
@@ -316,7 +409,20 @@ __global__ void __launch_bounds__(NT)
   float v[V][8];
   float ss = 0.f;
 #pragma unroll
-  for (int k = 0; k < V; ++k) load_unit<false, VEC>(xr, (tid + k * NT) * 8, h, v[k]);
+  for (int k = 0; k < V; ++k) {
+    const int c = (tid + k * NT) * 8;
+    if (VEC && c + 8 <= h) {
+      uint32_t q[8];
+      load_block((const uint8_t*)(xr + c), q);
+      to_floats(q, v[k]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 f = c + i < h ? __ldcs((const float4*)(xr + c + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k][i] = f.x, v[k][i + 1] = f.y, v[k][i + 2] = f.z, v[k][i + 3] = f.w;
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -332,7 +438,12 @@ __global__ void __launch_bounds__(NT)
     const uint32_t b = block_byte<FMT, 8>(v[k]);
     encode_unit<FMT, 8>(b, v[k], q);
     if (c < h) {
-      store_codes<8, VEC>(codes + t * h, c, h, q);
+      if (VEC) {
+        *(uint2*)(codes + t * h + c) = make_uint2(q[0], q[1]);
+      } else {
+        *(uint32_t*)(codes + t * h + c) = q[0];
+        if (c + 4 < h) *(uint32_t*)(codes + t * h + c + 4) = q[1];
+      }
       if ((tid & 3) == 0) scales[t * nb + c / 32] = (uint8_t)b;
     }
   }
@@ -346,23 +457,18 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (tid + k * NT) * 8;
-    float g[8];
     uint32_t o[4];
-    if (VEC && c + 8 <= h) {
-      const float4 g0 = *(const float4*)(w + c), g1 = *(const float4*)(w + c + 4);
-      g[0] = g0.x, g[1] = g0.y, g[2] = g0.z, g[3] = g0.w, g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = c + i < h ? w[c + i] : 0.f;
+    for (int i = 0; i < 8; i += 4) {
+      const float4 g = c + i < h ? *(const float4*)(w + c + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      o[i / 2] = pack_bf2(v[k][i] * r * g.x, v[k][i + 1] * r * g.y);
+      o[i / 2 + 1] = pack_bf2(v[k][i + 2] * r * g.z, v[k][i + 3] * r * g.w);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = pack_bf2(v[k][2 * i] * r * g[2 * i], v[k][2 * i + 1] * r * g[2 * i + 1]);
-    if (VEC && c + 8 <= h) {
-      *(uint4*)(yr + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (VEC) {
+      if (c < h) *(uint4*)(yr + c) = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < h) yr[c + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+      if (c < h) *(uint2*)(yr + c) = make_uint2(o[0], o[1]);
+      if (c + 4 < h) *(uint2*)(yr + c + 4) = make_uint2(o[2], o[3]);
     }
   }
 }
@@ -375,10 +481,10 @@ __global__ void __launch_bounds__(NT)
 // in registers; a second kernel adds the parts in order.
 // ---------------------------------------------------------------------------
 // A block holds a row: V float4 a thread (two where h > 4096), w and the
-// sums of dw in registers. One thread requests whole rows of codes, dy and
-// resid stages - 1 rows ahead as bulk copies into shared memory, so loads
-// stay in flight across a row's reduction and hold no registers; rows that
-// are not whole 16-byte pieces (BULK false) are loaded by the threads.
+// sums of dw in registers. One thread requests whole rows of dy and resid
+// stages - 1 rows ahead as bulk copies into shared memory, so loads stay in
+// flight across a row's reduction and hold no registers; codes and scales,
+// whose rows need not be whole 16-byte pieces, are loaded one row ahead.
 // Measured at 8192 x 4096 (504 MB, floor 74 us) with the sum of the parts:
 // per-thread loads 103 us, per-thread cp.async staging 128 us (its 4-byte
 // copies and second reads cost more than the loads it hides), bulk copies
@@ -391,14 +497,14 @@ struct BwdShape {
   int threads, vecs, stages, parts;
 };
 // 1024 threads an SM where the rows allow, the shared memory shared out among
-// their blocks as stages of 9 h bytes (5 h without a residual).
+// their blocks as stages of 8 h bytes (4 h without a residual).
 BwdShape bwd_shape(int T, int h) {
   BwdShape s;
   const int n4 = h / 4;
   s.vecs = h > 4096 ? 2 : 1;
   s.threads = std::max(32, (n4 + s.vecs * 32 - 1) / (s.vecs * 32) * 32);
   const int an_sm = std::min(8, 1024 / s.threads);
-  s.stages = std::min(kBwdMaxStages, 222 * 1024 / an_sm / (9 * h));
+  s.stages = std::min(kBwdMaxStages, 222 * 1024 / an_sm / (8 * h));
   s.parts = std::min(T, 152 * an_sm);
   return s;
 }
@@ -410,37 +516,34 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <int FMT, int V, bool BULK>
+template <int FMT, int V>
 __global__ void __launch_bounds__(kBwdMaxThreads)
     rmsnorm_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                              const float* __restrict__ w, const float* __restrict__ rstd,
                              const float* __restrict__ dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
                              float* __restrict__ part, int T, int h, int nb, int stages) {
-  extern __shared__ __align__(128) uint8_t stage[];  // [stages]: dy, resid, codes of a row
+  extern __shared__ __align__(128) uint8_t stage[];  // [stages]: dy, resid of a row
   __shared__ float red[2][kBwdMaxThreads / 32];
   __shared__ uint64_t full[kBwdMaxStages];
   __shared__ int abort_flag;
   const int n4 = h >> 2, tid = threadIdx.x, NT = blockDim.x, nw = NT >> 5;
   const float inv_h = 1.f / (float)h;
-  const uint32_t row_bytes = (uint32_t)h * (resid ? 9u : 5u);
+  const uint32_t row_bytes = (uint32_t)h * (resid ? 8u : 4u);
   auto request = [&](int t, int s) {  // one thread
     if (t >= T) return;
     uint8_t* p = stage + (size_t)s * row_bytes;
     mbar_arrive_expect_tx(&full[s], row_bytes);
     bulk_load(p, dy + (size_t)t * h, 4u * h, &full[s]);
     if (resid) bulk_load(p + 4 * h, resid + (size_t)t * h, 4u * h, &full[s]);
-    bulk_load(p + row_bytes - h, codes + (size_t)t * h, (uint32_t)h, &full[s]);
   };
-  if (BULK) {
-    if (tid == 0) {
-      abort_flag = 0;
-      for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-      fence_barrier_init();
-    }
-    __syncthreads();
-    if (tid == 0)
-      for (int s = 0; s < stages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
   }
+  __syncthreads();
+  if (tid == 0)
+    for (int s = 0; s < stages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
   float4 acc[V], wv[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -448,8 +551,8 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     wv[j] = i < n4 ? ((const float4*)w)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // a row's scales and rstd, requested one row ahead
-  uint32_t b_next[V];
+  // a row's codes, scales and rstd, requested one row ahead
+  uint32_t q_next[V], b_next[V];
   float r_next = 0.f;
   auto small = [&](int t) {
     if (t < T) {
@@ -457,7 +560,10 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int i = tid + j * NT;
-        if (i < n4) b_next[j] = scales[(size_t)t * nb + i / 8];
+        if (i < n4) {
+          q_next[j] = __ldcs((const uint32_t*)(codes + (size_t)t * h) + i);
+          b_next[j] = scales[(size_t)t * nb + i / 8];
+        }
       }
     }
   };
@@ -467,32 +573,16 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
 #pragma unroll 1
   for (int t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
     const float r = r_next;
-    float4 g[V], e[V], x[V];
-    uint32_t q[V];
-    if (BULK) {
-      if (!mbar_wait(&full[st], phase, &abort_flag, kErrTimeoutTma)) break;
-    }
+    float4 g[V], x[V];
+    if (!mbar_wait(&full[st], phase, &abort_flag, kErrTimeoutTma)) break;
     const uint8_t* p = stage + (size_t)st * row_bytes;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = tid + j * NT;
-      if (i < n4) {
-        if (BULK) {
-          g[j] = ((const float4*)p)[i];
-          q[j] = ((const uint32_t*)(p + row_bytes - h))[i];
-        } else {
-          g[j] = __ldcs((const float4*)(dy + (size_t)t * h) + i);
-          q[j] = __ldcs((const uint32_t*)(codes + (size_t)t * h) + i);
-          if (resid) e[j] = ((const float4*)(resid + (size_t)t * h))[i];
-        }
-      }
-    }
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = tid + j * NT;
       if (i < n4) {
-        x[j] = decode4<FMT>(q[j], scale_up(b_next[j]));
+        g[j] = ((const float4*)p)[i];
+        x[j] = decode4<FMT>(q_next[j], scale_up(b_next[j]));
         dot += g[j].x * wv[j].x * x[j].x + g[j].y * wv[j].y * x[j].y + g[j].z * wv[j].z * x[j].z +
                g[j].w * wv[j].w * x[j].w;
       }
@@ -503,7 +593,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     // two buffers in turn: one barrier a row is enough; it also says that the
     // last row's stage has been read
     __syncthreads();
-    if (BULK && tid == 0) request(t + (stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
+    if (tid == 0) request(t + (stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
     dot = (tid & 31) < nw ? red[flip][tid & 31] : 0.f;
     const float mean = warp_sum(dot) * r * inv_h;
 #pragma unroll
@@ -514,11 +604,11 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
         float4 o = make_float4(r * (g[j].x * wv[j].x - xh.x * mean), r * (g[j].y * wv[j].y - xh.y * mean),
                                r * (g[j].z * wv[j].z - xh.z * mean), r * (g[j].w * wv[j].w - xh.w * mean));
         if (resid) {
-          if (BULK) e[j] = ((const float4*)(p + 4 * h))[i];
-          o.x += e[j].x;
-          o.y += e[j].y;
-          o.z += e[j].z;
-          o.w += e[j].w;
+          const float4 e = ((const float4*)(p + 4 * h))[i];
+          o.x += e.x;
+          o.y += e.y;
+          o.z += e.z;
+          o.w += e.w;
         }
         ((float4*)(dx + (size_t)t * h))[i] = o;
         if (dxb) ((uint2*)(dxb + (size_t)t * h))[i] = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
@@ -534,7 +624,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (BULK && *(volatile int*)&abort_flag) {  // a wait ran out: give the copies in flight time to land
+  if (*(volatile int*)&abort_flag) {  // a wait ran out: give the copies in flight time to land
     for (int k = 0; k < stages - 1; ++k) {
       for (int spin = 0; spin < (1 << 20) && !mbar_try_wait(smem_u32(&full[st]), phase); ++spin) {
       }
@@ -596,43 +686,27 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
   unpair(v, a, b);
   return pack_bf2(a, b);
 }
-__device__ __forceinline__ void spread8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-// Eight bf16 from column c; columns at or past n read as 0.
-template <bool VEC>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int n) {
-  if (VEC && c + 8 <= n) return __ldcs((const uint4*)(row + c));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < n) w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 constexpr int kSwRows = 2;
 
 template <int FMT, bool VEC>
 __global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t* __restrict__ gu,
-                                                               uint16_t* __restrict__ act,
-                                                               uint8_t* __restrict__ codes,
-                                                               uint8_t* __restrict__ scales, int T, int F, int ld,
-                                                               int nb) {
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+                                                                  uint16_t* __restrict__ act,
+                                                                  uint8_t* __restrict__ codes,
+                                                                  uint8_t* __restrict__ scales, int T, int F, int ld,
+                                                                  int nb) {
+  bool own;
+  const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
+  const void* hi = gu + (2 * (size_t)T - 1) * ld + F;
   // the whole block leaves the loop together: shuffles need every lane
   for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kSwRows) {
-    uint4 gq[kSwRows], uq[kSwRows];
+    uint32_t gq[kSwRows][4], uq[kSwRows][4];
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
       const uint16_t* row = gu + (size_t)t * 2 * ld;
-      gq[r] = load8<VEC>(row, c, t < T ? F : 0);
-      uq[r] = load8<VEC>(row + ld, c, t < T ? F : 0);
+      load_cols<4, VEC>(row, x, t < T ? F : 0, gu, hi, gq[r]);
+      load_cols<4, VEC>(row + ld, x, t < T ? F : 0, gu, hi, uq[r]);
     }
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
@@ -643,35 +717,26 @@ __global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t
       m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
       float g[8], u[8];
-      spread8(gq[r], g);
-      spread8(uq[r], u);
-      uint32_t wg[2], wu[2];
+      to_floats(gq[r], g);
+      to_floats(uq[r], u);
+      uint32_t wg[2], wu[2], a[4];
       const uint32_t bg = scale_byte<FMT, 7>(m & 0xffffu), bu = scale_byte<FMT, 7>(m >> 16);
       encode_unit<FMT, 8>(bg, g, wg);
       encode_unit<FMT, 8>(bu, u, wu);
-      if (t < T) {
-        uint32_t a[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t g2 = pair(g[2 * i], g[2 * i + 1]), u2 = pair(u[2 * i], u[2 * i + 1]);
-          a[i] = pack_pair(mul2(mul2(g2, sigmoid2(g2)), u2));
-        }
-        uint8_t* crow = codes + (size_t)t * 2 * ld;
-        uint16_t* arow = act + (size_t)t * ld;
-        // columns F..ld-1 are padding: codes and act are 0 there (the loads gave 0)
-        store_codes<8, VEC>(crow, c, ld, wg);
-        store_codes<8, VEC>(crow + ld, c, ld, wu);
-        if (VEC && c + 8 <= ld) {
-          *(uint4*)(arow + c) = make_uint4(a[0], a[1], a[2], a[3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < ld) arow[c + i] = (uint16_t)(a[i >> 1] >> (16 * (i & 1)));
-        }
-        if ((threadIdx.x & 3) == 0 && c < F) {
-          scales[(size_t)t * 2 * nb + c / 32] = (uint8_t)bg;
-          scales[(size_t)t * 2 * nb + nb + c / 32] = (uint8_t)bu;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t g2 = pair(g[2 * i], g[2 * i + 1]), u2 = pair(u[2 * i], u[2 * i + 1]);
+        a[i] = pack_pair(mul2(mul2(g2, sigmoid2(g2)), u2));
+      }
+      const bool write = own && t < T;
+      uint8_t* crow = codes + (size_t)t * 2 * ld;
+      // columns F..ld-1 are padding: codes and act are 0 there (the loads gave 0)
+      store_cols<2, VEC>(crow, x, ld, wg, write);
+      store_cols<2, VEC>(crow + ld, x, ld, wu, write);
+      store_cols<4, VEC>(act + (size_t)t * ld, x, ld, a, write);
+      if (t < T && (x & 3) == 0 && x * 8 < F) {
+        scales[(size_t)t * 2 * nb + x / 4] = (uint8_t)bg;
+        scales[(size_t)t * 2 * nb + nb + x / 4] = (uint8_t)bu;
       }
     }
   }
@@ -684,32 +749,29 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
                                                                const uint16_t* __restrict__ dact,
                                                                uint16_t* __restrict__ dgu, int T, int F, int ld,
                                                                int nb) {
-  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
-  if (c >= ld) return;
+  bool own;
+  const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
-  for (int t0 = blockIdx.y * blockDim.y + threadIdx.y; t0 < T; t0 += step * kSwRows) {
-    uint32_t wg[kSwRows][2], wu[kSwRows][2], bg[kSwRows], bu[kSwRows];
-    uint4 dq[kSwRows];
+  const void *chi = codes + (2 * (size_t)T - 1) * ld + F, *dhi = dact + (size_t)(T - 1) * ld + F;
+  for (int t0 = blockIdx.y * blockDim.y; t0 < T; t0 += step * kSwRows) {
+    uint32_t wg[kSwRows][2], wu[kSwRows][2], bg[kSwRows], bu[kSwRows], dq[kSwRows][4];
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
-      const int t = t0 + r * step;
-      if (t < T) {
-        const uint8_t* crow = codes + (size_t)t * 2 * ld;
-        load_codes<8, VEC>(crow, c, F, wg[r]);
-        load_codes<8, VEC>(crow + ld, c, F, wu[r]);
-        dq[r] = load8<VEC>(dact + (size_t)t * ld, c, F);
-        // a unit that lies in the padding has no block of its own
-        bg[r] = c < F ? scales[(size_t)t * 2 * nb + c / 32] : 0u;
-        bu[r] = c < F ? scales[(size_t)t * 2 * nb + nb + c / 32] : 0u;
-      }
+      const int t = t0 + r * step + threadIdx.y, n = t < T ? F : 0;
+      const uint8_t* crow = codes + (size_t)t * 2 * ld;
+      load_cols<2, VEC>(crow, x, n, codes, chi, wg[r]);
+      load_cols<2, VEC>(crow + ld, x, n, codes, chi, wu[r]);
+      load_cols<4, VEC>(dact + (size_t)t * ld, x, n, dact, dhi, dq[r]);
+      // a unit that lies in the padding has no block of its own
+      bg[r] = x * 8 < n ? scales[(size_t)t * 2 * nb + x / 4] : 0u;
+      bu[r] = x * 8 < n ? scales[(size_t)t * 2 * nb + nb + x / 4] : 0u;
     }
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
-      const int t = t0 + r * step;
-      if (t >= T) break;
+      const int t = t0 + r * step + threadIdx.y;
       const float sg = scale_up(bg[r]), su = scale_up(bu[r]);
       float d[8];
-      spread8(dq[r], d);
+      to_floats(dq[r], d);
       uint32_t og[4], ou[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -726,18 +788,19 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
           ou[2 * k + i] = pack_pair(du);
         }
       }
-      uint16_t* row = dgu + (size_t)t * 2 * ld;
-      if (VEC && c + 8 <= F) {
-        *(uint4*)(row + c) = make_uint4(og[0], og[1], og[2], og[3]);
-        *(uint4*)(row + ld + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-      } else {
+      if (x * 8 + 8 > F) {  // padding columns carry no gradient (a NaN block reaches into them)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (c + i < ld) {  // padding columns carry no gradient
-            row[c + i] = c + i < F ? (uint16_t)(og[i >> 1] >> (16 * (i & 1))) : (uint16_t)0;
-            row[ld + c + i] = c + i < F ? (uint16_t)(ou[i >> 1] >> (16 * (i & 1))) : (uint16_t)0;
+          if (x * 8 + i >= F) {
+            const uint32_t keep = (i & 1) ? 0x0000ffffu : 0xffff0000u;
+            og[i >> 1] &= keep;
+            ou[i >> 1] &= keep;
           }
       }
+      const bool write = own && t < T;
+      uint16_t* row = dgu + (size_t)t * 2 * ld;
+      store_cols<4, VEC>(row, x, ld, og, write);
+      store_cols<4, VEC>(row + ld, x, ld, ou, write);
     }
   }
 }
@@ -746,8 +809,9 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
 struct Shape2 {
   dim3 grid, block;
 };
-Shape2 shape2(int T, int units, int rows) {
-  int bx = 8;
+Shape2 shape2(int T, int units, int rows, bool vec) {
+  if (!vec) units = (units + kOwnUnits - 1) / kOwnUnits * 32;  // threads along a row
+  int bx = vec ? 8 : 32;
   while (bx < units && bx < 256) bx *= 2;
   // narrower blocks where the last one along a row would idle by a quarter or more
   while (bx > 32 && (units + bx - 1) / bx * bx - units >= units / 4) bx /= 2;
@@ -772,9 +836,9 @@ int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scale
                cudaStream_t st) {
   if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
   const int nb = blocks32(n);
-  const Shape2 s = shape2(T, (n + 7) / 8, kRows);
   // whole loads and stores of eight values where every row starts on their boundary
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
+  const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(x, codes, scales, T, n, ldx, ldc, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
@@ -790,8 +854,8 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
                  int ldx, cudaStream_t st) {
   if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
   const int nb = blocks32(n);
-  const Shape2 s = shape2(T, (n + 7) / 8, kRows);
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
+  const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, x, T, n, ldc, ldx, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
@@ -809,7 +873,7 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
       !al(y, 8) || !al(codes, 4))
     return -1;
   const int units = (h + 7) / 8, nb = blocks32(h);
-  // whole units where every row starts on a 32-byte boundary
+  // whole units where every row starts on a 32-byte boundary, else their halves
   const bool vec = h % 8 == 0 && al(x, 32) && al(y, 16) && al(codes, 8);
   auto go = [&](auto k, int threads) { k<<<T, threads, 0, st>>>(x, w, y, rstd, codes, scales, h, nb, eps); };
   auto pick = [&](auto f, auto v) {
@@ -836,10 +900,9 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
     return -1;
   const int nb = blocks32(h);
   const BwdShape shape = bwd_shape(T, h);
-  const bool bulk = h % 16 == 0 && al(codes, 16);  // every row of codes starts and ends on 16 bytes
   bool ok = true;
-  auto go = [&](auto k, bool staged) {
-    const int smem = staged ? shape.stages * h * (resid ? 9 : 5) : 0;
+  auto go = [&](auto k) {
+    const int smem = shape.stages * h * (resid ? 8 : 4);
     if (smem > 48 * 1024)
       ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) == cudaSuccess;
     if (ok)
@@ -848,8 +911,8 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   };
   auto pick = [&](auto f) {
     constexpr int F = decltype(f)::value;
-    if (shape.vecs == 1) bulk ? go(rmsnorm_bwd_ckpt8_kernel<F, 1, true>, true) : go(rmsnorm_bwd_ckpt8_kernel<F, 1, false>, false);
-    else bulk ? go(rmsnorm_bwd_ckpt8_kernel<F, 2, true>, true) : go(rmsnorm_bwd_ckpt8_kernel<F, 2, false>, false);
+    if (shape.vecs == 1) go(rmsnorm_bwd_ckpt8_kernel<F, 1>);
+    else go(rmsnorm_bwd_ckpt8_kernel<F, 2>);
   };
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
@@ -870,8 +933,8 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
 int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t* scales, int fmt, int T, int F,
                      int ld, cudaStream_t st) {
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return -1;
-  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows);
   const bool vec = ld % 8 == 0 && al(gu, 16) && al(act, 16) && al(codes, 8);
+  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(gu, act, codes, scales, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_fwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, false>);
@@ -881,8 +944,8 @@ int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t*
 int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const uint16_t* dact, uint16_t* dgu,
                      int T, int F, int ld, cudaStream_t st) {
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return -1;
-  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows);
   const bool vec = ld % 8 == 0 && al(dact, 16) && al(dgu, 16) && al(codes, 8);
+  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
   auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_bwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, false>);

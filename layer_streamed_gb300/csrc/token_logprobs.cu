@@ -523,16 +523,20 @@ constexpr int kBwdVecs = 2;
 
 // Blocks of blockDim.x threads along a row by blockDim.y rows (short rows
 // share a block). A thread's logits are requested before the row's scalars,
-// whose loads they do not depend on.
+// whose loads they do not depend on. VEC: logits and gradient come to a
+// 16-byte boundary at the same columns of a row; a row's units then start at
+// its first such column, and the first threads take the columns before it.
 template <bool BF16, bool OBF16, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
   constexpr int W = kBwdVecs * (BF16 ? 8 : 4);  // logits a thread holds at a time
   const uint64_t cc = pair(a.c, a.c), ll = pair(kLog2e, kLog2e);
-  const int j = (int)(blockIdx.x * blockDim.x + threadIdx.x) * W;
-  if (j >= a.V) return;
-  const bool whole = VEC && j + W <= a.V;
+  const int unit = (int)(blockIdx.x * blockDim.x + threadIdx.x);
   for (int t = blockIdx.y * blockDim.y + threadIdx.y; t < a.T; t += gridDim.y * blockDim.y) {
+    const int head = VEC ? (int)((8 - ((size_t)t * a.ld & 7)) & 7) : 0;  // a unit of 8 starts on every boundary
+    const int j = unit * W + head - (head ? W : 0);  // unit 0 holds the columns before the boundary
+    if (j >= a.V) continue;
+    const bool whole = VEC && j >= 0 && j + W <= a.V;
     const uint8_t* zr = (const uint8_t*)a.z + (size_t)t * a.ld * esz;
     uint8_t* dr = (uint8_t*)a.dz + (size_t)t * a.ldd * (OBF16 ? 2 : 4);
     uint4 u[kBwdVecs];
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdA
       } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-          z[i] = j + i < a.V ? (BF16 ? bf2f(((const uint16_t*)zr)[j + i]) : ((const float*)zr)[j + i]) : 0.f;
+          z[i] = j + i >= 0 && j + i < a.V ? (BF16 ? bf2f(((const uint16_t*)zr)[j + i]) : ((const float*)zr)[j + i]) : 0.f;
       }
       if (!BF16 || !whole) {
 #pragma unroll
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdA
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i)
-        if (j + i < a.V) {
+        if (j + i >= 0 && j + i < a.V) {
           if (OBF16) ((uint16_t*)dr)[j + i] = f2bf(g[i]);
           else ((float*)dr)[j + i] = g[i];
         }
@@ -672,8 +676,9 @@ int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, co
       ((uintptr_t)z & (bf16 ? 1 : 3)) || ((uintptr_t)dz & (dz_bf16 ? 1 : 3)))
     return -1;
   BwdArgs a{z, ids, lse, ent, g_logp, g_ent, dz, T, V, ld, ldd, c};
-  const bool vec = al16(z) && al16(dz) && ld % (bf16 ? 8 : 4) == 0 && ldd % (dz_bf16 ? 8 : 4) == 0;
-  const int W = kBwdVecs * (bf16 ? 8 : 4), units = (V + W - 1) / W;
+  // every eighth element of both on a 16-byte boundary at the same columns
+  const bool vec = al16(z) && al16(dz) && (ld - ldd) % 8 == 0;
+  const int W = kBwdVecs * (bf16 ? 8 : 4), units = (V + W - 1) / W + (vec && ld % 8 ? 1 : 0);
   int bx = 8;
   while (bx < units && bx < kBwdThreads) bx *= 2;
   const int by = kBwdThreads / bx;
