@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
 }
 
 // ---------------------------------------------------------------------------
-// Sort: one cluster of kSortCtas blocks of 32 warps. Every warp owns a
+// Sort: one cluster of eight blocks of 32 warps (one block for few positions,
+// where the barriers between blocks cost more than the work: 1266 positions
+// 7.5 us in eight blocks). Every warp owns a
 // contiguous part of the positions; a pass counts its digits per warp, turns
 // the counts into offsets (digit, then block, then warp: a stable order) with
 // one scan over the cluster, and walks its part again to place its keys (equal
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
 // 78 us for 131072 positions, counting with it included).
 // ---------------------------------------------------------------------------
 constexpr int kSortCtas = 8;
+constexpr int kSortOne = 4096;  // positions that one block sorts alone
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 10;  // bits: 32 warps x 1024 counters in shared memory
@@ -141,7 +144,7 @@ struct SortArgs {
   int32_t* ctl;      // counters of the later steps, zeroed here: [0] long runs, [1] clearing
   void* clear;       // the part of the table's gradient to clear here
   size_t clear_bytes;
-  int T, V, passes, digit;
+  int T, V, passes, digit, ctas;
 };
 
 // One block's share of clearing: 16-byte stores, 2-byte ones at the ends.
@@ -192,29 +195,34 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
   return x;
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the block's totals [bins]
   __shared__ uint32_t scratch[kSortWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums wait for this launch's end themselves
-  if (blockIdx.x >= kSortCtas) {
-    clear_share(a.clear, a.clear_bytes, (int)blockIdx.x - kSortCtas);
+  const int ctas = a.ctas;
+  if ((int)blockIdx.x >= ctas) {
+    clear_share(a.clear, a.clear_bytes, (int)blockIdx.x - ctas);
     return;
   }
   const int bins = 1 << a.digit;
   uint32_t* tot = cnt + kSortWarps * bins;
-  const uint32_t rank = cluster_rank(), warp = warp_id(), lane = lane_id(), below_mask = (1u << lane) - 1;
+  const uint32_t rank = ctas > 1 ? cluster_rank() : 0u, warp = warp_id(), lane = lane_id(), below_mask = (1u << lane) - 1;
   const int tid = threadIdx.x;
   uint32_t* mine = cnt + warp * bins;
   if (rank == 0 && tid < 2) a.ctl[tid] = 0;
+  auto sync_all = [&] {  // what the cluster's blocks have written is visible to all of them
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+  };
   if (a.used) {  // [V] rounded up to whole 16-byte words
     uint4* u = (uint4*)a.used;
-    for (int i = (int)rank * kSortThreads + tid; i < (a.V + 15) / 16; i += kSortCtas * kSortThreads)
+    for (int i = (int)rank * kSortThreads + tid; i < (a.V + 15) / 16; i += ctas * kSortThreads)
       u[i] = make_uint4(0, 0, 0, 0);
-    cluster_sync();
+    sync_all();
   }
 
   // the warp's part: whole groups of 32 positions
-  const int groups = (a.T + 31) / 32, all = kSortCtas * kSortWarps;
+  const int groups = (a.T + 31) / 32, all = ctas * kSortWarps;
   const int wid = (int)rank * kSortWarps + (int)warp;
   const int lo = (int)((int64_t)groups * wid / all) * 32;
   const int hi = min(a.T, (int)((int64_t)groups * (wid + 1) / all) * 32);
@@ -248,14 +256,17 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       for (int w = 0; w < kSortWarps; ++w) own += cnt[w * bins + tid];
       tot[tid] = own;
     }
-    cluster_sync();
-    uint32_t before = 0, total = 0;
-    if (tid < bins) {
+    uint32_t before = 0, total = own;
+    if (ctas > 1) {
+      cluster_sync();
+      total = 0;
+      if (tid < bins) {
 #pragma unroll
-      for (uint32_t r = 0; r < kSortCtas; ++r) {
-        const uint32_t x = peer_word(tot + tid, r);
-        if (r < rank) before += x;
-        total += x;
+        for (uint32_t r = 0; r < kSortCtas; ++r) {
+          const uint32_t x = peer_word(tot + tid, r);
+          if (r < rank) before += x;
+          total += x;
+        }
       }
     }
     const uint32_t base = block_scan(total, scratch);
@@ -292,14 +303,17 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       }
       __syncwarp();
     }
-    cluster_sync();  // the sorted keys are visible to the cluster
+    sync_all();
   }
 
 }
 
 // ---------------------------------------------------------------------------
-// Sums. A warp takes a range of L sorted positions and 256 N columns (eight
-// groups of N a lane), two rows ahead of the sums. Runs of at most kShort
+// Sums. A warp takes a range of L sorted positions and 32 N G columns (G
+// groups of N a lane), 16 / G rows ahead of the sums: G = 8 for many wide
+// rows, G = 2 where rows are narrow or few (a warp then has eight rows on
+// their way: 10155 positions of 168 columns 24 us with G = 8, most of it one
+// warp waiting for row after row of a run). Runs of at most kShort
 // belong whole to the range of their first position; a longer one is cut at
 // the ranges' borders, each piece going to a partial sum: slot 2 j + 1 in the
 // range j where the run begins, slot 2 j in the later ones.
@@ -307,7 +321,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 // run 136 us, blocks for pieces and warps for short runs 92 us.
 // ---------------------------------------------------------------------------
 constexpr int kShort = 32;
-constexpr int kGroups = 8;
+constexpr int kInFlight = 16;  // row parts a lane has on their way
 
 struct SumArgs {
   const int2* s;
@@ -322,9 +336,10 @@ struct SumArgs {
   int clear_row0, clear_rows;  // rows from clear_row0 on are cleared, clear_rows at a time (0: none)
 };
 
-template <bool DB, bool EB, int N>
+template <bool DB, bool EB, int N, int G>
 __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
   constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kGroups = G, D = kInFlight / G;
   const int lane = (int)lane_id(), h = a.h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -376,18 +391,18 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
       pend = tail_piece ? e : n;
     }
     const int tail_from = tail_piece ? 63 - __clzll((long long)mine) : 64;
-    float4 acc[kGroups], v0[kGroups], v1[kGroups];
-    auto load = [&](int p, float4 (&v)[kGroups]) {
+    float4 acc[kGroups], v[D][kGroups];
+    auto load = [&](int p, float4 (&row)[kGroups]) {
       const int pos = __shfl_sync(kAll, p < 32 ? cur.y : fol.y, p & 31);
       const size_t base = (size_t)pos * h + c0;
 #pragma unroll
       for (int k = 0; k < kGroups; ++k)
-        if (c0 + 32 * N * k < h) v[k] = loadn<DB, N>(a.dout, base + 32 * N * k);
+        if (c0 + 32 * N * k < h) row[k] = loadn<DB, N>(a.dout, base + 32 * N * k);
     };
     bool fresh = true, in_head = head_piece;
-    auto step = [&](int p, const float4 (&v)[kGroups]) {
+    auto step = [&](int p, const float4 (&row)[kGroups]) {
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k) acc[k] = fresh ? v[k] : add4(acc[k], v[k]);
+      for (int k = 0; k < kGroups; ++k) acc[k] = fresh ? row[k] : add4(acc[k], row[k]);
       fresh = p + 1 == pend || ((heads >> (p + 1)) & 1);
       if (!fresh) return;
       const bool tail = p >= tail_from;
@@ -413,15 +428,16 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
       const int id = __shfl_sync(kAll, cur.x, tail_from);
       if (lane == 0) a.longs[atomicAdd(a.ctl, 1)] = make_int2(j, id);  // their order does not enter the sums
     }
-    if (p0 < pend) load(p0, v0);
-    if (p0 + 1 < pend) load(p0 + 1, v1);
-    for (int p = p0; p < pend; p += 2) {
-      step(p, v0);
-      if (p + 2 < pend) load(p + 2, v0);
-      if (p + 1 < pend) {
-        step(p + 1, v1);
-        if (p + 3 < pend) load(p + 3, v1);
-      }
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      if (p0 + i < pend) load(p0 + i, v[i]);
+    for (int p = p0; p < pend; p += D) {
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if (p + i < pend) {
+          step(p + i, v[i]);
+          if (p + i + D < pend) load(p + i + D, v[i]);
+        }
     }
   }
 
@@ -451,14 +467,15 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
   }
 }
 
-// Long runs: their partial sums added in order, four groups of 256 threads
-// each a quarter of them, then the quarters in order.
+// Long runs: their partial sums added in order by 1024 / CX groups of CX
+// threads (a column each), every group an equal share, then the groups in
+// order.
 template <bool EB, int N>
-__global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a) {
-  __shared__ float4 quarter[4][256];
+__global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a, int CX) {
+  __shared__ float4 share[1024];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int g = (int)threadIdx.x >> 8, x = (int)threadIdx.x & 255, c = ((int)blockIdx.y * 256 + x) * N, h = a.h;
-  const int n = a.ctl[0];
+  const int x = (int)threadIdx.x & (CX - 1), g = (int)threadIdx.x / CX, groups = 1024 / CX;
+  const int c = ((int)blockIdx.y * CX + x) * N, h = a.h, n = a.ctl[0];
   for (int r = blockIdx.x; r < n; r += gridDim.x) {
     const int j0 = a.longs[r].x, id = a.longs[r].y;
     int k = 0;  // later ranges that the run reaches into
@@ -470,7 +487,7 @@ __global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a) {
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < h) {
-      const int lo = (int)((int64_t)k * g / 4), hi = (int)((int64_t)k * (g + 1) / 4);
+      const int lo = (int)((int64_t)k * g / groups), hi = (int)((int64_t)k * (g + 1) / groups);
       if (g == 0) acc = loadn<false, N>(a.part, (size_t)(2 * j0 + 1) * h + c);
       for (int q = lo; q < hi; q += 8) {
         float4 v[8];
@@ -482,10 +499,12 @@ __global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a) {
           if (q + i < hi) acc = add4(acc, v[i]);
       }
     }
-    quarter[g][x] = acc;
+    share[threadIdx.x] = acc;
     __syncthreads();
     if (g == 0 && c < h) {
-      acc = scaled(add4(add4(acc, quarter[1][x]), add4(quarter[2][x], quarter[3][x])), a.scale);
+#pragma unroll 4
+      for (int i = 1; i < groups; ++i) acc = add4(acc, share[i * CX + x]);
+      acc = scaled(acc, a.scale);
       const size_t to = (size_t)id * h + c;
       if (a.add) accumulate<EB, N>(a.dtable, to, acc);
       else storen<EB, N>(a.dtable, to, acc);
@@ -494,13 +513,17 @@ __global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a) {
   }
 }
 
-// Positions a range covers: 32 for many, fewer where that would leave warps
-// without work.
-int range_len(int T, int h) {
-  const int chunks = (h + 1023) / 1024;
-  int L = 32;
-  while (L > 4 && (int64_t)(T / L) * chunks < 2048) L /= 2;
-  return L;
+// Column groups a lane takes, and positions a range covers: 8 and 32 for many
+// wide rows, fewer where that would leave warps without work.
+struct SumShape {
+  int G, L;
+};
+SumShape sum_shape(int T, int h) {
+  SumShape s{8, 32};
+  if (h <= 512 || (int64_t)(T / 16) * ((h + 1023) / 1024) < 2048) s.G = 2;
+  const int chunks = (h + 128 * s.G - 1) / (128 * s.G);
+  while (s.L > 4 && (int64_t)(T / s.L) * chunks < 2048) s.L /= 2;
+  return s;
 }
 
 struct EmbedWs {
@@ -514,7 +537,7 @@ EmbedWs embed_ws(int T, int V, int h) {
     x += (bytes + 255) / 256 * 256;
     return r;
   };
-  const int L = range_len(T, h);
+  const int L = sum_shape(T, h).L;
   o.a = take((size_t)T * 8);
   o.b = take((size_t)T * 8);
   o.used = take((size_t)V);
@@ -584,8 +607,22 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
                            ((kSortWarps + 1) << kMaxDigit) * 4) != cudaSuccess)
     return -1;
   const size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
-  const unsigned blocks = (unsigned)(kSortCtas + (clearers + kSortCtas - 1) / kSortCtas * kSortCtas);
-  embed_sort_kernel<<<blocks, kSortThreads, smem, st>>>(a);
+  a.ctas = T <= kSortOne ? 1 : kSortCtas;
+  cudaError_t e = cudaSuccess;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.ctas + (clearers + a.ctas - 1) / a.ctas * a.ctas));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)a.ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.ctas > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
+  }
 
   SumArgs b;
   b.s = (a.passes & 1) ? a.a : a.b;
@@ -599,8 +636,9 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   b.T = T;
   b.V = V;
   b.h = h;
-  b.L = range_len(T, h);
-  b.chunks = (units + 32 * kGroups - 1) / (32 * kGroups);
+  const SumShape shape = sum_shape(T, h);
+  b.L = shape.L;
+  b.chunks = (units + 32 * shape.G - 1) / (32 * shape.G);
   b.add = add ? 1 : 0;
   b.clear_row0 = first;
   b.clear_rows = a.used ? (int)std::max<size_t>(1, 32768 / row) : 0;
@@ -616,21 +654,30 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (jobs > (1 << 30)) return -1;
   cfg.gridDim = dim3((unsigned)(a.used ? 304 : std::min<int64_t>(304, (jobs + 7) / 8)));
   cfg.blockDim = dim3(256);
-  cudaError_t e = cudaSuccess;
-  auto go = [&](auto k) { e = cudaLaunchKernelEx(&cfg, k, b); };
-  auto sums = [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    if (db) eb ? go(embed_sum_kernel<true, true, N>) : go(embed_sum_kernel<true, false, N>);
-    else eb ? go(embed_sum_kernel<false, true, N>) : go(embed_sum_kernel<false, false, N>);
+  auto sums = [&](auto n, auto gr) {
+    constexpr int N = decltype(n)::value, G = decltype(gr)::value;
+    auto go = [&](auto k) {
+      if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, b);
+    };
+    if (db) eb ? go(embed_sum_kernel<true, true, N, G>) : go(embed_sum_kernel<true, false, N, G>);
+    else eb ? go(embed_sum_kernel<false, true, N, G>) : go(embed_sum_kernel<false, false, N, G>);
   };
-  if (vec) sums(std::integral_constant<int, 4>());
-  else sums(std::integral_constant<int, 1>());
-  if (T > kShort && e == cudaSuccess) {
-    cfg.gridDim = dim3((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + 255) / 256));
+  auto sums_n = [&](auto n) {
+    if (shape.G == 8) sums(n, std::integral_constant<int, 8>());
+    else sums(n, std::integral_constant<int, 2>());
+  };
+  if (vec) sums_n(std::integral_constant<int, 4>());
+  else sums_n(std::integral_constant<int, 1>());
+  if (T > kShort) {
+    int CX = 32;
+    while (CX < units && CX < 256) CX *= 2;
+    cfg.gridDim = dim3((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + CX - 1) / CX));
     cfg.blockDim = dim3(1024);
     auto longs = [&](auto n) {
       constexpr int N = decltype(n)::value;
-      eb ? go(embed_long_kernel<true, N>) : go(embed_long_kernel<false, N>);
+      if (e == cudaSuccess)
+        e = eb ? cudaLaunchKernelEx(&cfg, embed_long_kernel<true, N>, b, CX)
+               : cudaLaunchKernelEx(&cfg, embed_long_kernel<false, N>, b, CX);
     };
     if (vec) longs(std::integral_constant<int, 4>());
     else longs(std::integral_constant<int, 1>());
