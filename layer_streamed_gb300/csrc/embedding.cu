@@ -310,18 +310,18 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
 
 // ---------------------------------------------------------------------------
 // Sums. A warp takes a range of L sorted positions and 32 N G columns (G
-// groups of N a lane), 16 / G rows ahead of the sums: G = 8 for many wide
-// rows, G = 2 where rows are narrow or few (a warp then has eight rows on
-// their way: 10155 positions of 168 columns 24 us with G = 8, most of it one
-// warp waiting for row after row of a run). Runs of at most kShort
-// belong whole to the range of their first position; a longer one is cut at
-// the ranges' borders, each piece going to a partial sum: slot 2 j + 1 in the
-// range j where the run begins, slot 2 j in the later ones.
+// groups of N a lane). Each lane copies its part of the rows into shared
+// memory D rows ahead of the sums (cp.async: nothing to wait for but its own
+// copies), so a row's way from memory is hidden however short the runs are.
+// Runs of at most kShort belong whole to the range of their first position; a
+// longer one is cut at the ranges' borders, each piece going to a partial sum:
+// slot 2 j + 1 in the range j where the run begins, slot 2 j in the later ones.
 // Measured for 8192 tokens of 128256 x 4096, added to the table: a block a
-// run 136 us, blocks for pieces and warps for short runs 92 us.
+// run 136 us, blocks for pieces and warps for short runs 92 us, rows ahead in
+// registers 76 us (and their unrolled code 18 us for 1266 tokens of 884 x 192,
+// most of it instruction fetches).
 // ---------------------------------------------------------------------------
 constexpr int kShort = 32;
-constexpr int kInFlight = 16;  // row parts a lane has on their way
 
 struct SumArgs {
   const int2* s;
@@ -336,10 +336,15 @@ struct SumArgs {
   int clear_row0, clear_rows;  // rows from clear_row0 on are cleared, clear_rows at a time (0: none)
 };
 
+constexpr int sum_depth(int G) { return G == 1 ? 8 : 6; }
+constexpr int sum_smem(int G, bool bf16) { return 8 * sum_depth(G) * G * 32 * (bf16 ? 8 : 16); }
+
 template <bool DB, bool EB, int N, int G>
-__global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
+__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   constexpr uint32_t kAll = 0xffffffffu;
-  constexpr int kGroups = G, D = kInFlight / G;
+  constexpr int kGroups = G, D = sum_depth(G), kPart = DB ? 8 : 16;
+  extern __shared__ __align__(16) uint8_t ring[];  // [warp][D][G][lane]: 4 columns
+  uint8_t* mine_ring = ring + ((int)warp_id() * D * G * 32 + (int)lane_id()) * kPart;
   const int lane = (int)lane_id(), h = a.h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -391,20 +396,43 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
       pend = tail_piece ? e : n;
     }
     const int tail_from = tail_piece ? 63 - __clzll((long long)mine) : 64;
-    float4 acc[kGroups], v[D][kGroups];
-    auto load = [&](int p, float4 (&row)[kGroups]) {
-      const int pos = __shfl_sync(kAll, p < 32 ? cur.y : fol.y, p & 31);
-      const size_t base = (size_t)pos * h + c0;
+    float4 acc[kGroups];
+    auto row_of = [&](int p) { return (size_t)__shfl_sync(kAll, p < 32 ? cur.y : fol.y, p & 31) * h + c0; };
+    auto request = [&](int p, int slot) {  // one column at a time: read directly, below
+      if (N == 4 && p < pend) {
+        const size_t base = row_of(p);
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k)
-        if (c0 + 32 * N * k < h) row[k] = loadn<DB, N>(a.dout, base + 32 * N * k);
+        for (int k = 0; k < kGroups; ++k)
+          if (c0 + 128 * k < h) {
+            const void* g = (const uint8_t*)a.dout + (base + 128 * k) * (DB ? 2 : 4);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                             smem_u32(mine_ring + (slot * G + k) * 32 * kPart)),
+                         "l"(g), "n"(kPart)
+                         : "memory");
+          }
+      }
+      if (N == 4) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto row_value = [&](int slot, int k, size_t base) {
+      if (N == 4) return load4<DB>(mine_ring + (slot * G + k) * 32 * kPart, 0);
+      return loadn<DB, N>(a.dout, base + 32 * N * k);
     };
     bool fresh = true, in_head = head_piece;
-    auto step = [&](int p, const float4 (&row)[kGroups]) {
+    int slot = 0;
+    for (int i = 0; i < D; ++i) request(p0 + i, i);
+    for (int p = p0; p < pend; ++p) {
+      if (N == 4) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const size_t base = N == 4 ? 0 : row_of(p);
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k) acc[k] = fresh ? row[k] : add4(acc[k], row[k]);
+      for (int k = 0; k < kGroups; ++k)
+        if (c0 + 32 * N * k < h) {
+          const float4 v = row_value(slot, k, base);
+          acc[k] = fresh ? v : add4(acc[k], v);
+        }
+      request(p + D, slot);
+      slot = slot + 1 == D ? 0 : slot + 1;
       fresh = p + 1 == pend || ((heads >> (p + 1)) & 1);
-      if (!fresh) return;
+      if (!fresh) continue;
       const bool tail = p >= tail_from;
       if (in_head || tail) {
         float* dst = a.part + (size_t)(2 * j + (in_head ? 0 : 1)) * h + c0;
@@ -423,21 +451,11 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(SumArgs a) {
           }
       }
       in_head = false;
-    };
+    }
+    if (N == 4) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (tail_piece && chunk == 0) {
       const int id = __shfl_sync(kAll, cur.x, tail_from);
       if (lane == 0) a.longs[atomicAdd(a.ctl, 1)] = make_int2(j, id);  // their order does not enter the sums
-    }
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-      if (p0 + i < pend) load(p0 + i, v[i]);
-    for (int p = p0; p < pend; p += D) {
-#pragma unroll
-      for (int i = 0; i < D; ++i)
-        if (p + i < pend) {
-          step(p + i, v[i]);
-          if (p + i + D < pend) load(p + i + D, v[i]);
-        }
     }
   }
 
@@ -513,14 +531,14 @@ __global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a, int CX) {
   }
 }
 
-// Column groups a lane takes, and positions a range covers: 8 and 32 for many
+// Column groups a lane takes, and positions a range covers: 4 and 32 for many
 // wide rows, fewer where that would leave warps without work.
 struct SumShape {
   int G, L;
 };
 SumShape sum_shape(int T, int h) {
-  SumShape s{8, 32};
-  if (h <= 512 || (int64_t)(T / 16) * ((h + 1023) / 1024) < 2048) s.G = 2;
+  SumShape s{4, 32};
+  if (h <= 128 || (int64_t)(T / 16) * ((h + 511) / 512) < 2048) s.G = 1;
   const int chunks = (h + 128 * s.G - 1) / (128 * s.G);
   while (s.L > 4 && (int64_t)(T / s.L) * chunks < 2048) s.L /= 2;
   return s;
@@ -652,19 +670,24 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   cfg.numAttrs = 1;
   const int64_t jobs = (int64_t)((T + b.L - 1) / b.L) * b.chunks;
   if (jobs > (1 << 30)) return -1;
-  cfg.gridDim = dim3((unsigned)(a.used ? 304 : std::min<int64_t>(304, (jobs + 7) / 8)));
+  const int resident = 152 * (shape.G == 1 ? 6 : db ? 4 : 2);  // blocks by their shared memory
+  cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
   cfg.blockDim = dim3(256);
   auto sums = [&](auto n, auto gr) {
     constexpr int N = decltype(n)::value, G = decltype(gr)::value;
+    const int ring = sum_smem(G, db);
+    cfg.dynamicSmemBytes = ring;
     auto go = [&](auto k) {
+      if (e == cudaSuccess && ring > 48 * 1024)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
       if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, b);
     };
     if (db) eb ? go(embed_sum_kernel<true, true, N, G>) : go(embed_sum_kernel<true, false, N, G>);
     else eb ? go(embed_sum_kernel<false, true, N, G>) : go(embed_sum_kernel<false, false, N, G>);
   };
   auto sums_n = [&](auto n) {
-    if (shape.G == 8) sums(n, std::integral_constant<int, 8>());
-    else sums(n, std::integral_constant<int, 2>());
+    if (shape.G == 4) sums(n, std::integral_constant<int, 4>());
+    else sums(n, std::integral_constant<int, 1>());
   };
   if (vec) sums_n(std::integral_constant<int, 4>());
   else sums_n(std::integral_constant<int, 1>());
@@ -673,6 +696,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
     while (CX < units && CX < 256) CX *= 2;
     cfg.gridDim = dim3((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + CX - 1) / CX));
     cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = 0;
     auto longs = [&](auto n) {
       constexpr int N = decltype(n)::value;
       if (e == cudaSuccess)
