@@ -351,7 +351,9 @@ int mt_debug_inject_fault(mt_ctx* ctx, int kind, int nth);
  * current device; `stream` is a cudaStream_t (null = legacy default stream).
  * Calls are asynchronous; errors in launch configuration are returned, and
  * device-side barrier timeouts are reported by mt_op_device_error.
- * bf16 tensors are raw 16-bit bfloat16 storage.
+ * bf16 tensors are raw 16-bit bfloat16 storage. A workspace belongs to one
+ * call at a time: calls that may overlap on the GPU (other streams, captured
+ * graphs) each need their own.
  * ------------------------------------------------------------------------- */
 
 /* GEMM on the tensor cores, bf16 operands, fp32 accumulation.

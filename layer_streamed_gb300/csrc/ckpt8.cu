@@ -30,6 +30,7 @@
 namespace mt {
 
 MT_DEVICE_ERROR_READER(ckpt8_take_device_error)
+MT_DEVICE_ERROR_PEEKER(ckpt8_peek_device_error)
 
 namespace {
 

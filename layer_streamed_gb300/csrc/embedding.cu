@@ -605,6 +605,10 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
   const int units = vec ? h / 4 : h, esz = eb ? 2 : 4;
   const size_t row = (size_t)h * esz;
+  const SumShape shape = sum_shape(T, h);
+  const int chunks = (units + 32 * shape.G - 1) / (32 * shape.G);
+  const int64_t jobs = (int64_t)((T + shape.L - 1) / shape.L) * chunks;
+  if (jobs > (1 << 30)) return -1;
   SortArgs a;
   a.ids = ids;
   a.a = (int2*)(w + o.a);
@@ -654,9 +658,8 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   b.T = T;
   b.V = V;
   b.h = h;
-  const SumShape shape = sum_shape(T, h);
   b.L = shape.L;
-  b.chunks = (units + 32 * shape.G - 1) / (32 * shape.G);
+  b.chunks = chunks;
   b.add = add ? 1 : 0;
   b.clear_row0 = first;
   b.clear_rows = a.used ? (int)std::max<size_t>(1, 32768 / row) : 0;
@@ -668,8 +671,6 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = early;
   cfg.numAttrs = 1;
-  const int64_t jobs = (int64_t)((T + b.L - 1) / b.L) * b.chunks;
-  if (jobs > (1 << 30)) return -1;
   const int resident = 152 * (shape.G == 1 ? 6 : db ? 4 : 2);  // blocks by their shared memory
   cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
   cfg.blockDim = dim3(256);

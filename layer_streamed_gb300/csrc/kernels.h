@@ -182,6 +182,7 @@ uint32_t gemm_take_device_error();
 uint32_t attention_tc_take_device_error();
 uint32_t gemm_peek_device_error();  // the same words, not cleared
 uint32_t attention_tc_peek_device_error();
+uint32_t ckpt8_peek_device_error();
 
 // Tensor-core flash attention (attention_tc.cu); head_dim in {16,32,64,128},
 // row strides multiples of 8. work: attention_bwd_workspace(B, S, nq) floats

@@ -926,6 +926,11 @@ struct NvtxRange {
   }
 };
 
+// Error words of the step's kernels that wait on barriers, not cleared.
+uint32_t step_peek_device_error() {
+  return gemm_peek_device_error() | attention_tc_peek_device_error() | ckpt8_peek_device_error();
+}
+
 struct Step {
   mt_ctx* ctx;
   int B, S, T, K, nb;
@@ -1847,7 +1852,7 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
           opt.status = MT_ERR_TIMEOUT;
           return;
         }
-        if (gemm_peek_device_error() | attention_tc_peek_device_error()) {
+        if (step_peek_device_error()) {
           opt.status = MT_ERR_DEVICE;
           return;
         }
@@ -1863,7 +1868,7 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
       const int nthr = ctx->opt_threads > 0 ? ctx->opt_threads
                                             : (int)std::max(1u, std::thread::hardware_concurrency());
       auto update = [&](int u) {
-        if (gemm_peek_device_error() | attention_tc_peek_device_error()) {  // garbage gradients: apply nothing
+        if (step_peek_device_error()) {  // garbage gradients: apply nothing
           opt.status = MT_ERR_DEVICE;
           return false;
         }
@@ -2426,7 +2431,7 @@ int step_common(mt_ctx* ctx, const int32_t* tokens, const int32_t* labels, int B
     cudaGetLastError();
     ctx->err = msg;
   } else {
-    const uint32_t derr = gemm_take_device_error() | attention_tc_take_device_error();
+    const uint32_t derr = gemm_take_device_error() | attention_tc_take_device_error() | ckpt8_take_device_error();
     if (derr) {
       char b[96];
       snprintf(b, sizeof b, "device error word 0x%x (barrier timeout inside a kernel)", derr);

@@ -5,6 +5,9 @@
   python -m layer_streamed_gb300.kbench attn --B 2 --S 4096 --heads 32 --kv-heads 8 --head-dim 128 [--bwd]
   python -m layer_streamed_gb300.kbench norm --T 8192 --h 4096 [--bwd]
   python -m layer_streamed_gb300.kbench moe --T 4096 --h 4096 --experts 128 --top-k 8 --expert-ffn 1536
+  python -m layer_streamed_gb300.kbench ckpt --op pack|unpack|norm|swiglu --T 8192 --n 4096 --fmt i8 [--bwd]
+  python -m layer_streamed_gb300.kbench logp --T 8192 --V 128256 --dtype f32 --top-k 8 [--bwd]
+  python -m layer_streamed_gb300.kbench embed --T 8192 --V 128256 --h 4096 --grad f32 [--bwd] [--add]
 
 Inputs are random bf16 tensors on the current GPU (larger than L2 at the 8B
 shapes); each launch is timed with CUDA events on the launching stream after
@@ -18,6 +21,7 @@ from __future__ import annotations
 
 import argparse
 import json
+import math
 
 import torch
 
@@ -164,9 +168,87 @@ def bench_moe(args) -> dict:
             "tflops": flop / ms / 1e9}
 
 
+def bench_ckpt(args) -> dict:
+    """8-bit checkpoints: pack or unpack an fp32 [T, n], or the RMSNorm
+    (width n) or SwiGLU (FFN width n) pass that writes or (--bwd) reads one.
+    GB/s counts every operand once."""
+    T, n, fmt = args.T, args.n, {"i8": mt.MT_CKPT_I8, "e4m3": mt.MT_CKPT_E4M3}[args.fmt]
+    e = lambda *s, dt=torch.float32: torch.empty(s, device="cuda", dtype=dt)
+    bf, u8, nb = torch.bfloat16, torch.uint8, -(-n // 32)
+    if args.op == "swiglu":
+        gu, act, dgu = torch.randn((T, 2 * n), device="cuda").to(bf), e(T, n, dt=bf), e(T, 2 * n, dt=bf)
+        codes, scales = e(T, 2 * n, dt=u8), e(T, 2 * nb, dt=u8)
+        fwd = lambda: mt.mt_op_swiglu_fwd_ckpt8(gu, act, codes, scales, fmt, T, n, n)
+        bwd = lambda: mt.mt_op_swiglu_bwd_ckpt8(codes, scales, fmt, act, dgu, T, n, n)
+        nbytes = T * (8 * n + 2 * nb)
+    else:
+        x, codes, scales = torch.randn((T, n), device="cuda"), e(T, n, dt=u8), e(T, nb, dt=u8)
+        if args.op == "norm":
+            w, dy, res = torch.ones(n, device="cuda"), torch.randn_like(x), torch.randn_like(x)
+            y, r, dx, dxb, dw = e(T, n, dt=bf), e(T), e(T, n), e(T, n, dt=bf), e(n)
+            ws = e(mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, n))
+            fwd = lambda: mt.mt_op_rmsnorm_fwd_ckpt8(x, w, y, r, codes, scales, fmt, T, n, 1e-5)
+            bwd = lambda: mt.mt_op_rmsnorm_bwd_ckpt8(codes, scales, fmt, w, r, dy, res, dx, dxb, dw, ws, T, n)
+            nbytes = T * n * (15 if args.bwd else 7) + T * nb
+        else:
+            fwd = lambda: mt.mt_op_ckpt8_pack(x, mt.MT_F32, fmt, codes, scales, T, n, n, n)
+            bwd = lambda: mt.mt_op_ckpt8_unpack(codes, scales, fmt, x, mt.MT_F32, T, n, n, n)
+            nbytes = T * (5 * n + nb)
+    fwd()
+    back = args.op == "unpack" or (args.bwd and args.op in ("norm", "swiglu"))
+    ms = _time(bwd if back else fwd, args.reps)
+    return {"kernel": f"ckpt8_{args.op}" + ("_bwd" if back and args.op != "unpack" else ""), "T": T, "n": n,
+            "fmt": args.fmt, "ms": ms, "gbs": nbytes / ms / 1e6}
+
+
+def bench_logp(args) -> dict:
+    """Log probabilities of given tokens with entropy and top-k, or (--bwd)
+    the gradient of the logits in their type."""
+    T, V, k = args.T, args.V, args.top_k
+    dt, code, b = (torch.float32, mt.MT_F32, 4) if args.dtype == "f32" else (torch.bfloat16, mt.MT_BF16, 2)
+    z = torch.randn((T, V), device="cuda", dtype=dt)
+    ids = torch.randint(0, V, (T,), device="cuda", dtype=torch.int32)
+    lse, logp, ent, g = (torch.empty(T, device="cuda") for _ in range(4))
+    ti, tl = torch.empty((T, k), device="cuda", dtype=torch.int32), torch.empty((T, k), device="cuda")
+    fwd = lambda: mt.mt_op_token_logprobs(z, code, ids, 1.0, k, lse, logp, ent, ti, tl, T, V, V)
+    fwd()
+    if not args.bwd:
+        ms, nbytes = _time(fwd, args.reps), T * V * b
+    else:
+        dz = torch.empty_like(z)
+        g.fill_(1.0)
+        ms = _time(lambda: mt.mt_op_token_logprobs_bwd(z, code, ids, 1.0, lse, ent, g, g, dz, code, T, V, V, V), args.reps)
+        nbytes = 2 * T * V * b
+    return {"kernel": "token_logprobs" + ("_bwd" if args.bwd else ""), "T": T, "V": V, "dtype": args.dtype, "top_k": k,
+            "ms": ms, "gbs": nbytes / ms / 1e6}
+
+
+def bench_embed(args) -> dict:
+    """Embedding lookup (bf16 table, fp32 out), or (--bwd) the table's
+    gradient from fp32 rows, written whole or (--add) added to; ids with
+    frequencies that fall off with their rank. GB/s counts the rows and, for
+    the gradient, the table once (--add: the used rows twice)."""
+    T, V, h = args.T, args.V, args.h
+    rank = torch.exp(torch.rand(T, device="cuda", dtype=torch.float64) * math.log(V)).long() - 1
+    ids = ((rank.clamp(0, V - 1) * 7919) % V).int()
+    rows = torch.randn((T, h), device="cuda")
+    if not args.bwd:
+        table = torch.randn((V, h), device="cuda").to(torch.bfloat16)
+        ms = _time(lambda: mt.mt_op_embed_fwd(table, mt.MT_BF16, ids, 2.0, rows, mt.MT_F32, T, V, h), args.reps)
+        nbytes = T * h * 6
+    else:
+        gt, code, b = (torch.float32, mt.MT_F32, 4) if args.grad == "f32" else (torch.bfloat16, mt.MT_BF16, 2)
+        dE = torch.zeros((V, h), device="cuda", dtype=gt)
+        ws = torch.empty(mt.mt_op_embed_bwd_workspace(T, V, h), device="cuda", dtype=torch.uint8)
+        ms = _time(lambda: mt.mt_op_embed_bwd(ids, rows, mt.MT_F32, 2.0, dE, code, args.add, ws, T, V, h), args.reps)
+        nbytes = T * h * 4 + (2 * int(ids.unique().numel()) if args.add else V) * h * b
+    return {"kernel": "embed_bwd" if args.bwd else "embed_fwd", "T": T, "V": V, "h": h, "grad": args.grad, "ms": ms,
+            "gbs": nbytes / ms / 1e6}
+
+
 def main():
     ap = argparse.ArgumentParser()
-    sub = ap.add_subparsers(dest="op", required=True)
+    sub = ap.add_subparsers(dest="kernel", required=True)
     g = sub.add_parser("gemm")
     g.add_argument("--mode", default="nt", choices=["nt", "nn", "tn"])
     g.add_argument("--M", type=int, default=8192)
@@ -196,9 +278,32 @@ def main():
     e.add_argument("--top-k", type=int, default=8)
     e.add_argument("--expert-ffn", type=int, default=1536)
     e.add_argument("--reps", type=int, default=20)
+    c = sub.add_parser("ckpt")
+    c.add_argument("--op", default="norm", choices=["pack", "unpack", "norm", "swiglu"])
+    c.add_argument("--T", type=int, default=8192)
+    c.add_argument("--n", type=int, default=4096)
+    c.add_argument("--fmt", default="i8", choices=["i8", "e4m3"])
+    c.add_argument("--bwd", action="store_true")
+    c.add_argument("--reps", type=int, default=20)
+    lp = sub.add_parser("logp")
+    lp.add_argument("--T", type=int, default=8192)
+    lp.add_argument("--V", type=int, default=128256)
+    lp.add_argument("--dtype", default="f32", choices=["f32", "bf16"])
+    lp.add_argument("--top-k", type=int, default=0)
+    lp.add_argument("--bwd", action="store_true")
+    lp.add_argument("--reps", type=int, default=20)
+    em = sub.add_parser("embed")
+    em.add_argument("--T", type=int, default=8192)
+    em.add_argument("--V", type=int, default=128256)
+    em.add_argument("--h", type=int, default=4096)
+    em.add_argument("--grad", default="f32", choices=["f32", "bf16"])
+    em.add_argument("--bwd", action="store_true")
+    em.add_argument("--add", action="store_true")
+    em.add_argument("--reps", type=int, default=20)
     args = ap.parse_args()
     mt.build()
-    res = {"gemm": bench_gemm, "attn": bench_attn, "norm": bench_norm, "moe": bench_moe}[args.op](args)
+    res = {"gemm": bench_gemm, "attn": bench_attn, "norm": bench_norm, "moe": bench_moe, "ckpt": bench_ckpt,
+           "logp": bench_logp, "embed": bench_embed}[args.kernel](args)
     res["device_error"] = mt.mt_op_device_error()
     print(json.dumps(res), flush=True)
 

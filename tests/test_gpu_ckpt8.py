@@ -61,6 +61,34 @@ def test_pack_and_unpack_follow_the_definition(fmt, bf16, T, n, ldx, ldc):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,n,ldx,ldc,x0,c0", [(5, 777, 777, 777, 1, 1), (40, 1003, 1004, 1010, 3, 5), (3, 224, 225, 231, 2, 7),
+                                               (9, 4097, 4097, 4099, 5, 3), (200, 33, 35, 33, 7, 2)])
+def test_pack_and_unpack_off_the_boundary(fmt, bf16, T, n, ldx, ldc, x0, c0):
+    """Tensors that start at any element, rows at any byte: what lies around them stays."""
+    torch, mt = need_gpu()
+    full = _activation(1, x0 + T * ldx + 9, 13 * T + n).reshape(-1)
+    X = torch.from_numpy(full).cuda().to(torch.bfloat16 if bf16 else torch.float32)
+    dtype = mt.MT_BF16 if bf16 else mt.MT_F32
+    x = from_dev(X)[x0:x0 + T * ldx].reshape(T, ldx)[:, :n]
+    raw = torch.full((c0 + T * ldc + 9,), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.empty((T, -(-n // 32)), dtype=torch.uint8, device="cuda")
+    mt.mt_op_ckpt8_pack(X[x0:], dtype, fmt, raw[c0:], scales, T, n, ldx, ldc)
+    r = raw.cpu().numpy()
+    codes, s = r[c0:c0 + T * ldc].reshape(T, ldc), scales.cpu().numpy()
+    assert np.all(r[:c0] == 0x55) and np.all(codes[:, n:] == 0x55) and np.all(r[c0 + T * ldc:] == 0x55)
+    want = ref.values_of(x, fmt)
+    assert np.array_equal(s, ref.scales_of(x, fmt))
+    assert np.array_equal(ref.decode(codes[:, :n].copy(), s, fmt), want)
+    back = torch.full_like(X, -7.0)
+    mt.mt_op_ckpt8_unpack(raw[c0:], scales, fmt, back[x0:], dtype, T, n, ldc, ldx)
+    b = from_dev(back)
+    got = b[x0:x0 + T * ldx].reshape(T, ldx)
+    assert np.array_equal(got[:, :n], bf16_round(want.astype(np.float32)) if bf16 else want.astype(np.float32))
+    assert np.all(b[:x0] == -7.0) and np.all(got[:, n:] == -7.0) and np.all(b[x0 + T * ldx:] == -7.0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_pack_borders(fmt):
     """Maxima on and around the limit, ties of both formats, subnormals,
     the largest fp32 values, zeros, infinities and NaN."""
@@ -116,7 +144,8 @@ def test_every_code_unpacks():
 @pytest.mark.parametrize("T,h,with_res,with_bf", [(1, 4, False, True), (5, 36, True, False), (77, 320, True, True),
                                                   (45, 1800, False, True), (700, 64, True, True),
                                                   (33, 4096, True, True), (9, 6000, True, False),
-                                                  (500, 8192, True, True), (3, 2052, False, False)])
+                                                  (500, 8192, True, True), (3, 2052, False, False), (400, 7452, True, True),
+                                                  (1300, 1032, False, True)])
 def test_rmsnorm_through_the_checkpoint(fmt, T, h, with_res, with_bf):
     torch, mt = need_gpu()
     eps = np.float32(1e-5)
@@ -203,7 +232,8 @@ def _act_bounds(g, u, d=None):
     be 0 (and the exponential infinite a little further out), which moves act
     and du by at most 2^-126 |g u| and |dact g|, and dg by 2^-126 |dact u|
     (1 + |g|); bf16 results below 2^-126 may be 0 too."""
-    s, silu, mag = silu_parts(g)
+    with np.errstate(over="ignore"):
+        s, silu, mag = silu_parts(g)
     e = (8 + 1.2 * np.abs(g)) * 2.0 ** -23
     if d is None:
         a = silu * u
@@ -250,6 +280,36 @@ def test_swiglu_through_the_checkpoint(fmt, T, F, ld):
     check(got[:, :F], dg, bg, "dg")
     check(got[:, ld:ld + F], du, bu, "du")
     assert np.all(got[:, F:ld] == 0) and np.all(got[:, ld + F:] == 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,F,off", [(7, 1001, 1), (65, 250, 3), (3, 4099, 6), (100, 31, 5)])
+def test_swiglu_off_the_boundary(fmt, T, F, off):
+    """Tensors that start at any element: the same values as from aligned ones, nothing written beside them."""
+    torch, mt = need_gpu()
+    gu = torch.randn((T, 2 * F), device="cuda").to(torch.bfloat16)
+    da = torch.randn((T, F), device="cuda").to(torch.bfloat16)
+    nb = -(-F // 32)
+
+    def run(o):
+        def place(t):
+            raw = torch.full((o + t.numel() + 9,), 3, dtype=t.dtype, device="cuda")
+            raw[o:o + t.numel()] = t.reshape(-1)
+            return raw
+        g, d = place(gu), place(da)
+        act, codes, dgu = place(torch.zeros_like(da)), place(torch.zeros((T, 2 * F), dtype=torch.uint8, device="cuda")), \
+            place(torch.zeros_like(gu))
+        scales = torch.empty((T, 2 * nb), dtype=torch.uint8, device="cuda")
+        mt.mt_op_swiglu_fwd_ckpt8(g[o:], act[o:], codes[o:], scales, fmt, T, F, F)
+        mt.mt_op_swiglu_bwd_ckpt8(codes[o:], scales, fmt, d[o:], dgu[o:], T, F, F)
+        out = []
+        for t in (act, codes, dgu):
+            assert bool((t[:o] == 3).all()) and bool((t[-9:] == 3).all())
+            out.append(t[o:-9].clone())
+        return out + [scales]
+
+    for a, b in zip(run(0), run(off)):
+        assert torch.equal(a, b)
 
 
 def test_swiglu_non_finite_block_is_nan_in_the_gradient():

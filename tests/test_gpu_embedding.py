@@ -98,6 +98,19 @@ def test_gradient(pattern, db, eb, T, V, h):
     assert mt.mt_op_device_error() == 0
 
 
+@pytest.mark.parametrize("db,eb,T,V,h", [(False, False, 33000, 50, 515), (True, True, 33000, 20, 516),
+                                         (True, False, 40000, 30000, 516), (False, True, 9000, 700, 2052)])
+def test_many_wide_rows(db, eb, T, V, h):
+    """Column groups several to a lane, whole and ragged, both types."""
+    torch, mt = need_gpu()
+    rng = np.random.default_rng(T + h)
+    ids = _ids("skewed", T, V, rng).astype(np.int32)
+    dout = torch.randn((T, h), device="cuda").to(torch.bfloat16 if db else torch.float32)
+    s, m, n = _reference(ids, from_dev(dout), V)
+    got = _grad(torch, mt, torch.from_numpy(ids).cuda(), dout, db, eb, 1.0, V)
+    _check_grad(from_dev(got), s, m, n, 1.0, eb)
+
+
 @pytest.mark.parametrize("V", [1 << 10, (1 << 10) - 1, 1 << 17, 151936, (1 << 20) + 3])
 def test_sort_over_the_vocabulary(V):
     """Vocabularies around the digits' borders, the largest ids in use: one
