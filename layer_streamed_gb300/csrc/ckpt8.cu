@@ -156,19 +156,27 @@ __device__ __forceinline__ void store_block(uint8_t* p, const uint32_t (&w)[8]) 
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-// WORDS words from byte offset o (less than a block) of NX words.
+// WORDS words from byte offset o (less than a block, the same in the whole
+// warp: a warp's units lie in one row) of NX words.
+template <int WORDS, int K, int NX>
+__device__ __forceinline__ void shift_from(const uint32_t (&x)[NX], uint32_t bits, uint32_t (&w)[WORDS]) {
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) w[i] = __funnelshift_r(x[i + K], i + K + 1 < NX ? x[i + K + 1] : 0u, bits);
+}
 template <int WORDS, int NX>
 __device__ __forceinline__ void shift_words(const uint32_t (&x)[NX], uint32_t o, uint32_t (&w)[WORDS]) {
-  constexpr int BW = block_bytes<WORDS>() / 4;
-  uint32_t a[WORDS + 1 + (BW == 4 ? 2 : 0)];
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(a) / 4); ++i) a[i] = i + 1 < NX && (o & 4) ? x[i + 1] : i < NX ? x[i] : 0u;
-  if constexpr (BW == 4) {
-#pragma unroll
-    for (int i = 0; i <= WORDS; ++i) a[i] = (o & 8) ? a[i + 2] : a[i];
+  const uint32_t bits = (o & 3) * 8;
+  if constexpr (block_bytes<WORDS>() == 8) {
+    if (o & 4) shift_from<WORDS, 1>(x, bits, w);
+    else shift_from<WORDS, 0>(x, bits, w);
+  } else {
+    switch (o >> 2) {
+      case 0: shift_from<WORDS, 0>(x, bits, w); break;
+      case 1: shift_from<WORDS, 1>(x, bits, w); break;
+      case 2: shift_from<WORDS, 2>(x, bits, w); break;
+      default: shift_from<WORDS, 3>(x, bits, w);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) w[i] = __funnelshift_r(a[i], a[i + 1], (o & 3) * 8);
 }
 template <int WORDS>
 __device__ __forceinline__ void load_elem(const uint8_t* p, int i, uint32_t (&w)[WORDS]) {
@@ -189,31 +197,34 @@ __device__ __forceinline__ void store_elem_of(uint8_t* p, int i, const uint32_t 
   else if (ES == 2) ((uint16_t*)p)[i] = (uint16_t)(y[(i >> 1) % BW] >> (16 * (i & 1)));
   else ((uint32_t*)p)[i] = y[i % BW];
 }
-// Unit u of a row of n columns, 0 past them. lo, hi: the tensor's bytes.
+// Whether the blocks that cover a row of `bytes` bytes lie within the
+// tensor's bytes [lo, hi) (the blocks reach 15 bytes back and 31 on).
+__device__ __forceinline__ bool inside(const void* row, size_t bytes, const void* lo, const void* hi) {
+  return (const uint8_t*)row - (const uint8_t*)lo >= 16 && (const uint8_t*)hi - (const uint8_t*)row >= (int64_t)bytes + 32;
+}
+// Unit u of a row of n columns, 0 past them. in: the row's blocks all lie
+// inside the tensor; else (its first and last rows) units go by elements.
 template <int WORDS, bool VEC>
-__device__ __forceinline__ void load_cols(const void* row, int u, int n, const void* lo, const void* hi,
-                                          uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ void load_cols(const void* row, int u, int n, bool in, uint32_t (&w)[WORDS]) {
   constexpr int BLK = block_bytes<WORDS>(), BW = BLK / 4, NB = WORDS / BW + 1;
   const uint8_t* p = (const uint8_t*)row + (size_t)u * (WORDS * 4);
   if (VEC && u * 8 + 8 <= n) {
     load_block(p, w);
     return;
   }
-  if (!VEC && u * 8 + 8 <= n) {
+  if (!VEC && in && u * 8 + 8 <= n) {
     const uint32_t o = (uint32_t)(uintptr_t)p & (BLK - 1);
     const uint8_t* q = p - o;
-    if (q >= (const uint8_t*)lo && q + NB * BLK <= (const uint8_t*)hi) {
-      uint32_t x[NB * BW];
+    uint32_t x[NB * BW];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        uint32_t y[BW];
-        load_block(q + k * BLK, y);
+    for (int k = 0; k < NB; ++k) {
+      uint32_t y[BW];
+      load_block(q + k * BLK, y);
 #pragma unroll
-        for (int i = 0; i < BW; ++i) x[k * BW + i] = y[i];
-      }
-      shift_words<WORDS>(x, o, w);
-      return;
+      for (int i = 0; i < BW; ++i) x[k * BW + i] = y[i];
     }
+    shift_words<WORDS>(x, o, w);
+    return;
   }
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) w[i] = 0;
@@ -227,7 +238,7 @@ template <int WORDS, bool VEC>
 __device__ __forceinline__ void store_cols(void* row, int u, int n, const uint32_t (&w)[WORDS], bool own) {
   constexpr int BLK = block_bytes<WORDS>(), BW = BLK / 4, ES = elem_bytes<WORDS>();
   uint8_t* p = (uint8_t*)row + (size_t)u * (WORDS * 4);
-  if (VEC) {
+  if constexpr (VEC) {
     if (!own) return;
     if (u * 8 + 8 <= n) {
       store_block(p, w);
@@ -236,35 +247,35 @@ __device__ __forceinline__ void store_cols(void* row, int u, int n, const uint32
       for (int i = 0; i < 8; ++i)
         if (u * 8 + i < n) store_elem(p, i, w);
     }
-    return;
-  }
-  uint32_t x[WORDS + BW], v[WORDS];
+  } else {
+    uint32_t x[WORDS + BW], v[WORDS];
 #pragma unroll
-  for (int i = 0; i < WORDS; ++i) x[i] = w[i];
+    for (int i = 0; i < WORDS; ++i) x[i] = w[i];
 #pragma unroll
-  for (int i = 0; i < BW; ++i) x[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-  const uint32_t o = (0u - (uint32_t)(uintptr_t)p) & (BLK - 1);  // bytes before the first boundary
-  shift_words<WORDS>(x, o, v);
-  if (!own) return;
-  const int first = u * 8 + (int)o / ES;  // column of the boundary
+    for (int i = 0; i < BW; ++i) x[WORDS + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+    const uint32_t o = (0u - (uint32_t)(uintptr_t)p) & (BLK - 1);  // bytes before the first boundary
+    shift_words<WORDS>(x, o, v);
+    if (!own) return;
+    const int first = u * 8 + (int)o / ES;  // column of the boundary
 #pragma unroll
-  for (int k = 0; k < WORDS / BW; ++k) {
-    const int c = first + k * (BLK / ES);
-    uint32_t y[BW];
+    for (int k = 0; k < WORDS / BW; ++k) {
+      const int c = first + k * (BLK / ES);
+      uint32_t y[BW];
 #pragma unroll
-    for (int i = 0; i < BW; ++i) y[i] = v[k * BW + i];
-    if (c + BLK / ES <= n) {
-      store_block(p + o + k * BLK, y);
-    } else if (c < n) {
+      for (int i = 0; i < BW; ++i) y[i] = v[k * BW + i];
+      if (c + BLK / ES <= n) {
+        store_block(p + o + k * BLK, y);
+      } else if (c < n) {
+#pragma unroll
+        for (int i = 0; i < BLK / ES; ++i)
+          if (c + i < n) store_elem_of<ES>(p + o + k * BLK, i, y);
+      }
+    }
+    if (u == 0 && o) {
 #pragma unroll
       for (int i = 0; i < BLK / ES; ++i)
-        if (c + i < n) store_elem_of<ES>(p + o + k * BLK, i, y);
+        if (i < (int)o / ES && i < n) store_elem(p, i, w);
     }
-  }
-  if (u == 0 && o) {
-#pragma unroll
-    for (int i = 0; i < BLK / ES; ++i)
-      if (i < (int)o / ES && i < n) store_elem(p, i, w);
   }
 }
 // The unit of a thread that is the x-th along its row, and whether it is its own.
@@ -338,7 +349,8 @@ __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict_
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
-      load_cols<W, VEC>((const uint8_t*)x + (size_t)t * ldx * esz, u, t < T ? n : 0, x, hi, xw[r]);
+      const uint8_t* row = (const uint8_t*)x + (size_t)t * ldx * esz;
+      load_cols<W, VEC>(row, u, t < T ? n : 0, !VEC && inside(row, (size_t)n * esz, x, hi), xw[r]);
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -369,7 +381,8 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __rest
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
-      load_cols<2, VEC>(codes + (size_t)t * ldc, u, t < T ? n : 0, codes, hi, w[r]);
+      const uint8_t* row = codes + (size_t)t * ldc;
+      load_cols<2, VEC>(row, u, t < T ? n : 0, !VEC && inside(row, n, codes, hi), w[r]);
       b[r] = t < T && u * 8 < n ? scales[(size_t)t * nb + u / 4] : 0u;
     }
 #pragma unroll
@@ -706,8 +719,9 @@ __global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y;
       const uint16_t* row = gu + (size_t)t * 2 * ld;
-      load_cols<4, VEC>(row, x, t < T ? F : 0, gu, hi, gq[r]);
-      load_cols<4, VEC>(row + ld, x, t < T ? F : 0, gu, hi, uq[r]);
+      const bool in = !VEC && inside(row, ((size_t)ld + F) * 2, gu, hi);
+      load_cols<4, VEC>(row, x, t < T ? F : 0, in, gq[r]);
+      load_cols<4, VEC>(row + ld, x, t < T ? F : 0, in, uq[r]);
     }
 #pragma unroll
     for (int r = 0; r < kSwRows; ++r) {
@@ -760,9 +774,11 @@ __global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __
     for (int r = 0; r < kSwRows; ++r) {
       const int t = t0 + r * step + threadIdx.y, n = t < T ? F : 0;
       const uint8_t* crow = codes + (size_t)t * 2 * ld;
-      load_cols<2, VEC>(crow, x, n, codes, chi, wg[r]);
-      load_cols<2, VEC>(crow + ld, x, n, codes, chi, wu[r]);
-      load_cols<4, VEC>(dact + (size_t)t * ld, x, n, dact, dhi, dq[r]);
+      const uint16_t* drow = dact + (size_t)t * ld;
+      const bool in = !VEC && inside(crow, (size_t)ld + F, codes, chi) && inside(drow, (size_t)F * 2, dact, dhi);
+      load_cols<2, VEC>(crow, x, n, in, wg[r]);
+      load_cols<2, VEC>(crow + ld, x, n, in, wu[r]);
+      load_cols<4, VEC>(drow, x, n, in, dq[r]);
       // a unit that lies in the padding has no block of its own
       bg[r] = x * 8 < n ? scales[(size_t)t * 2 * nb + x / 4] : 0u;
       bu[r] = x * 8 < n ? scales[(size_t)t * 2 * nb + nb + x / 4] : 0u;

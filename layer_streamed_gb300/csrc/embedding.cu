@@ -333,17 +333,20 @@ struct SumArgs {
   int32_t* ctl;
   float scale;
   int T, V, h, L, chunks, add;
+  int words;  // bf16 rows of single columns: dout starts on a word
   int clear_row0, clear_rows;  // rows from clear_row0 on are cleared, clear_rows at a time (0: none)
 };
 
-constexpr int sum_depth(int G) { return G == 1 ? 8 : 6; }
-constexpr int sum_smem(int G, bool bf16) { return 8 * sum_depth(G) * G * 32 * (bf16 ? 8 : 16); }
+// Bytes a lane copies at once: its N columns, or the word that a column lies in.
+constexpr int sum_part(int N, bool bf16) { return N == 1 ? 4 : bf16 ? 8 : 16; }
+constexpr int sum_depth(int G, int N) { return N == 1 ? 16 : G == 1 ? 8 : 6; }
+constexpr int sum_smem(int G, int N, bool bf16) { return 8 * sum_depth(G, N) * G * 32 * sum_part(N, bf16); }
 
 template <bool DB, bool EB, int N, int G>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   constexpr uint32_t kAll = 0xffffffffu;
-  constexpr int kGroups = G, D = sum_depth(G), kPart = DB ? 8 : 16;
-  extern __shared__ __align__(16) uint8_t ring[];  // [warp][D][G][lane]: 4 columns
+  constexpr int kGroups = G, D = sum_depth(G, N), kPart = sum_part(N, DB);
+  extern __shared__ __align__(16) uint8_t ring[];  // [warp][D][G][lane]: sum_part bytes
   uint8_t* mine_ring = ring + ((int)warp_id() * D * G * 32 + (int)lane_id()) * kPart;
   const int lane = (int)lane_id(), h = a.h;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -398,31 +401,39 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
     const int tail_from = tail_piece ? 63 - __clzll((long long)mine) : 64;
     float4 acc[kGroups];
     auto row_of = [&](int p) { return (size_t)__shfl_sync(kAll, p < 32 ? cur.y : fol.y, p & 31) * h + c0; };
-    auto request = [&](int p, int slot) {  // one column at a time: read directly, below
-      if (N == 4 && p < pend) {
+    auto request = [&](int p, int slot) {
+      if (p < pend) {
         const size_t base = row_of(p);
 #pragma unroll
         for (int k = 0; k < kGroups; ++k)
-          if (c0 + 128 * k < h) {
-            const void* g = (const uint8_t*)a.dout + (base + 128 * k) * (DB ? 2 : 4);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                             smem_u32(mine_ring + (slot * G + k) * 32 * kPart)),
-                         "l"(g), "n"(kPart)
-                         : "memory");
+          if (c0 + 32 * N * k < h) {
+            const size_t i = base + 32 * N * k;
+            const uint32_t to = smem_u32(mine_ring + (slot * G + k) * 32 * kPart);
+            if (N == 4 || !DB) {
+              const void* g = (const uint8_t*)a.dout + i * (DB ? 2 : 4);
+              asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(g), "n"(kPart) : "memory");
+            } else if (a.words) {  // the word with column i; nothing behind the last one is read
+              const void* g = (const uint8_t*)a.dout + (i & ~(size_t)1) * 2;
+              const int n = (i | 1) < (size_t)a.T * h ? 4 : 2;
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(g), "r"(n) : "memory");
+            }
           }
       }
-      if (N == 4) asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto row_value = [&](int slot, int k, size_t base) {
-      if (N == 4) return load4<DB>(mine_ring + (slot * G + k) * 32 * kPart, 0);
-      return loadn<DB, N>(a.dout, base + 32 * N * k);
+      const uint8_t* at = mine_ring + (slot * G + k) * 32 * kPart;
+      if (N == 4) return load4<DB>(at, 0);
+      const size_t i = base + 32 * k;
+      if (DB && !a.words) return loadn<DB, N>(a.dout, i);
+      return loadn<DB, N>(at, DB ? i & 1 : 0);
     };
     bool fresh = true, in_head = head_piece;
     int slot = 0;
     for (int i = 0; i < D; ++i) request(p0 + i, i);
     for (int p = p0; p < pend; ++p) {
-      if (N == 4) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-      const size_t base = N == 4 ? 0 : row_of(p);
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const size_t base = DB && N == 1 ? row_of(p) : 0;
 #pragma unroll
       for (int k = 0; k < kGroups; ++k)
         if (c0 + 32 * N * k < h) {
@@ -452,7 +463,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
       }
       in_head = false;
     }
-    if (N == 4) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (tail_piece && chunk == 0) {
       const int id = __shfl_sync(kAll, cur.x, tail_from);
       if (lane == 0) a.longs[atomicAdd(a.ctl, 1)] = make_int2(j, id);  // their order does not enter the sums
@@ -661,6 +672,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   b.L = shape.L;
   b.chunks = chunks;
   b.add = add ? 1 : 0;
+  b.words = al(dout, 4) ? 1 : 0;
   b.clear_row0 = first;
   b.clear_rows = a.used ? (int)std::max<size_t>(1, 32768 / row) : 0;
   // launched while the step before ends; they wait for it themselves
@@ -671,12 +683,12 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = early;
   cfg.numAttrs = 1;
-  const int resident = 152 * (shape.G == 1 ? 6 : db ? 4 : 2);  // blocks by their shared memory
-  cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
   cfg.blockDim = dim3(256);
   auto sums = [&](auto n, auto gr) {
     constexpr int N = decltype(n)::value, G = decltype(gr)::value;
-    const int ring = sum_smem(G, db);
+    const int ring = sum_smem(G, N, db);
+    const int resident = 152 * std::min(6, (227 << 10) / (ring + 1024));  // blocks by their shared memory
+    cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
     cfg.dynamicSmemBytes = ring;
     auto go = [&](auto k) {
       if (e == cudaSuccess && ring > 48 * 1024)

@@ -628,13 +628,13 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   // Threads a block: for many rows four chunks each (short rows then need no
   // more than a warp or two), else one; blocks a row: where the rows alone do
   // not fill the GPU twice over, as many as leave every thread a chunk, and
-  // larger blocks where even that does not.
+  // larger blocks (up to 1024 threads an SM) where even that does not.
   const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
   const int each = T >= 8 * sms ? 4 * chunk : chunk;
   int NT = 32, C = 1;
   while (NT < 128 && NT * each < V) NT *= 2;
   while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
-  if (C == kMaxCluster && T * C <= sms && V > C * NT * chunk) NT = kMaxThreads;
+  while (C == kMaxCluster && NT < kMaxThreads && 2 * NT * T * C <= 1024 * sms && V > C * NT * chunk) NT *= 2;
   // a block's vectors, at most, in chunks a thread; segments of G chunks
   const int vecs = V / (bf16 ? 8 : 4) / C + 1, chunks = (vecs + NT * kVecs - 1) / (NT * kVecs);
   const int G = (chunks + kSegs - 1) / kSegs;

@@ -111,6 +111,24 @@ def test_many_wide_rows(db, eb, T, V, h):
     _check_grad(from_dev(got), s, m, n, 1.0, eb)
 
 
+@pytest.mark.parametrize("T,V,h", [(3, 7, 1), (257, 60, 5), (5000, 900, 33), (33000, 4000, 517)])
+@pytest.mark.parametrize("db,eb", [(True, False), (True, True), (False, False)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_rows_of_odd_widths(off, db, eb, T, V, h):
+    """Rows that start anywhere, the first one an element past a boundary
+    too, NaN around the rows: only they are read."""
+    torch, mt = need_gpu()
+    rng = np.random.default_rng(T + off)
+    ids = _ids("skewed", T, V, rng).astype(np.int32)
+    flat = torch.full((T * h + off + 64,), float("nan"), device="cuda").to(torch.bfloat16 if db else torch.float32)
+    dout = flat[off:off + T * h].view(T, h)
+    dout.copy_(torch.randn((T, h), device="cuda"))
+    s, m, n = _reference(ids, from_dev(dout), V)
+    got = _grad(torch, mt, torch.from_numpy(ids).cuda(), dout, db, eb, 0.5, V)
+    _check_grad(from_dev(got), s, m, n, 0.5, eb)
+    assert np.all(from_dev(got)[n == 0] == 0)
+
+
 @pytest.mark.parametrize("V", [1 << 10, (1 << 10) - 1, 1 << 17, 151936, (1 << 20) + 3])
 def test_sort_over_the_vocabulary(V):
     """Vocabularies around the digits' borders, the largest ids in use: one
