@@ -126,7 +126,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 // completed by the next lane's words; only a row's first and last bytes go
 // one element at a time. The next lane has to hold the next unit, so a warp
 // then takes 28 units of its own and the first four (one scale block) of the
-// next warp's. (8192 x 14335 SwiGLU forward element by element: 680 us.)
+// next warp's. (SwiGLU 4690 x 8001: forward 174 us element by element, 86 us
+// so; backward 215 and 117 us.)
 // ---------------------------------------------------------------------------
 template <int WORDS>
 constexpr int block_bytes() { return WORDS == 2 ? 8 : 16; }

@@ -404,6 +404,14 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
     auto request = [&](int p, int slot) {
       if (p < pend) {
         const size_t base = row_of(p);
+        if (EB && N == 4 && a.add) {  // the table's row that the run is added to
+          const int id = __shfl_sync(kAll, p < 32 ? cur.x : fol.x, p & 31);
+          if ((heads >> p) & 1)
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k)
+              if (c0 + 32 * N * k < h && lane % 8 == 0)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"((const uint16_t*)a.dtable + (size_t)id * h + c0 + 32 * N * k));
+        }
 #pragma unroll
         for (int k = 0; k < kGroups; ++k)
           if (c0 + 32 * N * k < h) {
