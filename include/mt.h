@@ -533,8 +533,9 @@ int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd
 
 /* mt_op_rmsnorm_bwd that reads x from its 8-bit form (the formulas with x =
  * code * scale and the given rstd). resid may be null or equal dx, dx_bf16
- * may be null. workspace: mt_op_rmsnorm_bwd_ckpt8_workspace floats, 16-byte
- * aligned like w, dy, resid and dx (codes 4, dx_bf16 8). Deterministic. */
+ * may be null. workspace: mt_op_rmsnorm_bwd_ckpt8_workspace floats (0 for
+ * sizes the call refuses), 16-byte aligned like w, dy, resid and dx (codes 4,
+ * dx_bf16 8). Deterministic. */
 size_t mt_op_rmsnorm_bwd_ckpt8_workspace(int T, int h);
 int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, const float* w, const float* rstd,
                             const float* dy, const float* resid, float* dx, void* dx_bf16, float* dw,
@@ -572,9 +573,10 @@ int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, floa
 /* Its gradient: dlogits [T, V] (d_dtype, row stride ldd) =
  *   inv_temp * (g_logp ([j = id] - p_j) - g_entropy p_j (log p_j + entropy)),
  * p = e^{z - lse} (good to about 2^-24 |lse|: lse is fp32), for given g_logp
- * and g_entropy [T] (either may be null: zero); lse and entropy as the forward wrote them (entropy is read only with
- * g_entropy). Rows not scored and rows with nothing left get 0. dlogits may
- * be logits itself when type and stride are the same. */
+ * and g_entropy [T] (either may be null: zero); lse and entropy as the
+ * forward wrote them (entropy is read only with g_entropy). Rows not scored
+ * and rows with nothing left get 0. dlogits may be logits itself when type
+ * and stride are the same. */
 int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, float inv_temp, const float* lse,
                              const float* entropy, const float* g_logp, const float* g_entropy, void* dlogits,
                              int d_dtype, int T, int V, int ld, int ldd, void* stream);
@@ -587,7 +589,8 @@ int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, floa
 
 /* The table's gradient: dtable[v] = scale * sum of dout[t] over the t with
  * ids[t] = v, every row written (0 for unused ids); accumulate != 0: dtable
- * += that, rows of unused ids left as they are. Sums in fp32, in a fixed
+ * += that, rows of unused ids left as they are (added in memory: fp32
+ * subnormals there count as 0). Sums in fp32, in a fixed
  * order (ascending positions, long runs in pieces): deterministic. workspace:
  * mt_op_embed_bwd_workspace(T, V, h) bytes of device memory, 256-byte
  * aligned (0 for sizes the call refuses). Ids outside [0, V) as above. */

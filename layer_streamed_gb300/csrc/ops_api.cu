@@ -16,6 +16,11 @@ inline int rc(int r) {
   return cudaPeekAtLastError() != cudaSuccess ? MT_ERR_CUDA : MT_ERR_ARG;
 }
 inline bool f32_or_bf16(int dtype) { return dtype == MT_F32 || dtype == MT_BF16; }
+// Whether fp32 and int32 arrays lie on words (null does).
+template <class... P>
+bool on_words(P... p) {
+  return ((... | (uintptr_t)p) & 3) == 0;
+}
 size_t rup(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Carving of the mixture-of-experts workspace (byte offsets, 256-aligned).
 struct MoeWs {
@@ -359,19 +364,19 @@ int mt_op_ckpt8_unpack(const void* codes, const void* scales, int fmt, void* x, 
 
 int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd, void* codes, void* scales, int fmt,
                             int T, int h, float eps, void* stream) {
-  if (!x || !w || !y || !rstd || !codes || !scales) return MT_ERR_ARG;
+  if (!x || !w || !y || !rstd || !codes || !scales || !on_words(rstd)) return MT_ERR_ARG;
   return rc(rmsnorm_fwd_ckpt8(x, w, (uint16_t*)y, rstd, (uint8_t*)codes, (uint8_t*)scales, fmt, T, h, eps,
                               S(stream)));
 }
 
 size_t mt_op_rmsnorm_bwd_ckpt8_workspace(int T, int h) {
-  return T > 0 && h > 0 ? rmsnorm_bwd_ckpt8_partials(T, h) : 0;
+  return T > 0 && h > 0 && h % 4 == 0 && h <= 8192 ? rmsnorm_bwd_ckpt8_partials(T, h) : 0;
 }
 
 int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, const float* w, const float* rstd,
                             const float* dy, const float* resid, float* dx, void* dx_bf16, float* dw,
                             float* workspace, int T, int h, void* stream) {
-  if (!codes || !scales || !w || !rstd || !dy || !dx || !dw || !workspace) return MT_ERR_ARG;
+  if (!codes || !scales || !w || !rstd || !dy || !dx || !dw || !workspace || !on_words(rstd, dw)) return MT_ERR_ARG;
   return rc(rmsnorm_bwd_ckpt8((const uint8_t*)codes, (const uint8_t*)scales, fmt, w, rstd, dy, resid, dx,
                               (uint16_t*)dx_bf16, dw, workspace, T, h, S(stream)));
 }
@@ -393,7 +398,8 @@ int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const
 int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, float inv_temp, int k, float* lse,
                          float* logp, float* entropy, int32_t* top_ids, float* top_logp, int T, int V, int ld,
                          void* stream) {
-  if (!logits || !ids || !lse || !logp || !f32_or_bf16(dtype) || (k > 0 && (!top_ids || !top_logp)))
+  if (!logits || !ids || !lse || !logp || !f32_or_bf16(dtype) || (k > 0 && (!top_ids || !top_logp)) ||
+      !on_words(ids, lse, logp, entropy, top_ids, top_logp))
     return MT_ERR_ARG;
   return rc(token_logprobs(logits, dtype == MT_BF16, ids, inv_temp, k, lse, logp, entropy, top_ids, top_logp, T, V,
                            ld, S(stream)));
@@ -403,7 +409,7 @@ int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, 
                              const float* entropy, const float* g_logp, const float* g_entropy, void* dlogits,
                              int d_dtype, int T, int V, int ld, int ldd, void* stream) {
   if (!logits || !ids || !lse || !dlogits || (!g_logp && !g_entropy) || (g_entropy && !entropy) ||
-      !f32_or_bf16(dtype) || !f32_or_bf16(d_dtype))
+      !f32_or_bf16(dtype) || !f32_or_bf16(d_dtype) || !on_words(ids, lse, entropy, g_logp, g_entropy))
     return MT_ERR_ARG;
   return rc(token_logprobs_bwd(logits, dtype == MT_BF16, ids, inv_temp, lse, entropy, g_logp, g_entropy, dlogits,
                                d_dtype == MT_BF16, T, V, ld, ldd, S(stream)));
@@ -411,7 +417,7 @@ int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, 
 
 int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, float scale, void* out, int out_dtype,
                     int T, int V, int h, void* stream) {
-  if (!table || !ids || !out || !f32_or_bf16(table_dtype) || !f32_or_bf16(out_dtype)) return MT_ERR_ARG;
+  if (!table || !ids || !out || !f32_or_bf16(table_dtype) || !f32_or_bf16(out_dtype) || !on_words(ids)) return MT_ERR_ARG;
   return rc(embed_fwd(table, table_dtype == MT_BF16, ids, scale, out, out_dtype == MT_BF16, T, V, h, S(stream)));
 }
 
@@ -419,7 +425,8 @@ size_t mt_op_embed_bwd_workspace(int T, int V, int h) { return embed_bwd_workspa
 
 int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float scale, void* dtable, int dtable_dtype,
                     int accumulate, void* workspace, int T, int V, int h, void* stream) {
-  if (!ids || !dout || !dtable || !workspace || !f32_or_bf16(dout_dtype) || !f32_or_bf16(dtable_dtype))
+  if (!ids || !dout || !dtable || !workspace || !f32_or_bf16(dout_dtype) || !f32_or_bf16(dtable_dtype) ||
+      !on_words(ids))
     return MT_ERR_ARG;
   return rc(embed_bwd(ids, dout, dout_dtype == MT_BF16, scale, dtable, dtable_dtype == MT_BF16, accumulate != 0,
                       workspace, T, V, h, S(stream)));

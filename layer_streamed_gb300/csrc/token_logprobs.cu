@@ -50,8 +50,11 @@ __device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {
 struct Stat {
   float m, s, a;
 };
+// Distance of two maxima, kept where 2^d is 0 but d times a count is finite
+// (masked logits alone have the maximum -kBig and a count).
+__device__ __forceinline__ float apart(float x, float m, float c2) { return fmaxf((x - m) * c2, -1024.f); }
 __device__ __forceinline__ Stat merge(const Stat& x, const Stat& y, float c2) {
-  const float m = fmaxf(x.m, y.m), dx = (x.m - m) * c2, dy = (y.m - m) * c2;
+  const float m = fmaxf(x.m, y.m), dx = apart(x.m, m, c2), dy = apart(y.m, m, c2);
   const float ex = ex2(dx), ey = ex2(dy);
   return {m, x.s * ex + y.s * ey, (x.a + dx * x.s) * ex + (y.a + dy * y.s) * ey};
 }
@@ -69,7 +72,7 @@ constexpr uint32_t kKeyNone = ~0xf1800000u;  // key of -kBig: masked out, or not
 // The lanes' sets joined: one maximum, each lane's sums brought to it, then
 // plain sums in a fixed order.
 __device__ __forceinline__ Stat warp_join(Stat x, float c2) {
-  const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(x.m))), d = (x.m - m) * c2, e = ex2(d);
+  const float m = of_key(__reduce_max_sync(0xffffffffu, key_of(x.m))), d = apart(x.m, m, c2), e = ex2(d);
   x.a = (x.a + d * x.s) * e;
   x.s *= e;
 #pragma unroll
@@ -219,7 +222,7 @@ __device__ __forceinline__ float take(Run& r, uint4 (&u)[kVecs], float c2) {
     }
   }
   r.bad |= !(cm < kBig);
-  const float m = fmaxf(r.m, cm), d0 = (r.m - m) * c2, e0 = ex2(d0);
+  const float m = fmaxf(r.m, cm), d0 = apart(r.m, m, c2), e0 = ex2(d0);
   const uint64_t e02 = pair(e0, e0);
   r.a = mul2(fma2(pair(d0, d0), r.s, r.a), e02);
   r.s = mul2(r.s, e02);
@@ -530,7 +533,8 @@ template <bool BF16, bool OBF16, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
   constexpr int W = kBwdVecs * (BF16 ? 8 : 4);  // logits a thread holds at a time
-  const uint64_t cc = pair(a.c, a.c), ll = pair(kLog2e, kLog2e);
+  const float cs = a.c * -0x1p-8f;
+  const uint64_t ll = pair(-0x1p8f * kLog2e, -0x1p8f * kLog2e);
   const int unit = (int)(blockIdx.x * blockDim.x + threadIdx.x);
   for (int t = blockIdx.y * blockDim.y + threadIdx.y; t < a.T; t += gridDim.y * blockDim.y) {
     const int head = VEC ? (int)((8 - ((size_t)t * a.ld & 7)) & 7) : 0;  // a unit of 8 starts on every boundary
@@ -552,8 +556,8 @@ __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdA
     const float gl = a.g_logp ? a.g_logp[t] : 0.f, ge = a.g_ent ? a.g_ent[t] : 0.f;
     const float h = a.g_ent ? a.ent[t] : 0.f;
     // dz = c (gl [j = t] - p (gl + ge (log p + H)))
-    const float k0 = -a.c * (gl + ge * h), k1 = -a.c * ge;
-    const uint64_t kk0 = pair(k0, k0), kk1 = pair(k1, k1), nl = pair(-l, -l);
+    const float k0 = l == l ? -a.c * (gl + ge * h) : l, k1 = 0x1p8f * a.c * ge, ls = l * 0x1p-8f;
+    const uint64_t kk0 = pair(k0, k0), kk1 = pair(k1, k1);
     float g[W];
     if (zero) {
 #pragma unroll
@@ -562,30 +566,20 @@ __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdA
       float z[W];
       if (whole) {
 #pragma unroll
-        for (int i = 0; i < kBwdVecs; ++i) {
-          if (BF16) {
-            u[i].x = max_nan_bf2(u[i].x, kBigPair);
-            u[i].y = max_nan_bf2(u[i].y, kBigPair);
-            u[i].z = max_nan_bf2(u[i].z, kBigPair);
-            u[i].w = max_nan_bf2(u[i].w, kBigPair);
-          }
-          spread<BF16>(u[i], z + i * (W / kBwdVecs));
-        }
+        for (int i = 0; i < kBwdVecs; ++i) spread<BF16>(u[i], z + i * (W / kBwdVecs));
       } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
           z[i] = j + i >= 0 && j + i < a.V ? (BF16 ? bf2f(((const uint16_t*)zr)[j + i]) : ((const float*)zr)[j + i]) : 0.f;
       }
-      if (!BF16 || !whole) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) z[i] = max_nan(z[i], -kBig);  // keeps log p finite where p is 0
-      }
 #pragma unroll
       for (int i = 0; i < W; i += 2) {
-        const uint64_t lp = fma2(pair(z[i], z[i + 1]), cc, nl), x = mul2(lp, ll);  // log p, log2 p
+        // -log p / 256 within [0, 1]: p is 0 at the one end, and no product
+        // of its logarithm overflows; at the other, it is 1 at most
+        const uint64_t y = pair(__saturatef(fmaf(z[i], cs, ls)), __saturatef(fmaf(z[i + 1], cs, ls)));
         float x0, x1;
-        unpair(x, x0, x1);
-        unpair(mul2(pair(ex2(x0), ex2(x1)), fma2(kk1, lp, kk0)), g[i], g[i + 1]);
+        unpair(mul2(y, ll), x0, x1);  // log2 p
+        unpair(mul2(pair(ex2(x0), ex2(x1)), fma2(kk1, y, kk0)), g[i], g[i + 1]);
       }
       if ((unsigned)(id - j) < (unsigned)W) {
 #pragma unroll

@@ -198,6 +198,39 @@ def test_rows_left_out_and_extreme_logits():
     assert np.all(np.isfinite(d[[5, 10, 12, 13]]))
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("low", [-np.inf, -3.3e38, -2.0 ** 100])
+@pytest.mark.parametrize("c", [1e6, 4e4, 1e-6])
+def test_masked_stretches_at_the_temperatures_ends(c, low, bf16):
+    """Whole threads and warps of masked logits beside few live ones, at the
+    smallest and largest temperature: statistics as in float64, finite
+    gradients, none where the mask is."""
+    torch, mt = need_gpu()
+    T, V, k = 4, 70001, 3
+    z = np.full((T, V), low, np.float32)
+    z[0, 5], z[0, 69990] = 1.0, 1.0
+    z[1, :16] = 0.25
+    z[2, 35000:35002] = (-3.0, 2.0)
+    z[3, 70000] = -1e29
+    Z = torch.from_numpy(z).cuda().to(torch.bfloat16 if bf16 else torch.float32)
+    code = mt.MT_BF16 if bf16 else mt.MT_F32
+    ids = np.array([5, 3, 35001, 0], np.int32)
+    IDS, c64 = torch.from_numpy(ids).cuda(), float(np.float32(c))
+    o = _run(torch, mt, Z, code, IDS, c, k, T, V, V)
+    w = _reference(from_dev(Z), ids, c64, k)
+    _compare(o, w, k)
+    for gl, ge in ((1.0, 1e3), (0.0, 1.0)):
+        D = torch.full((T, V), 7.0, device="cuda")
+        GL, GE = torch.full((T,), gl, device="cuda"), torch.full((T,), ge, device="cuda")
+        mt.mt_op_token_logprobs_bwd(Z, code, IDS, c, o["lse"], o["ent"], GL, GE, D, mt.MT_F32, T, V, V, V)
+        d = from_dev(D).copy()
+        assert np.isfinite(d).all()
+        if gl:  # the given token's own term, where it is masked out itself
+            assert d[3, 0] == np.float32(c)
+            d[3, 0] = 0
+        assert np.all(d[~(from_dev(Z) > -BIG)] == 0)
+
+
 def test_ids_past_the_vocabulary_are_reported():
     torch, mt = need_gpu()
     V = 100

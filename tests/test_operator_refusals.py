@@ -44,7 +44,11 @@ def test_rmsnorm_ckpt8_refusals():
         _refused(lambda: mt.mt_op_rmsnorm_fwd_ckpt8(x, buf, buf, buf, buf, buf, fmt, T, h, 1e-5, 0))
         _refused(lambda: mt.mt_op_rmsnorm_bwd_ckpt8(buf, buf, fmt, buf, buf, x, None, buf, None, buf, buf, T, h, 0))
     _refused(lambda: mt.mt_op_rmsnorm_bwd_ckpt8(buf, buf, 1, buf, buf, buf, None, buf, None, buf, None, 1, 8, 0))
-    assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(0, 8) == 0
+    _refused(lambda: mt.mt_op_rmsnorm_fwd_ckpt8(buf, buf, buf, odd, buf, buf, 1, 1, 8, 1e-5, 0))
+    _refused(lambda: mt.mt_op_rmsnorm_bwd_ckpt8(buf, buf, 1, buf, odd, buf, None, buf, None, buf, buf, 1, 8, 0))
+    _refused(lambda: mt.mt_op_rmsnorm_bwd_ckpt8(buf, buf, 1, buf, buf, buf, None, buf, None, odd, buf, 1, 8, 0))
+    for T, h in ((0, 8), (1, 0), (1, 6), (1, 8196), (1, 1 << 20), (-1, 8), (1, -8)):
+        assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, h) == 0
     assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(1, 8) >= 8
 
 
@@ -59,14 +63,16 @@ def test_token_logprobs_refusals():
     ok = dict(z=buf, dt=F, ids=buf, c=1.0, k=2, lse=buf, logp=buf, ti=buf, tl=buf, T=2, V=8, ld=8)
     bad = [dict(z=None), dict(ids=None), dict(lse=None), dict(logp=None), dict(ti=None), dict(tl=None), dict(dt=2),
            dict(c=0.0), dict(c=-1.0), dict(c=float("nan")), dict(c=float("inf")), dict(k=-1), dict(k=9), dict(k=33, V=64, ld=64),
-           dict(T=0), dict(V=0), dict(ld=7), dict(z=odd)]
+           dict(T=0), dict(V=0), dict(ld=7), dict(z=odd), dict(ids=odd), dict(lse=odd), dict(logp=odd), dict(ti=odd),
+           dict(tl=odd)]
     for b in bad:
         a = {**ok, **b}
         _refused(lambda: mt.mt_op_token_logprobs(a["z"], a["dt"], a["ids"], a["c"], a["k"], a["lse"], a["logp"], None,
                                                  a["ti"], a["tl"], a["T"], a["V"], a["ld"], 0))
     ok = dict(z=buf, dt=F, ids=buf, c=1.0, lse=buf, ent=buf, gl=buf, ge=buf, dz=buf, ddt=B, T=2, V=8, ld=8, ldd=8)
     bad = [dict(z=None), dict(ids=None), dict(lse=None), dict(ent=None), dict(gl=None, ge=None), dict(dz=None),
-           dict(dt=2), dict(ddt=3), dict(c=0.0), dict(T=0), dict(V=0), dict(ld=7), dict(ldd=7), dict(dz=odd)]
+           dict(dt=2), dict(ddt=3), dict(c=0.0), dict(T=0), dict(V=0), dict(ld=7), dict(ldd=7), dict(dz=odd),
+           dict(ids=odd), dict(lse=odd), dict(ent=odd), dict(gl=odd), dict(ge=odd)]
     for b in bad:
         a = {**ok, **b}
         _refused(lambda: mt.mt_op_token_logprobs_bwd(a["z"], a["dt"], a["ids"], a["c"], a["lse"], a["ent"], a["gl"],
@@ -75,7 +81,7 @@ def test_token_logprobs_refusals():
 
 def test_embedding_refusals():
     for a in (dict(t=None), dict(i=None), dict(o=None), dict(dt=2), dict(od=7), dict(T=0), dict(V=0), dict(h=0),
-              dict(t=odd), dict(T=(1 << 28) + 1), dict(V=1 << 30)):
+              dict(t=odd), dict(i=odd), dict(o=odd), dict(T=(1 << 28) + 1), dict(V=1 << 30)):
         a = {**dict(t=buf, i=buf, o=buf, dt=F, od=F, T=2, V=3, h=4), **a}
         _refused(lambda: mt.mt_op_embed_fwd(a["t"], a["dt"], a["i"], 1.0, a["o"], a["od"], a["T"], a["V"], a["h"], 0))
         _refused(lambda: mt.mt_op_embed_bwd(a["i"], a["t"], a["dt"], 1.0, a["o"], a["od"], 0, buf, a["T"], a["V"],
