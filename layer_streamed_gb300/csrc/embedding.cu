@@ -699,7 +699,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
     cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
     cfg.dynamicSmemBytes = ring;
     auto go = [&](auto k) {
-      if (e == cudaSuccess && ring > 48 * 1024)
+      if (e == cudaSuccess && ring > 47 * 1024)
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
       if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, b);
     };

@@ -7,6 +7,10 @@ output, the logits' gradient: RMS 2^-9.8 each, into the logits and from there
 into every gradient), held to the step's bar of rel-L2 2e-2. Captured into a
 graph, on other streams and side by side the operators give the same bits.
 """
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 
@@ -164,3 +168,29 @@ def test_chains_side_by_side_on_other_streams():
     torch.cuda.synchronize()
     assert _same(torch, a.outputs(), want[0]) and _same(torch, b.outputs(), want[1])
     assert mt.mt_op_device_error() == 0
+
+
+FIRST_CALLS = {
+    "norm": "mt.mt_op_rmsnorm_bwd_ckpt8(c, c, 2, x, x, x, x, y, None, y[-h:], ws, 77, h)",
+    "norm_no_residual": "mt.mt_op_rmsnorm_bwd_ckpt8(c, c, 1, x, x, x, None, y, None, y[-h:], ws, 777, 2 * h)",
+    "logp": "mt.mt_op_token_logprobs(x, 1, ids, 1.0, 32, y, y[9:], None, ids[64:], y[64:], 1, 151936, 151936)",
+    "embed": "mt.mt_op_embed_bwd(ids, x, 1, 1.0, y, 0, 0, ws, 17000, 100, h)",
+    "embed_odd": "mt.mt_op_embed_bwd(ids, x, 0, 1.0, y, 1, 0, ws, 2000, 100, h + 1)",
+}
+
+
+@pytest.mark.parametrize("call", sorted(FIRST_CALLS))
+def test_first_call_of_a_process(call):
+    """A kernel's shared memory is asked for by the call that needs it, not
+    by an earlier one of another size."""
+    need_gpu()
+    code = ("import torch, layer_streamed_gb300 as mt\n"
+            "h, z = 1024, lambda n, t=torch.float32: torch.zeros(n, dtype=t, device='cuda')\n"
+            "x, y, ws = z(20 << 20), z(20 << 20), z(20 << 20)\n"
+            "c, ids = z(4 << 20, torch.uint8), z(1 << 20, torch.int32)\n"
+            f"{FIRST_CALLS[call]}\n"
+            "torch.cuda.synchronize()\n"
+            "assert mt.mt_op_device_error() == 0 and bool(torch.isfinite(y).all())\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
