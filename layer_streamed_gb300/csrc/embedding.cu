@@ -478,21 +478,22 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
     }
   }
 
-  // what is left to clear, a few rows at a time
+  // what is left to clear, a few rows (32 at most) at a time: every warp's
+  // first ones by its number, so that only a second turn waits for the counter
+  // (8192 tokens of 128256 x 4096: 479 us with 16 KB at a time, 321 with 32,
+  // 331 with 128)
   if (a.clear_rows == 0) return;
   constexpr int esz = EB ? 2 : 4;
-  auto ticket = [&] { return lane == 0 ? atomicAdd(a.ctl + 1, 1) : 0; };
-  const int end = (a.V - a.clear_row0 + a.clear_rows - 1) / a.clear_rows;
-  int next = ticket();
-  while (true) {
-    const int k = __shfl_sync(kAll, next, 0);
-    if (k >= end) break;
-    next = ticket();  // on its way during the stores
-    const int v_lo = a.clear_row0 + k * a.clear_rows, v_hi = min(a.V, v_lo + a.clear_rows);
-    for (int v = v_lo; v < v_hi; ++v) {
-      if (a.used[v]) continue;
-      uint8_t* row = (uint8_t*)a.dtable + (size_t)v * h * esz;
+  const int warps = gridDim.x * 8, end = (a.V - a.clear_row0 + a.clear_rows - 1) / a.clear_rows;
+  int next = blockIdx.x + gridDim.x * (int)warp_id();
+  while (next < end) {
+    const int v_lo = a.clear_row0 + next * a.clear_rows, n = min(a.clear_rows, a.V - v_lo);
+    if (end > warps && lane == 0) next = warps + atomicAdd(a.ctl + 1, 1);  // on its way during the stores
+    uint32_t rows = __ballot_sync(kAll, lane < n && !a.used[v_lo + min(lane, n - 1)]);
+    for (; rows; rows &= rows - 1) {
+      uint8_t* row = (uint8_t*)a.dtable + (size_t)(v_lo + __ffs(rows) - 1) * h * esz;
       if (N == 4) {
+#pragma unroll 4
         for (int c = lane; c < h / 4; c += 32) {
           if (EB) ((uint2*)row)[c] = make_uint2(0, 0);
           else ((uint4*)row)[c] = make_uint4(0, 0, 0, 0);
@@ -501,6 +502,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
         for (int c = lane; c < h; c += 32) store1<EB>(row, c, 0.f);
       }
     }
+    if (end <= warps) break;
+    next = __shfl_sync(kAll, next, 0);
   }
 }
 
@@ -682,7 +685,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   b.add = add ? 1 : 0;
   b.words = al(dout, 4) ? 1 : 0;
   b.clear_row0 = first;
-  b.clear_rows = a.used ? (int)std::max<size_t>(1, 32768 / row) : 0;
+  b.clear_rows = a.used ? (int)std::min<size_t>(32, std::max<size_t>(1, 32768 / row)) : 0;
   // launched while the step before ends; they wait for it themselves
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
