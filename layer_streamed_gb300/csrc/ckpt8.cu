@@ -336,10 +336,11 @@ __device__ __forceinline__ uint32_t amax_bf16x8(const uint32_t (&w)[4]) {
 constexpr int kRows = 4;
 
 template <int FMT, bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* x, uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales, int T, int n, int ldx, int ldc,
                                                          int nb) {
   constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
+  grid_wait();
   bool own;
   const int u = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -368,10 +369,11 @@ __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* __restrict_
 }
 
 template <int FMT, bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, void* __restrict__ x,
+__global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* codes,
+                                                           const uint8_t* scales, void* __restrict__ x,
                                                            int T, int n, int ldc, int ldx, int nb) {
   constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
+  grid_wait();
   bool own;
   const int u = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -414,10 +416,11 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* __rest
 // 38.9, four columns a unit 41.2.
 template <int FMT, int NT, int V, bool VEC>
 __global__ void __launch_bounds__(NT)
-    rmsnorm_fwd_ckpt8_kernel(const float* __restrict__ x, const float* __restrict__ w, uint16_t* __restrict__ y,
+    rmsnorm_fwd_ckpt8_kernel(const float* x, const float* w, uint16_t* __restrict__ y,
                              float* __restrict__ rstd, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                              int h, int nb, float eps) {
   __shared__ float red[NT / 32];
+  grid_wait();
   const size_t t = blockIdx.x;
   const float* xr = x + t * h;
   const int tid = threadIdx.x;
@@ -533,9 +536,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 template <int FMT, int V>
 __global__ void __launch_bounds__(kBwdMaxThreads)
-    rmsnorm_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                             const float* __restrict__ w, const float* __restrict__ rstd,
-                             const float* __restrict__ dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
+    rmsnorm_bwd_ckpt8_kernel(const uint8_t* codes, const uint8_t* scales,
+                             const float* w, const float* rstd,
+                             const float* dy, const float* resid, float* dx, uint16_t* __restrict__ dxb,
                              float* __restrict__ part, int T, int h, int nb, int stages) {
   extern __shared__ __align__(128) uint8_t stage[];  // [stages]: dy, resid of a row
   __shared__ float red[2][kBwdMaxThreads / 32];
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
     fence_barrier_init();
   }
   __syncthreads();
+  grid_wait();
   if (tid == 0)
     for (int s = 0; s < stages - 1; ++s) request(blockIdx.x + s * gridDim.x, s);
   float4 acc[V], wv[V];
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
       phase ^= 1;
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (*(volatile int*)&abort_flag) {  // a wait ran out: give the copies in flight time to land
     for (int k = 0; k < stages - 1; ++k) {
       for (int spin = 0; spin < (1 << 20) && !mbar_try_wait(smem_u32(&full[st]), phase); ++spin) {
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kBwdMaxThreads)
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int nparts, int n,
                                                          float* __restrict__ out) {
   __shared__ float red[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
@@ -704,11 +708,12 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
 constexpr int kSwRows = 2;
 
 template <int FMT, bool VEC>
-__global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t* __restrict__ gu,
+__global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t* gu,
                                                                   uint16_t* __restrict__ act,
                                                                   uint8_t* __restrict__ codes,
                                                                   uint8_t* __restrict__ scales, int T, int F, int ld,
                                                                   int nb) {
+  grid_wait();
   bool own;
   const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -760,11 +765,12 @@ __global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t
 
 // dg = dact u silu'(g), du = dact silu(g), with g and u from the 8-bit form.
 template <int FMT, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* __restrict__ codes,
-                                                               const uint8_t* __restrict__ scales,
-                                                               const uint16_t* __restrict__ dact,
+__global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* codes,
+                                                               const uint8_t* scales,
+                                                               const uint16_t* dact,
                                                                uint16_t* __restrict__ dgu, int T, int F, int ld,
                                                                int nb) {
+  grid_wait();
   bool own;
   const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -857,7 +863,7 @@ int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scale
   // whole loads and stores of eight values where every row starts on their boundary
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
-  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(x, codes, scales, T, n, ldx, ldc, nb); };
+  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, x, codes, scales, T, n, ldx, ldc, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
     else vec ? go(ckpt8_pack_kernel<FMT_I8, false, true>) : go(ckpt8_pack_kernel<FMT_I8, false, false>);
@@ -874,7 +880,7 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
   const int nb = blocks32(n);
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
-  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, x, T, n, ldc, ldx, nb); };
+  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, x, T, n, ldc, ldx, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
     else vec ? go(ckpt8_unpack_kernel<FMT_I8, false, true>) : go(ckpt8_unpack_kernel<FMT_I8, false, false>);
@@ -893,7 +899,7 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
   const int units = (h + 7) / 8, nb = blocks32(h);
   // whole units where every row starts on a 32-byte boundary, else their halves
   const bool vec = h % 8 == 0 && al(x, 32) && al(y, 16) && al(codes, 8);
-  auto go = [&](auto k, int threads) { k<<<T, threads, 0, st>>>(x, w, y, rstd, codes, scales, h, nb, eps); };
+  auto go = [&](auto k, int threads) { mt_host::launch_early(k, T, threads, 0, st, 1, x, w, y, rstd, codes, scales, h, nb, eps); };
   auto pick = [&](auto f, auto v) {
     constexpr int F = decltype(f)::value;
     constexpr bool X = decltype(v)::value;
@@ -924,8 +930,8 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
     if (smem > 47 * 1024)  // with the static part past the default limit
       ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) == cudaSuccess;
     if (ok)
-      k<<<shape.parts, shape.threads, smem, st>>>(codes, scales, w, rstd, dy, resid, dx, dx_bf16, work, T, h, nb,
-                                                  shape.stages);
+      ok = mt_host::launch_early(k, shape.parts, shape.threads, smem, st, 1, codes, scales, w, rstd, dy, resid, dx,
+                                 dx_bf16, work, T, h, nb, shape.stages) == cudaSuccess;
   };
   auto pick = [&](auto f) {
     constexpr int F = decltype(f)::value;
@@ -935,16 +941,9 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
   if (!ok) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((h + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, sum_parts_kernel, (const float*)work, shape.parts, h, dw) != cudaSuccess) return -1;
+  if (mt_host::launch_early(sum_parts_kernel, (h + 31) / 32, 1024, 0, st, 1, (const float*)work, shape.parts, h, dw) !=
+      cudaSuccess)
+    return -1;
   return done(2);
 }
 
@@ -953,7 +952,7 @@ int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t*
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return -1;
   const bool vec = ld % 8 == 0 && al(gu, 16) && al(act, 16) && al(codes, 8);
   const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
-  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(gu, act, codes, scales, T, F, ld, blocks32(F)); };
+  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, gu, act, codes, scales, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_fwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, false>);
   return done(1);
@@ -964,7 +963,7 @@ int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return -1;
   const bool vec = ld % 8 == 0 && al(dact, 16) && al(dgu, 16) && al(codes, 8);
   const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
-  auto go = [&](auto k) { k<<<s.grid, s.block, 0, st>>>(codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
+  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_bwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, false>);
   return done(1);

@@ -396,6 +396,13 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// First in a kernel launched by mt_host::launch_early: waits until the
+// launches before it are done and their writes visible (its inputs are then
+// ordinary loads: no __restrict__ const pointers, whose loads may move up).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next launch_early begin once every block has come here.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -416,4 +423,24 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, c
                       const uint64_t* gdim, const uint64_t* gstride_bytes, const uint32_t* box,
                       CUtensorMapSwizzle swz);
 int num_sms();
+
+// A launch whose blocks may start while the kernel before it on the stream
+// ends (each begins with grid_wait), in clusters of `cluster` blocks.
+template <class K, class... A>
+cudaError_t launch_early(K k, dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
 }  // namespace mt_host

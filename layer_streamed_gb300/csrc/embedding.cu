@@ -92,9 +92,10 @@ __device__ __forceinline__ void accumulate(void* p, size_t i, const float4& v) {
 constexpr int kFwdRows = 4;
 
 template <bool TB, bool OB, int N>
-__global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__ table,
-                                                        const int32_t* __restrict__ ids, float scale,
+__global__ void __launch_bounds__(256) embed_fwd_kernel(const void* table,
+                                                        const int32_t* ids, float scale,
                                                         void* __restrict__ out, int T, int V, int h) {
+  grid_wait();
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * N;
   if (c >= h) return;
   const int step = gridDim.y * blockDim.y;
@@ -198,7 +199,8 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the block's totals [bins]
   __shared__ uint32_t scratch[kSortWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums wait for this launch's end themselves
+  grid_release();  // the sums wait for this launch's end themselves
+  grid_wait();
   const int ctas = a.ctas;
   if ((int)blockIdx.x >= ctas) {
     clear_share(a.clear, a.clear_bytes, (int)blockIdx.x - ctas);
@@ -349,8 +351,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];  // [warp][D][G][lane]: sum_part bytes
   uint8_t* mine_ring = ring + ((int)warp_id() * D * G * 32 + (int)lane_id()) * kPart;
   const int lane = (int)lane_id(), h = a.h;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_wait();
+  grid_release();
   const int ranges = (a.T + a.L - 1) / a.L, jobs = ranges * a.chunks;
   for (int job = blockIdx.x * 8 + (int)warp_id(); job < jobs; job += gridDim.x * 8) {
     const int j = job / a.chunks, chunk = job - j * a.chunks, lo = j * a.L;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
 template <bool EB, int N>
 __global__ void __launch_bounds__(1024) embed_long_kernel(SumArgs a, int CX) {
   __shared__ float4 share[1024];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   const int x = (int)threadIdx.x & (CX - 1), g = (int)threadIdx.x / CX, groups = 1024 / CX;
   const int c = ((int)blockIdx.y * CX + x) * N, h = a.h, n = a.ctl[0];
   for (int r = blockIdx.x; r < n; r += gridDim.x) {
@@ -605,7 +607,7 @@ int embed_fwd(const void* table, bool tb, const int32_t* ids, float scale, void*
   const int by = 256 / bx;
   const dim3 block((unsigned)bx, (unsigned)by);
   const dim3 grid((unsigned)((units + bx - 1) / bx), (unsigned)std::min((T + by * kFwdRows - 1) / (by * kFwdRows), 65535));
-  auto go = [&](auto k) { k<<<grid, block, 0, st>>>(table, ids, scale, out, T, V, h); };
+  auto go = [&](auto k) { mt_host::launch_early(k, grid, block, 0, st, 1, table, ids, scale, out, T, V, h); };
   auto pick = [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (tb) ob ? go(embed_fwd_kernel<true, true, N>) : go(embed_fwd_kernel<true, false, N>);
@@ -652,21 +654,8 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
     return -1;
   const size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
   a.ctas = T <= kSortOne ? 1 : kSortCtas;
-  cudaError_t e = cudaSuccess;
-  {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.ctas + (clearers + a.ctas - 1) / a.ctas * a.ctas));
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.ctas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.ctas > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
-  }
+  const dim3 sorters((unsigned)(a.ctas + (clearers + a.ctas - 1) / a.ctas * a.ctas));
+  cudaError_t e = mt_host::launch_early(embed_sort_kernel, sorters, kSortThreads, smem, st, a.ctas, a);
 
   SumArgs b;
   b.s = (a.passes & 1) ? a.a : a.b;
@@ -686,25 +675,15 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   b.words = al(dout, 4) ? 1 : 0;
   b.clear_row0 = first;
   b.clear_rows = a.used ? (int)std::min<size_t>(32, std::max<size_t>(1, 32768 / row)) : 0;
-  // launched while the step before ends; they wait for it themselves
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(256);
   auto sums = [&](auto n, auto gr) {
     constexpr int N = decltype(n)::value, G = decltype(gr)::value;
     const int ring = sum_smem(G, N, db);
     const int resident = 152 * std::min(6, (227 << 10) / (ring + 1024));  // blocks by their shared memory
-    cfg.gridDim = dim3((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
-    cfg.dynamicSmemBytes = ring;
+    const dim3 grid((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
     auto go = [&](auto k) {
       if (e == cudaSuccess && ring > 47 * 1024)
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
-      if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, b);
+      if (e == cudaSuccess) e = mt_host::launch_early(k, grid, 256, ring, st, 1, b);
     };
     if (db) eb ? go(embed_sum_kernel<true, true, N, G>) : go(embed_sum_kernel<true, false, N, G>);
     else eb ? go(embed_sum_kernel<false, true, N, G>) : go(embed_sum_kernel<false, false, N, G>);
@@ -718,14 +697,12 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (T > kShort) {
     int CX = 32;
     while (CX < units && CX < 256) CX *= 2;
-    cfg.gridDim = dim3((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + CX - 1) / CX));
-    cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = 0;
+    const dim3 grid((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + CX - 1) / CX));
     auto longs = [&](auto n) {
       constexpr int N = decltype(n)::value;
-      if (e == cudaSuccess)
-        e = eb ? cudaLaunchKernelEx(&cfg, embed_long_kernel<true, N>, b, CX)
-               : cudaLaunchKernelEx(&cfg, embed_long_kernel<false, N>, b, CX);
+      if (e != cudaSuccess) return;
+      e = eb ? mt_host::launch_early(embed_long_kernel<true, N>, grid, 1024, 0, st, 1, b, CX)
+             : mt_host::launch_early(embed_long_kernel<false, N>, grid, 1024, 0, st, 1, b, CX);
     };
     if (vec) longs(std::integral_constant<int, 4>());
     else longs(std::integral_constant<int, 1>());

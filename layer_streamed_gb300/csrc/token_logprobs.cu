@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     for (int j = 0; j < kVecs; ++j)
       u[j] = v + j * NT < v_hi ? __ldcs(row.vec(v + j * NT)) : make_uint4(none, none, none, none);
   };
+  grid_wait();
   // the first chunk is requested before the row's token is known: their
   // latencies overlap
   uint4 next[kVecs];
@@ -533,6 +534,7 @@ template <bool BF16, bool OBF16, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
   constexpr int W = kBwdVecs * (BF16 ? 8 : 4);  // logits a thread holds at a time
+  grid_wait();
   const float cs = a.c * -0x1p-8f;
   const uint64_t ll = pair(-0x1p8f * kLog2e, -0x1p8f * kLog2e);
   const int unit = (int)(blockIdx.x * blockDim.x + threadIdx.x);
@@ -636,29 +638,14 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   FwdArgs a{z, ids, lse, logp, ent, top_logp, top_ids, T, V, ld, k, c, C, G, cap, segs};
   Smem unused;
   const size_t smem = smem_layout(nullptr, NT, C, k, cap, segs, &unused);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(T * C));
-  cfg.blockDim = dim3((unsigned)NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = C > 1 ? 1 : 0;
-  cfg.dynamicSmemBytes = smem;
   cudaError_t e = cudaSuccess;
   if (smem > 47 * 1024)  // with the static part past the default limit
     e = cudaFuncSetAttribute(bf16 ? token_logprobs_kernel<true, true> : token_logprobs_kernel<false, true>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
   if (e != cudaSuccess) return -1;
-  if (k > 0)
-    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, true>, a)
-             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, true>, a);
-  else
-    e = bf16 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<true, false>, a)
-             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<false, false>, a);
+  auto go = [&](auto f) { e = mt_host::launch_early(f, T * C, NT, smem, st, C, a); };
+  if (k > 0) bf16 ? go(token_logprobs_kernel<true, true>) : go(token_logprobs_kernel<false, true>);
+  else bf16 ? go(token_logprobs_kernel<true, false>) : go(token_logprobs_kernel<false, false>);
   count_launches(1);
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
@@ -678,7 +665,7 @@ int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, co
   const int by = kBwdThreads / bx;
   const dim3 block((unsigned)bx, (unsigned)by);
   const dim3 grid((unsigned)((units + bx - 1) / bx), (unsigned)std::min((T + by - 1) / by, 65535));
-  auto go = [&](auto k) { k<<<grid, block, 0, st>>>(a); };
+  auto go = [&](auto k) { mt_host::launch_early(k, grid, block, 0, st, 1, a); };
   auto pick = [&](auto v) {
     constexpr bool X = decltype(v)::value;
     if (bf16) dz_bf16 ? go(token_logprobs_bwd_kernel<true, true, X>) : go(token_logprobs_bwd_kernel<true, false, X>);
