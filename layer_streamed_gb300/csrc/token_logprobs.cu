@@ -106,7 +106,8 @@ __device__ __forceinline__ uint32_t warp_merge(uint32_t a, uint32_t b, uint32_t 
   return key;
 }
 
-constexpr int kMaxThreads = 512;
+constexpr int kOneThreads = 128;  // a block alone with a row, at most
+constexpr int kMaxThreads = 512;  // one of a cluster
 constexpr int kVecs = 4;  // 16-byte vectors a thread holds at a time
 constexpr int kMaxCluster = 8;
 constexpr int kSegs = 32;
@@ -114,7 +115,9 @@ constexpr int kSegs = 32;
 // A block's shared memory. cap: logits that may reach the bound before the
 // slow search takes over.
 struct Smem {
-  uint2 *cand, *list;  // [cap]; [C * k], k of each block, best first (the first block's is used)
+  uint2* cand;         // [cap]
+  uint64_t* list;      // [C * k] key and ~index: k of each block, best first (the first block's is used)
+  int* place;          // [C * k] places of the entries, where there are several blocks
   Stat* stat;          // [C * warps] (the first block's)
   uint32_t* key;       // [warps][32]
   float* seg;          // [segments][threads]
@@ -132,7 +135,8 @@ __host__ __device__ inline size_t smem_layout(uint8_t* base, int NT, int C, int 
   m.stat = (Stat*)take((size_t)C * nw * sizeof(Stat));
   if (k > 0) {
     m.cand = (uint2*)take((size_t)cap * 8);
-    m.list = (uint2*)take((size_t)C * k * 8);
+    m.list = (uint64_t*)take((size_t)C * k * 8);
+    m.place = (int*)take(C > 1 ? (size_t)C * k * 4 : 0);
     m.key = (uint32_t*)take((size_t)nw * 128);
     m.seg = (float*)take((size_t)segs * NT * 4);
     m.hot = (uint16_t*)take((size_t)cap * 2);
@@ -245,6 +249,24 @@ __device__ __forceinline__ float take(Run& r, uint4 (&u)[kVecs], float c2) {
   return cm;
 }
 
+// An entry's place is the number of entries before it: all compared with all,
+// the threads beyond one an entry sharing the comparisons out (halving in
+// each block's list took 4600 cycles for 8 x 20 entries, this 2400).
+__device__ __forceinline__ void places(const uint64_t* list, int* place, int n) {
+  const int tid = (int)threadIdx.x, NT = (int)blockDim.x;
+  const int wide = (n + 31) & ~31, shares = max(1, NT / wide), g = shares > 1 ? tid / wide : 0;
+  const int lo = n * g / shares, hi = n * (g + 1) / shares;
+  if (g >= shares) return;
+  for (int i = tid - g * wide; i < n; i += NT) {
+    const uint64_t e = list[i];
+    int before = 0;
+#pragma unroll 8
+    for (int j = lo; j < hi; ++j) before += list[j] > e ? 1 : 0;
+    if (shares > 1) atomicAdd(&place[i], before);
+    else place[i] = before;
+  }
+}
+
 // Forward. A cluster of C blocks a row (C = 1 for many rows; more where the
 // rows alone would leave SMs idle), each over its part of the row's vectors;
 // the blocks' results are joined in the first one's shared memory.
@@ -259,13 +281,17 @@ __device__ __forceinline__ float take(Run& r, uint4 (&u)[kVecs], float c2) {
 // 128256 fp32 rows (828 against 598 us without a list), and reading all of
 // the k best threads' logits again 137 us more, since DRAM moves 64 bytes for
 // every 16 of them.
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) {
+// ONE: a block a row (a.C = 1). Blocks an SM, by the registers a thread gets:
+// 4095 x 151936 bf16 with the 8 largest 211 us unbounded, 203 with nine, 199
+// with eight, 188 with seven, 191 with six; clusters (64 x 128256) 8.1 us
+// unbounded, 6.9 with two of the largest block.
+template <bool BF16, bool TOP, bool ONE>
+__global__ void __launch_bounds__(ONE ? kOneThreads : kMaxThreads, ONE ? 7 : 2) token_logprobs_kernel(FwdArgs a) {
   using R = RowView<BF16>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ uint32_t sh_kth;
   __shared__ int sh_bad, sh_nhot, sh_n;
-  const int C = a.C, G = a.G, cap = a.cap;
+  const int C = ONE ? 1 : a.C, G = a.G, cap = a.cap;
   const int t = blockIdx.x / C, rank = blockIdx.x % C;
   const uint32_t lane = lane_id(), warp = warp_id();
   const int tid = (int)threadIdx.x, NT = (int)blockDim.x, nw = NT >> 5;
@@ -304,6 +330,8 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     return;
   }
   if (tid == 0) sh_bad = 0, sh_nhot = 0, sh_n = 0;
+  if (TOP && C > 1)
+    for (int i = tid; i < C * a.k; i += NT) sm.place[i] = 0;
   // every block's shared memory is set up before another one writes to it
   // (waited for just before the first such write)
   if (C > 1) {
@@ -411,9 +439,10 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
     if (end >= 0) offer(row.at(end), end);
     __syncthreads();
     const int found = sh_n, n = max(found, nhot);  // too many segments count as too many logits
-    auto list = [&](int place, uint2 e) {
-      put(&sm.list[rank * a.k + place].x, e.x);
-      put(&sm.list[rank * a.k + place].y, e.y);
+    auto list = [&](int place, uint2 e) {  // empty entries follow the others, in an order of their own
+      uint32_t* to = (uint32_t*)&sm.list[rank * a.k + place];
+      put(to, ~(e.x > kKeyNone ? e.y : 0x80000000u + (uint32_t)(rank * a.k + place)));
+      put(to + 1, e.x);
     };
     if (n <= cap) {
       for (int i = tid; i < found; i += NT) {
@@ -477,36 +506,19 @@ __global__ void __launch_bounds__(kMaxThreads) token_logprobs_kernel(FwdArgs a) 
   }
   if (TOP) {
     const int n = C * a.k;
-    auto write = [&](int place, uint2 e) {
-      const bool there = e.x > kKeyNone && !broken;
-      a.top_ids[(size_t)t * a.k + place] = there ? (int32_t)e.y : -1;
-      a.top_logp[(size_t)t * a.k + place] = there ? logp_of(of_key(e.x)) : broken ? nan : -INFINITY;
+    auto write = [&](int place, uint64_t e) {
+      const uint32_t key = (uint32_t)(e >> 32);
+      const bool there = key > kKeyNone && !broken;
+      a.top_ids[(size_t)t * a.k + place] = there ? (int32_t)~(uint32_t)e : -1;
+      a.top_logp[(size_t)t * a.k + place] = there ? logp_of(of_key(key)) : broken ? nan : -INFINITY;
     };
     if (C == 1) {
       if (tid < a.k) write(tid, sm.list[tid]);
     } else {
-      // an entry's place: for every block's list, the number of its entries
-      // that come before (found by halving: the lists are sorted; empty
-      // entries follow the others, by block and place)
-      int* place = (int*)sm.cand;
-      for (int i = tid; i < n; i += NT) place[i] = 0;
-      __syncthreads();
-      for (int q = tid; q < n * C; q += NT) {
-        const int i = q / C, b = q % C;
-        const uint2 e = sm.list[i];
-        int lo = 0, hi = a.k;
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2, j = b * a.k + mid;
-          const uint2 g = sm.list[j];
-          const bool first = g.x > e.x || (g.x == e.x && (g.y < e.y || (g.y == e.y && j < i)));
-          if (first) lo = mid + 1;
-          else hi = mid;
-        }
-        if (lo) atomicAdd(&place[i], lo);
-      }
+      places(sm.list, sm.place, n);
       __syncthreads();
       for (int i = tid; i < n; i += NT)
-        if (place[i] < a.k) write(place[i], sm.list[i]);
+        if (sm.place[i] < a.k) write(sm.place[i], sm.list[i]);
     }
   }
 }
@@ -628,7 +640,7 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
   const int each = T >= 8 * sms ? 4 * chunk : chunk;
   int NT = 32, C = 1;
-  while (NT < 128 && NT * each < V) NT *= 2;
+  while (NT < kOneThreads && NT * each < V) NT *= 2;
   while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
   while (C == kMaxCluster && NT < kMaxThreads && 2 * NT * T * C <= 1024 * sms && V > C * NT * chunk) NT *= 2;
   // a block's vectors, at most, in chunks a thread; segments of G chunks
@@ -639,13 +651,18 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   Smem unused;
   const size_t smem = smem_layout(nullptr, NT, C, k, cap, segs, &unused);
   cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024)  // with the static part past the default limit
-    e = cudaFuncSetAttribute(bf16 ? token_logprobs_kernel<true, true> : token_logprobs_kernel<false, true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
-  if (e != cudaSuccess) return -1;
-  auto go = [&](auto f) { e = mt_host::launch_early(f, T * C, NT, smem, st, C, a); };
-  if (k > 0) bf16 ? go(token_logprobs_kernel<true, true>) : go(token_logprobs_kernel<false, true>);
-  else bf16 ? go(token_logprobs_kernel<true, false>) : go(token_logprobs_kernel<false, false>);
+  auto go = [&](auto f) {
+    if (smem > 47 * 1024)  // with the static part past the default limit
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    if (e == cudaSuccess) e = mt_host::launch_early(f, T * C, NT, smem, st, C, a);
+  };
+  auto pick = [&](auto one) {
+    constexpr bool X = decltype(one)::value;
+    if (k > 0) bf16 ? go(token_logprobs_kernel<true, true, X>) : go(token_logprobs_kernel<false, true, X>);
+    else bf16 ? go(token_logprobs_kernel<true, false, X>) : go(token_logprobs_kernel<false, false, X>);
+  };
+  if (C == 1) pick(std::true_type());
+  else pick(std::false_type());
   count_launches(1);
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
