@@ -194,3 +194,77 @@ def test_first_call_of_a_process(call):
     r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
                        text=True, timeout=120)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_from_copies_fills_and_other_streams(captured):
+    """Kernels that may begin early still wait for whatever wrote their
+    inputs: a copy, a fill, a library kernel, another stream's event, and the
+    operator before them; what they write is waited for in turn."""
+    torch, mt = need_gpu()
+    T, n = 4096, 2048
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rounds = [torch.randn((T, n), device="cuda", generator=g) for _ in range(3)]
+    x, back = torch.empty((T, n), device="cuda"), torch.empty((T, n), device="cuda")
+    y = torch.empty((T, n), device="cuda")
+    codes, scales = (torch.empty(s, dtype=torch.uint8, device="cuda") for s in ((T, n), (T, n // 32)))
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    lse, logp = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    side, outs = torch.cuda.Stream(), [torch.empty((T, n), device="cuda") for _ in range(4)]
+
+    def pack_unpack(out):
+        mt.mt_op_ckpt8_pack(x, mt.MT_F32, 1, codes, scales, T, n, n, n)
+        mt.mt_op_ckpt8_unpack(codes, scales, 1, back, mt.MT_F32, T, n, n, n)
+        out.copy_(back)  # a copy reads what the operator writes; the next round writes it again
+
+    def issue():
+        main = torch.cuda.current_stream()
+        for r, out in zip(rounds, outs):
+            x.copy_(r)
+            pack_unpack(out)
+        x.zero_()
+        mt.mt_op_token_logprobs(x, mt.MT_F32, ids, 1.0, 0, lse, logp, None, None, None, T, n, n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.mul(rounds[0], 3.0, out=y)
+            for _ in range(20):
+                y.add_(rounds[1])
+        main.wait_stream(side)
+        mt.mt_op_ckpt8_pack(y, mt.MT_F32, 2, codes, scales, T, n, n, n)
+        mt.mt_op_ckpt8_unpack(codes, scales, 2, back, mt.MT_F32, T, n, n, n)
+        outs[3].copy_(back)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        warm = torch.cuda.Stream()
+        with torch.cuda.stream(warm):
+            issue()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            issue()
+        run = graph.replay
+    else:
+        run = issue
+    z = rounds[0] * 3.0
+    for _ in range(20):
+        z.add_(rounds[1])
+    want = []
+    for r, fmt in [(q, 1) for q in rounds] + [(z, 2)]:
+        torch.cuda.synchronize()
+        w = torch.empty((T, n), device="cuda")
+        mt.mt_op_ckpt8_pack(r, mt.MT_F32, fmt, codes, scales, T, n, n, n)
+        torch.cuda.synchronize()
+        mt.mt_op_ckpt8_unpack(codes, scales, fmt, w, mt.MT_F32, T, n, n, n)
+        torch.cuda.synchronize()
+        want.append(w)
+    for _ in range(10):
+        for o in outs:
+            o.fill_(7.0)
+        lse.fill_(7.0)
+        run()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+        assert np.allclose(from_dev(lse), np.log(n), rtol=0, atol=2e-6)  # S = n exactly; ln n to a few units of 2^-22
+    assert mt.mt_op_device_error() == 0
