@@ -19,6 +19,7 @@
 // (223) 225, 64 of 32000 x 1024 fp32 (19.3) 23.5; where nothing hides the sort,
 // 8192 of 1000 x 4096 (22) 45 us. Lookup: 8192 rows of 4096 28 us.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -124,9 +125,10 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* table,
 }
 
 // ---------------------------------------------------------------------------
-// Sort: one cluster of eight blocks of 32 warps (one block for few positions,
-// where the barriers between blocks cost more than the work: 1266 positions
-// 7.5 us in eight blocks). Every warp owns a
+// Sort: one cluster of eight blocks of 32 warps, or one block for few
+// positions, where the barriers between blocks cost more than the work (a
+// gradient added to 32000 x 192: 300 positions 9.4 us by one block, 10.7 by the
+// cluster; 4096 17.9 and 13.5). Every warp owns a
 // contiguous part of the positions; a pass counts its digits per warp, turns
 // the counts into offsets (digit, then block, then warp: a stable order) with
 // one scan over the cluster, and walks its part again to place its keys (equal
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* table,
 // 78 us for 131072 positions, counting with it included).
 // ---------------------------------------------------------------------------
 constexpr int kSortCtas = 8;
-constexpr int kSortOne = 4096;  // positions that one block sorts alone
+constexpr int kSortOne = 1024;  // positions that one block sorts alone
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 10;  // bits: 32 warps x 1024 counters in shared memory
@@ -149,6 +151,7 @@ struct SortArgs {
   void* clear;       // the part of the table's gradient to clear here
   size_t clear_bytes;
   int T, V, passes, digit, ctas;
+  int warps;  // of a block that take positions (and have counters)
 };
 
 // One block's share of clearing: 16-byte stores, 2-byte ones at the ends.
@@ -200,7 +203,7 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
-  extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the block's totals [bins]
+  extern __shared__ uint32_t cnt[];  // [warps][bins], then the block's totals [bins]
   __shared__ uint32_t scratch[kSortWarps];
   grid_release();  // the sums wait for this launch's end themselves
   grid_wait();
@@ -210,10 +213,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
     return;
   }
   const int bins = 1 << a.digit;
-  uint32_t* tot = cnt + kSortWarps * bins;
+  const int W = a.warps;
+  uint32_t* tot = cnt + W * bins;
   const uint32_t rank = ctas > 1 ? cluster_rank() : 0u, warp = warp_id(), lane = lane_id(), below_mask = (1u << lane) - 1;
   const int tid = threadIdx.x;
-  uint32_t* mine = cnt + warp * bins;
+  uint32_t* mine = cnt + warp * bins;  // a warp past W has no positions
   if (rank == 0 && tid < 2) a.ctl[tid] = 0;
   auto sync_all = [&] {  // what the cluster's blocks have written is visible to all of them
     if (ctas > 1) cluster_sync();
@@ -227,10 +231,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
   }
 
   // the warp's part: whole groups of 32 positions
-  const int groups = (a.T + 31) / 32, all = ctas * kSortWarps;
-  const int wid = (int)rank * kSortWarps + (int)warp;
+  const int groups = (a.T + 31) / 32, all = ctas * W;
+  const int wid = (int)rank * W + (int)warp;
   const int lo = (int)((int64_t)groups * wid / all) * 32;
-  const int hi = min(a.T, (int)((int64_t)groups * (wid + 1) / all) * 32);
+  const int hi = (int)warp < W ? min(a.T, (int)((int64_t)groups * (wid + 1) / all) * 32) : lo;
 
   for (int p = 0; p < a.passes; ++p) {
     const int2* src = p == 0 ? nullptr : (p & 1) ? a.a : a.b;
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
       return make_int2(off ? a.V : id, i);
     };
     int2 next = key_at(lo + (int)lane);
-    for (int i = tid; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+    for (int i = tid; i < W * bins; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
     for (int i = lo; i < hi; i += 32) {
       const bool on = i + (int)lane < hi;
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
     uint32_t own = 0;
     if (tid < bins) {
 #pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) own += cnt[w * bins + tid];
+      for (int w = 0; w < W; ++w) own += cnt[w * bins + tid];
       tot[tid] = own;
     }
     uint32_t before = 0, total = own;
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
     if (tid < bins) {
       uint32_t at = base + before;
 #pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const uint32_t x = cnt[w * bins + tid];
         cnt[w * bins + tid] = at;
         at += x;
@@ -651,12 +655,20 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   while ((V >> bits) != 0) ++bits;  // keys 0..V
   a.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   a.digit = (bits + a.passes - 1) / a.passes;
-  const int smem = ((kSortWarps + 1) << a.digit) * 4;
+  a.ctas = T <= kSortOne ? 1 : kSortCtas;
+  // Every warp more has 2^digit counters that are gone over four times a pass,
+  // every group of 32 positions more is some hundred cycles of a warp's walk:
+  // the groups a warp takes where the sum of both is least (1266 positions of
+  // 884 rows 11.4 us with all warps, 10.5 so; 64 of 151936 10.2 and 8.7)
+  const int groups = ((T + 31) / 32 + a.ctas - 1) / a.ctas;
+  const double least = std::sqrt(groups * 8000.0 / (1 << a.digit));  // warps
+  const int each = (int)std::lround(std::max(1.0, groups / least));
+  a.warps = std::min(kSortWarps, (groups + each - 1) / each);
+  const int smem = ((a.warps + 1) << a.digit) * 4;
   if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ((kSortWarps + 1) << kMaxDigit) * 4) != cudaSuccess)
     return -1;
   const size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
-  a.ctas = T <= kSortOne ? 1 : kSortCtas;
   const dim3 sorters((unsigned)(a.ctas + (clearers + a.ctas - 1) / a.ctas * a.ctas));
   cudaError_t e = mt_host::launch_early(embed_sort_kernel, sorters, kSortThreads, smem, st, a.ctas, a);
 
