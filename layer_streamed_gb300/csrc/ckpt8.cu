@@ -126,8 +126,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 // completed by the next lane's words; only a row's first and last bytes go
 // one element at a time. The next lane has to hold the next unit, so a warp
 // then takes 28 units of its own and the first four (one scale block) of the
-// next warp's. (SwiGLU 4690 x 8001: forward 174 us element by element, 86 us
-// so; backward 215 and 117 us.)
+// next warp's. (SwiGLU 4690 x 8001: forward 174 us element by element, 74 us
+// so; backward 215 and 87 us.)
 // ---------------------------------------------------------------------------
 template <int WORDS>
 constexpr int block_bytes() { return WORDS == 2 ? 8 : 16; }
@@ -332,15 +332,17 @@ __device__ __forceinline__ uint32_t amax_bf16x8(const uint32_t (&w)[4]) {
 // Pack and unpack. A thread owns one unit of eight values in each of kRows
 // rows (their loads are in flight together); a 2D block covers blockDim.x
 // units of blockDim.y rows at a time, so narrow matrices still fill a block.
-// Measured for 8192 x 4096 fp32 (floor 24.7 us): pack 25.2 us, unpack 26.4;
-// 14783 x 777 (8.5): 16.6 and 14.6, the shifting of ragged rows.
+// Measured for 8192 x 4096 fp32 (floor 24.7 us): pack 25.1 us, unpack 26.6;
+// ragged 14783 x 777 (8.5): 12.6 with two rows a thread, 14.8 and 12.9 with
+// four; four are the faster for whole rows of bf16 (unpack 13.8, 14.5 us).
 // ---------------------------------------------------------------------------
-constexpr int kRows = 4;
+constexpr int pk_rows(bool vec) { return vec ? 4 : 2; }
 
 template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_pack_kernel(const void* x, uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales, int T, int n, int ldx, int ldc,
                                                          int nb) {
+  constexpr int kRows = pk_rows(VEC);
   constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
   grid_wait();
   bool own;
@@ -374,6 +376,7 @@ template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* codes,
                                                            const uint8_t* scales, void* __restrict__ x,
                                                            int T, int n, int ldc, int ldx, int nb) {
+  constexpr int kRows = pk_rows(VEC);
   constexpr int W = BF16 ? 4 : 8, esz = BF16 ? 2 : 4;
   grid_wait();
   bool own;
@@ -415,10 +418,11 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* codes,
 // row in registers, four neighbouring lanes hold a block of 32 columns.
 // ---------------------------------------------------------------------------
 // Measured at 8192 x 4096 (floor 34.5 us): 256 threads 37.8 us, 128 threads
-// 38.9, four columns a unit 41.2; launched early, 256 threads take 35.6 (e4m3)
-// to 37.7 (int8).
+// 38.9, four columns a unit 41.2; with the SM's 2048 threads and launched early
+// 36.0, 512 threads of one unit 38.6. 4096 x 8192: 36.6, 256 threads of four
+// units 38.3.
 template <int FMT, int NT, int V, bool VEC>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 2048 / NT)
     rmsnorm_fwd_ckpt8_kernel(const float* x, const float* w, uint16_t* __restrict__ y,
                              float* __restrict__ rstd, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                              int h, int nb, float eps) {
@@ -689,9 +693,11 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int 
 // cut into blocks of 32 separately. A thread owns 8 columns of g and the
 // same 8 of u, four lanes a block.
 // HBM bounds whole rows (8192 x 14336, floor 139 us each way: forward 139-140
-// us, backward 145; with exact divisions and single maxima 242 and 243), the
-// issue of instructions ragged ones (4690 x 8001, floor 44: 86 and 117 us).
-// Two rows a thread: more loads in flight, still five blocks an SM (forward).
+// us, backward 137-139; with exact divisions and single maxima 242 and 243),
+// the issue of instructions ragged ones (4690 x 8001, floor 44: 74 and 87 us).
+// Whole rows: two a thread, five blocks an SM forward, six backward (146 us
+// with the four that its registers allowed). Ragged: one row, eight blocks
+// (two rows at five and four: 85 and 118 us).
 // ---------------------------------------------------------------------------
 // 1 / (1 + e^-g) of two values with the hardware's exponential and
 // reciprocal (the exact division and the subnormal range of both cost more
@@ -712,15 +718,16 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
   unpair(v, a, b);
   return pack_bf2(a, b);
 }
-constexpr int kSwRows = 2;
+constexpr int sw_rows(bool vec) { return vec ? 2 : 1; }
 
 template <int FMT, bool VEC>
-__global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t* gu,
+__global__ void __launch_bounds__(256, VEC ? 5 : 8) swiglu_fwd_ckpt8_kernel(const uint16_t* gu,
                                                                   uint16_t* __restrict__ act,
                                                                   uint8_t* __restrict__ codes,
                                                                   uint8_t* __restrict__ scales, int T, int F, int ld,
                                                                   int nb) {
   grid_wait();
+  constexpr int kSwRows = sw_rows(VEC);
   bool own;
   const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -772,12 +779,13 @@ __global__ void __launch_bounds__(256, 5) swiglu_fwd_ckpt8_kernel(const uint16_t
 
 // dg = dact u silu'(g), du = dact silu(g), with g and u from the 8-bit form.
 template <int FMT, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_bwd_ckpt8_kernel(const uint8_t* codes,
+__global__ void __launch_bounds__(256, VEC ? 6 : 8) swiglu_bwd_ckpt8_kernel(const uint8_t* codes,
                                                                const uint8_t* scales,
                                                                const uint16_t* dact,
                                                                uint16_t* __restrict__ dgu, int T, int F, int ld,
                                                                int nb) {
   grid_wait();
+  constexpr int kSwRows = sw_rows(VEC);
   bool own;
   const int x = unit_of<VEC>(blockIdx.x * blockDim.x + threadIdx.x, own);
   const int step = gridDim.y * blockDim.y;
@@ -869,7 +877,7 @@ int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scale
   const int nb = blocks32(n);
   // whole loads and stores of eight values where every row starts on their boundary
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
-  const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
+  const Shape2 s = shape2(T, (n + 7) / 8, pk_rows(vec), vec);
   auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, x, codes, scales, T, n, ldx, ldc, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
@@ -886,7 +894,7 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
   if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
   const int nb = blocks32(n);
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
-  const Shape2 s = shape2(T, (n + 7) / 8, kRows, vec);
+  const Shape2 s = shape2(T, (n + 7) / 8, pk_rows(vec), vec);
   auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, x, T, n, ldc, ldx, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
@@ -913,7 +921,7 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
     if (units <= 128) go(rmsnorm_fwd_ckpt8_kernel<F, 128, 1, X>, 128);
     else if (units <= 256) go(rmsnorm_fwd_ckpt8_kernel<F, 256, 1, X>, 256);
     else if (units <= 512) go(rmsnorm_fwd_ckpt8_kernel<F, 256, 2, X>, 256);
-    else go(rmsnorm_fwd_ckpt8_kernel<F, 256, 4, X>, 256);
+    else go(rmsnorm_fwd_ckpt8_kernel<F, 512, 2, X>, 512);
   };
   auto pick_f = [&](auto f) { vec ? pick(f, std::true_type()) : pick(f, std::false_type()); };
   if (fmt == FMT_I8) pick_f(std::integral_constant<int, FMT_I8>());
@@ -958,7 +966,7 @@ int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t*
                      int ld, cudaStream_t st) {
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return -1;
   const bool vec = ld % 8 == 0 && al(gu, 16) && al(act, 16) && al(codes, 8);
-  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
+  const Shape2 s = shape2(T, (ld + 7) / 8, sw_rows(vec), vec);
   auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, gu, act, codes, scales, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_fwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, false>);
@@ -969,7 +977,7 @@ int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const
                      int T, int F, int ld, cudaStream_t st) {
   if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return -1;
   const bool vec = ld % 8 == 0 && al(dact, 16) && al(dgu, 16) && al(codes, 8);
-  const Shape2 s = shape2(T, (ld + 7) / 8, kSwRows, vec);
+  const Shape2 s = shape2(T, (ld + 7) / 8, sw_rows(vec), vec);
   auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_bwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, false>);
