@@ -12,10 +12,10 @@
 // Both directions are bound by reading the logits (and writing the gradient)
 // where there are many; 16-bit logits come close to the issue rate too, so
 // maxima and clamps are taken on packed pairs and sums on pairs of fp32.
-// Measured: 8192 x 128256 fp32 (floor 618 us) forward 580-590 us, with the 8
-// largest 598, gradient 1160 (floor 1236); 4095 x 151936 bf16 (183 and 366)
-// 177, 188 and 355. A few rows are bound by latency: one of 151936 4.8 us, with
-// its 20 largest 9.3.
+// Measured: 8192 x 128256 fp32 (floor 618 us) forward 576-587 us, with the 8
+// largest 589-599, gradient 1160 (floor 1236); 4095 x 151936 bf16 (183 and 366)
+// 174-177, 184-188 and 355; 4096 x 32000 bf16 (39) 41 and 49. A few rows are
+// bound by latency: one of 151936 4.8 us, with its 20 largest 9.4.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -637,12 +637,14 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   if (T <= 0 || V <= 0 || ld < V || k < 0 || k > kMaxTop || k > V || !(c >= kMinScale) || !(c <= kMaxScale) ||
       ((uintptr_t)z & (bf16 ? 1 : 3)) || T > (1 << 28))
     return -1;
-  // Threads a block: for many rows four chunks each (short rows then need no
-  // more than a warp or two), else one; blocks a row: where the rows alone do
-  // not fill the GPU twice over, as many as leave every thread a chunk, and
-  // larger blocks (up to 1024 threads an SM) where even that does not.
+  // Threads a block: the more rows, the more chunks each, so that a short row
+  // needs no more than a warp or two (4227 x 12722 bf16 with the 8 largest: 37
+  // us with four chunks each, 26 with sixteen; 2200 rows 21, 18 with eight);
+  // else one. Blocks a row: where the rows alone do not fill the GPU twice over,
+  // as many as leave every thread a chunk, and larger blocks (up to 1024 threads
+  // an SM) where even that does not.
   const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
-  const int each = T >= 8 * sms ? 4 * chunk : chunk;
+  const int each = T >= 16 * sms ? 16 * chunk : T >= 8 * sms ? 8 * chunk : chunk;
   int NT = 32, C = 1;
   while (NT < kOneThreads && NT * each < V) NT *= 2;
   while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
