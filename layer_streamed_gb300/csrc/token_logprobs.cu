@@ -255,17 +255,21 @@ __device__ __forceinline__ float take(Run& r, uint4 (&u)[kVecs], float c2) {
 
 // An entry's place is the number of entries before it: all compared with all,
 // the threads beyond one an entry sharing the comparisons out (halving in
-// each block's list took 4600 cycles for 8 x 20 entries, this 2400).
+// each block's list took 4600 cycles for 8 x 20 entries, single comparisons
+// 2400; two at a time 62 x 27089 with the 32 largest 15.6 -> 14.8 us).
 __device__ __forceinline__ void places(const uint64_t* list, int* place, int n) {
   const int tid = (int)threadIdx.x, NT = (int)blockDim.x;
   const int wide = (n + 31) & ~31, shares = max(1, NT / wide), g = shares > 1 ? tid / wide : 0;
-  const int lo = n * g / shares, hi = n * (g + 1) / shares;
+  const int pairs = n / 2, lo = pairs * g / shares, hi = pairs * (g + 1) / shares;  // n is even
   if (g >= shares) return;
   for (int i = tid - g * wide; i < n; i += NT) {
     const uint64_t e = list[i];
     int before = 0;
 #pragma unroll 8
-    for (int j = lo; j < hi; ++j) before += list[j] > e ? 1 : 0;
+    for (int j = lo; j < hi; ++j) {
+      const ulonglong2 f = ((const ulonglong2*)list)[j];
+      before += (f.x > e ? 1 : 0) + (f.y > e ? 1 : 0);
+    }
     if (shares > 1) atomicAdd(&place[i], before);
     else place[i] = before;
   }
@@ -641,14 +645,17 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   // needs no more than a warp or two (4227 x 12722 bf16 with the 8 largest: 37
   // us with four chunks each, 26 with sixteen; 2200 rows 21, 18 with eight);
   // else one. Blocks a row: where the rows alone do not fill the GPU twice over,
-  // as many as leave every thread a chunk, and larger blocks (up to 1024 threads
-  // an SM) where even that does not.
+  // as many as leave every thread a chunk (two or four where lists are to be
+  // joined: 141 x 7935 bf16 with the 8 largest 7.2 us with one, 5.4 with two; 62 x
+  // 27089 fp32 with 20 10.6 and 8.4 with four), and larger blocks (up to 512
+  // threads an SM: 64 x 128256 bf16 5.7 us, 6.6 with 1024) where even that does
+  // not.
   const int chunk = kVecs * (bf16 ? 8 : 4), sms = mt_host::num_sms();
   const int each = T >= 16 * sms ? 16 * chunk : T >= 8 * sms ? 8 * chunk : chunk;
   int NT = 32, C = 1;
   while (NT < kOneThreads && NT * each < V) NT *= 2;
-  while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk) C *= 2;
-  while (C == kMaxCluster && NT < kMaxThreads && 2 * NT * T * C <= 1024 * sms && V > C * NT * chunk) NT *= 2;
+  while (C < kMaxCluster && (int64_t)T * C < 2 * sms && V > C * NT * chunk * (k > 8 ? 4 : k ? 2 : 1)) C *= 2;
+  while (C == kMaxCluster && NT < kMaxThreads && 2 * NT * T * C <= 512 * sms && V > C * NT * chunk) NT *= 2;
   // a block's vectors, at most, in chunks a thread; segments of G chunks
   const int vecs = V / (bf16 ? 8 : 4) / C + 1, chunks = (vecs + NT * kVecs - 1) / (NT * kVecs);
   const int G = (chunks + kSegs - 1) / kSegs;

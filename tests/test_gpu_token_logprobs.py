@@ -231,6 +231,37 @@ def test_masked_stretches_at_the_temperatures_ends(c, low, bf16):
         assert np.all(d[~(from_dev(Z) > -BIG)] == 0)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,V,k", [(1, 151936, 20), (2, 32000, 32), (40, 9000, 8), (5, 40003, 1), (300, 30000, 20)])
+@pytest.mark.parametrize("pattern", ["soft_mask", "half", "ascending", "descending", "plateau", "stretch", "stripes"])
+def test_uneven_rows(pattern, T, V, k, bf16):
+    """Rows whose largest logits sit together, or whose threads and warps see
+    nothing but low ones: bounds on the k-th largest that the threads' maxima
+    give are far off there."""
+    torch, mt = need_gpu()
+    rng = np.random.default_rng(V + k)
+    z = rng.standard_normal((T, V)).astype(np.float32)
+    i = np.arange(V)
+    if pattern == "soft_mask":
+        z[:, (i < V // 3) | (i > V // 3 + 200)] -= 1e9
+    elif pattern == "half":
+        z[:, :V // 2] = -np.inf
+    elif pattern == "ascending":
+        z = np.broadcast_to(i / 1000, (T, V)).astype(np.float32)
+    elif pattern == "descending":
+        z = np.broadcast_to(-i / 1000, (T, V)).astype(np.float32)
+    elif pattern == "plateau":
+        z = np.where(rng.random((T, V)) < 0.02, 3, rng.integers(-3, 3, (T, V))).astype(np.float32)
+    elif pattern == "stretch":
+        z[:, V // 2:V // 2 + 700] += 20
+    else:
+        z[:, (i // 1024) % 3 != 1] -= 50
+    Z = torch.from_numpy(np.ascontiguousarray(z)).cuda().to(torch.bfloat16 if bf16 else torch.float32)
+    ids = rng.integers(0, V, T).astype(np.int32)
+    o = _run(torch, mt, Z, mt.MT_BF16 if bf16 else mt.MT_F32, torch.from_numpy(ids).cuda(), 1.0, k, T, V, V)
+    _compare(o, _reference(from_dev(Z), ids, 1.0, k), k)
+
+
 def test_ids_past_the_vocabulary_are_reported():
     torch, mt = need_gpu()
     V = 100
