@@ -1281,7 +1281,7 @@ int layer_forward(Step& st, int l, const LayerView& w, bool recompute) {
   cudaStream_t s = ctx->s_comp;
   const int b8 = ckpt8_of(st, l), fmt = ctx->cfg.ckpt_format;
   // (packed beside the norm, not by its fused form, whose sums run in another
-  // order: the forward stays bitwise that of fp32 checkpoints for 27 us a
+  // order: the forward stays bitwise that of fp32 checkpoints for 25 us a
   // block at T = 8192, h = 4096)
   if (b8 >= 0 && recompute)
     CKL(ckpt8_unpack(ckpt8_codes(ctx, b8), ckpt8_scales(ctx, b8), fmt, x, false, T, h, h, h, s));
