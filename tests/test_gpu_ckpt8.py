@@ -142,6 +142,9 @@ def test_every_code_unpacks():
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T,h,with_res,with_bf", [(1, 4, False, True), (5, 36, True, False), (77, 320, True, True),
+                                                  (16, 96, True, True), (17, 3200, True, True), (65, 1024, False, False),
+                                                  (128, 2048, True, True), (128, 3204, True, False), (129, 96, True, True),
+                                                  (1, 3200, True, True), (100, 3200, True, True),
                                                   (45, 1800, False, True), (700, 64, True, True),
                                                   (33, 4096, True, True), (9, 6000, True, False),
                                                   (500, 8192, True, True), (3, 2052, False, False), (400, 7452, True, True),
