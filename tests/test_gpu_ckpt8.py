@@ -331,3 +331,79 @@ def test_swiglu_non_finite_block_is_nan_in_the_gradient():
     assert nan[0, :32].all() and nan[0, F:F + 32].all() and not nan[0, 32:F].any()
     assert nan[1, 32:F].all() and not nan[1, :32].any()  # dg needs u; du of that block does not
     assert not nan[1, F:].any()
+
+
+@pytest.fixture
+def emptied():
+    """Gives the large buffers back to the device."""
+    yield
+    import torch
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("ld", [1 << 29, (1 << 29) - 3])
+def test_row_offsets_past_32_bits(emptied, ld):
+    """Rows 2^29 elements apart (element offsets to 2^31, byte offsets to
+    2^32): the same bits as the rows close together."""
+    torch, mt = need_gpu()
+    T, n, bf = 5, 1000, torch.bfloat16
+    x = torch.randn((T, n), device="cuda").to(bf)
+    small = torch.empty((T, n), dtype=torch.uint8, device="cuda"), torch.empty((T, 32), dtype=torch.uint8, device="cuda")
+    mt.mt_op_ckpt8_pack(x, mt.MT_BF16, 1, *small, T, n, n, n)
+    far = torch.empty(((T - 1) * ld + n,), dtype=bf, device="cuda").as_strided((T, n), (ld, 1))
+    far.copy_(x)
+    codes = torch.empty(((T - 1) * ld + n,), dtype=torch.uint8, device="cuda").as_strided((T, n), (ld, 1))
+    scales = torch.empty((T, 32), dtype=torch.uint8, device="cuda")
+    mt.mt_op_ckpt8_pack(far, mt.MT_BF16, 1, codes, scales, T, n, ld, ld)
+    assert torch.equal(codes, small[0]) and torch.equal(scales, small[1])
+    want, back = torch.empty_like(x), far.zero_()
+    mt.mt_op_ckpt8_unpack(*small, 1, want, mt.MT_BF16, T, n, n, n)
+    mt.mt_op_ckpt8_unpack(codes, scales, 1, back, mt.MT_BF16, T, n, ld, ld)
+    assert torch.equal(back, want)
+
+
+def test_swiglu_row_offsets_past_32_bits(emptied):
+    torch, mt = need_gpu()
+    T, F, ld, bf = 3, 300, 1 << 29, torch.bfloat16
+    g, u, d = (torch.randn((T, F), device="cuda").to(bf) for _ in range(3))
+
+    def run(ld):
+        e = lambda n, dt: torch.empty((T, n), dtype=dt, device="cuda")  # noqa: E731
+        gu, dact = e(2 * ld, bf), e(ld, bf)
+        gu[:, :F], gu[:, ld:ld + F], dact[:, :F] = g, u, d
+        act, codes, scales = e(ld, bf), e(2 * ld, torch.uint8), e(20, torch.uint8)
+        mt.mt_op_swiglu_fwd_ckpt8(gu, act, codes, scales, 2, T, F, ld)
+        mt.mt_op_swiglu_bwd_ckpt8(codes, scales, 2, dact, gu, T, F, ld)  # over g|u, which it does not read
+        return (act[:, :F].clone(), codes[:, :F].clone(), codes[:, ld:ld + F].clone(), scales, gu[:, :F].clone(),
+                gu[:, ld:ld + F].clone(), act[:, F:F + 4].clone(), act[:, ld - 4:].clone(), gu[:, -4:].clone())
+
+    for a, b in zip(run(F + 4), run(ld)):  # the last three are padding
+        assert torch.equal(a, b)
+
+
+def test_norm_of_more_than_2_to_32_values(emptied):
+    """The last rows of 4.3e9 values: the bits of the same rows alone."""
+    torch, mt = need_gpu()
+    T, h, last = (1 << 19) + 11, 8192, 40
+    x, dy = torch.empty((T, h), device="cuda"), torch.empty((T, h), device="cuda")
+    x[-last:], dy[-last:] = torch.randn((last, h), device="cuda"), torch.randn((last, h), device="cuda")
+    x[:-last], dy[:-last] = 1.0, 0.0
+    w = torch.randn(h, device="cuda")
+
+    def run(x, dy):
+        T = x.shape[0]
+        e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+        y, r = e(T, h, dt=torch.bfloat16), e(T)
+        codes, scales = e(T, h, dt=torch.uint8), e(T, h // 32, dt=torch.uint8)
+        mt.mt_op_rmsnorm_fwd_ckpt8(x, w, y, r, codes, scales, 1, T, h, 1e-5)
+        dx, dxb, dw = e(T, h), e(T, h, dt=torch.bfloat16), e(h)
+        ws = e(mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, h))
+        mt.mt_op_rmsnorm_bwd_ckpt8(codes, scales, 1, w, r, dy, None, dx, dxb, dw, ws, T, h)
+        return [t[-last:].clone() for t in (y, r, codes, scales, dx, dxb)] + [dw]
+
+    far, near = run(x, dy), run(x[-last:].clone(), dy[-last:].clone())
+    for a, b in zip(far[:-1], near[:-1]):
+        assert torch.equal(a, b)
+    # dw: the other rows add nothing; up to 40 terms in another order
+    bound = acc(last) * (dy[-last:].abs() * x[-last:].abs() * near[1][:, None]).sum(0)
+    assert bool(((far[-1] - near[-1]).abs() <= 2 * bound + 1e-30).all())

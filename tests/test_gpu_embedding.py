@@ -214,3 +214,32 @@ def test_full_size_gradient():
     for v in (0, 1, 2, int(used[len(used) // 2]), V - 1):
         rows = from_dev(dout[IDS == v]).astype(np.float64)
         check(from_dev(g[v]), rows.sum(axis=0), (acc(len(rows)) + 2 * U32) * np.abs(rows).sum(axis=0), f"row {v}")
+
+
+@pytest.fixture
+def emptied():
+    """Gives the large buffers back to the device."""
+    yield
+    import torch
+    torch.cuda.empty_cache()
+
+
+def test_more_than_2_to_32_values_of_rows(emptied):
+    """1.1 million rows of 4096: lookup, and whole-number gradients whose sums are exact."""
+    torch, mt = need_gpu()
+    T, V, h = 1_100_003, 53, 4096
+    ids = torch.randint(0, V, (T,), device="cuda").int()
+    table = torch.randn((V, h), device="cuda").to(torch.bfloat16)
+    out = torch.empty((T, h), dtype=torch.bfloat16, device="cuda")
+    mt.mt_op_embed_fwd(table, mt.MT_BF16, ids, 1.0, out, mt.MT_BF16, T, V, h)
+    for lo in (0, T // 2, T - 1000):
+        assert torch.equal(out[lo:lo + 1000], table[ids[lo:lo + 1000].long()])
+    t = (torch.arange(T, device="cuda") % 7).to(torch.bfloat16)
+    c = (torch.arange(h, device="cuda") % 3).to(torch.bfloat16)
+    out.copy_(t[:, None]).add_(c[None])
+    ws = torch.empty(mt.mt_op_embed_bwd_workspace(T, V, h), dtype=torch.uint8, device="cuda")
+    dE = torch.empty((V, h), device="cuda")
+    mt.mt_op_embed_bwd(ids, out, mt.MT_BF16, 1.0, dE, mt.MT_F32, 0, ws, T, V, h)
+    n = torch.bincount(ids.long(), minlength=V).double()
+    s = torch.bincount(ids.long(), weights=t.double(), minlength=V)
+    assert torch.equal(dE.double(), s[:, None] + n[:, None] * c.double()[None])

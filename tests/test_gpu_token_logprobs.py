@@ -390,3 +390,30 @@ def test_full_size_rows_sampled():
         want = -np.exp(lp) * float(g[t])
         want[int(ids[t])] += float(g[t])
         check(from_dev(D[t]), want, (U16 + 2.0 ** -20) * np.abs(want) + 2.0 ** -20 * np.exp(lp) * abs(float(g[t])) + 1e-36)
+
+
+@pytest.fixture
+def emptied():
+    """Gives the large buffers back to the device."""
+    yield
+    import torch
+    torch.cuda.empty_cache()
+
+
+def test_row_offsets_past_32_bits(emptied):
+    """Rows 2^30 elements and some apart: the same bits as the rows close together."""
+    torch, mt = need_gpu()
+    T, V, k, far = 4, 5003, 5, (1 << 30) + 8
+    ids = torch.tensor([3, 0, 5002, 77], dtype=torch.int32, device="cuda")
+    z = torch.randn((T, V), device="cuda").to(torch.bfloat16)
+    g = torch.randn(T, device="cuda")
+    outs = []
+    for ld in (5008, far):
+        Z = torch.empty(((T - 1) * ld + V,), dtype=torch.bfloat16, device="cuda").as_strided((T, V), (ld, 1))
+        Z.copy_(z)
+        o = _run(torch, mt, Z, mt.MT_BF16, ids, 1.0, k, T, V, ld)
+        mt.mt_op_token_logprobs_bwd(Z, mt.MT_BF16, ids, 1.0, o["lse"], o["ent"], g, g, Z, mt.MT_BF16, T, V, ld, ld)
+        outs.append(list(o.values()) + [Z.clone()])
+        del Z
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
