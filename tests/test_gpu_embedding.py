@@ -243,3 +243,23 @@ def test_more_than_2_to_32_values_of_rows(emptied):
     n = torch.bincount(ids.long(), minlength=V).double()
     s = torch.bincount(ids.long(), weights=t.double(), minlength=V)
     assert torch.equal(dE.double(), s[:, None] + n[:, None] * c.double()[None])
+
+
+@pytest.mark.parametrize("V,h,eb", [(60_000_000, 1, True), (9_000_000, 4, False), (3_000_017, 12, True),
+                                    (1_073_741_823, 1, True)])
+def test_large_tables_of_narrow_rows(emptied, V, h, eb):
+    """Cleared beside the sort and after it, up to the largest vocabulary: only
+    the rows of the given ids are other than 0."""
+    torch, mt = need_gpu()
+    T = 3000
+    rng = np.random.default_rng(V)
+    ids = np.concatenate([rng.integers(0, V, T - 4), [0, V - 1, V - 1, V // 2]]).astype(np.int32)
+    dout = torch.from_numpy(rng.integers(1, 9, (T, h)).astype(np.float32)).cuda()
+    got = _grad(torch, mt, torch.from_numpy(ids).cuda(), dout, False, eb, 1.0, V)
+    at, back = np.unique(ids, return_inverse=True)
+    want = np.zeros((len(at), h))
+    np.add.at(want, back, from_dev(dout))
+    rows = torch.from_numpy(at).cuda().long()
+    assert np.array_equal(from_dev(got[rows]), want)  # small whole numbers: exact in bf16 too
+    got[rows] = 0
+    assert int(torch.count_nonzero(got)) == 0

@@ -417,3 +417,28 @@ def test_row_offsets_past_32_bits(emptied):
         del Z
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_one_very_long_row(emptied):
+    """300 million logits: sums of that many terms, and indices past 2^28."""
+    torch, mt = need_gpu()
+    V, k = 300_000_007, 4
+    z = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    z[0, ::2] = 1.0
+    z[0, [299_999_998, 5, 268_435_457]] = torch.tensor([9.0, 8.0, 7.0], dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([268_435_457], dtype=torch.int32, device="cuda")
+    o = _run(torch, mt, z, mt.MT_BF16, ids, 1.0, k, 1, V, V)
+    # 299999998 is even, the other two odd; half of the rest has 1, half 0
+    ones, zeros = (V + 1) // 2 - 1, V // 2 - 2
+    terms = np.array([ones, zeros, 1, 1, 1]) * np.exp(np.array([1.0, 0, 9, 8, 7]) - 9)
+    S, lse = terms.sum(), 9 + np.log(terms.sum())
+    es = 2.0 ** -21 + acc(V) + 4 * U32 * (terms * np.array([8, 9, 0, 1, 2])).sum() / S
+    bound = es + 2 * U32 * (np.log(S) + 9)
+    assert abs(float(o["lse"]) - lse) <= bound and abs(float(o["logp"]) - (7 - lse)) <= bound
+    p = terms / S
+    ent = -(p[:2] * (np.array([1.0, 0]) - lse)).sum() - (p[2:] * (np.array([9.0, 8, 7]) - lse)).sum()
+    B = (p * np.array([8, 9, 0, 1, 2])).sum()
+    assert abs(float(o["ent"]) - ent) <= es * (1 + B) + (2.0 ** -21 + acc(V)) * B + 8 * U32 * (81 + B) + 2 * U32 * np.log(S)
+    assert o["top_ids"].tolist() == [[299_999_998, 5, 268_435_457, 0]]
+    want = np.array([9.0, 8, 7, 1]) - lse
+    assert np.all(np.abs(from_dev(o["top_logp"])[0] - want) <= bound + 2 * U32 * np.abs(want))
