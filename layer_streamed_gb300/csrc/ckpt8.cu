@@ -861,9 +861,9 @@ Shape2 shape2(int T, int units, int rows, bool vec) {
 
 inline int blocks32(int n) { return (n + 31) / 32; }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-inline int done(int launches) {
+inline int done(int launches, cudaError_t e) {
   count_launches(launches);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 // Sizes: row and column counters stay within 31 bits with room for a grid's step.
 inline bool dims_ok(int T, int n, int ld) { return T > 0 && n > 0 && ld >= n && T <= (1 << 30) && ld <= (1 << 29); }
@@ -873,12 +873,13 @@ inline bool fmt_ok(int fmt) { return fmt == FMT_I8 || fmt == FMT_E4M3; }
 
 int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scales, int T, int n, int ldx, int ldc,
                cudaStream_t st) {
-  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
+  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return kRefused;
   const int nb = blocks32(n);
   // whole loads and stores of eight values where every row starts on their boundary
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   const Shape2 s = shape2(T, (n + 7) / 8, pk_rows(vec), vec);
-  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, x, codes, scales, T, n, ldx, ldc, nb); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, s.grid, s.block, 0, st, 1, x, codes, scales, T, n, ldx, ldc, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_I8, true, true>) : go(ckpt8_pack_kernel<FMT_I8, true, false>);
     else vec ? go(ckpt8_pack_kernel<FMT_I8, false, true>) : go(ckpt8_pack_kernel<FMT_I8, false, false>);
@@ -886,16 +887,17 @@ int ckpt8_pack(const void* x, bool bf16, int fmt, uint8_t* codes, uint8_t* scale
     if (bf16) vec ? go(ckpt8_pack_kernel<FMT_E4M3, true, true>) : go(ckpt8_pack_kernel<FMT_E4M3, true, false>);
     else vec ? go(ckpt8_pack_kernel<FMT_E4M3, false, true>) : go(ckpt8_pack_kernel<FMT_E4M3, false, false>);
   }
-  return done(1);
+  return done(1, e);
 }
 
 int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, bool bf16, int T, int n, int ldc,
                  int ldx, cudaStream_t st) {
-  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return -1;
+  if (!dims_ok(T, n, ldx) || !dims_ok(T, n, ldc) || !fmt_ok(fmt) || !al(x, bf16 ? 2 : 4)) return kRefused;
   const int nb = blocks32(n);
   const bool vec = al(x, bf16 ? 16 : 32) && ldx % 8 == 0 && al(codes, 8) && ldc % 8 == 0;
   const Shape2 s = shape2(T, (n + 7) / 8, pk_rows(vec), vec);
-  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, x, T, n, ldc, ldx, nb); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, x, T, n, ldc, ldx, nb); };
   if (fmt == FMT_I8) {
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_I8, true, true>) : go(ckpt8_unpack_kernel<FMT_I8, true, false>);
     else vec ? go(ckpt8_unpack_kernel<FMT_I8, false, true>) : go(ckpt8_unpack_kernel<FMT_I8, false, false>);
@@ -903,18 +905,21 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
     if (bf16) vec ? go(ckpt8_unpack_kernel<FMT_E4M3, true, true>) : go(ckpt8_unpack_kernel<FMT_E4M3, true, false>);
     else vec ? go(ckpt8_unpack_kernel<FMT_E4M3, false, true>) : go(ckpt8_unpack_kernel<FMT_E4M3, false, false>);
   }
-  return done(1);
+  return done(1, e);
 }
 
 int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, uint8_t* codes, uint8_t* scales,
                       int fmt, int T, int h, float eps, cudaStream_t st) {
   if (T <= 0 || h <= 0 || (h & 3) || h > 8192 || !fmt_ok(fmt) || !al(x, 16) || !al(w, 16) ||
       !al(y, 8) || !al(codes, 4))
-    return -1;
+    return kRefused;
   const int units = (h + 7) / 8, nb = blocks32(h);
   // whole units where every row starts on a 32-byte boundary, else their halves
   const bool vec = h % 8 == 0 && al(x, 32) && al(y, 16) && al(codes, 8);
-  auto go = [&](auto k, int threads) { mt_host::launch_early(k, T, threads, 0, st, 1, x, w, y, rstd, codes, scales, h, nb, eps); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k, int threads) {
+    e = mt_host::launch_early(k, T, threads, 0, st, 1, x, w, y, rstd, codes, scales, h, nb, eps);
+  };
   auto pick = [&](auto f, auto v) {
     constexpr int F = decltype(f)::value;
     constexpr bool X = decltype(v)::value;
@@ -926,7 +931,7 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
   auto pick_f = [&](auto f) { vec ? pick(f, std::true_type()) : pick(f, std::false_type()); };
   if (fmt == FMT_I8) pick_f(std::integral_constant<int, FMT_I8>());
   else pick_f(std::integral_constant<int, FMT_E4M3>());
-  return done(1);
+  return done(1, e);
 }
 
 size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)bwd_shape(T, h).parts * h; }
@@ -936,17 +941,17 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
                       int T, int h, cudaStream_t st) {
   if (T <= 0 || h <= 0 || (h & 3) || h > 8192 || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) ||
       !al(dy, 16) || !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
-    return -1;
+    return kRefused;
   const int nb = blocks32(h);
   const BwdShape shape = bwd_shape(T, h);
-  bool ok = true;
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto k) {
     const int smem = shape.stages * h * (resid ? 8 : 4);
     if (smem > 47 * 1024)  // with the static part past the default limit
-      ok = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) == cudaSuccess;
-    if (ok)
-      ok = mt_host::launch_early(k, shape.parts, shape.threads, smem, st, 1, codes, scales, w, rstd, dy, resid, dx,
-                                 dx_bf16, work, T, h, nb, shape.stages) == cudaSuccess;
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+    if (e == cudaSuccess)
+      e = mt_host::launch_early(k, shape.parts, shape.threads, smem, st, 1, codes, scales, w, rstd, dy, resid, dx,
+                                dx_bf16, work, T, h, nb, shape.stages);
   };
   auto pick = [&](auto f) {
     constexpr int F = decltype(f)::value;
@@ -955,33 +960,33 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   };
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
-  if (!ok) return -1;
-  if (mt_host::launch_early(sum_parts_kernel, (h + 31) / 32, 1024, 0, st, 1, (const float*)work, shape.parts, h, dw) !=
-      cudaSuccess)
-    return -1;
-  return done(2);
+  if (e == cudaSuccess)
+    e = mt_host::launch_early(sum_parts_kernel, (h + 31) / 32, 1024, 0, st, 1, (const float*)work, shape.parts, h, dw);
+  return done(2, e);
 }
 
 int swiglu_fwd_ckpt8(const uint16_t* gu, uint16_t* act, uint8_t* codes, uint8_t* scales, int fmt, int T, int F,
                      int ld, cudaStream_t st) {
-  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return -1;
+  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(gu, 2) || !al(act, 2)) return kRefused;
   const bool vec = ld % 8 == 0 && al(gu, 16) && al(act, 16) && al(codes, 8);
   const Shape2 s = shape2(T, (ld + 7) / 8, sw_rows(vec), vec);
-  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, gu, act, codes, scales, T, F, ld, blocks32(F)); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, s.grid, s.block, 0, st, 1, gu, act, codes, scales, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_fwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_fwd_ckpt8_kernel<FMT_E4M3, false>);
-  return done(1);
+  return done(1, e);
 }
 
 int swiglu_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const uint16_t* dact, uint16_t* dgu,
                      int T, int F, int ld, cudaStream_t st) {
-  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return -1;
+  if (!dims_ok(T, F, ld) || !fmt_ok(fmt) || !al(dact, 2) || !al(dgu, 2)) return kRefused;
   const bool vec = ld % 8 == 0 && al(dact, 16) && al(dgu, 16) && al(codes, 8);
   const Shape2 s = shape2(T, (ld + 7) / 8, sw_rows(vec), vec);
-  auto go = [&](auto k) { mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, s.grid, s.block, 0, st, 1, codes, scales, dact, dgu, T, F, ld, blocks32(F)); };
   if (fmt == FMT_I8) vec ? go(swiglu_bwd_ckpt8_kernel<FMT_I8, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_I8, false>);
   else vec ? go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, true>) : go(swiglu_bwd_ckpt8_kernel<FMT_E4M3, false>);
-  return done(1);
+  return done(1, e);
 }
 
 }  // namespace mt

@@ -606,7 +606,7 @@ inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; 
 
 int embed_fwd(const void* table, bool tb, const int32_t* ids, float scale, void* out, bool ob, int T, int V, int h,
               cudaStream_t st) {
-  if (!embed_dims_ok(T, V, h) || !al(table, tb ? 2 : 4) || !al(out, ob ? 2 : 4)) return -1;
+  if (!embed_dims_ok(T, V, h) || !al(table, tb ? 2 : 4) || !al(out, ob ? 2 : 4)) return kRefused;
   const bool vec = h % 4 == 0 && al(table, tb ? 8 : 16) && al(out, ob ? 8 : 16);
   const int units = vec ? h / 4 : h;
   int bx = 32;
@@ -614,7 +614,8 @@ int embed_fwd(const void* table, bool tb, const int32_t* ids, float scale, void*
   const int by = 256 / bx;
   const dim3 block((unsigned)bx, (unsigned)by);
   const dim3 grid((unsigned)((units + bx - 1) / bx), (unsigned)std::min((T + by * kFwdRows - 1) / (by * kFwdRows), 65535));
-  auto go = [&](auto k) { mt_host::launch_early(k, grid, block, 0, st, 1, table, ids, scale, out, T, V, h); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, grid, block, 0, st, 1, table, ids, scale, out, T, V, h); };
   auto pick = [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (tb) ob ? go(embed_fwd_kernel<true, true, N>) : go(embed_fwd_kernel<true, false, N>);
@@ -623,14 +624,14 @@ int embed_fwd(const void* table, bool tb, const int32_t* ids, float scale, void*
   if (vec) pick(std::integral_constant<int, 4>());
   else pick(std::integral_constant<int, 1>());
   count_launches(1);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
 size_t embed_bwd_workspace(int T, int V, int h) { return embed_dims_ok(T, V, h) ? embed_ws(T, V, h).total : 0; }
 
 int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* dtable, bool eb, bool add, void* work,
               int T, int V, int h, cudaStream_t st) {
-  if (!embed_dims_ok(T, V, h) || !al(work, 256) || !al(dout, db ? 2 : 4) || !al(dtable, eb ? 2 : 4)) return -1;
+  if (!embed_dims_ok(T, V, h) || !al(work, 256) || !al(dout, db ? 2 : 4) || !al(dtable, eb ? 2 : 4)) return kRefused;
   const EmbedWs o = embed_ws(T, V, h);
   uint8_t* w = (uint8_t*)work;
   const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
@@ -642,7 +643,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (add && eb) shape.G = 1;
   const int chunks = (units + 32 * shape.G - 1) / (32 * shape.G);
   const int64_t jobs = (int64_t)((T + shape.L - 1) / shape.L) * chunks;
-  if (jobs > (1 << 30)) return -1;
+  if (jobs > (1 << 30)) return kRefused;
   SortArgs a;
   a.ids = ids;
   a.a = (int2*)(w + o.a);
@@ -670,7 +671,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   const int smem = ((a.warps + 1) << a.digit) * 4;
   if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            ((kSortWarps + 1) << kMaxDigit) * 4) != cudaSuccess)
-    return -1;
+    return kLaunchFailed;
   const size_t clearers = (a.clear_bytes + kClearBytes - 1) / kClearBytes;
   const dim3 sorters((unsigned)(a.ctas + (clearers + a.ctas - 1) / a.ctas * a.ctas));
   cudaError_t e = mt_host::launch_early(embed_sort_kernel, sorters, kSortThreads, smem, st, a.ctas, a);
@@ -726,7 +727,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
     else longs(std::integral_constant<int, 1>());
   }
   count_launches(T > kShort ? 3 : 2);
-  return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
 }  // namespace mt

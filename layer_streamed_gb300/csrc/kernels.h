@@ -138,6 +138,12 @@ int ce_finalize(const float2* part, int nslices, const float* zlab, float* lse, 
 int ce_slice_grad(const float* logits, int T, int R, int ld, int row0, const int32_t* labels, const float* lse,
                   float scale, uint16_t* dz, cudaStream_t st);
 
+// What the launchers below return beside 0: the request was refused on the
+// host, before anything was launched; or the runtime refused the launch. A
+// value each, so that neither is read from the thread's pending error, which
+// may be another call's.
+constexpr int kRefused = -1, kLaunchFailed = -2;
+
 // Activation checkpoints in 8 bits (ckpt8.cu): blocks of 32 columns with one
 // power-of-two scale byte each, fmt MT_CKPT_I8 or MT_CKPT_E4M3; a row has
 // ceil(n / 32) scale bytes (SwiGLU: ceil(F / 32) for g, then as many for u).

@@ -15,6 +15,8 @@ inline int rc(int r) {
   if (r == 0) return MT_OK;
   return cudaPeekAtLastError() != cudaSuccess ? MT_ERR_CUDA : MT_ERR_ARG;
 }
+// Of the launchers that tell a refusal from a failed launch themselves.
+inline int own_rc(int r) { return r == 0 ? MT_OK : r == kRefused ? MT_ERR_ARG : MT_ERR_CUDA; }
 inline bool f32_or_bf16(int dtype) { return dtype == MT_F32 || dtype == MT_BF16; }
 // Whether fp32 and int32 arrays lie on words (null does).
 template <class... P>
@@ -352,20 +354,20 @@ int mt_op_lmhead_ce(const void* X, const void* W, const int32_t* labels, float s
 int mt_op_ckpt8_pack(const void* x, int x_dtype, int fmt, void* codes, void* scales, int T, int n, int ldx, int ldc,
                      void* stream) {
   if (!x || !codes || !scales || !f32_or_bf16(x_dtype)) return MT_ERR_ARG;
-  return rc(ckpt8_pack(x, x_dtype == MT_BF16, fmt, (uint8_t*)codes, (uint8_t*)scales, T, n, ldx, ldc, S(stream)));
+  return own_rc(ckpt8_pack(x, x_dtype == MT_BF16, fmt, (uint8_t*)codes, (uint8_t*)scales, T, n, ldx, ldc, S(stream)));
 }
 
 int mt_op_ckpt8_unpack(const void* codes, const void* scales, int fmt, void* x, int x_dtype, int T, int n, int ldc,
                        int ldx, void* stream) {
   if (!x || !codes || !scales || !f32_or_bf16(x_dtype)) return MT_ERR_ARG;
-  return rc(ckpt8_unpack((const uint8_t*)codes, (const uint8_t*)scales, fmt, x, x_dtype == MT_BF16, T, n, ldc, ldx,
+  return own_rc(ckpt8_unpack((const uint8_t*)codes, (const uint8_t*)scales, fmt, x, x_dtype == MT_BF16, T, n, ldc, ldx,
                          S(stream)));
 }
 
 int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd, void* codes, void* scales, int fmt,
                             int T, int h, float eps, void* stream) {
   if (!x || !w || !y || !rstd || !codes || !scales || !on_words(rstd)) return MT_ERR_ARG;
-  return rc(rmsnorm_fwd_ckpt8(x, w, (uint16_t*)y, rstd, (uint8_t*)codes, (uint8_t*)scales, fmt, T, h, eps,
+  return own_rc(rmsnorm_fwd_ckpt8(x, w, (uint16_t*)y, rstd, (uint8_t*)codes, (uint8_t*)scales, fmt, T, h, eps,
                               S(stream)));
 }
 
@@ -377,21 +379,21 @@ int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, cons
                             const float* dy, const float* resid, float* dx, void* dx_bf16, float* dw,
                             float* workspace, int T, int h, void* stream) {
   if (!codes || !scales || !w || !rstd || !dy || !dx || !dw || !workspace || !on_words(rstd, dw)) return MT_ERR_ARG;
-  return rc(rmsnorm_bwd_ckpt8((const uint8_t*)codes, (const uint8_t*)scales, fmt, w, rstd, dy, resid, dx,
+  return own_rc(rmsnorm_bwd_ckpt8((const uint8_t*)codes, (const uint8_t*)scales, fmt, w, rstd, dy, resid, dx,
                               (uint16_t*)dx_bf16, dw, workspace, T, h, S(stream)));
 }
 
 int mt_op_swiglu_fwd_ckpt8(const void* gu, void* act, void* codes, void* scales, int fmt, int T, int F, int ld,
                            void* stream) {
   if (!gu || !act || !codes || !scales) return MT_ERR_ARG;
-  return rc(swiglu_fwd_ckpt8((const uint16_t*)gu, (uint16_t*)act, (uint8_t*)codes, (uint8_t*)scales, fmt, T, F, ld,
+  return own_rc(swiglu_fwd_ckpt8((const uint16_t*)gu, (uint16_t*)act, (uint8_t*)codes, (uint8_t*)scales, fmt, T, F, ld,
                              S(stream)));
 }
 
 int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const void* dact, void* dgu, int T, int F,
                            int ld, void* stream) {
   if (!codes || !scales || !dact || !dgu) return MT_ERR_ARG;
-  return rc(swiglu_bwd_ckpt8((const uint8_t*)codes, (const uint8_t*)scales, fmt, (const uint16_t*)dact,
+  return own_rc(swiglu_bwd_ckpt8((const uint8_t*)codes, (const uint8_t*)scales, fmt, (const uint16_t*)dact,
                              (uint16_t*)dgu, T, F, ld, S(stream)));
 }
 
@@ -401,7 +403,7 @@ int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, floa
   if (!logits || !ids || !lse || !logp || !f32_or_bf16(dtype) || (k > 0 && (!top_ids || !top_logp)) ||
       !on_words(ids, lse, logp, entropy, top_ids, top_logp))
     return MT_ERR_ARG;
-  return rc(token_logprobs(logits, dtype == MT_BF16, ids, inv_temp, k, lse, logp, entropy, top_ids, top_logp, T, V,
+  return own_rc(token_logprobs(logits, dtype == MT_BF16, ids, inv_temp, k, lse, logp, entropy, top_ids, top_logp, T, V,
                            ld, S(stream)));
 }
 
@@ -411,14 +413,14 @@ int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, 
   if (!logits || !ids || !lse || !dlogits || (!g_logp && !g_entropy) || (g_entropy && !entropy) ||
       !f32_or_bf16(dtype) || !f32_or_bf16(d_dtype) || !on_words(ids, lse, entropy, g_logp, g_entropy))
     return MT_ERR_ARG;
-  return rc(token_logprobs_bwd(logits, dtype == MT_BF16, ids, inv_temp, lse, entropy, g_logp, g_entropy, dlogits,
+  return own_rc(token_logprobs_bwd(logits, dtype == MT_BF16, ids, inv_temp, lse, entropy, g_logp, g_entropy, dlogits,
                                d_dtype == MT_BF16, T, V, ld, ldd, S(stream)));
 }
 
 int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, float scale, void* out, int out_dtype,
                     int T, int V, int h, void* stream) {
   if (!table || !ids || !out || !f32_or_bf16(table_dtype) || !f32_or_bf16(out_dtype) || !on_words(ids)) return MT_ERR_ARG;
-  return rc(embed_fwd(table, table_dtype == MT_BF16, ids, scale, out, out_dtype == MT_BF16, T, V, h, S(stream)));
+  return own_rc(embed_fwd(table, table_dtype == MT_BF16, ids, scale, out, out_dtype == MT_BF16, T, V, h, S(stream)));
 }
 
 size_t mt_op_embed_bwd_workspace(int T, int V, int h) { return embed_bwd_workspace(T, V, h); }
@@ -428,7 +430,7 @@ int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float 
   if (!ids || !dout || !dtable || !workspace || !f32_or_bf16(dout_dtype) || !f32_or_bf16(dtable_dtype) ||
       !on_words(ids))
     return MT_ERR_ARG;
-  return rc(embed_bwd(ids, dout, dout_dtype == MT_BF16, scale, dtable, dtable_dtype == MT_BF16, accumulate != 0,
+  return own_rc(embed_bwd(ids, dout, dout_dtype == MT_BF16, scale, dtable, dtable_dtype == MT_BF16, accumulate != 0,
                       workspace, T, V, h, S(stream)));
 }
 

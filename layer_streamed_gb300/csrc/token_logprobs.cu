@@ -640,7 +640,7 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
                    int32_t* top_ids, float* top_logp, int T, int V, int ld, cudaStream_t st) {
   if (T <= 0 || V <= 0 || ld < V || k < 0 || k > kMaxTop || k > V || !(c >= kMinScale) || !(c <= kMaxScale) ||
       ((uintptr_t)z & (bf16 ? 1 : 3)) || T > (1 << 28))
-    return -1;
+    return kRefused;
   // Threads a block: the more rows, the more chunks each, so that a short row
   // needs no more than a warp or two (4227 x 12722 bf16 with the 8 largest: 37
   // us with four chunks each, 26 with sixteen; 2200 rows 21, 18 with eight);
@@ -677,7 +677,7 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
   if (C == 1) pick(std::true_type());
   else pick(std::false_type());
   count_launches(1);
-  return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
 int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, const float* lse, const float* ent,
@@ -685,7 +685,7 @@ int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, co
                        cudaStream_t st) {
   if (T <= 0 || V <= 0 || ld < V || ldd < V || V > (1 << 30) || !(c >= kMinScale) || !(c <= kMaxScale) || (g_ent && !ent) ||
       ((uintptr_t)z & (bf16 ? 1 : 3)) || ((uintptr_t)dz & (dz_bf16 ? 1 : 3)))
-    return -1;
+    return kRefused;
   BwdArgs a{z, ids, lse, ent, g_logp, g_ent, dz, T, V, ld, ldd, c};
   // every eighth element of both on a 16-byte boundary at the same columns
   const bool vec = al16(z) && al16(dz) && (ld - ldd) % 8 == 0;
@@ -695,7 +695,8 @@ int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, co
   const int by = kBwdThreads / bx;
   const dim3 block((unsigned)bx, (unsigned)by);
   const dim3 grid((unsigned)((units + bx - 1) / bx), (unsigned)std::min((T + by - 1) / by, 65535));
-  auto go = [&](auto k) { mt_host::launch_early(k, grid, block, 0, st, 1, a); };
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto k) { e = mt_host::launch_early(k, grid, block, 0, st, 1, a); };
   auto pick = [&](auto v) {
     constexpr bool X = decltype(v)::value;
     if (bf16) dz_bf16 ? go(token_logprobs_bwd_kernel<true, true, X>) : go(token_logprobs_bwd_kernel<true, false, X>);
@@ -704,7 +705,7 @@ int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, co
   if (vec) pick(std::true_type());
   else pick(std::false_type());
   count_launches(1);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
 }  // namespace mt
