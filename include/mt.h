@@ -535,7 +535,7 @@ int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd
  * code * scale and the given rstd). resid may be null or equal dx, dx_bf16
  * may be null. workspace: mt_op_rmsnorm_bwd_ckpt8_workspace floats (0 for
  * sizes the call refuses), 16-byte aligned like w, dy, resid and dx (codes 4,
- * dx_bf16 8). Deterministic. */
+ * dx_bf16 8). T up to 2^30. Deterministic. */
 size_t mt_op_rmsnorm_bwd_ckpt8_workspace(int T, int h);
 int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, const float* w, const float* rstd,
                             const float* dy, const float* resid, float* dx, void* dx_bf16, float* dw,

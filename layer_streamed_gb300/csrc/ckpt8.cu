@@ -934,13 +934,18 @@ int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, 
   return done(1, e);
 }
 
+bool rmsnorm_bwd_ckpt8_dims(int T, int h) {
+  // a block's row counter goes up to stages rounds of the grid past T
+  return T > 0 && T <= (1 << 30) && h > 0 && h % 4 == 0 && h <= 8192;
+}
+
 size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)bwd_shape(T, h).parts * h; }
 
 int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
                       const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,
                       int T, int h, cudaStream_t st) {
-  if (T <= 0 || h <= 0 || (h & 3) || h > 8192 || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) ||
-      !al(dy, 16) || !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
+  if (!rmsnorm_bwd_ckpt8_dims(T, h) || !fmt_ok(fmt) || !al(codes, 4) || !al(w, 16) || !al(dy, 16) ||
+      !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
     return kRefused;
   const int nb = blocks32(h);
   const BwdShape shape = bwd_shape(T, h);

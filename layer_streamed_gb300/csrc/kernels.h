@@ -153,6 +153,7 @@ int ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, void* x, 
                  int ldx, cudaStream_t st);
 int rmsnorm_fwd_ckpt8(const float* x, const float* w, uint16_t* y, float* rstd, uint8_t* codes, uint8_t* scales,
                       int fmt, int T, int h, float eps, cudaStream_t st);
+bool rmsnorm_bwd_ckpt8_dims(int T, int h);        // sizes that the backward takes
 size_t rmsnorm_bwd_ckpt8_partials(int T, int h);  // floats of workspace
 int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
                       const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,

@@ -372,7 +372,7 @@ int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd
 }
 
 size_t mt_op_rmsnorm_bwd_ckpt8_workspace(int T, int h) {
-  return T > 0 && h > 0 && h % 4 == 0 && h <= 8192 ? rmsnorm_bwd_ckpt8_partials(T, h) : 0;
+  return rmsnorm_bwd_ckpt8_dims(T, h) ? rmsnorm_bwd_ckpt8_partials(T, h) : 0;
 }
 
 int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, const float* w, const float* rstd,

@@ -122,3 +122,14 @@ def test_a_sound_request_passes_the_checks_and_its_failed_launch_says_so(name):
     assert _code(name) == mt.MT_ERR_CUDA
     # and the error that this leaves pending does not colour the next refusal
     assert _code(name, T=0) == mt.MT_ERR_ARG
+
+
+@pytest.mark.parametrize("T", [(1 << 30) + 1, INT_MAX])
+@pytest.mark.parametrize("h", [4, 8192])
+def test_norm_backward_refuses_rows_its_counter_would_wrap_on(T, h):
+    """A block looks up to eight rounds of the grid (1216 blocks for narrow
+    rows) past its row: near 2^31 rows that sum is negative and names rows in
+    front of the buffers."""
+    assert _code("mt_op_rmsnorm_bwd_ckpt8", T=T, h=h) == mt.MT_ERR_ARG
+    assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, h) == 0
+    assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(1 << 30, h) > 0
