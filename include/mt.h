@@ -576,7 +576,7 @@ int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, floa
  * and g_entropy [T] (either may be null: zero); lse and entropy as the
  * forward wrote them (entropy is read only with g_entropy). Rows not scored
  * and rows with nothing left get 0. dlogits may be logits itself when type
- * and stride are the same. */
+ * and stride are the same. T and V up to 2^30. */
 int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, float inv_temp, const float* lse,
                              const float* entropy, const float* g_logp, const float* g_entropy, void* dlogits,
                              int d_dtype, int T, int V, int ld, int ldd, void* stream);

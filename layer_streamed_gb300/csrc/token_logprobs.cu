@@ -683,8 +683,10 @@ int token_logprobs(const void* z, bool bf16, const int32_t* ids, float c, int k,
 int token_logprobs_bwd(const void* z, bool bf16, const int32_t* ids, float c, const float* lse, const float* ent,
                        const float* g_logp, const float* g_ent, void* dz, bool dz_bf16, int T, int V, int ld, int ldd,
                        cudaStream_t st) {
-  if (T <= 0 || V <= 0 || ld < V || ldd < V || V > (1 << 30) || !(c >= kMinScale) || !(c <= kMaxScale) || (g_ent && !ent) ||
-      ((uintptr_t)z & (bf16 ? 1 : 3)) || ((uintptr_t)dz & (dz_bf16 ? 1 : 3)))
+  // (row and column counters step past the last one by up to a round of the grid)
+  if (T <= 0 || V <= 0 || ld < V || ldd < V || T > (1 << 30) || V > (1 << 30) || !(c >= kMinScale) ||
+      !(c <= kMaxScale) || (g_ent && !ent) || ((uintptr_t)z & (bf16 ? 1 : 3)) ||
+      ((uintptr_t)dz & (dz_bf16 ? 1 : 3)))
     return kRefused;
   BwdArgs a{z, ids, lse, ent, g_logp, g_ent, dz, T, V, ld, ldd, c};
   // every eighth element of both on a 16-byte boundary at the same columns

@@ -133,3 +133,11 @@ def test_norm_backward_refuses_rows_its_counter_would_wrap_on(T, h):
     assert _code("mt_op_rmsnorm_bwd_ckpt8", T=T, h=h) == mt.MT_ERR_ARG
     assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(T, h) == 0
     assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(1 << 30, h) > 0
+
+
+@pytest.mark.parametrize("T", [(1 << 30) + 1, INT_MAX - (1 << 21), INT_MAX])
+def test_logits_gradient_refuses_rows_its_counter_would_wrap_on(T):
+    """The row counter steps by up to 65535 * 32 rows: within that of 2^31 it
+    turns negative and passes the test against T."""
+    for V in (1, 8):
+        assert _code("mt_op_token_logprobs_bwd", T=T, V=V) == mt.MT_ERR_ARG
