@@ -600,6 +600,13 @@ EmbedWs embed_ws(int T, int V, int h) {
 bool embed_dims_ok(int T, int V, int h) {
   return T > 0 && V > 0 && h > 0 && T <= (1 << 28) && V < (1 << 30) && h <= (1 << 22);
 }
+// The sums' jobs are counted in 31 bits: ranges of at least four positions
+// by chunks of at least 32 columns. The bound takes no alignment into
+// account, so that the workspace query knows it too; 2^40 values fit no GPU.
+bool embed_bwd_dims_ok(int T, int V, int h) {
+  return embed_dims_ok(T, V, h) &&
+         (int64_t)((T + sum_shape(T, h).L - 1) / sum_shape(T, h).L) * ((h + 31) / 32) <= (1 << 30);
+}
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 }  // namespace
@@ -627,11 +634,11 @@ int embed_fwd(const void* table, bool tb, const int32_t* ids, float scale, void*
   return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
-size_t embed_bwd_workspace(int T, int V, int h) { return embed_dims_ok(T, V, h) ? embed_ws(T, V, h).total : 0; }
+size_t embed_bwd_workspace(int T, int V, int h) { return embed_bwd_dims_ok(T, V, h) ? embed_ws(T, V, h).total : 0; }
 
 int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* dtable, bool eb, bool add, void* work,
               int T, int V, int h, cudaStream_t st) {
-  if (!embed_dims_ok(T, V, h) || !al(work, 256) || !al(dout, db ? 2 : 4) || !al(dtable, eb ? 2 : 4)) return kRefused;
+  if (!embed_bwd_dims_ok(T, V, h) || !al(work, 256) || !al(dout, db ? 2 : 4) || !al(dtable, eb ? 2 : 4)) return kRefused;
   const EmbedWs o = embed_ws(T, V, h);
   uint8_t* w = (uint8_t*)work;
   const bool vec = h % 4 == 0 && al(dout, db ? 8 : 16) && al(dtable, eb ? 8 : 16);
@@ -643,7 +650,6 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (add && eb) shape.G = 1;
   const int chunks = (units + 32 * shape.G - 1) / (32 * shape.G);
   const int64_t jobs = (int64_t)((T + shape.L - 1) / shape.L) * chunks;
-  if (jobs > (1 << 30)) return kRefused;
   SortArgs a;
   a.ids = ids;
   a.a = (int2*)(w + o.a);

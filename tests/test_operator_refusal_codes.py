@@ -141,3 +141,15 @@ def test_logits_gradient_refuses_rows_its_counter_would_wrap_on(T):
     turns negative and passes the test against T."""
     for V in (1, 8):
         assert _code("mt_op_token_logprobs_bwd", T=T, V=V) == mt.MT_ERR_ARG
+
+
+@pytest.mark.parametrize("T,h", [(1 << 28, 1 << 22), (1 << 28, 1 << 13), (1 << 20, 1 << 22), (1 << 28, 4), (1, 1 << 22)])
+@pytest.mark.parametrize("od,off", [(F, 0), (B, 0), (F, 4)])
+def test_embedding_workspace_is_nothing_exactly_where_the_gradient_is_refused(T, h, od, off):
+    """Sizes, whatever the alignment and the types: the query answers 0 for
+    those that the call refuses and for no others."""
+    size = mt.mt_op_embed_bwd_workspace(T, 4, h)
+    if torch.cuda.is_available() and size:
+        pytest.skip("a sound request on host memory")
+    code = _code("mt_op_embed_bwd", T=T, V=4, h=h, od=od, d=off4 if off else buf)
+    assert code == (mt.MT_ERR_CUDA if size else mt.MT_ERR_ARG)
