@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* table,
 #pragma unroll
     for (int r = 0; r < kFwdRows; ++r) {
       const int t = t0 + r * step;
-      if (t < T) storen<OB, N>(out, (size_t)t * h + c, scaled(v[r], scale));
+      // (padding is 0 whatever the scale: an infinite one would make it NaN)
+      if (t < T) storen<OB, N>(out, (size_t)t * h + c, scaled(v[r], id[r] >= 0 ? scale : 0.f));
     }
   }
 }
