@@ -179,7 +179,7 @@ struct RowView {
   // End logit e (0..7 the head's, 8..15 the tail's) of a block that owns those ends, or -1.
   __device__ __forceinline__ int end_index(int e, bool lo, bool hi, int V) const {
     if (e < 8) return lo && e < head ? e : -1;
-    return hi && e < 16 && tail0 + e - 8 < V ? tail0 + e - 8 : -1;
+    return hi && e < 16 && e - 8 < V - tail0 ? tail0 + (e - 8) : -1;  // (V may be 2^31 - 1)
   }
 };
 template <bool BF16>
