@@ -86,14 +86,16 @@ typedef struct {
    * size): MT_F32 (0, the default) or MT_BF16 (gradients rounded to nearest
    * even on the device before they stream back: half the D2H bytes; the host
    * optimizer entry points take MT_F32 gradients only). */
-  int32_t grad_dtype;
+  int16_t grad_dtype;
   /* mt_ckpt_format of the residual checkpoints on the device: MT_CKPT_F32 (0,
    * the default), or MT_CKPT_I8 / MT_CKPT_E4M3 (8 bits and a scale per 32
    * channels, a quarter of the bytes). The loss, the head's gradients and
    * those of the layers in the top block are the same bits as with fp32
    * checkpoints; lower blocks are recomputed from the rounded residual, so
-   * their gradients carry its rounding and depend on K. */
-  int32_t ckpt_format;
+   * their gradients carry its rounding and depend on K. It is the upper half
+   * of what was a 32-bit grad_dtype: a program built when there was no
+   * ckpt_format passes a struct of the same size, with 0 here. */
+  int16_t ckpt_format;
 } mt_layer_cfg;
 
 typedef struct mt_ctx mt_ctx;

@@ -65,7 +65,7 @@ class mt_layer_cfg(ctypes.Structure):
                 ("vocab", ctypes.c_int32), ("rope_theta", ctypes.c_float), ("norm_eps", ctypes.c_float),
                 ("max_batch", ctypes.c_int32), ("max_seq", ctypes.c_int32), ("max_K", ctypes.c_int32),
                 ("param_dtype", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
-                ("expert_ffn", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("ckpt_format", ctypes.c_int32)]
+                ("expert_ffn", ctypes.c_int32), ("grad_dtype", ctypes.c_int16), ("ckpt_format", ctypes.c_int16)]
 
 
 class mt_stats(ctypes.Structure):
@@ -204,6 +204,9 @@ def _check(rc: int, ctx=None):
 def make_cfg(n_layers, hidden, n_heads, n_kv_heads, head_dim, ffn_dim, vocab, rope_theta=1e4, norm_eps=1e-5,
              max_batch=1, max_seq=1, max_K=1, param_dtype=MT_F32, n_experts=0, top_k=0,
              expert_ffn=0, grad_dtype=MT_F32, ckpt_format=MT_CKPT_F32) -> mt_layer_cfg:
+    for name, v in (("grad_dtype", grad_dtype), ("ckpt_format", ckpt_format)):
+        if not -(1 << 15) <= v < 1 << 15:  # ctypes would cut it to 16 bits
+            raise MtError(MT_ERR_ARG, f"{name} {v}")
     return mt_layer_cfg(n_layers, hidden, n_heads, n_kv_heads, head_dim, ffn_dim, vocab, rope_theta, norm_eps,
                         max_batch, max_seq, max_K, param_dtype, n_experts, top_k, expert_ffn, grad_dtype,
                         ckpt_format)
