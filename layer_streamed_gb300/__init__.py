@@ -516,20 +516,28 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-_torch_c = None
+_raw_stream = None
+
+
+def _raw_stream_reader():
+    """Reads torch's current stream as a handle: by the functions that build
+    no Stream object for it (host time of every launch) where torch has them."""
+    import torch
+    torch.cuda.init()
+    c = torch._C
+    if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+        return lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return lambda: torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream) -> int | None:
-    """The given cudaStream_t, or torch's current stream (its handle, without
-    building a Stream object for every launch)."""
-    global _torch_c
+    """The given cudaStream_t, or torch's current stream."""
+    global _raw_stream
     if stream is not None:
         return int(stream)
-    if _torch_c is None:
-        import torch
-        torch.cuda.init()
-        _torch_c = torch._C
-    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+    if _raw_stream is None:
+        _raw_stream = _raw_stream_reader()
+    return _raw_stream()
 
 
 def mt_op_gemm(mode, epi, A, B, C, addend, M, N, K, lda, ldb, ldc, stream=None):
