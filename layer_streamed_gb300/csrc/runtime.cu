@@ -742,11 +742,7 @@ int carve(mt_ctx* ctx) {
   ctx->terms = (float*)take(T * 4);
   ctx->loss_dev = (float*)take(256);
   int32_t* ints = (int32_t*)take((T * 5 + 1) * 4);
-  ctx->tok_d = ints;
-  ctx->lab_d = ints + T;
-  ctx->perm_d = ints + 2 * T;
-  ctx->ids_d = ints + 3 * T;
-  ctx->ids_start_d = ints + 4 * T;
+  ctx->tok_d = ints;  // the other four lie behind each step's tokens (run_step)
   ctx->rope_tab = (float2*)take((size_t)ctx->cfg.max_seq * p.d / 2 * 8);
   ctx->gains[0] = (float*)take(2 * (size_t)p.h * 4);
   ctx->gains[1] = (float*)take(2 * (size_t)p.h * 4);
@@ -1614,6 +1610,12 @@ int run_step(Step& st, const int32_t* tokens, const int32_t* labels, float* loss
   int32_t* perm = hs + 2 * T;
   int32_t* ids = hs + 3 * T;
   int32_t* ranges = hs + 4 * T;
+  // one copy brings them all: on the device they follow one another by this
+  // step's T too, which may be less than the context's most
+  ctx->lab_d = ctx->tok_d + T;
+  ctx->perm_d = ctx->tok_d + 2 * T;
+  ctx->ids_d = ctx->tok_d + 3 * T;
+  ctx->ids_start_d = ctx->tok_d + 4 * T;
   std::vector<int32_t>& start = ctx->csr;
   start.assign((size_t)p.V + 1, 0);
   for (int t = 0; t < T; ++t) start[tokens[t] + 1]++;
