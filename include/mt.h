@@ -527,9 +527,11 @@ int mt_op_ckpt8_pack(const void* x, int x_dtype, int fmt, void* codes, void* sca
 int mt_op_ckpt8_unpack(const void* codes, const void* scales, int fmt, void* x, int x_dtype, int T, int n, int ldc,
                        int ldx, void* stream);
 
-/* mt_op_rmsnorm_fwd that also packs its input x [T, h] (same results and
- * sizes; h a multiple of 4, at most 8192): codes [T, h], scales
- * [T, ceil(h/32)]. x, w 16-byte, y 8-byte, codes 4-byte aligned. */
+/* mt_op_rmsnorm_fwd that also packs its input x [T, h] (the same formula and
+ * sizes, h a multiple of 4, at most 8192; the sum of squares is added in
+ * another order, so rstd and y may differ from that call's by rounding):
+ * codes [T, h], scales [T, ceil(h/32)]. x, w 16-byte, y 8-byte, codes 4-byte
+ * aligned. */
 int mt_op_rmsnorm_fwd_ckpt8(const float* x, const float* w, void* y, float* rstd, void* codes, void* scales, int fmt,
                             int T, int h, float eps, void* stream);
 
