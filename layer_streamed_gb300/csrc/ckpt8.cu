@@ -518,19 +518,23 @@ __global__ void __launch_bounds__(NT, 2048 / NT)
 constexpr int kBwdMaxThreads = 1024;
 constexpr int kBwdMaxStages = 8;
 
+// The SMs of the GPU that this is built for: sizes the workspace, so that it
+// does not depend on the machine that asks (a budget is computed without one).
+constexpr int kMaxSms = 152;
+
 struct BwdShape {
-  int threads, vecs, stages, parts;
+  int threads, vecs, stages, an_sm;
+  int parts(int T, int sms) const { return std::min(T, sms * an_sm); }
 };
 // 1024 threads an SM where the rows allow, the shared memory shared out among
 // their blocks as stages of 8 h bytes (4 h without a residual).
-BwdShape bwd_shape(int T, int h) {
+BwdShape bwd_shape(int h) {
   BwdShape s;
   const int n4 = h / 4;
   s.vecs = h > 4096 ? 2 : 1;
   s.threads = std::max(32, (n4 + s.vecs * 32 - 1) / (s.vecs * 32) * 32);
-  const int an_sm = std::min(8, 1024 / s.threads);
-  s.stages = std::min(kBwdMaxStages, 222 * 1024 / an_sm / (8 * h));
-  s.parts = std::min(T, 152 * an_sm);
+  s.an_sm = std::min(8, 1024 / s.threads);
+  s.stages = std::min(kBwdMaxStages, 222 * 1024 / s.an_sm / (8 * h));
   return s;
 }
 
@@ -939,7 +943,7 @@ bool rmsnorm_bwd_ckpt8_dims(int T, int h) {
   return T > 0 && T <= (1 << 30) && h > 0 && h % 4 == 0 && h <= 8192;
 }
 
-size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)bwd_shape(T, h).parts * h; }
+size_t rmsnorm_bwd_ckpt8_partials(int T, int h) { return (size_t)bwd_shape(h).parts(T, kMaxSms) * h; }
 
 int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, const float* w, const float* rstd,
                       const float* dy, const float* resid, float* dx, uint16_t* dx_bf16, float* dw, float* work,
@@ -948,14 +952,15 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
       !al(resid, 16) || !al(dx, 16) || !al(dx_bf16, 8) || !al(work, 16))
     return kRefused;
   const int nb = blocks32(h);
-  const BwdShape shape = bwd_shape(T, h);
+  const BwdShape shape = bwd_shape(h);
+  const int parts = shape.parts(T, std::min(mt_host::num_sms(), kMaxSms));
   cudaError_t e = cudaSuccess;
   auto go = [&](auto k) {
     const int smem = shape.stages * h * (resid ? 8 : 4);
     if (smem > 47 * 1024)  // with the static part past the default limit
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
     if (e == cudaSuccess)
-      e = mt_host::launch_early(k, shape.parts, shape.threads, smem, st, 1, codes, scales, w, rstd, dy, resid, dx,
+      e = mt_host::launch_early(k, parts, shape.threads, smem, st, 1, codes, scales, w, rstd, dy, resid, dx,
                                 dx_bf16, work, T, h, nb, shape.stages);
   };
   auto pick = [&](auto f) {
@@ -966,7 +971,7 @@ int rmsnorm_bwd_ckpt8(const uint8_t* codes, const uint8_t* scales, int fmt, cons
   if (fmt == FMT_I8) pick(std::integral_constant<int, FMT_I8>());
   else pick(std::integral_constant<int, FMT_E4M3>());
   if (e == cudaSuccess)
-    e = mt_host::launch_early(sum_parts_kernel, (h + 31) / 32, 1024, 0, st, 1, (const float*)work, shape.parts, h, dw);
+    e = mt_host::launch_early(sum_parts_kernel, (h + 31) / 32, 1024, 0, st, 1, (const float*)work, parts, h, dw);
   return done(2, e);
 }
 

@@ -704,7 +704,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   auto sums = [&](auto n, auto gr) {
     constexpr int N = decltype(n)::value, G = decltype(gr)::value;
     const int ring = sum_smem(G, N, db);
-    const int resident = 152 * std::min(6, (227 << 10) / (ring + 1024));  // blocks by their shared memory
+    const int resident = mt_host::num_sms() * std::min(6, (227 << 10) / (ring + 1024));  // blocks by their shared memory
     const dim3 grid((unsigned)(a.used ? resident : std::min<int64_t>(resident, (jobs + 7) / 8)));
     auto go = [&](auto k) {
       if (e == cudaSuccess && ring > 47 * 1024)
@@ -723,7 +723,7 @@ int embed_bwd(const int32_t* ids, const void* dout, bool db, float scale, void* 
   if (T > kShort) {
     int CX = 32;
     while (CX < units && CX < 256) CX *= 2;
-    const dim3 grid((unsigned)std::min(T / kShort + 1, 152), (unsigned)((units + CX - 1) / CX));
+    const dim3 grid((unsigned)std::min(T / kShort + 1, mt_host::num_sms()), (unsigned)((units + CX - 1) / CX));
     auto longs = [&](auto n) {
       constexpr int N = decltype(n)::value;
       if (e != cudaSuccess) return;

@@ -153,3 +153,10 @@ def test_embedding_workspace_is_nothing_exactly_where_the_gradient_is_refused(T,
         pytest.skip("a sound request on host memory")
     code = _code("mt_op_embed_bwd", T=T, V=4, h=h, od=od, d=off4 if off else buf)
     assert code == (mt.MT_ERR_CUDA if size else mt.MT_ERR_ARG)
+
+
+@pytest.mark.parametrize("h,blocks", [(8192, 1), (4096, 1), (2048, 2), (512, 8), (4, 8)])
+def test_norm_backward_workspace_does_not_depend_on_the_machine_that_asks(h, blocks):
+    """The parts of as many blocks as 152 SMs hold, with or without a device."""
+    assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(1 << 20, h) == 152 * blocks * h
+    assert mt.mt_op_rmsnorm_bwd_ckpt8_workspace(3, h) == 3 * h
