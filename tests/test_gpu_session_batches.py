@@ -103,3 +103,35 @@ def test_smaller_training_steps():
         assert ends[0][0] == ends[1][0], form
         for a, b in zip(ends[0][1:], ends[1][1:]):
             assert _same(a, b), form
+
+
+@pytest.mark.parametrize("cfg,bf16", [(with_layers(TINY, 4), False), (with_layers(TINY_MOE, 4), True)],
+                         ids=["tiny", "tiny_moe"])
+@pytest.mark.parametrize("fmt", [0, 1, 2], ids=["fp32", "i8", "e4m3"])
+def test_what_the_arena_held_before_does_not_matter(cfg, bf16, fmt):
+    """An arena of NaN bits (and of whole numbers -1): every value that a step reads, it has written."""
+    torch, mt = need_gpu()
+    dt = mt.MT_BF16 if bf16 else mt.MT_F32
+    packed = make_params(cfg, 264, bf16=bf16)
+    out = []
+    for fill in (None, 0xff):
+        shape = mt.make_cfg(cfg.n_layers, cfg.hidden, cfg.n_heads, cfg.n_kv_heads, cfg.head_dim, cfg.ffn_dim, cfg.vocab,
+                            cfg.rope_theta, cfg.norm_eps, 2, 32, 3, dt, cfg.n_experts, cfg.top_k, cfg.expert_ffn,
+                            ckpt_format=fmt)
+        kw = {}
+        if fill is not None:
+            arena = torch.full((mt.mt_required_budget(shape),), fill, dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            kw = dict(device_arena=arena.data_ptr())
+        runs = []
+        for K, B, S in ((1, 1, 9), (3, 2, 32), (2, 2, 5)):
+            if fill is not None:
+                arena.fill_(fill)
+                torch.cuda.synchronize()
+            with _session(mt, cfg, 2, 32, 3, dt, ckpt_format=fmt, **kw) as s:
+                s.params[:] = packed
+                runs.append((s.step(*make_tokens(cfg, B, S, 265 + K), K), s.grads.copy()))
+        out.append(runs)
+    for (l0, g0), (l1, g1) in zip(*out):
+        assert l0 == l1 and _same(g0, g1)
+    assert mt.mt_op_device_error() == 0
