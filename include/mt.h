@@ -516,7 +516,10 @@ int mt_op_moe_ffn_bwd(const void* m, const void* Wr, const void* Wgu, const void
  *  MT_CKPT_E4M3 : limit 448, codes are FP8 E4M3
  * (i8 has the finer steps near a block's maximum, e4m3 keeps 2^-4 relative
  * error for values far below it). A block with an infinity or a NaN gets
- * b = 255 and code 0 and stands for NaN throughout. */
+ * b = 255 and code 0 and stands for NaN throughout.
+ * These calls, the log probabilities and the embedding below answer a bad
+ * argument with MT_ERR_ARG before anything is launched and a failed launch
+ * with MT_ERR_CUDA, whatever error was pending in the thread. */
 
 /* Pack x [T, n] (x_dtype MT_F32 or MT_BF16, row stride ldx elements) into
  * codes [T, ldc] bytes and scales [T, ceil(n/32)] bytes; unpack restores
@@ -550,7 +553,8 @@ int mt_op_rmsnorm_bwd_ckpt8(const void* codes, const void* scales, int fmt, cons
  * blocks separately). Padding columns F..ld-1 get codes and act 0. act comes
  * from the exact g and u. Backward: dgu [T, 2*ld] = (dact*u*silu'(g),
  * dact*silu(g)) with g, u = code * scale; padding columns 0. dact's padding
- * is not read. Any F >= 1, ld in [F, 2^29]. */
+ * is not read. A sigmoid below 2^-126 (g under about -87.3) counts as 0 here.
+ * Any F >= 1, ld in [F, 2^29], T up to 2^30. */
 int mt_op_swiglu_fwd_ckpt8(const void* gu, void* act, void* codes, void* scales, int fmt, int T, int F, int ld,
                            void* stream);
 int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const void* dact, void* dgu, int T, int F,
@@ -569,7 +573,7 @@ int mt_op_swiglu_bwd_ckpt8(const void* codes, const void* scales, int fmt, const
  * ids[t] < 0: the row is not scored; its logits are not used, its outputs are
  * 0 and its top_ids -1. ids[t] >= V: outputs NaN and -1, and a bit in
  * mt_op_device_error. ids are device int32, everything else fp32; inv_temp in
- * [1e-6, 1e6]. */
+ * [1e-6, 1e6]; T up to 2^28. */
 int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, float inv_temp, int k, float* lse,
                          float* logp, float* entropy, int32_t* top_ids, float* top_logp, int T, int V, int ld,
                          void* stream);
@@ -578,16 +582,17 @@ int mt_op_token_logprobs(const void* logits, int dtype, const int32_t* ids, floa
  *   inv_temp * (g_logp ([j = id] - p_j) - g_entropy p_j (log p_j + entropy)),
  * p = e^{z - lse} (good to about 2^-24 |lse|: lse is fp32), for given g_logp
  * and g_entropy [T] (either may be null: zero); lse and entropy as the
- * forward wrote them (entropy is read only with g_entropy). Rows not scored
- * and rows with nothing left get 0. dlogits may be logits itself when type
- * and stride are the same. T and V up to 2^30. */
+ * forward wrote them (entropy is read only with g_entropy). Rows not scored,
+ * rows with ids[t] >= V and rows with nothing left get 0. dlogits may be
+ * logits itself when type and stride are the same. T and V up to 2^30. */
 int mt_op_token_logprobs_bwd(const void* logits, int dtype, const int32_t* ids, float inv_temp, const float* lse,
                              const float* entropy, const float* g_logp, const float* g_entropy, void* dlogits,
                              int d_dtype, int T, int V, int ld, int ldd, void* stream);
 
 /* Embedding lookup: out[t] = scale * table[ids[t]] for table [V, h] and out
  * [T, h] (MT_F32 or MT_BF16 each, one rounding); 0 where ids[t] < 0 (padding).
- * ids[t] >= V: 0, and a bit in mt_op_device_error. */
+ * ids[t] >= V: 0, and a bit in mt_op_device_error. T up to 2^28, V below 2^30,
+ * h up to 2^22, here and in the gradient (with T * h up to about 2^40 there). */
 int mt_op_embed_fwd(const void* table, int table_dtype, const int32_t* ids, float scale, void* out, int out_dtype,
                     int T, int V, int h, void* stream);
 

@@ -10,10 +10,10 @@
 // infinity or a NaN has b = 255 and codes 0, and stands for NaN throughout
 // (the same convention as the OCP microscaling formats' E8M0 scale).
 //
-// int8 steps evenly (error <= max|x| / 127 of the block's maximum when the
-// scale is tight, twice that at worst); e4m3 keeps 2^-4 relative error down
-// to 2^-14 of the block's maximum, so a block with one outlier keeps its
-// other values.
+// int8 steps evenly (error, half a step: at most max|x| / 254 of the block's
+// maximum when the scale is tight, max|x| / 127 at worst); e4m3 keeps 2^-4
+// relative error down to 2^-14 of the block's maximum, so a block with one
+// outlier keeps its other values.
 //
 // All kernels here are bound by HBM traffic: every operand is read once and
 // every result written once, loads are 16 or 32 bytes a thread, and a
@@ -335,6 +335,9 @@ __device__ __forceinline__ uint32_t amax_bf16x8(const uint32_t (&w)[4]) {
 // Measured for 8192 x 4096 fp32 (floor 24.7 us): pack 25.1 us, unpack 26.6;
 // ragged 14783 x 777 (8.5): 12.6 with two rows a thread, 14.8 and 12.9 with
 // four; four are the faster for whole rows of bf16 (unpack 13.8, 14.5 us).
+// Ragged rows are bound by the issue of instructions (4172 x 4525 bf16, floor
+// 8.4: 17 us each way, issue slots 75-80 % used): the shifts into place, and
+// four lanes of 32 that repeat the next warp's units.
 // ---------------------------------------------------------------------------
 constexpr int pk_rows(bool vec) { return vec ? 4 : 2; }
 
@@ -420,7 +423,8 @@ __global__ void __launch_bounds__(256) ckpt8_unpack_kernel(const uint8_t* codes,
 // Measured at 8192 x 4096 (floor 34.5 us): 256 threads 37.8 us, 128 threads
 // 38.9, four columns a unit 41.2; with the SM's 2048 threads and launched early
 // 36.0, 512 threads of one unit 38.6. 4096 x 8192: 36.6, 256 threads of four
-// units 38.3.
+// units 38.3. Two units do not quite fit the 32 registers that 2048 threads
+// leave: 4 to 8 bytes a thread spill at h = 4096, 8 to 24 above.
 template <int FMT, int NT, int V, bool VEC>
 __global__ void __launch_bounds__(NT, 2048 / NT)
     rmsnorm_fwd_ckpt8_kernel(const float* x, const float* w, uint16_t* __restrict__ y,
@@ -698,10 +702,11 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int 
 // same 8 of u, four lanes a block.
 // HBM bounds whole rows (8192 x 14336, floor 139 us each way: forward 139-140
 // us, backward 137-139; with exact divisions and single maxima 242 and 243),
-// the issue of instructions ragged ones (4690 x 8001, floor 44: 74 and 87 us).
-// Whole rows: two a thread, five blocks an SM forward, six backward (146 us
-// with the four that its registers allowed). Ragged: one row, eight blocks
-// (two rows at five and four: 85 and 118 us).
+// the issue of instructions ragged ones (4690 x 8001, floor 44: 74 and 87 us;
+// issue slots 83 and 80 % used). Whole rows: two a thread, five blocks an SM
+// forward, six backward (146 us with the four that its registers allowed).
+// Ragged: one row, eight blocks (two rows at five and four: 85 and 118 us).
+// These bounds make the backward spill: 4 to 24 bytes a thread whole, 8 ragged.
 // ---------------------------------------------------------------------------
 // 1 / (1 + e^-g) of two values with the hardware's exponential and
 // reciprocal (the exact division and the subnormal range of both cost more

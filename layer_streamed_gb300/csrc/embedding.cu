@@ -16,8 +16,12 @@
 // whole: dout read once, the table's gradient written once; the sort (some 10
 // us for small batches) hides behind the first clearing. Measured: 8192 tokens
 // of 128256 x 4096 fp32 (floor 329 us) 316-322 us, 16384 of 151936 x 4096 bf16
-// (223) 225, 64 of 32000 x 1024 fp32 (19.3) 23.5; where nothing hides the sort,
-// 8192 of 1000 x 4096 (22) 45 us. Lookup: 8192 rows of 4096 28 us.
+// (223) 226, 64 of 32000 x 1024 fp32 (19.3) 24; where nothing hides the sort,
+// 8192 of 1000 x 4096 (22) 46 us, 131072 of 32000 x 1024 (98) 198. Rows of bf16:
+// 8192 of 128256 x 4096 fp32 (319) 320, 16384 of 151936 x 4096 bf16 (203) 220.
+// Added to the table: 8192 of 128256 x 4096 fp32 (39) 62, 16384 of 151936 x 4096
+// bf16 (57) 107. Lookup from bf16, 8192 rows of 4096: 33 us to fp32 (30), 25 to
+// bf16 (20).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

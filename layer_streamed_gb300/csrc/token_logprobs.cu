@@ -550,6 +550,8 @@ constexpr int kBwdVecs = 2;
 // whose loads they do not depend on. VEC: logits and gradient come to a
 // 16-byte boundary at the same columns of a row; a row's units then start at
 // its first such column, and the first threads take the columns before it.
+// (Six blocks an SM: the 40 registers spill 12 to 16 bytes of bf16 logits
+// without VEC, and nothing else.)
 template <bool BF16, bool OBF16, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 6) token_logprobs_bwd_kernel(BwdArgs a) {
   constexpr int esz = BF16 ? 2 : 4;
