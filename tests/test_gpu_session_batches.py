@@ -61,6 +61,24 @@ def test_steps_of_changing_interval_and_batch(cfg, bf16):
     assert mt.mt_op_device_error() == 0
 
 
+@pytest.mark.parametrize("fmt", [0, 1], ids=["fp32", "i8"])
+def test_steps_of_changing_length(fmt):
+    """Sequences of several attention tiles, whole and ragged, below the session's longest."""
+    torch, mt = need_gpu()
+    cfg = with_layers(TINY_GQA, 3)
+    packed = make_params(cfg, 234)
+    runs = [(1, 2, 129), (2, 2, 300), (1, 1, 200), (3, 2, 128), (2, 1, 257), (2, 2, 1), (1, 2, 300)]
+    with _session(mt, cfg, 2, 300, 3, mt.MT_F32, ckpt_format=fmt) as s:
+        s.params[:] = packed
+        got = [(s.step(*make_tokens(cfg, B, S, 235 + i), K), s.grads.copy()) for i, (K, B, S) in enumerate(runs)]
+    for i, (K, B, S) in enumerate(runs):
+        with _session(mt, cfg, B, S, K, mt.MT_F32, ckpt_format=fmt) as s:
+            s.params[:] = packed
+            assert s.step(*make_tokens(cfg, B, S, 235 + i), K) == got[i][0], runs[i]
+            assert _same(s.grads, got[i][1]), runs[i]
+    assert mt.mt_op_device_error() == 0
+
+
 def test_smaller_training_steps():
     """Synchronous and asynchronous steps of the host optimizer on batches below the session's."""
     torch, mt = need_gpu()
