@@ -60,7 +60,7 @@ typedef enum { MT_CKPT_F32 = 0, MT_CKPT_I8 = 1, MT_CKPT_E4M3 = 2 } mt_ckpt_forma
  * Shapes: hidden h, n_heads query heads and n_kv_heads key/value heads of
  * head_dim d (n_heads % n_kv_heads == 0; query head j reads KV head
  * j / (n_heads / n_kv_heads)), SwiGLU FFN width ffn_dim, untied vocab.
- * Supported: h % 64 == 0, d in {16, 32, 64, 128}, for MT_BF16 params
+ * Supported: h % 64 == 0, any vocab >= 1, d in {16, 32, 64, 128}, for MT_BF16 params
  * ffn_dim % 8 == 0; any ffn_dim >= 1 for MT_F32 params; for MT_FP8 params
  * ffn_dim % 16 == 0.
  * max_batch * max_seq bounds the tokens of one call; max_K bounds the

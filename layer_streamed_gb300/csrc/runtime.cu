@@ -394,7 +394,7 @@ bool make_plan(const mt_layer_cfg& c, Plan* P) {
     int ns = (int)std::max<size_t>(1, (p.V * row_bytes + cap - 1) / cap);
     while (true) {
       int r = (int)rup((p.V + ns - 1) / ns, 256);
-      if (r > p.V) r = p.V;
+      if (r > p.V) r = (int)rup(p.V, 8);  // the logits' row stride: whole 16-byte pieces of bf16
       if ((size_t)r * row_bytes <= cap || r <= 256) {
         *rows = r;
         *n = (p.V + r - 1) / r;
