@@ -607,6 +607,41 @@ size_t mt_op_embed_bwd_workspace(int T, int V, int h);
 int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float scale, void* dtable, int dtable_dtype,
                     int accumulate, void* workspace, int T, int V, int h, void* stream);
 
+/* Cross entropy over a large vocabulary from the head's inputs and weights,
+ * per token, without storing the logits. X bf16 [T, h] (row stride ldx), W
+ * bf16 [V, h] (row stride ldw), z = logit_scale * X W^T:
+ *   lse[t]  = log sum_j e^{z_j}
+ *   loss[t] = lse - (1 - smoothing) z_label - smoothing * mean_j z_j + z_coef * lse^2
+ * labels device int32 [T]; labels[t] < 0: the row is not scored, loss and lse
+ * are 0. labels[t] >= V: both NaN, and a bit in mt_op_device_error. loss, lse
+ * fp32 [T]. h, ldx, ldw multiples of 8, h up to 2^16, T and V up to 2^24 with
+ * T * V up to 2^40; logit_scale in [1e-6, 1e6], smoothing in [0, 1), z_coef in
+ * [0, 1e6]. X and W 16-byte aligned, workspace (bytes) 256. (mt_op_lmhead_ce
+ * keeps all logits and gives the mean loss with fp32 gradients in one call.) */
+size_t mt_op_linear_ce_fwd_workspace(int T, int V, int h);
+int mt_op_linear_ce_fwd(const void* X, const void* W, const int32_t* labels, float logit_scale, float smoothing,
+                        float z_coef, float* loss, float* lse, void* workspace, int T, int V, int h, int ldx, int ldw,
+                        void* stream);
+
+/* Its gradients for given gradients g_loss fp32 [T] of the losses, lse as the
+ * forward wrote it:
+ *   dz_j = g_loss ((1 + 2 z_coef lse) p_j - (1 - smoothing) [j = label] - smoothing / V)
+ *   dX [T, h] = logit_scale dz W,  dW [V, h] = logit_scale dz^T X
+ * (MT_F32 or MT_BF16 each, dense; either may be null: not wanted). dz is
+ * rounded to bf16 once, the sums run in fp32 and are rounded once; p below
+ * 2^-126 counts as 0.
+ * accumulate != 0: dW += that. Rows that are not scored, or whose label is V
+ * or more, have dX = 0 and leave no trace in dW, whatever X and g_loss hold
+ * there (dX: where W is finite). The vocabulary is worked off in pieces of up
+ * to 2^28 / T columns. workspace as above (0 for sizes that are refused). Not
+ * bitwise independent of T; the same call gives the same bits every time. dX,
+ * dW 16-byte aligned, and neither overlaps an input. */
+size_t mt_op_linear_ce_bwd_workspace(int T, int V, int h);
+int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, float logit_scale, float smoothing,
+                        float z_coef, const float* lse, const float* g_loss, void* dX, int dx_dtype, void* dW,
+                        int dw_dtype, int accumulate, void* workspace, int T, int V, int h, int ldx, int ldw,
+                        void* stream);
+
 /* Device error word of the kernels (barrier timeouts, token ids outside the
  * vocabulary etc.): returns and clears it (0 = none). Synchronizes the
  * device. */

@@ -50,7 +50,8 @@ EXPORTS = ("mt_packed_bytes", "mt_tensor_offset", "mt_required_budget", "mt_crea
            "mt_op_moe_ffn_bwd", "mt_op_ckpt8_pack", "mt_op_ckpt8_unpack", "mt_op_rmsnorm_fwd_ckpt8",
            "mt_op_rmsnorm_bwd_ckpt8_workspace", "mt_op_rmsnorm_bwd_ckpt8", "mt_op_swiglu_fwd_ckpt8",
            "mt_op_swiglu_bwd_ckpt8", "mt_op_token_logprobs", "mt_op_token_logprobs_bwd", "mt_op_embed_fwd",
-           "mt_op_embed_bwd_workspace", "mt_op_embed_bwd")
+           "mt_op_embed_bwd_workspace", "mt_op_embed_bwd", "mt_op_linear_ce_fwd_workspace", "mt_op_linear_ce_fwd",
+           "mt_op_linear_ce_bwd_workspace", "mt_op_linear_ce_bwd")
 
 
 class MtError(RuntimeError):
@@ -180,6 +181,10 @@ def lib() -> ctypes.CDLL:
         "mt_op_embed_fwd": (i32, [vp, i32, vp, f32, vp, i32, i32, i32, i32, vp]),
         "mt_op_embed_bwd_workspace": (sz, [i32, i32, i32]),
         "mt_op_embed_bwd": (i32, [vp, vp, i32, f32, vp, i32, i32, vp, i32, i32, i32, vp]),
+        "mt_op_linear_ce_fwd_workspace": (sz, [i32, i32, i32]),
+        "mt_op_linear_ce_fwd": (i32, [vp, vp, vp, f32, f32, f32, vp, vp, vp] + [i32] * 5 + [vp]),
+        "mt_op_linear_ce_bwd_workspace": (sz, [i32, i32, i32]),
+        "mt_op_linear_ce_bwd": (i32, [vp, vp, vp, f32, f32, f32, vp, vp, vp, i32, vp, i32, i32, vp] + [i32] * 5 + [vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -711,6 +716,31 @@ def mt_op_embed_bwd(ids, dout, dout_dtype, scale, dtable, dtable_dtype, accumula
     """The table's gradient, summed per token in a fixed order."""
     _check(lib().mt_op_embed_bwd(_ptr(ids), _ptr(dout), dout_dtype, scale, _ptr(dtable), dtable_dtype,
                                  int(accumulate), _ptr(workspace), T, V, h, _stream(stream)))
+
+
+def mt_op_linear_ce_fwd_workspace(T, V, h) -> int:
+    return lib().mt_op_linear_ce_fwd_workspace(T, V, h)
+
+
+def mt_op_linear_ce_fwd(X, W, labels, logit_scale, smoothing, z_coef, loss, lse, workspace, T, V, h, ldx, ldw,
+                        stream=None):
+    """Per-token cross entropy of logit_scale * X W^T and its log-sum-exp,
+    the logits never stored (see include/mt.h)."""
+    _check(lib().mt_op_linear_ce_fwd(_ptr(X), _ptr(W), _ptr(labels), logit_scale, smoothing, z_coef, _ptr(loss),
+                                     _ptr(lse), _ptr(workspace), T, V, h, ldx, ldw, _stream(stream)))
+
+
+def mt_op_linear_ce_bwd_workspace(T, V, h) -> int:
+    return lib().mt_op_linear_ce_bwd_workspace(T, V, h)
+
+
+def mt_op_linear_ce_bwd(X, W, labels, logit_scale, smoothing, z_coef, lse, g_loss, dX, dx_dtype, dW, dw_dtype,
+                        accumulate, workspace, T, V, h, ldx, ldw, stream=None):
+    """Gradients of X and W for given gradients of the losses, in pieces of
+    the vocabulary."""
+    _check(lib().mt_op_linear_ce_bwd(_ptr(X), _ptr(W), _ptr(labels), logit_scale, smoothing, z_coef, _ptr(lse),
+                                     _ptr(g_loss), _ptr(dX), dx_dtype, _ptr(dW), dw_dtype, int(accumulate),
+                                     _ptr(workspace), T, V, h, ldx, ldw, _stream(stream)))
 
 
 def mt_op_device_error() -> int:

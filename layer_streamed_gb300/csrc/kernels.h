@@ -183,6 +183,20 @@ uint32_t ckpt8_take_device_error();
 uint32_t token_logprobs_take_device_error();
 uint32_t embedding_take_device_error();
 
+// Cross entropy of X W^T without the logits, and its gradients
+// (linear_ce.cu). linear_ce_dims: sizes that are taken; linear_ce_aligned:
+// operands on their boundaries (null is). dX or dW may be null.
+bool linear_ce_dims(int T, int V, int h);
+bool linear_ce_aligned(const void* X, const void* W, const void* dX, const void* dW, const void* work);
+size_t linear_ce_fwd_workspace(int T, int V);
+size_t linear_ce_bwd_workspace(int T, int V, int h);
+int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, float scale, float smooth, float zc,
+                  float* loss, float* lse, void* work, int T, int V, int h, int ldx, int ldw, cudaStream_t st);
+int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, float scale, float smooth, float zc,
+                  const float* lse, const float* g, void* dX, bool dx_bf16, void* dW, bool dw_bf16, bool accumulate,
+                  void* work, int T, int V, int h, int ldx, int ldw, cudaStream_t st);
+uint32_t linear_ce_take_device_error();
+
 // Read and clear the device error words of the kernels that wait on
 // barriers (0 = no error). Synchronous with respect to the device.
 uint32_t gemm_take_device_error();

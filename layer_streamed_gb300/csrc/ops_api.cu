@@ -434,10 +434,51 @@ int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float 
                       workspace, T, V, h, S(stream)));
 }
 
+namespace {
+// Arguments that both directions of the linear cross entropy share.
+bool linear_ce_ok(const void* X, const void* W, const int32_t* labels, float scale, float smooth, float zc,
+                  const void* work, int T, int V, int h, int ldx, int ldw) {
+  return X && W && labels && work && linear_ce_dims(T, V, h) && scale >= 1e-6f && scale <= 1e6f && smooth >= 0.f &&
+         smooth < 1.f && zc >= 0.f && zc <= 1e6f && ldx >= h && ldw >= h && ldx % 8 == 0 && ldw % 8 == 0 &&
+         on_words(labels);
+}
+}  // namespace
+
+size_t mt_op_linear_ce_fwd_workspace(int T, int V, int h) {
+  return linear_ce_dims(T, V, h) ? linear_ce_fwd_workspace(T, V) : 0;
+}
+
+int mt_op_linear_ce_fwd(const void* X, const void* W, const int32_t* labels, float logit_scale, float smoothing,
+                        float z_coef, float* loss, float* lse, void* workspace, int T, int V, int h, int ldx, int ldw,
+                        void* stream) {
+  if (!linear_ce_ok(X, W, labels, logit_scale, smoothing, z_coef, workspace, T, V, h, ldx, ldw) || !loss || !lse ||
+      !on_words(loss, lse) || !linear_ce_aligned(X, W, nullptr, nullptr, workspace))
+    return MT_ERR_ARG;
+  return own_rc(linear_ce_fwd((const uint16_t*)X, (const uint16_t*)W, labels, logit_scale, smoothing, z_coef, loss, lse,
+                              workspace, T, V, h, ldx, ldw, S(stream)));
+}
+
+size_t mt_op_linear_ce_bwd_workspace(int T, int V, int h) {
+  return linear_ce_dims(T, V, h) ? linear_ce_bwd_workspace(T, V, h) : 0;
+}
+
+int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, float logit_scale, float smoothing,
+                        float z_coef, const float* lse, const float* g_loss, void* dX, int dx_dtype, void* dW,
+                        int dw_dtype, int accumulate, void* workspace, int T, int V, int h, int ldx, int ldw,
+                        void* stream) {
+  if (!linear_ce_ok(X, W, labels, logit_scale, smoothing, z_coef, workspace, T, V, h, ldx, ldw) || !lse || !g_loss ||
+      (!dX && !dW) || !f32_or_bf16(dx_dtype) || !f32_or_bf16(dw_dtype) || !on_words(lse, g_loss) ||
+      !linear_ce_aligned(X, W, dX, dW, workspace))
+    return MT_ERR_ARG;
+  return own_rc(linear_ce_bwd((const uint16_t*)X, (const uint16_t*)W, labels, logit_scale, smoothing, z_coef, lse,
+                              g_loss, dX, dx_dtype == MT_BF16, dW, dw_dtype == MT_BF16, accumulate != 0, workspace, T,
+                              V, h, ldx, ldw, S(stream)));
+}
+
 int mt_op_device_error(void) {
   cudaDeviceSynchronize();
   return (int)(gemm_take_device_error() | attention_tc_take_device_error() | ckpt8_take_device_error() |
-               token_logprobs_take_device_error() | embedding_take_device_error());
+               token_logprobs_take_device_error() | embedding_take_device_error() | linear_ce_take_device_error());
 }
 
 }  // extern "C"

@@ -1,0 +1,322 @@
+// Tensor-core products whose results are used where they are made: D = A B^T
+// over a batch, bf16 or fp16 operands, fp32 accumulators in tensor memory,
+// and an epilogue type E that sees every output tile there and decides what
+// leaves the SM (the statistics of a softmax, a gradient, a polynomial of a
+// matrix). The plain products of the decoder's layers are gemm.cu's.
+//
+// A tile is TM x BN outputs: 256 x 256 by a pair of SMs (tcgen05.mma
+// cta_group::2; each CTA holds 128 rows of A and 128 of B, 32 KB a 64-deep
+// step, six steps in flight) where there are enough of them for the GPU, else
+// 128 x 128 by one SM. Warp 0 fills the ring by TMA, one thread of warp 1
+// issues the MMAs, warps 2 to 5 drain the two accumulators, so one tile's
+// epilogue overlaps the next one's products. CTAs are persistent and take
+// tiles in a fixed order; each output is one fixed sum, whatever the grid.
+//
+// Rows, columns and depth need not be multiples of anything: TMA fills zeros
+// outside a matrix, and the epilogues look at M and N.
+#pragma once
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mt {
+
+struct ProductShape {
+  int M, N, K;
+  int batch;     // matrices, one after another (the tensor maps' third axis)
+  int num_m, num_n, tiles;  // of one matrix; set by product_shape
+  int group_m;   // row blocks that share a sweep over the columns
+};
+
+// BN: tile columns; PAIR: two SMs a tile; A_MN / B_MN: the operand is stored
+// with its outputs' axis contiguous ([K, M] and [K, N]) rather than K; F16:
+// fp16 operands; SYM: A = B and D symmetric, only tiles on and above the
+// diagonal are made (the epilogue mirrors them).
+template <int BN_, bool PAIR_, bool A_MN_, bool B_MN_, bool F16_ = false, bool SYM_ = false>
+struct ProductCfg {
+  static constexpr int BN = BN_;
+  static constexpr bool PAIR = PAIR_, A_MN = A_MN_, B_MN = B_MN_, F16 = F16_, SYM = SYM_;
+  static constexpr int BM = 128, BK = 64;
+  static constexpr int TM = PAIR ? 2 * BM : BM;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B in one CTA
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = B_ROWS * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 6;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int TMEM_COLS = 2 * BN;
+};
+
+// What an epilogue knows of its tile: this lane's row of D, the warp's first
+// row, the tile's first column and its matrix.
+struct TileAt {
+  int row, row0, n0, nb, b;
+  bool mirror;  // SYM: the tile lies above the diagonal
+};
+
+template <class C>
+__device__ __forceinline__ void product_tile(const ProductShape& s, int tile, int& mb, int& nb, int& b) {
+  b = tile / s.tiles;
+  const int t = tile - b * s.tiles;
+  if (C::SYM) {  // column nb holds nb + 1 tiles
+    nb = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while (nb * (nb + 1) / 2 > t) --nb;
+    while ((nb + 1) * (nb + 2) / 2 <= t) ++nb;
+    mb = t - nb * (nb + 1) / 2;
+  } else {
+    const int per_group = s.group_m * s.num_n;
+    const int g = t / per_group;
+    const int first = g * s.group_m;
+    const int size = min(s.num_m - first, s.group_m);
+    const int r = t - g * per_group;
+    mb = first + r % size;
+    nb = r / size;
+  }
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int x, int y,
+                                                 int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+
+template <class C, class E>
+__global__ void __launch_bounds__(192, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const ProductShape s, const typename E::Args args) {
+  constexpr int BN = C::BN, BM = C::BM, BK = C::BK;
+  constexpr bool PAIR = C::PAIR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
+  uint64_t* full = (uint64_t*)(smem + C::STAGES * C::STAGE_BYTES);  // PAIR: the even CTA's, for both halves
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;  // PAIR: the even CTA's, both CTAs drained
+  uint32_t* tmem_slot = (uint32_t*)(tempty + 2);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], PAIR ? 8 : 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc2(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish2();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_wait();
+  grid_release();
+
+  const int all = s.tiles * s.batch;
+  const int num_kb = (s.K + BK - 1) / BK;
+  const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+  if (warp == 0) {
+    if (lane == 0) {  // TMA producer
+      const uint32_t full0 = PAIR ? mapa_shared(full, 0) : 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = first; tile < all; tile += step) {
+        int mb, nb, b;
+        product_tile<C>(s, tile, mb, nb, b);
+        const int m0 = mb * C::TM + rank * BM, n0 = nb * BN + rank * C::B_ROWS;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          mbar_wait<PAIR>(&empty[stage], phase ^ 1, abort_flag, kErrTimeoutTma);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if (PAIR) tma_load_3d_pair(dst, map, full0 + stage * 8, x, y, b);
+            else tma_load_3d(dst, map, &full[stage], x, y, b);
+          };
+          uint8_t* a_dst = sA + stage * C::A_BYTES;
+          uint8_t* b_dst = sB + stage * C::B_BYTES;
+          if (!C::A_MN) {
+            load(a_dst, &tmA, kb * BK, m0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j) load(a_dst + j * 8192, &tmA, m0 + 64 * j, kb * BK);
+          }
+          if (!C::B_MN) {
+            load(b_dst, &tmB, kb * BK, n0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < C::B_ROWS / 64; ++j) load(b_dst + j * 8192, &tmB, n0 + 64 * j, kb * BK);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {  // MMA issuer
+      constexpr uint32_t IDESC =
+          make_idesc(C::TM, BN, C::A_MN, C::B_MN) & (C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      for (int tile = first; tile < all; tile += step, ++local) {
+        const int acc = local & 1;
+        mbar_wait<PAIR>(&tempty[acc], ((local >> 1) & 1) ^ 1, abort_flag, kErrTimeoutMma);
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          mbar_wait(&full[stage], phase, abort_flag, kErrTimeoutMma);
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(sA + stage * C::A_BYTES);
+          const uint32_t b_base = smem_u32(sB + stage * C::B_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad =
+                C::A_MN ? make_sdesc(a_base + kk * 2048, 8192, 1024) : make_sdesc(a_base + kk * 32, 16, 1024);
+            const uint64_t bd =
+                C::B_MN ? make_sdesc(b_base + kk * 2048, 8192, 1024) : make_sdesc(b_base + kk * 32, 16, 1024);
+            if (PAIR) tc_mma2(d_tmem, ad, bd, IDESC, (kb | kk) != 0);
+            else tc_mma(d_tmem, ad, bd, IDESC, (kb | kk) != 0);
+          }
+          if (PAIR) tc_commit2(&empty[stage], 0x3);
+          else tc_commit(&empty[stage]);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (PAIR) tc_commit2(&tfull[acc], 0x3);
+        else tc_commit(&tfull[acc]);
+      }
+    }
+    __syncwarp();
+  } else {  // epilogue: warp w reads tensor memory lanes 32 (w % 4) ..
+    const uint32_t q = warp & 3;
+    const uint32_t tempty0 = PAIR ? mapa_shared(tempty, 0) : 0;
+    int local = 0;
+    for (int tile = first; tile < all; tile += step, ++local) {
+      int mb, nb, b;
+      product_tile<C>(s, tile, mb, nb, b);
+      const int acc = local & 1;
+      TileAt at;
+      at.row0 = mb * C::TM + rank * BM + (int)q * 32;
+      at.row = at.row0 + (int)lane;
+      at.nb = nb;
+      at.n0 = nb * BN;
+      at.b = b;
+      at.mirror = C::SYM && mb != nb;
+      // per-row values that the epilogue needs are loaded while the products run
+      typename E::Row row_in;
+      E::load_row(args, s, at, row_in);
+      mbar_wait<PAIR>(&tfull[acc], (local >> 1) & 1, abort_flag, kErrTimeoutEpi);
+      tc_fence_after();
+      E::template tile<BN>(args, s, at, row_in, tmem_base + ((q * 32) << 16) + acc * BN);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(tempty0 + acc * 8);
+        else mbar_arrive(&tempty[acc]);
+      }
+    }
+  }
+  if (*abort_flag) {  // a wait ran out: give the copies in flight time to land
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 24)) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // the peer may still address this CTA's barriers or tensor memory
+  if (warp == 1) {
+    tc_fence_after();
+    if (PAIR) tmem_dealloc2(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// 32 accumulator columns of this lane's row.
+__device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
+  uint32_t r[32];
+  __syncwarp();
+  tmem_ld32(tb + c * 32, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// A batch of matrices [rows, cols] of 16-bit values, row stride ld, matrices
+// `apart` elements from each other; boxes of 64 columns by `box_rows`.
+inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, int64_t ld, int64_t apart, int batch,
+                        int box_rows, bool f16) {
+  const uint64_t gdim[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
+  const uint64_t gstride[2] = {(uint64_t)ld * 2, (uint64_t)apart * 2};
+  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  return mt_host::encode_tiled(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base,
+                               gdim, gstride, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+// Box heights of an operand: the tile's rows where K is contiguous, K steps else.
+template <class C>
+constexpr int a_box() { return C::A_MN ? 64 : C::BM; }
+template <class C>
+constexpr int b_box() { return C::B_MN ? 64 : C::B_ROWS; }
+
+template <class C>
+ProductShape product_shape(int M, int N, int K, int batch) {
+  ProductShape s;
+  s.M = M;
+  s.N = N;
+  s.K = K;
+  s.batch = batch;
+  s.num_m = (M + C::TM - 1) / C::TM;
+  s.num_n = (N + C::BN - 1) / C::BN;
+  s.tiles = C::SYM ? s.num_m * (s.num_m + 1) / 2 : s.num_m * s.num_n;
+  // the rows of A that a sweep over the columns shares stay in L2: 32 MB, as measured for the layers' products
+  const size_t band = (size_t)C::TM * K * 2;
+  s.group_m = (int)std::min<size_t>(s.num_m, std::max<size_t>(1, ((size_t)32 << 20) / band));
+  return s;
+}
+
+template <class C, class E>
+cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const ProductShape& s,
+                           const typename E::Args& args, cudaStream_t st) {
+  auto kern = product_kernel<C, E>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t all = (int64_t)s.tiles * s.batch;
+  const int sms = mt_host::num_sms();
+  const int grid = C::PAIR ? 2 * (int)std::min<int64_t>(all, std::max(1, sms / 2)) : (int)std::min<int64_t>(all, sms);
+  e = mt_host::launch_early(kern, grid, 192, C::SMEM, st, C::PAIR ? 2 : 1, a, b, s, args);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace mt
