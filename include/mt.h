@@ -642,6 +642,40 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
                         int dw_dtype, int accumulate, void* workspace, int T, int V, int h, int ldx, int ldw,
                         void* stream);
 
+/* Orthogonalised matrices: each of `batch` dense matrices G [rows, cols] (one
+ * after another, MT_F32 or MT_BF16) is scaled to Frobenius norm 1,
+ * X = G / (|G| + eps), and taken through `steps` Newton-Schulz steps
+ *   X <- a X + (b A + c A A) X,  A = X X^T,
+ * (a, b, c) = coef[3 i ..] of step i: a host array, read before the call
+ * returns, or null for Muon's quintic (3.4445, -4.7750, 2.0315) every step.
+ * O [batch, rows, cols] (MT_F32 or MT_BF16) receives X: singular vectors kept,
+ * singular values taken through the polynomial (with the quintic, five steps:
+ * from 1e-2 of the norm up to between 0.7 and 1.2). Products are made of fp16
+ * operands with fp32 sums, with X carried in 22 bits: O is within about 1e-3
+ * (relative, Frobenius) of exact arithmetic for the quintic's 5 or 6 steps
+ * before its own rounding. A zero matrix gives zeros, one with an infinity or
+ * a NaN (or whose squares' sum passes fp32) NaN throughout; the others of the
+ * batch are not touched by it. Singular values have to stay below 15 in every
+ * step (fp16's range). Any rows and cols up to 2^16, batch up to 4096, steps
+ * 1 to 32, |coef| up to 100, eps >= 0. workspace: bytes, 256-byte aligned (0
+ * for sizes that are refused). O may be G where the types are the same.
+ * Deterministic. */
+size_t mt_op_orthogonalize_workspace(int batch, int rows, int cols);
+int mt_op_orthogonalize(const void* G, int g_dtype, void* O, int o_dtype, const float* coef, int steps, float eps,
+                        void* workspace, int batch, int rows, int cols, void* stream);
+
+/* The Muon optimiser's step on device-resident matrices (the host AdamW above
+ * is for everything else: gains, embedding, head):
+ *   M <- mu M + G,  U = G + mu M (nesterov != 0) or M,  X = U orthogonalised,
+ *   W <- W - lr (scale X + weight_decay W)
+ * W [batch, rows, cols] MT_F32 or MT_BF16, M fp32, both updated in place; G is
+ * read. scale is the caller's (0.2 sqrt(max(rows, cols)) gives X the size of
+ * an Adam step). mu in [0, 1). Workspace, coef, steps, eps and limits as
+ * above; W, M and G do not overlap. */
+int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype, float mu, int nesterov, float lr,
+                      float weight_decay, float scale, const float* coef, int steps, float eps, void* workspace,
+                      int batch, int rows, int cols, void* stream);
+
 /* Device error word of the kernels (barrier timeouts, token ids outside the
  * vocabulary etc.): returns and clears it (0 = none). Synchronizes the
  * device. */

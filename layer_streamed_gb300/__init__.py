@@ -51,7 +51,8 @@ EXPORTS = ("mt_packed_bytes", "mt_tensor_offset", "mt_required_budget", "mt_crea
            "mt_op_rmsnorm_bwd_ckpt8_workspace", "mt_op_rmsnorm_bwd_ckpt8", "mt_op_swiglu_fwd_ckpt8",
            "mt_op_swiglu_bwd_ckpt8", "mt_op_token_logprobs", "mt_op_token_logprobs_bwd", "mt_op_embed_fwd",
            "mt_op_embed_bwd_workspace", "mt_op_embed_bwd", "mt_op_linear_ce_fwd_workspace", "mt_op_linear_ce_fwd",
-           "mt_op_linear_ce_bwd_workspace", "mt_op_linear_ce_bwd")
+           "mt_op_linear_ce_bwd_workspace", "mt_op_linear_ce_bwd", "mt_op_orthogonalize_workspace", "mt_op_orthogonalize",
+           "mt_op_muon_update")
 
 
 class MtError(RuntimeError):
@@ -184,6 +185,9 @@ def lib() -> ctypes.CDLL:
         "mt_op_linear_ce_fwd_workspace": (sz, [i32, i32, i32]),
         "mt_op_linear_ce_fwd": (i32, [vp, vp, vp, f32, f32, f32, vp, vp, vp] + [i32] * 5 + [vp]),
         "mt_op_linear_ce_bwd_workspace": (sz, [i32, i32, i32]),
+        "mt_op_orthogonalize_workspace": (sz, [i32, i32, i32]),
+        "mt_op_orthogonalize": (i32, [vp, i32, vp, i32, vp, i32, f32, vp, i32, i32, i32, vp]),
+        "mt_op_muon_update": (i32, [vp, i32, vp, vp, i32, f32, i32, f32, f32, f32, vp, i32, f32, vp, i32, i32, i32, vp]),
         "mt_op_linear_ce_bwd": (i32, [vp, vp, vp, f32, f32, f32, vp, vp, vp, i32, vp, i32, i32, vp] + [i32] * 5 + [vp]),
     }
     for name, (res, args) in sig.items():
@@ -741,6 +745,37 @@ def mt_op_linear_ce_bwd(X, W, labels, logit_scale, smoothing, z_coef, lse, g_los
     _check(lib().mt_op_linear_ce_bwd(_ptr(X), _ptr(W), _ptr(labels), logit_scale, smoothing, z_coef, _ptr(lse),
                                      _ptr(g_loss), _ptr(dX), dx_dtype, _ptr(dW), dw_dtype, int(accumulate),
                                      _ptr(workspace), T, V, h, ldx, ldw, _stream(stream)))
+
+
+def _coef(coef, steps):
+    """(steps, 3) Newton-Schulz coefficients as a host array, or None."""
+    if coef is None:
+        return None
+    a = np.ascontiguousarray(coef, dtype=np.float32).reshape(-1)
+    if a.size != 3 * steps:
+        raise MtError(MT_ERR_ARG, f"{a.size} coefficients for {steps} steps of three")
+    return a
+
+
+def mt_op_orthogonalize_workspace(batch, rows, cols) -> int:
+    return lib().mt_op_orthogonalize_workspace(batch, rows, cols)
+
+
+def mt_op_orthogonalize(G, g_dtype, O, o_dtype, coef, steps, eps, workspace, batch, rows, cols, stream=None):
+    """Orthogonalised form of each matrix of a batch by Newton-Schulz steps;
+    coef: None (Muon's quintic) or (steps, 3) numbers (see include/mt.h)."""
+    c = _coef(coef, steps)
+    _check(lib().mt_op_orthogonalize(_ptr(G), g_dtype, _ptr(O), o_dtype, None if c is None else c.ctypes.data, steps,
+                                     eps, _ptr(workspace), batch, rows, cols, _stream(stream)))
+
+
+def mt_op_muon_update(W, w_dtype, M, G, g_dtype, mu, nesterov, lr, weight_decay, scale, coef, steps, eps, workspace,
+                      batch, rows, cols, stream=None):
+    """Momentum M and weights W updated in place by the Muon optimiser."""
+    c = _coef(coef, steps)
+    _check(lib().mt_op_muon_update(_ptr(W), w_dtype, _ptr(M), _ptr(G), g_dtype, mu, int(nesterov), lr, weight_decay,
+                                   scale, None if c is None else c.ctypes.data, steps, eps, _ptr(workspace), batch,
+                                   rows, cols, _stream(stream)))
 
 
 def mt_op_device_error() -> int:

@@ -197,6 +197,17 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
                   void* work, int T, int V, int h, int ldx, int ldw, cudaStream_t st);
 uint32_t linear_ce_take_device_error();
 
+// Orthogonalised matrices and momentum (muon.cu). With M: M <- mu M + G and
+// U = G + mu M (nesterov) or M, else U = G; out = X, the result of `steps`
+// Newton-Schulz steps with coef [steps][3] from U / (|U| + eps), or with
+// update out <- keep * out - step * X.
+bool orthogonalize_dims(int batch, int rows, int cols);
+size_t orthogonalize_workspace(int batch, int rows, int cols);
+int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov, void* out, bool out_bf16, bool update,
+                  float keep, float step, const float* coef, int steps, float eps, void* work, int batch, int rows,
+                  int cols, cudaStream_t st);
+uint32_t muon_take_device_error();
+
 // Read and clear the device error words of the kernels that wait on
 // barriers (0 = no error). Synchronous with respect to the device.
 uint32_t gemm_take_device_error();

@@ -1,0 +1,540 @@
+// Orthogonalised updates of weight matrices (Muon): momentum, then an
+// approximate polar factor of it by Newton-Schulz products, then the step.
+//
+//   M <- mu M + G,  U = G + mu M (Nesterov) or M
+//   X <- U / (|U|_F + eps);  steps times:  A = X X^T,  X <- a X + (b A + c A^2) X
+//   W <- W - lr (scale X + decay W)
+//
+// (A = X^T X and X (b A + c A^2) where there are more rows than columns: the
+// square matrices are always as small as they can be, and nothing is
+// transposed, the products read X by rows or by columns as they need it.)
+//
+// Numbers. The products' operands are fp16 with power-of-two scales (X 2^10,
+// the square matrices 2^8: fp16's normal range then covers them from 2^-24
+// and 2^-22 of their largest values up), the sums fp32. Two things keep an
+// operand's rounding (2^-12) from being what the result is off by:
+//  - X itself is carried as two fp16 values, hi + lo (22 bits). Only hi is
+//    multiplied; a X is formed from both. Directions in which X is small grow
+//    by a factor a a step (3.44^5 = 485): with hi alone their rounding would
+//    grow with them, and it is what momentum of low rank ends in (4e-2 of the
+//    result in a float64 model of these roundings, 1e-3 with both).
+//  - A's and B = b A + c A^2's diagonals stay fp32, beside matrices whose
+//    diagonal is zero: with D the diagonal and O the rest, A^2 = O^2 + (d_i +
+//    d_j) O + D^2, and B X = (B's rest) X + d X. Diagonals are near to each
+//    other and to 1, so their rounding errors would all point the same way
+//    (2.7e-3 of the result in that model, 0.8e-3 so). lo gets half of d: all
+//    of it where X is flat, none where B takes lo's direction to zero.
+// Together 0.2e-3 to 1.4e-3 of the result against exact arithmetic (bf16
+// products: 1e-2 to 3e-2, and 3e-1 at low rank), below what rounding the
+// result to bf16 costs (1.7e-3).
+//
+// m n^2-like work: 3 m^2 n + m^3 operations a step (m <= n), the symmetric
+// products made on and above the diagonal only and mirrored by the epilogue,
+// which also forms every linear combination: nothing runs between products.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "tile_product.cuh"
+
+namespace mt {
+
+MT_DEVICE_ERROR_READER(muon_take_device_error)
+
+namespace {
+
+constexpr float kXUp = 1024.f, kXDown = 1.f / 1024.f;  // X in fp16
+constexpr float kAUp = 256.f, kADown = 1.f / 256.f;    // the square matrices
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t w) { return __half22float2(*(const __half2*)&w); }
+__device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__float2half_rn(f)); }
+__device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
+
+// Eight fp16 values at a 16-byte boundary.
+__device__ __forceinline__ void load8h(const uint16_t* p, float* v) {
+  const uint4 w = *(const uint4*)p;
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack_h2(ws[e]);
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8h(uint16_t* p, const float* v) {
+  *(uint4*)p = make_uint4(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]), pack_h2(v[4], v[5]), pack_h2(v[6], v[7]));
+}
+// The columns [col, col + n) of a row of a square matrix, n <= 32, and those
+// entries of the columns they mirror. Rows are padded to whole 64 columns, so
+// groups of eight that begin inside the matrix can be written whole.
+__device__ __forceinline__ void store_square(uint16_t* mat, int64_t ld, int row, int col, int N, bool mirror,
+                                             const float (&v)[32]) {
+  uint16_t* p = mat + (size_t)row * ld + col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + 8 * i < N) store8h(p + 8 * i, v + 8 * i);
+  if (mirror) {  // a column of the mirror image: neighbouring lanes, neighbouring addresses
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < N) mat[(size_t)(col + i) * ld + row] = f2h(v[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Momentum and the norm of the update
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float load1(const void* p, size_t i, bool bf16) {
+  return bf16 ? bf2f(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+}
+__device__ __forceinline__ void load4(const void* p, size_t i, bool bf16, float (&v)[4]) {
+  if (bf16) {
+    const uint2 w = *(const uint2*)((const uint16_t*)p + i);
+    v[0] = bf2f(w.x & 0xffff), v[1] = bf2f(w.x >> 16), v[2] = bf2f(w.y & 0xffff), v[3] = bf2f(w.y >> 16);
+  } else {
+    const float4 w = *(const float4*)((const float*)p + i);
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+  }
+}
+
+__device__ __forceinline__ float block_sum256(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = threadIdx.x < 8 ? red[threadIdx.x] : 0.f;
+  return warp_sum(v);  // in warp 0
+}
+
+// M <- mu M + G where there is an M, and a block's part of the sum of U^2.
+// Block (x, y) takes every gridDim.x-th group of values of matrix y.
+template <bool VEC>
+__global__ void __launch_bounds__(256) momentum_kernel(const void* G, bool bf16, float* M, float mu, int nesterov,
+                                                       int64_t n, float* part) {
+  __shared__ float red[8];
+  grid_wait();
+  grid_release();
+  constexpr int E = VEC ? 4 : 1;
+  const size_t base = (size_t)blockIdx.y * n;
+  const int64_t step = (int64_t)gridDim.x * 256 * E;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E; i < n; i += step) {
+    float g[4], m[4];
+    if (VEC) load4(G, base + i, bf16, g);
+    else g[0] = load1(G, base + i, bf16);
+    if (M) {
+      if (VEC) load4(M, base + i, false, m);
+      else m[0] = M[base + i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        m[e] = fmaf(mu, m[e], g[e]);
+        g[e] = nesterov ? fmaf(mu, m[e], g[e]) : m[e];
+      }
+      if (VEC) *(float4*)(M + base + i) = make_float4(m[0], m[1], m[2], m[3]);
+      else M[base + i] = m[0];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum = fmaf(g[e], g[e], sum);
+  }
+  sum = block_sum256(sum, red);
+  if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+}
+
+// X = U / (|U| + eps) as hi + lo. VEC: rows are whole groups of eight values
+// on their boundary.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+    normalise_kernel(const void* G, bool bf16, const float* M, float mu, int nesterov, int rows, int cols, int64_t ld,
+                     const float* part, int parts, float eps, uint16_t* hi, uint16_t* lo) {
+  __shared__ float red[8];
+  __shared__ float inv_s;
+  grid_wait();
+  grid_release();
+  const size_t b = blockIdx.y;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < parts; i += 256) s += part[b * parts + i];
+  s = block_sum256(s, red);
+  if (threadIdx.x == 0) {
+    const float norm = sqrtf(s) + eps;
+    // a zero matrix stays zero; an infinite norm (or a NaN) stands for NaN throughout
+    inv_s = norm < INFINITY ? (norm > 0.f ? kXUp / norm : 0.f) : __uint_as_float(0x7fffffffu);
+  }
+  __syncthreads();
+  const float inv = inv_s;
+  const size_t in0 = b * rows * (size_t)cols, out0 = b * rows * (size_t)ld;
+  const int per_row = (cols + 7) / 8;
+  const int64_t all = (int64_t)rows * per_row;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
+    const int r = (int)(u / per_row), c = (int)(u - (int64_t)r * per_row) * 8;
+    const size_t at = in0 + (size_t)r * cols + c;
+    float v[8], l[8];
+#pragma unroll
+    for (int q = 0; q < 8; q += 4) {
+      float g[4], m[4];
+      if (VEC) {
+        load4(G, at + q, bf16, g);
+        if (M) load4(M, at + q, false, m);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = c + q + e < cols;
+          g[e] = in ? load1(G, at + q + e, bf16) : 0.f;
+          m[e] = in && M ? M[at + q + e] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q + e] = M ? (nesterov ? fmaf(mu, m[e], g[e]) : m[e]) : g[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] *= inv;
+      l[e] = v[e] - h2f(f2h(v[e]));
+    }
+    const size_t o = out0 + (size_t)r * ld + c;
+    store8h(hi + o, v);
+    store8h(lo + o, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues
+// ---------------------------------------------------------------------------
+// A = X X^T: the rest of A to fp16, its diagonal to fp32.
+struct GramEpi {
+  struct Args {
+    uint16_t* O;
+    float* d;
+    int64_t ld, dpad;  // row stride; diagonal entries of a matrix
+  };
+  struct Row {};
+  static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
+                                              uint32_t tb) {
+    uint16_t* mat = a.O + (size_t)at.b * s.M * a.ld;
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      const int col = at.n0 + c * 32;
+      if (col >= s.N) break;
+      float v[32];
+      tile_chunk(tb, c, v);
+      if (at.row >= s.M) continue;
+      const int here = at.row - col;  // the diagonal's place among the 32
+      if (here >= 0 && here < 32) {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (i == here) {
+            d = v[i];
+            v[i] = 0.f;
+          }
+        }
+        a.d[at.b * a.dpad + at.row] = d * (kXDown * kXDown);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= kAUp * kXDown * kXDown;
+      store_square(mat, a.ld, at.row, col, s.N, at.mirror, v);
+    }
+  }
+};
+
+// B = b A + c A^2 from O O^T, O and the diagonal.
+struct PolyEpi {
+  struct Args {
+    const uint16_t* O;
+    const float* d;
+    uint16_t* B;
+    float* db;
+    int64_t ld, dpad;
+    float b, c;
+  };
+  struct Row {
+    float d;
+  };
+  static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
+    r.d = at.row < s.M ? a.d[at.b * a.dpad + at.row] : 0.f;
+  }
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              uint32_t tb) {
+    const size_t mat = (size_t)at.b * s.M * a.ld;
+    const float* dcol = a.d + at.b * a.dpad;
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      const int col = at.n0 + c * 32;
+      if (col >= s.N) break;
+      float o[32], dj[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = dj[i] = 0.f;
+      if (at.row < s.M) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col + 8 * i >= s.N) break;  // the padding behind it holds finite values or is not used
+          load8h(a.O + mat + (size_t)at.row * a.ld + col + 8 * i, o + 8 * i);
+          load4(dcol, col + 8 * i, false, *(float(*)[4])(dj + 8 * i));
+          load4(dcol, col + 8 * i + 4, false, *(float(*)[4])(dj + 8 * i + 4));
+        }
+      }
+      float v[32];
+      tile_chunk(tb, c, v);
+      if (at.row >= s.M) continue;
+      const int here = at.row - col;
+      if (here >= 0 && here < 32) {
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i == here) sq = v[i];
+        a.db[at.b * a.dpad + at.row] = r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown));
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = fmaf(a.c, fmaf(r.d + dj[i], o[i], v[i] * kADown), a.b * o[i]);
+        if (i == here) v[i] = 0.f;
+      }
+      store_square(a.B + mat, a.ld, at.row, col, s.N, at.mirror, v);
+    }
+  }
+};
+
+// X <- a X + B X; the last step leaves the result or takes the weights' step.
+template <bool LAST>
+struct ApplyEpi {
+  struct Args {
+    const uint16_t* hi;
+    uint16_t* lo;       // in place
+    uint16_t* hi_out;   // not LAST
+    const float* db;
+    int64_t ld, dpad;
+    float a;
+    int by_col;         // the diagonal runs along the columns (X B) or the rows (B X)
+    // LAST: out [M, N] dense per matrix, out <- keep * out - step * X with
+    // update, else X
+    void* out;
+    int out_bf16, update, vec;
+    float keep, step;
+  };
+  struct Row {
+    float d;
+  };
+  static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
+    r.d = !a.by_col && at.row < s.M ? a.db[at.b * a.dpad + at.row] : 0.f;
+  }
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              uint32_t tb) {
+    const size_t x0 = ((size_t)at.b * s.M + at.row) * a.ld;
+    const float* dcol = a.db + at.b * a.dpad;
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      const int col = at.n0 + c * 32;
+      if (col >= s.N) break;
+      uint4 h4[4], l4[4];
+      if (at.row < s.M) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col + 8 * i >= s.N) break;
+          h4[i] = *(const uint4*)(a.hi + x0 + col + 8 * i);
+          l4[i] = *(const uint4*)(a.lo + x0 + col + 8 * i);
+        }
+      }
+      float v[32];
+      tile_chunk(tb, c, v);
+      if (at.row >= s.M) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col + 8 * i >= s.N) break;
+        const int cc = col + 8 * i;
+        float h[8], l[8], d[8];
+        const uint32_t hw[4] = {h4[i].x, h4[i].y, h4[i].z, h4[i].w}, lw[4] = {l4[i].x, l4[i].y, l4[i].z, l4[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 p = unpack_h2(hw[e]), q = unpack_h2(lw[e]);
+          h[2 * e] = p.x, h[2 * e + 1] = p.y, l[2 * e] = q.x, l[2 * e + 1] = q.y;
+        }
+        if (a.by_col) {
+          load4(dcol, cc, false, *(float(*)[4])d);
+          load4(dcol, cc + 4, false, *(float(*)[4])(d + 4));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = r.d;
+        }
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = fmaf(a.a + d[e], h[e], fmaf(fmaf(0.5f, d[e], a.a), l[e], v[8 * i + e] * kADown));
+        if (!LAST) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) l[e] = x[e] - h2f(f2h(x[e]));
+          store8h(a.hi_out + x0 + cc, x);
+          store8h(a.lo + x0 + cc, l);
+        } else {
+          const size_t o = ((size_t)at.b * s.M + at.row) * s.N + cc;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= kXDown;
+          if (a.vec) {
+            if (a.update) {
+              float w[8];
+              load4(a.out, o, a.out_bf16, *(float(*)[4])w);
+              load4(a.out, o + 4, a.out_bf16, *(float(*)[4])(w + 4));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = fmaf(a.keep, w[e], -a.step * x[e]);
+            }
+            if (a.out_bf16) {
+              *(uint4*)((uint16_t*)a.out + o) =
+                  make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+            } else {
+              *(float4*)((float*)a.out + o) = make_float4(x[0], x[1], x[2], x[3]);
+              *(float4*)((float*)a.out + o + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (cc + e >= s.N) break;
+              const float r1 = a.update ? fmaf(a.keep, load1(a.out, o + e, a.out_bf16), -a.step * x[e]) : x[e];
+              if (a.out_bf16) ((uint16_t*)a.out)[o + e] = f2bf(r1);
+              else ((float*)a.out)[o + e] = r1;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Blocks that share the sum of a matrix's squares: one per 8192 values, as
+// many as eight on every SM.
+int norm_parts(int64_t n) { return (int)std::min<int64_t>((n + 8191) / 8192, 152 * 8); }
+
+struct Ws {
+  size_t part, hi[2], lo, o, b, d, db, total;
+  int m, parts;
+  int64_t ldx, lda, dpad;
+};
+Ws workspace(int batch, int rows, int cols) {
+  Ws w;
+  w.m = std::min(rows, cols);
+  w.ldx = (int64_t)up(cols, 64);
+  w.lda = (int64_t)up(w.m, 64);
+  w.dpad = w.lda;
+  w.parts = norm_parts((int64_t)rows * cols);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += up(n, 256);
+    return r;
+  };
+  w.part = take((size_t)batch * w.parts * 4);
+  const size_t x = (size_t)batch * rows * w.ldx * 2, a = (size_t)batch * w.m * w.lda * 2;
+  w.hi[0] = take(x);
+  w.hi[1] = take(x);
+  w.lo = take(x);
+  w.o = take(a);
+  w.b = take(a);
+  w.d = take((size_t)batch * w.dpad * 4);
+  w.db = take((size_t)batch * w.dpad * 4);
+  w.total = at;
+  return w;
+}
+
+// D = A B^T of fp16 matrices in a batch, tiles by how many there are.
+struct Operand {
+  const void* p;
+  int rows, cols;
+  int64_t ld;
+};
+template <bool A_MN, bool B_MN, bool SYM, class E>
+cudaError_t product(const Operand& A, const Operand& B, int M, int N, int K, int batch, const typename E::Args& args,
+                    cudaStream_t st) {
+  auto go = [&](auto cfg) {
+    using C = decltype(cfg);
+    CUtensorMap ta, tb;
+    if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(), true) ||
+        !product_map(&tb, B.p, B.rows, B.cols, B.ld, B.ld * B.rows, batch, b_box<C>(), true))
+      return cudaErrorUnknown;
+    return launch_product<C, E>(ta, tb, product_shape<C>(M, N, K, batch), args, st);
+  };
+  using Wide = ProductCfg<256, true, A_MN, B_MN, true, SYM>;
+  // 256 x 256 tiles on SM pairs where they fill half of the pairs, else 128 x 128 on single SMs
+  const ProductShape w = product_shape<Wide>(M, N, K, batch);
+  if ((int64_t)w.tiles * batch >= mt_host::num_sms() / 4) return go(Wide());
+  return go(ProductCfg<128, false, A_MN, B_MN, true, SYM>());
+}
+
+}  // namespace
+
+bool orthogonalize_dims(int batch, int rows, int cols) {
+  return batch > 0 && rows > 0 && cols > 0 && batch <= 4096 && rows <= (1 << 16) && cols <= (1 << 16) &&
+         (int64_t)rows * cols * batch <= ((int64_t)1 << 40);
+}
+size_t orthogonalize_workspace(int batch, int rows, int cols) { return workspace(batch, rows, cols).total; }
+
+int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov, void* out, bool out_bf16, bool update,
+                  float keep, float step, const float* coef, int steps, float eps, void* work, int batch, int rows,
+                  int cols, cudaStream_t st) {
+  const Ws w = workspace(batch, rows, cols);
+  uint8_t* base = (uint8_t*)work;
+  float* part = (float*)(base + w.part);
+  uint16_t* hi[2] = {(uint16_t*)(base + w.hi[0]), (uint16_t*)(base + w.hi[1])};
+  uint16_t *lo = (uint16_t*)(base + w.lo), *O = (uint16_t*)(base + w.o), *B = (uint16_t*)(base + w.b);
+  float *d = (float*)(base + w.d), *db = (float*)(base + w.db);
+  const int64_t n = (int64_t)rows * cols;
+  const size_t gs = g_bf16 ? 8 : 16;
+  const bool flat = n % 4 == 0 && al(G, gs) && al(M, 16);
+  const dim3 pg((unsigned)w.parts, (unsigned)batch);
+  cudaError_t e = mt_host::launch_early(flat ? momentum_kernel<true> : momentum_kernel<false>, pg, 256, 0, st, 1, G,
+                                        g_bf16, M, mu, (int)nesterov, n, part);
+  const bool whole = cols % 8 == 0 && al(G, gs) && al(M, 16);
+  if (e == cudaSuccess)
+    e = mt_host::launch_early(whole ? normalise_kernel<true> : normalise_kernel<false>, pg, 256, 0, st, 1, G, g_bf16,
+                              (const float*)M, mu, (int)nesterov, rows, cols, w.ldx, (const float*)part, w.parts, eps,
+                              hi[0], lo);
+  count_launches(2);
+  const bool tall = rows > cols;
+  const int m = w.m;
+  const Operand o{O, m, m, w.lda}, p{B, m, m, w.lda};
+  for (int i = 0; i < steps && e == cudaSuccess; ++i) {
+    const float *c = coef + 3 * i;
+    const Operand x{hi[i & 1], rows, cols, w.ldx};
+    const GramEpi::Args ga{O, d, w.lda, w.dpad};
+    e = tall ? product<true, true, true, GramEpi>(x, x, m, m, rows, batch, ga, st)
+             : product<false, false, true, GramEpi>(x, x, m, m, cols, batch, ga, st);
+    if (e != cudaSuccess) break;
+    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{O, d, B, db, w.lda, w.dpad, c[1], c[2]},
+                                             st);
+    if (e != cudaSuccess) break;
+    auto apply = [&](auto epi) {
+      using E = decltype(epi);
+      typename E::Args a{};
+      a.hi = hi[i & 1];
+      a.lo = lo;
+      a.hi_out = hi[(i + 1) & 1];
+      a.db = db;
+      a.ld = w.ldx;
+      a.dpad = w.dpad;
+      a.a = c[0];
+      a.by_col = tall;
+      a.out = out;
+      a.out_bf16 = out_bf16;
+      a.update = update;
+      a.vec = cols % 8 == 0 && al(out, 16);
+      a.keep = keep;
+      a.step = step;
+      return tall ? product<false, false, false, E>(x, p, rows, cols, m, batch, a, st)
+                  : product<false, true, false, E>(p, x, rows, cols, m, batch, a, st);
+    };
+    e = i + 1 < steps ? apply(ApplyEpi<false>()) : apply(ApplyEpi<true>());
+  }
+  return e == cudaSuccess ? 0 : kLaunchFailed;
+}
+
+}  // namespace mt

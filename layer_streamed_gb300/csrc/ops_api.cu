@@ -475,10 +475,63 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
                               V, h, ldx, ldw, S(stream)));
 }
 
+namespace {
+constexpr int kMaxNsSteps = 32;
+// The quintic of the Muon optimiser: singular values from about 1e-2 up end
+// between 0.7 and 1.2 after five steps.
+constexpr float kQuintic[3] = {3.4445f, -4.7750f, 2.0315f};
+struct NsCoef {
+  float c[3 * kMaxNsSteps];
+  bool ok = false;
+  NsCoef(const float* given, int steps) {
+    if (steps < 1 || steps > kMaxNsSteps) return;
+    ok = true;
+    for (int i = 0; i < 3 * steps; ++i) {
+      c[i] = given ? given[i] : kQuintic[i % 3];
+      ok = ok && c[i] >= -100.f && c[i] <= 100.f;
+    }
+  }
+};
+bool on_elements(const void* p, int dtype) { return ((uintptr_t)p & (dtype == MT_BF16 ? 1 : 3)) == 0; }
+}  // namespace
+
+size_t mt_op_orthogonalize_workspace(int batch, int rows, int cols) {
+  return orthogonalize_dims(batch, rows, cols) ? orthogonalize_workspace(batch, rows, cols) : 0;
+}
+
+int mt_op_orthogonalize(const void* G, int g_dtype, void* O, int o_dtype, const float* coef, int steps, float eps,
+                        void* workspace, int batch, int rows, int cols, void* stream) {
+  if (!G || !O || !workspace || !f32_or_bf16(g_dtype) || !f32_or_bf16(o_dtype) || !on_elements(G, g_dtype) ||
+      !on_elements(O, o_dtype) || ((uintptr_t)workspace & 255) || !orthogonalize_dims(batch, rows, cols) ||
+      !(eps >= 0.f && eps <= 1e30f))
+    return MT_ERR_ARG;
+  const NsCoef c(coef, steps);
+  if (!c.ok) return MT_ERR_ARG;
+  return own_rc(orthogonalize(G, g_dtype == MT_BF16, nullptr, 0.f, false, O, o_dtype == MT_BF16, false, 0.f, 0.f, c.c,
+                              steps, eps, workspace, batch, rows, cols, S(stream)));
+}
+
+int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype, float mu, int nesterov, float lr,
+                      float weight_decay, float scale, const float* coef, int steps, float eps, void* workspace,
+                      int batch, int rows, int cols, void* stream) {
+  auto number = [](float v) { return v >= -1e30f && v <= 1e30f; };
+  if (!W || !M || !G || !workspace || !f32_or_bf16(w_dtype) || !f32_or_bf16(g_dtype) || !on_elements(W, w_dtype) ||
+      !on_elements(G, g_dtype) || !on_words(M) || ((uintptr_t)workspace & 255) ||
+      !orthogonalize_dims(batch, rows, cols) || !(eps >= 0.f && eps <= 1e30f) || !(mu >= 0.f && mu < 1.f) ||
+      !number(lr) || !number(weight_decay) || !number(scale))
+    return MT_ERR_ARG;
+  const NsCoef c(coef, steps);
+  if (!c.ok) return MT_ERR_ARG;
+  return own_rc(orthogonalize(G, g_dtype == MT_BF16, M, mu, nesterov != 0, W, w_dtype == MT_BF16, true,
+                              1.f - lr * weight_decay, lr * scale, c.c, steps, eps, workspace, batch, rows, cols,
+                              S(stream)));
+}
+
 int mt_op_device_error(void) {
   cudaDeviceSynchronize();
   return (int)(gemm_take_device_error() | attention_tc_take_device_error() | ckpt8_take_device_error() |
-               token_logprobs_take_device_error() | embedding_take_device_error() | linear_ce_take_device_error());
+               token_logprobs_take_device_error() | embedding_take_device_error() |
+               linear_ce_take_device_error() | muon_take_device_error());
 }
 
 }  // extern "C"
