@@ -676,6 +676,30 @@ int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype
                       float weight_decay, float scale, const float* coef, int steps, float eps, void* workspace,
                       int batch, int rows, int cols, void* stream);
 
+/* The norms around a block's end (as in decoders that also normalise what a
+ * block puts out): with y the block's output and gate its gate's values
+ * (y_dtype MT_F32 or MT_BF16 both, [T, h]; gate null: 1), x fp32 the residual,
+ *   x_out = alpha x + sigmoid(gate) * (w_post * y * rstd_post),  rstd_post = 1/sqrt(mean(y^2) + eps)
+ *   n_out = bf16(w_pre * x_out * rstd_pre),                      rstd_pre = 1/sqrt(mean(x_out^2) + eps)
+ * x_out fp32 [T, h] (may be x), n_out bf16 [T, h], rstd_post, rstd_pre fp32 [T],
+ * w_post, w_pre fp32 [h]. h a multiple of 4 up to 8192, T up to 2^30, eps >= 0.
+ * fp32 arrays 16-byte aligned (rstd and the weights' gradients 4), bf16 ones 8. */
+int mt_op_sandwich_norm_fwd(const float* x, const void* y, const void* gate, int y_dtype, const float* w_post,
+                            const float* w_pre, float alpha, float eps, float* x_out, void* n_out, float* rstd_post,
+                            float* rstd_pre, int T, int h, void* stream);
+
+/* Its gradients, for dn fp32 [T, h] of n_out and dres fp32 [T, h] (null: 0) of
+ * x_out: dx fp32 (may be dres), dy and dgate in y's type (dgate null exactly
+ * where gate is), dw_post, dw_pre fp32 [h] (fixed-order sums; workspace fp32
+ * of mt_op_sandwich_norm_bwd_workspace(T, h) floats, 0 for sizes that are
+ * refused, 16-byte aligned). x_out, rstd_post and rstd_pre as the forward left
+ * them. A sigmoid below 2^-126 counts as 0. Deterministic. */
+size_t mt_op_sandwich_norm_bwd_workspace(int T, int h);
+int mt_op_sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, int y_dtype, const float* w_post,
+                            const float* w_pre, float alpha, const float* rstd_post, const float* rstd_pre,
+                            const float* dn, const float* dres, float* dx, void* dy, void* dgate, float* dw_post,
+                            float* dw_pre, float* workspace, int T, int h, void* stream);
+
 /* Device error word of the kernels (barrier timeouts, token ids outside the
  * vocabulary etc.): returns and clears it (0 = none). Synchronizes the
  * device. */

@@ -52,7 +52,8 @@ EXPORTS = ("mt_packed_bytes", "mt_tensor_offset", "mt_required_budget", "mt_crea
            "mt_op_swiglu_bwd_ckpt8", "mt_op_token_logprobs", "mt_op_token_logprobs_bwd", "mt_op_embed_fwd",
            "mt_op_embed_bwd_workspace", "mt_op_embed_bwd", "mt_op_linear_ce_fwd_workspace", "mt_op_linear_ce_fwd",
            "mt_op_linear_ce_bwd_workspace", "mt_op_linear_ce_bwd", "mt_op_orthogonalize_workspace", "mt_op_orthogonalize",
-           "mt_op_muon_update")
+           "mt_op_muon_update", "mt_op_sandwich_norm_fwd", "mt_op_sandwich_norm_bwd_workspace",
+           "mt_op_sandwich_norm_bwd")
 
 
 class MtError(RuntimeError):
@@ -185,6 +186,9 @@ def lib() -> ctypes.CDLL:
         "mt_op_linear_ce_fwd_workspace": (sz, [i32, i32, i32]),
         "mt_op_linear_ce_fwd": (i32, [vp, vp, vp, f32, f32, f32, vp, vp, vp] + [i32] * 5 + [vp]),
         "mt_op_linear_ce_bwd_workspace": (sz, [i32, i32, i32]),
+        "mt_op_sandwich_norm_fwd": (i32, [vp, vp, vp, i32, vp, vp, f32, f32, vp, vp, vp, vp, i32, i32, vp]),
+        "mt_op_sandwich_norm_bwd_workspace": (sz, [i32, i32]),
+        "mt_op_sandwich_norm_bwd": (i32, [vp, vp, vp, i32, vp, vp, f32] + [vp] * 10 + [i32, i32, vp]),
         "mt_op_orthogonalize_workspace": (sz, [i32, i32, i32]),
         "mt_op_orthogonalize": (i32, [vp, i32, vp, i32, vp, i32, f32, vp, i32, i32, i32, vp]),
         "mt_op_muon_update": (i32, [vp, i32, vp, vp, i32, f32, i32, f32, f32, f32, vp, i32, f32, vp, i32, i32, i32, vp]),
@@ -776,6 +780,28 @@ def mt_op_muon_update(W, w_dtype, M, G, g_dtype, mu, nesterov, lr, weight_decay,
     _check(lib().mt_op_muon_update(_ptr(W), w_dtype, _ptr(M), _ptr(G), g_dtype, mu, int(nesterov), lr, weight_decay,
                                    scale, None if c is None else c.ctypes.data, steps, eps, _ptr(workspace), batch,
                                    rows, cols, _stream(stream)))
+
+
+def mt_op_sandwich_norm_fwd(x, y, gate, y_dtype, w_post, w_pre, alpha, eps, x_out, n_out, rstd_post, rstd_pre, T, h,
+                            stream=None):
+    """x_out = alpha x + sigmoid(gate) * rmsnorm(y, w_post), n_out =
+    rmsnorm(x_out, w_pre) (see include/mt.h)."""
+    _check(lib().mt_op_sandwich_norm_fwd(_ptr(x), _ptr(y), _ptr(gate), y_dtype, _ptr(w_post), _ptr(w_pre), alpha, eps,
+                                         _ptr(x_out), _ptr(n_out), _ptr(rstd_post), _ptr(rstd_pre), T, h,
+                                         _stream(stream)))
+
+
+def mt_op_sandwich_norm_bwd_workspace(T, h) -> int:
+    return lib().mt_op_sandwich_norm_bwd_workspace(T, h)
+
+
+def mt_op_sandwich_norm_bwd(x_out, y, gate, y_dtype, w_post, w_pre, alpha, rstd_post, rstd_pre, dn, dres, dx, dy, dgate,
+                            dw_post, dw_pre, workspace, T, h, stream=None):
+    """Gradients of mt_op_sandwich_norm_fwd for dn of n_out and dres of x_out."""
+    _check(lib().mt_op_sandwich_norm_bwd(_ptr(x_out), _ptr(y), _ptr(gate), y_dtype, _ptr(w_post), _ptr(w_pre), alpha,
+                                         _ptr(rstd_post), _ptr(rstd_pre), _ptr(dn), _ptr(dres), _ptr(dx), _ptr(dy),
+                                         _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(workspace), T, h,
+                                         _stream(stream)))
 
 
 def mt_op_device_error() -> int:

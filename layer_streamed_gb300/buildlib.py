@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmt.so")
 SOURCES = ["gemm.cu", "attention_tc.cu", "elementwise.cu", "moe.cu", "ckpt8.cu", "token_logprobs.cu",
-           "embedding.cu", "linear_ce.cu", "muon.cu", "runtime.cu", "ops_api.cu"]
+           "embedding.cu", "linear_ce.cu", "muon.cu", "sandwich_norm.cu",
+           "runtime.cu", "ops_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -208,6 +208,20 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
                   int cols, cudaStream_t st);
 uint32_t muon_take_device_error();
 
+// The norm after a block with its gate and the scaled residual, fused with
+// the norm before the next block (sandwich_norm.cu). gate and dres may be
+// null. work: sandwich_norm_bwd_partials floats, 16-byte aligned.
+bool sandwich_norm_dims(int T, int h);
+size_t sandwich_norm_bwd_partials(int T, int h);
+int sandwich_norm_fwd(const float* x, const void* y, const void* gate, bool bf16, const float* w_post,
+                      const float* w_pre, float alpha, float eps, float* x_out, uint16_t* n_out, float* rstd_post,
+                      float* rstd_pre, int T, int h, cudaStream_t st);
+int sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, bool bf16, const float* w_post,
+                      const float* w_pre, float alpha, const float* rstd_post, const float* rstd_pre, const float* dn,
+                      const float* dres, float* dx, void* dy, void* dgate, float* dw_post, float* dw_pre, float* work,
+                      int T, int h, cudaStream_t st);
+uint32_t sandwich_norm_take_device_error();
+
 // Read and clear the device error words of the kernels that wait on
 // barriers (0 = no error). Synchronous with respect to the device.
 uint32_t gemm_take_device_error();

@@ -527,11 +527,37 @@ int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype
                               S(stream)));
 }
 
+int mt_op_sandwich_norm_fwd(const float* x, const void* y, const void* gate, int y_dtype, const float* w_post,
+                            const float* w_pre, float alpha, float eps, float* x_out, void* n_out, float* rstd_post,
+                            float* rstd_pre, int T, int h, void* stream) {
+  if (!x || !y || !w_post || !w_pre || !x_out || !n_out || !rstd_post || !rstd_pre || !f32_or_bf16(y_dtype) ||
+      !on_words(rstd_post, rstd_pre) || !(eps >= 0.f && eps <= 1e30f) || !(alpha >= -1e30f && alpha <= 1e30f))
+    return MT_ERR_ARG;
+  return own_rc(sandwich_norm_fwd(x, y, gate, y_dtype == MT_BF16, w_post, w_pre, alpha, eps, x_out, (uint16_t*)n_out,
+                                  rstd_post, rstd_pre, T, h, S(stream)));
+}
+
+size_t mt_op_sandwich_norm_bwd_workspace(int T, int h) {
+  return sandwich_norm_dims(T, h) ? sandwich_norm_bwd_partials(T, h) : 0;
+}
+
+int mt_op_sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, int y_dtype, const float* w_post,
+                            const float* w_pre, float alpha, const float* rstd_post, const float* rstd_pre,
+                            const float* dn, const float* dres, float* dx, void* dy, void* dgate, float* dw_post,
+                            float* dw_pre, float* workspace, int T, int h, void* stream) {
+  if (!x_out || !y || !w_post || !w_pre || !rstd_post || !rstd_pre || !dn || !dx || !dy || !dw_post || !dw_pre ||
+      !workspace || !gate != !dgate || !f32_or_bf16(y_dtype) || !on_words(rstd_post, rstd_pre, dw_post, dw_pre) ||
+      !(alpha >= -1e30f && alpha <= 1e30f))
+    return MT_ERR_ARG;
+  return own_rc(sandwich_norm_bwd(x_out, y, gate, y_dtype == MT_BF16, w_post, w_pre, alpha, rstd_post, rstd_pre, dn,
+                                  dres, dx, dy, dgate, dw_post, dw_pre, workspace, T, h, S(stream)));
+}
+
 int mt_op_device_error(void) {
   cudaDeviceSynchronize();
   return (int)(gemm_take_device_error() | attention_tc_take_device_error() | ckpt8_take_device_error() |
                token_logprobs_take_device_error() | embedding_take_device_error() |
-               linear_ce_take_device_error() | muon_take_device_error());
+               linear_ce_take_device_error() | muon_take_device_error() | sandwich_norm_take_device_error());
 }
 
 }  // extern "C"
