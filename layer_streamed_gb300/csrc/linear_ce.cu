@@ -42,11 +42,14 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^(. - maximum); with smoothing the sum of the accumulators too; the
 // label's own logit.
 // ---------------------------------------------------------------------------
-struct StatsEpi {
+// Two warps a row of a tile, half of the columns each, hide each other's
+// latencies: with one, 8 us a tile of 256 x 256 against 4.2 us of MMAs at h = 1024.
+struct StatsEpi : NoSlabs {
+  static constexpr int WARPS = 8, SLABS = 0;
   struct Args {
     const int32_t* labels;
-    float2* part;  // [M][num_n]
-    float* sums;   // [M][num_n] or null
+    float2* part;  // [M][2 num_n]
+    float* sums;   // [M][2 num_n] or null
     float* zlab;   // [M]
     float scale;
   };
@@ -58,23 +61,21 @@ struct StatsEpi {
   }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              uint32_t tb) {
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
     const float k = a.scale * kLog2e;
     float m = -INFINITY, sum = 0.f, plain = 0.f;
     const int here = r.label - at.n0;  // the label's column in this tile, if it is one
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = w.part * (BN / 64); c < (w.part + 1) * (BN / 64); ++c) {
       if (at.n0 + c * 32 >= s.N) break;  // the same in every lane
       float v[32];
       tile_chunk(tb, c, v);
       if (a.sums) {
-        float p0 = 0.f, p1 = 0.f;  // columns past N hold zeros
+        float p[4] = {0.f, 0.f, 0.f, 0.f};  // columns past N hold zeros
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          p0 += v[i];
-          p1 += v[i + 1];
-        }
-        plain += p0 + p1;
+        for (int i = 0; i < 32; ++i) p[i & 3] += v[i];
+        plain += (p[0] + p[1]) + (p[2] + p[3]);
       }
       if (here >= c * 32 && here < c * 32 + 32 && at.row < s.M) {
         float z = 0.f;
@@ -87,24 +88,20 @@ struct StatsEpi {
         for (int i = 0; i < 32; ++i)
           if (at.n0 + c * 32 + i >= s.N) v[i] = -INFINITY;
       }
-      float cm = v[0];
+      float cm[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int i = 1; i < 32; ++i) cm = fmaxf(cm, v[i]);
-      cm *= k;
-      const float mn = fmaxf(m, cm);
+      for (int i = 4; i < 32; ++i) cm[i & 3] = fmaxf(cm[i & 3], v[i]);
+      const float mn = fmaxf(m, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])) * k);
       const float ref = mn == -INFINITY ? 0.f : mn;
-      float s0 = 0.f, s1 = 0.f;
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        s0 += ex2(fmaf(v[i], k, -ref));
-        s1 += ex2(fmaf(v[i + 1], k, -ref));
-      }
-      sum = sum * ex2(m - ref) + (s0 + s1);
+      for (int i = 0; i < 32; ++i) p[i & 3] += ex2(fmaf(v[i], k, -ref));
+      sum = sum * ex2(m - ref) + ((p[0] + p[1]) + (p[2] + p[3]));
       m = mn;
     }
     if (at.row < s.M) {
-      const size_t o = (size_t)at.row * s.num_n + at.nb;
-      a.part[o] = make_float2(m, sum);
+      const size_t o = (size_t)at.row * (2 * s.num_n) + 2 * at.nb + w.part;
+      a.part[o] = make_float2(m, sum);  // (-inf, 0) where the half lies past N
       if (a.sums) a.sums[o] = plain;
     }
   }
@@ -113,7 +110,7 @@ struct StatsEpi {
 // One warp a row: the tiles' pairs joined, the loss.
 __global__ void __launch_bounds__(256)
     join_rows_kernel(const float2* part, const float* sums, const float* zlab, const int32_t* labels, int T, int V,
-                     int num_n, float scale, float smooth, float zc, float* loss, float* lse_out) {
+                     int parts, float scale, float smooth, float zc, float* loss, float* lse_out) {
   grid_wait();
   grid_release();
   const int lane = threadIdx.x & 31;
@@ -127,14 +124,14 @@ __global__ void __launch_bounds__(256)
     }
     return;
   }
-  const float2* p = part + (size_t)row * num_n;
+  const float2* p = part + (size_t)row * parts;
   float m = -INFINITY, s = 0.f, plain = 0.f;
-  for (int i = lane; i < num_n; i += 32) {
+  for (int i = lane; i < parts; i += 32) {
     const float2 v = p[i];
     const float mn = fmaxf(m, v.x), ref = mn == -INFINITY ? 0.f : mn;
     s = s * ex2(m - ref) + v.y * ex2(v.x - ref);
     m = mn;
-    if (sums) plain += sums[(size_t)row * num_n + i];
+    if (sums) plain += sums[(size_t)row * parts + i];
   }
   const float top = warp_max(m), ref = top == -INFINITY ? 0.f : top;
   s = warp_sum(s * ex2(m - ref));
@@ -195,13 +192,14 @@ __device__ __forceinline__ void store8(void* base, size_t at, bool bf16, const f
 }
 
 // A piece's dz in bf16 (without the factor `scale`, which the next products'
-// epilogues apply), zero past its last column up to the row stride.
-struct GradEpi {
+// epilogues apply). Two warps a row as above, slabs of 64 columns out.
+struct GradEpi : NoSlabs {
+  static constexpr int kSlab = 4096;
+  static constexpr int WARPS = 8, SLABS = 2 * kSlab;
   struct Args {
+    CUtensorMap dz;
     const int32_t* labels;
     const float *lse, *g;
-    uint16_t* dz;
-    int64_t ld;
     int V, v0;  // vocabulary, the piece's first column
     float scale, smooth, zc;
   };
@@ -213,7 +211,7 @@ struct GradEpi {
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     const int y = at.row < s.M ? a.labels[at.row] : -1;
     r.scored = y >= 0 && y < a.V;
-    r.label = y - a.v0;
+    r.label = r.scored ? y - a.v0 : -1;
     const float g = r.scored ? a.g[at.row] : 0.f, lse = r.scored ? a.lse[at.row] : 0.f;
     r.lse2 = lse * kLog2e;
     r.cp = g * (1.f + 2.f * a.zc * lse);
@@ -222,37 +220,53 @@ struct GradEpi {
   }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              uint32_t tb) {
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
     const float k = a.scale * kLog2e;
     const int here = r.label - at.n0;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
-      const int col = at.n0 + c * 32;
-      if (col >= a.ld) break;
-      float v[32];
-      tile_chunk(tb, c, v);
-      if (at.row >= s.M) continue;
+    for (int j = w.part * (BN / 128); j < (w.part + 1) * (BN / 128); ++j) {
+      const int col = at.n0 + j * 64;
+      if (col >= s.N) break;
+      uint8_t* slab = w.smem + (w.begun++ & 1) * kSlab;
+      if (w.lane == 0) bulk_store_wait<1, true>();
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = r.scored ? fmaf(r.cp, ex2(fmaf(v[i], k, -r.lse2)), -r.c0) : 0.f;
-      if (here >= c * 32 && here < c * 32 + 32 && r.scored) {
+      for (int half = 0; half < 2; ++half) {
+        const int c0 = j * 64 + half * 32;
+        float v[32];
+        tile_chunk(tb, 2 * j + half, v);
+        // the rows that X has been cleared in have z = 0, lse = 0 and all factors 0
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] -= here == c * 32 + i ? r.cl : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(r.cp, ex2(fmaf(v[i], k, -r.lse2)), -r.c0);
+        if (here >= c0 && here < c0 + 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] -= here == c0 + i ? r.cl : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *slab_piece(slab, w.lane, half * 4 + i) =
+              make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                         pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
       }
-      if (col + 32 > s.N) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col + i >= s.N) v[i] = 0.f;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) {
+        tma_store_3d(&a.dz, slab, col, at.row0, 0);
+        bulk_store_commit();
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + 8 * i < a.ld) store8(a.dz, (size_t)at.row * a.ld + col + 8 * i, true, v + 8 * i);
     }
   }
 };
 
-// out = scale * accumulator (+ what is there, or an fp32 sum), N a multiple of 8.
-struct SumEpi {
+// out = scale * accumulator, N a multiple of 8: bf16 or fp32 by slabs, or
+// added to what is there or to an fp32 sum (the addend is asked for ahead of
+// the accumulator, a chunk of 32 columns at a time).
+struct SumEpi : NoSlabs {
+  static constexpr int kSlab = 4096;
+  static constexpr int WARPS = 4, SLABS = 2 * kSlab;
   struct Args {
+    CUtensorMap map;  // of out
     void* out;
     const void* add;  // same row stride; null: nothing
     int64_t ld;
@@ -263,7 +277,46 @@ struct SumEpi {
   static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
-                                              uint32_t tb) {
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
+    if (a.add) {
+      added<BN>(a, s, at, tb);
+      return;
+    }
+    const int wide = a.out_bf16 ? 64 : 32;  // columns of a slab
+#pragma unroll 1
+    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += wide) {
+      uint8_t* slab = w.smem + (w.begun++ & 1) * kSlab;
+      if (w.lane == 0) bulk_store_wait<1, true>();
+      __syncwarp();
+#pragma unroll 1
+      for (int half = 0; half < wide / 32; ++half) {
+        float v[32];
+        tile_chunk(tb, (col - at.n0) / 32 + half, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= a.scale;
+        if (a.out_bf16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *slab_piece(slab, w.lane, half * 4 + i) =
+                make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *(float4*)slab_piece(slab, w.lane, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) {
+        tma_store_3d(&a.map, slab, col, at.row0, at.b);
+        bulk_store_commit();
+      }
+    }
+  }
+  template <int BN>
+  static __device__ __forceinline__ void added(const Args& a, const ProductShape& s, const TileAt& at, uint32_t tb) {
     const bool ok = at.row < s.M;
     const size_t row = (size_t)at.row * a.ld;
 #pragma unroll 1
@@ -271,11 +324,9 @@ struct SumEpi {
       const int col = at.n0 + c * 32;
       if (col >= s.N) break;
       float add[4][8];
-      if (a.add && ok) {  // asked for before the accumulator, which the stores below would hold up
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (ok && col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
       float v[32];
       tile_chunk(tb, c, v);
       if (!ok) continue;
@@ -283,16 +334,41 @@ struct SumEpi {
       for (int i = 0; i < 4; ++i) {
         if (col + 8 * i >= s.N) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] = a.add ? fmaf(v[8 * i + j], a.scale, add[i][j]) : v[8 * i + j] * a.scale;
+        for (int j = 0; j < 8; ++j) v[8 * i + j] = fmaf(v[8 * i + j], a.scale, add[i][j]);
         store8(a.out, row + col + 8 * i, a.out_bf16, v + 8 * i);
       }
     }
   }
 };
 
+// A gradient from the partial sums of the ranges that its K was cut into, in
+// their order, and what it is added to.
+__global__ void __launch_bounds__(256)
+    join_ranges_kernel(const float* part, int ranges, int64_t n, void* out, int bf16, int add) {
+  grid_wait();
+  grid_release();
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (add && bf16) {
+      const uint2 o = *(const uint2*)((const uint16_t*)out + i);
+      s = make_float4(bf2f(o.x & 0xffff), bf2f(o.x >> 16), bf2f(o.y & 0xffff), bf2f(o.y >> 16));
+    } else if (add) {
+      s = *(const float4*)((const float*)out + i);
+    }
+#pragma unroll 8
+    for (int r = 0; r < ranges; ++r) {
+      const float4 p = *(const float4*)(part + r * n + i);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    if (bf16) *(uint2*)((uint16_t*)out + i) = make_uint2(pack_bf2(s.x, s.y), pack_bf2(s.z, s.w));
+    else *(float4*)((float*)out + i) = s;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+constexpr int kSms = 152;  // sizes the workspace, whatever machine asks
 inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -310,9 +386,28 @@ int piece_cols(int T, int V) {
   return (int)std::min<int64_t>(up((size_t)((V + pieces - 1) / pieces), 256), up(V, 64));
 }
 
+// Ranges that the K of a gradient's product [M, N] is cut into: few tiles
+// (few tokens, or a small vocabulary) leave most of the GPU idle otherwise.
+// The number that takes the least time by a count of SM pairs' steps (512
+// cycles for a 256 x 256 tile 64 deep), with what the partial sums cost to
+// write and to read at 3500 bytes a cycle.
+int ranges_of(int64_t M, int64_t N, int K) {
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), steps = (K + 63) / 64, pairs = kSms / 2;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int64_t r = 1; r <= pairs && (r == 1 || (tiles < 4 * pairs && steps / r >= 4)); ++r) {
+    const int64_t cycles = (tiles * r + pairs - 1) / pairs * ((steps + r - 1) / r) * 512 + (r > 1 ? 4000 + r * M * N * 8 / 3500 : 0);
+    if (cycles < least) {
+      least = cycles;
+      best = (int)r;
+    }
+  }
+  return best;
+}
+
 struct BwdWs {
   size_t x, dz, acc, total;
-  int cols;
+  int cols, dx_ranges, dw_ranges;
 };
 BwdWs bwd_ws(int T, int V, int h) {
   BwdWs o;
@@ -320,13 +415,19 @@ BwdWs bwd_ws(int T, int V, int h) {
   o.x = 0;
   o.dz = up((size_t)T * h * 2, 256);
   o.acc = o.dz + up((size_t)T * o.cols * 2, 256);
-  o.total = o.acc + (o.cols < V ? up((size_t)T * h * 4, 256) : 0);
+  const bool pieces = o.cols < V;
+  o.dx_ranges = pieces ? 1 : ranges_of(T, h, V);
+  o.dw_ranges = pieces ? 1 : ranges_of(V, h, T);
+  // dX's sum over the pieces, or partial sums of either
+  const size_t dx = pieces || o.dx_ranges > 1 ? (size_t)o.dx_ranges * T * h * 4 : 0;
+  const size_t dw = o.dw_ranges > 1 ? (size_t)o.dw_ranges * V * h * 4 : 0;
+  o.total = o.acc + up(std::max(dx, dw), 256);
   return o;
 }
 
 template <bool A_MN, bool B_MN, class E>
 cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int M, int N, int K,
-                    const typename E::Args& args, cudaStream_t st) {
+                    const typename E::Args& args, cudaStream_t st, int ranges = 1) {
   auto go = [&](auto cfg) {
     using C = decltype(cfg);
     CUtensorMap ta, tb;
@@ -334,10 +435,43 @@ cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int 
     if (!product_map(&ta, A, ar, ac, lda, lda, 1, a_box<C>(), false) ||
         !product_map(&tb, B, br, bc, ldb, ldb, 1, b_box<C>(), false))
       return cudaErrorUnknown;
-    return launch_product<C, E>(ta, tb, product_shape<C>(M, N, K, 1), args, st);
+    ProductShape s = product_shape<C>(M, N, K, 1);
+    if (ranges > 1) {
+      const int steps = (K + C::BK - 1) / C::BK;
+      s.split_kb = (steps + ranges - 1) / ranges;
+      s.batch = (steps + s.split_kb - 1) / s.split_kb;
+    }
+    return launch_product<C, E>(ta, tb, s, args, st);
   };
-  if (wide(M, N)) return go(ProductCfg<256, true, A_MN, B_MN>());
+  if (ranges > 1 || wide(M, N)) return go(ProductCfg<256, true, A_MN, B_MN>());
   return go(ProductCfg<128, false, A_MN, B_MN>());
+}
+
+// out [M, N] = scale * (product over K) + add, dense, in `ranges` of K by way
+// of partial sums (add is then out itself or nothing).
+template <bool A_MN, bool B_MN>
+cudaError_t gradient(const void* A, int64_t lda, const void* B, int64_t ldb, int M, int N, int K, int ranges,
+                     float* part, void* out, bool bf16, const void* add, bool add_bf16, float scale, cudaStream_t st) {
+  const int steps = (K + 63) / 64, each = (steps + ranges - 1) / ranges, used = (steps + each - 1) / each;
+  const int64_t all = (int64_t)M * N;
+  SumEpi::Args s{};
+  s.out = ranges > 1 ? (void*)part : out;
+  s.add = ranges > 1 ? nullptr : add;
+  s.ld = N;
+  s.scale = scale;
+  s.out_bf16 = ranges == 1 && bf16;
+  s.add_bf16 = add_bf16;
+  const int64_t apart = used > 1 ? all : N;
+  if (!(s.out_bf16 ? product_map(&s.map, s.out, M, N, N, apart, used, 32, false)
+                   : product_map_f32(&s.map, s.out, M, N, N, apart, used)))
+    return cudaErrorUnknown;
+  cudaError_t e = product<A_MN, B_MN, SumEpi>(A, lda, B, ldb, M, N, K, s, st, ranges);
+  if (ranges > 1 && e == cudaSuccess) {
+    e = mt_host::launch_early(join_ranges_kernel, (int)std::min<int64_t>((all + 1023) / 1024, kSms * 8), 256, 0, st, 1,
+                              (const float*)part, used, all, out, (int)bf16, (int)(add != nullptr));
+    count_launches(1);
+  }
+  return e;
 }
 
 }  // namespace
@@ -349,14 +483,14 @@ bool linear_ce_dims(int T, int V, int h) {
 }
 
 size_t linear_ce_fwd_workspace(int T, int V) {
-  const size_t n = (size_t)T * ((V + 127) / 128);
+  const size_t n = (size_t)T * (2 * ((V + 127) / 128));
   return up(n * 8, 256) + up(n * 4, 256) + up((size_t)T * 4, 256);
 }
 size_t linear_ce_bwd_workspace(int T, int V, int h) { return bwd_ws(T, V, h).total; }
 
 int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, float scale, float smooth, float zc,
                   float* loss, float* lse, void* work, int T, int V, int h, int ldx, int ldw, cudaStream_t st) {
-  const size_t n = (size_t)T * ((V + 127) / 128);
+  const size_t n = (size_t)T * (2 * ((V + 127) / 128));
   StatsEpi::Args a;
   a.labels = labels;
   a.part = (float2*)work;
@@ -365,9 +499,9 @@ int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   a.scale = scale;
   cudaError_t e = product<false, false, StatsEpi>(X, ldx, W, ldw, T, V, h, a, st);
   if (e != cudaSuccess) return kLaunchFailed;
-  const int num_n = wide(T, V) ? (V + 255) / 256 : (V + 127) / 128;
+  const int parts = 2 * (wide(T, V) ? (V + 255) / 256 : (V + 127) / 128);
   e = mt_host::launch_early(join_rows_kernel, (T + 7) / 8, 256, 0, st, 1, (const float2*)a.part, (const float*)a.sums,
-                            (const float*)a.zlab, labels, T, V, num_n, scale, smooth, zc, loss, lse);
+                            (const float*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
   count_launches(1);
   return e == cudaSuccess ? 0 : kLaunchFailed;
 }
@@ -378,7 +512,8 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   const BwdWs o = bwd_ws(T, V, h);
   uint16_t* xs = (uint16_t*)((uint8_t*)work + o.x);
   uint16_t* dz = (uint16_t*)((uint8_t*)work + o.dz);
-  float* acc = dx_bf16 ? (float*)((uint8_t*)work + o.acc) : (float*)dX;
+  float* part = (float*)((uint8_t*)work + o.acc);
+  float* acc = dx_bf16 ? part : (float*)dX;
   const int64_t units = ((int64_t)T * (h / 8) + 255) / 256;
   cudaError_t e = mt_host::launch_early(scored_rows_kernel, (int)std::min<int64_t>(units, 152 * 16), 256, 0, st, 1, X,
                                         (int64_t)ldx, labels, V, xs, T, h);
@@ -387,17 +522,26 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
     const int n = std::min(o.cols, V - v0);
     const int64_t ld = (int64_t)up(n, 64);
     const uint16_t* Wp = W + (int64_t)v0 * ldw;
-    GradEpi::Args a{labels, lse, g, dz, ld, V, v0, scale, smooth, zc};
+    GradEpi::Args a{};
+    if (!product_map(&a.dz, dz, T, n, ld, ld, 1, 32, false)) return kLaunchFailed;
+    a.labels = labels;
+    a.lse = lse;
+    a.g = g;
+    a.V = V;
+    a.v0 = v0;
+    a.scale = scale;
+    a.smooth = smooth;
+    a.zc = zc;
     e = product<false, false, GradEpi>(xs, h, Wp, ldw, T, n, h, a, st);
     if (e == cudaSuccess && dX) {
       const bool last = v0 + n == V;
-      SumEpi::Args s{last ? dX : acc, v0 ? acc : nullptr, h, scale, last && dx_bf16, 0};
-      e = product<false, true, SumEpi>(dz, ld, Wp, ldw, T, h, n, s, st);
+      e = gradient<false, true>(dz, ld, Wp, ldw, T, h, n, o.dx_ranges, part, last ? dX : acc, last && dx_bf16,
+                                v0 ? acc : nullptr, false, scale, st);
     }
     if (e == cudaSuccess && dW) {
       void* out = dw_bf16 ? (void*)((uint16_t*)dW + (int64_t)v0 * h) : (void*)((float*)dW + (int64_t)v0 * h);
-      SumEpi::Args s{out, accumulate ? out : nullptr, h, scale, dw_bf16, dw_bf16};
-      e = product<true, true, SumEpi>(dz, ld, xs, h, n, h, T, s, st);
+      e = gradient<true, true>(dz, ld, xs, h, n, h, T, o.dw_ranges, part, out, dw_bf16, accumulate ? out : nullptr,
+                               dw_bf16, scale, st);
     }
   }
   return e == cudaSuccess ? 0 : kLaunchFailed;

@@ -69,22 +69,6 @@ __device__ __forceinline__ void load8h(const uint16_t* p, float* v) {
 __device__ __forceinline__ void store8h(uint16_t* p, const float* v) {
   *(uint4*)p = make_uint4(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]), pack_h2(v[4], v[5]), pack_h2(v[6], v[7]));
 }
-// The columns [col, col + n) of a row of a square matrix, n <= 32, and those
-// entries of the columns they mirror. Rows are padded to whole 64 columns, so
-// groups of eight that begin inside the matrix can be written whole.
-__device__ __forceinline__ void store_square(uint16_t* mat, int64_t ld, int row, int col, int N, bool mirror,
-                                             const float (&v)[32]) {
-  uint16_t* p = mat + (size_t)row * ld + col;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col + 8 * i < N) store8h(p + 8 * i, v + 8 * i);
-  if (mirror) {  // a column of the mirror image: neighbouring lanes, neighbouring addresses
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < N) mat[(size_t)(col + i) * ld + row] = f2h(v[i]);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Momentum and the norm of the update
 // ---------------------------------------------------------------------------
@@ -201,55 +185,102 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues
+// Epilogues. Each works on slabs of 32 rows by 64 columns that come and go by
+// TMA (tile_product.cuh): a warp has two pairs of 4 KB, one in work and one on
+// its way. The square matrices' slabs leave twice, as they are and transposed.
 // ---------------------------------------------------------------------------
+constexpr int kSlab = 4096;
+
+// The next slab's place: free once what left from there before has been read.
+__device__ __forceinline__ uint8_t* next_slab(EpiWarp& w) {
+  uint8_t* p = w.smem + (w.begun++ & 1) * 2 * kSlab;
+  if (w.lane == 0) bulk_store_wait<1, true>();
+  __syncwarp();
+  return p;
+}
+// 32 columns (half 0 or 1 of a slab's) of this lane's row of a square matrix
+// into the slab, and into its transposed image behind it: there a column of
+// the slab is a row of 64 bytes, this lane's value at 2 * lane.
+__device__ __forceinline__ void put_square(uint8_t* slab, int lane, int half, bool mirror, const float (&v)[32]) {
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = pack_h2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *slab_piece(slab, lane, half * 4 + i) = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+  if (mirror) {
+    uint16_t* t = (uint16_t*)(slab + kSlab) + half * 1024 + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      t[64 * i] = (uint16_t)p[i];
+      t[64 * i + 32] = (uint16_t)(p[i] >> 16);
+    }
+  }
+}
+__device__ __forceinline__ void send_square(const CUtensorMap* m, const CUtensorMap* mt, uint8_t* slab, int lane, int col,
+                                            const TileAt& at) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(m, slab, col, at.row0, at.b);
+    if (at.mirror) tma_store_3d(mt, slab + kSlab, at.row0, col, at.b);
+    bulk_store_commit();
+  }
+}
+
 // A = X X^T: the rest of A to fp16, its diagonal to fp32.
-struct GramEpi {
+struct GramEpi : NoSlabs {
+  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
   struct Args {
-    uint16_t* O;
+    CUtensorMap O, OT;  // A's rest in slabs, and in transposed ones
     float* d;
-    int64_t ld, dpad;  // row stride; diagonal entries of a matrix
+    int64_t dpad;  // diagonal entries of a matrix
   };
   struct Row {};
   static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
+  // 32 columns from col of this lane's row, the diagonal taken out
+  static __device__ __forceinline__ void values(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                                float (&v)[32]) {
+    const int here = at.row - col;
+    if (here >= 0 && here < 32) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        d = i == here ? v[i] : d;
+        v[i] = i == here ? 0.f : v[i];
+      }
+      if (at.row < s.M) a.d[at.b * a.dpad + at.row] = d * (kXDown * kXDown);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= kAUp * kXDown * kXDown;
+  }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
-                                              uint32_t tb) {
-    uint16_t* mat = a.O + (size_t)at.b * s.M * a.ld;
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
-      const int col = at.n0 + c * 32;
-      if (col >= s.N) break;
-      float v[32];
-      tile_chunk(tb, c, v);
-      if (at.row >= s.M) continue;
-      const int here = at.row - col;  // the diagonal's place among the 32
-      if (here >= 0 && here < 32) {
-        float d = 0.f;
+    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
+      uint8_t* slab = next_slab(w);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (i == here) {
-            d = v[i];
-            v[i] = 0.f;
-          }
-        }
-        a.d[at.b * a.dpad + at.row] = d * (kXDown * kXDown);
+      for (int half = 0; half < 2; ++half) {
+        float v[32];
+        tile_chunk(tb, (col - at.n0) / 32 + half, v);
+        values(a, s, at, col + 32 * half, v);
+        put_square(slab, w.lane, half, at.mirror, v);
       }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= kAUp * kXDown * kXDown;
-      store_square(mat, a.ld, at.row, col, s.N, at.mirror, v);
+      send_square(&a.O, &a.OT, slab, w.lane, col, at);
     }
   }
 };
 
 // B = b A + c A^2 from O O^T, O and the diagonal.
 struct PolyEpi {
+  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
   struct Args {
-    const uint16_t* O;
+    CUtensorMap O, B, BT;
     const float* d;
-    uint16_t* B;
     float* db;
-    int64_t ld, dpad;
+    int64_t dpad;
     float b, c;
   };
   struct Row {
@@ -258,44 +289,60 @@ struct PolyEpi {
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     r.d = at.row < s.M ? a.d[at.b * a.dpad + at.row] : 0.f;
   }
+  static __device__ __forceinline__ void values(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                                int col, const float (&o)[32], const float* dj, float (&v)[32]) {
+    const int here = at.row - col;
+    if (here >= 0 && here < 32) {
+      float sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sq = i == here ? v[i] : sq;
+      if (at.row < s.M) a.db[at.b * a.dpad + at.row] = r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown));
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = fmaf(a.c, fmaf(r.d + dj[i], o[i], v[i] * kADown), a.b * o[i]);
+      v[i] = i == here ? 0.f : v[i];
+    }
+  }
+  static __device__ __forceinline__ void request(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                                 EpiWarp& w) {
+    if (w.lane == 0 && at.row0 < s.M) {
+      uint64_t* bar = &w.bars[w.begun & 1];
+      mbar_arrive_expect_tx(bar, kSlab);
+      tma_load_3d(w.smem + (w.begun & 1) * 2 * kSlab, &a.O, bar, col, at.row0, at.b);
+    }
+  }
+  static __device__ __forceinline__ void prefetch(const Args& a, const ProductShape& s, const TileAt& at, EpiWarp& w) {
+    if (w.lane == 0) bulk_store_wait<0, true>();
+    request(a, s, at, at.n0, w);
+  }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              uint32_t tb) {
-    const size_t mat = (size_t)at.b * s.M * a.ld;
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
     const float* dcol = a.d + at.b * a.dpad;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
-      const int col = at.n0 + c * 32;
-      if (col >= s.N) break;
-      float o[32], dj[32];
+    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
+      uint8_t* slab = w.smem + (w.begun & 1) * 2 * kSlab;
+      mbar_wait(&w.bars[w.begun & 1], (w.begun >> 1) & 1, w.abort, kErrTimeoutEpi);
+      ++w.begun;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = dj[i] = 0.f;
-      if (at.row < s.M) {
+      for (int half = 0; half < 2; ++half) {
+        float v[32], o[32], dj[32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (col + 8 * i >= s.N) break;  // the padding behind it holds finite values or is not used
-          load8h(a.O + mat + (size_t)at.row * a.ld + col + 8 * i, o + 8 * i);
-          load4(dcol, col + 8 * i, false, *(float(*)[4])(dj + 8 * i));
-          load4(dcol, col + 8 * i + 4, false, *(float(*)[4])(dj + 8 * i + 4));
+        for (int i = 0; i < 8; ++i) *(float4*)(dj + 4 * i) = ((const float4*)(dcol + col + 32 * half))[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load8h((const uint16_t*)slab_piece(slab, w.lane, half * 4 + i), o + 8 * i);
+        tile_chunk(tb, (col - at.n0) / 32 + half, v);
+        values(a, s, at, r, col + 32 * half, o, dj, v);
+        put_square(slab, w.lane, half, at.mirror, v);
+        if (half == 0 && col + 64 < at.n0 + BN && col + 64 < s.N) {
+          // the other place: what left from it has been read meanwhile
+          if (w.lane == 0) bulk_store_wait<0, true>();
+          request(a, s, at, col + 64, w);
         }
       }
-      float v[32];
-      tile_chunk(tb, c, v);
-      if (at.row >= s.M) continue;
-      const int here = at.row - col;
-      if (here >= 0 && here < 32) {
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i == here) sq = v[i];
-        a.db[at.b * a.dpad + at.row] = r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown));
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[i] = fmaf(a.c, fmaf(r.d + dj[i], o[i], v[i] * kADown), a.b * o[i]);
-        if (i == here) v[i] = 0.f;
-      }
-      store_square(a.B + mat, a.ld, at.row, col, s.N, at.mirror, v);
+      send_square(&a.B, &a.BT, slab, w.lane, col, at);
     }
   }
 };
@@ -303,18 +350,17 @@ struct PolyEpi {
 // X <- a X + B X; the last step leaves the result or takes the weights' step.
 template <bool LAST>
 struct ApplyEpi {
+  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
   struct Args {
-    const uint16_t* hi;
-    uint16_t* lo;       // in place
-    uint16_t* hi_out;   // not LAST
+    CUtensorMap hi, lo, hi_out;  // lo in place; hi_out: not LAST
     const float* db;
-    int64_t ld, dpad;
+    int64_t dpad;
     float a;
-    int by_col;         // the diagonal runs along the columns (X B) or the rows (B X)
+    int by_col;  // the diagonal runs along the columns (X B) or the rows (B X)
     // LAST: out [M, N] dense per matrix, out <- keep * out - step * X with
     // update, else X
     void* out;
-    int out_bf16, update, vec;
+    int out_bf16, update;
     float keep, step;
   };
   struct Row {
@@ -323,83 +369,159 @@ struct ApplyEpi {
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     r.d = !a.by_col && at.row < s.M ? a.db[at.b * a.dpad + at.row] : 0.f;
   }
-  template <int BN>
-  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              uint32_t tb) {
-    const size_t x0 = ((size_t)at.b * s.M + at.row) * a.ld;
-    const float* dcol = a.db + at.b * a.dpad;
+  // four neighbouring values of the new X (times kXUp)
+  static __device__ __forceinline__ void step4(float a, const float* d, const float* h, const float* l, float* v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = fmaf(a + d[e], h[e], fmaf(fmaf(0.5f, d[e], a), l[e], v[e] * kADown));
+  }
+  static __device__ __forceinline__ void request(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                                 EpiWarp& w) {
+    if (w.lane == 0 && at.row0 < s.M) {
+      uint64_t* bar = &w.bars[w.begun & 1];
+      uint8_t* p = w.smem + (w.begun & 1) * 2 * kSlab;
+      mbar_arrive_expect_tx(bar, 2 * kSlab);
+      tma_load_3d(p, &a.hi, bar, col, at.row0, at.b);
+      tma_load_3d(p + kSlab, &a.lo, bar, col, at.row0, at.b);
+    }
+  }
+  static __device__ __forceinline__ void prefetch(const Args& a, const ProductShape& s, const TileAt& at, EpiWarp& w) {
+    if (LAST) fence_proxy_async_smem();
+    __syncwarp();
+    if (!LAST && w.lane == 0) bulk_store_wait<0, true>();
+    request(a, s, at, at.n0, w);
+  }
+  // LAST: 64 columns of 32 rows of results in the slab pair (fp32; of eight
+  // columns the first four where their hi were, the others where their lo
+  // were) to out, whole rows at a time: neighbouring lanes, neighbouring columns.
+  static __device__ __forceinline__ void write_rows(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                                    uint8_t* slab, int lane) {
+    const int rows = min(32, s.M - at.row0);
+    const int c = col + 2 * lane;
+    uint8_t* half = slab + (lane & 2 ? kSlab : 0);
+    const size_t o0 = ((size_t)at.b * s.M + at.row0) * s.N + c;
+    // pairs at a time where every row's pairs lie on their boundary
+    const bool pairs = (s.N & 1) == 0 && ((uintptr_t)a.out & (a.out_bf16 ? 3 : 7)) == 0;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
-      const int col = at.n0 + c * 32;
-      if (col >= s.N) break;
-      uint4 h4[4], l4[4];
-      if (at.row < s.M) {
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float2 old[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (col + 8 * i >= s.N) break;
-          h4[i] = *(const uint4*)(a.hi + x0 + col + 8 * i);
-          l4[i] = *(const uint4*)(a.lo + x0 + col + 8 * i);
-        }
-      }
-      float v[32];
-      tile_chunk(tb, c, v);
-      if (at.row >= s.M) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i >= s.N) break;
-        const int cc = col + 8 * i;
-        float h[8], l[8], d[8];
-        const uint32_t hw[4] = {h4[i].x, h4[i].y, h4[i].z, h4[i].w}, lw[4] = {l4[i].x, l4[i].y, l4[i].z, l4[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 p = unpack_h2(hw[e]), q = unpack_h2(lw[e]);
-          h[2 * e] = p.x, h[2 * e + 1] = p.y, l[2 * e] = q.x, l[2 * e + 1] = q.y;
-        }
-        if (a.by_col) {
-          load4(dcol, cc, false, *(float(*)[4])d);
-          load4(dcol, cc + 4, false, *(float(*)[4])(d + 4));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = r.d;
-        }
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = fmaf(a.a + d[e], h[e], fmaf(fmaf(0.5f, d[e], a.a), l[e], v[8 * i + e] * kADown));
-        if (!LAST) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) l[e] = x[e] - h2f(f2h(x[e]));
-          store8h(a.hi_out + x0 + cc, x);
-          store8h(a.lo + x0 + cc, l);
-        } else {
-          const size_t o = ((size_t)at.b * s.M + at.row) * s.N + cc;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= kXDown;
-          if (a.vec) {
-            if (a.update) {
-              float w[8];
-              load4(a.out, o, a.out_bf16, *(float(*)[4])w);
-              load4(a.out, o + 4, a.out_bf16, *(float(*)[4])(w + 4));
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = fmaf(a.keep, w[e], -a.step * x[e]);
-            }
+      for (int i = 0; i < 8; ++i) {
+        old[i] = make_float2(0.f, 0.f);
+        const size_t o = o0 + (size_t)(r0 + i) * s.N;
+        if (a.update && r0 + i < rows && c < s.N) {
+          if (pairs) {
             if (a.out_bf16) {
-              *(uint4*)((uint16_t*)a.out + o) =
-                  make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+              const uint32_t u = *(const uint32_t*)((const uint16_t*)a.out + o);
+              old[i] = make_float2(bf2f(u & 0xffff), bf2f(u >> 16));
             } else {
-              *(float4*)((float*)a.out + o) = make_float4(x[0], x[1], x[2], x[3]);
-              *(float4*)((float*)a.out + o + 4) = make_float4(x[4], x[5], x[6], x[7]);
+              old[i] = *(const float2*)((const float*)a.out + o);
             }
           } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (cc + e >= s.N) break;
-              const float r1 = a.update ? fmaf(a.keep, load1(a.out, o + e, a.out_bf16), -a.step * x[e]) : x[e];
-              if (a.out_bf16) ((uint16_t*)a.out)[o + e] = f2bf(r1);
-              else ((float*)a.out)[o + e] = r1;
-            }
+            old[i].x = load1(a.out, o, a.out_bf16);
+            if (c + 1 < s.N) old[i].y = load1(a.out, o + 1, a.out_bf16);
           }
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i >= rows || c >= s.N) break;
+        const size_t o = o0 + (size_t)(r0 + i) * s.N;
+        float2 x = ((const float2*)slab_piece(half, r0 + i, lane >> 2))[lane & 1];
+        if (a.update) {
+          x.x = fmaf(a.keep, old[i].x, -a.step * x.x);
+          x.y = fmaf(a.keep, old[i].y, -a.step * x.y);
+        }
+        if (pairs) {
+          if (a.out_bf16) *(uint32_t*)((uint16_t*)a.out + o) = pack_bf2(x.x, x.y);
+          else *(float2*)((float*)a.out + o) = x;
+        } else if (a.out_bf16) {
+          ((uint16_t*)a.out)[o] = f2bf(x.x);
+          if (c + 1 < s.N) ((uint16_t*)a.out)[o + 1] = f2bf(x.y);
+        } else {
+          ((float*)a.out)[o] = x.x;
+          if (c + 1 < s.N) ((float*)a.out)[o + 1] = x.y;
+        }
+      }
+    }
+  }
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
+    const float* dcol = a.db + at.b * a.dpad;
+#pragma unroll 1
+    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
+      uint8_t* slab = w.smem + (w.begun & 1) * 2 * kSlab;
+      mbar_wait(&w.bars[w.begun & 1], (w.begun >> 1) & 1, w.abort, kErrTimeoutEpi);
+      ++w.begun;
+      const bool more = col + 64 < at.n0 + BN && col + 64 < s.N;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float v[32];
+        tile_chunk(tb, (col - at.n0) / 32 + half, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4* hp = slab_piece(slab, w.lane, half * 4 + i);
+          uint4* lp = slab_piece(slab + kSlab, w.lane, half * 4 + i);
+          float h[8], l[8], d[8];
+          load8h((const uint16_t*)hp, h);
+          load8h((const uint16_t*)lp, l);
+          if (a.by_col) {
+            *(float4*)d = ((const float4*)(dcol + col + 32 * half))[2 * i];
+            *(float4*)(d + 4) = ((const float4*)(dcol + col + 32 * half))[2 * i + 1];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = r.d;
+          }
+          step4(a.a, d, h, l, v + 8 * i);
+          step4(a.a, d + 4, h + 4, l + 4, v + 8 * i + 4);
+          if (!LAST) {
+            uint32_t p[4], q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] = pack_h2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+              const float2 f = unpack_h2(p[e]);
+              q[e] = pack_h2(v[8 * i + 2 * e] - f.x, v[8 * i + 2 * e + 1] - f.y);
+            }
+            *hp = make_uint4(p[0], p[1], p[2], p[3]);
+            *lp = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+        if (LAST) {
+          // the half's own 32 columns: their hi and lo have been read, and the
+          // other half's lie in the other half of the pieces
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *slab_piece(slab, w.lane, half * 4 + i) =
+                make_uint4(__float_as_uint(v[8 * i] * kXDown), __float_as_uint(v[8 * i + 1] * kXDown),
+                           __float_as_uint(v[8 * i + 2] * kXDown), __float_as_uint(v[8 * i + 3] * kXDown));
+            *slab_piece(slab + kSlab, w.lane, half * 4 + i) =
+                make_uint4(__float_as_uint(v[8 * i + 4] * kXDown), __float_as_uint(v[8 * i + 5] * kXDown),
+                           __float_as_uint(v[8 * i + 6] * kXDown), __float_as_uint(v[8 * i + 7] * kXDown));
+          }
+        }
+        if (half == 0 && more) {
+          if (!LAST && w.lane == 0) bulk_store_wait<0, true>();
+          if (LAST) {  // the other place has been read by this warp's own loads
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          request(a, s, at, col + 64, w);
+        }
+      }
+      if (!LAST) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (w.lane == 0) {
+          tma_store_3d(&a.hi_out, slab, col, at.row0, at.b);
+          tma_store_3d(&a.lo, slab + kSlab, col, at.row0, at.b);
+          bulk_store_commit();
+        }
+      } else {
+        __syncwarp();
+        write_rows(a, s, at, col, slab, w.lane);
+        __syncwarp();
       }
     }
   }
@@ -502,31 +624,39 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
   const bool tall = rows > cols;
   const int m = w.m;
   const Operand o{O, m, m, w.lda}, p{B, m, m, w.lda};
+  // slabs of X and of the square matrices, these also as 64 rows of 32 columns
+  CUtensorMap mX[2], mLo, mO, mOT, mB, mBT;
+  const int64_t xa = w.ldx * rows, aa = w.lda * m;
+  if (!product_map(&mX[0], hi[0], rows, cols, w.ldx, xa, batch, 32, true) ||
+      !product_map(&mX[1], hi[1], rows, cols, w.ldx, xa, batch, 32, true) ||
+      !product_map(&mLo, lo, rows, cols, w.ldx, xa, batch, 32, true) ||
+      !product_map(&mO, O, m, m, w.lda, aa, batch, 32, true) ||
+      !product_map(&mOT, O, m, m, w.lda, aa, batch, 64, true, 32) ||
+      !product_map(&mB, B, m, m, w.lda, aa, batch, 32, true) ||
+      !product_map(&mBT, B, m, m, w.lda, aa, batch, 64, true, 32))
+    return kLaunchFailed;
   for (int i = 0; i < steps && e == cudaSuccess; ++i) {
     const float *c = coef + 3 * i;
     const Operand x{hi[i & 1], rows, cols, w.ldx};
-    const GramEpi::Args ga{O, d, w.lda, w.dpad};
+    const GramEpi::Args ga{mO, mOT, d, w.dpad};
     e = tall ? product<true, true, true, GramEpi>(x, x, m, m, rows, batch, ga, st)
              : product<false, false, true, GramEpi>(x, x, m, m, cols, batch, ga, st);
     if (e != cudaSuccess) break;
-    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{O, d, B, db, w.lda, w.dpad, c[1], c[2]},
-                                             st);
+    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mB, mBT, d, db, w.dpad, c[1], c[2]}, st);
     if (e != cudaSuccess) break;
     auto apply = [&](auto epi) {
       using E = decltype(epi);
       typename E::Args a{};
-      a.hi = hi[i & 1];
-      a.lo = lo;
-      a.hi_out = hi[(i + 1) & 1];
+      a.hi = mX[i & 1];
+      a.lo = mLo;
+      a.hi_out = mX[(i + 1) & 1];
       a.db = db;
-      a.ld = w.ldx;
       a.dpad = w.dpad;
       a.a = c[0];
       a.by_col = tall;
       a.out = out;
       a.out_bf16 = out_bf16;
       a.update = update;
-      a.vec = cols % 8 == 0 && al(out, 16);
       a.keep = keep;
       a.step = step;
       return tall ? product<false, false, false, E>(x, p, rows, cols, m, batch, a, st)

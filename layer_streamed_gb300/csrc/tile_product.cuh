@@ -6,14 +6,24 @@
 //
 // A tile is TM x BN outputs: 256 x 256 by a pair of SMs (tcgen05.mma
 // cta_group::2; each CTA holds 128 rows of A and 128 of B, 32 KB a 64-deep
-// step, six steps in flight) where there are enough of them for the GPU, else
-// 128 x 128 by one SM. Warp 0 fills the ring by TMA, one thread of warp 1
-// issues the MMAs, warps 2 to 5 drain the two accumulators, so one tile's
-// epilogue overlaps the next one's products. CTAs are persistent and take
-// tiles in a fixed order; each output is one fixed sum, whatever the grid.
+// step, five or six steps in flight) where there are enough of them for the
+// GPU, else 128 x 128 by one SM. Warp 0 fills the ring by TMA, one thread of
+// warp 1 issues the MMAs, the E::WARPS warps behind them drain the two
+// accumulators, so one tile's epilogue overlaps the next one's products. CTAs
+// are persistent and take tiles in a fixed order; each output is one fixed
+// sum, whatever the grid.
+//
+// An epilogue that has a tile's worth of other operands to read or results to
+// write moves them in slabs of 32 rows by 128 bytes, each warp its own, by
+// TMA through shared memory: while one is worked on, the next one is on its
+// way in and the last one on its way out. (Row by row from the lanes' own
+// loads and stores, one warp a scheduler had nothing else to do while it
+// waited: 24 us for a 256 x 256 tile that reads and writes four fp16 matrices,
+// against 6 us of MMAs at K = 1536.)
 //
 // Rows, columns and depth need not be multiples of anything: TMA fills zeros
-// outside a matrix, and the epilogues look at M and N.
+// outside a matrix and drops what is stored there, and the epilogues look at
+// M and N.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -28,6 +38,7 @@ struct ProductShape {
   int batch;     // matrices, one after another (the tensor maps' third axis)
   int num_m, num_n, tiles;  // of one matrix; set by product_shape
   int group_m;   // row blocks that share a sweep over the columns
+  int split_kb;  // not 0: one matrix, `batch` counts ranges of split_kb 64-deep steps of its K
 };
 
 // BN: tile columns; PAIR: two SMs a tile; A_MN / B_MN: the operand is stored
@@ -43,9 +54,15 @@ struct ProductCfg {
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B in one CTA
   static constexpr int A_BYTES = BM * BK * 2, B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 6;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 256 /*barriers*/;
   static constexpr int TMEM_COLS = 2 * BN;
+};
+// Ring depth and shared memory of a product with epilogue E, which gets
+// E::SLABS bytes of it a warp (each a multiple of 1024).
+template <class C, class E>
+struct ProductSmem {
+  static constexpr int SLABS = E::WARPS * E::SLABS;
+  static constexpr int STAGES = SLABS > 32 * 1024 ? 5 : 6;
+  static constexpr int TOTAL = STAGES * C::STAGE_BYTES + SLABS + 1024 /*align*/ + 512 /*barriers*/;
 };
 
 // What an epilogue knows of its tile: this lane's row of D, the warp's first
@@ -84,34 +101,102 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+template <class C>
+__host__ __device__ constexpr uint32_t product_idesc() {
+  return make_idesc(C::TM, C::BN, C::A_MN, C::B_MN) & (C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
+// One 64-deep step: four MMAs of depth 16.
+template <class C>
+__device__ __forceinline__ void product_mma(uint32_t d_tmem, uint32_t a_base, uint32_t b_base, uint32_t idesc,
+                                            bool first) {
+#pragma unroll
+  for (int kk = 0; kk < C::BK / 16; ++kk) {
+    const uint64_t ad = C::A_MN ? make_sdesc(a_base + kk * 2048, 8192, 1024) : make_sdesc(a_base + kk * 32, 16, 1024);
+    const uint64_t bd = C::B_MN ? make_sdesc(b_base + kk * 2048, 8192, 1024) : make_sdesc(b_base + kk * 32, 16, 1024);
+    if (C::PAIR) tc_mma2(d_tmem, ad, bd, idesc, !first || kk != 0);
+    else tc_mma(d_tmem, ad, bd, idesc, !first || kk != 0);
+  }
+}
+
+// Slabs: tiles of shared memory that TMA reads from or writes to.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"((uint64_t)map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until all but the last N groups of this thread's stores have been read out
+// of shared memory (READ) or are complete.
+template <int N, bool READ>
+__device__ __forceinline__ void bulk_store_wait() {
+  if (READ) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  else asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
+}
+// 16-byte piece k of this lane's row of a slab of 128-byte rows (128-byte swizzle).
+__device__ __forceinline__ uint4* slab_piece(uint8_t* slab, int row, int k) {
+  return (uint4*)(slab + row * 128 + ((k ^ (row & 7)) << 4));
+}
+
+// What an epilogue warp keeps from tile to tile: its slabs and their two
+// barriers, how many slabs it has begun, its share of the columns.
+struct EpiWarp {
+  uint8_t* smem;
+  uint64_t* bars;
+  volatile int* abort;
+  int lane, part;
+  uint32_t begun;
+};
+// For epilogues without slabs coming in.
+struct NoSlabs {
+  template <class A>
+  static __device__ __forceinline__ void prefetch(const A&, const ProductShape&, const TileAt&, EpiWarp&) {}
+};
+
+template <class C>
+__device__ __forceinline__ TileAt tile_at(const ProductShape& s, int tile, int rank, int q, int lane) {
+  int mb, nb;
+  TileAt at;
+  product_tile<C>(s, tile, mb, nb, at.b);
+  at.row0 = mb * C::TM + rank * C::BM + q * 32;
+  at.row = at.row0 + lane;
+  at.nb = nb;
+  at.n0 = nb * C::BN;
+  at.mirror = C::SYM && mb != nb;
+  return at;
+}
+
 template <class C, class E>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const ProductShape s, const typename E::Args args) {
+                   const __grid_constant__ ProductShape s, const __grid_constant__ typename E::Args args) {
   constexpr int BN = C::BN, BM = C::BM, BK = C::BK;
   constexpr bool PAIR = C::PAIR;
+  constexpr int STAGES = ProductSmem<C, E>::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
-  uint64_t* full = (uint64_t*)(smem + C::STAGES * C::STAGE_BYTES);  // PAIR: the even CTA's, for both halves
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
+  uint8_t* sB = smem + STAGES * C::A_BYTES;
+  uint8_t* slabs = smem + STAGES * C::STAGE_BYTES;
+  uint64_t* full = (uint64_t*)(slabs + ProductSmem<C, E>::SLABS);  // PAIR: the even CTA's, for both halves
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // PAIR: the even CTA's, both CTAs drained
-  uint32_t* tmem_slot = (uint32_t*)(tempty + 2);
+  uint64_t* slab_bars = tempty + 2;  // two a warp
+  uint32_t* tmem_slot = (uint32_t*)(slab_bars + 2 * E::WARPS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
 
   const uint32_t warp = warp_id(), lane = lane_id();
   const int rank = PAIR ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], PAIR ? 8 : 4);
+      mbar_init(&tempty[a], (PAIR ? 2 : 1) * E::WARPS);
     }
+    for (int i = 0; i < 2 * E::WARPS; ++i) mbar_init(&slab_bars[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -137,9 +222,12 @@ __global__ void __launch_bounds__(192, 1)
   grid_release();
 
   const int all = s.tiles * s.batch;
-  const int num_kb = (s.K + BK - 1) / BK;
   const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  const int all_kb = (s.K + BK - 1) / BK;
+  // K steps of a tile, and the first one
+  auto steps_of = [&](int b) { return s.split_kb ? min(s.split_kb, all_kb - b * s.split_kb) : all_kb; };
+  auto first_of = [&](int b) { return s.split_kb ? b * s.split_kb : 0; };
 
   if (warp == 0) {
     if (lane == 0) {  // TMA producer
@@ -150,12 +238,13 @@ __global__ void __launch_bounds__(192, 1)
         int mb, nb, b;
         product_tile<C>(s, tile, mb, nb, b);
         const int m0 = mb * C::TM + rank * BM, n0 = nb * BN + rank * C::B_ROWS;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        const int k0 = first_of(b), num_kb = steps_of(b), z = s.split_kb ? 0 : b;
+        for (int kb = k0; kb < k0 + num_kb; ++kb) {
           mbar_wait<PAIR>(&empty[stage], phase ^ 1, abort_flag, kErrTimeoutTma);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
-            if (PAIR) tma_load_3d_pair(dst, map, full0 + stage * 8, x, y, b);
-            else tma_load_3d(dst, map, &full[stage], x, y, b);
+            if (PAIR) tma_load_3d_pair(dst, map, full0 + stage * 8, x, y, z);
+            else tma_load_3d(dst, map, &full[stage], x, y, z);
           };
           uint8_t* a_dst = sA + stage * C::A_BYTES;
           uint8_t* b_dst = sB + stage * C::B_BYTES;
@@ -171,7 +260,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
             for (int j = 0; j < C::B_ROWS / 64; ++j) load(b_dst + j * 8192, &tmB, n0 + 64 * j, kb * BK);
           }
-          if (++stage == C::STAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
@@ -181,32 +270,22 @@ __global__ void __launch_bounds__(192, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {  // MMA issuer
-      constexpr uint32_t IDESC =
-          make_idesc(C::TM, BN, C::A_MN, C::B_MN) & (C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+      constexpr uint32_t IDESC = product_idesc<C>();
       int stage = 0, local = 0;
       uint32_t phase = 0;
       for (int tile = first; tile < all; tile += step, ++local) {
         const int acc = local & 1;
+        const int num_kb = steps_of(tile / s.tiles);
         mbar_wait<PAIR>(&tempty[acc], ((local >> 1) & 1) ^ 1, abort_flag, kErrTimeoutMma);
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < num_kb; ++kb) {
           mbar_wait(&full[stage], phase, abort_flag, kErrTimeoutMma);
           tc_fence_after();
-          const uint32_t a_base = smem_u32(sA + stage * C::A_BYTES);
-          const uint32_t b_base = smem_u32(sB + stage * C::B_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad =
-                C::A_MN ? make_sdesc(a_base + kk * 2048, 8192, 1024) : make_sdesc(a_base + kk * 32, 16, 1024);
-            const uint64_t bd =
-                C::B_MN ? make_sdesc(b_base + kk * 2048, 8192, 1024) : make_sdesc(b_base + kk * 32, 16, 1024);
-            if (PAIR) tc_mma2(d_tmem, ad, bd, IDESC, (kb | kk) != 0);
-            else tc_mma(d_tmem, ad, bd, IDESC, (kb | kk) != 0);
-          }
+          product_mma<C>(d_tmem, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == 0);
           if (PAIR) tc_commit2(&empty[stage], 0x3);
           else tc_commit(&empty[stage]);
-          if (++stage == C::STAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
@@ -217,33 +296,35 @@ __global__ void __launch_bounds__(192, 1)
     }
     __syncwarp();
   } else {  // epilogue: warp w reads tensor memory lanes 32 (w % 4) ..
-    const uint32_t q = warp & 3;
+    const int q = (int)(warp & 3);
     const uint32_t tempty0 = PAIR ? mapa_shared(tempty, 0) : 0;
+    EpiWarp w;
+    w.smem = slabs + (warp - 2) * E::SLABS;
+    w.bars = slab_bars + (warp - 2) * 2;
+    w.abort = abort_flag;
+    w.lane = (int)lane;
+    w.part = (int)(warp - 2) >> 2;
+    w.begun = 0;
+    if (first < all) E::prefetch(args, s, tile_at<C>(s, first, rank, q, (int)lane), w);
     int local = 0;
     for (int tile = first; tile < all; tile += step, ++local) {
-      int mb, nb, b;
-      product_tile<C>(s, tile, mb, nb, b);
       const int acc = local & 1;
-      TileAt at;
-      at.row0 = mb * C::TM + rank * BM + (int)q * 32;
-      at.row = at.row0 + (int)lane;
-      at.nb = nb;
-      at.n0 = nb * BN;
-      at.b = b;
-      at.mirror = C::SYM && mb != nb;
+      const TileAt at = tile_at<C>(s, tile, rank, q, (int)lane);
       // per-row values that the epilogue needs are loaded while the products run
       typename E::Row row_in;
       E::load_row(args, s, at, row_in);
       mbar_wait<PAIR>(&tfull[acc], (local >> 1) & 1, abort_flag, kErrTimeoutEpi);
       tc_fence_after();
-      E::template tile<BN>(args, s, at, row_in, tmem_base + ((q * 32) << 16) + acc * BN);
+      E::template tile<BN>(args, s, at, row_in, w, tmem_base + ((q * 32) << 16) + acc * BN);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (PAIR) mbar_arrive_cluster(tempty0 + acc * 8);
         else mbar_arrive(&tempty[acc]);
       }
+      if (tile + step < all) E::prefetch(args, s, tile_at<C>(s, tile + step, rank, q, (int)lane), w);
     }
+    if (lane == 0) bulk_store_wait<0, false>();
   }
   if (*abort_flag) {  // a wait ran out: give the copies in flight time to land
     const long long t0 = clock64();
@@ -276,12 +357,22 @@ __device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
 // A batch of matrices [rows, cols] of 16-bit values, row stride ld, matrices
 // `apart` elements from each other; boxes of 64 columns by `box_rows`.
 inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, int64_t ld, int64_t apart, int batch,
-                        int box_rows, bool f16) {
+                        int box_rows, bool f16, int box_cols = 64) {
   const uint64_t gdim[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
   const uint64_t gstride[2] = {(uint64_t)ld * 2, (uint64_t)apart * 2};
-  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  const uint32_t box[3] = {(uint32_t)box_cols, (uint32_t)box_rows, 1};
   return mt_host::encode_tiled(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base,
-                               gdim, gstride, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+                               gdim, gstride, box,
+                               box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ==
+         CUDA_SUCCESS;
+}
+// The same for fp32 results, in slabs of 32 columns by 32 rows.
+inline bool product_map_f32(CUtensorMap* m, const void* base, int rows, int cols, int64_t ld, int64_t apart, int batch) {
+  const uint64_t gdim[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
+  const uint64_t gstride[2] = {(uint64_t)ld * 4, (uint64_t)apart * 4};
+  const uint32_t box[3] = {32, 32, 1};
+  return mt_host::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, gdim, gstride, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 // Box heights of an operand: the tile's rows where K is contiguous, K steps else.
 template <class C>
@@ -296,6 +387,7 @@ ProductShape product_shape(int M, int N, int K, int batch) {
   s.N = N;
   s.K = K;
   s.batch = batch;
+  s.split_kb = 0;
   s.num_m = (M + C::TM - 1) / C::TM;
   s.num_n = (N + C::BN - 1) / C::BN;
   s.tiles = C::SYM ? s.num_m * (s.num_m + 1) / 2 : s.num_m * s.num_n;
@@ -309,12 +401,14 @@ template <class C, class E>
 cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const ProductShape& s,
                            const typename E::Args& args, cudaStream_t st) {
   auto kern = product_kernel<C, E>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  constexpr int smem = ProductSmem<C, E>::TOTAL;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t all = (int64_t)s.tiles * s.batch;
   const int sms = mt_host::num_sms();
   const int grid = C::PAIR ? 2 * (int)std::min<int64_t>(all, std::max(1, sms / 2)) : (int)std::min<int64_t>(all, sms);
-  e = mt_host::launch_early(kern, grid, 192, C::SMEM, st, C::PAIR ? 2 : 1, a, b, s, args);
+  e = mt_host::launch_early(kern, grid, 64 + 32 * E::WARPS, smem, st, C::PAIR ? 2 : 1, a, b, s, args);
   count_launches(1);
   return e;
 }
