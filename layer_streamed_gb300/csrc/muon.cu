@@ -56,16 +56,6 @@ __device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__flo
 __device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 
 // Eight fp16 values at a 16-byte boundary.
-__device__ __forceinline__ void load8h(const uint16_t* p, float* v) {
-  const uint4 w = *(const uint4*)p;
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = unpack_h2(ws[e]);
-    v[2 * e] = f.x;
-    v[2 * e + 1] = f.y;
-  }
-}
 __device__ __forceinline__ void store8h(uint16_t* p, const float* v) {
   *(uint4*)p = make_uint4(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]), pack_h2(v[4], v[5]), pack_h2(v[6], v[7]));
 }
@@ -185,31 +175,61 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues. Each works on slabs of 32 rows by 64 columns that come and go by
-// TMA (tile_product.cuh): a warp has two pairs of 4 KB, one in work and one on
-// its way. The square matrices' slabs leave twice, as they are and transposed.
+// Epilogues: eight warps, two to a row of the tile, each its half of the
+// columns in slabs of 32 rows by 64. What a slab needs comes by TMA; it is
+// taken into registers at once, so that the next one (of the next tile, often)
+// is on its way while this one is worked on. Results leave from the lanes, 32
+// bytes of a row at a time: whole sectors, and nothing waits for them. The
+// square matrices' mirror images leave transposed, by TMA.
+// (Results by TMA from where the operands came in, two places a warp, four
+// warps: 13 us for a 256 x 256 tile of X, the place being free again only when
+// the store has read it.)
 // ---------------------------------------------------------------------------
 constexpr int kSlab = 4096;
 
-// The next slab's place: free once what left from there before has been read.
-__device__ __forceinline__ uint8_t* next_slab(EpiWarp& w) {
-  uint8_t* p = w.smem + (w.begun++ & 1) * 2 * kSlab;
-  if (w.lane == 0) bulk_store_wait<1, true>();
-  __syncwarp();
-  return p;
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
-// 32 columns (half 0 or 1 of a slab's) of this lane's row of a square matrix
-// into the slab, and into its transposed image behind it: there a column of
-// the slab is a row of 64 bytes, this lane's value at 2 * lane.
-__device__ __forceinline__ void put_square(uint8_t* slab, int lane, int half, bool mirror, const float (&v)[32]) {
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+// Eight fp16 values as they came.
+__device__ __forceinline__ void unpack8h(const uint4& w, float* v) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack_h2(ws[e]);
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
+  }
+}
+// First column and one past the last of this warp's share of a tile.
+template <int BN>
+__device__ __forceinline__ void share(const TileAt& at, const ProductShape& s, const EpiWarp& w, int& c0, int& c1) {
+  c0 = at.n0 + w.part * (BN / 2);
+  c1 = min(c0 + BN / 2, s.N);
+}
+
+// 32 columns from col of this lane's row of a square matrix: the row itself
+// (rows are padded to whole 64 columns, so 32 bytes that begin inside can be
+// written whole), and into the transposed slab, where a column is 64 bytes and
+// this lane's value lies at 2 * lane.
+__device__ __forceinline__ void put_square(uint16_t* row, bool ok, uint8_t* slab, int lane, int col, int N, int half,
+                                           bool mirror, const float (&v)[32]) {
   uint32_t p[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = pack_h2(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *slab_piece(slab, lane, half * 4 + i) = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+  if (ok) {
+    if (col < N) store32(row + col, p);
+    if (col + 16 < N) store32(row + col + 16, p + 8);
+  }
   if (mirror) {
-    uint16_t* t = (uint16_t*)(slab + kSlab) + half * 1024 + lane;
+    uint16_t* t = (uint16_t*)slab + half * 1024 + lane;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       t[64 * i] = (uint16_t)p[i];
@@ -217,24 +237,32 @@ __device__ __forceinline__ void put_square(uint8_t* slab, int lane, int half, bo
     }
   }
 }
-__device__ __forceinline__ void send_square(const CUtensorMap* m, const CUtensorMap* mt, uint8_t* slab, int lane, int col,
-                                            const TileAt& at) {
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(m, slab, col, at.row0, at.b);
-    if (at.mirror) tma_store_3d(mt, slab + kSlab, at.row0, col, at.b);
-    bulk_store_commit();
+// The transposed slab's place is free when what left from it has been read.
+__device__ __forceinline__ void mirror_free(const TileAt& at, int lane) {
+  if (at.mirror) {
+    if (lane == 0) bulk_store_wait<0, true>();
+    __syncwarp();
+  }
+}
+__device__ __forceinline__ void send_mirror(const CUtensorMap* mt, uint8_t* slab, int lane, int col, const TileAt& at) {
+  if (at.mirror) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(mt, slab, at.row0, col, at.b);
+      bulk_store_commit();
+    }
   }
 }
 
 // A = X X^T: the rest of A to fp16, its diagonal to fp32.
 struct GramEpi : NoSlabs {
-  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
+  static constexpr int WARPS = 8, SLABS = kSlab;
   struct Args {
-    CUtensorMap O, OT;  // A's rest in slabs, and in transposed ones
+    CUtensorMap OT;  // A's rest in transposed slabs
+    uint16_t* O;
     float* d;
-    int64_t dpad;  // diagonal entries of a matrix
+    int64_t ld, dpad;  // row stride; diagonal entries of a matrix
   };
   struct Row {};
   static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
@@ -258,29 +286,33 @@ struct GramEpi : NoSlabs {
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
+    uint16_t* row = a.O + ((size_t)at.b * s.M + at.row) * a.ld;
+    int c0, c1;
+    share<BN>(at, s, w, c0, c1);
 #pragma unroll 1
-    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
-      uint8_t* slab = next_slab(w);
+    for (int col = c0; col < c1; col += 64) {
+      mirror_free(at, w.lane);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float v[32];
         tile_chunk(tb, (col - at.n0) / 32 + half, v);
         values(a, s, at, col + 32 * half, v);
-        put_square(slab, w.lane, half, at.mirror, v);
+        put_square(row, at.row < s.M, w.smem, w.lane, col + 32 * half, s.N, half, at.mirror, v);
       }
-      send_square(&a.O, &a.OT, slab, w.lane, col, at);
+      send_mirror(&a.OT, w.smem, w.lane, col, at);
     }
   }
 };
 
 // B = b A + c A^2 from O O^T, O and the diagonal.
 struct PolyEpi {
-  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
+  static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // O in, the mirror image out
   struct Args {
-    CUtensorMap O, B, BT;
+    CUtensorMap O, BT;
+    uint16_t* B;
     const float* d;
     float* db;
-    int64_t dpad;
+    int64_t ld, dpad;
     float b, c;
   };
   struct Row {
@@ -290,7 +322,7 @@ struct PolyEpi {
     r.d = at.row < s.M ? a.d[at.b * a.dpad + at.row] : 0.f;
   }
   static __device__ __forceinline__ void values(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                                int col, const float (&o)[32], const float* dj, float (&v)[32]) {
+                                                int col, const float (&o)[32], const float* dcol, float (&v)[32]) {
     const int here = at.row - col;
     if (here >= 0 && here < 32) {
       float sq = 0.f;
@@ -299,50 +331,56 @@ struct PolyEpi {
       if (at.row < s.M) a.db[at.b * a.dpad + at.row] = r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown));
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = fmaf(a.c, fmaf(r.d + dj[i], o[i], v[i] * kADown), a.b * o[i]);
-      v[i] = i == here ? 0.f : v[i];
+    for (int i = 0; i < 32; i += 4) {
+      const float4 dj = *(const float4*)(dcol + col + i);
+      const float d4[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = fmaf(a.c, fmaf(r.d + d4[e], o[i + e], v[i + e] * kADown), a.b * o[i + e]);
+        v[i + e] = i + e == here ? 0.f : x;
+      }
     }
   }
-  static __device__ __forceinline__ void request(const Args& a, const ProductShape& s, const TileAt& at, int col,
-                                                 EpiWarp& w) {
-    if (w.lane == 0 && at.row0 < s.M) {
-      uint64_t* bar = &w.bars[w.begun & 1];
-      mbar_arrive_expect_tx(bar, kSlab);
-      tma_load_3d(w.smem + (w.begun & 1) * 2 * kSlab, &a.O, bar, col, at.row0, at.b);
+  static __device__ __forceinline__ void request(const Args& a, const TileAt& at, int col, EpiWarp& w) {
+    if (w.lane == 0) {
+      mbar_arrive_expect_tx(&w.bars[0], kSlab);
+      tma_load_3d(w.smem, &a.O, &w.bars[0], col, at.row0, at.b);
     }
   }
+  template <int BN>
   static __device__ __forceinline__ void prefetch(const Args& a, const ProductShape& s, const TileAt& at, EpiWarp& w) {
-    if (w.lane == 0) bulk_store_wait<0, true>();
-    request(a, s, at, at.n0, w);
+    int c0, c1;
+    share<BN>(at, s, w, c0, c1);
+    if (at.row0 < s.M && c0 < c1) request(a, at, c0, w);
   }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
     const float* dcol = a.d + at.b * a.dpad;
+    uint16_t* row = a.B + ((size_t)at.b * s.M + at.row) * a.ld;
+    int c0, c1;
+    share<BN>(at, s, w, c0, c1);
 #pragma unroll 1
-    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
-      uint8_t* slab = w.smem + (w.begun & 1) * 2 * kSlab;
-      mbar_wait(&w.bars[w.begun & 1], (w.begun >> 1) & 1, w.abort, kErrTimeoutEpi);
-      ++w.begun;
+    for (int col = c0; col < c1; col += 64) {
+      mbar_wait(&w.bars[0], w.begun++ & 1, w.abort, kErrTimeoutEpi);
+      uint4 raw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = *slab_piece(w.smem, w.lane, i);
+      fence_proxy_async_smem();
+      mirror_free(at, w.lane);
+      __syncwarp();
+      if (col + 64 < c1) request(a, at, col + 64, w);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float v[32], o[32], dj[32];
+        float v[32], o[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *(float4*)(dj + 4 * i) = ((const float4*)(dcol + col + 32 * half))[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load8h((const uint16_t*)slab_piece(slab, w.lane, half * 4 + i), o + 8 * i);
+        for (int i = 0; i < 4; ++i) unpack8h(raw[half * 4 + i], o + 8 * i);
         tile_chunk(tb, (col - at.n0) / 32 + half, v);
-        values(a, s, at, r, col + 32 * half, o, dj, v);
-        put_square(slab, w.lane, half, at.mirror, v);
-        if (half == 0 && col + 64 < at.n0 + BN && col + 64 < s.N) {
-          // the other place: what left from it has been read meanwhile
-          if (w.lane == 0) bulk_store_wait<0, true>();
-          request(a, s, at, col + 64, w);
-        }
+        values(a, s, at, r, col + 32 * half, o, dcol, v);
+        put_square(row, at.row < s.M, w.smem + kSlab, w.lane, col + 32 * half, s.N, half, at.mirror, v);
       }
-      send_square(&a.B, &a.BT, slab, w.lane, col, at);
+      send_mirror(&a.BT, w.smem + kSlab, w.lane, col, at);
     }
   }
 };
@@ -350,17 +388,18 @@ struct PolyEpi {
 // X <- a X + B X; the last step leaves the result or takes the weights' step.
 template <bool LAST>
 struct ApplyEpi {
-  static constexpr int WARPS = 4, SLABS = 4 * kSlab;
+  static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // hi and lo in
   struct Args {
-    CUtensorMap hi, lo, hi_out;  // lo in place; hi_out: not LAST
+    CUtensorMap hi, lo;
+    uint16_t *hi_out, *lo_out;  // not LAST; lo_out is lo
     const float* db;
-    int64_t dpad;
+    int64_t ld, dpad;
     float a;
     int by_col;  // the diagonal runs along the columns (X B) or the rows (B X)
     // LAST: out [M, N] dense per matrix, out <- keep * out - step * X with
-    // update, else X
+    // update, else X; vec: 32 bytes of a row at a time
     void* out;
-    int out_bf16, update;
+    int out_bf16, update, vec;
     float keep, step;
   };
   struct Row {
@@ -369,80 +408,58 @@ struct ApplyEpi {
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     r.d = !a.by_col && at.row < s.M ? a.db[at.b * a.dpad + at.row] : 0.f;
   }
-  // four neighbouring values of the new X (times kXUp)
-  static __device__ __forceinline__ void step4(float a, const float* d, const float* h, const float* l, float* v) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = fmaf(a + d[e], h[e], fmaf(fmaf(0.5f, d[e], a), l[e], v[e] * kADown));
-  }
-  static __device__ __forceinline__ void request(const Args& a, const ProductShape& s, const TileAt& at, int col,
-                                                 EpiWarp& w) {
-    if (w.lane == 0 && at.row0 < s.M) {
-      uint64_t* bar = &w.bars[w.begun & 1];
-      uint8_t* p = w.smem + (w.begun & 1) * 2 * kSlab;
-      mbar_arrive_expect_tx(bar, 2 * kSlab);
-      tma_load_3d(p, &a.hi, bar, col, at.row0, at.b);
-      tma_load_3d(p + kSlab, &a.lo, bar, col, at.row0, at.b);
+  static __device__ __forceinline__ void request(const Args& a, const TileAt& at, int col, EpiWarp& w) {
+    if (w.lane == 0) {
+      mbar_arrive_expect_tx(&w.bars[0], 2 * kSlab);
+      tma_load_3d(w.smem, &a.hi, &w.bars[0], col, at.row0, at.b);
+      tma_load_3d(w.smem + kSlab, &a.lo, &w.bars[0], col, at.row0, at.b);
     }
   }
+  template <int BN>
   static __device__ __forceinline__ void prefetch(const Args& a, const ProductShape& s, const TileAt& at, EpiWarp& w) {
-    if (LAST) fence_proxy_async_smem();
-    __syncwarp();
-    if (!LAST && w.lane == 0) bulk_store_wait<0, true>();
-    request(a, s, at, at.n0, w);
+    int c0, c1;
+    share<BN>(at, s, w, c0, c1);
+    if (at.row0 < s.M && c0 < c1) request(a, at, c0, w);
   }
-  // LAST: 64 columns of 32 rows of results in the slab pair (fp32; of eight
-  // columns the first four where their hi were, the others where their lo
-  // were) to out, whole rows at a time: neighbouring lanes, neighbouring columns.
-  static __device__ __forceinline__ void write_rows(const Args& a, const ProductShape& s, const TileAt& at, int col,
-                                                    uint8_t* slab, int lane) {
-    const int rows = min(32, s.M - at.row0);
-    const int c = col + 2 * lane;
-    uint8_t* half = slab + (lane & 2 ? kSlab : 0);
-    const size_t o0 = ((size_t)at.b * s.M + at.row0) * s.N + c;
-    // pairs at a time where every row's pairs lie on their boundary
-    const bool pairs = (s.N & 1) == 0 && ((uintptr_t)a.out & (a.out_bf16 ? 3 : 7)) == 0;
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      float2 old[8];
+  // LAST: 16 results from `col` of this lane's row.
+  static __device__ __forceinline__ void finish16(const Args& a, const ProductShape& s, size_t row, int col, float* x) {
+    const size_t o = row + col;
+    if (a.vec && col + 16 <= s.N) {
+      if (a.out_bf16) {
+        uint32_t u[8];
+        if (a.update) {
+          load32((uint16_t*)a.out + o, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        old[i] = make_float2(0.f, 0.f);
-        const size_t o = o0 + (size_t)(r0 + i) * s.N;
-        if (a.update && r0 + i < rows && c < s.N) {
-          if (pairs) {
-            if (a.out_bf16) {
-              const uint32_t u = *(const uint32_t*)((const uint16_t*)a.out + o);
-              old[i] = make_float2(bf2f(u & 0xffff), bf2f(u >> 16));
-            } else {
-              old[i] = *(const float2*)((const float*)a.out + o);
-            }
-          } else {
-            old[i].x = load1(a.out, o, a.out_bf16);
-            if (c + 1 < s.N) old[i].y = load1(a.out, o + 1, a.out_bf16);
+          for (int e = 0; e < 8; ++e) {
+            x[2 * e] = fmaf(a.keep, bf2f(u[e] & 0xffff), -a.step * x[2 * e]);
+            x[2 * e + 1] = fmaf(a.keep, bf2f(u[e] >> 16), -a.step * x[2 * e + 1]);
           }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (r0 + i >= rows || c >= s.N) break;
-        const size_t o = o0 + (size_t)(r0 + i) * s.N;
-        float2 x = ((const float2*)slab_piece(half, r0 + i, lane >> 2))[lane & 1];
-        if (a.update) {
-          x.x = fmaf(a.keep, old[i].x, -a.step * x.x);
-          x.y = fmaf(a.keep, old[i].y, -a.step * x.y);
-        }
-        if (pairs) {
-          if (a.out_bf16) *(uint32_t*)((uint16_t*)a.out + o) = pack_bf2(x.x, x.y);
-          else *(float2*)((float*)a.out + o) = x;
-        } else if (a.out_bf16) {
-          ((uint16_t*)a.out)[o] = f2bf(x.x);
-          if (c + 1 < s.N) ((uint16_t*)a.out)[o + 1] = f2bf(x.y);
-        } else {
-          ((float*)a.out)[o] = x.x;
-          if (c + 1 < s.N) ((float*)a.out)[o + 1] = x.y;
+        for (int e = 0; e < 8; ++e) u[e] = pack_bf2(x[2 * e], x[2 * e + 1]);
+        store32((uint16_t*)a.out + o, u);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; q += 8) {
+          uint32_t u[8];
+          if (a.update) {
+            load32((float*)a.out + o + q, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[q + e] = fmaf(a.keep, __uint_as_float(u[e]), -a.step * x[q + e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(x[q + e]);
+          store32((float*)a.out + o + q, u);
         }
       }
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (col + e >= s.N) break;
+      const float r = a.update ? fmaf(a.keep, load1(a.out, o + e, a.out_bf16), -a.step * x[e]) : x[e];
+      if (a.out_bf16) ((uint16_t*)a.out)[o + e] = f2bf(r);
+      else ((float*)a.out)[o + e] = r;
     }
   }
   template <int BN>
@@ -450,78 +467,67 @@ struct ApplyEpi {
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
     const float* dcol = a.db + at.b * a.dpad;
+    const size_t x0 = ((size_t)at.b * s.M + at.row) * a.ld, out0 = ((size_t)at.b * s.M + at.row) * s.N;
+    int c0, c1;
+    share<BN>(at, s, w, c0, c1);
+    if (LAST && a.update && at.row < s.M) {  // the weights' lines, while the sums are waited for
+      const int e = a.out_bf16 ? 2 : 4;
+      for (int c = c0 * e; c < c1 * e; c += 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.out + out0 * e + c));
+    }
 #pragma unroll 1
-    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += 64) {
-      uint8_t* slab = w.smem + (w.begun & 1) * 2 * kSlab;
-      mbar_wait(&w.bars[w.begun & 1], (w.begun >> 1) & 1, w.abort, kErrTimeoutEpi);
-      ++w.begun;
-      const bool more = col + 64 < at.n0 + BN && col + 64 < s.N;
+    for (int col = c0; col < c1; col += 64) {
+      mbar_wait(&w.bars[0], w.begun++ & 1, w.abort, kErrTimeoutEpi);
+      uint4 rh[8], rl[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        rh[i] = *slab_piece(w.smem, w.lane, i);
+        rl[i] = *slab_piece(w.smem + kSlab, w.lane, i);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (col + 64 < c1) request(a, at, col + 64, w);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float v[32];
         tile_chunk(tb, (col - at.n0) / 32 + half, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4* hp = slab_piece(slab, w.lane, half * 4 + i);
-          uint4* lp = slab_piece(slab + kSlab, w.lane, half * 4 + i);
-          float h[8], l[8], d[8];
-          load8h((const uint16_t*)hp, h);
-          load8h((const uint16_t*)lp, l);
-          if (a.by_col) {
-            *(float4*)d = ((const float4*)(dcol + col + 32 * half))[2 * i];
-            *(float4*)(d + 4) = ((const float4*)(dcol + col + 32 * half))[2 * i + 1];
+        for (int q = 0; q < 2; ++q) {  // 16 columns
+          float* x = v + 16 * q;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float h[8], l[8];
+            unpack8h(rh[half * 4 + q * 2 + i], h);
+            unpack8h(rl[half * 4 + q * 2 + i], l);
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              float d[4] = {r.d, r.d, r.d, r.d};
+              if (a.by_col) *(float4*)d = *(const float4*)(dcol + col + 32 * half + 16 * q + 8 * i + e);
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                float& y = x[8 * i + e + f];
+                y = fmaf(a.a + d[f], h[e + f], fmaf(fmaf(0.5f, d[f], a.a), l[e + f], y * kADown));
+              }
+            }
+          }
+          const int c = col + 32 * half + 16 * q;
+          if (at.row >= s.M || c >= s.N) continue;
+          if (!LAST) {
+            uint32_t p[8], l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              p[e] = pack_h2(x[2 * e], x[2 * e + 1]);
+              const float2 f = unpack_h2(p[e]);
+              l[e] = pack_h2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+            }
+            store32(a.hi_out + x0 + c, p);
+            store32(a.lo_out + x0 + c, l);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = r.d;
-          }
-          step4(a.a, d, h, l, v + 8 * i);
-          step4(a.a, d + 4, h + 4, l + 4, v + 8 * i + 4);
-          if (!LAST) {
-            uint32_t p[4], q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = pack_h2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
-              const float2 f = unpack_h2(p[e]);
-              q[e] = pack_h2(v[8 * i + 2 * e] - f.x, v[8 * i + 2 * e + 1] - f.y);
-            }
-            *hp = make_uint4(p[0], p[1], p[2], p[3]);
-            *lp = make_uint4(q[0], q[1], q[2], q[3]);
+            for (int e = 0; e < 16; ++e) x[e] *= kXDown;
+            finish16(a, s, out0, c, x);
           }
         }
-        if (LAST) {
-          // the half's own 32 columns: their hi and lo have been read, and the
-          // other half's lie in the other half of the pieces
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *slab_piece(slab, w.lane, half * 4 + i) =
-                make_uint4(__float_as_uint(v[8 * i] * kXDown), __float_as_uint(v[8 * i + 1] * kXDown),
-                           __float_as_uint(v[8 * i + 2] * kXDown), __float_as_uint(v[8 * i + 3] * kXDown));
-            *slab_piece(slab + kSlab, w.lane, half * 4 + i) =
-                make_uint4(__float_as_uint(v[8 * i + 4] * kXDown), __float_as_uint(v[8 * i + 5] * kXDown),
-                           __float_as_uint(v[8 * i + 6] * kXDown), __float_as_uint(v[8 * i + 7] * kXDown));
-          }
-        }
-        if (half == 0 && more) {
-          if (!LAST && w.lane == 0) bulk_store_wait<0, true>();
-          if (LAST) {  // the other place has been read by this warp's own loads
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          request(a, s, at, col + 64, w);
-        }
-      }
-      if (!LAST) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (w.lane == 0) {
-          tma_store_3d(&a.hi_out, slab, col, at.row0, at.b);
-          tma_store_3d(&a.lo, slab + kSlab, col, at.row0, at.b);
-          bulk_store_commit();
-        }
-      } else {
-        __syncwarp();
-        write_rows(a, s, at, col, slab, w.lane);
-        __syncwarp();
       }
     }
   }
@@ -624,39 +630,41 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
   const bool tall = rows > cols;
   const int m = w.m;
   const Operand o{O, m, m, w.lda}, p{B, m, m, w.lda};
-  // slabs of X and of the square matrices, these also as 64 rows of 32 columns
-  CUtensorMap mX[2], mLo, mO, mOT, mB, mBT;
+  // slabs of X, of A, and transposed ones of A and of B (64 rows of 32 columns)
+  CUtensorMap mX[2], mLo, mO, mOT, mBT;
   const int64_t xa = w.ldx * rows, aa = w.lda * m;
   if (!product_map(&mX[0], hi[0], rows, cols, w.ldx, xa, batch, 32, true) ||
       !product_map(&mX[1], hi[1], rows, cols, w.ldx, xa, batch, 32, true) ||
       !product_map(&mLo, lo, rows, cols, w.ldx, xa, batch, 32, true) ||
       !product_map(&mO, O, m, m, w.lda, aa, batch, 32, true) ||
       !product_map(&mOT, O, m, m, w.lda, aa, batch, 64, true, 32) ||
-      !product_map(&mB, B, m, m, w.lda, aa, batch, 32, true) ||
       !product_map(&mBT, B, m, m, w.lda, aa, batch, 64, true, 32))
     return kLaunchFailed;
   for (int i = 0; i < steps && e == cudaSuccess; ++i) {
     const float *c = coef + 3 * i;
     const Operand x{hi[i & 1], rows, cols, w.ldx};
-    const GramEpi::Args ga{mO, mOT, d, w.dpad};
+    const GramEpi::Args ga{mOT, O, d, w.lda, w.dpad};
     e = tall ? product<true, true, true, GramEpi>(x, x, m, m, rows, batch, ga, st)
              : product<false, false, true, GramEpi>(x, x, m, m, cols, batch, ga, st);
     if (e != cudaSuccess) break;
-    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mB, mBT, d, db, w.dpad, c[1], c[2]}, st);
+    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mBT, B, d, db, w.lda, w.dpad, c[1], c[2]}, st);
     if (e != cudaSuccess) break;
     auto apply = [&](auto epi) {
       using E = decltype(epi);
       typename E::Args a{};
       a.hi = mX[i & 1];
       a.lo = mLo;
-      a.hi_out = mX[(i + 1) & 1];
+      a.hi_out = hi[(i + 1) & 1];
+      a.lo_out = lo;
       a.db = db;
+      a.ld = w.ldx;
       a.dpad = w.dpad;
       a.a = c[0];
       a.by_col = tall;
       a.out = out;
       a.out_bf16 = out_bf16;
       a.update = update;
+      a.vec = cols % (out_bf16 ? 16 : 8) == 0 && al(out, 32);
       a.keep = keep;
       a.step = step;
       return tall ? product<false, false, false, E>(x, p, rows, cols, m, batch, a, st)

@@ -148,7 +148,7 @@ struct EpiWarp {
 };
 // For epilogues without slabs coming in.
 struct NoSlabs {
-  template <class A>
+  template <int BN, class A>
   static __device__ __forceinline__ void prefetch(const A&, const ProductShape&, const TileAt&, EpiWarp&) {}
 };
 
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
     w.lane = (int)lane;
     w.part = (int)(warp - 2) >> 2;
     w.begun = 0;
-    if (first < all) E::prefetch(args, s, tile_at<C>(s, first, rank, q, (int)lane), w);
+    if (first < all) E::template prefetch<BN>(args, s, tile_at<C>(s, first, rank, q, (int)lane), w);
     int local = 0;
     for (int tile = first; tile < all; tile += step, ++local) {
       const int acc = local & 1;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
         if (PAIR) mbar_arrive_cluster(tempty0 + acc * 8);
         else mbar_arrive(&tempty[acc]);
       }
-      if (tile + step < all) E::prefetch(args, s, tile_at<C>(s, tile + step, rank, q, (int)lane), w);
+      if (tile + step < all) E::template prefetch<BN>(args, s, tile_at<C>(s, tile + step, rank, q, (int)lane), w);
     }
     if (lane == 0) bulk_store_wait<0, false>();
   }
