@@ -32,6 +32,7 @@
 // products made on and above the diagonal only and mirrored by the epilogue,
 // which also forms every linear combination: nothing runs between products.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -237,6 +238,28 @@ __device__ __forceinline__ void put_square(uint16_t* row, bool ok, uint8_t* slab
     }
   }
 }
+// The same straight to memory, the mirror image a column at a time: the lanes'
+// rows are neighbours there.
+__device__ __forceinline__ void write_square(uint16_t* mat, int64_t ld, const TileAt& at, int col, int m,
+                                             const float (&v)[32]) {
+  if (at.row >= m) return;
+  put_square(mat + (size_t)at.row * ld, true, nullptr, 0, col, m, 0, false, v);
+  if (at.mirror) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < m) mat[(size_t)(col + i) * ld + at.row] = f2h(v[i]);
+  }
+}
+// 32 fp16 values of a padded row, as far as it has groups of 16 from col on.
+__device__ __forceinline__ void load_row32(const uint16_t* row, int col, int N, uint32_t (&w)[16]) {
+  load32(row + col, w);
+  if (col + 16 < N) {
+    load32(row + col + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int i = 8; i < 16; ++i) w[i] = 0;
+  }
+}
 // The transposed slab's place is free when what left from it has been read.
 __device__ __forceinline__ void mirror_free(const TileAt& at, int lane) {
   if (at.mirror) {
@@ -302,6 +325,13 @@ struct GramEpi : NoSlabs {
       send_mirror(&a.OT, w.smem, w.lane, col, at);
     }
   }
+  struct Early {};
+  static __device__ __forceinline__ void early(const Args&, const ProductShape&, const TileAt&, int, Early&) {}
+  static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
+                                               const Early&, int col, float (&v)[32]) {
+    values(a, s, at, col, v);
+    write_square(a.O + (size_t)at.b * s.M * a.ld, a.ld, at, col, s.M, v);
+  }
 };
 
 // B = b A + c A^2 from O O^T, O and the diagonal.
@@ -309,6 +339,7 @@ struct PolyEpi {
   static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // O in, the mirror image out
   struct Args {
     CUtensorMap O, BT;
+    const uint16_t* O_rows;
     uint16_t* B;
     const float* d;
     float* db;
@@ -383,6 +414,25 @@ struct PolyEpi {
       send_mirror(&a.BT, w.smem + kSlab, w.lane, col, at);
     }
   }
+  struct Early {
+    uint32_t o[16];
+  };
+  static __device__ __forceinline__ void early(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                               Early& e) {
+    if (at.row < s.M) load_row32(a.O_rows + ((size_t)at.b * s.M + at.row) * a.ld, col, s.N, e.o);
+  }
+  static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                               const Early& e, int col, float (&v)[32]) {
+    float o[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = unpack_h2(e.o[i]);
+      o[2 * i] = f.x;
+      o[2 * i + 1] = f.y;
+    }
+    values(a, s, at, r, col, o, a.d + at.b * a.dpad, v);
+    write_square(a.B + (size_t)at.b * s.M * a.ld, a.ld, at, col, s.M, v);
+  }
 };
 
 // X <- a X + B X; the last step leaves the result or takes the weights' step.
@@ -391,7 +441,8 @@ struct ApplyEpi {
   static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // hi and lo in
   struct Args {
     CUtensorMap hi, lo;
-    uint16_t *hi_out, *lo_out;  // not LAST; lo_out is lo
+    const uint16_t* hi_rows;
+    uint16_t *hi_out, *lo_out;  // lo_out is lo
     const float* db;
     int64_t ld, dpad;
     float a;
@@ -466,8 +517,7 @@ struct ApplyEpi {
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
-    const float* dcol = a.db + at.b * a.dpad;
-    const size_t x0 = ((size_t)at.b * s.M + at.row) * a.ld, out0 = ((size_t)at.b * s.M + at.row) * s.N;
+    const size_t out0 = ((size_t)at.b * s.M + at.row) * s.N;
     int c0, c1;
     share<BN>(at, s, w, c0, c1);
     if (LAST && a.update && at.row < s.M) {  // the weights' lines, while the sums are waited for
@@ -492,44 +542,62 @@ struct ApplyEpi {
         float v[32];
         tile_chunk(tb, (col - at.n0) / 32 + half, v);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // 16 columns
-          float* x = v + 16 * q;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float h[8], l[8];
-            unpack8h(rh[half * 4 + q * 2 + i], h);
-            unpack8h(rl[half * 4 + q * 2 + i], l);
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              float d[4] = {r.d, r.d, r.d, r.d};
-              if (a.by_col) *(float4*)d = *(const float4*)(dcol + col + 32 * half + 16 * q + 8 * i + e);
-#pragma unroll
-              for (int f = 0; f < 4; ++f) {
-                float& y = x[8 * i + e + f];
-                y = fmaf(a.a + d[f], h[e + f], fmaf(fmaf(0.5f, d[f], a.a), l[e + f], y * kADown));
-              }
-            }
-          }
-          const int c = col + 32 * half + 16 * q;
-          if (at.row >= s.M || c >= s.N) continue;
-          if (!LAST) {
-            uint32_t p[8], l[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              p[e] = pack_h2(x[2 * e], x[2 * e + 1]);
-              const float2 f = unpack_h2(p[e]);
-              l[e] = pack_h2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
-            }
-            store32(a.hi_out + x0 + c, p);
-            store32(a.lo_out + x0 + c, l);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= kXDown;
-            finish16(a, s, out0, c, x);
-          }
+        for (int q = 0; q < 2; ++q) {
+          const uint4 *hq = rh + half * 4 + q * 2, *lq = rl + half * 4 + q * 2;
+          const uint32_t h[8] = {hq[0].x, hq[0].y, hq[0].z, hq[0].w, hq[1].x, hq[1].y, hq[1].z, hq[1].w};
+          const uint32_t l[8] = {lq[0].x, lq[0].y, lq[0].z, lq[0].w, lq[1].x, lq[1].y, lq[1].z, lq[1].w};
+          step16(a, s, at, r, col + 32 * half + 16 * q, h, l, v + 16 * q);
         }
       }
     }
+  }
+  // 16 columns from col of this lane's row
+  static __device__ __forceinline__ void step16(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                                int col, const uint32_t* hw, const uint32_t* lw, float* x) {
+    const float* dcol = a.db + at.b * a.dpad + col;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float d[4] = {r.d, r.d, r.d, r.d};
+      if (a.by_col) *(float4*)d = *(const float4*)(dcol + i);
+      const float2 h0 = unpack_h2(hw[i / 2]), h1 = unpack_h2(hw[i / 2 + 1]), l0 = unpack_h2(lw[i / 2]),
+                   l1 = unpack_h2(lw[i / 2 + 1]);
+      const float h[4] = {h0.x, h0.y, h1.x, h1.y}, l[4] = {l0.x, l0.y, l1.x, l1.y};
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        x[i + f] = fmaf(a.a + d[f], h[f], fmaf(fmaf(0.5f, d[f], a.a), l[f], x[i + f] * kADown));
+    }
+    if (at.row >= s.M || col >= s.N) return;
+    const size_t row = (size_t)at.b * s.M + at.row;
+    if (!LAST) {
+      uint32_t p[8], l[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = pack_h2(x[2 * e], x[2 * e + 1]);
+        const float2 f = unpack_h2(p[e]);
+        l[e] = pack_h2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
+      }
+      store32(a.hi_out + row * a.ld + col, p);
+      store32(a.lo_out + row * a.ld + col, l);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= kXDown;
+      finish16(a, s, row * s.N, col, x);
+    }
+  }
+  struct Early {
+    uint32_t h[16], l[16];
+  };
+  static __device__ __forceinline__ void early(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                               Early& e) {
+    if (at.row >= s.M) return;
+    const size_t o = ((size_t)at.b * s.M + at.row) * a.ld;
+    load_row32(a.hi_rows + o, col, s.N, e.h);
+    load_row32(a.lo_out + o, col, s.N, e.l);
+  }
+  static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                               const Early& e, int col, float (&v)[32]) {
+    step16(a, s, at, r, col, e.h, e.l, v);
+    step16(a, s, at, r, col + 16, e.h + 8, e.l + 8, v + 16);
   }
 };
 
@@ -574,7 +642,9 @@ Ws workspace(int batch, int rows, int cols) {
   return w;
 }
 
-// D = A B^T of fp16 matrices in a batch, tiles by how many there are.
+// D = A B^T of fp16 matrices in a batch. Few tiles: 128 x 128, each shared by
+// four or two CTAs where that still leaves every CTA an SM; else 256 x 256 on
+// SM pairs where they fill half of the pairs, 128 x 128 on single SMs.
 struct Operand {
   const void* p;
   int rows, cols;
@@ -583,19 +653,26 @@ struct Operand {
 template <bool A_MN, bool B_MN, bool SYM, class E>
 cudaError_t product(const Operand& A, const Operand& B, int M, int N, int K, int batch, const typename E::Args& args,
                     cudaStream_t st) {
-  auto go = [&](auto cfg) {
+  auto go = [&](auto cfg, auto split) {
     using C = decltype(cfg);
+    constexpr int S = decltype(split)::value;
     CUtensorMap ta, tb;
     if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(), true) ||
         !product_map(&tb, B.p, B.rows, B.cols, B.ld, B.ld * B.rows, batch, b_box<C>(), true))
       return cudaErrorUnknown;
-    return launch_product<C, E>(ta, tb, product_shape<C>(M, N, K, batch), args, st);
+    const ProductShape s = product_shape<C>(M, N, K, batch);
+    if constexpr (S > 1) return launch_split<C, E, S>(ta, tb, s, args, st);
+    else return launch_product<C, E>(ta, tb, s, args, st);
   };
   using Wide = ProductCfg<256, true, A_MN, B_MN, true, SYM>;
-  // 256 x 256 tiles on SM pairs where they fill half of the pairs, else 128 x 128 on single SMs
-  const ProductShape w = product_shape<Wide>(M, N, K, batch);
-  if ((int64_t)w.tiles * batch >= mt_host::num_sms() / 4) return go(Wide());
-  return go(ProductCfg<128, false, A_MN, B_MN, true, SYM>());
+  using Small = ProductCfg<128, false, A_MN, B_MN, true, SYM>;
+  const int sms = mt_host::num_sms();
+  const int64_t wide = (int64_t)product_shape<Wide>(M, N, K, batch).tiles * batch;
+  const int64_t small = (int64_t)product_shape<Small>(M, N, K, batch).tiles * batch;
+  if (4 * small <= sms) return go(Small(), std::integral_constant<int, 4>());
+  if (2 * small <= sms) return go(Small(), std::integral_constant<int, 2>());
+  if (wide >= sms / 4) return go(Wide(), std::integral_constant<int, 1>());
+  return go(Small(), std::integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -647,13 +724,14 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
     e = tall ? product<true, true, true, GramEpi>(x, x, m, m, rows, batch, ga, st)
              : product<false, false, true, GramEpi>(x, x, m, m, cols, batch, ga, st);
     if (e != cudaSuccess) break;
-    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mBT, B, d, db, w.lda, w.dpad, c[1], c[2]}, st);
+    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mBT, O, B, d, db, w.lda, w.dpad, c[1], c[2]}, st);
     if (e != cudaSuccess) break;
     auto apply = [&](auto epi) {
       using E = decltype(epi);
       typename E::Args a{};
       a.hi = mX[i & 1];
       a.lo = mLo;
+      a.hi_rows = hi[i & 1];
       a.hi_out = hi[(i + 1) & 1];
       a.lo_out = lo;
       a.db = db;

@@ -352,6 +352,205 @@ __device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
 }
 
 // ---------------------------------------------------------------------------
+// The form for few tiles: a cluster of S CTAs (2 or 4) shares one 128 x 128
+// tile, each a range of K; then each gets a 128 / S wide share of its columns
+// from the others through distributed shared memory, adds the parts in rank
+// order and runs the epilogue on it, 32 columns of a row a thread. Three
+// 32 KB steps in flight and one accumulator let two CTAs share an SM: a
+// launch's CTAs set up while those of the launch before it end.
+// E::early asks for what E::chunk needs beside the sums, while these are made.
+// ---------------------------------------------------------------------------
+struct SplitSmem {
+  static constexpr int STAGES = 3;
+  static constexpr int PART = 128 * 32 * 4;  // 128 rows of a 32-column chunk
+};
+
+template <class C, class E, int S>
+__global__ void __launch_bounds__(192, 2)
+    product_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ ProductShape s, const __grid_constant__ typename E::Args args) {
+  constexpr int BN = C::BN, BM = C::BM, BK = C::BK, STAGES = SplitSmem::STAGES;
+  static_assert(!C::PAIR && BN == 128 && (S == 2 || S == 4), "one SM a CTA, chunks of 32 columns");
+  static_assert(4 * SplitSmem::PART <= STAGES * C::STAGE_BYTES, "the parts take the ring's place");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * C::A_BYTES;
+  uint64_t* full = (uint64_t*)(smem + STAGES * C::STAGE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* done = empty + STAGES;
+  uint32_t* tmem_slot = (uint32_t*)(done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int rank = (int)cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_wait();
+  grid_release();
+
+  const int tile = (int)blockIdx.x / S;
+  const int all_kb = (s.K + BK - 1) / BK, each = (all_kb + S - 1) / S;
+  const int k0 = min(all_kb, rank * each), k1 = min(all_kb, k0 + each);
+  int mb, nb, b;
+  product_tile<C>(s, tile, mb, nb, b);
+  constexpr int CHUNKS = 4 / S;  // of this CTA's share
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int kb = k0; kb < k1; ++kb) {
+        const int stage = (kb - k0) % STAGES;
+        mbar_wait(&empty[stage], (((kb - k0) / STAGES) & 1) ^ 1, abort_flag, kErrTimeoutTma);
+        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        uint8_t* a_dst = sA + stage * C::A_BYTES;
+        uint8_t* b_dst = sB + stage * C::B_BYTES;
+        if (!C::A_MN) {
+          tma_load_3d(a_dst, &tmA, &full[stage], kb * BK, mb * BM, b);
+        } else {
+#pragma unroll
+          for (int j = 0; j < BM / 64; ++j)
+            tma_load_3d(a_dst + j * 8192, &tmA, &full[stage], mb * BM + 64 * j, kb * BK, b);
+        }
+        if (!C::B_MN) {
+          tma_load_3d(b_dst, &tmB, &full[stage], kb * BK, nb * BN, b);
+        } else {
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j)
+            tma_load_3d(b_dst + j * 8192, &tmB, &full[stage], nb * BN + 64 * j, kb * BK, b);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t IDESC = product_idesc<C>();
+      for (int kb = k0; kb < k1; ++kb) {
+        const int stage = (kb - k0) % STAGES;
+        mbar_wait(&full[stage], ((kb - k0) / STAGES) & 1, abort_flag, kErrTimeoutMma);
+        tc_fence_after();
+        product_mma<C>(tmem_base, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == k0);
+        tc_commit(&empty[stage]);
+      }
+      tc_commit(done);  // with no steps: arrives at once
+    }
+    __syncwarp();
+  }
+  // warps 2 ..: lanes 32 (w % 4) .. of tensor memory
+  const int q = (int)(warp & 3);
+  TileAt at;
+  at.row0 = mb * BM + q * 32;
+  at.row = at.row0 + (int)lane;
+  at.nb = nb;
+  at.n0 = nb * BN;
+  at.b = b;
+  at.mirror = C::SYM && mb != nb;
+  const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+  const bool finish = warp >= 2 && at.row0 < s.M;
+  typename E::Row row_in;
+  typename E::Early early[CHUNKS];
+  if (warp >= 2) {
+    E::load_row(args, s, at, row_in);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int col = at.n0 + 32 * (rank * CHUNKS + c);
+      if (finish && col < s.N) E::early(args, s, at, col, early[c]);
+    }
+    mbar_wait(done, 0, abort_flag, kErrTimeoutEpi);
+    tc_fence_after();
+  }
+  cluster_sync();  // every CTA's MMAs have read their operands: the rings are free
+  if (warp >= 2) {
+#pragma unroll 1
+    for (int j = 1; j < S; ++j) {  // each CTA begins with another one's share
+      const int owner = (rank + j) % S;
+#pragma unroll 1
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int chunk = owner * CHUNKS + c;
+        if (at.n0 + 32 * chunk >= s.N) break;
+        float v[32];
+        if (k0 < k1) {
+          tile_chunk(tb, chunk, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        // [source][chunk of the owner's share][4 columns][row]
+        const uint32_t to =
+            mapa_shared(smem + (rank * CHUNKS + c) * SplitSmem::PART, (uint32_t)owner) + (q * 32 + lane) * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + i * 128 * 16), "f"(v[4 * i]),
+                       "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                       : "memory");
+      }
+    }
+    __syncwarp();
+  }
+  cluster_sync();  // the parts are there
+  if (finish) {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int chunk = rank * CHUNKS + c;
+      if (at.n0 + 32 * chunk >= s.N) break;
+      float v[32], sum[32];
+      if (k0 < k1) {
+        tile_chunk(tb, chunk, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        if (r == rank) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i] += v[i];
+        } else {
+          const float4* p = (const float4*)(smem + (r * CHUNKS + c) * SplitSmem::PART) + q * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 w = p[i * 128];
+            sum[4 * i] += w.x, sum[4 * i + 1] += w.y, sum[4 * i + 2] += w.z, sum[4 * i + 3] += w.w;
+          }
+        }
+      }
+      E::chunk(args, s, at, row_in, early[c], at.n0 + 32 * chunk, sum);
+    }
+  }
+  if (*abort_flag) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 24)) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, BN);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 // A batch of matrices [rows, cols] of 16-bit values, row stride ld, matrices
@@ -409,6 +608,18 @@ cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Pro
   const int sms = mt_host::num_sms();
   const int grid = C::PAIR ? 2 * (int)std::min<int64_t>(all, std::max(1, sms / 2)) : (int)std::min<int64_t>(all, sms);
   e = mt_host::launch_early(kern, grid, 64 + 32 * E::WARPS, smem, st, C::PAIR ? 2 : 1, a, b, s, args);
+  count_launches(1);
+  return e;
+}
+
+template <class C, class E, int S>
+cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const ProductShape& s,
+                         const typename E::Args& args, cudaStream_t st) {
+  auto kern = product_split_kernel<C, E, S>;
+  constexpr int smem = SplitSmem::STAGES * C::STAGE_BYTES + 1024 + 128;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = mt_host::launch_early(kern, s.tiles * s.batch * S, 192, smem, st, S, a, b, s, args);
   count_launches(1);
   return e;
 }
