@@ -17,8 +17,8 @@
 // tensor cores, bound them.
 //
 // Rows that are not scored (label below 0) have dz = 0 whatever their inputs
-// hold: the backward works on a copy of X in which they are zero, since 0
-// times an infinity or a NaN would reach every row of dW.
+// hold; dW is made from a copy of X in which they are zero, since 0 times an
+// infinity or a NaN would reach every row of it.
 #include <algorithm>
 
 #include "tile_product.cuh"
@@ -148,22 +148,6 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
-// X with the rows that are not scored set to zero: eight values a thread.
-__global__ void __launch_bounds__(256) scored_rows_kernel(const uint16_t* X, int64_t ldx, const int32_t* labels, int V,
-                                                          uint16_t* out, int T, int h) {
-  grid_wait();
-  grid_release();
-  const int n8 = h >> 3;
-  const int64_t all = (int64_t)T * n8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int t = (int)(i / n8), c = (int)(i - (int64_t)t * n8);
-    const int y = labels[t];
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (y >= 0 && y < V) v = *(const uint4*)(X + t * ldx + 8 * c);
-    *(uint4*)(out + (int64_t)t * h + 8 * c) = v;
-  }
-}
-
 // Eight values at p (16-byte aligned) in either type.
 __device__ __forceinline__ void load8(const void* base, size_t at, bool bf16, float (&v)[8]) {
   if (bf16) {
@@ -202,7 +186,27 @@ struct GradEpi : NoSlabs {
     const float *lse, *g;
     int V, v0;  // vocabulary, the piece's first column
     float scale, smooth, zc;
+    // with the first piece: X with the rows that are not scored set to zero
+    const uint16_t* X;
+    uint16_t* xs;  // null: not wanted
+    int64_t ldx;
+    int T, h;
   };
+  // The copy of X is made by the epilogue's warps, which have nothing to do
+  // until the first tile's products are there.
+  static __device__ __forceinline__ void begin(const Args& a, int warp) {
+    if (!a.xs) return;
+    const int n8 = a.h >> 3;
+    const int64_t all = (int64_t)a.T * n8, step = (int64_t)gridDim.x * (32 * WARPS);
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.x * (32 * WARPS) + warp * 32 + lane_id(); i < all; i += step) {
+      const int t = (int)(i / n8), c = (int)(i - (int64_t)t * n8);
+      const int y = a.labels[t];
+      uint4 v = *(const uint4*)(a.X + t * a.ldx + 8 * c);
+      if (y < 0 || y >= a.V) v = make_uint4(0, 0, 0, 0);
+      *(uint4*)(a.xs + (int64_t)t * a.h + 8 * c) = v;
+    }
+  }
   struct Row {
     int label;      // in the piece's columns
     float lse2, cp, cl, c0;
@@ -236,9 +240,8 @@ struct GradEpi : NoSlabs {
         const int c0 = j * 64 + half * 32;
         float v[32];
         tile_chunk(tb, 2 * j + half, v);
-        // the rows that X has been cleared in have z = 0, lse = 0 and all factors 0
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(r.cp, ex2(fmaf(v[i], k, -r.lse2)), -r.c0);
+        for (int i = 0; i < 32; ++i) v[i] = r.scored ? fmaf(r.cp, ex2(fmaf(v[i], k, -r.lse2)), -r.c0) : 0.f;
         if (here >= c0 && here < c0 + 32) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] -= here == c0 + i ? r.cl : 0.f;
@@ -259,19 +262,17 @@ struct GradEpi : NoSlabs {
   }
 };
 
-// out = scale * accumulator, N a multiple of 8: bf16 or fp32 by slabs, or
-// added to what is there or to an fp32 sum (the addend is asked for ahead of
-// the accumulator, a chunk of 32 columns at a time).
+// out = scale * accumulator (+ what is there, or an fp32 sum), N a multiple of
+// 8; two warps a row as above, 32 columns at a time. The addend is asked for
+// ahead of the accumulator.
 struct SumEpi : NoSlabs {
-  static constexpr int kSlab = 4096;
-  static constexpr int WARPS = 4, SLABS = 2 * kSlab;
+  static constexpr int WARPS = 8, SLABS = 0;
   struct Args {
-    CUtensorMap map;  // of out
     void* out;
     const void* add;  // same row stride; null: nothing
-    int64_t ld;
+    int64_t ld, apart;  // row stride; from one range's sums to the next one's
     float scale;
-    int out_bf16, add_bf16;
+    int out_bf16, add_bf16, sectors;  // sectors: bf16 rows in pieces of 32 bytes
   };
   struct Row {};
   static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
@@ -279,63 +280,33 @@ struct SumEpi : NoSlabs {
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
-    if (a.add) {
-      added<BN>(a, s, at, tb);
-      return;
-    }
-    const int wide = a.out_bf16 ? 64 : 32;  // columns of a slab
-#pragma unroll 1
-    for (int col = at.n0; col < at.n0 + BN && col < s.N; col += wide) {
-      uint8_t* slab = w.smem + (w.begun++ & 1) * kSlab;
-      if (w.lane == 0) bulk_store_wait<1, true>();
-      __syncwarp();
-#pragma unroll 1
-      for (int half = 0; half < wide / 32; ++half) {
-        float v[32];
-        tile_chunk(tb, (col - at.n0) / 32 + half, v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= a.scale;
-        if (a.out_bf16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *slab_piece(slab, w.lane, half * 4 + i) =
-                make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
-                           pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *(float4*)slab_piece(slab, w.lane, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (w.lane == 0) {
-        tma_store_3d(&a.map, slab, col, at.row0, at.b);
-        bulk_store_commit();
-      }
-    }
-  }
-  template <int BN>
-  static __device__ __forceinline__ void added(const Args& a, const ProductShape& s, const TileAt& at, uint32_t tb) {
     const bool ok = at.row < s.M;
-    const size_t row = (size_t)at.row * a.ld;
+    const size_t row = (size_t)at.b * a.apart + (size_t)at.row * a.ld;
 #pragma unroll 1
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = w.part * (BN / 64); c < (w.part + 1) * (BN / 64); ++c) {
       const int col = at.n0 + c * 32;
       if (col >= s.N) break;
       float add[4][8];
+      if (a.add && ok) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (ok && col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
+        for (int i = 0; i < 4; ++i)
+          if (col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
+      }
       float v[32];
       tile_chunk(tb, c, v);
       if (!ok) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i >= s.N) break;
+      for (int i = 0; i < 32; ++i) v[i] = a.add ? fmaf(v[i], a.scale, add[i >> 3][i & 7]) : v[i] * a.scale;
+      if (a.out_bf16 && a.sectors && col + 32 <= s.N) {
+        uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] = fmaf(v[8 * i + j], a.scale, add[i][j]);
-        store8(a.out, row + col + 8 * i, a.out_bf16, v + 8 * i);
+        for (int i = 0; i < 16; ++i) p[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
+        store32((uint16_t*)a.out + row + col, p);
+        store32((uint16_t*)a.out + row + col + 16, p + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + 8 * i < s.N) store8(a.out, row + col + 8 * i, a.out_bf16, v + 8 * i);
       }
     }
   }
@@ -459,12 +430,10 @@ cudaError_t gradient(const void* A, int64_t lda, const void* B, int64_t ldb, int
   s.add = ranges > 1 ? nullptr : add;
   s.ld = N;
   s.scale = scale;
+  s.apart = all;
   s.out_bf16 = ranges == 1 && bf16;
   s.add_bf16 = add_bf16;
-  const int64_t apart = used > 1 ? all : N;
-  if (!(s.out_bf16 ? product_map(&s.map, s.out, M, N, N, apart, used, 32, false)
-                   : product_map_f32(&s.map, s.out, M, N, N, apart, used)))
-    return cudaErrorUnknown;
+  s.sectors = N % 16 == 0 && al(out, 32);
   cudaError_t e = product<A_MN, B_MN, SumEpi>(A, lda, B, ldb, M, N, K, s, st, ranges);
   if (ranges > 1 && e == cudaSuccess) {
     e = mt_host::launch_early(join_ranges_kernel, (int)std::min<int64_t>((all + 1023) / 1024, kSms * 8), 256, 0, st, 1,
@@ -514,10 +483,7 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   uint16_t* dz = (uint16_t*)((uint8_t*)work + o.dz);
   float* part = (float*)((uint8_t*)work + o.acc);
   float* acc = dx_bf16 ? part : (float*)dX;
-  const int64_t units = ((int64_t)T * (h / 8) + 255) / 256;
-  cudaError_t e = mt_host::launch_early(scored_rows_kernel, (int)std::min<int64_t>(units, 152 * 16), 256, 0, st, 1, X,
-                                        (int64_t)ldx, labels, V, xs, T, h);
-  count_launches(1);
+  cudaError_t e = cudaSuccess;
   for (int v0 = 0; v0 < V && e == cudaSuccess; v0 += o.cols) {
     const int n = std::min(o.cols, V - v0);
     const int64_t ld = (int64_t)up(n, 64);
@@ -532,7 +498,12 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
     a.scale = scale;
     a.smooth = smooth;
     a.zc = zc;
-    e = product<false, false, GradEpi>(xs, h, Wp, ldw, T, n, h, a, st);
+    a.X = X;
+    a.xs = dW && v0 == 0 ? xs : nullptr;
+    a.ldx = ldx;
+    a.T = T;
+    a.h = h;
+    e = product<false, false, GradEpi>(X, ldx, Wp, ldw, T, n, h, a, st);
     if (e == cudaSuccess && dX) {
       const bool last = v0 + n == V;
       e = gradient<false, true>(dz, ld, Wp, ldw, T, h, n, o.dx_ranges, part, last ? dX : acc, last && dx_bf16,

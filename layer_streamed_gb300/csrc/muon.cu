@@ -188,17 +188,6 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------
 constexpr int kSlab = 4096;
 
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
-}
 // Eight fp16 values as they came.
 __device__ __forceinline__ void unpack8h(const uint4& w, float* v) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -337,6 +326,8 @@ struct GramEpi : NoSlabs {
 // B = b A + c A^2 from O O^T, O and the diagonal.
 struct PolyEpi {
   static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // O in, the mirror image out
+  template <class A>
+  static __device__ __forceinline__ void begin(const A&, int) {}
   struct Args {
     CUtensorMap O, BT;
     const uint16_t* O_rows;
@@ -439,6 +430,8 @@ struct PolyEpi {
 template <bool LAST>
 struct ApplyEpi {
   static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // hi and lo in
+  template <class A>
+  static __device__ __forceinline__ void begin(const A&, int) {}
   struct Args {
     CUtensorMap hi, lo;
     const uint16_t* hi_rows;

@@ -368,7 +368,9 @@ int sandwich_norm_fwd(const float* x, const void* y, const void* gate, bool bf16
   };
   auto pick = [&](auto b, auto g) {
     constexpr bool B = decltype(b)::value, G = decltype(g)::value;
-    if (n4 <= 1024) go(sandwich_fwd_kernel<B, G, 1>, 1);
+    // one group a thread is the shortest way through few rows; four keep more of
+    // many rows in flight
+    if (n4 <= 1024 && T <= kMaxSms * 2) go(sandwich_fwd_kernel<B, G, 1>, 1);
     else go(sandwich_fwd_kernel<B, G, 4>, 4);
   };
   auto pick_g = [&](auto b) { gate ? pick(b, std::true_type()) : pick(b, std::false_type()); };
@@ -385,12 +387,14 @@ int sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, bool 
   if (!sandwich_norm_dims(T, h) || !al(x_out, 16) || !al(y, ya) || !al(gate, ya) || !al(w_post, 16) ||
       !al(w_pre, 16) || !al(dn, 16) || !al(dres, 16) || !al(dx, 16) || !al(dy, ya) || !al(dgate, ya) || !al(work, 16))
     return kRefused;
-  const BwdShape shape = bwd_shape(h);
+  BwdShape shape = bwd_shape(h);
   const int parts = shape.parts(T, std::min(mt_host::num_sms(), kMaxSms));
+  shape.stages = std::min(shape.stages, (T + parts - 1) / parts + 1);  // no more than there are rows for
   cudaError_t e = cudaSuccess;
   auto go = [&](auto k) {
     const int smem = shape.stages * h * (dres ? 12 : 8);
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+    if (smem > 47 * 1024)  // with the static part past the default limit
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
     if (e == cudaSuccess)
       e = mt_host::launch_early(k, parts, shape.threads, smem, st, 1, x_out, y, gate, w_post, w_pre, alpha, rstd_post,
                                 rstd_pre, dn, dres, dx, dy, dgate, work, T, h, shape.stages);

@@ -146,8 +146,11 @@ struct EpiWarp {
   int lane, part;
   uint32_t begun;
 };
-// For epilogues without slabs coming in.
+// For epilogues without slabs coming in, and without work of their own before
+// the first tile.
 struct NoSlabs {
+  template <class A>
+  static __device__ __forceinline__ void begin(const A&, int) {}
   template <int BN, class A>
   static __device__ __forceinline__ void prefetch(const A&, const ProductShape&, const TileAt&, EpiWarp&) {}
 };
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
     w.lane = (int)lane;
     w.part = (int)(warp - 2) >> 2;
     w.begun = 0;
+    E::begin(args, (int)(warp - 2));
     if (first < all) E::template prefetch<BN>(args, s, tile_at<C>(s, first, rank, q, (int)lane), w);
     int local = 0;
     for (int tile = first; tile < all; tile += step, ++local) {
@@ -341,6 +345,18 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
   }
 }
 
+// 32 bytes at a 32-byte boundary: a whole sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
 // 32 accumulator columns of this lane's row.
 __device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
   uint32_t r[32];
@@ -564,14 +580,6 @@ inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, in
                                gdim, gstride, box,
                                box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ==
          CUDA_SUCCESS;
-}
-// The same for fp32 results, in slabs of 32 columns by 32 rows.
-inline bool product_map_f32(CUtensorMap* m, const void* base, int rows, int cols, int64_t ld, int64_t apart, int batch) {
-  const uint64_t gdim[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
-  const uint64_t gstride[2] = {(uint64_t)ld * 4, (uint64_t)apart * 4};
-  const uint32_t box[3] = {32, 32, 1};
-  return mt_host::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, gdim, gstride, box,
-                               CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 // Box heights of an operand: the tile's rows where K is contiguous, K steps else.
 template <class C>
