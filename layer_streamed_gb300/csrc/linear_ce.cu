@@ -343,10 +343,14 @@ constexpr int kSms = 152;  // sizes the workspace, whatever machine asks
 inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Tiles of 256 x 256 on SM pairs where they fill half of the pairs, else 128 x
-// 128 on single SMs.
-bool wide(int64_t M, int64_t N) {
-  return ((M + 255) / 256) * ((N + 255) / 256) >= mt_host::num_sms() / 4;
+// Tiles of 256 x 256 on SM pairs where they fill half of the pairs; 128 x 128
+// on single SMs for fewer of them, for few rows (M up to 128: half of a pair's
+// tile would be empty; 128 tokens, V 32000, h 1024: dX 40 us on pairs, 36.4 on
+// single SMs) and for shallow sums (K up to 256: what counts is how many warps
+// write results; there dW of 7 tokens 47 against 41 us, of 256 tokens 50.5
+// against 48.5, of 512 66.6 against 75.4).
+bool wide(int64_t M, int64_t N, int64_t K) {
+  return M > 128 && K > 256 && ((M + 255) / 256) * ((N + 255) / 256) >= mt_host::num_sms() / 4;
 }
 
 // The columns of a piece: dz of a piece has at most 2^28 values (or 256
@@ -360,14 +364,16 @@ int piece_cols(int T, int V) {
 // Ranges that the K of a gradient's product [M, N] is cut into: few tiles
 // (few tokens, or a small vocabulary) leave most of the GPU idle otherwise.
 // The number that takes the least time by a count of SM pairs' steps (512
-// cycles for a 256 x 256 tile 64 deep), with what the partial sums cost to
+// cycles for a 256 x 256 tile 64 deep; 300 for 128 x 128 on one SM), with what the partial sums cost to
 // write and to read at 3500 bytes a cycle.
 int ranges_of(int64_t M, int64_t N, int K) {
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), steps = (K + 63) / 64, pairs = kSms / 2;
+  const int64_t edge = M <= 128 ? 128 : 256, units = M <= 128 ? kSms : kSms / 2, step = M <= 128 ? 300 : 512;
+  const int64_t tiles = ((M + edge - 1) / edge) * ((N + edge - 1) / edge), steps = (K + 63) / 64;
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int64_t r = 1; r <= pairs && (r == 1 || (tiles < 4 * pairs && steps / r >= 4)); ++r) {
-    const int64_t cycles = (tiles * r + pairs - 1) / pairs * ((steps + r - 1) / r) * 512 + (r > 1 ? 4000 + r * M * N * 8 / 3500 : 0);
+  for (int64_t r = 1; r <= units && (r == 1 || (tiles < 4 * units && steps / r >= 4)); ++r) {
+    const int64_t cycles =
+        (tiles * r + units - 1) / units * ((steps + r - 1) / r) * step + (r > 1 ? 4000 + r * M * N * 8 / 3500 : 0);
     if (cycles < least) {
       least = cycles;
       best = (int)r;
@@ -403,7 +409,7 @@ cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int 
     using C = decltype(cfg);
     CUtensorMap ta, tb;
     const int ar = A_MN ? K : M, ac = A_MN ? M : K, br = B_MN ? K : N, bc = B_MN ? N : K;
-    if (!product_map(&ta, A, ar, ac, lda, lda, 1, a_box<C>(), false) ||
+    if (!product_map(&ta, A, ar, ac, lda, lda, 1, a_box<C>(M), false) ||
         !product_map(&tb, B, br, bc, ldb, ldb, 1, b_box<C>(), false))
       return cudaErrorUnknown;
     ProductShape s = product_shape<C>(M, N, K, 1);
@@ -414,7 +420,7 @@ cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int 
     }
     return launch_product<C, E>(ta, tb, s, args, st);
   };
-  if (ranges > 1 || wide(M, N)) return go(ProductCfg<256, true, A_MN, B_MN>());
+  if (wide(M, N, K) || (ranges > 1 && M > 128)) return go(ProductCfg<256, true, A_MN, B_MN>());
   return go(ProductCfg<128, false, A_MN, B_MN>());
 }
 
@@ -468,7 +474,7 @@ int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   a.scale = scale;
   cudaError_t e = product<false, false, StatsEpi>(X, ldx, W, ldw, T, V, h, a, st);
   if (e != cudaSuccess) return kLaunchFailed;
-  const int parts = 2 * (wide(T, V) ? (V + 255) / 256 : (V + 127) / 128);
+  const int parts = 2 * (wide(T, V, h) ? (V + 255) / 256 : (V + 127) / 128);
   e = mt_host::launch_early(join_rows_kernel, (T + 7) / 8, 256, 0, st, 1, (const float2*)a.part, (const float*)a.sums,
                             (const float*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
   count_launches(1);

@@ -650,7 +650,7 @@ cudaError_t product(const Operand& A, const Operand& B, int M, int N, int K, int
     using C = decltype(cfg);
     constexpr int S = decltype(split)::value;
     CUtensorMap ta, tb;
-    if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(), true) ||
+    if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(M), true) ||
         !product_map(&tb, B.p, B.rows, B.cols, B.ld, B.ld * B.rows, batch, b_box<C>(), true))
       return cudaErrorUnknown;
     const ProductShape s = product_shape<C>(M, N, K, batch);

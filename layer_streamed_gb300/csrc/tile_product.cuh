@@ -38,6 +38,7 @@ struct ProductShape {
   int batch;     // matrices, one after another (the tensor maps' third axis)
   int num_m, num_n, tiles;  // of one matrix; set by product_shape
   int group_m;   // row blocks that share a sweep over the columns
+  int a_rows;    // rows of A that a CTA loads: 128, or fewer where M is (single SMs, K contiguous)
   int split_kb;  // not 0: one matrix, `batch` counts ranges of split_kb 64-deep steps of its K
 };
 
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
   if (warp == 0) {
     if (lane == 0) {  // TMA producer
       const uint32_t full0 = PAIR ? mapa_shared(full, 0) : 0;
+      const uint32_t stage_bytes = PAIR ? 2 * C::STAGE_BYTES : s.a_rows * (BK * 2) + C::B_BYTES;
       int stage = 0;
       uint32_t phase = 0;
       for (int tile = first; tile < all; tile += step) {
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
         const int k0 = first_of(b), num_kb = steps_of(b), z = s.split_kb ? 0 : b;
         for (int kb = k0; kb < k0 + num_kb; ++kb) {
           mbar_wait<PAIR>(&empty[stage], phase ^ 1, abort_flag, kErrTimeoutTma);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], stage_bytes);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
             if (PAIR) tma_load_3d_pair(dst, map, full0 + stage * 8, x, y, z);
             else tma_load_3d(dst, map, &full[stage], x, y, z);
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(192, 2)
       for (int kb = k0; kb < k1; ++kb) {
         const int stage = (kb - k0) % STAGES;
         mbar_wait(&empty[stage], (((kb - k0) / STAGES) & 1) ^ 1, abort_flag, kErrTimeoutTma);
-        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        mbar_arrive_expect_tx(&full[stage], s.a_rows * (BK * 2) + C::B_BYTES);
         uint8_t* a_dst = sA + stage * C::A_BYTES;
         uint8_t* b_dst = sB + stage * C::B_BYTES;
         if (!C::A_MN) {
@@ -581,9 +583,13 @@ inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, in
                                box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ==
          CUDA_SUCCESS;
 }
-// Box heights of an operand: the tile's rows where K is contiguous, K steps else.
+// Box heights of an operand: the tile's rows where K is contiguous, K steps
+// else. Fewer rows of A than a tile has are loaded alone: what lies behind
+// them in the ring is never zeroed and makes rows of D that nobody reads.
+// (Boxes that TMA has to fill with zeros cost time: 128256 x 4096 times 7
+// rows took 248 us, times 64 rows 181.)
 template <class C>
-constexpr int a_box() { return C::A_MN ? 64 : C::BM; }
+int a_box(int M) { return C::A_MN ? 64 : C::PAIR ? C::BM : std::min(C::BM, (M + 7) / 8 * 8); }
 template <class C>
 constexpr int b_box() { return C::B_MN ? 64 : C::B_ROWS; }
 
@@ -594,6 +600,7 @@ ProductShape product_shape(int M, int N, int K, int batch) {
   s.N = N;
   s.K = K;
   s.batch = batch;
+  s.a_rows = C::PAIR || C::A_MN ? C::BM : a_box<C>(M);
   s.split_kb = 0;
   s.num_m = (M + C::TM - 1) / C::TM;
   s.num_n = (N + C::BN - 1) / C::BN;
