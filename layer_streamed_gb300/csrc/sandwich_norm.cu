@@ -74,8 +74,11 @@ __device__ __forceinline__ float block_sum(float v, float* red, int nw) {
 }
 
 // One block a row, the row in registers: V groups of four values a thread.
+// 8192 x 4096, bf16 y and gate (floor 70.3 us): V = 2 70.1 us, V = 1 89.7,
+// V = 4 81.2. Wider rows take V = 4, with a bf16 gate three blocks an
+// SM (4095 x 5636: 53.7 us, 58.7 with two; without a gate 51.5 against 49.7).
 template <bool BF16, bool GATE, int V>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && GATE && BF16 ? 3 : 1)
     sandwich_fwd_kernel(const float* x, const void* y, const void* gate, const float* w_post, const float* w_pre,
                         float alpha, float eps, float* x_out, uint16_t* n_out, float* rstd_post, float* rstd_pre,
                         int h) {
@@ -144,6 +147,13 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
 // x', dn and dres stages - 1 rows ahead as bulk copies into shared memory;
 // y and s, whose rows need not be whole 16-byte pieces, are loaded one row
 // ahead. A row has two sums, one after the other.
+// A thread has V groups of four columns. One up to 4096 columns (8192 x 4096,
+// bf16 and gate, floor 120.5 us: 129). Up to 6144 two with up to 768 threads,
+// three with up to 512 where there is a gate: more threads leave too few
+// registers (4095 x 5636 fp32 without a gate, floor 82.9: 109 us spilling at
+// the bound of 1024 threads, 87 at 768; bf16 with a gate 127, 102 and, with
+// three, 92). Up to 8192 two, spilling 16 to 224 bytes (2000 x 8192 with a
+// gate, floor 58.8: 83 us; four with 512 threads 88).
 // ---------------------------------------------------------------------------
 constexpr int kMaxThreads = 1024, kMaxStages = 8;
 constexpr int kMaxSms = 152;  // sizes the workspace, whatever machine asks
@@ -152,12 +162,12 @@ struct BwdShape {
   int threads, vecs, stages, an_sm;
   int parts(int T, int sms) const { return std::min(T, sms * an_sm); }
 };
-BwdShape bwd_shape(int h) {
+BwdShape bwd_shape(int h, bool gate) {
   BwdShape s;
   const int n4 = h / 4;
-  s.vecs = h > 4096 ? 2 : 1;
+  s.vecs = h <= 4096 ? 1 : h <= 6144 && gate ? 3 : 2;
   s.threads = std::max(32, (n4 + s.vecs * 32 - 1) / (s.vecs * 32) * 32);
-  s.an_sm = std::min(8, 1024 / s.threads);
+  s.an_sm = h > 4096 ? 1 : std::min(8, 1024 / s.threads);
   s.stages = std::min(kMaxStages, 222 * 1024 / s.an_sm / (12 * h));
   return s;
 }
@@ -169,8 +179,8 @@ __device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t by
                : "memory");
 }
 
-template <bool BF16, bool GATE, int V>
-__global__ void __launch_bounds__(kMaxThreads)
+template <bool BF16, bool GATE, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     sandwich_bwd_kernel(const float* x_out, const void* y, const void* gate, const float* w_post, const float* w_pre,
                         float alpha, const float* rstd_post, const float* rstd_pre, const float* dn, const float* dres,
                         float* dx, void* dy, void* dgate, float* part, int T, int h, int stages) {
@@ -350,7 +360,7 @@ bool sandwich_norm_dims(int T, int h) {
   // a block's row counter goes up to stages rounds of the grid past T
   return T > 0 && T <= (1 << 30) && h > 0 && h % 4 == 0 && h <= 8192;
 }
-size_t sandwich_norm_bwd_partials(int T, int h) { return (size_t)bwd_shape(h).parts(T, kMaxSms) * 2 * h; }
+size_t sandwich_norm_bwd_partials(int T, int h) { return (size_t)bwd_shape(h, false).parts(T, kMaxSms) * 2 * h; }
 
 int sandwich_norm_fwd(const float* x, const void* y, const void* gate, bool bf16, const float* w_post,
                       const float* w_pre, float alpha, float eps, float* x_out, uint16_t* n_out, float* rstd_post,
@@ -368,9 +378,10 @@ int sandwich_norm_fwd(const float* x, const void* y, const void* gate, bool bf16
   };
   auto pick = [&](auto b, auto g) {
     constexpr bool B = decltype(b)::value, G = decltype(g)::value;
-    // one group a thread is the shortest way through few rows; four keep more of
+    // one group a thread is the shortest way through few rows; more keep more of
     // many rows in flight
     if (n4 <= 1024 && T <= kMaxSms * 2) go(sandwich_fwd_kernel<B, G, 1>, 1);
+    else if (n4 <= 1024) go(sandwich_fwd_kernel<B, G, 2>, 2);
     else go(sandwich_fwd_kernel<B, G, 4>, 4);
   };
   auto pick_g = [&](auto b) { gate ? pick(b, std::true_type()) : pick(b, std::false_type()); };
@@ -387,7 +398,7 @@ int sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, bool 
   if (!sandwich_norm_dims(T, h) || !al(x_out, 16) || !al(y, ya) || !al(gate, ya) || !al(w_post, 16) ||
       !al(w_pre, 16) || !al(dn, 16) || !al(dres, 16) || !al(dx, 16) || !al(dy, ya) || !al(dgate, ya) || !al(work, 16))
     return kRefused;
-  BwdShape shape = bwd_shape(h);
+  BwdShape shape = bwd_shape(h, gate != nullptr);
   const int parts = shape.parts(T, std::min(mt_host::num_sms(), kMaxSms));
   shape.stages = std::min(shape.stages, (T + parts - 1) / parts + 1);  // no more than there are rows for
   cudaError_t e = cudaSuccess;
@@ -401,8 +412,10 @@ int sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, bool 
   };
   auto pick = [&](auto b, auto g) {
     constexpr bool B = decltype(b)::value, G = decltype(g)::value;
-    if (shape.vecs == 1) go(sandwich_bwd_kernel<B, G, 1>);
-    else go(sandwich_bwd_kernel<B, G, 2>);
+    if (shape.vecs == 1) go(sandwich_bwd_kernel<B, G, 1, 1024>);
+    else if (h > 6144) go(sandwich_bwd_kernel<B, G, 2, 1024>);
+    else if constexpr (G) go(sandwich_bwd_kernel<B, G, 3, 512>);
+    else go(sandwich_bwd_kernel<B, G, 2, 768>);
   };
   auto pick_g = [&](auto b) { gate ? pick(b, std::true_type()) : pick(b, std::false_type()); };
   bf16 ? pick_g(std::true_type()) : pick_g(std::false_type());
