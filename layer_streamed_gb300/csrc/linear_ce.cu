@@ -50,9 +50,39 @@ struct StatsEpi : NoSlabs {
     const int32_t* labels;
     float2* part;  // [M][2 num_n]
     float* sums;   // [M][2 num_n] or null
-    float* zlab;   // [M]
+    float2* zlab;  // [M]: the label's logit as the product has it, and as begin() does
     float scale;
+    const uint16_t *X, *W;
+    int64_t ldx, ldw;
+    int T, V, h;
   };
+  // The label's logit again, in fp32 (a sum of h / 32 terms a lane, then a
+  // tree): the tensor core's long sums come out a few 2^-24 of their terms
+  // short, 1.6e-6 of the loss at h = 4096; the label's own term is most of what
+  // counts of that, in the loss and, where its probability is high, in the
+  // log-sum-exp. By the epilogue's warps, idle until the first tile is there.
+  static __device__ __forceinline__ void begin(const Args& a, int warp) {
+    const int lane = (int)lane_id(), n8 = a.h >> 3;
+    for (int t = (int)blockIdx.x * WARPS + warp; t < a.T; t += (int)gridDim.x * WARPS) {
+      const int y = a.labels[t];
+      if (y < 0 || y >= a.V) continue;
+      const uint4* x = (const uint4*)(a.X + t * a.ldx);
+      const uint4* w = (const uint4*)(a.W + y * a.ldw);
+      float z0 = 0.f, z1 = 0.f;
+#pragma unroll 4
+      for (int i = lane; i < n8; i += 32) {
+        const uint4 p = x[i], q = w[i];
+        const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z0 = fmaf(bf2f(ps[e] & 0xffff), bf2f(qs[e] & 0xffff), z0);
+          z1 = fmaf(bf2f(ps[e] >> 16), bf2f(qs[e] >> 16), z1);
+        }
+      }
+      const float z = warp_sum(z0 + z1);
+      if (lane == 0) a.zlab[t].y = z * a.scale;
+    }
+  }
   struct Row {
     int label;
   };
@@ -81,7 +111,7 @@ struct StatsEpi : NoSlabs {
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) z = here == c * 32 + i ? v[i] : z;
-        a.zlab[at.row] = z * a.scale;
+        a.zlab[at.row].x = z * a.scale;
       }
       if (at.n0 + c * 32 + 32 > s.N) {
 #pragma unroll
@@ -109,7 +139,7 @@ struct StatsEpi : NoSlabs {
 
 // One warp a row: the tiles' pairs joined, the loss.
 __global__ void __launch_bounds__(256)
-    join_rows_kernel(const float2* part, const float* sums, const float* zlab, const int32_t* labels, int T, int V,
+    join_rows_kernel(const float2* part, const float* sums, const float2* zlab, const int32_t* labels, int T, int V,
                      int parts, float scale, float smooth, float zc, float* loss, float* lse_out) {
   grid_wait();
   grid_release();
@@ -137,8 +167,11 @@ __global__ void __launch_bounds__(256)
   s = warp_sum(s * ex2(m - ref));
   if (sums) plain = warp_sum(plain);
   if (lane == 0) {
+    // the label's term in the sum, then the label's logit, by its better value
+    const float2 z = zlab[row];
+    s += ex2(z.y * kLog2e - ref) - ex2(z.x * kLog2e - ref);
     const float lse = fmaf(top, kLn2, logf(s));
-    float l = lse - (1.f - smooth) * zlab[row];
+    float l = lse - (1.f - smooth) * z.y;
     if (sums) l -= smooth * (plain * scale / (float)V);
     loss[row] = l + zc * lse * lse;
     lse_out[row] = lse;
@@ -459,24 +492,31 @@ bool linear_ce_dims(int T, int V, int h) {
 
 size_t linear_ce_fwd_workspace(int T, int V) {
   const size_t n = (size_t)T * (2 * ((V + 127) / 128));
-  return up(n * 8, 256) + up(n * 4, 256) + up((size_t)T * 4, 256);
+  return up(n * 8, 256) + up(n * 4, 256) + up((size_t)T * 8, 256);
 }
 size_t linear_ce_bwd_workspace(int T, int V, int h) { return bwd_ws(T, V, h).total; }
 
 int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, float scale, float smooth, float zc,
                   float* loss, float* lse, void* work, int T, int V, int h, int ldx, int ldw, cudaStream_t st) {
   const size_t n = (size_t)T * (2 * ((V + 127) / 128));
-  StatsEpi::Args a;
+  StatsEpi::Args a{};
   a.labels = labels;
   a.part = (float2*)work;
   a.sums = smooth != 0.f ? (float*)((uint8_t*)work + up(n * 8, 256)) : nullptr;
-  a.zlab = (float*)((uint8_t*)work + up(n * 8, 256) + up(n * 4, 256));
+  a.zlab = (float2*)((uint8_t*)work + up(n * 8, 256) + up(n * 4, 256));
   a.scale = scale;
+  a.X = X;
+  a.W = W;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.T = T;
+  a.V = V;
+  a.h = h;
   cudaError_t e = product<false, false, StatsEpi>(X, ldx, W, ldw, T, V, h, a, st);
   if (e != cudaSuccess) return kLaunchFailed;
   const int parts = 2 * (wide(T, V, h) ? (V + 255) / 256 : (V + 127) / 128);
   e = mt_host::launch_early(join_rows_kernel, (T + 7) / 8, 256, 0, st, 1, (const float2*)a.part, (const float*)a.sums,
-                            (const float*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
+                            (const float2*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
   count_launches(1);
   return e == cudaSuccess ? 0 : kLaunchFailed;
 }
