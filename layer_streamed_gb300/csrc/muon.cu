@@ -595,6 +595,365 @@ struct ApplyEpi {
 };
 
 // ---------------------------------------------------------------------------
+// Matrices with a side of at most 128: everything in one launch. A cluster of
+// S CTAs takes a matrix, each up to 256 of the long side's values (tall ones
+// are taken transposed). X lives in tensor memory in fp32 (256 columns of 128
+// lanes) and its fp16 copy in shared memory as blocks of 64 columns by 128
+// rows of 128 bytes, which one matrix descriptor reads as X (K along the
+// columns: the Gram product) and another one as X transposed (B X). A step is
+// three rounds of MMAs with their epilogues by all eight warps, and between
+// the first and the second the sum of the CTAs' parts of A: each CTA adds up
+// 128 / S columns of it, from the others' shared memory, and sends them all
+// that share of A's rest in fp16 and of its diagonal. Latency is all that
+// counts here: 64 x 64 took 72 us as a chain of seventeen launches.
+// ---------------------------------------------------------------------------
+struct NarrowArgs {
+  const void* G;
+  float* M;  // null: none
+  void* out;
+  int g_bf16, nesterov, out_bf16, update, steps, tall;
+  int m, n, cols;  // short and long side; columns as stored
+  float mu, keep, step, eps;
+  float coef[96];
+};
+constexpr int kXBlock = 128 * 128;  // bytes of 64 columns of X, of 64 columns of a square matrix
+constexpr int kNarrowCols = 256;    // columns of X in a CTA
+constexpr int kNarrowSmem = 4 * kXBlock + 2 * kXBlock + 65536 + 1024 /*align*/;
+
+// 16-byte piece k (8 columns) of a row of such blocks.
+__device__ __forceinline__ uint4* block_piece(uint8_t* blocks, int row, int k) {
+  return slab_piece(blocks + (k >> 3) * kXBlock, row, k & 7);
+}
+
+// 32 values of this lane's row to tensor memory.
+__device__ __forceinline__ void put_chunk(uint32_t t, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  __syncwarp();
+  tmem_st32(t, r);
+}
+
+template <int S>
+__global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* xh = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // 4 blocks of X
+  uint8_t* sq = xh + 4 * kXBlock;                                             // 2 blocks of O, then of B
+  uint8_t* ex = sq + 2 * kXBlock;                                             // the others' parts: [S][128 / S / 4][128] float4
+  __shared__ float dg[128], dbs[128], norms[8], red[8];
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, half = warp >> 2;
+  const int row = q * 32 + lane;
+  const int rank = S > 1 ? (int)cluster_rank() : 0;
+  const size_t mat = (size_t)(blockIdx.x / S) * p.m * p.n;
+  if (tid == 0) {
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
+  tc_fence_after();
+  const uint32_t tx = tmem_slot + ((uint32_t)(q * 32) << 16);  // X: columns 0 .. 255; sums: 256 ..
+  const uint32_t td = tx + 256;
+  grid_wait();
+  grid_release();
+
+  const int j0 = rank * kNarrowCols;
+  const int mine = max(0, min(kNarrowCols, p.n - j0));  // columns of this CTA
+  const int blocks = (mine + 63) / 64;
+  // where X[row][j] lies, and whether four neighbours can be read at once
+  const bool vec = !p.tall && p.cols % 4 == 0 && ((uintptr_t)p.G & (p.g_bf16 ? 7 : 15)) == 0 && ((uintptr_t)p.M & 15) == 0;
+  const bool vec_out = !p.tall && p.cols % 4 == 0 && ((uintptr_t)p.out & (p.out_bf16 ? 7 : 15)) == 0;
+  auto at = [&](int j) { return mat + (p.tall ? (size_t)j * p.cols + row : (size_t)row * p.cols + j); };
+
+  // U into tensor memory, the sum of its squares
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int col = half * 128 + c * 32;
+    float u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = 0.f;
+    if (row < p.m && col < mine) {
+      float m[32];
+      if (vec && col + 32 <= mine) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          load4(p.G, at(j0 + col + i), p.g_bf16, *(float(*)[4])(u + i));
+          if (p.M) load4(p.M, at(j0 + col + i), false, *(float(*)[4])(m + i));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const bool in = col + i < mine;
+          u[i] = in ? load1(p.G, at(j0 + col + i), p.g_bf16) : 0.f;
+          m[i] = in && p.M ? p.M[at(j0 + col + i)] : 0.f;
+        }
+      }
+      if (p.M) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          m[i] = fmaf(p.mu, m[i], u[i]);
+          u[i] = p.nesterov ? fmaf(p.mu, m[i], u[i]) : m[i];
+        }
+        if (vec && col + 32 <= mine) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *(float4*)(p.M + at(j0 + col + i)) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i < mine) p.M[at(j0 + col + i)] = m[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum = fmaf(u[i], u[i], sum);
+    }
+    put_chunk(tx + col, u);
+  }
+  tmem_st_wait();
+  sum = warp_sum(sum);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (tid < S) {
+    float s = 0.f;
+    for (int i = 0; i < 8; ++i) s += red[i];
+    if (S > 1) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(&norms[rank], (uint32_t)tid)), "f"(s) : "memory");
+    } else {
+      norms[0] = s;
+    }
+  }
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int r = 0; r < S; ++r) sum += norms[r];
+  const float norm = sqrtf(sum) + p.eps;
+  const float inv = norm < INFINITY ? (norm > 0.f ? kXUp / norm : 0.f) : __uint_as_float(0x7fffffffu);
+
+  // X (times kXUp) to tensor memory, its fp16 copy to the blocks
+  auto keep_x = [&](int col, float (&x)[32]) {
+    put_chunk(tx + col, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *block_piece(xh, row, col / 8 + i) = make_uint4(pack_h2(x[8 * i], x[8 * i + 1]), pack_h2(x[8 * i + 2], x[8 * i + 3]),
+                                                      pack_h2(x[8 * i + 4], x[8 * i + 5]), pack_h2(x[8 * i + 6], x[8 * i + 7]));
+  };
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float x[32];
+    tile_chunk(tx, half * 4 + c, x);
+    // padding stays zero where the norm is not a number
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = row < p.m && half * 128 + c * 32 + i < mine ? x[i] * inv : 0.f;
+    keep_x(half * 128 + c * 32, x);
+  }
+  tmem_st_wait();
+
+  constexpr uint32_t kSquare = make_idesc(128, 128, false, false) & ~((1u << 7) | (1u << 10));
+  constexpr uint32_t kTimesX = make_idesc(128, 256, false, true) & ~((1u << 7) | (1u << 10));
+  uint32_t phase = 0;
+  auto sync = [&] {  // shared and tensor memory as the other warps have left them, for the MMAs
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  auto wait = [&] {
+    mbar_wait(&done, phase, &abort_flag, kErrTimeoutMma);
+    phase ^= 1;
+    tc_fence_after();
+  };
+
+#pragma unroll 1
+  for (int step = 0; step < p.steps; ++step) {
+    const float ca = p.coef[3 * step], cb = p.coef[3 * step + 1], cc = p.coef[3 * step + 2];
+    // A = X X^T, this CTA's columns
+    sync();
+    if (tid == 0) {
+      const uint32_t x = smem_u32(xh);
+      for (int k = 0; k < blocks * 4; ++k) {
+        const uint64_t d = make_sdesc(x + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024);
+        tc_mma(tmem_slot + 256, d, d, kSquare, k != 0);
+      }
+      tc_commit(&done);
+    }
+    __syncwarp();
+    wait();
+    if (S > 1) {
+      // 16 columns at a time to the CTA that adds them up: [source][4 columns][row]
+      constexpr int SHARE = 128 / S;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        float v[32];
+        tile_chunk(td, half * 2 + c, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = blocks ? v[i] : 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = half * 64 + c * 32 + h * 16;
+          const uint32_t to = mapa_shared(ex + ((rank * SHARE + col % SHARE) / 4) * 2048, (uint32_t)(col / SHARE)) + row * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + i * 2048), "f"(v[16 * h + 4 * i]),
+                         "f"(v[16 * h + 4 * i + 1]), "f"(v[16 * h + 4 * i + 2]), "f"(v[16 * h + 4 * i + 3])
+                         : "memory");
+        }
+      }
+      tc_fence_before();
+      cluster_sync();
+      // this CTA's share, half of it a warp: eight columns at a time to all
+#pragma unroll 1
+      for (int g = 0; g < SHARE / 16; ++g) {
+        const int in = (half * (SHARE / 16) + g) * 8, col = rank * SHARE + in;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+          const float4* e = (const float4*)(ex + ((r * SHARE + in) / 4) * 2048) + row;
+          const float4 a = e[0], b = e[128];
+          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d = col + i == row ? v[i] * (kXDown * kXDown) : d;
+          v[i] = col + i == row ? 0.f : v[i] * (kAUp * kXDown * kXDown);
+        }
+        const uint32_t w[4] = {pack_h2(v[0], v[1]), pack_h2(v[2], v[3]), pack_h2(v[4], v[5]), pack_h2(v[6], v[7])};
+        uint4* to = block_piece(sq, row, col / 8);
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mapa_shared(to, (uint32_t)r)), "r"(w[0]),
+                       "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+          if (col <= row && row < col + 8)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(&dg[row], (uint32_t)r)), "f"(d) : "memory");
+        }
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+      cluster_sync();
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        const int col = half * 64 + c * 32;
+        float v[32];
+        tile_chunk(td, half * 2 + c, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (col + i == row) dg[row] = v[i] * (kXDown * kXDown);
+          v[i] = col + i == row ? 0.f : v[i] * (kAUp * kXDown * kXDown);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *block_piece(sq, row, col / 8 + i) = make_uint4(pack_h2(v[8 * i], v[8 * i + 1]), pack_h2(v[8 * i + 2], v[8 * i + 3]),
+                                                          pack_h2(v[8 * i + 4], v[8 * i + 5]), pack_h2(v[8 * i + 6], v[8 * i + 7]));
+      }
+    }
+    // A^2's rest, then B in A's place
+    sync();
+    if (tid == 0) {
+      const uint32_t o = smem_u32(sq);
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t d = make_sdesc(o + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024);
+        tc_mma(tmem_slot + 256, d, d, kSquare, k != 0);
+      }
+      tc_commit(&done);
+    }
+    __syncwarp();
+    wait();
+    const float d = dg[row];
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      const int col = half * 64 + c * 32;
+      float v[32], o[32];
+      tile_chunk(td, half * 2 + c, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpack8h(*block_piece(sq, row, col / 8 + i), o + 8 * i);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (col + i == row) dbs[row] = d * cb + cc * fmaf(d, d, v[i] * (kADown * kADown));
+        v[i] = col + i == row ? 0.f : fmaf(cc, fmaf(d + dg[col + i], o[i], v[i] * kADown), cb * o[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *block_piece(sq, row, col / 8 + i) = make_uint4(pack_h2(v[8 * i], v[8 * i + 1]), pack_h2(v[8 * i + 2], v[8 * i + 3]),
+                                                        pack_h2(v[8 * i + 4], v[8 * i + 5]), pack_h2(v[8 * i + 6], v[8 * i + 7]));
+    }
+    // X <- a X + B X
+    sync();
+    if (tid == 0) {
+      const uint32_t b = smem_u32(sq), x = smem_u32(xh);
+      for (int k = 0; k < 8; ++k)
+        tc_mma(tmem_slot + 256, make_sdesc(b + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024),
+               make_sdesc(x + k * 2048, kXBlock, 1024), kTimesX, k != 0);
+      tc_commit(&done);
+    }
+    __syncwarp();
+    wait();
+    const float db = dbs[row], ah = ca + db, al_ = ca + 0.5f * db;
+    const bool last = step + 1 == p.steps;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const int col = half * 128 + c * 32;
+      float v[32], x[32];
+      tile_chunk(td, half * 4 + c, v);
+      tile_chunk(tx, half * 4 + c, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float h = h2f(f2h(x[i]));
+        x[i] = fmaf(ah, h, fmaf(al_, x[i] - h, v[i] * kADown));
+      }
+      if (!last) {
+        keep_x(col, x);
+      } else if (row < p.m && vec_out && col + 32 <= mine) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const size_t o = at(j0 + col + i);
+          float r[4] = {x[i] * kXDown, x[i + 1] * kXDown, x[i + 2] * kXDown, x[i + 3] * kXDown};
+          if (p.update) {
+            float w[4];
+            load4(p.out, o, p.out_bf16, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = fmaf(p.keep, w[e], -p.step * r[e]);
+          }
+          if (p.out_bf16) *(uint2*)((uint16_t*)p.out + o) = make_uint2(pack_bf2(r[0], r[1]), pack_bf2(r[2], r[3]));
+          else *(float4*)((float*)p.out + o) = make_float4(r[0], r[1], r[2], r[3]);
+        }
+      } else if (row < p.m) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (col + i >= mine) break;
+          const size_t o = at(j0 + col + i);
+          float r = x[i] * kXDown;
+          if (p.update) r = fmaf(p.keep, load1(p.out, o, p.out_bf16), -p.step * r);
+          if (p.out_bf16) ((uint16_t*)p.out)[o] = f2bf(r);
+          else ((float*)p.out)[o] = r;
+        }
+      }
+    }
+    if (!last) tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_slot, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -679,6 +1038,35 @@ size_t orthogonalize_workspace(int batch, int rows, int cols) { return workspace
 int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov, void* out, bool out_bf16, bool update,
                   float keep, float step, const float* coef, int steps, float eps, void* work, int batch, int rows,
                   int cols, cudaStream_t st) {
+  const int sides[2] = {std::min(rows, cols), std::max(rows, cols)};
+  if (sides[0] <= 128 && sides[1] <= 8 * kNarrowCols) {
+    NarrowArgs a{};
+    a.G = G;
+    a.M = M;
+    a.out = out;
+    a.g_bf16 = g_bf16;
+    a.nesterov = nesterov;
+    a.out_bf16 = out_bf16;
+    a.update = update;
+    a.steps = steps;
+    a.tall = rows > cols;
+    a.m = sides[0];
+    a.n = sides[1];
+    a.cols = cols;
+    a.mu = mu;
+    a.keep = keep;
+    a.step = step;
+    a.eps = eps;
+    std::copy(coef, coef + 3 * steps, a.coef);
+    auto go = [&](auto k, int ctas) {
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+      if (e == cudaSuccess) e = mt_host::launch_early(k, batch * ctas, 256, kNarrowSmem, st, ctas, a);
+      count_launches(1);
+      return e == cudaSuccess ? 0 : kLaunchFailed;
+    };
+    const int ctas = (sides[1] + kNarrowCols - 1) / kNarrowCols;
+    return ctas == 1 ? go(narrow_kernel<1>, 1) : ctas == 2 ? go(narrow_kernel<2>, 2) : ctas <= 4 ? go(narrow_kernel<4>, 4) : go(narrow_kernel<8>, 8);
+  }
   const Ws w = workspace(batch, rows, cols);
   uint8_t* base = (uint8_t*)work;
   float* part = (float*)(base + w.part);

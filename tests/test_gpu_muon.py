@@ -59,7 +59,8 @@ def _check(torch, got, G, steps=5, coef=None, eps=0.0):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 9), (1, 7, 1), (2, 2, 3), (1, 33, 40), (3, 64, 64), (1, 100, 37), (2, 129, 257),
-          (1, 300, 1000), (1, 777, 130), (5, 65, 520), (1, 1024, 1024), (2, 513, 2049), (1, 2600, 700)]
+          (1, 300, 1000), (1, 777, 130), (5, 65, 520), (1, 1024, 1024), (2, 513, 2049), (1, 2600, 700), (1, 128, 2048),
+          (1, 128, 2049), (2, 1500, 90), (40, 64, 256), (3, 20, 1100), (1, 2048, 127), (170, 30, 300), (1, 600, 128)]
 
 
 @pytest.mark.parametrize("kind", ["flat", "spikes", "low", "gradient"])
@@ -147,7 +148,7 @@ def test_values_off_any_boundary():
 
 @pytest.mark.parametrize("nesterov", [0, 1])
 @pytest.mark.parametrize("wb,gb", [(False, False), (True, False), (True, True), (False, True)])
-@pytest.mark.parametrize("b,rows,cols", [(1, 1, 5), (2, 129, 130), (1, 520, 264), (3, 40, 333)])
+@pytest.mark.parametrize("b,rows,cols", [(1, 1, 5), (2, 129, 130), (1, 520, 264), (3, 40, 333), (2, 700, 100), (3, 64, 1536)])
 def test_update(b, rows, cols, wb, gb, nesterov):
     torch, mt = need_gpu()
     bf, f4 = torch.bfloat16, torch.float32
