@@ -601,7 +601,7 @@ struct ApplyEpi {
 // lanes) and its fp16 copy in shared memory as blocks of 64 columns by 128
 // rows of 128 bytes, which one matrix descriptor reads as X (K along the
 // columns: the Gram product) and another one as X transposed (B X). A step is
-// three rounds of MMAs with their epilogues by all eight warps, and between
+// three rounds of MMAs with their epilogues by all sixteen warps, and between
 // the first and the second the sum of the CTAs' parts of A: each CTA adds up
 // 128 / S columns of it, from the others' shared memory, and sends them all
 // that share of A's rest in fp16 and of its diagonal. Latency is all that
@@ -635,17 +635,17 @@ __device__ __forceinline__ void put_chunk(uint32_t t, const float (&v)[32]) {
 }
 
 template <int S>
-__global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
+__global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* xh = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // 4 blocks of X
   uint8_t* sq = xh + 4 * kXBlock;                                             // 2 blocks of O, then of B
   uint8_t* ex = sq + 2 * kXBlock;                                             // the others' parts: [S][128 / S / 4][128] float4
-  __shared__ float dg[128], dbs[128], norms[8], red[8];
+  __shared__ float dg[128], dbs[128], norms[S], red[16];
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q = warp & 3, half = warp >> 2;
+  const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, quarter of the columns
   const int row = q * 32 + lane;
   const int rank = S > 1 ? (int)cluster_rank() : 0;
   const size_t mat = (size_t)(blockIdx.x / S) * p.m * p.n;
@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     abort_flag = 0;
     fence_barrier_init();
   }
+  if (tid < 128) dg[tid] = dbs[tid] = 0.f;
   if (warp == 0) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -678,8 +679,8 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
   // U into tensor memory, the sum of its squares
   float sum = 0.f;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = half * 128 + c * 32;
+  for (int c = 0; c < 2; ++c) {
+    const int col = part * 64 + c * 32;
     float u[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = 0.f;
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
   __syncthreads();
   if (tid < S) {
     float s = 0.f;
-    for (int i = 0; i < 8; ++i) s += red[i];
+    for (int i = 0; i < 16; ++i) s += red[i];
     if (S > 1) {
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(&norms[rank], (uint32_t)tid)), "f"(s) : "memory");
     } else {
@@ -750,18 +751,24 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
                                                       pack_h2(x[8 * i + 4], x[8 * i + 5]), pack_h2(x[8 * i + 6], x[8 * i + 7]));
   };
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
+    const int col = part * 64 + c * 32;
     float x[32];
-    tile_chunk(tx, half * 4 + c, x);
+    tile_chunk(tx, part * 2 + c, x);
     // padding stays zero where the norm is not a number
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = row < p.m && half * 128 + c * 32 + i < mine ? x[i] * inv : 0.f;
-    keep_x(half * 128 + c * 32, x);
+    for (int i = 0; i < 32; ++i) x[i] = row < p.m && col + i < mine ? x[i] * inv : 0.f;
+    keep_x(col, x);
   }
   tmem_st_wait();
 
   constexpr uint32_t kSquare = make_idesc(128, 128, false, false) & ~((1u << 7) | (1u << 10));
-  constexpr uint32_t kTimesX = make_idesc(128, 256, false, true) & ~((1u << 7) | (1u << 10));
+  const uint32_t times_x = make_idesc(128, blocks * 64, false, true) & ~((1u << 7) | (1u << 10));
+  // Rows from m on and this CTA's columns behind its own are zeros: sums along
+  // them end at the next whole 16, and chunks of 32 results that lie there
+  // altogether are left out.
+  const int deep = (p.m + 15) / 16;
+  const bool square = part * 32 < p.m;  // this warp has columns of the square matrices
   uint32_t phase = 0;
   auto sync = [&] {  // shared and tensor memory as the other warps have left them, for the MMAs
     fence_proxy_async_smem();
@@ -791,31 +798,30 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     __syncwarp();
     wait();
     if (S > 1) {
-      // 16 columns at a time to the CTA that adds them up: [source][4 columns][row]
+      // eight columns at a time to the CTA that adds them up: [source][4 columns][row]
       constexpr int SHARE = 128 / S;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
+      if (square) {
         float v[32];
-        tile_chunk(td, half * 2 + c, v);
+        tile_chunk(td, part, v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = blocks ? v[i] : 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = half * 64 + c * 32 + h * 16;
+        for (int i = 0; i < 32; i += 8) {
+          const int col = part * 32 + i;
           const uint32_t to = mapa_shared(ex + ((rank * SHARE + col % SHARE) / 4) * 2048, (uint32_t)(col / SHARE)) + row * 16;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + i * 2048), "f"(v[16 * h + 4 * i]),
-                         "f"(v[16 * h + 4 * i + 1]), "f"(v[16 * h + 4 * i + 2]), "f"(v[16 * h + 4 * i + 3])
+          for (int e = 0; e < 8; e += 4)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + e * 512),
+                         "f"(blocks ? v[i + e] : 0.f), "f"(blocks ? v[i + e + 1] : 0.f), "f"(blocks ? v[i + e + 2] : 0.f),
+                         "f"(blocks ? v[i + e + 3] : 0.f)
                          : "memory");
         }
       }
       tc_fence_before();
       cluster_sync();
-      // this CTA's share, half of it a warp: eight columns at a time to all
+      // this CTA's share: eight columns at a time to all
 #pragma unroll 1
-      for (int g = 0; g < SHARE / 16; ++g) {
-        const int in = (half * (SHARE / 16) + g) * 8, col = rank * SHARE + in;
+      for (int in = part * 8; in < SHARE; in += 32) {
+        const int col = rank * SHARE + in;
+        if (col / 32 * 32 >= p.m) break;
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -845,11 +851,10 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
       asm volatile("fence.proxy.async;" ::: "memory");
       cluster_sync();
     } else {
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        const int col = half * 64 + c * 32;
+      if (square) {
+        const int col = part * 32;
         float v[32];
-        tile_chunk(td, half * 2 + c, v);
+        tile_chunk(td, part, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           if (col + i == row) dg[row] = v[i] * (kXDown * kXDown);
@@ -865,7 +870,7 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     sync();
     if (tid == 0) {
       const uint32_t o = smem_u32(sq);
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < deep; ++k) {
         const uint64_t d = make_sdesc(o + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024);
         tc_mma(tmem_slot + 256, d, d, kSquare, k != 0);
       }
@@ -874,11 +879,10 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     __syncwarp();
     wait();
     const float d = dg[row];
-#pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      const int col = half * 64 + c * 32;
+    if (square) {
+      const int col = part * 32;
       float v[32], o[32];
-      tile_chunk(td, half * 2 + c, v);
+      tile_chunk(td, part, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpack8h(*block_piece(sq, row, col / 8 + i), o + 8 * i);
 #pragma unroll
@@ -895,9 +899,9 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     sync();
     if (tid == 0) {
       const uint32_t b = smem_u32(sq), x = smem_u32(xh);
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < deep && blocks; ++k)
         tc_mma(tmem_slot + 256, make_sdesc(b + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024),
-               make_sdesc(x + k * 2048, kXBlock, 1024), kTimesX, k != 0);
+               make_sdesc(x + k * 2048, kXBlock, 1024), times_x, k != 0);
       tc_commit(&done);
     }
     __syncwarp();
@@ -905,11 +909,12 @@ __global__ void __launch_bounds__(256, 1) narrow_kernel(const __grid_constant__ 
     const float db = dbs[row], ah = ca + db, al_ = ca + 0.5f * db;
     const bool last = step + 1 == p.steps;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      const int col = half * 128 + c * 32;
+    for (int c = 0; c < 2; ++c) {
+      const int col = part * 64 + c * 32;
+      if (col >= mine) break;
       float v[32], x[32];
-      tile_chunk(td, half * 4 + c, v);
-      tile_chunk(tx, half * 4 + c, x);
+      tile_chunk(td, part * 2 + c, v);
+      tile_chunk(tx, part * 2 + c, x);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float h = h2f(f2h(x[i]));
@@ -994,9 +999,13 @@ Ws workspace(int batch, int rows, int cols) {
   return w;
 }
 
-// D = A B^T of fp16 matrices in a batch. Few tiles: 128 x 128, each shared by
-// four or two CTAs where that still leaves every CTA an SM; else 256 x 256 on
-// SM pairs where they fill half of the pairs, 128 x 128 on single SMs.
+// D = A B^T of fp16 matrices in a batch. Few tiles of 128 x 128: each shared by
+// four CTAs where that leaves every CTA an SM (1024 x 1024: 152 us a call of
+// five steps without, 138 so), by two where the sum is deep or, a little less
+// deep, the result not symmetric (two CTAs for all: 2 x 1024 x 1024 172 us,
+// 160 so; none: 1024 x 1024 153). One SM a tile up to as many as there are SMs
+// (4 x 1024 x 1024: 235 us on pairs, 192 so), then 256 x 256 on SM pairs where
+// they fill half of the pairs.
 struct Operand {
   const void* p;
   int rows, cols;
@@ -1022,9 +1031,19 @@ cudaError_t product(const Operand& A, const Operand& B, int M, int N, int K, int
   const int64_t wide = (int64_t)product_shape<Wide>(M, N, K, batch).tiles * batch;
   const int64_t small = (int64_t)product_shape<Small>(M, N, K, batch).tiles * batch;
   if (4 * small <= sms) return go(Small(), std::integral_constant<int, 4>());
-  if (2 * small <= sms) return go(Small(), std::integral_constant<int, 2>());
-  if (wide >= sms / 4) return go(Wide(), std::integral_constant<int, 1>());
+  if (2 * small <= sms && K >= (SYM ? 2048 : 1024)) return go(Small(), std::integral_constant<int, 2>());
+  if (small > sms && wide >= sms / 4) return go(Wide(), std::integral_constant<int, 1>());
   return go(Small(), std::integral_constant<int, 1>());
+}
+
+template <int S>
+int launch_narrow(const NarrowArgs& a, int batch, cudaStream_t st) {
+  auto k = narrow_kernel<S>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+  if (S > 8 && e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = mt_host::launch_early(k, batch * S, 512, kNarrowSmem, st, S, a);
+  count_launches(1);
+  return e == cudaSuccess ? 0 : kLaunchFailed;
 }
 
 }  // namespace
@@ -1039,7 +1058,7 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
                   float keep, float step, const float* coef, int steps, float eps, void* work, int batch, int rows,
                   int cols, cudaStream_t st) {
   const int sides[2] = {std::min(rows, cols), std::max(rows, cols)};
-  if (sides[0] <= 128 && sides[1] <= 8 * kNarrowCols) {
+  if (sides[0] <= 128 && sides[1] <= 16 * kNarrowCols) {
     NarrowArgs a{};
     a.G = G;
     a.M = M;
@@ -1058,14 +1077,12 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
     a.step = step;
     a.eps = eps;
     std::copy(coef, coef + 3 * steps, a.coef);
-    auto go = [&](auto k, int ctas) {
-      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
-      if (e == cudaSuccess) e = mt_host::launch_early(k, batch * ctas, 256, kNarrowSmem, st, ctas, a);
-      count_launches(1);
-      return e == cudaSuccess ? 0 : kLaunchFailed;
-    };
     const int ctas = (sides[1] + kNarrowCols - 1) / kNarrowCols;
-    return ctas == 1 ? go(narrow_kernel<1>, 1) : ctas == 2 ? go(narrow_kernel<2>, 2) : ctas <= 4 ? go(narrow_kernel<4>, 4) : go(narrow_kernel<8>, 8);
+    return ctas == 1   ? launch_narrow<1>(a, batch, st)
+           : ctas == 2 ? launch_narrow<2>(a, batch, st)
+           : ctas <= 4 ? launch_narrow<4>(a, batch, st)
+           : ctas <= 8 ? launch_narrow<8>(a, batch, st)
+                       : launch_narrow<16>(a, batch, st);
   }
   const Ws w = workspace(batch, rows, cols);
   uint8_t* base = (uint8_t*)work;

@@ -60,7 +60,7 @@ def _check(torch, got, G, steps=5, coef=None, eps=0.0):
 
 SHAPES = [(1, 1, 1), (1, 1, 9), (1, 7, 1), (2, 2, 3), (1, 33, 40), (3, 64, 64), (1, 100, 37), (2, 129, 257),
           (1, 300, 1000), (1, 777, 130), (5, 65, 520), (1, 1024, 1024), (2, 513, 2049), (1, 2600, 700), (1, 128, 2048),
-          (1, 128, 2049), (2, 1500, 90), (40, 64, 256), (3, 20, 1100), (1, 2048, 127), (170, 30, 300), (1, 600, 128)]
+          (1, 128, 2049), (2, 1500, 90), (40, 64, 256), (3, 20, 1100), (1, 2048, 127), (170, 30, 300), (1, 600, 128), (1, 100, 4096), (2, 3001, 64), (1, 2300, 128), (30, 16, 2500), (1, 60, 4097)]
 
 
 @pytest.mark.parametrize("kind", ["flat", "spikes", "low", "gradient"])
