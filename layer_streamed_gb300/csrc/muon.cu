@@ -964,9 +964,9 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Blocks that share the sum of a matrix's squares: one per 8192 values, as
+// Blocks that share the sum of a matrix's squares: one per 2048 values, as
 // many as eight on every SM.
-int norm_parts(int64_t n) { return (int)std::min<int64_t>((n + 8191) / 8192, 152 * 8); }
+int norm_parts(int64_t n) { return (int)std::min<int64_t>((n + 2047) / 2048, 152 * 8); }
 
 struct Ws {
   size_t part, hi[2], lo, o, b, d, db, total;
