@@ -182,6 +182,22 @@ def test_label_past_the_vocabulary():
     _check(torch, r, f)
 
 
+def test_a_bad_label_does_not_reach_the_calls_after_it():
+    """Its bit waits in the device error word; later calls, with waits of many microseconds, run as ever."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _case(torch, 300, 9000, 8192, 61)
+    bf = torch.bfloat16
+    clean = _run(torch, mt, X, W, labels, gl, 1.0, 0.1, 1e-3, bf, bf)
+    assert mt.mt_op_device_error() == 0
+    bad = labels.clone()
+    bad[0] = 9000
+    _run(torch, mt, X, W, bad, gl, 1.0, 0.1, 1e-3)
+    after = _run(torch, mt, X, W, labels, gl, 1.0, 0.1, 1e-3, bf, bf)
+    for k in ("loss", "lse", "dX", "dW"):
+        assert torch.equal(getattr(clean, k), getattr(after, k)), k
+    assert mt.mt_op_device_error() != 0 and mt.mt_op_device_error() == 0
+
+
 @pytest.mark.parametrize("which", ["dX", "dW"])
 def test_one_gradient_alone_is_the_same(which):
     torch, mt = need_gpu()
