@@ -651,11 +651,12 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
  * O [batch, rows, cols] (MT_F32 or MT_BF16) receives X: singular vectors kept,
  * singular values taken through the polynomial (with the quintic, five steps:
  * from 1e-2 of the norm up to between 0.7 and 1.2). Products are made of fp16
- * operands with fp32 sums, with X carried in 22 bits: O is within about 1e-3
- * (relative, Frobenius) of exact arithmetic for the quintic's 5 or 6 steps
- * before its own rounding. A zero matrix gives zeros, one with an infinity or
- * a NaN (or whose squares' sum passes fp32) NaN throughout; the others of the
- * batch are not touched by it. Singular values have to stay below 15 in every
+ * operands with fp32 sums, with X carried in 22 bits: O is 0.4e-3 to 1.1e-3
+ * (relative, Frobenius; up to 2e-3 for matrices of low rank) from exact
+ * arithmetic for the quintic's 5 or 6 steps before its own rounding. A zero
+ * matrix (or one whose squares' sum is 0 in fp32) gives zeros, one with an
+ * infinity or a NaN (or whose squares' sum passes fp32) NaN throughout; the
+ * others of the batch are not touched by it. Singular values have to stay below 15 in every
  * step (fp16's range). Any rows and cols up to 2^16, batch up to 4096, steps
  * 1 to 32, |coef| up to 100, eps >= 0. workspace: bytes, 256-byte aligned (0
  * for sizes that are refused). O may be G where the types are the same.
@@ -682,7 +683,8 @@ int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype
  *   x_out = alpha x + sigmoid(gate) * (w_post * y * rstd_post),  rstd_post = 1/sqrt(mean(y^2) + eps)
  *   n_out = bf16(w_pre * x_out * rstd_pre),                      rstd_pre = 1/sqrt(mean(x_out^2) + eps)
  * x_out fp32 [T, h] (may be x), n_out bf16 [T, h], rstd_post, rstd_pre fp32 [T],
- * w_post, w_pre fp32 [h]. h a multiple of 4 up to 8192, T up to 2^30, eps >= 0.
+ * w_post, w_pre fp32 [h]. h a multiple of 4 up to 8192, T up to 2^30, eps >= 0
+ * (with 0, rows of zeros are NaN).
  * fp32 arrays 16-byte aligned (rstd and the weights' gradients 4), bf16 ones 8. */
 int mt_op_sandwich_norm_fwd(const float* x, const void* y, const void* gate, int y_dtype, const float* w_post,
                             const float* w_pre, float alpha, float eps, float* x_out, void* n_out, float* rstd_post,

@@ -17,20 +17,26 @@
 //    multiplied; a X is formed from both. Directions in which X is small grow
 //    by a factor a a step (3.44^5 = 485): with hi alone their rounding would
 //    grow with them, and it is what momentum of low rank ends in (4e-2 of the
-//    result in a float64 model of these roundings, 1e-3 with both).
+//    result in a float64 model of these roundings, 0.8e-3 to 2.1e-3 with both).
 //  - A's and B = b A + c A^2's diagonals stay fp32, beside matrices whose
 //    diagonal is zero: with D the diagonal and O the rest, A^2 = O^2 + (d_i +
 //    d_j) O + D^2, and B X = (B's rest) X + d X. Diagonals are near to each
 //    other and to 1, so their rounding errors would all point the same way
-//    (2.7e-3 of the result in that model, 0.8e-3 so). lo gets half of d: all
-//    of it where X is flat, none where B takes lo's direction to zero.
-// Together 0.2e-3 to 1.4e-3 of the result against exact arithmetic (bf16
-// products: 1e-2 to 3e-2, and 3e-1 at low rank), below what rounding the
-// result to bf16 costs (1.7e-3).
+//    (2.7e-3 of a flat spectrum's result in that model, 0.6e-3 to 1.1e-3 so).
+//    lo gets half of d: all of it is right where X is flat, none where B takes
+//    lo's direction to zero.
+// Together 0.4e-3 to 1.1e-3 of the result against exact arithmetic, up to
+// 2.1e-3 at low rank (bf16 products: 1e-2 to 3e-2, and 3e-1 at low rank);
+// rounding the result to bf16 costs 1.7e-3.
 //
-// m n^2-like work: 3 m^2 n + m^3 operations a step (m <= n), the symmetric
-// products made on and above the diagonal only and mirrored by the epilogue,
-// which also forms every linear combination: nothing runs between products.
+// Work: 3 m^2 n + m^3 operations a step (m <= n), the symmetric products made
+// on and above the diagonal only and mirrored by the epilogue, which also
+// forms every linear combination: nothing runs between products. Large
+// matrices are bound by the tensor cores, the way from L2 to the SMs (the
+// operands take 64 bytes a cycle of it, X's slabs come on top) and the board's
+// power limit; the depth of the ring, bands of rows, staged whole-line stores
+// and loads of the sums ahead of their use moved the times by no more than the
+// clocks do. Small ones are bound by their chain of launches.
 #include <algorithm>
 #include <type_traits>
 
@@ -183,8 +189,9 @@ __global__ void __launch_bounds__(256)
 // bytes of a row at a time: whole sectors, and nothing waits for them. The
 // square matrices' mirror images leave transposed, by TMA.
 // (Results by TMA from where the operands came in, two places a warp, four
-// warps: 13 us for a 256 x 256 tile of X, the place being free again only when
-// the store has read it.)
+// warps: 13 us for a 256 x 256 tile of X against 11, the place being free again
+// only when the store has read it. Results through the slab's place in whole
+// 128-byte lines: 3 % slower, for it is the next slab that then waits.)
 // ---------------------------------------------------------------------------
 constexpr int kSlab = 4096;
 
@@ -365,8 +372,8 @@ struct PolyEpi {
   }
   static __device__ __forceinline__ void request(const Args& a, const TileAt& at, int col, EpiWarp& w) {
     if (w.lane == 0) {
-      mbar_arrive_expect_tx(&w.bars[0], kSlab);
-      tma_load_3d(w.smem, &a.O, &w.bars[0], col, at.row0, at.b);
+      mbar_arrive_expect_tx(w.bar, kSlab);
+      tma_load_3d(w.smem, &a.O, w.bar, col, at.row0, at.b);
     }
   }
   template <int BN>
@@ -385,7 +392,7 @@ struct PolyEpi {
     share<BN>(at, s, w, c0, c1);
 #pragma unroll 1
     for (int col = c0; col < c1; col += 64) {
-      mbar_wait(&w.bars[0], w.begun++ & 1, w.abort, kErrTimeoutEpi);
+      mbar_wait(w.bar, w.begun++ & 1, w.abort, kErrTimeoutEpi);
       uint4 raw[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) raw[i] = *slab_piece(w.smem, w.lane, i);
@@ -454,9 +461,9 @@ struct ApplyEpi {
   }
   static __device__ __forceinline__ void request(const Args& a, const TileAt& at, int col, EpiWarp& w) {
     if (w.lane == 0) {
-      mbar_arrive_expect_tx(&w.bars[0], 2 * kSlab);
-      tma_load_3d(w.smem, &a.hi, &w.bars[0], col, at.row0, at.b);
-      tma_load_3d(w.smem + kSlab, &a.lo, &w.bars[0], col, at.row0, at.b);
+      mbar_arrive_expect_tx(w.bar, 2 * kSlab);
+      tma_load_3d(w.smem, &a.hi, w.bar, col, at.row0, at.b);
+      tma_load_3d(w.smem + kSlab, &a.lo, w.bar, col, at.row0, at.b);
     }
   }
   template <int BN>
@@ -520,7 +527,7 @@ struct ApplyEpi {
     }
 #pragma unroll 1
     for (int col = c0; col < c1; col += 64) {
-      mbar_wait(&w.bars[0], w.begun++ & 1, w.abort, kErrTimeoutEpi);
+      mbar_wait(w.bar, w.begun++ & 1, w.abort, kErrTimeoutEpi);
       uint4 rh[8], rl[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -605,7 +612,7 @@ struct ApplyEpi {
 // the first and the second the sum of the CTAs' parts of A: each CTA adds up
 // 128 / S columns of it, from the others' shared memory, and sends them all
 // that share of A's rest in fp16 and of its diagonal. Latency is all that
-// counts here: 64 x 64 took 72 us as a chain of seventeen launches.
+// counts here: 64 x 64 took 72 us as a chain of seventeen launches, 20 so.
 // ---------------------------------------------------------------------------
 struct NarrowArgs {
   const void* G;

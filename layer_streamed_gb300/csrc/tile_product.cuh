@@ -13,13 +13,14 @@
 // are persistent and take tiles in a fixed order; each output is one fixed
 // sum, whatever the grid.
 //
-// An epilogue that has a tile's worth of other operands to read or results to
-// write moves them in slabs of 32 rows by 128 bytes, each warp its own, by
-// TMA through shared memory: while one is worked on, the next one is on its
-// way in and the last one on its way out. (Row by row from the lanes' own
-// loads and stores, one warp a scheduler had nothing else to do while it
-// waited: 24 us for a 256 x 256 tile that reads and writes four fp16 matrices,
-// against 6 us of MMAs at K = 1536.)
+// What an epilogue reads beside the sums comes by TMA in slabs of 32 rows by
+// 64 columns, each warp its own, asked for as soon as the one before is in
+// registers: for the next tile while its products run. Results leave from the
+// lanes in whole 32-byte sectors, or by TMA where shared memory gathers them
+// anyway. (Four warps with plain 16-byte loads and stores took 24 us for a 256
+// x 256 tile that reads and writes two fp16 matrices, against 7 us of MMAs at
+// K = 1536; eight so 11, most of it the way to and from L2, which the operands
+// share.)
 //
 // Rows, columns and depth need not be multiples of anything: TMA fills zeros
 // outside a matrix and drops what is stored there, and the epilogues look at
@@ -138,11 +139,11 @@ __device__ __forceinline__ uint4* slab_piece(uint8_t* slab, int row, int k) {
   return (uint4*)(slab + row * 128 + ((k ^ (row & 7)) << 4));
 }
 
-// What an epilogue warp keeps from tile to tile: its slabs and their two
-// barriers, how many slabs it has begun, its share of the columns.
+// What an epilogue warp keeps from tile to tile: its slabs and their barrier,
+// how many slabs it has begun, its share of the columns.
 struct EpiWarp {
   uint8_t* smem;
-  uint64_t* bars;
+  uint64_t* bar;
   volatile int* abort;
   int lane, part;
   uint32_t begun;
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // PAIR: the even CTA's, both CTAs drained
-  uint64_t* slab_bars = tempty + 2;  // two a warp
-  uint32_t* tmem_slot = (uint32_t*)(slab_bars + 2 * E::WARPS);
+  uint64_t* slab_bars = tempty + 2;  // one a warp
+  uint32_t* tmem_slot = (uint32_t*)(slab_bars + E::WARPS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
 
   const uint32_t warp = warp_id(), lane = lane_id();
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], (PAIR ? 2 : 1) * E::WARPS);
     }
-    for (int i = 0; i < 2 * E::WARPS; ++i) mbar_init(&slab_bars[i], 1);
+    for (int i = 0; i < E::WARPS; ++i) mbar_init(&slab_bars[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
     const uint32_t tempty0 = PAIR ? mapa_shared(tempty, 0) : 0;
     EpiWarp w;
     w.smem = slabs + (warp - 2) * E::SLABS;
-    w.bars = slab_bars + (warp - 2) * 2;
+    w.bar = slab_bars + (warp - 2);
     w.abort = abort_flag;
     w.lane = (int)lane;
     w.part = (int)(warp - 2) >> 2;

@@ -246,6 +246,71 @@ def bench_embed(args) -> dict:
             "gbs": nbytes / ms / 1e6}
 
 
+def bench_lce(args) -> dict:
+    """Cross entropy of X [T, h] with a head W [V, h] without the logits:
+    losses, or (--bwd) dX and dW in bf16. TFLOP/s counts one product forward,
+    three backward."""
+    T, V, h = args.T, args.V, args.h
+    X = torch.randn((T, h), device="cuda").to(torch.bfloat16)
+    W = (torch.randn((V, h), device="cuda") * 0.02).to(torch.bfloat16)
+    labels = torch.randint(0, V, (T,), device="cuda", dtype=torch.int32)
+    loss, lse, g = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.full((T,), 1.0 / T, device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    ws = torch.empty(max(mt.mt_op_linear_ce_fwd_workspace(T, V, h), mt.mt_op_linear_ce_bwd_workspace(T, V, h)),
+                     device="cuda", dtype=torch.uint8)
+    fwd = lambda: mt.mt_op_linear_ce_fwd(X, W, labels, 1.0, args.smoothing, 0.0, loss, lse, ws, T, V, h, h, h)
+    bwd = lambda: mt.mt_op_linear_ce_bwd(X, W, labels, 1.0, args.smoothing, 0.0, lse, g, dX, mt.MT_BF16, dW, mt.MT_BF16,
+                                         0, ws, T, V, h, h, h)
+    fwd()
+    ms = _time(bwd if args.bwd else fwd, args.reps)
+    return {"kernel": "linear_ce" + ("_bwd" if args.bwd else ""), "T": T, "V": V, "h": h, "ms": ms,
+            "tflops": (6.0 if args.bwd else 2.0) * T * V * h / ms / 1e9}
+
+
+def bench_muon(args) -> dict:
+    """The Muon step (fp32 momentum and gradient, bf16 weights) on a batch of
+    matrices, or (--ortho) the orthogonalised form of bf16 gradients alone.
+    TFLOP/s counts the symmetric products by half."""
+    b, r, c = args.batch, args.rows, args.cols
+    G = torch.randn((b, r, c), device="cuda")
+    ws = torch.empty(mt.mt_op_orthogonalize_workspace(b, r, c), device="cuda", dtype=torch.uint8)
+    if args.ortho:
+        Gb = G.to(torch.bfloat16)
+        O = torch.empty_like(Gb)
+        f = lambda: mt.mt_op_orthogonalize(Gb, mt.MT_BF16, O, mt.MT_BF16, None, args.steps, 1e-7, ws, b, r, c)
+    else:
+        W, M = (torch.randn_like(G) * 0.02).to(torch.bfloat16), torch.zeros_like(G)
+        f = lambda: mt.mt_op_muon_update(W, mt.MT_BF16, M, G, mt.MT_F32, 0.95, 1, 1e-3, 0.1, 1.0, None, args.steps, 1e-7,
+                                         ws, b, r, c)
+    ms = _time(f, args.reps)
+    m, n = min(r, c), max(r, c)
+    return {"kernel": "orthogonalize" if args.ortho else "muon_update", "batch": b, "rows": r, "cols": c,
+            "steps": args.steps, "ms": ms, "tflops": b * args.steps * (3.0 * m * m * n + 1.0 * m ** 3) / ms / 1e9}
+
+
+def bench_snorm(args) -> dict:
+    """The norms around a block's end (bf16 block output and gate), or (--bwd)
+    their gradients. GB/s counts every operand once."""
+    T, h, bf = args.T, args.h, torch.bfloat16
+    n = lambda dt=torch.float32: torch.randn((T, h), device="cuda").to(dt)
+    e = lambda *s, dt=torch.float32: torch.empty(s, device="cuda", dtype=dt)
+    x, y, gate, w = n(), n(bf), None if args.no_gate else n(bf), torch.ones(h, device="cuda")
+    xo, no, ra, rb = e(T, h), e(T, h, dt=bf), e(T), e(T)
+    fwd = lambda: mt.mt_op_sandwich_norm_fwd(x, y, gate, mt.MT_BF16, w, w, 0.9, 1e-5, xo, no, ra, rb, T, h)
+    fwd()
+    nbytes = T * h * (12 + (0 if args.no_gate else 2))
+    f = fwd
+    if args.bwd:
+        dn, dres, dx, dy, dwa, dwb = n(), n(), e(T, h), e(T, h, dt=bf), e(h), e(h)
+        dg, ws = None if args.no_gate else e(T, h, dt=bf), e(mt.mt_op_sandwich_norm_bwd_workspace(T, h))
+        f = lambda: mt.mt_op_sandwich_norm_bwd(xo, y, gate, mt.MT_BF16, w, w, 0.9, ra, rb, dn, dres, dx, dy, dg, dwa, dwb,
+                                               ws, T, h)
+        nbytes = T * h * (20 + (0 if args.no_gate else 4))
+    ms = _time(f, args.reps)
+    return {"kernel": "sandwich_norm" + ("_bwd" if args.bwd else ""), "T": T, "h": h, "gate": not args.no_gate, "ms": ms,
+            "gbs": nbytes / ms / 1e6}
+
+
 def main():
     ap = argparse.ArgumentParser()
     sub = ap.add_subparsers(dest="kernel", required=True)
@@ -300,10 +365,30 @@ def main():
     em.add_argument("--bwd", action="store_true")
     em.add_argument("--add", action="store_true")
     em.add_argument("--reps", type=int, default=20)
+    lc = sub.add_parser("lce")
+    lc.add_argument("--T", type=int, default=8192)
+    lc.add_argument("--V", type=int, default=128256)
+    lc.add_argument("--h", type=int, default=4096)
+    lc.add_argument("--smoothing", type=float, default=0.0)
+    lc.add_argument("--bwd", action="store_true")
+    lc.add_argument("--reps", type=int, default=20)
+    mu = sub.add_parser("muon")
+    mu.add_argument("--batch", type=int, default=1)
+    mu.add_argument("--rows", type=int, default=4096)
+    mu.add_argument("--cols", type=int, default=4096)
+    mu.add_argument("--steps", type=int, default=5)
+    mu.add_argument("--ortho", action="store_true")
+    mu.add_argument("--reps", type=int, default=20)
+    sn = sub.add_parser("snorm")
+    sn.add_argument("--T", type=int, default=8192)
+    sn.add_argument("--h", type=int, default=4096)
+    sn.add_argument("--no-gate", action="store_true")
+    sn.add_argument("--bwd", action="store_true")
+    sn.add_argument("--reps", type=int, default=20)
     args = ap.parse_args()
     mt.build()
     res = {"gemm": bench_gemm, "attn": bench_attn, "norm": bench_norm, "moe": bench_moe, "ckpt": bench_ckpt,
-           "logp": bench_logp, "embed": bench_embed}[args.kernel](args)
+           "logp": bench_logp, "embed": bench_embed, "lce": bench_lce, "muon": bench_muon, "snorm": bench_snorm}[args.kernel](args)
     res["device_error"] = mt.mt_op_device_error()
     print(json.dumps(res), flush=True)
 
