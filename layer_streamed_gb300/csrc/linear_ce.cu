@@ -457,8 +457,8 @@ cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int 
     using C = decltype(cfg);
     CUtensorMap ta, tb;
     const int ar = A_MN ? K : M, ac = A_MN ? M : K, br = B_MN ? K : N, bc = B_MN ? N : K;
-    if (!product_map(&ta, A, ar, ac, lda, lda, 1, a_box<C>(M), false) ||
-        !product_map(&tb, B, br, bc, ldb, ldb, 1, b_box<C>(), false))
+    if (!product_map(&ta, A, ar, ac, lda, lda, 1, a_box<C>(M, K), false) ||
+        !product_map(&tb, B, br, bc, ldb, ldb, 1, b_box<C>(K), false))
       return cudaErrorUnknown;
     ProductShape s = product_shape<C>(M, N, K, 1);
     if (ranges > 1) {

@@ -1025,8 +1025,8 @@ cudaError_t product(const Operand& A, const Operand& B, int M, int N, int K, int
     using C = decltype(cfg);
     constexpr int S = decltype(split)::value;
     CUtensorMap ta, tb;
-    if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(M), true) ||
-        !product_map(&tb, B.p, B.rows, B.cols, B.ld, B.ld * B.rows, batch, b_box<C>(), true))
+    if (!product_map(&ta, A.p, A.rows, A.cols, A.ld, A.ld * A.rows, batch, a_box<C>(M, K), true) ||
+        !product_map(&tb, B.p, B.rows, B.cols, B.ld, B.ld * B.rows, batch, b_box<C>(K), true))
       return cudaErrorUnknown;
     const ProductShape s = product_shape<C>(M, N, K, batch);
     if constexpr (S > 1) return launch_split<C, E, S>(ta, tb, s, args, st);

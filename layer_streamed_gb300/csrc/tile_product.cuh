@@ -40,6 +40,7 @@ struct ProductShape {
   int num_m, num_n, tiles;  // of one matrix; set by product_shape
   int group_m;   // row blocks that share a sweep over the columns
   int a_rows;    // rows of A that a CTA loads: 128, or fewer where M is (single SMs, K contiguous)
+  int k_rows;    // rows of a step of an operand with K along its rows: 64, or fewer where K is
   int split_kb;  // not 0: one matrix, `batch` counts ranges of split_kb 64-deep steps of its K
 };
 
@@ -103,16 +104,22 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Bytes that a CTA's loads of one step bring.
+template <class C>
+__device__ __forceinline__ uint32_t step_bytes(const ProductShape& s) {
+  return (C::A_MN ? C::BM / 64 * s.k_rows : s.a_rows) * 128 + (C::B_MN ? C::B_ROWS / 64 * s.k_rows : C::B_ROWS) * 128;
+}
 template <class C>
 __host__ __device__ constexpr uint32_t product_idesc() {
   return make_idesc(C::TM, C::BN, C::A_MN, C::B_MN) & (C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
-// One 64-deep step: four MMAs of depth 16.
+// One 64-deep step: four MMAs of depth 16, fewer where K ends (`rows` of it).
 template <class C>
 __device__ __forceinline__ void product_mma(uint32_t d_tmem, uint32_t a_base, uint32_t b_base, uint32_t idesc,
-                                            bool first) {
+                                            bool first, int rows) {
 #pragma unroll
   for (int kk = 0; kk < C::BK / 16; ++kk) {
+    if (kk * 16 >= rows) break;
     const uint64_t ad = C::A_MN ? make_sdesc(a_base + kk * 2048, 8192, 1024) : make_sdesc(a_base + kk * 32, 16, 1024);
     const uint64_t bd = C::B_MN ? make_sdesc(b_base + kk * 2048, 8192, 1024) : make_sdesc(b_base + kk * 32, 16, 1024);
     if (C::PAIR) tc_mma2(d_tmem, ad, bd, idesc, !first || kk != 0);
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
   if (warp == 0) {
     if (lane == 0) {  // TMA producer
       const uint32_t full0 = PAIR ? mapa_shared(full, 0) : 0;
-      const uint32_t stage_bytes = PAIR ? 2 * C::STAGE_BYTES : s.a_rows * (BK * 2) + C::B_BYTES;
+      const uint32_t stage_bytes = (PAIR ? 2 : 1) * step_bytes<C>(s);
       int stage = 0;
       uint32_t phase = 0;
       for (int tile = first; tile < all; tile += step) {
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
         for (int kb = 0; kb < num_kb; ++kb) {
           mbar_wait(&full[stage], phase, abort_flag, kErrTimeoutMma);
           tc_fence_after();
-          product_mma<C>(d_tmem, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == 0);
+          product_mma<C>(d_tmem, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == 0, s.k_rows);
           if (PAIR) tc_commit2(&empty[stage], 0x3);
           else tc_commit(&empty[stage]);
           if (++stage == STAGES) {
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(192, 1)
       for (int kb = k0; kb < k1; ++kb) {
         const int stage = (kb - k0) % STAGES;
         mbar_wait(&empty[stage], (((kb - k0) / STAGES) & 1) ^ 1, abort_flag, kErrTimeoutTma);
-        mbar_arrive_expect_tx(&full[stage], s.a_rows * (BK * 2) + C::B_BYTES);
+        mbar_arrive_expect_tx(&full[stage], step_bytes<C>(s));
         uint8_t* a_dst = sA + stage * C::A_BYTES;
         uint8_t* b_dst = sB + stage * C::B_BYTES;
         if (!C::A_MN) {
@@ -467,7 +474,7 @@ __global__ void __launch_bounds__(192, 1)
         const int stage = (kb - k0) % STAGES;
         mbar_wait(&full[stage], ((kb - k0) / STAGES) & 1, abort_flag, kErrTimeoutMma);
         tc_fence_after();
-        product_mma<C>(tmem_base, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == k0);
+        product_mma<C>(tmem_base, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == k0, s.k_rows);
         tc_commit(&empty[stage]);
       }
       tc_commit(done);  // with no steps: arrives at once
@@ -586,13 +593,15 @@ inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, in
 }
 // Box heights of an operand: the tile's rows where K is contiguous, K steps
 // else. Fewer rows of A than a tile has are loaded alone: what lies behind
-// them in the ring is never zeroed and makes rows of D that nobody reads.
-// (Boxes that TMA has to fill with zeros cost time: 128256 x 4096 times 7
-// rows took 248 us, times 64 rows 181.)
+// them in the ring is never zeroed and makes rows of D that nobody reads. A
+// K of fewer than 64 rows is loaded to its next whole 16, as deep as the MMAs
+// then go. (Boxes that TMA has to fill with zeros cost time: 128256 x 4096
+// times 7 rows took 248 us, times 64 rows 181.)
+inline int k_box(int K) { return std::min(64, (K + 15) / 16 * 16); }
 template <class C>
-int a_box(int M) { return C::A_MN ? 64 : C::PAIR ? C::BM : std::min(C::BM, (M + 7) / 8 * 8); }
+int a_box(int M, int K) { return C::A_MN ? k_box(K) : C::PAIR ? C::BM : std::min(C::BM, (M + 7) / 8 * 8); }
 template <class C>
-constexpr int b_box() { return C::B_MN ? 64 : C::B_ROWS; }
+int b_box(int K) { return C::B_MN ? k_box(K) : C::B_ROWS; }
 
 template <class C>
 ProductShape product_shape(int M, int N, int K, int batch) {
@@ -601,7 +610,8 @@ ProductShape product_shape(int M, int N, int K, int batch) {
   s.N = N;
   s.K = K;
   s.batch = batch;
-  s.a_rows = C::PAIR || C::A_MN ? C::BM : a_box<C>(M);
+  s.a_rows = C::A_MN ? C::BM : a_box<C>(M, K);
+  s.k_rows = k_box(K);
   s.split_kb = 0;
   s.num_m = (M + C::TM - 1) / C::TM;
   s.num_n = (N + C::BN - 1) / C::BN;
