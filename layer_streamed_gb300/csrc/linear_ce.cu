@@ -224,10 +224,11 @@ __device__ __forceinline__ void store8(void* base, size_t at, bool bf16, const f
 }
 
 // A piece's dz in bf16 (without the factor `scale`, which the next products'
-// epilogues apply). Two warps a row as above, slabs of 64 columns out.
+// epilogues apply). Two warps a row as above, slabs of 64 columns out by TMA,
+// one place a warp (two leave the ring a step shorter: 2 % slower).
 struct GradEpi : NoSlabs {
   static constexpr int kSlab = 4096;
-  static constexpr int WARPS = 8, SLABS = 2 * kSlab;
+  static constexpr int WARPS = 8, SLABS = kSlab;
   struct Args {
     CUtensorMap dz;
     const int32_t* labels;
@@ -280,8 +281,8 @@ struct GradEpi : NoSlabs {
     for (int j = w.part * (BN / 128); j < (w.part + 1) * (BN / 128); ++j) {
       const int col = at.n0 + j * 64;
       if (col >= s.N) break;
-      uint8_t* slab = w.smem + (w.begun++ & 1) * kSlab;
-      if (w.lane == 0) bulk_store_wait<1, true>();
+      uint8_t* slab = w.smem;
+      if (w.lane == 0) bulk_store_wait<0, true>();
       __syncwarp();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -310,52 +311,87 @@ struct GradEpi : NoSlabs {
   }
 };
 
-// out = scale * accumulator (+ what is there, or an fp32 sum), N a multiple of
-// 8; two warps a row as above, 32 columns at a time. The addend is asked for
-// ahead of the accumulator.
+// out = scale * accumulator, N a multiple of 8, by slabs of 64 bf16 or 32 fp32
+// columns; or added to what is there or to an fp32 sum, 32 columns at a time
+// straight to memory, the addend asked for ahead of the accumulator. Two warps
+// a row as above. (From the lanes' rows, 32 bytes at a time: dW of 7 tokens, V
+// 128256, h 4096, 397 us, so 353.)
 struct SumEpi : NoSlabs {
-  static constexpr int WARPS = 8, SLABS = 0;
+  static constexpr int kSlab = 4096;
+  static constexpr int WARPS = 8, SLABS = kSlab;
   struct Args {
+    CUtensorMap map;  // of out
     void* out;
     const void* add;  // same row stride; null: nothing
-    int64_t ld, apart;  // row stride; from one range's sums to the next one's
+    int64_t ld;
     float scale;
-    int out_bf16, add_bf16, sectors;  // sectors: bf16 rows in pieces of 32 bytes
+    int out_bf16, add_bf16;
   };
   struct Row {};
   static __device__ __forceinline__ void load_row(const Args&, const ProductShape&, const TileAt&, Row&) {}
+  template <int BN, bool BF16>
+  static __device__ __forceinline__ void written(const Args& a, const ProductShape& s, const TileAt& at, EpiWarp& w,
+                                                 uint32_t tb) {
+    constexpr int WIDE = BF16 ? 64 : 32;
+    const int c0 = at.n0 + w.part * (BN / 2), c1 = min(c0 + BN / 2, s.N);
+#pragma unroll 1
+    for (int col = c0; col < c1; col += WIDE) {
+      uint8_t* slab = w.smem;
+      if (w.lane == 0) bulk_store_wait<0, true>();
+      __syncwarp();
+#pragma unroll
+      for (int half = 0; half < WIDE / 32; ++half) {
+        float v[32];
+        tile_chunk(tb, (col - at.n0) / 32 + half, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= a.scale;
+        if (BF16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *slab_piece(slab, w.lane, half * 4 + i) =
+                make_uint4(pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *(float4*)slab_piece(slab, w.lane, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) {
+        tma_store_3d(&a.map, slab, col, at.row0, at.b);
+        bulk_store_commit();
+      }
+    }
+  }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
+    if (!a.add) {
+      if (a.out_bf16) written<BN, true>(a, s, at, w, tb);
+      else written<BN, false>(a, s, at, w, tb);
+      return;
+    }
     const bool ok = at.row < s.M;
-    const size_t row = (size_t)at.b * a.apart + (size_t)at.row * a.ld;
+    const size_t row = (size_t)at.row * a.ld;
 #pragma unroll 1
     for (int c = w.part * (BN / 64); c < (w.part + 1) * (BN / 64); ++c) {
       const int col = at.n0 + c * 32;
       if (col >= s.N) break;
       float add[4][8];
-      if (a.add && ok) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (ok && col + 8 * i < s.N) load8(a.add, row + col + 8 * i, a.add_bf16, add[i]);
       float v[32];
       tile_chunk(tb, c, v);
       if (!ok) continue;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = a.add ? fmaf(v[i], a.scale, add[i >> 3][i & 7]) : v[i] * a.scale;
-      if (a.out_bf16 && a.sectors && col + 32 <= s.N) {
-        uint32_t p[16];
+      for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], a.scale, add[i >> 3][i & 7]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
-        store32((uint16_t*)a.out + row + col, p);
-        store32((uint16_t*)a.out + row + col + 16, p + 8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + 8 * i < s.N) store8(a.out, row + col + 8 * i, a.out_bf16, v + 8 * i);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (col + 8 * i < s.N) store8(a.out, row + col + 8 * i, a.out_bf16, v + 8 * i);
     }
   }
 };
@@ -394,11 +430,11 @@ inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; 
 // Tiles of 256 x 256 on SM pairs where they fill half of the pairs; 128 x 128
 // on single SMs for fewer of them, for few rows (M up to 128: half of a pair's
 // tile would be empty; 128 tokens, V 32000, h 1024: dX 40 us on pairs, 36.4 on
-// single SMs) and for shallow sums (K up to 256: what counts is how many warps
-// write results; there dW of 7 tokens 47 against 41 us, of 256 tokens 50.5
-// against 48.5, of 512 66.6 against 75.4).
+// single SMs) and for shallow sums (K up to 128: what counts is how many warps
+// write results; dW of V 32000, h 1024: 7 tokens 39.8 us on pairs, 33.6 so, 128
+// tokens 41.9 and 39.4, 256 tokens 46.5 and 51.4).
 bool wide(int64_t M, int64_t N, int64_t K) {
-  return M > 128 && K > 256 && ((M + 255) / 256) * ((N + 255) / 256) >= mt_host::num_sms() / 4;
+  return M > 128 && K > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= mt_host::num_sms() / 4;
 }
 
 // The columns of a piece: dz of a piece has at most 2^28 values (or 256
@@ -412,8 +448,9 @@ int piece_cols(int T, int V) {
 // Ranges that the K of a gradient's product [M, N] is cut into: few tiles
 // (few tokens, or a small vocabulary) leave most of the GPU idle otherwise.
 // The number that takes the least time by a count of SM pairs' steps (512
-// cycles for a 256 x 256 tile 64 deep; 300 for 128 x 128 on one SM), with what the partial sums cost to
-// write and to read at 3500 bytes a cycle.
+// cycles for a 256 x 256 tile 64 deep; 300 for 128 x 128 on one SM), with what
+// the partial sums cost to write and to read at 3500 bytes a cycle (dX of 7
+// tokens, V 32000, h 1024: 141 us in one range, 17 in nineteen).
 int ranges_of(int64_t M, int64_t N, int K) {
   const int64_t edge = M <= 128 ? 128 : 256, units = M <= 128 ? kSms : kSms / 2, step = M <= 128 ? 300 : 512;
   const int64_t tiles = ((M + edge - 1) / edge) * ((N + edge - 1) / edge), steps = (K + 63) / 64;
@@ -469,6 +506,9 @@ cudaError_t product(const void* A, int64_t lda, const void* B, int64_t ldb, int 
     return launch_product<C, E>(ta, tb, s, args, st);
   };
   if (wide(M, N, K) || (ranges > 1 && M > 128)) return go(ProductCfg<256, true, A_MN, B_MN>());
+  if constexpr (A_MN) {  // dW of few tokens
+    if (K < 64) return go(ProductCfg<128, false, A_MN, B_MN, false, false, true>());
+  }
   return go(ProductCfg<128, false, A_MN, B_MN>());
 }
 
@@ -484,10 +524,12 @@ cudaError_t gradient(const void* A, int64_t lda, const void* B, int64_t ldb, int
   s.add = ranges > 1 ? nullptr : add;
   s.ld = N;
   s.scale = scale;
-  s.apart = all;
   s.out_bf16 = ranges == 1 && bf16;
   s.add_bf16 = add_bf16;
-  s.sectors = N % 16 == 0 && al(out, 32);
+  const int64_t apart = used > 1 ? all : N;
+  if (!(s.out_bf16 ? product_map(&s.map, s.out, M, N, N, apart, used, 32, false)
+                   : product_map_f32(&s.map, s.out, M, N, N, apart, used)))
+    return cudaErrorUnknown;
   cudaError_t e = product<A_MN, B_MN, SumEpi>(A, lda, B, ldb, M, N, K, s, st, ranges);
   if (ranges > 1 && e == cudaSuccess) {
     e = mt_host::launch_early(join_ranges_kernel, (int)std::min<int64_t>((all + 1023) / 1024, kSms * 8), 256, 0, st, 1,

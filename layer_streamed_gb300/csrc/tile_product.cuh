@@ -47,11 +47,14 @@ struct ProductShape {
 // BN: tile columns; PAIR: two SMs a tile; A_MN / B_MN: the operand is stored
 // with its outputs' axis contiguous ([K, M] and [K, N]) rather than K; F16:
 // fp16 operands; SYM: A = B and D symmetric, only tiles on and above the
-// diagonal are made (the epilogue mirrors them).
-template <int BN_, bool PAIR_, bool A_MN_, bool B_MN_, bool F16_ = false, bool SYM_ = false>
+// diagonal are made (the epilogue mirrors them); SHALLOW: K is below 64 and
+// operands with K along their rows are loaded and multiplied no deeper (a kind
+// of its own: the test of it in the MMAs' loop costs the others 4 %).
+template <int BN_, bool PAIR_, bool A_MN_, bool B_MN_, bool F16_ = false, bool SYM_ = false, bool SHALLOW_ = false>
 struct ProductCfg {
   static constexpr int BN = BN_;
-  static constexpr bool PAIR = PAIR_, A_MN = A_MN_, B_MN = B_MN_, F16 = F16_, SYM = SYM_;
+  static constexpr bool PAIR = PAIR_, A_MN = A_MN_, B_MN = B_MN_, F16 = F16_, SYM = SYM_,
+                        SHALLOW = SHALLOW_;
   static constexpr int BM = 128, BK = 64;
   static constexpr int TM = PAIR ? 2 * BM : BM;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B in one CTA
@@ -107,21 +110,27 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
 // Bytes that a CTA's loads of one step bring.
 template <class C>
 __device__ __forceinline__ uint32_t step_bytes(const ProductShape& s) {
-  return (C::A_MN ? C::BM / 64 * s.k_rows : s.a_rows) * 128 + (C::B_MN ? C::B_ROWS / 64 * s.k_rows : C::B_ROWS) * 128;
+  const int k = C::SHALLOW ? s.k_rows : C::BK;
+  return (C::A_MN ? C::BM / 64 * k : C::PAIR ? C::BM : s.a_rows) * 128 + (C::B_MN ? C::B_ROWS / 64 * k : C::B_ROWS) * 128;
 }
 template <class C>
 __host__ __device__ constexpr uint32_t product_idesc() {
   return make_idesc(C::TM, C::BN, C::A_MN, C::B_MN) & (C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
-// One 64-deep step: four MMAs of depth 16, fewer where K ends (`rows` of it).
+// Matrix descriptors of an operand's first step; a later place in the ring is
+// its distance / 16 further, the low bits being the address / 16.
+template <bool MN>
+__device__ __forceinline__ uint64_t first_desc(const void* ring) {
+  return MN ? make_sdesc(smem_u32(ring), 8192, 1024) : make_sdesc(smem_u32(ring), 16, 1024);
+}
+// One 64-deep step: four MMAs of depth 16, fewer where K has fewer `rows`.
 template <class C>
-__device__ __forceinline__ void product_mma(uint32_t d_tmem, uint32_t a_base, uint32_t b_base, uint32_t idesc,
-                                            bool first, int rows) {
+__device__ __forceinline__ void product_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool first,
+                                            int rows) {
 #pragma unroll
   for (int kk = 0; kk < C::BK / 16; ++kk) {
-    if (kk * 16 >= rows) break;
-    const uint64_t ad = C::A_MN ? make_sdesc(a_base + kk * 2048, 8192, 1024) : make_sdesc(a_base + kk * 32, 16, 1024);
-    const uint64_t bd = C::B_MN ? make_sdesc(b_base + kk * 2048, 8192, 1024) : make_sdesc(b_base + kk * 32, 16, 1024);
+    if (C::SHALLOW && kk * 16 >= rows) break;
+    const uint64_t ad = a + kk * ((C::A_MN ? 2048 : 32) >> 4), bd = b + kk * ((C::B_MN ? 2048 : 32) >> 4);
     if (C::PAIR) tc_mma2(d_tmem, ad, bd, idesc, !first || kk != 0);
     else tc_mma(d_tmem, ad, bd, idesc, !first || kk != 0);
   }
@@ -284,6 +293,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {  // MMA issuer
       constexpr uint32_t IDESC = product_idesc<C>();
+      const uint64_t a0 = first_desc<C::A_MN>(sA), b0 = first_desc<C::B_MN>(sB);
       int stage = 0, local = 0;
       uint32_t phase = 0;
       for (int tile = first; tile < all; tile += step, ++local) {
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(64 + 32 * E::WARPS, 1)
         for (int kb = 0; kb < num_kb; ++kb) {
           mbar_wait(&full[stage], phase, abort_flag, kErrTimeoutMma);
           tc_fence_after();
-          product_mma<C>(d_tmem, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == 0, s.k_rows);
+          product_mma<C>(d_tmem, a0 + stage * (C::A_BYTES >> 4), b0 + stage * (C::B_BYTES >> 4), IDESC, kb == 0, s.k_rows);
           if (PAIR) tc_commit2(&empty[stage], 0x3);
           else tc_commit(&empty[stage]);
           if (++stage == STAGES) {
@@ -470,11 +480,12 @@ __global__ void __launch_bounds__(192, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t IDESC = product_idesc<C>();
+      const uint64_t a0 = first_desc<C::A_MN>(sA), b0 = first_desc<C::B_MN>(sB);
       for (int kb = k0; kb < k1; ++kb) {
         const int stage = (kb - k0) % STAGES;
         mbar_wait(&full[stage], ((kb - k0) / STAGES) & 1, abort_flag, kErrTimeoutMma);
         tc_fence_after();
-        product_mma<C>(tmem_base, smem_u32(sA + stage * C::A_BYTES), smem_u32(sB + stage * C::B_BYTES), IDESC, kb == k0, s.k_rows);
+        product_mma<C>(tmem_base, a0 + stage * (C::A_BYTES >> 4), b0 + stage * (C::B_BYTES >> 4), IDESC, kb == k0, s.k_rows);
         tc_commit(&empty[stage]);
       }
       tc_commit(done);  // with no steps: arrives at once
@@ -591,17 +602,26 @@ inline bool product_map(CUtensorMap* m, const void* base, int rows, int cols, in
                                box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ==
          CUDA_SUCCESS;
 }
+// The same for fp32 results, in slabs of 32 columns by 32 rows.
+inline bool product_map_f32(CUtensorMap* m, const void* base, int rows, int cols, int64_t ld, int64_t apart, int batch) {
+  const uint64_t gdim[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
+  const uint64_t gstride[2] = {(uint64_t)ld * 4, (uint64_t)apart * 4};
+  const uint32_t box[3] = {32, 32, 1};
+  return mt_host::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, gdim, gstride, box,
+                               CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
 // Box heights of an operand: the tile's rows where K is contiguous, K steps
 // else. Fewer rows of A than a tile has are loaded alone: what lies behind
 // them in the ring is never zeroed and makes rows of D that nobody reads. A
-// K of fewer than 64 rows is loaded to its next whole 16, as deep as the MMAs
-// then go. (Boxes that TMA has to fill with zeros cost time: 128256 x 4096
+// shallow K's rows are loaded to the next whole 16, as deep as the MMAs then
+// go. (Boxes that TMA has to fill with zeros cost time: 128256 x 4096
 // times 7 rows took 248 us, times 64 rows 181.)
-inline int k_box(int K) { return std::min(64, (K + 15) / 16 * 16); }
 template <class C>
-int a_box(int M, int K) { return C::A_MN ? k_box(K) : C::PAIR ? C::BM : std::min(C::BM, (M + 7) / 8 * 8); }
+int k_box(int K) { return C::SHALLOW ? std::min(64, (K + 15) / 16 * 16) : 64; }
 template <class C>
-int b_box(int K) { return C::B_MN ? k_box(K) : C::B_ROWS; }
+int a_box(int M, int K) { return C::A_MN ? k_box<C>(K) : C::PAIR ? C::BM : std::min(C::BM, (M + 7) / 8 * 8); }
+template <class C>
+int b_box(int K) { return C::B_MN ? k_box<C>(K) : C::B_ROWS; }
 
 template <class C>
 ProductShape product_shape(int M, int N, int K, int batch) {
@@ -611,7 +631,7 @@ ProductShape product_shape(int M, int N, int K, int batch) {
   s.K = K;
   s.batch = batch;
   s.a_rows = C::A_MN ? C::BM : a_box<C>(M, K);
-  s.k_rows = k_box(K);
+  s.k_rows = k_box<C>(K);
   s.split_kb = 0;
   s.num_m = (M + C::TM - 1) / C::TM;
   s.num_n = (N + C::BN - 1) / C::BN;
