@@ -244,6 +244,44 @@ def test_several_pieces_of_the_vocabulary():
         _check(torch, r, f)
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,V,h", [(3000, 300, 64), (130, 20000, 128), (5000, 200, 320)])
+def test_sums_cut_into_ranges_and_added(T, V, h, bf16):
+    """Few tiles and deep sums: partial sums, joined and added to what is there."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _case(torch, T, V, h, 71)
+    labels[::5] = -1
+    dt = torch.bfloat16 if bf16 else torch.float32
+    start = torch.randn((V, h), device="cuda").to(dt)
+    r = _run(torch, mt, X, W, labels, gl, 1.0, 0.0, 1e-3, dt, dt, start=start)
+    f = _reference(torch, X, W, labels, gl, 1.0, 0.0, 1e-3, h)
+    _check(torch, r, f, start)
+
+
+@pytest.mark.parametrize("T,V,h", [(1 << 24, 200, 8), (3, 1 << 24, 8), (5, 70, 1 << 16)])
+def test_largest_sizes(T, V, h):
+    """The most rows, columns and depth that are taken, at rows picked from all over."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _case(torch, T, V, h, 81)
+    ws = torch.empty(max(mt.mt_op_linear_ce_fwd_workspace(T, V, h), mt.mt_op_linear_ce_bwd_workspace(T, V, h)),
+                     dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dX, dW = torch.empty((T, h), device="cuda"), torch.empty((V, h), device="cuda")
+    mt.mt_op_linear_ce_fwd(X, W, labels, 1.0, 0.0, 0.0, loss, lse, ws, T, V, h, h, h)
+    mt.mt_op_linear_ce_bwd(X, W, labels, 1.0, 0.0, 0.0, lse, gl, dX, mt.MT_F32, dW, mt.MT_F32, 0, ws, T, V, h, h, h)
+    at = torch.unique(torch.linspace(0, T - 1, 37, device="cuda").long())
+    f = _reference(torch, X[at], W, labels[at], gl[at], 1.0, 0.0, 0.0, h)
+    r = Result()
+    r.loss, r.lse, r.dX = loss[at], lse[at], dX[at]
+    _check(torch, r, f)
+    # over the vocabulary a row's dz adds up to g (sum p - 1) = 0, so dW's rows do: up to dz's rounding, at most 2^-8 of
+    # the magnitudes |g| (p + 1) |x|, and the fp32 sums
+    total = dW.double().sum(0)
+    mag = sum((2 * gl[i:i + (1 << 20)].double().abs()[:, None] * X[i:i + (1 << 20)].double().abs()).sum(0) for i in range(0, T, 1 << 20))
+    assert bool((total.abs() <= (U16 * 1.1 + acc(T)) * mag).all())
+    assert mt.mt_op_device_error() == 0
+
+
 def test_gradient_against_differences():
     """Central differences of the float64 sum of the kernel's own losses' definition, by the direction of dX and dW."""
     torch, mt = need_gpu()

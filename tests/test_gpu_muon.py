@@ -109,25 +109,37 @@ def test_known_results():
     assert float((O - poly(1 / 16) * Q).norm() / O.norm()) < 4e-3
 
 
-def test_scale_eps_and_odd_matrices_of_a_batch():
+@pytest.mark.parametrize("rows,cols", [(70, 90), (140, 200), (333, 150)])
+def test_scale_eps_and_odd_matrices_of_a_batch(rows, cols):
     torch, mt = need_gpu()
-    G = _matrix(torch, "gradient", 6, 70, 90, 9)
+    G = _matrix(torch, "gradient", 6, rows, cols, 9)
     plain = _ortho(torch, mt, G)
     for k in (2.0 ** -40, 2.0 ** 30):  # powers of two change nothing but the norm's own range
         assert torch.equal(_ortho(torch, mt, G * k), plain)
     _check(torch, _ortho(torch, mt, G, eps=float(G[0].norm())), G, eps=float(np.float32(float(G[0].norm()))))
     G[1] = 0
     G[2, 3, 4] = float("inf")
-    G[3, 69, 89] = float("nan")
+    G[3, -1, -1] = float("nan")
     G[4] *= 1e30
     got = _ortho(torch, mt, G)
     assert torch.equal(got[0], plain[0]) and torch.equal(got[5], plain[5])
     assert not got[1].any() and torch.isnan(got[2:5]).all()
 
 
+@pytest.mark.parametrize("b,rows,cols", [(1, 1, 1 << 16), (1, 1 << 16, 3), (4096, 3, 2), (1, 130, 1 << 16), (1, 1 << 16, 200)])
+def test_longest_sides_and_largest_batches(b, rows, cols):
+    torch, mt = need_gpu()
+    G = _matrix(torch, "gradient", b, rows, cols, 29)
+    got = _ortho(torch, mt, G)
+    if b > 8:
+        at = torch.tensor([0, 1, b // 2, b - 1], device="cuda")
+        G, got = G[at].contiguous(), got[at]
+    _check(torch, got, G)
+
+
 def test_in_place_and_repeats():
     torch, mt = need_gpu()
-    for shape in ((2, 100, 300), (2, 300, 101)):
+    for shape in ((2, 100, 300), (2, 300, 101), (2, 200, 300), (1, 700, 260)):
         G = _matrix(torch, "spikes", *shape, 11)
         want = _ortho(torch, mt, G)
         assert torch.equal(want, _ortho(torch, mt, G))
