@@ -324,7 +324,7 @@ struct GramEpi : NoSlabs {
   struct Early {};
   static __device__ __forceinline__ void early(const Args&, const ProductShape&, const TileAt&, int, Early&) {}
   static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row&,
-                                               const Early&, int col, float (&v)[32]) {
+                                               const Early&, int col, float (&v)[32], uint8_t*) {
     values(a, s, at, col, v);
     write_square(a.O + (size_t)at.b * s.M * a.ld, a.ld, at, col, s.M, v);
   }
@@ -420,7 +420,7 @@ struct PolyEpi {
     if (at.row < s.M) load_row32(a.O_rows + ((size_t)at.b * s.M + at.row) * a.ld, col, s.N, e.o);
   }
   static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                               const Early& e, int col, float (&v)[32]) {
+                                               const Early& e, int col, float (&v)[32], uint8_t*) {
     float o[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -471,6 +471,12 @@ struct ApplyEpi {
     int c0, c1;
     share<BN>(at, s, w, c0, c1);
     if (at.row0 < s.M && c0 < c1) request(a, at, c0, w);
+    if (LAST && a.update && at.row < s.M) {  // the weights' lines into L2, while the sums are made
+      const int e = a.out_bf16 ? 2 : 4;
+      const char* line = (const char*)a.out + ((size_t)at.b * s.M + at.row) * s.N * e;
+      for (int c = c0 * e; c < c1 * e; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + c));
+      if (c0 < c1) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + c1 * e - 1));
+    }
   }
   // LAST: 16 results from `col` of this lane's row.
   static __device__ __forceinline__ void finish16(const Args& a, const ProductShape& s, size_t row, int col, float* x) {
@@ -513,18 +519,88 @@ struct ApplyEpi {
       else ((float*)a.out)[o + e] = r;
     }
   }
+  // LAST where rows lie on no boundary: results wait in shared memory, 32 fp32
+  // columns by 32 rows a slab, and leave a row at a time: fp32 a column a lane,
+  // bf16 two a lane, at whole words wherever a row begins (lane 0 of a row that
+  // begins between two has the first column and the last).
+  // (Muon step of 8 x 936 x 7753, the last product: from the lanes' own rows,
+  // value by value, 1100 us; a column a lane 415; so 271.)
+  static __device__ __forceinline__ void hold16(uint8_t* slab, int lane, int k, const float* x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *(float4*)slab_piece(slab, lane, k + e) =
+          make_float4(x[4 * e] * kXDown, x[4 * e + 1] * kXDown, x[4 * e + 2] * kXDown, x[4 * e + 3] * kXDown);
+  }
+  static __device__ __forceinline__ float held_at(uint8_t* slab, int row, int col) {  // of 64 columns in two slabs
+    return ((const float*)slab_piece(slab + (col >> 5) * kSlab, row, (col & 31) >> 2))[col & 3];
+  }
+  // `cols` (32 or 64) columns from col
+  static __device__ __forceinline__ void write_rows(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                                    uint8_t* slab, int lane, int cols) {
+    const int rows = min(32, s.M - at.row0), end = min(s.N - col, cols);
+    const size_t o0 = ((size_t)at.b * s.M + at.row0) * s.N + col;
+    if (!a.out_bf16) {
+      for (int c = lane; c < end; c += 32) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          float* p = (float*)a.out + o0 + (size_t)r0 * s.N + c;
+          float old[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) old[i] = a.update && r0 + i < rows ? p[(size_t)i * s.N] : 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (r0 + i >= rows) break;
+            const float x = held_at(slab, r0 + i, c);
+            p[(size_t)i * s.N] = a.update ? fmaf(a.keep, old[i], -a.step * x) : x;
+          }
+        }
+      }
+      return;
+    }
+    if (2 * lane >= cols) return;
+    uint16_t* out = (uint16_t*)a.out;
+    const size_t between = ((uintptr_t)out >> 1) & 1;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      // asked for together: nothing is made of a value before the last is on its way
+      uint32_t both[8];
+      uint16_t first[8], second[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        both[i] = 0;
+        first[i] = second[i] = 0;
+        const size_t o = o0 + (size_t)(r0 + i) * s.N;
+        const int e = 2 * lane - (int)((o + between) & 1), f = e < 0 ? cols - 1 : e;
+        const bool in = a.update && r0 + i < rows, word = e >= 0 && e + 1 < end;
+        if (in && word) both[i] = *(const uint32_t*)(out + o + e);
+        if (in && !word && f < end) first[i] = out[o + f];
+        if (in && !word && e + 1 < end) second[i] = out[o + e + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i >= rows) break;
+        const size_t o = o0 + (size_t)(r0 + i) * s.N;
+        const int e = 2 * lane - (int)((o + between) & 1), f = e < 0 ? cols - 1 : e;
+        const bool word = e >= 0 && e + 1 < end;
+        float x = f < end ? held_at(slab, r0 + i, f) : 0.f, y = e + 1 < end ? held_at(slab, r0 + i, e + 1) : 0.f;
+        if (a.update) {
+          x = fmaf(a.keep, bf2f(word ? (uint16_t)both[i] : first[i]), -a.step * x);
+          y = fmaf(a.keep, bf2f(word ? (uint16_t)(both[i] >> 16) : second[i]), -a.step * y);
+        }
+        const uint32_t w = pack_bf2(x, y);
+        if (word) *(uint32_t*)(out + o + e) = w;
+        if (!word && f < end) out[o + f] = (uint16_t)w;
+        if (!word && e + 1 < end) out[o + e + 1] = (uint16_t)(w >> 16);
+      }
+    }
+  }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
-    const size_t out0 = ((size_t)at.b * s.M + at.row) * s.N;
+    const bool held = LAST && !a.vec;  // the results take the slabs' place for a while
     int c0, c1;
     share<BN>(at, s, w, c0, c1);
-    if (LAST && a.update && at.row < s.M) {  // the weights' lines, while the sums are waited for
-      const int e = a.out_bf16 ? 2 : 4;
-      for (int c = c0 * e; c < c1 * e; c += 128)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)a.out + out0 * e + c));
-    }
 #pragma unroll 1
     for (int col = c0; col < c1; col += 64) {
       mbar_wait(w.bar, w.begun++ & 1, w.abort, kErrTimeoutEpi);
@@ -536,7 +612,7 @@ struct ApplyEpi {
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (col + 64 < c1) request(a, at, col + 64, w);
+      if (!held && col + 64 < c1) request(a, at, col + 64, w);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float v[32];
@@ -546,14 +622,23 @@ struct ApplyEpi {
           const uint4 *hq = rh + half * 4 + q * 2, *lq = rl + half * 4 + q * 2;
           const uint32_t h[8] = {hq[0].x, hq[0].y, hq[0].z, hq[0].w, hq[1].x, hq[1].y, hq[1].z, hq[1].w};
           const uint32_t l[8] = {lq[0].x, lq[0].y, lq[0].z, lq[0].w, lq[1].x, lq[1].y, lq[1].z, lq[1].w};
-          step16(a, s, at, r, col + 32 * half + 16 * q, h, l, v + 16 * q);
+          new16(a, at, r, col + 32 * half + 16 * q, h, l, v + 16 * q);
+          if (held) hold16(w.smem + half * kSlab, w.lane, 4 * q, v + 16 * q);
+          else put16(a, s, at, col + 32 * half + 16 * q, v + 16 * q);
         }
+      }
+      if (held) {
+        __syncwarp();
+        write_rows(a, s, at, col, w.smem, w.lane, 64);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (col + 64 < c1) request(a, at, col + 64, w);
       }
     }
   }
-  // 16 columns from col of this lane's row
-  static __device__ __forceinline__ void step16(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                                int col, const uint32_t* hw, const uint32_t* lw, float* x) {
+  // 16 values of the new X (times kXUp) from col of this lane's row
+  static __device__ __forceinline__ void new16(const Args& a, const TileAt& at, const Row& r, int col,
+                                               const uint32_t* hw, const uint32_t* lw, float* x) {
     const float* dcol = a.db + at.b * a.dpad + col;
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -566,6 +651,9 @@ struct ApplyEpi {
       for (int f = 0; f < 4; ++f)
         x[i + f] = fmaf(a.a + d[f], h[f], fmaf(fmaf(0.5f, d[f], a.a), l[f], x[i + f] * kADown));
     }
+  }
+  static __device__ __forceinline__ void put16(const Args& a, const ProductShape& s, const TileAt& at, int col,
+                                               float* x) {
     if (at.row >= s.M || col >= s.N) return;
     const size_t row = (size_t)at.b * s.M + at.row;
     if (!LAST) {
@@ -595,9 +683,19 @@ struct ApplyEpi {
     load_row32(a.lo_out + o, col, s.N, e.l);
   }
   static __device__ __forceinline__ void chunk(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                               const Early& e, int col, float (&v)[32]) {
-    step16(a, s, at, r, col, e.h, e.l, v);
-    step16(a, s, at, r, col + 16, e.h + 8, e.l + 8, v + 16);
+                                               const Early& e, int col, float (&v)[32], uint8_t* room) {
+    const bool held = LAST && !a.vec;
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      new16(a, at, r, col + 16 * q, e.h + 8 * q, e.l + 8 * q, v + 16 * q);
+      if (held) hold16(room, lane, 4 * q, v + 16 * q);
+      else put16(a, s, at, col + 16 * q, v + 16 * q);
+    }
+    if (held) {
+      __syncwarp();
+      write_rows(a, s, at, col, room, lane, 32);
+    }
   }
 };
 

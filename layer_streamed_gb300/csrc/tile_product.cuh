@@ -392,7 +392,8 @@ __device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
 // tile, each a range of K; then each gets a 128 / S wide share of its columns
 // from the others through distributed shared memory, adds the parts in rank
 // order and runs the epilogue on it, 32 columns of a row a thread.
-// E::early asks for what E::chunk needs beside the sums, while these are made.
+// E::early asks for what E::chunk needs beside the sums, while these are made;
+// E::chunk has 4 KB of shared memory a warp.
 // (Three 32 KB steps in flight, so that the CTAs of two launches fit on an SM:
 // 1024 x 4096 orthogonalised in 210 us, with four 183, with more no faster.)
 // ---------------------------------------------------------------------------
@@ -571,7 +572,9 @@ __global__ void __launch_bounds__(192, 1)
           }
         }
       }
-      E::chunk(args, s, at, row_in, early[c], at.n0 + 32 * chunk, sum);
+      // 4 KB of the place that this CTA's own part does not need
+      uint8_t* room = parts + (rank * CHUNKS + c) * SplitSmem::PART + q * 4096;
+      E::chunk(args, s, at, row_in, early[c], at.n0 + 32 * chunk, sum, room);
     }
   }
   if (*abort_flag) {

@@ -156,11 +156,19 @@ def test_values_off_any_boundary():
         shifted.copy_(G)
         out = torch.empty(G.numel() + 1, device="cuda", dtype=dt)[1:].view(G.shape)
         assert torch.equal(_ortho(torch, mt, shifted, o=out), _ortho(torch, mt, G, out=dt))
+        # rows whose ends lie between two words, guards on both sides
+        for rows, cols in ((130, 201), (700, 513), (150, 264)):
+            G = _matrix(torch, "spikes", 1, rows, cols, 13).to(dt)
+            raw = torch.full((G.numel() + 2,), 7.0, device="cuda", dtype=dt)
+            out = raw[1:-1].view(G.shape)
+            _ortho(torch, mt, G, o=out)
+            assert torch.equal(out, _ortho(torch, mt, G, out=dt)) and raw[0] == 7 and raw[-1] == 7
 
 
 @pytest.mark.parametrize("nesterov", [0, 1])
 @pytest.mark.parametrize("wb,gb", [(False, False), (True, False), (True, True), (False, True)])
-@pytest.mark.parametrize("b,rows,cols", [(1, 1, 5), (2, 129, 130), (1, 520, 264), (3, 40, 333), (2, 700, 100), (3, 64, 1536)])
+@pytest.mark.parametrize("b,rows,cols", [(1, 1, 5), (2, 129, 130), (1, 520, 264), (3, 40, 333), (2, 700, 100), (3, 64, 1536), (2, 131, 259),
+                                         (1, 401, 6001), (1, 5003, 301), (3, 260, 140), (1, 2001, 1999)])
 def test_update(b, rows, cols, wb, gb, nesterov):
     torch, mt = need_gpu()
     bf, f4 = torch.bfloat16, torch.float32
