@@ -524,7 +524,7 @@ struct ApplyEpi {
   // bf16 two a lane, at whole words wherever a row begins (lane 0 of a row that
   // begins between two has the first column and the last).
   // (Muon step of 8 x 936 x 7753, the last product: from the lanes' own rows,
-  // value by value, 1100 us; a column a lane 415; so 271.)
+  // value by value, took 1100 us; a column a lane 415; as here 271.)
   static __device__ __forceinline__ void hold16(uint8_t* slab, int lane, int k, const float* x) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -781,15 +781,51 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
   const bool vec_out = !p.tall && p.cols % 4 == 0 && ((uintptr_t)p.out & (p.out_bf16 ? 7 : 15)) == 0;
   auto at = [&](int j) { return mat + (p.tall ? (size_t)j * p.cols + row : (size_t)row * p.cols + j); };
 
-  // U into tensor memory, the sum of its squares
+  // U into tensor memory, the sum of its squares. Rows on no boundary come a row
+  // at a time, a column a lane, and wait in shared memory (the blocks' place,
+  // not yet in use; a row is 257 words, so that neither side meets a bank
+  // twice). 100 x 1001: 54 us, and 78 value by value from the lanes' own rows.
   float sum = 0.f;
+  float* rows = (float*)xh;
+  constexpr int kRow = 257;
+  const bool by_rows = !p.tall && !vec;
+  if (by_rows) {
+#pragma unroll 1
+    for (int r = warp; r < p.m; r += 16) {
+      float u[8], m[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = lane + 32 * k;
+        const size_t o = mat + (size_t)r * p.cols + j0 + c;
+        u[k] = c < mine ? load1(p.G, o, p.g_bf16) : 0.f;
+        m[k] = c < mine && p.M ? p.M[o] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = lane + 32 * k;
+        if (p.M) {
+          m[k] = fmaf(p.mu, m[k], u[k]);
+          u[k] = p.nesterov ? fmaf(p.mu, m[k], u[k]) : m[k];
+          if (c < mine) p.M[mat + (size_t)r * p.cols + j0 + c] = m[k];
+        }
+        rows[r * kRow + c] = u[k];
+      }
+    }
+    __syncthreads();
+  }
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const int col = part * 64 + c * 32;
     float u[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = 0.f;
-    if (row < p.m && col < mine) {
+    if (by_rows && row < p.m) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        u[i] = rows[row * kRow + col + i];
+        sum = fmaf(u[i], u[i], sum);
+      }
+    } else if (row < p.m && col < mine) {
       float m[32];
       if (vec && col + 32 <= mine) {
 #pragma unroll
@@ -1041,6 +1077,9 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
           if (p.out_bf16) *(uint2*)((uint16_t*)p.out + o) = make_uint2(pack_bf2(r[0], r[1]), pack_bf2(r[2], r[3]));
           else *(float4*)((float*)p.out + o) = make_float4(r[0], r[1], r[2], r[3]);
         }
+      } else if (!p.tall && !vec_out) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) rows[row * kRow + col + i] = x[i] * kXDown;  // the blocks have been read
       } else if (row < p.m) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -1054,6 +1093,24 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
       }
     }
     if (!last) tmem_st_wait();
+  }
+  if (!p.tall && !vec_out) {  // rows on no boundary leave as they come
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < p.m; r += 16) {
+      const size_t o = mat + (size_t)r * p.cols + j0 + lane;
+      float old[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) old[k] = p.update && lane + 32 * k < mine ? load1(p.out, o + 32 * k, p.out_bf16) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (lane + 32 * k >= mine) break;
+        float x = rows[r * kRow + lane + 32 * k];
+        if (p.update) x = fmaf(p.keep, old[k], -p.step * x);
+        if (p.out_bf16) ((uint16_t*)p.out)[o + 32 * k] = f2bf(x);
+        else ((float*)p.out)[o + 32 * k] = x;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
