@@ -202,3 +202,38 @@ def test_offsets_past_32_bits():
     O = _ortho(torch, mt, G, steps=2, o=G)
     _check(torch, O[-1:].clone(), last, 2)
     assert torch.equal(O[0], O[1500]) and torch.equal(O[0], O[-2])
+
+
+@pytest.mark.parametrize("b,rows,cols", [(1, 128, 256), (2, 128, 260), (3, 97, 512), (1, 128, 1028), (1, 5, 2052), (2, 128, 4096)])
+def test_one_launch_from_any_boundary(b, rows, cols):
+    """Tensors that begin one value off take the way by rows: the same sums in the same order, so equal bits."""
+    torch, mt = need_gpu()
+    bf, f4 = torch.bfloat16, torch.float32
+
+    def off(t):
+        raw = torch.full((t.numel() + 2,), 7.0, device="cuda", dtype=t.dtype)
+        raw[1:-1] = t.flatten()
+        return raw, raw[1:-1].view(t.shape)
+
+    for dt in (f4, bf):
+        G = _matrix(torch, "gradient", b, rows, cols, 37).to(dt)
+        M = 3 * _matrix(torch, "gradient", b, rows, cols, 38)
+        W = (0.02 * _matrix(torch, "flat", b, rows, cols, 39)).to(dt)
+        (_, g), (rm, m), (rw, w) = off(G), off(M), off(W)
+        code = mt.MT_F32 if dt == f4 else mt.MT_BF16
+        ws = torch.empty(mt.mt_op_orthogonalize_workspace(b, rows, cols), device="cuda", dtype=torch.uint8)
+        mt.mt_op_muon_update(W, code, M, G, code, 0.9, 1, 0.01, 0.1, 1.0, None, 5, 1e-7, ws, b, rows, cols)
+        mt.mt_op_muon_update(w, code, m, g, code, 0.9, 1, 0.01, 0.1, 1.0, None, 5, 1e-7, ws, b, rows, cols)
+        assert torch.equal(m, M) and torch.equal(w, W)
+        assert rm[0] == 7 and rm[-1] == 7 and rw[0] == 7 and rw[-1] == 7
+
+
+@pytest.mark.parametrize("b,rows,cols", [(2, 128, 255), (1, 128, 257), (1, 127, 1027), (2, 128, 4095)])
+def test_one_launch_of_odd_rows_in_place(b, rows, cols):
+    torch, mt = need_gpu()
+    G = _matrix(torch, "gradient", b, rows, cols, 41)
+    want = _ortho(torch, mt, G)
+    _check(torch, want, G)
+    o = G.clone()
+    assert torch.equal(want, _ortho(torch, mt, o, o=o))
+    assert mt.mt_op_device_error() == 0
