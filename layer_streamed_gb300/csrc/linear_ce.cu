@@ -54,8 +54,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ---------------------------------------------------------------------------
 // Forward epilogue: per row and tile the maximum of z log2(e) and the sum of
-// 2^(. - maximum); with smoothing the sum of the accumulators too; the
-// label's own logit.
+// 2^(. - maximum) over all columns but the label's; with smoothing the sum of
+// the accumulators too; the label's own logit. The label's term joins the
+// others' sum last (join_rows_kernel), so that nothing is ever taken out of a sum.
 // ---------------------------------------------------------------------------
 // Two warps a row of a tile, half of the columns each, hide each other's
 // latencies: with one, 8 us a tile of 256 x 256 against 4.2 us of MMAs at h = 1024.
@@ -73,9 +74,8 @@ struct StatsEpi : NoSlabs {
   };
   // The label's logit again, in fp32 (a sum of h / 32 terms a lane, then a
   // tree): the tensor core's long sums come out a few 2^-24 of their terms
-  // short, 1.6e-6 of the loss at h = 4096; the label's own term is most of what
-  // counts of that, in the loss and, where its probability is high, in the
-  // log-sum-exp. By the epilogue's warps, idle until the first tile is there.
+  // short, 1.6e-6 of the loss at h = 4096, and the label's own is most of what
+  // counts of that. By the epilogue's warps, idle until the first tile is there.
   static __device__ __forceinline__ void begin(const Args& a, int warp) {
     const int lane = (int)lane_id(), n8 = a.h >> 3;
     for (int t = (int)blockIdx.x * WARPS + warp; t < a.T; t += (int)gridDim.x * WARPS) {
@@ -102,14 +102,14 @@ struct StatsEpi : NoSlabs {
     int label;
   };
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
-    r.label = at.row < s.M ? a.labels[at.row] : -1;
+    r.label = at.row < s.M ? max(a.labels[at.row], -1) : -1;
   }
   template <int BN>
   static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
                                               EpiWarp& w, uint32_t tb) {
     if (at.row0 >= s.M) return;
     const float k = a.scale * kLog2e;
-    float m = -INFINITY, sum = 0.f, plain = 0.f;
+    float top = -INFINITY, m = -INFINITY, sum = 0.f, plain = 0.f;  // m = top k
     const int here = r.label - at.n0;  // the label's column in this tile, if it is one
 #pragma unroll 1
     for (int c = w.part * (BN / 64); c < (w.part + 1) * (BN / 64); ++c) {
@@ -122,10 +122,13 @@ struct StatsEpi : NoSlabs {
         for (int i = 0; i < 32; ++i) p[i & 3] += v[i];
         plain += (p[0] + p[1]) + (p[2] + p[3]);
       }
-      if (here >= c * 32 && here < c * 32 + 32 && at.row < s.M) {
+      if (here >= c * 32 && here < c * 32 + 32) {
         float z = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) z = here == c * 32 + i ? v[i] : z;
+        for (int i = 0; i < 32; ++i) {
+          z = here == c * 32 + i ? v[i] : z;
+          v[i] = here == c * 32 + i ? -INFINITY : v[i];
+        }
         a.zlab[at.row].x = z * a.scale;
       }
       if (at.n0 + c * 32 + 32 > s.N) {
@@ -136,11 +139,17 @@ struct StatsEpi : NoSlabs {
       float cm[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
       for (int i = 4; i < 32; ++i) cm[i & 3] = fmaxf(cm[i & 3], v[i]);
-      const float mn = fmaxf(m, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])) * k);
+      top = fmaxf(top, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])));
+      const float mn = top * k;
       const float ref = mn == -INFINITY ? 0.f : mn;
       float p[4] = {0.f, 0.f, 0.f, 0.f};
+      if (fabsf(ref) <= 0x1p22f) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) p[i & 3] += ex2(fmaf(v[i], k, -ref));
+        for (int i = 0; i < 32; ++i) p[i & 3] += ex2(fmaf(v[i], k, -ref));
+      } else {  // mn's own rounding is a factor here, from 2^31 on any factor: the largest term has to be 1
+#pragma unroll
+        for (int i = 0; i < 32; ++i) p[i & 3] += ex2((v[i] - top) * k);
+      }
       sum = sum * ex2(m - ref) + ((p[0] + p[1]) + (p[2] + p[3]));
       m = mn;
     }
@@ -152,7 +161,12 @@ struct StatsEpi : NoSlabs {
   }
 };
 
-// One warp a row: the tiles' pairs joined, the loss.
+// One warp a row: the tiles' pairs joined, then the label's term with them.
+// With rest = s 2^top the others' sum, the loss without smoothing and penalty
+// is log(1 + rest / e^z): never below 0, and with its own size's accuracy
+// where the label holds nearly everything. It takes the label's better logit;
+// the log-sum-exp takes the product's, which is what the backward's products
+// make again: its p of the label then is e^0 where nothing else counts.
 __global__ void __launch_bounds__(256)
     join_rows_kernel(const float2* part, const float* sums, const float2* zlab, const int32_t* labels, int T, int V,
                      int parts, float scale, float smooth, float zc, float* loss, float* lse_out) {
@@ -178,16 +192,16 @@ __global__ void __launch_bounds__(256)
     m = mn;
     if (sums) plain += sums[(size_t)row * parts + i];
   }
-  const float top = warp_max(m), ref = top == -INFINITY ? 0.f : top;
-  s = warp_sum(s * ex2(m - ref));
+  const float top = warp_max(m);
+  s = warp_sum(s * ex2(m - (top == -INFINITY ? 0.f : top)));
   if (sums) plain = warp_sum(plain);
   if (lane == 0) {
-    // the label's term in the sum, then the label's logit, by its better value
     const float2 z = zlab[row];
-    s += ex2(z.y * kLog2e - ref) - ex2(z.x * kLog2e - ref);
-    const float lse = fmaf(top, kLn2, logf(s));
-    float l = lse - (1.f - smooth) * z.y;
-    if (sums) l -= smooth * (plain * scale / (float)V);
+    const float dx = fmaf(-kLog2e, z.x, top), dy = fmaf(-kLog2e, z.y, top);
+    const float lse = dx > 0.f ? fmaf(top, kLn2, logf(s + ex2(-dx))) : z.x + log1pf(s * ex2(dx));
+    float l = dy > 0.f ? fmaf(dy, kLn2, logf(s + ex2(-dy))) : log1pf(s * ex2(dy));
+    if (!(z.y < INFINITY)) l = z.y - z.y;  // not a number
+    if (sums) l += smooth * (z.y - plain * scale / (float)V);
     loss[row] = l + zc * lse * lse;
     lse_out[row] = lse;
   }
