@@ -629,7 +629,9 @@ int mt_op_linear_ce_fwd(const void* X, const void* W, const int32_t* labels, flo
  *   dX [T, h] = logit_scale dz W,  dW [V, h] = logit_scale dz^T X
  * (MT_F32 or MT_BF16 each, dense; either may be null: not wanted). dz is
  * rounded to bf16 once, the sums run in fp32 and are rounded once; p below
- * 2^-126 counts as 0.
+ * 2^-126 counts as 0, none counts as more than 1. The label's p is off by the
+ * rounding of lse, 2^-24 |lse|, and 2^-21: what dz of a label with p near 1
+ * has to be taken for beside its own rounding.
  * accumulate != 0: dW += that. Rows that are not scored, or whose label is V
  * or more, have dX = 0 and leave no trace in dW, whatever X and g_loss hold
  * there (dX: where W is finite). The vocabulary is worked off in pieces of up

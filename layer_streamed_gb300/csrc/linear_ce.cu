@@ -52,6 +52,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // Forward epilogue: per row and tile the maximum of z log2(e) and the sum of
 // 2^(. - maximum) over all columns but the label's; with smoothing the sum of
@@ -272,16 +278,23 @@ struct GradEpi : NoSlabs {
   }
   struct Row {
     int label;      // in the piece's columns
-    float lse2, cp, cl, c0;
+    float lse, lse2, cp, cl, c0;
     bool scored;
   };
+  // The label's dz. Its p - 1 may be all that is left of it, so p is formed
+  // from z - lse, which is exact where they are near each other; z is what the
+  // forward's log-sum-exp holds, the product's, rounded as it was there.
+  static __device__ __forceinline__ float at_label(const Row& r, float v, float scale) {
+    return fmaf(r.cp, ex2(min_nan((__fmul_rn(v, scale) - r.lse) * kLog2e, 0.f)), -r.c0) - r.cl;
+  }
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     const int y = at.row < s.M ? a.labels[at.row] : -1;
     r.scored = y >= 0 && y < a.V;
     r.label = r.scored ? y - a.v0 : -1;
-    const float g = r.scored ? a.g[at.row] : 0.f, lse = r.scored ? a.lse[at.row] : 0.f;
-    r.lse2 = lse * kLog2e;
-    r.cp = g * (1.f + 2.f * a.zc * lse);
+    const float g = r.scored ? a.g[at.row] : 0.f;
+    r.lse = r.scored ? a.lse[at.row] : 0.f;
+    r.lse2 = r.lse * kLog2e;
+    r.cp = g * (1.f + 2.f * a.zc * r.lse);
     r.cl = g * (1.f - a.smooth);
     r.c0 = g * a.smooth / (float)a.V;
   }
@@ -303,11 +316,24 @@ struct GradEpi : NoSlabs {
         const int c0 = j * 64 + half * 32;
         float v[32];
         tile_chunk(tb, 2 * j + half, v);
+        const bool label = here >= c0 && here < c0 + 32;
+        float y = 0.f;
+        if (label) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = r.scored ? fmaf(r.cp, ex2(fmaf(v[i], k, -r.lse2)), -r.c0) : 0.f;
-        if (here >= c0 && here < c0 + 32) {
+          for (int i = 0; i < 32; ++i) y = here == c0 + i ? v[i] : y;
+          y = at_label(r, y, a.scale);
+        }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] -= here == c0 + i ? r.cl : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], k, -r.lse2);
+        if (fabsf(r.lse2) > 0x1p18f) {  // the roundings of logits this large would pass for p above 1
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = min_nan(v[i], 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = r.scored ? fmaf(r.cp, ex2(v[i]), -r.c0) : 0.f;
+        if (label) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = here == c0 + i ? y : v[i];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -5,7 +5,7 @@ The gradients of the logits are read off dX: beside random columns W has an
 identity, X zeros there, so dX's columns there are dz itself (one term a sum)."""
 import pytest
 
-from tests.bounds import U32, check
+from tests.bounds import U16, U32, check
 from tests.gpu_util import need_gpu
 from tests.test_gpu_linear_ce import _case, _check, _reference, _run
 
@@ -67,6 +67,31 @@ def test_losses_of_confident_tokens(T, V, h, shift, e, c):
     check(n(r.lse), n(lse), n(2 * E + 8 * U32 * lse.abs()), "lse")
 
 
+@pytest.mark.parametrize("e,c", [(0.0, 0.0), (0.1, 1e-3)])
+@pytest.mark.parametrize("T,V,h", CONFIDENT)
+@pytest.mark.parametrize("shift", [0.0, -14.0, -30.0])
+def test_gradients_of_confident_tokens(T, V, h, shift, e, c):
+    """dz of the label keeps its own size's accuracy. q moves with the products' errors, 2 E of itself; beside that the
+    label's dz knows lse to a rounding (2^-24 of |lse|) and the hardware's exponential to 2^-22: nothing that grows with
+    h is left of p. dz is rounded to bf16."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _confident(torch, T, V, h, T + V, shift)
+    r = _run(torch, mt, X, W, labels, gl, 1.0, e, c, torch.float32, torch.float32)
+    z, at, zy, lse, p, q = _definition(torch, X, W, labels)
+    n = lambda t: t.double().cpu().numpy()  # noqa: E731
+    E = _logit_error(h)
+    k = 1 + 2 * c * lse
+    dz = p * k[:, None] - e / V
+    by_label = k - 1 + e - k * q - e / V  # k p - (1 - e) - e / V
+    dz = gl.double()[:, None] * dz.scatter(1, at, by_label[:, None])
+    pe = p * (2 * E + 8 * U32 * (lse.abs()[:, None] + z.abs()) + 2.0 ** -21)
+    pe = pe.scatter(1, at, (2 * E * q + 1.01 * U32 * lse.abs() + 2.0 ** -21)[:, None])
+    mag = p * k[:, None] + e / V + torch.zeros_like(p).scatter(1, at, 1 - e)
+    de = gl.double().abs()[:, None] * (k[:, None] * pe + (e > 0) * (8 * U32 + 4 * c * E) * mag)
+    check(n(r.dX[:, h - V:]), n(dz), n(U16 * dz.abs() + (1 + U16) * de + 1e-37), "dz")
+    assert mt.mt_op_device_error() == 0
+
+
 def _far(torch, V, sign, size, scale):
     """Logits of `size`: the label's is the largest by far, with sign -1 in every other row the lowest."""
     X, W, labels, gl = _case(torch, 400, V, 64, 77, spread=1.0)
@@ -89,6 +114,21 @@ def test_losses_of_logits_of_any_size(V, sign, size, scale):
     assert bool((r.loss >= 0).all())
     _check(torch, r, _reference(torch, X, W, labels, gl, scale, 0.0, 0.0, 64))
     assert V > 1 or not r.loss.any()
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.0, 30.0, 1e6])
+@pytest.mark.parametrize("size", [1e5, 1e6, 1e7, 1e8, 3e9, 1e13])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("V", [1, 2, 300])
+def test_gradients_of_logits_of_any_size(V, sign, size, scale):
+    """Probabilities of at most 1, whatever the sums' rounding."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _far(torch, V, sign, size, scale)
+    r = _run(torch, mt, X, W, labels, gl, scale, 0.0, 0.0, torch.float32, torch.float32)
+    most = 1.02 * scale * (V + 1) * gl.abs()[:, None] * W.float().abs().amax(0)[None]  # |dz_j| <= |g| (p_j + [label])
+    assert bool((r.dX.abs() <= most).all()) and torch.isfinite(r.dW).all()
+    assert V > 1 or not (r.dX.any() or r.dW.any())
+    assert mt.mt_op_device_error() == 0
 
 
 def test_one_infinite_logit():
