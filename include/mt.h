@@ -658,8 +658,9 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
  * arithmetic for the quintic's 5 or 6 steps before its own rounding. A zero
  * matrix (or one whose squares' sum is 0 in fp32) gives zeros, one with an
  * infinity or a NaN (or whose squares' sum passes fp32) NaN throughout; the
- * others of the batch are not touched by it. Singular values have to stay below 15 in every
- * step (fp16's range). Any rows and cols up to 2^16, batch up to 4096, steps
+ * others of the batch are not touched by it. Singular values have to stay
+ * below 15 before every step (fp16's range): past that a result may be
+ * infinite or NaN. Any rows and cols up to 2^16, batch up to 4096, steps
  * 1 to 32, |coef| up to 100, eps >= 0. workspace: bytes, 256-byte aligned (0
  * for sizes that are refused). O may be G where the types are the same.
  * Deterministic. */

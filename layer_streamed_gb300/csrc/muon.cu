@@ -11,7 +11,8 @@
 //
 // Numbers. The products' operands are fp16 with power-of-two scales (X 2^10,
 // the square matrices 2^8: fp16's normal range then covers them from 2^-24
-// and 2^-22 of their largest values up), the sums fp32. Two things keep an
+// and 2^-22 of their largest values up; B less where a step's coefficients can
+// take it past fp16, see b_scales), the sums fp32. Two things keep an
 // operand's rounding (2^-12) from being what the result is off by:
 //  - X itself is carried as two fp16 values, hi + lo (22 bits). Only hi is
 //    multiplied; a X is formed from both. Directions in which X is small grow
@@ -342,7 +343,7 @@ struct PolyEpi {
     const float* d;
     float* db;
     int64_t ld, dpad;
-    float b, c;
+    float b, c, undo;  // times B's scale / kAUp; its reciprocal, for the diagonal
   };
   struct Row {
     float d;
@@ -357,7 +358,7 @@ struct PolyEpi {
       float sq = 0.f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) sq = i == here ? v[i] : sq;
-      if (at.row < s.M) a.db[at.b * a.dpad + at.row] = r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown));
+      if (at.row < s.M) a.db[at.b * a.dpad + at.row] = (r.d * a.b + a.c * fmaf(r.d, r.d, sq * (kADown * kADown))) * a.undo;
     }
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -445,7 +446,7 @@ struct ApplyEpi {
     uint16_t *hi_out, *lo_out;  // lo_out is lo
     const float* db;
     int64_t ld, dpad;
-    float a;
+    float a, down;  // down: 1 / B's scale
     int by_col;  // the diagonal runs along the columns (X B) or the rows (B X)
     // LAST: out [M, N] dense per matrix, out <- keep * out - step * X with
     // update, else X; vec: 32 bytes of a row at a time
@@ -649,7 +650,7 @@ struct ApplyEpi {
       const float h[4] = {h0.x, h0.y, h1.x, h1.y}, l[4] = {l0.x, l0.y, l1.x, l1.y};
 #pragma unroll
       for (int f = 0; f < 4; ++f)
-        x[i + f] = fmaf(a.a + d[f], h[f], fmaf(fmaf(0.5f, d[f], a.a), l[f], x[i + f] * kADown));
+        x[i + f] = fmaf(a.a + d[f], h[f], fmaf(fmaf(0.5f, d[f], a.a), l[f], x[i + f] * a.down));
     }
   }
   static __device__ __forceinline__ void put16(const Args& a, const ProductShape& s, const TileAt& at, int col,
@@ -719,7 +720,7 @@ struct NarrowArgs {
   int g_bf16, nesterov, out_bf16, update, steps, tall;
   int m, n, cols;  // short and long side; columns as stored
   float mu, keep, step, eps;
-  float coef[96];
+  float coef[96], up[32], down[32];  // B's scale / kAUp, 1 / B's scale of each step
 };
 constexpr int kXBlock = 128 * 128;  // bytes of 64 columns of X, of 64 columns of a square matrix
 constexpr int kNarrowCols = 256;    // columns of X in a CTA
@@ -926,6 +927,7 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 #pragma unroll 1
   for (int step = 0; step < p.steps; ++step) {
     const float ca = p.coef[3 * step], cb = p.coef[3 * step + 1], cc = p.coef[3 * step + 2];
+    const float up = p.up[step], down = p.down[step];
     // A = X X^T, this CTA's columns
     sync();
     if (tid == 0) {
@@ -1029,7 +1031,7 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         if (col + i == row) dbs[row] = d * cb + cc * fmaf(d, d, v[i] * (kADown * kADown));
-        v[i] = col + i == row ? 0.f : fmaf(cc, fmaf(d + dg[col + i], o[i], v[i] * kADown), cb * o[i]);
+        v[i] = col + i == row ? 0.f : fmaf(cc * up, fmaf(d + dg[col + i], o[i], v[i] * kADown), cb * up * o[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -1059,7 +1061,7 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float h = h2f(f2h(x[i]));
-        x[i] = fmaf(ah, h, fmaf(al_, x[i] - h, v[i] * kADown));
+        x[i] = fmaf(ah, h, fmaf(al_, x[i] - h, v[i] * down));
       }
       if (!last) {
         keep_x(col, x);
@@ -1125,6 +1127,41 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 inline size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// The scale of B = b A + c A^2 in each step: 2^8, or the largest power of two
+// with which no value off B's diagonal can pass fp16. Such a value is at most
+// half of the range of q(t) = b t + c t^2 over A's eigenvalues t = s^2. The
+// singular values s begin below 1 and go through s (a + q(s^2)); past 15 the
+// matrices themselves leave fp16, so no bound beyond that is of use. (Muon's
+// quintic stays with 2^8; 5 X in one step and the quintic in the next has B up
+// to 575.)
+void b_scales(const float* coef, int steps, float* scale) {
+  double s = 1.01;  // roundings
+  for (int i = 0; i < steps; ++i) {
+    const double a = coef[3 * i], b = coef[3 * i + 1], c = coef[3 * i + 2], top = s * s;
+    auto q = [&](double t) { return (b + c * t) * t; };
+    double lo = std::min(0.0, q(top)), hi = std::max(0.0, q(top));
+    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < top) {
+      lo = std::min(lo, q(-b / (2.0 * c)));
+      hi = std::max(hi, q(-b / (2.0 * c)));
+    }
+    scale[i] = kAUp;
+    while ((hi - lo) * 0.5 * scale[i] > 60000.0) scale[i] *= 0.5f;
+    // |s (a + q(s^2))| is largest at the end or where a + 3 b t + 5 c t^2 = 0
+    double most = std::fabs(s * (a + q(top)));
+    auto at = [&](double t) {
+      if (t > 0.0 && t < top) most = std::max(most, std::fabs(std::sqrt(t) * (a + q(t))));
+    };
+    const double root = 9.0 * b * b - 20.0 * a * c;
+    if (c == 0.0) {
+      if (b != 0.0) at(-a / (3.0 * b));
+    } else if (root >= 0.0) {
+      at((-3.0 * b + std::sqrt(root)) / (10.0 * c));
+      at((-3.0 * b - std::sqrt(root)) / (10.0 * c));
+    }
+    s = std::min(15.0, 1.01 * most);
+  }
+}
 
 // Blocks that share the sum of a matrix's squares: one per 2048 values, as
 // many as eight on every SM.
@@ -1220,6 +1257,8 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
                   float keep, float step, const float* coef, int steps, float eps, void* work, int batch, int rows,
                   int cols, cudaStream_t st) {
   const int sides[2] = {std::min(rows, cols), std::max(rows, cols)};
+  float scale[32];
+  b_scales(coef, steps, scale);
   if (sides[0] <= 128 && sides[1] <= 16 * kNarrowCols) {
     NarrowArgs a{};
     a.G = G;
@@ -1239,6 +1278,10 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
     a.step = step;
     a.eps = eps;
     std::copy(coef, coef + 3 * steps, a.coef);
+    for (int i = 0; i < steps; ++i) {
+      a.up[i] = scale[i] * kADown;
+      a.down[i] = 1.f / scale[i];
+    }
     const int ctas = (sides[1] + kNarrowCols - 1) / kNarrowCols;
     return ctas == 1   ? launch_narrow<1>(a, batch, st)
            : ctas == 2 ? launch_narrow<2>(a, batch, st)
@@ -1284,7 +1327,9 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
     e = tall ? product<true, true, true, GramEpi>(x, x, m, m, rows, batch, ga, st)
              : product<false, false, true, GramEpi>(x, x, m, m, cols, batch, ga, st);
     if (e != cudaSuccess) break;
-    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, PolyEpi::Args{mO, mBT, O, B, d, db, w.lda, w.dpad, c[1], c[2]}, st);
+    const float f = scale[i] * kADown;
+    const PolyEpi::Args pa{mO, mBT, O, B, d, db, w.lda, w.dpad, c[1] * f, c[2] * f, 1.f / f};
+    e = product<false, false, true, PolyEpi>(o, o, m, m, m, batch, pa, st);
     if (e != cudaSuccess) break;
     auto apply = [&](auto epi) {
       using E = decltype(epi);
@@ -1298,6 +1343,7 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
       a.ld = w.ldx;
       a.dpad = w.dpad;
       a.a = c[0];
+      a.down = 1.f / scale[i];
       a.by_col = tall;
       a.out = out;
       a.out_bf16 = out_bf16;
