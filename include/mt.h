@@ -656,7 +656,7 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
  * operands with fp32 sums, with X carried in 22 bits: O is 0.4e-3 to 1.1e-3
  * (relative, Frobenius; up to 2e-3 for matrices of low rank) from exact
  * arithmetic for the quintic's 5 or 6 steps before its own rounding. A zero
- * matrix (or one whose squares' sum is 0 in fp32) gives zeros, one with an
+ * matrix (or one of values below 2e-41 throughout) gives zeros, one with an
  * infinity or a NaN (or whose squares' sum passes fp32) NaN throughout; the
  * others of the batch are not touched by it. Singular values have to stay
  * below 15 before every step (fp16's range): past that a result may be

@@ -83,26 +83,52 @@ __device__ __forceinline__ void load4(const void* p, size_t i, bool bf16, float 
   }
 }
 
-__device__ __forceinline__ float block_sum256(float v, float* red) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+// The sum of an update's squares, twice: as it is, and of values kSmall times
+// as large, which is what counts where squares end among fp32's subnormals or
+// below them.
+constexpr float kSmall = 0x1p60f;
+struct Squares {
+  float plain = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float u) {
+    plain = fmaf(u, u, plain);
+    small = fmaf(u * kSmall, u * kSmall, small);
+  }
+};
+__device__ __forceinline__ Squares block_sum256(Squares v, float2* red) {
+  v.plain = warp_sum(v.plain);
+  v.small = warp_sum(v.small);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.plain, v.small);
   __syncthreads();
-  v = threadIdx.x < 8 ? red[threadIdx.x] : 0.f;
-  return warp_sum(v);  // in warp 0
+  const float2 w = threadIdx.x < 8 ? red[threadIdx.x] : make_float2(0.f, 0.f);
+  v.plain = warp_sum(w.x);  // in warp 0
+  v.small = warp_sum(w.y);
+  return v;
+}
+// X is u * first * then for the values u of an update with these squares.
+// Nothing (a zero matrix) stays nothing whatever eps is; an infinite norm (or
+// a NaN) stands for NaN throughout. From 2^-60 on the plain sum's own losses,
+// 2^-126 a value, are far below its rounding.
+struct Factors {
+  float first, then;
+};
+__device__ __forceinline__ Factors factors(const Squares& s, float eps) {
+  if (s.plain < 0x1p-60f) return {kSmall, s.small > 0.f ? kXUp / (sqrtf(s.small) + eps * kSmall) : 0.f};
+  const float norm = sqrtf(s.plain) + eps;
+  return {1.f, norm < INFINITY ? kXUp / norm : __uint_as_float(0x7fffffffu)};
 }
 
 // M <- mu M + G where there is an M, and a block's part of the sum of U^2.
 // Block (x, y) takes every gridDim.x-th group of values of matrix y.
 template <bool VEC>
-__global__ void __launch_bounds__(256) momentum_kernel(const void* G, bool bf16, float* M, float mu, int nesterov,
-                                                       int64_t n, float* part) {
-  __shared__ float red[8];
+__global__ void __launch_bounds__(256, 5) momentum_kernel(const void* G, bool bf16, float* M, float mu, int nesterov,
+                                                       int64_t n, float2* part) {
+  __shared__ float2 red[8];
   grid_wait();
   grid_release();
   constexpr int E = VEC ? 4 : 1;
   const size_t base = (size_t)blockIdx.y * n;
   const int64_t step = (int64_t)gridDim.x * 256 * E;
-  float sum = 0.f;
+  Squares sum;
 #pragma unroll 4
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E; i < n; i += step) {
     float g[4], m[4];
@@ -120,10 +146,10 @@ __global__ void __launch_bounds__(256) momentum_kernel(const void* G, bool bf16,
       else M[base + i] = m[0];
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum = fmaf(g[e], g[e], sum);
+    for (int e = 0; e < E; ++e) sum.add(g[e]);
   }
   sum = block_sum256(sum, red);
-  if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+  if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = make_float2(sum.plain, sum.small);
 }
 
 // X = U / (|U| + eps) as hi + lo. VEC: rows are whole groups of eight values
@@ -131,22 +157,21 @@ __global__ void __launch_bounds__(256) momentum_kernel(const void* G, bool bf16,
 template <bool VEC>
 __global__ void __launch_bounds__(256)
     normalise_kernel(const void* G, bool bf16, const float* M, float mu, int nesterov, int rows, int cols, int64_t ld,
-                     const float* part, int parts, float eps, uint16_t* hi, uint16_t* lo) {
-  __shared__ float red[8];
-  __shared__ float inv_s;
+                     const float2* part, int parts, float eps, uint16_t* hi, uint16_t* lo) {
+  __shared__ float2 red[8];
+  __shared__ Factors all_threads;
   grid_wait();
   grid_release();
   const size_t b = blockIdx.y;
-  float s = 0.f;
-  for (int i = threadIdx.x; i < parts; i += 256) s += part[b * parts + i];
-  s = block_sum256(s, red);
-  if (threadIdx.x == 0) {
-    const float norm = sqrtf(s) + eps;
-    // a zero matrix stays zero; an infinite norm (or a NaN) stands for NaN throughout
-    inv_s = norm < INFINITY ? (norm > 0.f ? kXUp / norm : 0.f) : __uint_as_float(0x7fffffffu);
+  Squares s;
+  for (int i = threadIdx.x; i < parts; i += 256) {
+    s.plain += part[b * parts + i].x;
+    s.small += part[b * parts + i].y;
   }
+  s = block_sum256(s, red);
+  if (threadIdx.x == 0) all_threads = factors(s, eps);
   __syncthreads();
-  const float inv = inv_s;
+  const Factors f = all_threads;
   const size_t in0 = b * rows * (size_t)cols, out0 = b * rows * (size_t)ld;
   const int per_row = (cols + 7) / 8;
   const int64_t all = (int64_t)rows * per_row;
@@ -173,7 +198,7 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[e] *= inv;
+      v[e] = v[e] * f.first * f.then;
       l[e] = v[e] - h2f(f2h(v[e]));
     }
     const size_t o = out0 + (size_t)r * ld + c;
@@ -746,7 +771,8 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
   uint8_t* xh = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // 4 blocks of X
   uint8_t* sq = xh + 4 * kXBlock;                                             // 2 blocks of O, then of B
   uint8_t* ex = sq + 2 * kXBlock;                                             // the others' parts: [S][128 / S / 4][128] float4
-  __shared__ float dg[128], dbs[128], norms[S], red[16];
+  __shared__ float dg[128], dbs[128];
+  __shared__ float2 norms[S], red[16];
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -782,11 +808,11 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
   const bool vec_out = !p.tall && p.cols % 4 == 0 && ((uintptr_t)p.out & (p.out_bf16 ? 7 : 15)) == 0;
   auto at = [&](int j) { return mat + (p.tall ? (size_t)j * p.cols + row : (size_t)row * p.cols + j); };
 
-  // U into tensor memory, the sum of its squares. Rows on no boundary come a row
+  // U into tensor memory, the sums of its squares. Rows on no boundary come a row
   // at a time, a column a lane, and wait in shared memory (the blocks' place,
   // not yet in use; a row is 257 words, so that neither side meets a bank
   // twice). 100 x 1001: 54 us, and 78 value by value from the lanes' own rows.
-  float sum = 0.f;
+  Squares sum;
   float* rows = (float*)xh;
   constexpr int kRow = 257;
   const bool by_rows = !p.tall && !vec;
@@ -824,7 +850,7 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         u[i] = rows[row * kRow + col + i];
-        sum = fmaf(u[i], u[i], sum);
+        sum.add(u[i]);
       }
     } else if (row < p.m && col < mine) {
       float m[32];
@@ -859,30 +885,38 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
         }
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum = fmaf(u[i], u[i], sum);
+      for (int i = 0; i < 32; ++i) sum.add(u[i]);
     }
     put_chunk(tx + col, u);
   }
   tmem_st_wait();
-  sum = warp_sum(sum);
-  if (lane == 0) red[warp] = sum;
+  sum.plain = warp_sum(sum.plain);
+  sum.small = warp_sum(sum.small);
+  if (lane == 0) red[warp] = make_float2(sum.plain, sum.small);
   __syncthreads();
   if (tid < S) {
-    float s = 0.f;
-    for (int i = 0; i < 16; ++i) s += red[i];
+    Squares s;
+    for (int i = 0; i < 16; ++i) {
+      s.plain += red[i].x;
+      s.small += red[i].y;
+    }
     if (S > 1) {
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(&norms[rank], (uint32_t)tid)), "f"(s) : "memory");
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(&norms[rank], (uint32_t)tid)), "f"(s.plain),
+                   "f"(s.small)
+                   : "memory");
     } else {
-      norms[0] = s;
+      norms[0] = make_float2(s.plain, s.small);
     }
   }
   if (S > 1) cluster_sync();
   else __syncthreads();
-  sum = 0.f;
+  sum = Squares();
 #pragma unroll
-  for (int r = 0; r < S; ++r) sum += norms[r];
-  const float norm = sqrtf(sum) + p.eps;
-  const float inv = norm < INFINITY ? (norm > 0.f ? kXUp / norm : 0.f) : __uint_as_float(0x7fffffffu);
+  for (int r = 0; r < S; ++r) {
+    sum.plain += norms[r].x;
+    sum.small += norms[r].y;
+  }
+  const Factors f = factors(sum, p.eps);
 
   // X (times kXUp) to tensor memory, its fp16 copy to the blocks
   auto keep_x = [&](int col, float (&x)[32]) {
@@ -899,7 +933,7 @@ __global__ void __launch_bounds__(512, 1) narrow_kernel(const __grid_constant__ 
     tile_chunk(tx, part * 2 + c, x);
     // padding stays zero where the norm is not a number
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = row < p.m && col + i < mine ? x[i] * inv : 0.f;
+    for (int i = 0; i < 32; ++i) x[i] = row < p.m && col + i < mine ? x[i] * f.first * f.then : 0.f;
     keep_x(col, x);
   }
   tmem_st_wait();
@@ -1185,7 +1219,7 @@ Ws workspace(int batch, int rows, int cols) {
     at += up(n, 256);
     return r;
   };
-  w.part = take((size_t)batch * w.parts * 4);
+  w.part = take((size_t)batch * w.parts * 8);
   const size_t x = (size_t)batch * rows * w.ldx * 2, a = (size_t)batch * w.m * w.lda * 2;
   w.hi[0] = take(x);
   w.hi[1] = take(x);
@@ -1291,7 +1325,7 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
   }
   const Ws w = workspace(batch, rows, cols);
   uint8_t* base = (uint8_t*)work;
-  float* part = (float*)(base + w.part);
+  float2* part = (float2*)(base + w.part);
   uint16_t* hi[2] = {(uint16_t*)(base + w.hi[0]), (uint16_t*)(base + w.hi[1])};
   uint16_t *lo = (uint16_t*)(base + w.lo), *O = (uint16_t*)(base + w.o), *B = (uint16_t*)(base + w.b);
   float *d = (float*)(base + w.d), *db = (float*)(base + w.db);
@@ -1304,7 +1338,7 @@ int orthogonalize(const void* G, bool g_bf16, float* M, float mu, bool nesterov,
   const bool whole = cols % 8 == 0 && al(G, gs) && al(M, 16);
   if (e == cudaSuccess)
     e = mt_host::launch_early(whole ? normalise_kernel<true> : normalise_kernel<false>, pg, 256, 0, st, 1, G, g_bf16,
-                              (const float*)M, mu, (int)nesterov, rows, cols, w.ldx, (const float*)part, w.parts, eps,
+                              (const float*)M, mu, (int)nesterov, rows, cols, w.ldx, (const float2*)part, w.parts, eps,
                               hi[0], lo);
   count_launches(2);
   const bool tall = rows > cols;

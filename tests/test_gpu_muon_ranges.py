@@ -7,7 +7,7 @@ import pytest
 from tests import muon_ref as ref
 from tests.bounds import U32, check
 from tests.gpu_util import need_gpu
-from tests.test_gpu_muon import _matrix, _ortho
+from tests.test_gpu_muon import _check, _matrix, _ortho
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,30 @@ def test_past_the_limit_is_right_or_not_finite(b, rows, cols):
         G[0, 0, 0] = float("inf")
         after = _ortho(torch, mt, G, 2, mild)
         assert torch.equal(after[1:], before[1:]) and torch.isnan(after[0]).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1e-37, 1e-30, 1e-7, 1e30])
+@pytest.mark.parametrize("b,rows,cols", [(3, 20, 30), (2, 90, 1000), (3, 300, 200), (2, 140, 333)])
+def test_zero_matrices_are_zero_for_any_eps(b, rows, cols, eps):
+    torch, mt = need_gpu()
+    G = torch.zeros((b, rows, cols), device="cuda")
+    assert not _ortho(torch, mt, G, eps=eps).any()
+    W, M = torch.ones_like(G), torch.zeros_like(G)
+    ws = torch.empty(mt.mt_op_orthogonalize_workspace(b, rows, cols), dtype=torch.uint8, device="cuda")
+    mt.mt_op_muon_update(W, mt.MT_F32, M, G, mt.MT_F32, 0.9, 1, 0.5, 0.0, 1.0, None, 5, eps, ws, b, rows, cols)
+    assert bool((W == 1).all()) and not M.any()
+
+
+@pytest.mark.parametrize("size", [1e-18, 1e-20, 1e-22, 1e-26, 1e-32, 1e-35])
+@pytest.mark.parametrize("b,rows,cols", [(3, 20, 30), (2, 90, 1000), (2, 200, 60), (3, 300, 200), (2, 140, 333), (1, 257, 1024)])
+def test_small_updates_are_scaled_to_norm_one(b, rows, cols, size):
+    """Their squares lie among fp32's subnormals or below all of them."""
+    torch, mt = need_gpu()
+    G = _matrix(torch, "flat", b, rows, cols, 3) * size
+    _check(torch, _ortho(torch, mt, G), G)
+    Gb = G.bfloat16()
+    _check(torch, _ortho(torch, mt, Gb), Gb)
+    eps = float(np.float32(3 * size))
+    _check(torch, _ortho(torch, mt, G, eps=eps), G, eps=eps)
+    k = 2.0 ** 40
+    assert torch.equal(_ortho(torch, mt, G * k), _ortho(torch, mt, (G * k) * 2.0 ** 20))
