@@ -698,7 +698,7 @@ int mt_op_sandwich_norm_fwd(const float* x, const void* y, const void* gate, int
  * where gate is), dw_post, dw_pre fp32 [h] (fixed-order sums; workspace fp32
  * of mt_op_sandwich_norm_bwd_workspace(T, h) floats, 0 for sizes that are
  * refused, 16-byte aligned). x_out, rstd_post and rstd_pre as the forward left
- * them. A sigmoid below 2^-126 counts as 0. Deterministic. */
+ * them. A sigmoid, or 1 - sigmoid, below 2^-126 counts as 0. Deterministic. */
 size_t mt_op_sandwich_norm_bwd_workspace(int T, int h);
 int mt_op_sandwich_norm_bwd(const float* x_out, const void* y, const void* gate, int y_dtype, const float* w_post,
                             const float* w_pre, float alpha, const float* rstd_post, const float* rstd_pre,

@@ -24,9 +24,17 @@ MT_DEVICE_ERROR_READER(sandwich_norm_take_device_error)
 namespace {
 
 // sigmoid by the hardware's exponential and reciprocal; below 2^-126 it is 0
-__device__ __forceinline__ float sigmoid(float s) {
+__device__ __forceinline__ float sigmoid_of(float e) {  // e = e^-s
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-s)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+__device__ __forceinline__ float sigmoid(float s) { return sigmoid_of(__expf(-s)); }
+// and 1 - sigmoid, from the exponential where it is the small one of the two
+// (the difference of 1 and a rounded sigmoid is 0 from s = 17 on)
+__device__ __forceinline__ float sigmoid(float s, float& rest) {
+  const float e = __expf(-s), r = sigmoid_of(e);
+  rest = e <= 1.f ? e * r : 1.f - r;
   return r;
 }
 
@@ -283,12 +291,12 @@ __global__ void __launch_bounds__(THREADS)
         float4 yh = value4<BF16>(yr[j]);
         yh.x *= ra, yh.y *= ra, yh.z *= ra, yh.w *= ra;
         if (GATE) {
-          float4 s = value4<BF16>(sr[j]);
-          s = make_float4(sigmoid(s.x), sigmoid(s.y), sigmoid(s.z), sigmoid(s.w));
+          float4 s = value4<BF16>(sr[j]), c;
+          s = make_float4(sigmoid(s.x, c.x), sigmoid(s.y, c.y), sigmoid(s.z, c.z), sigmoid(s.w, c.w));
           const float4 k = make_float4(d.x * s.x, d.y * s.y, d.z * s.z, d.w * s.w);
           put4<BF16>(row_of<BF16>(dgate, t, h), i,
-                     make_float4(k.x * (yh.x * wa[j].x) * (1.f - s.x), k.y * (yh.y * wa[j].y) * (1.f - s.y),
-                                 k.z * (yh.z * wa[j].z) * (1.f - s.z), k.w * (yh.w * wa[j].w) * (1.f - s.w)));
+                     make_float4(k.x * (yh.x * wa[j].x) * c.x, k.y * (yh.y * wa[j].y) * c.y,
+                                 k.z * (yh.z * wa[j].z) * c.z, k.w * (yh.w * wa[j].w) * c.w));
           d = k;
         }
         acc_post[j].x += d.x * yh.x, acc_post[j].y += d.y * yh.y, acc_post[j].z += d.z * yh.z, acc_post[j].w += d.w * yh.w;

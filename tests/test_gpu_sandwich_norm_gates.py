@@ -1,0 +1,35 @@
+"""The gate's gradient at open and closed gates relative to its own size."""
+import pytest
+
+from tests.bounds import U16, U32, acc, check
+from tests.gpu_util import from_dev, need_gpu
+from tests.test_gpu_sandwich_norm import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,h", [(170, 256), (40, 4096), (33, 5636), (21, 8192)])
+def test_gate_gradients_keep_their_own_size(T, h, bf16):
+    """dgate = d u s (1 - s) for gates from -80 to 80: s and 1 - s are each e^-|gate| where they are small, whose relative
+    error is the exponential's (2^-22, and its argument's rounding, |gate| 2^-23) and the reciprocal's."""
+    torch, mt = need_gpu()
+    c = Case(torch, T, h, bf16, True, T + h)
+    c.gate = torch.linspace(-80, 80, T * h, device="cuda")[torch.randperm(T * h, device="cuda")].view(T, h).to(c.dt)
+    r = c.run(mt)
+    f = lambda t: t.double()  # noqa: E731
+    xo, ra, rb, y, s = f(r.x_out), f(r.ra)[:, None], f(r.rb)[:, None], f(c.y), f(c.gate)
+    u = y * ra * f(c.wa)
+    xh = xo * rb
+    g = f(c.dn) * f(c.wb)
+    prod = g * xh
+    mb = prod.mean(1, keepdim=True)
+    d = rb * (g - xh * mb) + f(c.dres)
+    de = rb * (6 * U32 * (g.abs() + (xh * mb).abs()) + xh.abs() * (acc(h) + 8 * U32) * prod.abs().mean(1, keepdim=True)) \
+        + 2 * U32 * (d.abs() + f(c.dres).abs())
+    ss = torch.sigmoid(s) * torch.sigmoid(-s)
+    want = d * u * ss
+    rel = 16 * U32 + 4 * U32 * s.abs()
+    e = (de * u.abs() + (rel + 8 * U32) * (d * u).abs()) * ss
+    n = lambda t: t.cpu().numpy()  # noqa: E731
+    check(from_dev(r.ds), n(want), n(e + (U16 if bf16 else U32) * (want.abs() + e) + 1e-37), "dgate")
