@@ -687,7 +687,8 @@ int mt_op_muon_update(void* W, int w_dtype, float* M, const void* G, int g_dtype
  *   n_out = bf16(w_pre * x_out * rstd_pre),                      rstd_pre = 1/sqrt(mean(x_out^2) + eps)
  * x_out fp32 [T, h] (may be x), n_out bf16 [T, h], rstd_post, rstd_pre fp32 [T],
  * w_post, w_pre fp32 [h]. h a multiple of 4 up to 8192, T up to 2^30, eps >= 0
- * (with 0, rows of zeros are NaN).
+ * (with 0, rows of zeros are NaN). A row's bits do not depend on T or on the
+ * other rows, here and in dx, dy and dgate below.
  * fp32 arrays 16-byte aligned (rstd and the weights' gradients 4), bf16 ones 8. */
 int mt_op_sandwich_norm_fwd(const float* x, const void* y, const void* gate, int y_dtype, const float* w_post,
                             const float* w_pre, float alpha, float eps, float* x_out, void* n_out, float* rstd_post,

@@ -81,6 +81,23 @@ __device__ __forceinline__ float block_sum(float v, float* red, int nw) {
   return warp_sum((threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f);
 }
 
+__device__ __forceinline__ float squares(float4 v) {
+  return fmaf(v.w, v.w, fmaf(v.z, v.z, fmaf(v.y, v.y, v.x * v.x)));
+}
+// The sum over a row of a thread's G sums. Each goes through its warp by
+// itself: with one group a thread or two, up to 32 warps' worth of groups are
+// added up in the same order, so that a row's bits do not depend on which.
+template <int G>
+__device__ __forceinline__ float row_sum(const float (&v)[G], float* red, int nw) {
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const float s = warp_sum(v[j]);
+    if ((threadIdx.x & 31) == 0) red[j * nw + (threadIdx.x >> 5)] = s;
+  }
+  __syncthreads();
+  return warp_sum((threadIdx.x & 31) < G * nw ? red[threadIdx.x & 31] : 0.f);
+}
+
 // One block a row, the row in registers: V groups of four values a thread.
 // 8192 x 4096, bf16 y and gate (floor 70.3 us): V = 2 70.1 us, V = 1 89.7,
 // V = 4 81.2. Wider rows take V = 4, with a bf16 gate three blocks an
@@ -107,16 +124,14 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && GATE && BF16 ? 
       xv[j] = ((const float4*)(x + t * h))[i];
     }
   }
-  float sum = 0.f;
+  constexpr int G = V > 2 ? 1 : V;
+  float sum[G] = {};
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (tid + j * NT < n4) {
-      const float4 v = value4<BF16>(yr[j]);
-      sum += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
-    }
-  }
-  const float ra = rsqrtf(block_sum(sum, red[0], nw) * inv_h + eps);
-  sum = 0.f;
+  for (int j = 0; j < V; ++j)
+    if (tid + j * NT < n4) sum[j % G] += squares(value4<BF16>(yr[j]));
+  const float ra = rsqrtf(row_sum(sum, red[0], nw) * inv_h + eps);
+#pragma unroll
+  for (int j = 0; j < G; ++j) sum[j] = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = tid + j * NT;
@@ -130,10 +145,10 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && GATE && BF16 ? 
       float4& o = xv[j];
       o.x = fmaf(alpha, o.x, u.x), o.y = fmaf(alpha, o.y, u.y), o.z = fmaf(alpha, o.z, u.z), o.w = fmaf(alpha, o.w, u.w);
       ((float4*)(x_out + t * h))[i] = o;
-      sum += o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w;
+      sum[j % G] += squares(o);
     }
   }
-  const float rb = rsqrtf(block_sum(sum, red[1], nw) * inv_h + eps);
+  const float rb = rsqrtf(row_sum(sum, red[1], nw) * inv_h + eps);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = tid + j * NT;

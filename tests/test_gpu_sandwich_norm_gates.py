@@ -1,4 +1,5 @@
-"""The gate's gradient at open and closed gates relative to its own size."""
+"""The gate's gradient at open and closed gates relative to its own size, and
+rows whose bits do not depend on how many there are."""
 import pytest
 
 from tests.bounds import U16, U32, acc, check
@@ -33,3 +34,23 @@ def test_gate_gradients_keep_their_own_size(T, h, bf16):
     e = (de * u.abs() + (rel + 8 * U32) * (d * u).abs()) * ss
     n = lambda t: t.cpu().numpy()  # noqa: E731
     check(from_dev(r.ds), n(want), n(e + (U16 if bf16 else U32) * (want.abs() + e) + 1e-37), "dgate")
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("h", [4, 36, 260, 1024, 1028, 2052, 4092, 4096, 5636, 8192])
+def test_a_rows_bits_do_not_depend_on_the_others(h, gate, bf16):
+    torch, mt = need_gpu()
+    T = 700
+    c = Case(torch, T, h, bf16, gate, h)
+    code = mt.MT_BF16 if bf16 else mt.MT_F32
+
+    def fwd(t):
+        xo, n, ra, rb = torch.empty_like(c.x[:t]), torch.empty((t, h), device="cuda", dtype=torch.bfloat16), *torch.empty((2, t), device="cuda")
+        mt.mt_op_sandwich_norm_fwd(c.x, c.y, c.gate, code, c.wa, c.wb, c.alpha, c.eps, xo, n, ra, rb, t, h)
+        return xo, n, ra, rb
+
+    full = fwd(T)
+    for t in (1, 33, 304, 305):
+        for a, b in zip(fwd(t), full):
+            assert torch.equal(a, b[:t]), t
