@@ -20,6 +20,7 @@
 // hold; dW is made from a copy of X in which they are zero, since 0 times an
 // infinity or a NaN would reach every row of it.
 #include <algorithm>
+#include <type_traits>
 
 #include "tile_product.cuh"
 
@@ -58,11 +59,57 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// The label's logits of R tokens side by side, x and w their rows (x null:
+// none), U pieces of a row asked for together: sums in fp32, h / 32 terms a
+// lane and then a tree, the same bits wherever they are made. The tensor core's
+// long sums come out a few 2^-24 of their terms short, 1.6e-6 of a loss at h =
+// 4096, and the label's own is most of what counts of that: where its
+// probability is high, in the log-sum-exp, and then in dz = p - 1. So both
+// directions take it from here, and the products' column of the label is not
+// used. By the epilogue's warps, while products run.
+template <int R, int U>
+__device__ __forceinline__ void label_logits(const uint16_t* const (&x)[R], const uint16_t* const (&w)[R], int h,
+                                             float scale, float (&z)[R]) {
+  const int n8 = h >> 3;
+  float z0[R] = {}, z1[R] = {};
+#pragma unroll 1
+  for (int i0 = (int)lane_id(); i0 - (int)lane_id() < n8; i0 += 32 * U) {
+    uint4 p[R][U], q[R][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        p[r][u] = q[r][u] = make_uint4(0, 0, 0, 0);
+        if (x[r] && i0 + 32 * u < n8) {
+          p[r][u] = ((const uint4*)x[r])[i0 + 32 * u];
+          q[r][u] = ((const uint4*)w[r])[i0 + 32 * u];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t ps[4] = {p[r][u].x, p[r][u].y, p[r][u].z, p[r][u].w},
+                       qs[4] = {q[r][u].x, q[r][u].y, q[r][u].z, q[r][u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z0[r] = fmaf(bf2f(ps[e] & 0xffff), bf2f(qs[e] & 0xffff), z0[r]);
+          z1[r] = fmaf(bf2f(ps[e] >> 16), bf2f(qs[e] >> 16), z1[r]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < R; ++r) z[r] = __fmul_rn(warp_sum(z0[r] + z1[r]), scale);
+}
+
 // ---------------------------------------------------------------------------
 // Forward epilogue: per row and tile the maximum of z log2(e) and the sum of
 // 2^(. - maximum) over all columns but the label's; with smoothing the sum of
-// the accumulators too; the label's own logit. The label's term joins the
-// others' sum last (join_rows_kernel), so that nothing is ever taken out of a sum.
+// the accumulators too. The label's term joins the others' sum last
+// (join_rows_kernel).
 // ---------------------------------------------------------------------------
 // Two warps a row of a tile, half of the columns each, hide each other's
 // latencies: with one, 8 us a tile of 256 x 256 against 4.2 us of MMAs at h = 1024.
@@ -72,36 +119,19 @@ struct StatsEpi : NoSlabs {
     const int32_t* labels;
     float2* part;  // [M][2 num_n]
     float* sums;   // [M][2 num_n] or null
-    float2* zlab;  // [M]: the label's logit as the product has it, and as begin() does
+    float* zlab;   // [M]: the label's logit
     float scale;
     const uint16_t *X, *W;
     int64_t ldx, ldw;
     int T, V, h;
   };
-  // The label's logit again, in fp32 (a sum of h / 32 terms a lane, then a
-  // tree): the tensor core's long sums come out a few 2^-24 of their terms
-  // short, 1.6e-6 of the loss at h = 4096, and the label's own is most of what
-  // counts of that. By the epilogue's warps, idle until the first tile is there.
   static __device__ __forceinline__ void begin(const Args& a, int warp) {
-    const int lane = (int)lane_id(), n8 = a.h >> 3;
     for (int t = (int)blockIdx.x * WARPS + warp; t < a.T; t += (int)gridDim.x * WARPS) {
       const int y = a.labels[t];
       if (y < 0 || y >= a.V) continue;
-      const uint4* x = (const uint4*)(a.X + t * a.ldx);
-      const uint4* w = (const uint4*)(a.W + y * a.ldw);
-      float z0 = 0.f, z1 = 0.f;
-#pragma unroll 4
-      for (int i = lane; i < n8; i += 32) {
-        const uint4 p = x[i], q = w[i];
-        const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z0 = fmaf(bf2f(ps[e] & 0xffff), bf2f(qs[e] & 0xffff), z0);
-          z1 = fmaf(bf2f(ps[e] >> 16), bf2f(qs[e] >> 16), z1);
-        }
-      }
-      const float z = warp_sum(z0 + z1);
-      if (lane == 0) a.zlab[t].y = z * a.scale;
+      float z[1];
+      label_logits<1, 4>({a.X + t * a.ldx}, {a.W + y * a.ldw}, a.h, a.scale, z);
+      if (lane_id() == 0) a.zlab[t] = z[0];
     }
   }
   struct Row {
@@ -110,32 +140,30 @@ struct StatsEpi : NoSlabs {
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     r.label = at.row < s.M ? max(a.labels[at.row], -1) : -1;
   }
-  template <int BN>
-  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              EpiWarp& w, uint32_t tb) {
-    if (at.row0 >= s.M) return;
+  // This warp's share of the columns: m = max v k, the sum of 2^(v k - m) and
+  // (FAR = false, with sums) that of v. m is rounded, which is a factor of the
+  // sum that goes with it; FAR, for logits so large that the factor could leave
+  // fp32, takes the exponents from differences to the maximum itself.
+  template <int BN, bool FAR>
+  static __device__ __forceinline__ void scan(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              const EpiWarp& w, uint32_t tb, float& m_out, float& sum_out, float& plain) {
     const float k = a.scale * kLog2e;
-    float top = -INFINITY, m = -INFINITY, sum = 0.f, plain = 0.f;  // m = top k
+    float top = -INFINITY, m = -INFINITY, sum = 0.f;
     const int here = r.label - at.n0;  // the label's column in this tile, if it is one
 #pragma unroll 1
     for (int c = w.part * (BN / 64); c < (w.part + 1) * (BN / 64); ++c) {
       if (at.n0 + c * 32 >= s.N) break;  // the same in every lane
       float v[32];
       tile_chunk(tb, c, v);
-      if (a.sums) {
+      if (!FAR && a.sums) {
         float p[4] = {0.f, 0.f, 0.f, 0.f};  // columns past N hold zeros
 #pragma unroll
         for (int i = 0; i < 32; ++i) p[i & 3] += v[i];
         plain += (p[0] + p[1]) + (p[2] + p[3]);
       }
       if (here >= c * 32 && here < c * 32 + 32) {
-        float z = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          z = here == c * 32 + i ? v[i] : z;
-          v[i] = here == c * 32 + i ? -INFINITY : v[i];
-        }
-        a.zlab[at.row].x = z * a.scale;
+        for (int i = 0; i < 32; ++i) v[i] = here == c * 32 + i ? -INFINITY : v[i];
       }
       if (at.n0 + c * 32 + 32 > s.N) {
 #pragma unroll
@@ -145,19 +173,31 @@ struct StatsEpi : NoSlabs {
       float cm[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
       for (int i = 4; i < 32; ++i) cm[i & 3] = fmaxf(cm[i & 3], v[i]);
-      top = fmaxf(top, fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3])));
-      const float mn = top * k;
-      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float here_top = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
+      if (FAR) top = fmaxf(top, here_top);
+      const float mn = FAR ? top * k : fmaxf(m, here_top * k);
+      const float ref = mn == -INFINITY ? 0.f : mn, from = top == -INFINITY ? 0.f : top;
       float p[4] = {0.f, 0.f, 0.f, 0.f};
-      if (fabsf(ref) <= 0x1p22f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) p[i & 3] += ex2(fmaf(v[i], k, -ref));
-      } else {  // mn's own rounding is a factor here, from 2^31 on any factor: the largest term has to be 1
-#pragma unroll
-        for (int i = 0; i < 32; ++i) p[i & 3] += ex2((v[i] - top) * k);
-      }
+      for (int i = 0; i < 32; ++i) p[i & 3] += ex2(FAR ? (v[i] - from) * k : fmaf(v[i], k, -ref));
       sum = sum * ex2(m - ref) + ((p[0] + p[1]) + (p[2] + p[3]));
       m = mn;
+    }
+    m_out = m;
+    sum_out = sum;
+  }
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
+    float m, sum, plain = 0.f;
+    scan<BN, false>(a, s, at, r, w, tb, m, sum, plain);
+    const bool far = fabsf(m) > 0x1p22f && m != -INFINITY;
+    if (__any_sync(0xffffffffu, far)) {
+      float m2, sum2;
+      scan<BN, true>(a, s, at, r, w, tb, m2, sum2, plain);
+      m = far ? m2 : m;
+      sum = far ? sum2 : sum;
     }
     if (at.row < s.M) {
       const size_t o = (size_t)at.row * (2 * s.num_n) + 2 * at.nb + w.part;
@@ -170,11 +210,9 @@ struct StatsEpi : NoSlabs {
 // One warp a row: the tiles' pairs joined, then the label's term with them.
 // With rest = s 2^top the others' sum, the loss without smoothing and penalty
 // is log(1 + rest / e^z): never below 0, and with its own size's accuracy
-// where the label holds nearly everything. It takes the label's better logit;
-// the log-sum-exp takes the product's, which is what the backward's products
-// make again: its p of the label then is e^0 where nothing else counts.
+// where the label holds nearly everything.
 __global__ void __launch_bounds__(256)
-    join_rows_kernel(const float2* part, const float* sums, const float2* zlab, const int32_t* labels, int T, int V,
+    join_rows_kernel(const float2* part, const float* sums, const float* zlab, const int32_t* labels, int T, int V,
                      int parts, float scale, float smooth, float zc, float* loss, float* lse_out) {
   grid_wait();
   grid_release();
@@ -202,12 +240,15 @@ __global__ void __launch_bounds__(256)
   s = warp_sum(s * ex2(m - (top == -INFINITY ? 0.f : top)));
   if (sums) plain = warp_sum(plain);
   if (lane == 0) {
-    const float2 z = zlab[row];
-    const float dx = fmaf(-kLog2e, z.x, top), dy = fmaf(-kLog2e, z.y, top);
-    const float lse = dx > 0.f ? fmaf(top, kLn2, logf(s + ex2(-dx))) : z.x + log1pf(s * ex2(dx));
-    float l = dy > 0.f ? fmaf(dy, kLn2, logf(s + ex2(-dy))) : log1pf(s * ex2(dy));
-    if (!(z.y < INFINITY)) l = z.y - z.y;  // not a number
-    if (sums) l += smooth * (z.y - plain * scale / (float)V);
+    const float z = zlab[row], d = fmaf(-kLog2e, z, top);
+    const bool over = d > 0.f;
+    // log(1 + r) of small r as log(u) r / (u - 1), u = 1 + r as rounded (Kahan's)
+    const float r = s * ex2(over ? 0.f : d), u = over ? s + ex2(-d) : 1.f + r, lg = logf(u);
+    const float more = over ? lg : u == 1.f ? r : lg * __fdividef(r, u - 1.f);
+    const float lse = over ? fmaf(top, kLn2, lg) : z + more;
+    float l = over ? fmaf(d, kLn2, lg) : more;
+    if (!(z < INFINITY)) l = z - z;  // not a number
+    if (sums) l += smooth * (z - plain * scale / (float)V);
     loss[row] = l + zc * lse * lse;
     lse_out[row] = lse;
   }
@@ -249,6 +290,7 @@ __device__ __forceinline__ void store8(void* base, size_t at, bool bf16, const f
 struct GradEpi : NoSlabs {
   static constexpr int kSlab = 4096;
   static constexpr int WARPS = 8, SLABS = kSlab;
+  static constexpr float kFar = 0x1p18f;
   struct Args {
     CUtensorMap dz;
     const int32_t* labels;
@@ -258,7 +300,8 @@ struct GradEpi : NoSlabs {
     // with the first piece: X with the rows that are not scored set to zero
     const uint16_t* X;
     uint16_t* xs;  // null: not wanted
-    int64_t ldx;
+    const uint16_t* W;  // the piece's rows
+    int64_t ldx, ldw;
     int T, h;
   };
   // The copy of X is made by the epilogue's warps, which have nothing to do
@@ -277,32 +320,54 @@ struct GradEpi : NoSlabs {
     }
   }
   struct Row {
-    int label;      // in the piece's columns
-    float lse, lse2, cp, cl, c0;
+    int label;  // in the piece's columns
+    float lse2, cp, c0, dz;  // dz: the label's
     bool scored;
   };
-  // The label's dz. Its p - 1 may be all that is left of it, so p is formed
-  // from z - lse, which is exact where they are near each other; z is what the
-  // forward's log-sum-exp holds, the product's, rounded as it was there.
-  static __device__ __forceinline__ float at_label(const Row& r, float v, float scale) {
-    return fmaf(r.cp, ex2(min_nan((__fmul_rn(v, scale) - r.lse) * kLog2e, 0.f)), -r.c0) - r.cl;
-  }
+  // The label's dz is made before its tile is there, by the warp whose columns
+  // hold it (a row in V / 128 of them), from z - lse, which is exact where they
+  // are near each other: its p - 1 may be all that is left of it. (Nothing to be
+  // seen at vocabularies of 32000 and h of 1024 up, 2 % at h = 256; where every
+  // row's label is in the one tile there is, V 256, 16384 tokens, 13 to 15 %,
+  // which a launch of its own for all rows takes as well: 7 tokens, V 32000,
+  // then 51.7 us, so 47.4.)
   static __device__ __forceinline__ void load_row(const Args& a, const ProductShape& s, const TileAt& at, Row& r) {
     const int y = at.row < s.M ? a.labels[at.row] : -1;
     r.scored = y >= 0 && y < a.V;
     r.label = r.scored ? y - a.v0 : -1;
-    const float g = r.scored ? a.g[at.row] : 0.f;
-    r.lse = r.scored ? a.lse[at.row] : 0.f;
-    r.lse2 = r.lse * kLog2e;
-    r.cp = g * (1.f + 2.f * a.zc * r.lse);
-    r.cl = g * (1.f - a.smooth);
+    const float g = r.scored ? a.g[at.row] : 0.f, lse = r.scored ? a.lse[at.row] : 0.f;
+    r.lse2 = lse * kLog2e;
+    r.cp = g * (1.f + 2.f * a.zc * lse);
     r.c0 = g * a.smooth / (float)a.V;
+    r.dz = 0.f;
+    const int half = at.width / 2, c = r.label - at.n0 - ((int)(warp_id() - 2) >> 2) * half;
+    const int lane = (int)lane_id();
+    uint32_t left = __ballot_sync(0xffffffffu, c >= 0 && c < half && r.label < s.N);
+    auto next = [&](auto rows) {  // the next rows of those left
+      constexpr int R = decltype(rows)::value;
+      const uint16_t *x[R], *w[R];
+      int l[R];
+      float z[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        l[k] = left ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+        x[k] = l[k] < 0 ? nullptr : a.X + (at.row0 + l[k]) * a.ldx;
+        w[k] = a.W + __shfl_sync(0xffffffffu, r.label, max(l[k], 0)) * (l[k] < 0 ? 0 : a.ldw);
+      }
+      label_logits<R, 8 / R>(x, w, a.h, a.scale, z);
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (lane == l[k]) r.dz = fmaf(r.cp, ex2(min_nan((z[k] - lse) * kLog2e, 0.f)), -r.c0) - g * (1.f - a.smooth);
+    };
+    while (left & (left - 1)) next(std::integral_constant<int, 4>());
+    if (left) next(std::integral_constant<int, 1>());
   }
-  template <int BN>
-  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
-                                              EpiWarp& w, uint32_t tb) {
-    if (at.row0 >= s.M) return;
-    const float k = a.scale * kLog2e;
+  // FAR: some row's logits are so large that their roundings would pass for p above 1
+  template <int BN, bool FAR>
+  static __device__ __forceinline__ void write(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                               EpiWarp& w, uint32_t tb) {
+    const float k = a.scale * kLog2e, most = fabsf(r.lse2) > kFar ? 0.f : INFINITY;
     const int here = r.label - at.n0;
 #pragma unroll 1
     for (int j = w.part * (BN / 128); j < (w.part + 1) * (BN / 128); ++j) {
@@ -316,24 +381,14 @@ struct GradEpi : NoSlabs {
         const int c0 = j * 64 + half * 32;
         float v[32];
         tile_chunk(tb, 2 * j + half, v);
-        const bool label = here >= c0 && here < c0 + 32;
-        float y = 0.f;
-        if (label) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y = here == c0 + i ? v[i] : y;
-          y = at_label(r, y, a.scale);
+        for (int i = 0; i < 32; ++i) {
+          const float e = fmaf(v[i], k, -r.lse2);
+          v[i] = r.scored ? fmaf(r.cp, ex2(FAR ? min_nan(e, most) : e), -r.c0) : 0.f;
         }
+        if (here >= c0 && here < c0 + 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], k, -r.lse2);
-        if (fabsf(r.lse2) > 0x1p18f) {  // the roundings of logits this large would pass for p above 1
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = min_nan(v[i], 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = r.scored ? fmaf(r.cp, ex2(v[i]), -r.c0) : 0.f;
-        if (label) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = here == c0 + i ? y : v[i];
+          for (int i = 0; i < 32; ++i) v[i] = here == c0 + i ? r.dz : v[i];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -348,6 +403,13 @@ struct GradEpi : NoSlabs {
         bulk_store_commit();
       }
     }
+  }
+  template <int BN>
+  static __device__ __forceinline__ void tile(const Args& a, const ProductShape& s, const TileAt& at, const Row& r,
+                                              EpiWarp& w, uint32_t tb) {
+    if (at.row0 >= s.M) return;
+    if (__any_sync(0xffffffffu, fabsf(r.lse2) > kFar)) write<BN, true>(a, s, at, r, w, tb);
+    else write<BN, false>(a, s, at, r, w, tb);
   }
 };
 
@@ -589,7 +651,7 @@ bool linear_ce_dims(int T, int V, int h) {
 
 size_t linear_ce_fwd_workspace(int T, int V) {
   const size_t n = (size_t)T * (2 * ((V + 127) / 128));
-  return up(n * 8, 256) + up(n * 4, 256) + up((size_t)T * 8, 256);
+  return up(n * 8, 256) + up(n * 4, 256) + up((size_t)T * 4, 256);
 }
 size_t linear_ce_bwd_workspace(int T, int V, int h) { return bwd_ws(T, V, h).total; }
 
@@ -600,7 +662,7 @@ int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   a.labels = labels;
   a.part = (float2*)work;
   a.sums = smooth != 0.f ? (float*)((uint8_t*)work + up(n * 8, 256)) : nullptr;
-  a.zlab = (float2*)((uint8_t*)work + up(n * 8, 256) + up(n * 4, 256));
+  a.zlab = (float*)((uint8_t*)work + up(n * 8, 256) + up(n * 4, 256));
   a.scale = scale;
   a.X = X;
   a.W = W;
@@ -613,7 +675,7 @@ int linear_ce_fwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
   if (e != cudaSuccess) return kLaunchFailed;
   const int parts = 2 * (wide(T, V, h) ? (V + 255) / 256 : (V + 127) / 128);
   e = mt_host::launch_early(join_rows_kernel, (T + 7) / 8, 256, 0, st, 1, (const float2*)a.part, (const float*)a.sums,
-                            (const float2*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
+                            (const float*)a.zlab, labels, T, V, parts, scale, smooth, zc, loss, lse);
   count_launches(1);
   return e == cudaSuccess ? 0 : kLaunchFailed;
 }
@@ -643,7 +705,9 @@ int linear_ce_bwd(const uint16_t* X, const uint16_t* W, const int32_t* labels, f
     a.zc = zc;
     a.X = X;
     a.xs = dW && v0 == 0 ? xs : nullptr;
+    a.W = Wp;
     a.ldx = ldx;
+    a.ldw = ldw;
     a.T = T;
     a.h = h;
     e = product<false, false, GradEpi>(X, ldx, Wp, ldw, T, n, h, a, st);

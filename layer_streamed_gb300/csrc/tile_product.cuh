@@ -72,9 +72,9 @@ struct ProductSmem {
 };
 
 // What an epilogue knows of its tile: this lane's row of D, the warp's first
-// row, the tile's first column and its matrix.
+// row, the tile's first column, its columns and its matrix.
 struct TileAt {
-  int row, row0, n0, nb, b;
+  int row, row0, n0, width, nb, b;
   bool mirror;  // SYM: the tile lies above the diagonal
 };
 
@@ -182,6 +182,7 @@ __device__ __forceinline__ TileAt tile_at(const ProductShape& s, int tile, int r
   at.row = at.row0 + lane;
   at.nb = nb;
   at.n0 = nb * C::BN;
+  at.width = C::BN;
   at.mirror = C::SYM && mb != nb;
   return at;
 }
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(192, 1)
   at.row = at.row0 + (int)lane;
   at.nb = nb;
   at.n0 = nb * BN;
+  at.width = BN;
   at.b = b;
   at.mirror = C::SYM && mb != nb;
   const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);

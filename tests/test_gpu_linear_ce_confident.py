@@ -92,6 +92,17 @@ def test_gradients_of_confident_tokens(T, V, h, shift, e, c):
     assert mt.mt_op_device_error() == 0
 
 
+@pytest.mark.parametrize("T,V,h", CONFIDENT)
+def test_log_sum_exp_of_confident_tokens_leans_to_no_side(T, V, h):
+    """It is the label's logit there, a tree of fp32 sums whose roundings have no sign of their own (the products' have:
+    1e-6 of it and more). A mean over the rows is off by less than 2^-22 of it, eight single roundings' mean size."""
+    torch, mt = need_gpu()
+    X, W, labels, gl = _confident(torch, T, V, h, T + V, 0.0)
+    r = _run(torch, mt, X, W, labels, gl, 1.0, 0.0, 0.0)
+    lse = _definition(torch, X, W, labels)[3]
+    assert abs(float((r.lse.double() - lse).mean())) <= 2.0 ** -22 * float(lse.abs().mean())
+
+
 def _far(torch, V, sign, size, scale):
     """Logits of `size`: the label's is the largest by far, with sign -1 in every other row the lowest."""
     X, W, labels, gl = _case(torch, 400, V, 64, 77, spread=1.0)
