@@ -169,3 +169,53 @@ def test_one_infinite_logit():
     X[2, 1] = 3e38
     r = _run(torch, mt, X, W, labels, gl, 1.0, 0.0, 0.0)
     assert not torch.isfinite(r.loss[2]) and torch.isfinite(r.loss[[0, 1, 3, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_several_pieces_added_and_one_gradient_alone(bf16):
+    torch, mt = need_gpu()
+    T, V, h = 70000, 5000, 16
+    X, W, labels, gl = _case(torch, T, V, h, 33)
+    labels[::7] = -1
+    X[::7] = float("nan")
+    dt = torch.bfloat16 if bf16 else torch.float32
+    start = torch.randn((V, h), device="cuda").to(dt)
+    both = _run(torch, mt, X, W, labels, gl, 1.0, 0.1, 1e-3, dt, dt, start=start)
+    Xc = torch.where((labels >= 0)[:, None], X, torch.zeros_like(X))
+    _check(torch, both, _reference(torch, Xc, W, labels, gl, 1.0, 0.1, 1e-3, h), start)
+    assert torch.equal(_run(torch, mt, X, W, labels, gl, 1.0, 0.1, 1e-3, dt, None).dX, both.dX)
+    assert torch.equal(_run(torch, mt, X, W, labels, gl, 1.0, 0.1, 1e-3, None, dt, start=start).dW, both.dW)
+
+
+def test_gradient_against_differences_of_the_definition():
+    """As close as dz's rounding allows: an error of at most U16 dz in each, in no particular direction, so that six of
+    their joint standard deviations (U16 / sqrt(3) each) hold."""
+    torch, mt = need_gpu()
+    T, V, h, e, c = 50, 333, 64, 0.1, 1e-2
+    X, W, labels, gl = _case(torch, T, V, h, 43)
+    r = _run(torch, mt, X, W, labels, gl, 1.0, e, c, torch.float32, torch.float32)
+    x, w, g = X.double(), W.double(), gl.double()
+    at = labels.long()[:, None]
+
+    def total(x, w):
+        z = x @ w.T
+        lse = torch.logsumexp(z, 1)
+        return (g * (lse - (1 - e) * z.gather(1, at)[:, 0] - e * z.mean(1) + c * lse ** 2)).sum()
+
+    z = x @ w.T
+    lse = torch.logsumexp(z, 1)
+    dz = torch.exp(z - lse[:, None]) * (1 + 2 * c * lse)[:, None] - e / V
+    dz = g[:, None] * (dz - torch.zeros_like(z).scatter_(1, at, 1 - e))
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    for k in range(4):
+        for which, base in (("dX", x), ("dW", w)):
+            d = torch.randn(base.shape, device="cuda", dtype=torch.float64, generator=gen)
+            s = 1e-5
+            num = (total(x + s * d, w) - total(x - s * d, w)) if which == "dX" else (total(x, w + s * d) - total(x, w - s * d))
+            num = float(num) / (2 * s)
+            along = (d @ w.T) if which == "dX" else (x @ d.T)
+            sd = float((dz * along).norm()) * U16 / 3 ** 0.5
+            got = float((getattr(r, which).double() * d).sum())
+            # differences: s^2 times the third derivative, and 1e-16 of the sums over s
+            assert abs(got - num) <= 6 * sd + 4e-6 * float((dz * along).abs().sum()), (which, got, num, sd)
