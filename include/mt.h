@@ -653,9 +653,12 @@ int mt_op_linear_ce_bwd(const void* X, const void* W, const int32_t* labels, flo
  * O [batch, rows, cols] (MT_F32 or MT_BF16) receives X: singular vectors kept,
  * singular values taken through the polynomial (with the quintic, five steps:
  * from 1e-2 of the norm up to between 0.7 and 1.2). Products are made of fp16
- * operands with fp32 sums, with X carried in 22 bits: O is 0.4e-3 to 1.1e-3
- * (relative, Frobenius; up to 2e-3 for matrices of low rank) from exact
- * arithmetic for the quintic's 5 or 6 steps before its own rounding. A zero
+ * operands with fp32 sums, with X carried in 22 bits: with the quintic and
+ * sides of 16 up O is within 1.6e-3 of exact arithmetic (relative, Frobenius,
+ * before its own rounding) after 5 steps, 2e-3 after 6. Few directions are
+ * harder: rank 1 to 4, m the shorter side, within 0.7 / m and 1.4 / m where
+ * that is more, and up to 8e-3 after 6 steps of matrices of thousands a side,
+ * where the polynomial takes the sums' errors five times as far. A zero
  * matrix (or one of values below 2e-41 throughout) gives zeros, one with an
  * infinity or a NaN (or whose squares' sum passes fp32) NaN throughout; the
  * others of the batch are not touched by it. Singular values have to stay

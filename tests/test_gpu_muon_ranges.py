@@ -125,3 +125,25 @@ def test_small_updates_are_scaled_to_norm_one(b, rows, cols, size):
     _check(torch, _ortho(torch, mt, G, eps=eps), G, eps=eps)
     k = 2.0 ** 40
     assert torch.equal(_ortho(torch, mt, G * k), _ortho(torch, mt, (G * k) * 2.0 ** 20))
+
+
+@pytest.mark.parametrize("steps,full,ranks", [(5, 1.6e-3, 0.7), (6, 2e-3, 1.4)])
+@pytest.mark.parametrize("kind", ["flat", "spikes", "gradient", 1, 2, 4])
+@pytest.mark.parametrize("b,rows,cols", [(8, 16, 64), (4, 64, 64), (1, 4096, 64), (3, 100, 1001), (2, 300, 1000), (1, 1024, 1024),
+                                         (2, 700, 260), (1, 5003, 4100)])
+def test_accuracy_as_stated(b, rows, cols, kind, steps, full, ranks):
+    """Of full rank within `full`; of rank 1 to 4 within ranks / m as well: what the first step's rounding leaves in the
+    other directions grows by 3.44 a step. Few directions also feel the sums' cutting, 2^-23 K / 16 of each product: four
+    products a step, c s^5 up to 5 times what a s + b s^3 leave of it, and the next steps take a relative error up to 5
+    times as far (s p'(s) / p(s) at 1.2, the top of the quintic's range) and then about as it is twice: 20 (1 + 5 + 5)."""
+    torch, mt = need_gpu()
+    if isinstance(kind, str):
+        G = _matrix(torch, kind, b, rows, cols, 51)
+    else:
+        g = torch.Generator(device="cuda")
+        g.manual_seed(51 + kind)
+        G = torch.randn((b, rows, kind), device="cuda", generator=g) @ torch.randn((b, kind, cols), device="cuda", generator=g)
+        full = max(full, ranks / min(rows, cols)) + 220 * max(rows, cols) / 16 * 2.0 ** -23
+    got, want = _ortho(torch, mt, G, steps).double(), ref.exact(G, steps)
+    rel = (got - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert bool((rel <= full).all()), rel
