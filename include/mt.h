@@ -614,7 +614,10 @@ int mt_op_embed_bwd(const int32_t* ids, const void* dout, int dout_dtype, float 
  *   loss[t] = lse - (1 - smoothing) z_label - smoothing * mean_j z_j + z_coef * lse^2
  * labels device int32 [T]; labels[t] < 0: the row is not scored, loss and lse
  * are 0. labels[t] >= V: both NaN, and a bit in mt_op_device_error. loss, lse
- * fp32 [T]. h, ldx, ldw multiples of 8, h up to 2^16, T and V up to 2^24 with
+ * fp32 [T]. Without smoothing and penalty a loss is formed as log(1 + the
+ * others' sum / e^{z_label}): at least 0, and as exact for its size where the
+ * label's probability is near 1 as elsewhere; losses are finite where the logits
+ * are, in fp32. h, ldx, ldw multiples of 8, h up to 2^16, T and V up to 2^24 with
  * T * V up to 2^40; logit_scale in [1e-6, 1e6], smoothing in [0, 1), z_coef in
  * [0, 1e6]. X and W 16-byte aligned, workspace (bytes) 256. (mt_op_lmhead_ce
  * keeps all logits and gives the mean loss with fp32 gradients in one call.) */

@@ -417,7 +417,9 @@ struct GradEpi : NoSlabs {
 // columns; or added to what is there or to an fp32 sum, 32 columns at a time
 // straight to memory, the addend asked for ahead of the accumulator. Two warps
 // a row as above. (From the lanes' rows, 32 bytes at a time: dW of 7 tokens, V
-// 128256, h 4096, 397 us, so 353.)
+// 128256, h 4096, 397 us, so 353. Adding to dW goes that way still: a backward
+// of 512 x 32000 x 1024 takes a third longer in bf16 and 58 % in fp32, of 8192 x
+// 128256 x 4096 3 % and 1 %.)
 struct SumEpi : NoSlabs {
   static constexpr int kSlab = 4096;
   static constexpr int WARPS = 8, SLABS = kSlab;

@@ -466,6 +466,8 @@ struct PolyEpi {
 };
 
 // X <- a X + B X; the last step leaves the result or takes the weights' step.
+// (The last one's form for single SMs spills 208 bytes: ten warps leave it 168
+// registers, and the way out by rows shares the kernel with the aligned one.)
 template <bool LAST>
 struct ApplyEpi {
   static constexpr int WARPS = 8, SLABS = 2 * kSlab;  // hi and lo in

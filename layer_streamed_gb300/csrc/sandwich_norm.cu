@@ -100,8 +100,10 @@ __device__ __forceinline__ float row_sum(const float (&v)[G], float* red, int nw
 
 // One block a row, the row in registers: V groups of four values a thread.
 // 8192 x 4096, bf16 y and gate (floor 70.3 us): V = 2 70.1 us, V = 1 89.7,
-// V = 4 81.2. Wider rows take V = 4, with a bf16 gate three blocks an
-// SM (4095 x 5636: 53.7 us, 58.7 with two; without a gate 51.5 against 49.7).
+// V = 4 81.2 with a thread's groups added up before its warp's; apart, as here,
+// 1.7 % more with V = 2. Wider rows take V = 4, with a bf16 gate three blocks an
+// SM (4095 x 5636: 53.7 us, 58.7 with two; without a gate 51.5 against 49.7),
+// at the price of 24 bytes spilled.
 template <bool BF16, bool GATE, int V>
 __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && GATE && BF16 ? 3 : 1)
     sandwich_fwd_kernel(const float* x, const void* y, const void* gate, const float* w_post, const float* w_pre,
@@ -175,8 +177,9 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, V == 4 && GATE && BF16 ? 
 // three with up to 512 where there is a gate: more threads leave too few
 // registers (4095 x 5636 fp32 without a gate, floor 82.9: 109 us spilling at
 // the bound of 1024 threads, 87 at 768; bf16 with a gate 127, 102 and, with
-// three, 92). Up to 8192 two, spilling 16 to 224 bytes (2000 x 8192 with a
-// gate, floor 58.8: 83 us; four with 512 threads 88).
+// three, 92; fp32 with a gate spills 32 bytes there). Up to 8192 two, spilling
+// 16 to 196 bytes (2000 x 8192 with a gate, floor 58.8: 83 us; four with 512
+// threads 88).
 // ---------------------------------------------------------------------------
 constexpr int kMaxThreads = 1024, kMaxStages = 8;
 constexpr int kMaxSms = 152;  // sizes the workspace, whatever machine asks

@@ -395,8 +395,10 @@ __device__ __forceinline__ void tile_chunk(uint32_t tb, int c, float (&v)[32]) {
 // order and runs the epilogue on it, 32 columns of a row a thread.
 // E::early asks for what E::chunk needs beside the sums, while these are made;
 // E::chunk has 4 KB of shared memory a warp.
-// (Three 32 KB steps in flight, so that the CTAs of two launches fit on an SM:
-// 1024 x 4096 orthogonalised in 210 us, with four 183, with more no faster.)
+// Four 32 KB steps are in flight and the parts have 64 KB of their own: one CTA
+// an SM. (1024 x 4096 orthogonalised in 183 us so when it was built; with three
+// steps, so that the CTAs of two launches fit on an SM, 210; with more steps no
+// faster.)
 // ---------------------------------------------------------------------------
 struct SplitSmem {
   static constexpr int STAGES = 4;
