@@ -192,7 +192,8 @@ struct StatsEpi : NoSlabs {
     if (at.row0 >= s.M) return;
     float m, sum, plain = 0.f;
     scan<BN, false>(a, s, at, r, w, tb, m, sum, plain);
-    const bool far = fabsf(m) > 0x1p22f && m != -INFINITY;
+    // rows behind the last token hold what the ring held
+    const bool far = at.row < s.M && fabsf(m) > 0x1p22f && m != -INFINITY;
     if (__any_sync(0xffffffffu, far)) {
       float m2, sum2;
       scan<BN, true>(a, s, at, r, w, tb, m2, sum2, plain);
